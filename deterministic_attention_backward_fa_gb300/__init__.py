@@ -12,6 +12,7 @@ function without it raises, there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -55,6 +56,7 @@ TRACE_SLOTS = 21
 _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 _F = ctypes.c_float
 
 _SIGS = {
@@ -83,6 +85,16 @@ _SIGS = {
     "dash_place_schedule": ([_P, _P] + [_I] * 5 + [_P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P], _I),
     "dash_die_map": ([_P, _P, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),
     "dash_cluster_links": ([_P, _P] + [_I] * 5 + [_P, ctypes.POINTER(ctypes.c_longlong)], _I),
+    "dash_packed_plan_create": ([_P] + [_I] * 6 + [ctypes.POINTER(_P)], _I),
+    "dash_packed_plan_destroy": ([_P], None),
+    "dash_packed_bwd_workspace": ([_P], _L),
+    "dash_build_packed_schedule": ([_P] + [_I] * 5 + [_P, _P, ctypes.POINTER(_I), ctypes.POINTER(_L)], _I),
+    "dash_attn_packed_fwd": ([_P] * 6 + [_L, _P, _F, _P], _I),
+    "dash_attn_packed_bwd": ([_P] * 10 + [_L, _P, _F, _P, _L, _P], _I),
+    "dash_attn_decode": ([_P] * 7 + [_I] * 7 + [_P, _F, _P, _L, _P], _I),
+    "dash_decode_workspace": ([_I] * 5, _L),
+    "dash_cache_write": ([_P] * 7 + [_L] + [_I] * 6 + [_P, _P], _I),
+    "dash_cache_copy": ([_P] * 4 + [_I] * 5 + [_P, _P], _I),
     "dash_sync_status": ([_P], _I),
     "dash_release_workspace": ([], None),
     "dash_last_error": ([], ctypes.c_char_p),
@@ -408,6 +420,219 @@ def dash_die_map(max_sm: int = 1023, stream=None):
     return g, n0.value, n1.value
 
 
+# ---- packed, grouped-head attention and the paged cache
+def _on(device, stream, tensors):
+    """Checks that the tensors lie on ``device`` and returns the stream to run on (that device's current one)."""
+    for name, t in tensors:
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, not to {device}")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _rows(name, t, heads=None, dim=None, rows=None):
+    """A [rows, heads, D] bf16 CUDA tensor whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim) or \
+            (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {heads or 'heads'}, {dim or 'D'}], "
+                         f"not {list(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _plain(name, t, dtype, shape, device):
+    """A contiguous CUDA tensor of the given type and shape (None: any extent)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous on {device}")
+    return t
+
+
+def _strides(*tensors):
+    v = [x for t in tensors for x in t.stride()[:2]]
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+class PackedPlan:
+    """Tables of one set of sequence lengths (host ints) on a GPU, for ``heads`` Q heads that share ``kv_heads``
+    K/V heads: made once per batch, used by every layer's ``attn_packed_fwd`` and, with ``backward=True``,
+    ``attn_packed_bwd``.  Read-only once made; keep it while work that uses it (replays of captured graphs
+    included) may still run."""
+
+    def __init__(self, lengths, heads: int, kv_heads: int, head_dim: int, causal: bool = True,
+                 backward: bool = False, device=None):
+        self._handle = None
+        values = lengths.tolist() if hasattr(lengths, "tolist") else list(lengths)
+        self.lengths = tuple(int(x) for x in values)
+        self.heads, self.kv_heads, self.head_dim, self.causal = int(heads), int(kv_heads), int(head_dim), bool(causal)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("a plan needs a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(self.device):
+            self._handle = dash_packed_plan_create(self.lengths, self.heads, self.kv_heads, self.head_dim,
+                                                   self.causal, backward)
+        self.rows = sum(self.lengths)
+        self.workspace_bytes = dash_packed_bwd_workspace(self._handle) if backward else -1
+
+    def __del__(self):
+        if getattr(self, "_handle", None) is not None and _LIB is not None:
+            dash_packed_plan_destroy(self._handle)
+            self._handle = None
+
+
+def _handle(plan):
+    return plan._handle if isinstance(plan, PackedPlan) else plan
+
+
+def dash_packed_plan_create(lengths, heads: int, kv_heads: int, head_dim: int, causal: bool, backward: bool):
+    """The plan's handle on the current device (``PackedPlan`` owns one and frees it)."""
+    if any(not -2**31 <= x < 2**31 for x in lengths):
+        raise ValueError("lengths must fit 32 bits")
+    arr = (ctypes.c_int32 * max(len(lengths), 1))(*lengths)
+    out = _P()
+    _check(lib().dash_packed_plan_create(arr, len(lengths), heads, kv_heads, head_dim, int(causal), int(backward),
+                                         ctypes.byref(out)))
+    return out
+
+
+def dash_packed_plan_destroy(plan):
+    lib().dash_packed_plan_destroy(_handle(plan))
+
+
+def dash_packed_bwd_workspace(plan) -> int:
+    return int(lib().dash_packed_bwd_workspace(_handle(plan)))
+
+
+def dash_build_packed_schedule(lengths, heads: int, kv_heads: int, causal: bool, P: int):
+    """Host-only.  The packed backward's table: (tasks int32 [N, 4], cta_off int32 [CTAs + 1])."""
+    arr = (ctypes.c_int32 * max(len(lengths), 1))(*lengths)
+    n, ctas = _L(0), _I(0)
+    head = (arr, len(lengths), heads, kv_heads, int(causal), P)
+    _check(lib().dash_build_packed_schedule(*head, None, None, ctypes.byref(ctas), ctypes.byref(n)))
+    tasks = np.zeros((max(n.value, 1), 4), dtype=np.int32)
+    off = np.zeros(ctas.value + 1, dtype=np.int32)
+    _check(lib().dash_build_packed_schedule(*head, tasks.ctypes.data, off.ctypes.data, None, ctypes.byref(n)))
+    return tasks[:n.value], off
+
+
+def dash_attn_packed_fwd(plan: PackedPlan, q, k, v, o, lse, scale: float, stream=None):
+    rows, dev = q.shape[0], plan.device
+    for name, t, h in (("q", q, plan.heads), ("k", k, plan.kv_heads), ("v", v, plan.kv_heads), ("o", o, plan.heads)):
+        _rows(name, t, h, plan.head_dim, rows)
+    _plain("lse", lse, torch.float32, (plan.heads, rows), dev)
+    st = _on(dev, stream, (("q", q), ("k", k), ("v", v), ("o", o)))
+    with torch.cuda.device(dev):
+        _check(lib().dash_attn_packed_fwd(plan._handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                          lse.data_ptr(), rows, _strides(q, k, v, o), float(scale), st))
+
+
+def dash_attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, stream=None):
+    rows, dev, hq, hk = q.shape[0], plan.device, plan.heads, plan.kv_heads
+    named = (("q", q, hq), ("k", k, hk), ("v", v, hk), ("o", o, hq), ("do", do, hq), ("dq", dq, hq), ("dk", dk, hk),
+             ("dv", dv, hk))
+    for name, t, h in named:
+        _rows(name, t, h, plan.head_dim, rows)
+    _plain("lse", lse, torch.float32, (hq, rows), dev)
+    _plain("workspace", workspace, torch.uint8, (None,), dev)
+    st = _on(dev, stream, [(n, t) for n, t, _ in named])
+    with torch.cuda.device(dev):
+        _check(lib().dash_attn_packed_bwd(plan._handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                          do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                          rows, _strides(q, k, v, o, do, dq, dk, dv), float(scale),
+                                          workspace.data_ptr(), workspace.numel(), st))
+
+
+def _cache(k_pages, v_pages):
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a CUDA bfloat16 tensor [pages, tokens, heads, D], contiguous in D")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    return k_pages.shape
+
+
+def _cache_strides(a, b, k_pages, v_pages, table):
+    v = (*a.stride()[:2], *b.stride()[:2], *k_pages.stride()[:3], *v_pages.stride()[:3], table.stride(0))
+    return (ctypes.c_int64 * 11)(*v)
+
+
+def _table(page_table, n_seqs, device):
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_seqs:
+        raise ValueError(f"page_table must be int32 [{n_seqs}, pages]")
+    if page_table.device != device or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must lie on {device} with contiguous rows")
+
+
+def dash_decode_workspace(B: int, heads: int, head_dim: int, page_size: int, max_pages: int) -> int:
+    return int(lib().dash_decode_workspace(B, heads, head_dim, page_size, max_pages))
+
+
+def dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale: float, workspace=None, stream=None):
+    """``lse`` may be None; ``workspace`` as dash_decode_workspace asks for (uint8)."""
+    n_pages, page, hkv, D = _cache(k_pages, v_pages)
+    _rows("q", q, None, D)
+    B, hq = q.shape[0], q.shape[1]
+    _rows("o", o, hq, D, B)
+    dev = q.device
+    _table(page_table, B, dev)
+    _plain("lengths", lengths, torch.int32, (B,), dev)
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (B, hq), dev)
+    if workspace is not None:
+        _plain("workspace", workspace, torch.uint8, (None,), dev)
+    st = _on(dev, stream, (("o", o), ("k_pages", k_pages), ("v_pages", v_pages)))
+    with torch.cuda.device(dev):
+        _check(lib().dash_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                      lengths.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+                                      B, hq, hkv, D, n_pages, page, page_table.shape[1],
+                                      _cache_strides(q, o, k_pages, v_pages, page_table), float(scale),
+                                      None if workspace is None else workspace.data_ptr(),
+                                      0 if workspace is None else workspace.numel(), st))
+
+
+def dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=None):
+    n_pages, page, hkv, D = _cache(k_pages, v_pages)
+    _rows("k", k, hkv, D)
+    _rows("v", v, hkv, D, k.shape[0])
+    dev = k.device
+    _plain("starts", starts, torch.int32, (None,), dev)
+    B = starts.shape[0]
+    _plain("cu_new", cu_new, torch.int32, (B + 1,), dev)
+    _table(page_table, B, dev)
+    st = _on(dev, stream, (("v", v), ("k_pages", k_pages), ("v_pages", v_pages)))
+    with torch.cuda.device(dev):
+        _check(lib().dash_cache_write(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                      page_table.data_ptr(), starts.data_ptr(), cu_new.data_ptr(), k.shape[0], B, hkv,
+                                      D, n_pages, page, page_table.shape[1],
+                                      _cache_strides(k, v, k_pages, v_pages, page_table), st))
+
+
+def dash_cache_copy(k_pages, v_pages, src, dst, stream=None):
+    """``src``, ``dst``: page numbers on the host (lists, arrays or CPU tensors)."""
+    n_pages, page, hkv, D = _cache(k_pages, v_pages)
+    s, d = np.asarray(src, dtype=np.int32).reshape(-1), np.asarray(dst, dtype=np.int32).reshape(-1)
+    if s.size != d.size:
+        raise ValueError("src and dst must have the same length")
+    s, d = np.ascontiguousarray(s), np.ascontiguousarray(d)
+    dev = k_pages.device
+    st = _on(dev, stream, (("v_pages", v_pages),))
+    strides = (ctypes.c_int64 * 6)(*k_pages.stride()[:3], *v_pages.stride()[:3])
+    with torch.cuda.device(dev):
+        _check(lib().dash_cache_copy(k_pages.data_ptr(), v_pages.data_ptr(), s.ctypes.data, d.ctypes.data, s.size,
+                                     hkv, D, n_pages, page, strides, st))
+
+
 def dash_sync_status(stream=None):
     _check(lib().dash_sync_status(_stream(stream)))
 
@@ -425,6 +650,21 @@ def dash_version() -> int:
 
 
 # ------------------------------------------------------------ conveniences
+@contextlib.contextmanager
+def _using(stream, *tensors):
+    """Runs torch's own work on ``stream`` if one is given, and tells the allocator that it uses the tensors (made
+    on the current stream, whose work so far it waits for)."""
+    if stream is None:
+        yield
+        return
+    stream.wait_stream(torch.cuda.current_stream(stream.device))
+    with torch.cuda.stream(stream):
+        yield
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def attn_fwd(q, k, v, causal: bool, scale: float | None = None, stream=None, cta_pair: int = -1):
     """O (bf16) and LSE (fp32, natural log) of softmax attention."""
     B, H, S, D = _shape(q)
@@ -451,3 +691,58 @@ def attn_bwd(q, k, v, o, do, lse, causal: bool, scale: float | None = None, sche
         dash_attn_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, causal, scale, schedule, dq_accum_out=acc,
                          stream=stream, **opts)
     return (dq, dk, dv, acc) if dq_accum else (dq, dk, dv)
+
+
+def attn_packed_fwd(plan: PackedPlan, q, k, v, scale: float | None = None, stream=None):
+    """O [rows, heads, D] (bf16) and LSE [heads, rows] (fp32) of attention over the plan's packed sequences.  Rows
+    behind the last sequence are zero (-inf in LSE)."""
+    _rows("q", q, plan.heads, plan.head_dim)
+    scale = 1.0 / math.sqrt(plan.head_dim) if scale is None else scale
+    rows = q.shape[0]
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((plan.heads, rows), dtype=torch.float32, device=q.device)
+    with _using(stream, o, lse):
+        dash_attn_packed_fwd(plan, q, k, v, o, lse, scale, stream)
+        if rows > plan.rows:
+            o[plan.rows:].zero_()
+            lse[:, plan.rows:].fill_(float("-inf"))
+    return o, lse
+
+
+def attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, scale: float | None = None, stream=None):
+    """dQ [rows, heads, D], dK, dV [rows, kv_heads, D] (bf16); zero behind the last sequence."""
+    _rows("q", q, plan.heads, plan.head_dim)
+    scale = 1.0 / math.sqrt(plan.head_dim) if scale is None else scale
+    rows = q.shape[0]
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk, dv = (torch.empty((rows, plan.kv_heads, plan.head_dim), dtype=q.dtype, device=q.device) for _ in range(2))
+    ws = torch.empty(max(plan.workspace_bytes, 0), dtype=torch.uint8, device=q.device)
+    with _using(stream, dq, dk, dv, ws):
+        dash_attn_packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, scale, ws, stream)
+        if rows > plan.rows:
+            for t in (dq, dk, dv):
+                t[plan.rows:].zero_()
+    return dq, dk, dv
+
+
+def attn_decode(q, k_pages, v_pages, page_table, lengths, scale: float | None = None, stream=None):
+    """O [B, heads, D] (bf16) and LSE [B, heads] (fp32) of one new token per sequence over a paged cache."""
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    _cache(k_pages, v_pages)
+    need = dash_decode_workspace(q.shape[0], q.shape[1], q.shape[2], k_pages.shape[1], page_table.shape[1])
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    with _using(stream, o, lse, ws):
+        dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale, ws, stream)
+    return o, lse
+
+
+def cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=None):
+    """Writes new tokens' K and V rows into the pages of their sequences, in place (see dash_cache_write)."""
+    dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream)
+
+
+def cache_copy(k_pages, v_pages, src, dst, stream=None):
+    """Copies pages ``src`` to pages ``dst`` (host page numbers) inside the cache, in place."""
+    dash_cache_copy(k_pages, v_pages, src, dst, stream)

@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdash.so")
 
-SOURCES = ["api.cpp", "schedule.cpp", "place.cpp", "bwd.cu", "fwd.cu", "noalloc.cu", "place.cu"]
+SOURCES = ["api.cpp", "schedule.cpp", "place.cpp", "packed_api.cpp", "packed_plan.cpp", "bwd.cu", "fwd.cu",
+           "noalloc.cu", "place.cu", "packed_fwd.cu", "packed_bwd.cu", "paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE]
 

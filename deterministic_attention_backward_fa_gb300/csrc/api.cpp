@@ -24,6 +24,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "packed.h"
 #include "place.h"
 #include "schedule.h"
 
@@ -68,12 +69,13 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D map over a contiguous bf16 [BH][S][D] tensor; boxes of 64 columns x box_rows rows.
-dash_status_t make_map(CUtensorMap *m, const void *base, int BH, int S, int D, int box_rows) {
+// 3-D map over a bf16 [heads][rows][D] tensor with element strides; boxes of 64 columns x box_rows rows.
+dash_status_t make_rows_map(CUtensorMap *m, const void *base, int heads, long long rows, int D, long long row_stride,
+                            long long head_stride, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(DASH_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)BH};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)S * D * 2};
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)head_stride * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
@@ -81,6 +83,11 @@ dash_status_t make_map(CUtensorMap *m, const void *base, int BH, int S, int D, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DASH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return DASH_OK;
+}
+
+// The map of a contiguous bf16 [BH][S][D] tensor.
+dash_status_t make_map(CUtensorMap *m, const void *base, int BH, int S, int D, int box_rows) {
+  return make_rows_map(m, base, BH, S, D, D, (long long)S * D, box_rows);
 }
 
 // ------------------------------------------------------------ workspace
@@ -642,6 +649,10 @@ void set_last_error(const char *msg) { g_last_error = msg; }
 bool encode_bhsd_map(CUtensorMap *m, const void *base, int BH, int S, int D, int box_rows) {
   return make_map(m, base, BH, S, D, box_rows) == DASH_OK;
 }
+dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long long rows, int D, long long row_stride,
+                              long long head_stride, int box_rows) {
+  return make_rows_map(m, base, heads, rows, D, row_stride, head_stride, box_rows);
+}
 }  // namespace dash
 
 extern "C" {
@@ -995,14 +1006,24 @@ dash_status_t dash_sync_status(dash_stream_t stream_) {
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_mu);
-  auto it = g_ws.find({dev, (void *)stream});
-  if (it == g_ws.end() || !it->second->status.ptr) return DASH_OK;
   int word = 0;
-  if ((e = cudaMemcpy(&word, it->second->status.ptr, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
+  auto take = [&](void *p) -> cudaError_t {  // reads the word and clears it if it is set
+    cudaError_t err = cudaMemcpy(&word, p, 4, cudaMemcpyDeviceToHost);
+    const int zero = 0;
+    if (err == cudaSuccess && word != 0) err = cudaMemcpy(p, &zero, 4, cudaMemcpyHostToDevice);
+    return err;
+  };
+  auto it = g_ws.find({dev, (void *)stream});
+  if (it != g_ws.end() && it->second->status.ptr && (e = take(it->second->status.ptr)) != cudaSuccess)
     return cuda_fail(e, "reading the status word");
+  if (word == 0 && dash::ops_status_used()) {
+    int *ops = nullptr;
+    if ((e = dash::ops_status_address(&ops)) != cudaSuccess || (e = take(ops)) != cudaSuccess)
+      return cuda_fail(e, "reading the status word");
+  }
   if (word == 0) return DASH_OK;
-  const int zero = 0;
-  cudaMemcpy(it->second->status.ptr, &zero, 4, cudaMemcpyHostToDevice);
+  if (word == dash::kStatusBadPage)
+    return fail(DASH_ERR_INVALID_ARG, "a page table entry or token position lies outside the cache");
   if (word == dash::kStatusSmemMisaligned)
     return fail(DASH_ERR_CUDA, "device status %d: dynamic shared memory not 1024-byte aligned", word);
   return fail(DASH_ERR_TIMEOUT, "device status %d: a bounded wait ran out (%s)", word,

@@ -1,0 +1,572 @@
+// C ABI of the packed attention and the paged cache (declared in include/dash.h).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <memory>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "dash.h"
+#include "packed.h"
+#include "packed_plan.h"
+
+namespace dash {
+dash_status_t report(dash_status_t code, const char *fmt, ...);  // api.cpp
+dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long long rows, int D,
+                              long long row_stride, long long head_stride, int box_rows);
+}  // namespace dash
+
+using dash::report;
+
+// A plan: the tables of one set of lengths on the device it was made on.
+struct dash_packed_plan_st {
+  int device = 0, Hq = 0, Hkv = 0, D = 0, causal = 0, n_seqs = 0;
+  long long rows = 0, n_tiles = 0;
+  int fwd_ctas = 0, bwd_ctas = 0;  // 0: nothing to do, or (backward) not planned
+  bool backward = false;
+  void *mem = nullptr;
+  const int2 *seqs = nullptr;
+  const int4 *tiles = nullptr;
+  const dash::PackedFwdItem *items = nullptr;
+  const int *fwd_off = nullptr, *bwd_off = nullptr;
+  const int4 *tasks = nullptr;
+  int *status = nullptr;
+};
+
+namespace {
+
+constexpr long long kSpinNs = 2000000000LL;  // 2 s bound on every device wait
+constexpr float kLog2e = 1.4426950408889634f;
+
+dash_status_t cuda_error(cudaError_t e, const char *what) {
+  return report(DASH_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+dash_status_t check_scale(float scale) {
+  if (!(scale > 0.f) || !std::isfinite(scale)) return report(DASH_ERR_INVALID_ARG, "scale must be finite and > 0");
+  return DASH_OK;
+}
+
+dash_status_t check_ptr(const void *p, const char *name) {
+  if (!p) return report(DASH_ERR_INVALID_ARG, "%s is a null pointer", name);
+  if (reinterpret_cast<uintptr_t>(p) & 15u) return report(DASH_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  return DASH_OK;
+}
+
+// Strides of a [rows][heads][D] tensor, in elements.
+struct Rows {
+  long long row, head;
+};
+
+// Takes strides {row, head} (null: contiguous) and checks that 16-byte vectors
+// are aligned and that no two rows share elements.  A stride along an extent of
+// one is never used and set to its contiguous value.
+dash_status_t rows_of(const int64_t *s, int i, long long rows, int heads, int D, const char *name, Rows *out) {
+  Rows r{s ? (long long)s[2 * i] : (long long)heads * D, s ? (long long)s[2 * i + 1] : D};
+  if (rows == 1) r.row = (long long)heads * (heads > 1 ? std::max<long long>(r.head, D) : D);
+  if (heads == 1) r.head = rows > 1 ? std::max<long long>(rows * std::max<long long>(r.row, D), D) : D;
+  if (r.row < D || r.head < D || (r.row & 7) || (r.head & 7))
+    return report(DASH_ERR_INVALID_ARG, "%s: strides (%lld, %lld) must be multiples of 8 of at least D", name,
+                  r.row, r.head);
+  if (rows > 1 && heads > 1 && r.row < (heads - 1) * r.head + D && r.head < (rows - 1) * r.row + D)
+    return report(DASH_ERR_INVALID_ARG, "%s: its rows overlap", name);
+  if (r.row >= (1LL << 38) || r.head >= (1LL << 38))
+    return report(DASH_ERR_UNSUPPORTED, "%s: strides of 2^38 elements and more", name);
+  *out = r;
+  return DASH_OK;
+}
+
+dash_status_t check_heads(int Hq, int Hkv, int D) {
+  if (D != 64 && D != 128) return report(DASH_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", D);
+  if (Hkv < 1 || Hq < 1 || Hq % Hkv)
+    return report(DASH_ERR_INVALID_ARG, "%d Q heads are not a multiple of %d K/V heads", Hq, Hkv);
+  if (Hq > 65535) return report(DASH_ERR_UNSUPPORTED, "more than 65535 Q heads");
+  return DASH_OK;
+}
+
+struct Region {
+  size_t bytes = 0;
+  size_t add(size_t n) {
+    const size_t at = bytes;
+    bytes = (bytes + n + 255) / 256 * 256;
+    return at;
+  }
+};
+
+// Workspace of a packed backward.
+struct BwdLayout {
+  size_t accum, lse2, delta, sem, maps, bytes;
+};
+BwdLayout bwd_layout(const dash_packed_plan_st *p) {
+  const size_t tiles = (size_t)p->n_tiles * p->Hq;
+  Region r;
+  BwdLayout l;
+  l.maps = r.add((size_t)p->n_seqs * 4 * sizeof(CUtensorMap));
+  l.sem = r.add(tiles * dash::kSemStride * 4);
+  l.lse2 = r.add(tiles * dash::kPackedTile * 4);
+  l.delta = r.add(tiles * dash::kPackedTile * 4);
+  l.accum = r.add(tiles * dash::kPackedTile * p->D * 4);
+  l.bytes = r.bytes;
+  return l;
+}
+
+dash_status_t check_plan(const dash_packed_plan_st *p, long long rows) {
+  if (!p) return report(DASH_ERR_INVALID_ARG, "null plan");
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+  if (dev != p->device)
+    return report(DASH_ERR_INVALID_ARG, "the plan was made on device %d, the current device is %d", p->device, dev);
+  if (rows < p->rows)
+    return report(DASH_ERR_INVALID_ARG, "%lld rows are fewer than the plan's %lld", rows, p->rows);
+  if (rows > INT32_MAX - dash::kPackedTile) return report(DASH_ERR_UNSUPPORTED, "more than 2^31 packed rows");
+  return DASH_OK;
+}
+
+dash_status_t sm_count(int *dev, int *sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "device query");
+}
+
+dash_status_t cache_strides(const int64_t *s, int n_pages, int page_size, int heads, int D, const char *name,
+                            dash::CacheStrides *out) {
+  dash::CacheStrides c{(long long)page_size * heads * D, (long long)heads * D, D};
+  if (s) c = {(long long)s[0], (long long)s[1], (long long)s[2]};
+  if (n_pages == 1) c.page = 0;
+  if (page_size == 1) c.token = 0;
+  if (heads == 1) c.head = 0;
+  const long long ext[3] = {n_pages, page_size, heads}, st[3] = {c.page, c.token, c.head};
+  for (int i = 0; i < 3; ++i)
+    if (ext[i] > 1 && (st[i] < D || (st[i] & 7)))
+      return report(DASH_ERR_INVALID_ARG, "%s: strides (%lld, %lld, %lld) must be multiples of 8 of at least D", name,
+                    c.page, c.token, c.head);
+  // walked from the innermost extent outwards, no two rows may share elements
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return st[a] < st[b]; });
+  long long span = D;
+  for (int i : order) {
+    if (ext[i] <= 1) continue;
+    if (st[i] < span) return report(DASH_ERR_INVALID_ARG, "%s: its rows overlap", name);
+    if (st[i] > (1LL << 60) / ext[i]) return report(DASH_ERR_UNSUPPORTED, "%s: strides too large", name);
+    span = (ext[i] - 1) * st[i] + span;
+  }
+  *out = c;
+  return DASH_OK;
+}
+
+// The status word of the current device; its first look-up loads the kernels.
+dash_status_t status_word(int **p) {
+  const cudaError_t e = dash::ops_status_address(p);
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "status word");
+}
+
+dash_status_t check_cache(int Hkv, int D, int n_pages, int page_size) {
+  if (n_pages < 1 || page_size < 1) return report(DASH_ERR_INVALID_ARG, "the cache needs pages and tokens in a page");
+  if (Hkv < 1) return report(DASH_ERR_INVALID_ARG, "the cache needs heads");
+  if (D != 64 && D != 128) return report(DASH_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", D);
+  if ((long long)page_size * Hkv * (D / 8) > INT32_MAX) return report(DASH_ERR_UNSUPPORTED, "pages too large");
+  return DASH_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int D, int causal,
+                                      int backward, dash_packed_plan_t **plan_out) try {
+  if (!plan_out) return report(DASH_ERR_INVALID_ARG, "null plan pointer");
+  *plan_out = nullptr;
+  if (n_seqs < 0 || (n_seqs > 0 && !lengths)) return report(DASH_ERR_INVALID_ARG, "null lengths");
+  dash_status_t st = check_heads(Hq, Hkv, D);
+  if (st != DASH_OK) return st;
+  dash::PackedTables t;
+  std::string why = dash::packed_tiles(lengths, n_seqs, &t);
+  if (!why.empty()) return report(DASH_ERR_INVALID_ARG, "%s", why.c_str());
+  int dev = 0, sms = 0;
+  if ((st = sm_count(&dev, &sms)) != DASH_OK) return st;
+  std::unique_ptr<dash_packed_plan_st> p(new dash_packed_plan_st());
+  p->device = dev;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->D = D;
+  p->causal = causal ? 1 : 0;
+  p->n_seqs = n_seqs;
+  p->rows = t.rows;
+  p->n_tiles = (long long)t.tiles.size();
+  p->backward = backward != 0;
+  if (t.rows > 0) {
+    dash::packed_forward(t, Hq, Hkv, causal != 0, sms, &t);
+    p->fwd_ctas = (int)t.fwd_off.size() - 1;
+    if (backward) {
+      why = dash::packed_backward(t, Hq, Hkv, causal != 0, sms, &t);
+      if (!why.empty()) return report(DASH_ERR_UNSUPPORTED, "%s", why.c_str());
+      p->bwd_ctas = (int)t.bwd_off.size() - 1;
+    }
+    cudaError_t e = dash::prepare_packed_fwd(D);
+    if (e != cudaSuccess) return cuda_error(e, "packed forward");
+    if (backward && (e = dash::prepare_packed_bwd(D)) != cudaSuccess) return cuda_error(e, "packed backward");
+    if ((st = status_word(&p->status)) != DASH_OK) return st;
+    // one block of device memory, copied once
+    Region r;
+    const size_t a = r.add(t.seqs.size() * sizeof(int2)), b = r.add(t.tiles.size() * sizeof(int4)),
+                 c = r.add(t.items.size() * sizeof(dash::PackedFwdItem)), d = r.add(t.fwd_off.size() * 4),
+                 f = r.add(t.bwd_off.size() * 4), g = r.add(t.tasks.size() * 4);
+    std::vector<uint8_t> host(r.bytes);
+    auto put = [&](size_t at, const void *src, size_t n) {
+      if (n) std::memcpy(host.data() + at, src, n);
+    };
+    put(a, t.seqs.data(), t.seqs.size() * sizeof(int2));
+    put(b, t.tiles.data(), t.tiles.size() * sizeof(int4));
+    put(c, t.items.data(), t.items.size() * sizeof(dash::PackedFwdItem));
+    put(d, t.fwd_off.data(), t.fwd_off.size() * 4);
+    put(f, t.bwd_off.data(), t.bwd_off.size() * 4);
+    put(g, t.tasks.data(), t.tasks.size() * 4);
+    if ((e = cudaMalloc(&p->mem, r.bytes)) != cudaSuccess)
+      return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", r.bytes, cudaGetErrorString(e));
+    if ((e = cudaMemcpy(p->mem, host.data(), r.bytes, cudaMemcpyHostToDevice)) != cudaSuccess) {
+      cudaFree(p->mem);
+      return cuda_error(e, "plan tables");
+    }
+    uint8_t *m = static_cast<uint8_t *>(p->mem);
+    p->seqs = reinterpret_cast<const int2 *>(m + a);
+    p->tiles = reinterpret_cast<const int4 *>(m + b);
+    p->items = reinterpret_cast<const dash::PackedFwdItem *>(m + c);
+    p->fwd_off = reinterpret_cast<const int *>(m + d);
+    p->bwd_off = reinterpret_cast<const int *>(m + f);
+    p->tasks = reinterpret_cast<const int4 *>(m + g);
+  }
+  *plan_out = p.release();
+  return DASH_OK;
+} catch (const std::bad_alloc &) {
+  return report(DASH_ERR_NO_MEMORY, "plan: out of host memory");
+} catch (...) {
+  return report(DASH_ERR_NO_MEMORY, "plan: the host tables could not be built");
+}
+
+void dash_packed_plan_destroy(dash_packed_plan_t *plan) {
+  if (!plan) return;
+  if (plan->mem) {
+    int dev = 0;
+    const bool other = cudaGetDevice(&dev) == cudaSuccess && dev != plan->device;
+    if (other) cudaSetDevice(plan->device);
+    cudaFree(plan->mem);
+    if (other) cudaSetDevice(dev);
+  }
+  delete plan;
+}
+
+long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan) {
+  if (!plan || !plan->backward) return -1;
+  return plan->rows ? (long long)bwd_layout(plan).bytes : 0;
+}
+
+dash_status_t dash_build_packed_schedule(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int P,
+                                         int32_t *tasks_out, int32_t *cta_off_out, int *ctas_out,
+                                         long long *n_tasks_out) try {
+  if (n_seqs < 0 || (n_seqs > 0 && !lengths) || P < 1 || !n_tasks_out)
+    return report(DASH_ERR_INVALID_ARG, "dash_build_packed_schedule: null pointer or sizes out of range");
+  dash_status_t st = check_heads(Hq, Hkv, 64);
+  if (st != DASH_OK) return st;
+  dash::PackedTables t;
+  std::string why = dash::packed_tiles(lengths, n_seqs, &t);
+  if (!why.empty()) return report(DASH_ERR_INVALID_ARG, "%s", why.c_str());
+  why = dash::packed_backward(t, Hq, Hkv, causal != 0, P, &t);
+  if (!why.empty()) return report(DASH_ERR_UNSUPPORTED, "%s", why.c_str());
+  *n_tasks_out = (long long)t.tasks.size() / 4;
+  if (ctas_out) *ctas_out = (int)t.bwd_off.size() - 1;
+  if (tasks_out && !t.tasks.empty()) std::memcpy(tasks_out, t.tasks.data(), t.tasks.size() * 4);
+  if (cta_off_out) std::memcpy(cta_off_out, t.bwd_off.data(), t.bwd_off.size() * 4);
+  return DASH_OK;
+} catch (...) {
+  return report(DASH_ERR_NO_MEMORY, "dash_build_packed_schedule: out of host memory");
+}
+
+dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
+                                   void *o, float *lse, long long rows, const int64_t *strides, float scale,
+                                   dash_stream_t stream) {
+  dash_status_t st = check_scale(scale);
+  if (st != DASH_OK || (st = check_plan(plan, rows)) != DASH_OK) return st;
+  if (plan->rows == 0) return DASH_OK;
+  if ((st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) || (st = check_ptr(o, "o")))
+    return st;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return report(DASH_ERR_INVALID_ARG, "lse must be a pointer to floats");
+  const int D = plan->D;
+  Rows rq, rk, rv, ro;
+  if ((st = rows_of(strides, 0, rows, plan->Hq, D, "q", &rq)) || (st = rows_of(strides, 1, rows, plan->Hkv, D, "k", &rk)) ||
+      (st = rows_of(strides, 2, rows, plan->Hkv, D, "v", &rv)) || (st = rows_of(strides, 3, rows, plan->Hq, D, "o", &ro)))
+    return st;
+  CUtensorMap mq, mk, mv;
+  if ((st = dash::encode_rows_map(&mq, q, plan->Hq, rows, D, rq.row, rq.head, dash::kPackedTile)) ||
+      (st = dash::encode_rows_map(&mk, k, plan->Hkv, rows, D, rk.row, rk.head, dash::kPackedTile)) ||
+      (st = dash::encode_rows_map(&mv, v, plan->Hkv, rows, D, rv.row, rv.head, dash::kPackedTile)))
+    return st;
+  dash::PackedFwdParams p;
+  p.items = plan->items;
+  p.cta_off = plan->fwd_off;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.o_row = ro.row;
+  p.o_head = ro.head;
+  p.lse = lse;
+  p.lse_head = rows;
+  p.status = plan->status;
+  p.scale_log2 = scale * kLog2e;
+  p.causal = plan->causal;
+  p.spin_limit_ns = kSpinNs;
+  const cudaError_t e =
+      dash::launch_packed_fwd(D, mq, mk, mv, p, plan->fwd_ctas, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "packed forward launch");
+}
+
+dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
+                                   const void *o, const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                                   long long rows, const int64_t *strides, float scale, void *workspace,
+                                   long long workspace_bytes, dash_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  dash_status_t st = check_scale(scale);
+  if (st != DASH_OK || (st = check_plan(plan, rows)) != DASH_OK) return st;
+  if (!plan->backward) return report(DASH_ERR_INVALID_ARG, "the plan was made without its backward");
+  if (plan->rows == 0) return DASH_OK;
+  const void *ptrs[8] = {q, k, v, o, dout, dq, dk, dv};
+  const char *names[8] = {"q", "k", "v", "o", "dout", "dq", "dk", "dv"};
+  const int heads[8] = {plan->Hq, plan->Hkv, plan->Hkv, plan->Hq, plan->Hq, plan->Hq, plan->Hkv, plan->Hkv};
+  Rows r[8];
+  for (int i = 0; i < 8; ++i)
+    if ((st = check_ptr(ptrs[i], names[i])) || (st = rows_of(strides, i, rows, heads[i], plan->D, names[i], &r[i])))
+      return st;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return report(DASH_ERR_INVALID_ARG, "lse must be a pointer to floats");
+  const BwdLayout l = bwd_layout(plan);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < (long long)l.bytes)
+    return report(DASH_ERR_INVALID_ARG, "the workspace must hold %zu bytes, 256-byte aligned", l.bytes);
+  uint8_t *w = static_cast<uint8_t *>(workspace);
+
+  CUtensorMap m[4];
+  const int of[4] = {0, 1, 2, 4};  // Q, K, V, dO
+  dash::PackedPreParams pre;
+  for (int i = 0; i < 4; ++i) {
+    const int x = of[i];
+    if ((st = dash::encode_rows_map(&m[i], ptrs[x], heads[x], rows, plan->D, r[x].row, r[x].head,
+                                    dash::kPackedTile)) != DASH_OK)
+      return st;
+    pre.base[i] = ptrs[x];
+    pre.base_row[i] = r[x].row * 2;
+  }
+  pre.o = static_cast<const __nv_bfloat16 *>(o);
+  pre.dout = static_cast<const __nv_bfloat16 *>(dout);
+  pre.lse = lse;
+  pre.o_row = r[3].row;
+  pre.o_head = r[3].head;
+  pre.do_row = r[4].row;
+  pre.do_head = r[4].head;
+  pre.lse_head = rows;
+  pre.tiles = plan->tiles;
+  pre.seqs = plan->seqs;
+  pre.lse2 = reinterpret_cast<float *>(w + l.lse2);
+  pre.delta = reinterpret_cast<float *>(w + l.delta);
+  pre.sem = reinterpret_cast<int *>(w + l.sem);
+  pre.maps = reinterpret_cast<CUtensorMap *>(w + l.maps);
+  pre.n_tiles = (int)plan->n_tiles;
+  pre.n_seqs = plan->n_seqs;
+  pre.heads = plan->Hq;
+  cudaError_t e = dash::launch_packed_preprocess(plan->D, m[0], m[1], m[2], m[3], pre, stream);
+  if (e != cudaSuccess) return cuda_error(e, "packed preprocess launch");
+
+  dash::BwdMainParams mp = {};
+  mp.tasks = plan->tasks;
+  mp.cta_off = plan->bwd_off;
+  mp.lse2 = pre.lse2;
+  mp.delta = pre.delta;
+  mp.dq_accum = reinterpret_cast<float *>(w + l.accum);
+  mp.sem = pre.sem;
+  mp.dk = static_cast<__nv_bfloat16 *>(dk);
+  mp.dv = static_cast<__nv_bfloat16 *>(dv);
+  mp.status = plan->status;
+  mp.S = INT32_MAX;  // the bounds are the tiles' own
+  mp.n = (int)plan->n_tiles;
+  mp.scale = scale;
+  mp.scale_log2 = scale * kLog2e;
+  mp.causal = plan->causal;
+  mp.ordered = 1;
+  mp.spin_limit_ns = kSpinNs;
+  mp.chains = 1;
+  mp.chain_stride = 0;
+  mp.packed.tiles = plan->tiles;
+  mp.packed.maps = pre.maps;
+  mp.packed.group = plan->Hq / plan->Hkv;
+  mp.packed.dk_row = r[6].row;
+  mp.packed.dk_head = r[6].head;
+  mp.packed.dv_row = r[7].row;
+  mp.packed.dv_head = r[7].head;
+  if ((e = dash::launch_packed_bwd_main(plan->D, mp, plan->bwd_ctas, stream)) != cudaSuccess)
+    return cuda_error(e, "packed main launch");
+
+  dash::PackedConvertParams cp;
+  cp.accum = mp.dq_accum;
+  cp.tiles = plan->tiles;
+  cp.dq = static_cast<__nv_bfloat16 *>(dq);
+  cp.dq_row = r[5].row;
+  cp.dq_head = r[5].head;
+  cp.scale = scale;
+  cp.n_tiles = (int)plan->n_tiles;
+  cp.heads = plan->Hq;
+  if ((e = dash::launch_packed_convert(plan->D, cp, stream)) != cudaSuccess)
+    return cuda_error(e, "packed convert launch");
+  return DASH_OK;
+}
+
+long long dash_decode_workspace(int B, int Hq, int D, int page_size, int max_pages) {
+  if (B < 0 || Hq < 1 || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 ||
+      (long long)page_size * max_pages > INT32_MAX)
+    return -1;
+  const long long splits = dash::decode_splits(page_size * max_pages);
+  return splits <= 1 ? 0 : (long long)B * Hq * splits * (D * 4 + 8) + 256;
+}
+
+dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
+                               const int32_t *lengths, void *o, float *lse, int B, int Hq, int Hkv, int D,
+                               int n_pages, int page_size, int max_pages, const int64_t *strides, float scale,
+                               void *workspace, long long workspace_bytes, dash_stream_t stream) {
+  dash_status_t st = check_scale(scale);
+  if (st != DASH_OK || (st = check_heads(Hq, Hkv, D)) || (st = check_cache(Hkv, D, n_pages, page_size))) return st;
+  if (B < 0 || max_pages < 0) return report(DASH_ERR_INVALID_ARG, "B and max_pages must be >= 0");
+  if ((long long)page_size * max_pages > INT32_MAX)
+    return report(DASH_ERR_UNSUPPORTED, "a page table row covers more than 2^31 tokens");
+  if (B > 65535) return report(DASH_ERR_UNSUPPORTED, "more than 65535 sequences");
+  if (B == 0) return DASH_OK;
+  if ((st = check_ptr(q, "q")) || (st = check_ptr(k_pages, "k_pages")) || (st = check_ptr(v_pages, "v_pages")) ||
+      (st = check_ptr(o, "o")))
+    return st;
+  if ((max_pages > 0 && !page_table) || !lengths) return report(DASH_ERR_INVALID_ARG, "null page table or lengths");
+  Rows rq, ro;
+  if ((st = rows_of(strides, 0, B, Hq, D, "q", &rq)) || (st = rows_of(strides, 1, B, Hq, D, "o", &ro))) return st;
+  dash::DecodeParams p;
+  if ((st = cache_strides(strides ? strides + 4 : nullptr, n_pages, page_size, Hkv, D, "k_pages", &p.ks)) ||
+      (st = cache_strides(strides ? strides + 7 : nullptr, n_pages, page_size, Hkv, D, "v_pages", &p.vs)))
+    return st;
+  p.table_row = strides ? strides[10] : max_pages;
+  if (B > 1 && p.table_row < max_pages) return report(DASH_ERR_INVALID_ARG, "page table rows overlap");
+  p.max_splits = std::max(1, dash::decode_splits(page_size * max_pages));
+  const long long need = dash_decode_workspace(B, Hq, D, page_size, max_pages);
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
+    return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.k = static_cast<const __nv_bfloat16 *>(k_pages);
+  p.v = static_cast<const __nv_bfloat16 *>(v_pages);
+  p.table = page_table;
+  p.lengths = lengths;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.lse = lse;
+  p.part_o = static_cast<float *>(workspace);
+  p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)B * Hq * p.max_splits * D);
+  p.q_batch = rq.row;
+  p.q_head = rq.head;
+  p.o_batch = ro.row;
+  p.o_head = ro.head;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.n_pages = n_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.hblocks = (p.group + 15) / 16;
+  p.scale_log2 = scale * kLog2e;
+  int dev = 0, sms = 0;
+  if ((st = sm_count(&dev, &sms)) || (st = status_word(&p.status))) return st;
+  const cudaError_t e = dash::launch_decode(D, p, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "decode launch");
+}
+
+dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void *v_pages,
+                               const int32_t *page_table, const int32_t *starts, const int32_t *cu_new,
+                               long long n_tokens, int B, int Hkv, int D, int n_pages, int page_size, int max_pages,
+                               const int64_t *strides, dash_stream_t stream) {
+  dash_status_t st = check_cache(Hkv, D, n_pages, page_size);
+  if (st != DASH_OK) return st;
+  if (B < 0 || max_pages < 0 || n_tokens < 0 || n_tokens > INT32_MAX - 65536)
+    return report(DASH_ERR_INVALID_ARG, "sizes must be >= 0 and below 2^31");
+  if (B == 0 || n_tokens == 0) return DASH_OK;
+  if ((st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) || (st = check_ptr(k_pages, "k_pages")) ||
+      (st = check_ptr(v_pages, "v_pages")))
+    return st;
+  if ((max_pages > 0 && !page_table) || !starts || !cu_new)
+    return report(DASH_ERR_INVALID_ARG, "null page table, starts or cu_new");
+  Rows rk, rv;
+  if ((st = rows_of(strides, 0, n_tokens, Hkv, D, "k", &rk)) || (st = rows_of(strides, 1, n_tokens, Hkv, D, "v", &rv)))
+    return st;
+  dash::CacheWriteParams p;
+  if ((st = cache_strides(strides ? strides + 4 : nullptr, n_pages, page_size, Hkv, D, "k_pages", &p.ks)) ||
+      (st = cache_strides(strides ? strides + 7 : nullptr, n_pages, page_size, Hkv, D, "v_pages", &p.vs)))
+    return st;
+  p.table_row = strides ? strides[10] : max_pages;
+  if (B > 1 && p.table_row < max_pages) return report(DASH_ERR_INVALID_ARG, "page table rows overlap");
+  p.k = static_cast<const __nv_bfloat16 *>(k);
+  p.v = static_cast<const __nv_bfloat16 *>(v);
+  p.k_row = rk.row;
+  p.k_head = rk.head;
+  p.v_row = rv.row;
+  p.v_head = rv.head;
+  p.kp = static_cast<__nv_bfloat16 *>(k_pages);
+  p.vp = static_cast<__nv_bfloat16 *>(v_pages);
+  p.table = page_table;
+  p.starts = starts;
+  p.cu = cu_new;
+  p.n_tokens = (int)n_tokens;
+  p.B = B;
+  p.heads = Hkv;
+  p.D = D;
+  p.n_pages = n_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  int dev = 0, sms = 0;
+  if ((st = sm_count(&dev, &sms)) || (st = status_word(&p.status))) return st;
+  const cudaError_t e = dash::launch_cache_write(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "cache write launch");
+}
+
+dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, const int32_t *dst, int n, int Hkv,
+                              int D, int n_pages, int page_size, const int64_t *strides, dash_stream_t stream) try {
+  dash_status_t st = check_cache(Hkv, D, n_pages, page_size);
+  if (st != DASH_OK) return st;
+  if (n < 0) return report(DASH_ERR_INVALID_ARG, "n must be >= 0");
+  if (n == 0) return DASH_OK;
+  if (!src || !dst) return report(DASH_ERR_INVALID_ARG, "null page list");
+  if ((st = check_ptr(k_pages, "k_pages")) || (st = check_ptr(v_pages, "v_pages"))) return st;
+  dash::CacheCopyParams p;
+  if ((st = cache_strides(strides, n_pages, page_size, Hkv, D, "k_pages", &p.ks)) ||
+      (st = cache_strides(strides ? strides + 3 : nullptr, n_pages, page_size, Hkv, D, "v_pages", &p.vs)))
+    return st;
+  std::vector<int32_t> to(dst, dst + n);
+  std::sort(to.begin(), to.end());
+  if (to.front() < 0 || to.back() >= n_pages)
+    return report(DASH_ERR_INVALID_ARG, "destination page outside the cache's %d pages", n_pages);
+  if (std::adjacent_find(to.begin(), to.end()) != to.end())
+    return report(DASH_ERR_INVALID_ARG, "a destination page is named twice");
+  std::vector<int2> pairs(n);
+  for (int i = 0; i < n; ++i) {
+    if (src[i] < 0 || src[i] >= n_pages)
+      return report(DASH_ERR_INVALID_ARG, "source page %d outside the cache's %d pages", src[i], n_pages);
+    if (std::binary_search(to.begin(), to.end(), src[i]))
+      return report(DASH_ERR_INVALID_ARG, "page %d is a source and a destination of one call", src[i]);
+    pairs[i] = make_int2(src[i], dst[i]);
+  }
+  p.kp = static_cast<__nv_bfloat16 *>(k_pages);
+  p.vp = static_cast<__nv_bfloat16 *>(v_pages);
+  p.page_size = page_size;
+  p.heads = Hkv;
+  p.D = D;
+  const cudaError_t e = dash::launch_cache_copy(p, pairs.data(), n, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "cache copy launch");
+} catch (...) {
+  return report(DASH_ERR_NO_MEMORY, "cache copy: out of host memory");
+}
+
+}  // extern "C"

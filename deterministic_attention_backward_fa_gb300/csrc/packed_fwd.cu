@@ -1,0 +1,465 @@
+// Packed, grouped-head softmax attention forward for sm_103a.
+//
+// One pass over the keys with the running maximum and sum of the softmax:
+//   m' = max(m, max_j x_j),  l' = l 2^(m-m') + sum_j 2^(x_j - m'),
+//   O' = O 2^(m-m') + P V,   x = scale log2(e) q.k,  P = 2^(x - m'),
+// O / l at the end and LSE = ln2 (m + log2 l).  O stays in tensor memory.  The
+// maximum a row refers to moves only when it has grown by more than 2^8
+// (kLazy): until then P may exceed 1, which costs no precision (P keeps its
+// eight bits, l and O are fp32), and the rescaling of O, a round trip through
+// registers, happens a few times a row at most.
+//
+// A persistent CTA walks the items that the plan gave it.  An item is two
+// 128-row Q tiles on one K/V head, so that every K and V tile in shared memory
+// feeds four MMAs and one tile's softmax runs under the other tile's MMAs:
+//   tensor pipe   PV0(j) S0(j+1) | PV1(j) S1(j+1) | PV0(j+1) ...
+//   softmax 0              ......| S0(j+1) -> P0  |
+// Two heads of a group on the same rows share keys exactly; with one head per
+// group (or an odd one left over) two neighbouring tiles of a head pair up.
+//
+// Warps: 0-3 softmax and epilogue of tile 0, 4-7 of tile 1 (a thread owns a
+// row), 8 MMA issue, 9 TMA, 10 clears the V rows past the sequence's end in
+// the last KV tile (they belong to the next sequence or to nobody: P is 0
+// there, but 0 x NaN is NaN).  K rows past the end are masked after the
+// product, Q rows past the end are computed and not written.
+//
+// Tensor memory: S0 at 0, S1 at 128 (P overwrites the first half of its S as
+// packed bf16, rounded once to the MMA's operand type), O0 at 256, O1 at 256+D.
+#include <cuda_runtime.h>
+
+#include "packed.h"
+#include "sm103.cuh"
+
+namespace dash {
+
+using namespace dev;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsLaunch = 168;   // 384 threads x 168 registers
+constexpr int kRegsSoftmax = 208;  // a row of S in registers
+constexpr int kRegsOther = 88;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= kRegsLaunch * kThreads,
+              "register split exceeds the CTA's allocation");
+constexpr float kLazy = 8.f;       // log2 growth of a row's maximum that is left standing
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr uint32_t kPanel = 128 * 128;
+  static constexpr int kStages = D == 128 ? 5 : 8;  // K and V tiles in turn
+  static constexpr uint32_t oQ = 0;                 // two Q tiles
+  static constexpr uint32_t oKV = 2 * kTile;
+  static constexpr uint32_t oBAR = oKV + kStages * kTile;
+  static constexpr int kNumBars = 13 + 2 * kStages;
+  static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
+  static constexpr uint32_t kSmemBytes = oMISC + 16;
+  static constexpr uint32_t cO = 256;
+};
+static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory of one CTA");
+
+enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bVFixed = 10, bFinal = 11, bVTail = 12, bKvFull0 = 13 };
+
+__device__ __forceinline__ PackedFwdItem load_item(const PackedFwdItem *p) {
+  PackedFwdItem it;
+  const int4 *s = reinterpret_cast<const int4 *>(p);
+  int4 *d = reinterpret_cast<int4 *>(&it);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __ldg(s + i);
+  return it;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Ring position: stage and the parity of its current pass.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dash_packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const PackedFwdParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
+  uint64_t *kvFull = bars + bKvFull0, *kvEmpty = kvFull + C::kStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
+
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[bQFull + s], 1);
+      mbar_init(&bars[bQEmpty + s], 1);
+      mbar_init(&bars[bSFull + s], 1);
+      mbar_init(&bars[bPFull + s], 4);
+      mbar_init(&bars[bOFull + s], 1);
+    }
+    mbar_init(&bars[bVFixed], 1);
+    mbar_init(&bars[bFinal], 1);
+    mbar_init(&bars[bVTail], 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&kvFull[s], 1);
+      mbar_init(&kvEmpty[s], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
+  const int i_begin = p.cta_off[blockIdx.x], i_end = p.cta_off[blockIdx.x + 1];
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 9 && lane == 0) {
+      // -------------------------------------------------------------- TMA
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      Ring<C::kStages> r;
+      uint32_t q_ph[2] = {1, 1};     // parity to wait for on the empty barriers: the first pass is free
+      uint32_t q_fills[2] = {0, 0};
+      uint32_t fills = 0;
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedFwdItem it = load_item(p.items + i);
+        const int n = max(it.nkv[0], it.nkv[1]);
+        auto load_q = [&](int s, int row0, int head) {
+          mbar_wait(&bars[bQEmpty + s], q_ph[s], g);
+          q_ph[s] ^= 1;
+          if (*g.abort) return;
+          mbar_arrive_expect_tx(&bars[bQFull + s], C::kTile);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + C::oQ + s * C::kTile + pn * C::kPanel, &tmQ, &bars[bQFull + s], pn * 64, row0,
+                        head);
+          ++q_fills[s];
+        };
+        auto load_kv = [&](const CUtensorMap *m, int j) {
+          mbar_wait(&kvEmpty[r.st], r.ph ^ 1, g);
+          if (*g.abort) return;
+          mbar_arrive_expect_tx(&kvFull[r.st], C::kTile);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + C::oKV + r.st * C::kTile + pn * C::kPanel, m, &kvFull[r.st], pn * 64,
+                        it.kv_row0 + j * kPackedTile, it.kv_head);
+          ++fills;
+          r.next();
+        };
+        load_q(0, it.row0[0], it.head[0]);
+        load_kv(&tmK, 0);
+        if (it.nkv[1] > 0) load_q(1, it.row0[1], it.head[1]);
+        for (int j = 0; j < n; ++j) {
+          load_kv(&tmV, j);
+          if (j + 1 < n) load_kv(&tmK, j + 1);
+        }
+      }
+      // copies still in flight land before the CTA exits
+      for (int s = 0; s < 2; ++s)
+        if (q_fills[s]) mbar_drain(&bars[bQFull + s], (q_fills[s] - 1) & 1, g.limit_ns);
+      for (int s = 0; s < C::kStages; ++s) {
+        const uint32_t f = fills / C::kStages + ((uint32_t)s < fills % C::kStages ? 1u : 0u);
+        if (f) mbar_drain(&kvFull[s], (f - 1) & 1, g.limit_ns);
+      }
+    } else if (warp == 8 && lane == 0) {
+      // -------------------------------------------------------------- MMA
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
+      Ring<C::kStages> rk;              // next K or V tile to be read
+      uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, fix_ph = 0;
+      bool issued = false;
+      auto issue_s = [&](int s, int stage) {
+        const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
+        const uint64_t dk = sw128_desc(smem_u32(smem + C::oKV + stage * C::kTile), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + s * 128, dq + off, dk + off, idS, kk > 0);
+        }
+        tc_commit(&bars[bSFull + s]);
+      };
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedFwdItem it = load_item(p.items + i);
+        const int n = max(it.nkv[0], it.nkv[1]);
+        const bool fix = n * kPackedTile > it.kv_len;
+        // S of the first KV tile
+        mbar_wait(&kvFull[rk.st], rk.ph, g);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (it.nkv[s] == 0) continue;
+          mbar_wait(&bars[bQFull + s], q_ph[s], g);
+          q_ph[s] ^= 1;
+          if (*g.abort) continue;
+          tc_fence_after();
+          issue_s(s, rk.st);
+          issued = true;
+          if (it.nkv[s] == 1) tc_commit(&bars[bQEmpty + s]);
+        }
+        if (!*g.abort) tc_commit(&kvEmpty[rk.st]);
+        rk.next();
+        for (int j = 0; j < n; ++j) {
+          const Ring<C::kStages> rv = rk;  // V tile j; the next K tile follows it in the ring
+          rk.next();
+          mbar_wait(&kvFull[rv.st], rv.ph, g);
+          if (fix && j == n - 1) {
+            mbar_arrive(&bars[bVTail]);  // it has landed: its rows past the end may be cleared
+            mbar_wait(&bars[bVFixed], fix_ph, g);
+            fix_ph ^= 1;
+          }
+          if (j + 1 < n) mbar_wait(&kvFull[rk.st], rk.ph, g);
+          const uint64_t dv = sw128_desc(smem_u32(smem + C::oKV + rv.st * C::kTile), C::kPanel, 1024);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (j >= it.nkv[s]) continue;
+            mbar_wait(&bars[bPFull + s], p_ph[s], g);  // P stands in tensor memory, O is at its scale
+            p_ph[s] ^= 1;
+            if (*g.abort) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tmem + C::cO + s * D, tmem + s * 128 + kk * 8, dv + ((kk * 2048) >> 4), idO,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 < it.nkv[s]) {
+              issue_s(s, rk.st);  // MMAs run in issue order: PV has read P before S overwrites it
+              if (j + 2 == it.nkv[s]) tc_commit(&bars[bQEmpty + s]);
+            } else {
+              tc_commit(&bars[bOFull + s]);
+            }
+          }
+          if (!*g.abort) {
+            tc_commit(&kvEmpty[rv.st]);
+            if (j + 1 < n) tc_commit(&kvEmpty[rk.st]);
+          }
+          if (j + 1 < n) rk.next();
+        }
+      }
+      if (issued) {  // every MMA has completed before tensor memory is released
+        tc_commit(&bars[bFinal]);
+        mbar_drain(&bars[bFinal], 0, g.limit_ns);
+      }
+    } else if (warp == 10) {
+      // ------------------------------- V rows past the end of the sequence
+      uint32_t loads = 0, tail_ph = 0;
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedFwdItem it = load_item(p.items + i);
+        const int n = max(it.nkv[0], it.nkv[1]);
+        loads += 2 * n;  // the item's last V tile is its last load
+        if (n * kPackedTile > it.kv_len) {
+          mbar_wait(&bars[bVTail], tail_ph, g);
+          tail_ph ^= 1;
+          uint8_t *v = smem + C::oKV + (loads - 1) % C::kStages * C::kTile;
+          const int first = it.kv_len - (n - 1) * kPackedTile;
+          if (!warp_aborted(g)) {
+            // a row is 128 bytes of each panel, whatever the swizzle does inside it
+            for (int x = first * 8 + lane; x < kPackedTile * 8; x += 32)
+#pragma unroll
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                *reinterpret_cast<uint4 *>(v + pn * C::kPanel + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[bVFixed]);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int s = warp >> 2, sub = warp & 3;
+    const int L = sub * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
+    const uint32_t tS = tl + s * 128, tO = tl + C::cO + s * D;
+    uint32_t s_ph = 0, o_ph = 0;
+    for (int i = i_begin; i < i_end; ++i) {
+      const PackedFwdItem it = load_item(p.items + i);
+      const int n = s ? it.nkv[1] : it.nkv[0];
+      if (n == 0) continue;
+      const int q_pos = (s ? it.q0[1] : it.q0[0]) + L;
+      // keys this row attends: those of the sequence, up to its own position
+      const int limit = p.causal ? min(it.kv_len, q_pos + 1) : it.kv_len;
+      float m = -INFINITY;   // the maximum the row refers to (scaled, log2)
+      uint64_t l2 = 0;       // its sum, in two halves
+      for (int j = 0; j < n; ++j) {
+        mbar_wait(&bars[bSFull + s], s_ph, g);
+        s_ph ^= 1;
+        if (!warp_aborted(g)) {
+          tc_fence_after();
+          uint32_t x[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) reg_order32(x[c]);
+          const int cols = limit - j * kPackedTile;  // valid columns of this tile
+          if (__any_sync(0xffffffffu, cols < kPackedTile)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= cols) x[c][e] = 0xff800000u;  // -inf
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2)
+              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          if (j == 0) {
+            m = top == -INFINITY ? 0.f : top;
+          } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
+            // PV(j-1) completed before S(j) did, so O may be rewritten here
+            const float m_new = fmaxf(m, top);
+            const float f = ex2(m - m_new);
+            m = m_new;
+            const uint64_t f2 = pack2(f, f);
+            l2 = mul2(l2, f2);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t r[16];
+              tmem_ld16(tO + c0, r);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tmem_st16(tO + c0, r);
+            }
+          }
+          const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nm2 = pack2(-m, -m);
+          uint64_t acc2[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const uint64_t y2 =
+                  fma2(pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2);
+              float a, b;
+              unpack2(y2, a, b);
+              a = ex2(a);
+              b = ex2(b);
+              acc2[(e >> 1) & 1] = add2(acc2[(e >> 1) & 1], pack2(a, b));
+              pk[e >> 1] = pack_bf16(a, b);
+            }
+            tmem_st16(tS + 16 * c, pk);
+          }
+          l2 = add2(l2, add2(acc2[0], acc2[1]));
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[bPFull + s]);
+      }
+      // ------------------------------------------------------- epilogue
+      mbar_wait(&bars[bOFull + s], o_ph, g);
+      o_ph ^= 1;
+      if (!warp_aborted(g)) {
+        tc_fence_after();
+        float la, lb;
+        unpack2(l2, la, lb);
+        const float l = la + lb;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const bool ok = L < (s ? it.rows[1] : it.rows[0]);
+        const long long row = (long long)(s ? it.row0[1] : it.row0[0]) + L;
+        const int head = s ? it.head[1] : it.head[0];
+        __nv_bfloat16 *orow = p.o + row * p.o_row + head * p.o_head;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(tO + c0, r);
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 w;
+              w.x = pack_bf16(inv * __uint_as_float(r[8 * k + 0]), inv * __uint_as_float(r[8 * k + 1]));
+              w.y = pack_bf16(inv * __uint_as_float(r[8 * k + 2]), inv * __uint_as_float(r[8 * k + 3]));
+              w.z = pack_bf16(inv * __uint_as_float(r[8 * k + 4]), inv * __uint_as_float(r[8 * k + 5]));
+              w.w = pack_bf16(inv * __uint_as_float(r[8 * k + 6]), inv * __uint_as_float(r[8 * k + 7]));
+              *reinterpret_cast<uint4 *>(orow + c0 + 8 * k) = w;
+            }
+          }
+        }
+        if (ok) p.lse[head * p.lse_head + row] = (m + log2f(l)) * 0.6931471805599453f;
+        tc_fence_before();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int smem_bytes() {
+  return Cfg<D>::kSmemBytes > (uint32_t)kMinSmemOneCtaPerSm ? (int)Cfg<D>::kSmemBytes : kMinSmemOneCtaPerSm;
+}
+
+template <int D>
+cudaError_t prepare_t() {
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, dash_packed_fwd_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+  return cudaFuncSetAttribute(dash_packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smem_bytes<D>());
+}
+
+}  // namespace
+
+cudaError_t prepare_packed_fwd(int D) { return D == 64 ? prepare_t<64>() : prepare_t<128>(); }
+
+cudaError_t launch_packed_fwd(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                              const PackedFwdParams &p, int num_ctas, cudaStream_t stream) {
+  if (D == 64)
+    dash_packed_fwd_kernel<64><<<num_ctas, kThreads, smem_bytes<64>(), stream>>>(q, k, v, p);
+  else
+    dash_packed_fwd_kernel<128><<<num_ctas, kThreads, smem_bytes<128>(), stream>>>(q, k, v, p);
+  return cudaGetLastError();
+}
+
+}  // namespace dash

@@ -452,10 +452,120 @@ dash_status_t dash_cluster_links(const int32_t *tasks, const int32_t *cta_off, i
  * DASH_ERR_UNSUPPORTED if no two groups were found. */
 dash_status_t dash_die_map(dash_stream_t stream, int32_t *group_of_smid_out, int max_sm, int *n0, int *n1);
 
+/* ------------------------------------------- packed, grouped-head attention
+ * Sequences of different lengths in one [rows][heads][D] tensor, one after the
+ * other: sequence s owns the `lengths[s]` rows behind those of the sequences
+ * before it.  Hq Q heads share Hkv K/V heads: Q head h reads K/V head
+ * h / (Hq / Hkv).  Causal masking is square inside each sequence.  q, o, dout
+ * and dq are [rows][Hq][D], k, v, dk and dv [rows][Hkv][D], bf16; lse is fp32
+ * [Hq][rows].  Rows behind the last sequence are neither read as keys nor
+ * written; a sequence of length 0 has no rows.
+ *
+ * `strides` gives {row, head} strides in elements for each bf16 tensor in the
+ * order of the arguments (NULL: contiguous), so that the parts of a fused
+ * projection need no copies.  Strides are multiples of 8, at least D, and rows
+ * must not overlap; D itself is contiguous.  Outputs must not overlap inputs.
+ * K and V must be finite inside their sequence: as in dash_attn_fwd, a
+ * non-finite value of a key that the causal mask hides can still reach the
+ * rows of its own 128-row tile.  Values outside a sequence never reach it. */
+
+/* The tables of one set of lengths (host pointer, n_seqs values >= 0) on the
+ * current device: made once per batch, used by every layer's forward and, with
+ * backward != 0, backward.  Allocates device memory and copies (not to be
+ * called during a stream capture); read-only afterwards, so concurrent calls
+ * on any streams and captured graphs may share a plan.  It must outlive the
+ * work enqueued with it, replays of graphs included. */
+typedef struct dash_packed_plan_st dash_packed_plan_t;
+dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int D, int causal,
+                                      int backward, dash_packed_plan_t **plan_out);
+void dash_packed_plan_destroy(dash_packed_plan_t *plan);
+
+/* Forward: o and lse (as dash_attn_fwd defines them, per sequence).  `rows` is
+ * the row count of every tensor, at least the sum of the lengths; strides: q,
+ * k, v, o (8 values).  No workspace; can be captured. */
+dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
+                                   void *o, float *lse, long long rows, const int64_t *strides, float scale,
+                                   dash_stream_t stream);
+
+/* Backward: dq, dk, dv from the forward's inputs, o, lse and dout; dk and dv of
+ * a shared head are sums over its Q heads, in 32 bits.  The dQ reduction runs
+ * in the order of the plan's task table, so the gradients are bit-identical
+ * from run to run (for the same lengths on the same GPU model).  strides: q, k,
+ * v, o, dout, dq, dk, dv (16 values).  `workspace` is device memory of
+ * dash_packed_bwd_workspace(plan) bytes, 256-byte aligned, used until the
+ * call's work is done: calls that overlap need one each.  Can be captured. */
+dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
+                                   const void *o, const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                                   long long rows, const int64_t *strides, float scale, void *workspace,
+                                   long long workspace_bytes, dash_stream_t stream);
+/* Bytes of that workspace; -1 for a plan made without its backward. */
+long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan);
+
+/* The backward's task table for at most P CTAs, as dash_packed_plan_create
+ * builds it for the GPU's SM count (host only): {Q head, KV tile, Q tile,
+ * word} per task, tiles of 128 rows numbered over all sequences.  A chain is
+ * one KV tile of one K/V head with every Q head of its group; list scheduling
+ * puts each chain, a sequence's longest first, on the CTA that is free first,
+ * and a dQ tile's partials are added in the order in which the schedule
+ * reaches the tile (timed ranks).  tasks_out (4 values per task) and
+ * cta_off_out (P + 1 values) may be NULL to ask for the counts. */
+dash_status_t dash_build_packed_schedule(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int P,
+                                         int32_t *tasks_out, int32_t *cta_off_out, int *ctas_out,
+                                         long long *n_tasks_out);
+
+/* ------------------------------------------------------ paged key-value cache
+ * k_pages and v_pages are bf16 [n_pages][page_size][Hkv][D] (strides {page,
+ * token, head} in elements, multiples of 8 of at least D, in any order as long
+ * as rows do not overlap).  Token t of sequence b lies in page
+ * page_table[b][t / page_size] at t % page_size.  page_table is int32
+ * [B][max_pages]; entries behind a sequence's last page are not read.  A page
+ * outside [0, n_pages) that a call needs is left out (its tokens are not
+ * attended, not written) and dash_sync_status reports DASH_ERR_INVALID_ARG. */
+
+/* Attention of one new token per sequence over its cached tokens: q, o
+ * [B][Hq][D], lengths int32 [B] on the device (the tokens to attend, the new
+ * one's among them if it was written; values are clipped to [0, max_pages *
+ * page_size]).  lse, if not NULL, is fp32 [B][Hq].  A sequence of length 0
+ * gets o = 0 and lse = -inf.  Long sequences are split and joined; the split
+ * depends on the sequence's own length alone, so its results are the same
+ * bits in any batch.  strides (NULL: contiguous), 11 values: q {batch, head},
+ * o {batch, head}, k_pages {page, token, head}, v_pages, page_table row.
+ * `workspace`: dash_decode_workspace() bytes of device memory, 16-byte
+ * aligned, one per call in flight (0 bytes, NULL allowed, when the table has
+ * room for one split only).  Can be captured. */
+dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
+                               const int32_t *lengths, void *o, float *lse, int B, int Hq, int Hkv, int D,
+                               int n_pages, int page_size, int max_pages, const int64_t *strides, float scale,
+                               void *workspace, long long workspace_bytes, dash_stream_t stream);
+long long dash_decode_workspace(int B, int Hq, int D, int page_size, int max_pages);
+
+/* Writes new tokens' K and V rows ([n_tokens][Hkv][D], packed by sequence) into
+ * the cache: tokens cu_new[b] .. cu_new[b + 1] - 1 (int32 [B + 1], ascending
+ * from 0) become tokens starts[b], starts[b] + 1, ... of sequence b.  One token
+ * per sequence or whole prompts.  Tokens behind cu_new[B] are ignored.  A page
+ * that the call writes must belong to one sequence only (copy a shared page
+ * first).  strides, 11 values: k {token, head}, v {token, head}, k_pages,
+ * v_pages, page_table row. */
+dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void *v_pages,
+                               const int32_t *page_table, const int32_t *starts, const int32_t *cu_new,
+                               long long n_tokens, int B, int Hkv, int D, int n_pages, int page_size, int max_pages,
+                               const int64_t *strides, dash_stream_t stream);
+
+/* Copies pages inside the cache, K and V: page src[i] to page dst[i] (host
+ * lists, which travel in the launches' arguments).  Forking a sequence copies
+ * the page that both will write; compacting copies pages to lower numbers.
+ * DASH_ERR_INVALID_ARG for a page outside the cache, a destination named
+ * twice, or a page that is source and destination of one call (its order
+ * would matter).  strides, 6 values: k_pages, v_pages. */
+dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, const int32_t *dst, int n, int Hkv,
+                              int D, int n_pages, int page_size, const int64_t *strides, dash_stream_t stream);
+
 /* Synchronises `stream` and returns the device status of the calling
  * thread's current device workspace for that stream: DASH_OK, or
  * DASH_ERR_TIMEOUT if a bounded wait ran out since the last call (the word is
- * then cleared). */
+ * then cleared).  The packed and paged operators share one such word per
+ * device, read and cleared here too: DASH_ERR_TIMEOUT, or
+ * DASH_ERR_INVALID_ARG for a page outside the cache. */
 dash_status_t dash_sync_status(dash_stream_t stream);
 
 /* Frees the workspaces and cached schedule tables of the current device. */

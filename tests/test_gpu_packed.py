@@ -1,0 +1,233 @@
+"""Packed, grouped-head attention on the GPU against 64-bit plain forms: lengths
+from none to several tiles, shared heads, strides, garbage around the sequences,
+run-to-run bits, streams and captured graphs."""
+import math
+
+import pytest
+import torch
+
+import deterministic_attention_backward_fa_gb300 as dash
+
+import _packed as R
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def problem(lens, hq, hkv, D, extra=0, seed=1):
+    rows = sum(lens) + extra
+    q, do = R.normal(seed, rows, hq, D), R.normal(seed + 1, rows, hq, D)
+    k, v = R.normal(seed + 2, rows, hkv, D), R.normal(seed + 3, rows, hkv, D)
+    return q, k, v, do
+
+
+def check_forward(lens, q, k, v, causal, scale, o, lse):
+    n = sum(lens)
+    ro, rl, mag = R.forward(lens, q[:n], k[:n], v[:n], causal, scale)
+    R.within("O", o[:n], ro, mag)
+    # a score is a 32-bit sum of D products: its error and that of the logarithm, in absolute terms
+    assert (lse[:, :n].double() - rl[:, :n]).abs().max() <= 1e-4 if n else True
+
+
+def check_backward(lens, q, k, v, o, do, lse, causal, scale, grads):
+    n = sum(lens)
+    ref, mags = R.backward(lens, *(t[:n] for t in (q, k, v, o, do)), lse[:, :n], causal, scale)
+    for name, x, r, m in zip(("dQ", "dK", "dV"), grads, ref, mags):
+        R.within(name, x[:n], r, m)
+
+
+CASES = [([1], 1, 1, 64, True), ([128], 2, 1, 128, True), ([129, 1, 127], 4, 2, 64, True),
+         ([0, 5, 0, 300, 0], 6, 2, 128, True), ([257, 64, 0, 1], 4, 4, 64, False), ([1000, 3], 8, 1, 128, True),
+         ([200], 5, 1, 64, False), ([700, 513], 2, 2, 128, False), ([1300, 384, 31], 4, 4, 128, True),
+         (list(range(1, 60, 3)), 8, 2, 128, True), ([2049], 16, 4, 64, True), ([640], 3, 3, 128, True)]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,D,causal", CASES, ids=str)
+def test_forward_and_backward(lens, hq, hkv, D, causal):
+    q, k, v, do = problem(lens, hq, hkv, D)
+    scale = 1 / math.sqrt(D)
+    plan = dash.PackedPlan(lens, hq, hkv, D, causal=causal, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    dash.dash_sync_status()
+    check_forward(lens, q, k, v, causal, scale, o, lse)
+    grads = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    dash.dash_sync_status()
+    check_backward(lens, q, k, v, o, do, lse, causal, scale, grads)
+    again = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    o2, lse2 = dash.attn_packed_fwd(plan, q, k, v)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_strides_garbage_and_rows_behind(D, causal):
+    # parts of a fused projection whose every other element is NaN, rows behind the last sequence that must stay
+    lens, hq, hkv, extra = [130, 1, 0, 300], 4, 2, 37
+    n, rows = sum(lens), sum(lens) + extra
+    src = problem(lens, hq, hkv, D, extra, seed=11)
+    fused = torch.full((rows + 3, 3 * hq + 3, D), NAN, dtype=torch.bfloat16, device="cuda")
+    q, k, v = fused[1:1 + rows, :hq], fused[1:1 + rows, hq:hq + hkv], fused[1:1 + rows, hq + hkv:hq + 2 * hkv]
+    headfirst = torch.full((hq + 1, rows, D), NAN, dtype=torch.bfloat16, device="cuda")
+    do = headfirst[:hq].transpose(0, 1)
+    for dst, t in zip((q, k, v, do), src):
+        dst[:n] = t[:n]
+    keep = 3.0
+    out = torch.full((rows, 2 * hq + 2 * hkv, D + 8), keep, dtype=torch.bfloat16, device="cuda")
+    o, dq = out[:, :hq, :D], out[:, hq:2 * hq, :D]
+    dk, dv = out[:, 2 * hq:2 * hq + hkv, :D], out[:, 2 * hq + hkv:, :D]
+    lse = torch.full((hq, rows), keep, device="cuda")
+    scale = 0.11
+    plan = dash.PackedPlan(lens, hq, hkv, D, causal=causal, backward=True)
+    ws = torch.full((plan.workspace_bytes,), 255, dtype=torch.uint8, device="cuda")  # NaN in every float
+    dash.dash_attn_packed_fwd(plan, q, k, v, o, lse, scale)
+    dash.dash_attn_packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, scale, ws)
+    dash.dash_sync_status()
+    check_forward(lens, q, k, v, causal, scale, o, lse)
+    check_backward(lens, q, k, v, o, do, lse, causal, scale, (dq, dk, dv))
+    assert (out[n:] == keep).all() and (out[:, :, D:] == keep).all() and (lse[:, n:] == keep).all()
+    # contiguous tensors give the same bits
+    oc, lc = dash.attn_packed_fwd(plan, *(t.contiguous() for t in (q, k, v)), scale)
+    gc = dash.attn_packed_bwd(plan, *(t.contiguous() for t in (q, k, v, o, do)), lse.contiguous(), scale)
+    for a, b in zip((oc, *gc), (o, dq, dk, dv)):
+        assert torch.equal(a[:n], b[:n]) and not a[n:].any()
+    assert torch.equal(lc[:, :n], lse[:, :n]) and (lc[:, n:] == float("-inf")).all()
+
+
+def test_sequences_do_not_touch_each_other():
+    # NaN and infinities in one sequence leave the others' bits as they are
+    lens, hq, hkv, D = [70, 150, 40], 4, 2, 128
+    q, k, v, do = problem(lens, hq, hkv, D, seed=21)
+    plan = dash.PackedPlan(lens, hq, hkv, D, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    g = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    bad = [t.clone() for t in (q, k, v, do)]
+    for t, x in zip(bad, (NAN, float("inf"), NAN, float("-inf"))):
+        t[70:220] = x
+    o2, lse2 = dash.attn_packed_fwd(plan, *bad[:3])
+    g2 = dash.attn_packed_bwd(plan, *bad[:3], o2, bad[3], lse2)
+    dash.dash_sync_status()
+    for a, b in zip((o, *g), (o2, *g2)):
+        assert torch.equal(a[:70], b[:70]) and torch.equal(a[220:], b[220:])
+    assert torch.equal(lse[:, :70], lse2[:, :70]) and torch.equal(lse[:, 220:], lse2[:, 220:])
+
+
+def test_forward_does_not_depend_on_the_batch():
+    # a sequence's forward bits are the same alone and packed between others
+    D, hq, hkv = 128, 6, 2
+    q, k, v, _ = problem([333], hq, hkv, D, seed=31)
+    alone = dash.attn_packed_fwd(dash.PackedPlan([333], hq, hkv, D), q, k, v)
+    pad = [torch.cat([R.normal(40 + i, 200, t.shape[1], D), t, R.normal(50 + i, 55, t.shape[1], D)])
+           for i, t in enumerate((q, k, v))]
+    o, lse = dash.attn_packed_fwd(dash.PackedPlan([200, 333, 55], hq, hkv, D), *pad)
+    assert torch.equal(o[200:533], alone[0]) and torch.equal(lse[:, 200:533], alone[1])
+
+
+def test_scores_of_every_size():
+    # rows whose maximum grows from tile to tile (the running maximum moves), and scores far from zero
+    D, lens = 64, [900]
+    q, k, v, do = problem(lens, 2, 1, D, seed=61)
+    k = (k.float() * torch.linspace(0.1, 6.0, 900, device="cuda")[:, None, None]).bfloat16()
+    q = (q.float() * 3).bfloat16()
+    plan = dash.PackedPlan(lens, 2, 1, D, causal=False, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v, 0.5)
+    dash.dash_sync_status()
+    ro, rl, mag = R.forward(lens, q, k, v, False, 0.5)
+    # scores reach 0.5 * 3 * 6 * 64 = 576 and more: a 32-bit sum of D products of that size is off by about
+    # D * 2^-24 * 2000 < 2^-7 at most, which moves every p by less than 2^-6 of itself
+    assert (lse.double() - rl).abs().max() <= 2 ** -7
+    assert ((o.double() - ro).abs() <= R.bound(ro, mag) + 2 ** -6 * mag).all()
+
+
+def test_against_the_dense_attention():
+    # equal lengths: the framework's dense forward and backward on the same values
+    B, H, S, D = 2, 3, 256, 128
+    q, k, v, do = problem([S] * B, H, H, D, seed=71)
+    plan = dash.PackedPlan([S] * B, H, H, D, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    g = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    dense = lambda t: t.reshape(B, S, H, D).transpose(1, 2).contiguous()
+    do_, lse_ = dash.attn_fwd(dense(q), dense(k), dense(v), True)
+    dg = dash.attn_bwd(dense(q), dense(k), dense(v), dense(o), dense(do),
+                       lse.reshape(H, B, S).transpose(0, 1).contiguous(), True, schedule="serial")
+    dash.dash_sync_status()
+    for a, b in zip((o, *g), (do_, *dg)):
+        # both are within U of the sums' magnitudes of the exact value; rows here have magnitudes below 8
+        assert (dense(a).float() - b.float()).abs().max() <= 4 * R.U * 8
+    assert (lse.reshape(H, B, S).transpose(0, 1) - lse_).abs().max() <= 1e-4
+
+
+def test_streams_and_captured_graphs():
+    lens, hq, hkv, D = [300, 77], 4, 2, 64
+    q, k, v, do = problem(lens, hq, hkv, D, seed=81)
+    plan = dash.PackedPlan(lens, hq, hkv, D, backward=True)
+
+    def step():
+        o, lse = dash.attn_packed_fwd(plan, q, k, v)
+        return (o, lse, *dash.attn_packed_bwd(plan, q, k, v, o, do, lse))
+
+    want = step()
+    side = torch.cuda.Stream()
+    o, lse = dash.attn_packed_fwd(plan, q, k, v, stream=side)
+    g = dash.attn_packed_bwd(plan, q, k, v, o, do, lse, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (o, lse, *g)))
+    # two captures whose replays overlap: each has its own workspace and outputs
+    graphs, outs = [], []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(step())
+        graphs.append(gr)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        eager = step()
+    torch.cuda.synchronize()
+    dash.dash_sync_status()
+    for got in (*outs, eager):
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_empty_problems():
+    for lens in ([], [0, 0]):
+        plan = dash.PackedPlan(lens, 2, 1, 64, backward=True)
+        q, k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda"), R.normal(1, 3, 1, 64)
+        o, lse = dash.attn_packed_fwd(plan, q, k, k)
+        assert not o.any() and (lse == float("-inf")).all()
+        g = dash.attn_packed_bwd(plan, q, k, k, o, q, lse)
+        assert not any(t.any() for t in g)
+
+
+def test_refusals():
+    q, k, v, do = problem([40], 4, 2, 64, seed=91)
+    plan = dash.PackedPlan([40], 4, 2, 64)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    with pytest.raises(dash.DashError, match="without its backward"):
+        dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    with pytest.raises(ValueError):
+        dash.attn_packed_fwd(plan, q, k[:39], v)
+    with pytest.raises(ValueError):
+        dash.attn_packed_fwd(plan, q.float(), k, v)
+    with pytest.raises(ValueError):
+        dash.attn_packed_fwd(plan, q[:, :2], k, v)
+    with pytest.raises(dash.DashError, match="fewer"):
+        dash.attn_packed_fwd(plan, q[:39], k[:39], v[:39])
+    with pytest.raises(dash.DashError, match="strides"):
+        dash.attn_packed_fwd(plan, q, k[:, :1].expand(40, 2, 64), v)
+    with pytest.raises(dash.DashError, match="aligned"):
+        dash.attn_packed_fwd(plan, torch.empty(40 * 4 * 64 + 1, dtype=q.dtype, device="cuda")[1:].view(40, 4, 64), k, v)
+    bp = dash.PackedPlan([40], 4, 2, 64, backward=True)
+    ws = torch.empty(bp.workspace_bytes - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(dash.DashError, match="workspace"):
+        dash.dash_attn_packed_bwd(bp, q, k, v, o, do, lse, torch.empty_like(q), torch.empty_like(k),
+                                  torch.empty_like(v), 0.1, ws)

@@ -1,0 +1,286 @@
+"""The paged cache on the GPU: decode attention, writing and copying pages,
+against 64-bit plain forms and torch's own indexing."""
+import math
+
+import pytest
+import torch
+
+import deterministic_attention_backward_fa_gb300 as dash
+
+import _packed as R
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cache(lens, hkv, D, page, seed=1, spare=3, width=None):
+    """Pages in random order; page table entries behind a sequence's last page point nowhere."""
+    need = [-(-n // page) for n in lens]
+    n_pages = sum(need) + spare
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    order = torch.randperm(n_pages, generator=g, device="cuda").int()
+    table = torch.full((len(lens), width or max(need + [1])), 2**31 - 1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return R.normal(seed, n_pages, page, hkv, D), R.normal(seed + 1, n_pages, page, hkv, D), table
+
+
+def check(q, kp, vp, table, lengths, scale, o, lse):
+    ro, rl, mag = R.decode(q, kp, vp, table, lengths, scale)
+    R.within("O", o, ro, mag)
+    none = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), none)
+    assert (lse.double() - rl)[~none].abs().max() <= 1e-4 if (~none).any() else True
+
+
+CASES = [([1], 1, 1, 64, 16), ([0, 5, 0], 4, 2, 128, 16), ([64, 63, 65, 256, 257, 255], 8, 2, 128, 16),
+         ([300, 1000, 17], 6, 2, 64, 24), ([2000, 1], 32, 1, 128, 64), ([777] * 3, 20, 1, 64, 1),
+         ([40000, 3], 4, 4, 128, 128), ([33000, 65], 3, 1, 64, 7), (list(range(0, 900, 5)), 2, 1, 64, 32)]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,D,page", CASES, ids=lambda x: str(x)[:40])
+def test_decode(lens, hq, hkv, D, page):
+    kp, vp, table = cache(lens, hkv, D, page)
+    # whatever stands behind a sequence's last token is not read into its result
+    for b, n in enumerate(lens):
+        if n % page:
+            last = table[b, n // page].long()
+            kp[last, n % page:], vp[last, n % page:] = NAN, NAN
+    q = R.normal(9, len(lens), hq, D)
+    o, lse = dash.attn_decode(q, kp, vp, table, i32(lens))
+    dash.dash_sync_status()
+    check(q, kp, vp, table, lens, 1 / math.sqrt(D), o, lse)
+    o2, lse2 = dash.attn_decode(q, kp, vp, table, i32(lens))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_does_not_depend_on_the_batch():
+    # the same bits alone, in a batch, and under a wider page table
+    lens, hq, hkv, D, page = [5000, 130, 20000, 1], 8, 2, 128, 16
+    kp, vp, table = cache(lens, hkv, D, page, width=4000)
+    q = R.normal(5, 4, hq, D)
+    o, lse = dash.attn_decode(q, kp, vp, table, i32(lens))
+    for b, n in enumerate(lens):
+        w = -(-n // page)
+        ob, lb = dash.attn_decode(q[b:b + 1], kp, vp, table[b:b + 1, :w].contiguous(), i32([n]))
+        assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0])
+
+
+def test_decode_strides_and_lengths_out_of_range():
+    lens, hq, hkv, D, page = [100, 700, 31], 8, 2, 64, 16
+    kp, vp, table = cache(lens, hkv, D, page)
+    want = dash.attn_decode(R.normal(6, 3, hq, D), kp, vp, table, i32(lens))
+    # a head-first cache, K and V side by side in one tensor, Q a part of a fused row, a table inside a larger one
+    both = torch.full((kp.shape[0], 2, hkv, page, D), NAN, dtype=kp.dtype, device="cuda")
+    k2, v2 = both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2)
+    k2.copy_(kp)
+    v2.copy_(vp)
+    fused = torch.full((3, hq + 4, D), NAN, dtype=kp.dtype, device="cuda")
+    q2 = fused[:, 2:2 + hq]
+    q2.copy_(R.normal(6, 3, hq, D))
+    t2 = torch.full((3, table.shape[1] + 9), -5, dtype=torch.int32, device="cuda")
+    t2[:, :table.shape[1]] = table
+    got = dash.attn_decode(q2, k2, v2, t2[:, :table.shape[1]], i32(lens))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # lengths are clipped to the table
+    small, full = table[:, :2].contiguous(), i32([32, 32, 31])
+    a = dash.attn_decode(q2, kp, vp, small, i32([-4, 10**9, 31]))
+    b = dash.attn_decode(q2, kp, vp, small, full)
+    dash.dash_sync_status()
+    assert torch.equal(a[0][1:], b[0][1:]) and not a[0][0].any() and (a[1][0] == float("-inf")).all()
+
+
+def test_bad_pages_are_reported_and_left_out():
+    lens, hq, hkv, D, page = [70, 40], 4, 2, 128, 16
+    kp, vp, table = cache(lens, hkv, D, page)
+    q = R.normal(7, 2, hq, D)
+    for bad in (-1, kp.shape[0], 2**31 - 1):
+        t = table.clone()
+        t[0, 1] = bad
+        o, lse = dash.attn_decode(q, kp, vp, t, i32(lens))
+        with pytest.raises(dash.DashError, match="outside the cache"):
+            dash.dash_sync_status()
+        dash.dash_sync_status()  # cleared
+        check(q, kp, vp, t, lens, 1 / math.sqrt(D), o, lse)
+
+
+def test_masked_out_scores_and_large_offsets():
+    # scores of -inf (a K row of -inf against a positive Q) weigh nothing; a cache of more than 2^31 elements
+    hq, hkv, D, page = 4, 4, 128, 64
+    n_pages = (2**31 // (page * hkv * D)) + 40
+    kp = torch.zeros(n_pages, page, hkv, D, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    pages = [n_pages - 1, 3, n_pages - 20, n_pages - 2]
+    for i, p in enumerate(pages):
+        kp[p], vp[p] = R.normal(100 + i, page, hkv, D), R.normal(200 + i, page, hkv, D)
+    kp[pages[1], 5:9] = float("-inf")
+    q = R.normal(8, 1, hq, D).abs()
+    table = i32([pages])
+    o, lse = dash.attn_decode(q, kp, vp, table, i32([250]))
+    dash.dash_sync_status()
+    check(q, kp, vp, table, [250], 1 / math.sqrt(D), o, lse)
+    dash.cache_copy(kp, vp, [n_pages - 1, n_pages - 2], [0, n_pages - 5])
+    assert torch.equal(kp[0], kp[-1]) and torch.equal(vp[-5], vp[-2])
+    k1 = R.normal(300, 3, hkv, D)
+    dash.cache_write(k1, k1, kp, vp, i32([[n_pages - 7]]), i32([61]), i32([0, 3]))
+    dash.dash_sync_status()
+    assert torch.equal(kp[-7, 61:], k1) and torch.equal(vp[-7, 61:], k1) and not kp[-7, :61].any()
+
+
+@pytest.mark.parametrize("hkv,D,page", [(1, 64, 16), (8, 128, 16), (3, 64, 1), (2, 128, 7)])
+def test_write(hkv, D, page):
+    starts, news = [0, 5, 31, 0, 16], [1, 40, 0, 33, 16]
+    lens = [a + b for a, b in zip(starts, news)]
+    kp, vp, table = cache(lens, hkv, D, page, seed=3)
+    cu = [sum(news[:i]) for i in range(len(news) + 1)]
+    extra = 4  # tokens behind the last sequence
+    fused = R.normal(4, cu[-1] + extra, 2 * hkv + 1, D)
+    k, v = fused[:, 1:1 + hkv], fused[:, 1 + hkv:]
+    wk, wv = kp.clone(), vp.clone()
+    for b, n in enumerate(news):
+        for i in range(n):
+            pos = starts[b] + i
+            wk[table[b, pos // page].long(), pos % page] = k[cu[b] + i]
+            wv[table[b, pos // page].long(), pos % page] = v[cu[b] + i]
+    dash.cache_write(k, v, kp, vp, table, i32(starts), i32(cu))
+    dash.dash_sync_status()
+    assert torch.equal(kp, wk) and torch.equal(vp, wv)
+
+
+def test_write_outside_the_cache_is_reported():
+    kp, vp, table = cache([32, 32], 2, 64, 16)
+    k = R.normal(2, 4, 2, 64)
+    table[1, 1] = -1
+    for starts in ([0, 15], [0, 40], [0, -3]):
+        wk = kp.clone()
+        dash.cache_write(k, k, kp, vp, table, i32(starts), i32([0, 2, 4]))
+        with pytest.raises(dash.DashError, match="outside the cache"):
+            dash.dash_sync_status()
+        wk[table[0, 0].long(), :2] = k[:2]
+        for i in (2, 3):
+            pos = starts[1] + i - 2
+            if 0 <= pos < 16:
+                wk[table[1, 0].long(), pos] = k[i]
+        assert torch.equal(kp, wk)
+
+
+@pytest.mark.parametrize("hkv,D,page,n", [(1, 64, 1, 5), (2, 128, 16, 64), (3, 64, 24, 65), (8, 128, 16, 3600)])
+def test_copy(hkv, D, page, n):
+    n_pages = 2 * n + 3
+    kp, vp = R.normal(1, n_pages, page, hkv, D), R.normal(2, n_pages, page, hkv, D)
+    perm = torch.randperm(n_pages, generator=torch.Generator().manual_seed(5))
+    src, dst = perm[:n], perm[n:2 * n]
+    src[n // 2] = src[0]  # a page may be copied to several
+    wk, wv = kp.clone(), vp.clone()
+    wk[dst], wv[dst] = kp[src], vp[src]
+    hk, hv = kp.transpose(1, 2).contiguous().transpose(1, 2), vp.transpose(1, 2).contiguous().transpose(1, 2)
+    dash.cache_copy(kp, vp, src, dst)
+    dash.cache_copy(hk, hv, src.tolist(), dst.tolist())
+    dash.cache_copy(kp, vp, [], [])
+    dash.dash_sync_status()
+    for got, want in ((kp, wk), (vp, wv), (hk, wk), (hv, wv)):
+        assert torch.equal(got, want)
+
+
+def test_refusals():
+    kp, vp, table = cache([32], 2, 64, 16)
+    q = R.normal(1, 1, 4, 64)
+    n = i32([32])
+    for bad in (lambda: dash.attn_decode(q.float(), kp, vp, table, n), lambda: dash.attn_decode(q, kp, vp[1:], table, n),
+                lambda: dash.attn_decode(q, kp, vp, table.long(), n), lambda: dash.attn_decode(q, kp, vp, table, n.long()),
+                lambda: dash.attn_decode(q, kp, vp, table, i32([1, 2])),
+                lambda: dash.attn_decode(q, kp, vp, table.cpu(), n), lambda: dash.cache_copy(kp, vp, [0], [1, 2])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(dash.DashError, match="overlap|strides"):
+        dash.attn_decode(q, kp[:, :, :1].expand(-1, -1, 2, -1), vp, table, n)
+    with pytest.raises(dash.DashError, match="twice"):
+        dash.cache_copy(kp, vp, [0, 1], [2, 2])
+
+
+def test_prompt_cache_fork_and_decode_together():
+    # two prompts go through the packed forward and into the cache, the first is forked (sharing its full pages,
+    # copying its last one), and all three take new tokens: each decode equals the last row of a packed forward
+    hq, hkv, D, page, lens = 8, 2, 128, 16, [150, 37]
+    q, k, v = R.normal(1, 187, hq, D), R.normal(2, 187, hkv, D), R.normal(3, 187, hkv, D)
+    kp, vp, table = cache([200, 200, 200], hkv, D, page, seed=4)
+    dash.cache_write(k, v, kp, vp, table[:2], i32([0, 0]), i32([0, 150, 187]))
+    own = table[2, 150 // page].clone()
+    table[2, :150 // page] = table[0, :150 // page]
+    dash.cache_copy(kp, vp, [int(table[0, 150 // page])], [int(own)])
+    hist = [[t[:150] for t in (k, v)], [t[150:] for t in (k, v)], [t[:150] for t in (k, v)]]
+    n = i32([150, 37, 150])
+    cu = i32([0, 1, 2, 3])
+    side = torch.cuda.Stream()
+    for step in range(20):
+        kn, vn, qn = (R.normal(50 + 3 * step + i, 3, h, D) for i, h in enumerate((hkv, hkv, hq)))
+        hist = [[torch.cat([a, x[b:b + 1]]) for a, x in zip(hist[b], (kn, vn))] for b in range(3)]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):  # tensors made on another stream
+            dash.cache_write(kn, vn, kp, vp, table, n, cu)
+            n = n + 1
+            o, lse = dash.attn_decode(qn, kp, vp, table, n)
+        side.synchronize()
+    dash.dash_sync_status()
+    for b in range(3):
+        kk, vv = hist[b]
+        x = torch.einsum("hgd,thd->hgt", qn[b].double().view(hkv, -1, D), kk.double()) / math.sqrt(D)
+        p = torch.softmax(x, -1)
+        R.within("O", o[b], torch.einsum("hgt,thd->hgd", p, vv.double()).reshape(hq, D),
+                 torch.einsum("hgt,thd->hgd", p, vv.double().abs()).reshape(hq, D))
+        rows = len(kk)
+        qq = torch.zeros(rows, hq, D, dtype=q.dtype, device="cuda")
+        qq[-1] = qn[b]
+        of, _ = dash.attn_packed_fwd(dash.PackedPlan([rows], hq, hkv, D), qq, kk, vv)
+        R.within("decode and forward", of[-1], torch.einsum("hgt,thd->hgd", p, vv.double()).reshape(hq, D),
+                 torch.einsum("hgt,thd->hgd", p, vv.double().abs()).reshape(hq, D))
+
+
+def test_decode_in_captured_graphs():
+    lens, hq, hkv, D, page = [3000, 41], 8, 2, 128, 16
+    kp, vp, table = cache(lens, hkv, D, page)
+    q, n = R.normal(3, 2, hq, D), i32(lens)
+    kn, cu = R.normal(4, 2, hkv, D), i32([0, 1, 2])
+    want = dash.attn_decode(q, kp, vp, table, n)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(dash.attn_decode(q, kp, vp, table, n))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for got in outs:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # a replay reads the lengths and pages as they are then
+    w = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(w):
+        dash.cache_write(kn, kn, kp, vp, table, n - 1, cu)
+        n2 = dash.attn_decode(q, kp, vp, table, n)
+    w.replay()
+    torch.cuda.synchronize()
+    dash.dash_sync_status()
+    check(q, kp, vp, table, lens, 1 / math.sqrt(D), *n2)
+    n -= 5
+    w.replay()
+    torch.cuda.synchronize()
+    dash.dash_sync_status()
+    check(q, kp, vp, table, [x - 5 for x in lens], 1 / math.sqrt(D), *n2)

@@ -1,0 +1,139 @@
+"""Packed attention and paged cache, what needs no GPU: the task tables, the
+refusals, and the plain 64-bit forms the GPU tests compare with."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import deterministic_attention_backward_fa_gb300 as dash
+
+import _packed as R
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+LENS = [[1], [128], [129, 1, 127], [0, 5, 0, 300, 0], [], [0], [1000, 3, 257], [4000], list(range(1, 40))]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 2), (6, 2), (8, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_task_table_is_complete_and_can_finish(lens, hq, hkv, causal):
+    for P in (1, 7, 152):
+        tasks, off = dash.dash_build_packed_schedule(lens, hq, hkv, causal, P)
+        tiles = [(s, i) for s, n in enumerate(lens) for i in range(-(-n // 128))]
+        want = {(h, a, b) for h in range(hq) for a, (sa, ia) in enumerate(tiles) for b, (sb, ib) in enumerate(tiles)
+                if sa == sb and (not causal or ib >= ia)}
+        assert {tuple(t[:3]) for t in tasks.tolist()} == want and len(tasks) == len(want)
+        assert off[0] == 0 and off[-1] == len(tasks) and (np.diff(off) >= 0).all() and len(off) - 1 <= P
+        order = {}
+        for c in range(len(off) - 1):
+            run = None
+            for i in range(off[c], off[c + 1]):
+                h, kv, q, w = (int(x) for x in tasks[i])
+                order.setdefault((h, q), []).append((w & dash.TASK_RANK_MASK, i - off[c], c))
+                if w & dash.TASK_FIRST:
+                    assert run is None
+                    run, heads = kv, set()
+                assert run == kv
+                heads.add(h)
+                if w & dash.TASK_LAST:  # every head of the group, so dK and dV are whole
+                    assert heads == set(range(h // (hq // hkv) * (hq // hkv), h + 1)) and len(heads) == hq // hkv
+                    run = None
+            assert run is None
+        for v in order.values():
+            v.sort()
+            assert [r for r, _, _ in v] == list(range(len(v)))
+            steps = [(i, c) for _, i, c in v]
+            # a rank's step comes before its successor's: (step, CTA) orders all tasks, so no waits form a cycle
+            assert steps == sorted(steps)
+
+
+def test_schedule_refusals():
+    for args, word in ((([-1], 4, 2, True, 8), "negative"), (([5], 4, 3, True, 8), "multiple"),
+                       (([5], 4, 0, True, 8), "multiple"), (([5], 4, 2, True, 0), "out of range"),
+                       (([2**31 - 1, 2**31 - 1], 1, 1, True, 8), "rows")):
+        with pytest.raises(dash.DashError, match=word) as ei:
+            dash.dash_build_packed_schedule(*args)
+        assert ei.value.code == 1
+    with pytest.raises(dash.DashError, match="32-bit") as ei:
+        dash.dash_build_packed_schedule([1 << 24], 64, 8, True, 152)
+    assert ei.value.code == 2
+
+
+def _nul(n):
+    return [ctypes.c_void_p(0)] * n
+
+
+def test_refusals_before_any_device_call():
+    L, nul = dash.lib(), ctypes.c_void_p(0)
+    fake = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced
+    out = ctypes.c_void_p()
+    lens = (ctypes.c_int32 * 2)(5, -7)
+    assert L.dash_packed_plan_create(lens, 2, 4, 2, 64, 1, 0, ctypes.byref(out)) == 1
+    assert "negative" in dash.dash_last_error()
+    assert L.dash_packed_plan_create(lens, 1, 4, 2, 96, 1, 0, ctypes.byref(out)) == 2
+    assert L.dash_packed_plan_create(lens, 1, 4, 3, 64, 1, 0, ctypes.byref(out)) == 1
+    assert L.dash_packed_plan_create(None, 1, 4, 2, 64, 1, 0, ctypes.byref(out)) == 1
+    assert L.dash_packed_plan_create(lens, 1, 4, 2, 64, 1, 0, None) == 1
+    assert L.dash_attn_packed_fwd(nul, *_nul(5), 5, None, 0.1, nul) == 1 and "plan" in dash.dash_last_error()
+    assert L.dash_attn_packed_fwd(nul, *_nul(5), 5, None, -1.0, nul) == 1 and "scale" in dash.dash_last_error()
+    assert L.dash_packed_bwd_workspace(nul) == -1
+
+    def decode(ptr=fake, B=2, hq=4, hkv=2, D=64, pages=8, page=16, width=4, strides=None, scale=0.1, ws=None, n=0):
+        return L.dash_attn_decode(ptr, ptr, ptr, ptr, ptr, ptr, nul, B, hq, hkv, D, pages, page, width, strides,
+                                  scale, ws, n, nul)
+
+    bad = lambda *v: (ctypes.c_int64 * 11)(*v)
+    good = (256, 64, 256, 64, 2048, 128, 64, 2048, 128, 64, 4)
+    for code, word, kw in ((2, "head dim", {"D": 96}), (1, "multiple", {"hq": 5}), (1, "scale", {"scale": 0.0}),
+                           (1, "null pointer", {"ptr": nul}), (1, "aligned", {"ptr": ctypes.c_void_p((1 << 20) + 8)}),
+                           (1, "pages", {"pages": 0}), (2, "2^31", {"width": 1 << 28}), (2, "65535", {"B": 70000}),
+                           (1, "workspace", {"width": 1024}), (1, ">= 0", {"B": -1}),
+                           (1, "strides", {"strides": bad(255, *good[1:])}),
+                           (1, "overlap", {"strides": bad(*good[:4], 2048, 128, 128, *good[7:])}),
+                           (1, "overlap", {"strides": bad(64, 64, *good[2:])}),
+                           (1, "table rows", {"strides": bad(*good[:10], 3)})):
+        assert decode(**kw) == code, kw
+        assert word in dash.dash_last_error(), (kw, dash.dash_last_error())
+    assert decode(B=0) == 0
+    copy = lambda s, d, pages=8: L.dash_cache_copy(fake, fake, (ctypes.c_int32 * len(s))(*s),
+                                                   (ctypes.c_int32 * len(d))(*d), len(s), 2, 64, pages, 16, None, nul)
+    for s, d, word in (([0, 1], [2, 2], "twice"), ([0, 2], [2, 3], "source and a destination"),
+                       ([3], [3], "source and a destination"), ([8], [1], "outside"), ([-1], [1], "outside"),
+                       ([1], [8], "outside"), ([1], [-2], "outside")):
+        assert copy(s, d) == 1 and word in dash.dash_last_error()
+    write = lambda n=4, B=2, D=64, page=16: L.dash_cache_write(*[fake] * 7, n, B, 2, D, 8, page, 4, None, nul)
+    assert write(n=-1) == 1 and write(D=80) == 2 and write(page=0) == 1 and write(n=0) == 0 and write(B=0) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        dash._rows("q", q)
+    with pytest.raises(ValueError, match="CUDA bfloat16"):
+        dash.cache_copy(torch.zeros(2, 3, 4, 64), torch.zeros(2, 3, 4, 64), [0], [1])
+    with pytest.raises(ValueError, match="32 bits"):
+        dash.dash_packed_plan_create([2**40], 4, 2, 64, True, False)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_plain_backward_against_differences(causal):
+    # the 64-bit backward that the GPU tests compare with, against central differences of the 64-bit forward
+    lens, hq, hkv, D, scale, h = [5, 1, 9], 4, 2, 8, 0.3, 1e-5
+    g = torch.Generator().manual_seed(3)
+    q, do = (torch.randn(15, hq, D, generator=g, dtype=R.F64) for _ in range(2))
+    k, v = (torch.randn(15, hkv, D, generator=g, dtype=R.F64) for _ in range(2))
+    loss = lambda a, b, c: (R.forward(lens, a, b, c, causal, scale)[0] * do).sum()
+    o, lse, _ = R.forward(lens, q, k, v, causal, scale)
+    grads, _ = R.backward(lens, q, k, v, o, do, lse, causal, scale)
+    for i in range(3):
+        d = torch.randn([q, k, v][i].shape, generator=g, dtype=R.F64)
+        args = lambda s: [t + s * h * d if j == i else t for j, t in enumerate((q, k, v))]
+        diff = (loss(*args(1)) - loss(*args(-1))) / (2 * h)
+        assert abs(diff - (grads[i] * d).sum()) <= 1e-7 * (1 + abs(diff))
