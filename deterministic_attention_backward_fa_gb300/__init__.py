@@ -12,6 +12,7 @@ function without it raises, there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import math
@@ -427,10 +428,18 @@ def _on(device, stream, tensors):
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, not to {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _device(dev):
+    """Makes ``dev`` current, at no cost when it is already."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _rows(name, t, heads=None, dim=None, rows=None):
@@ -532,7 +541,7 @@ def dash_attn_packed_fwd(plan: PackedPlan, q, k, v, o, lse, scale: float, stream
         _rows(name, t, h, plan.head_dim, rows)
     _plain("lse", lse, torch.float32, (plan.heads, rows), dev)
     st = _on(dev, stream, (("q", q), ("k", k), ("v", v), ("o", o)))
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().dash_attn_packed_fwd(plan._handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                           lse.data_ptr(), rows, _strides(q, k, v, o), float(scale), st))
 
@@ -546,7 +555,7 @@ def dash_attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, dq, dk, dv, scal
     _plain("lse", lse, torch.float32, (hq, rows), dev)
     _plain("workspace", workspace, torch.uint8, (None,), dev)
     st = _on(dev, stream, [(n, t) for n, t, _ in named])
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().dash_attn_packed_bwd(plan._handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                           do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                           rows, _strides(q, k, v, o, do, dq, dk, dv), float(scale),
@@ -592,7 +601,7 @@ def dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale: fl
     if workspace is not None:
         _plain("workspace", workspace, torch.uint8, (None,), dev)
     st = _on(dev, stream, (("o", o), ("k_pages", k_pages), ("v_pages", v_pages)))
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().dash_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                       lengths.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
                                       B, hq, hkv, D, n_pages, page, page_table.shape[1],
@@ -611,7 +620,7 @@ def dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=
     _plain("cu_new", cu_new, torch.int32, (B + 1,), dev)
     _table(page_table, B, dev)
     st = _on(dev, stream, (("v", v), ("k_pages", k_pages), ("v_pages", v_pages)))
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().dash_cache_write(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                       page_table.data_ptr(), starts.data_ptr(), cu_new.data_ptr(), k.shape[0], B, hkv,
                                       D, n_pages, page, page_table.shape[1],
@@ -621,15 +630,14 @@ def dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=
 def dash_cache_copy(k_pages, v_pages, src, dst, stream=None):
     """``src``, ``dst``: page numbers on the host (lists, arrays or CPU tensors)."""
     n_pages, page, hkv, D = _cache(k_pages, v_pages)
-    s, d = np.asarray(src, dtype=np.int32).reshape(-1), np.asarray(dst, dtype=np.int32).reshape(-1)
-    if s.size != d.size:
+    s, d = (array.array("i", x if isinstance(x, (list, tuple)) else x.tolist()) for x in (src, dst))
+    if len(s) != len(d):
         raise ValueError("src and dst must have the same length")
-    s, d = np.ascontiguousarray(s), np.ascontiguousarray(d)
     dev = k_pages.device
     st = _on(dev, stream, (("v_pages", v_pages),))
     strides = (ctypes.c_int64 * 6)(*k_pages.stride()[:3], *v_pages.stride()[:3])
-    with torch.cuda.device(dev):
-        _check(lib().dash_cache_copy(k_pages.data_ptr(), v_pages.data_ptr(), s.ctypes.data, d.ctypes.data, s.size,
+    with _device(dev):
+        _check(lib().dash_cache_copy(k_pages.data_ptr(), v_pages.data_ptr(), s.buffer_info()[0], d.buffer_info()[0], len(s),
                                      hkv, D, n_pages, page, strides, st))
 
 
@@ -651,18 +659,19 @@ def dash_version() -> int:
 
 # ------------------------------------------------------------ conveniences
 @contextlib.contextmanager
-def _using(stream, *tensors):
-    """Runs torch's own work on ``stream`` if one is given, and tells the allocator that it uses the tensors (made
-    on the current stream, whose work so far it waits for)."""
-    if stream is None:
-        yield
-        return
+def _side(stream, tensors):
     stream.wait_stream(torch.cuda.current_stream(stream.device))
     with torch.cuda.stream(stream):
         yield
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+
+
+def _using(stream, *tensors):
+    """Runs torch's own work on ``stream`` if one is given, and tells the allocator that it uses the tensors (made
+    on the current stream, whose work so far it waits for)."""
+    return _HERE if stream is None else _side(stream, tensors)
 
 
 def attn_fwd(q, k, v, causal: bool, scale: float | None = None, stream=None, cta_pair: int = -1):

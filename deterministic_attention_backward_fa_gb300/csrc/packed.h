@@ -112,6 +112,7 @@ __host__ __device__ inline int decode_splits(int len) {
   const int c = decode_chunk(len);
   return (int)(((long long)len + c - 1) / c);
 }
+cudaError_t prepare_decode();  // loads the decode kernels on the current device and raises their shared-memory limit
 cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_t stream);
 
 struct CacheWriteParams {

@@ -7,7 +7,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <map>
 #include <memory>
+#include <mutex>
 #include <new>
 #include <string>
 #include <vector>
@@ -129,10 +131,29 @@ dash_status_t check_plan(const dash_packed_plan_st *p, long long rows) {
   return DASH_OK;
 }
 
-dash_status_t sm_count(int *dev, int *sms) {
+// What the entry points ask of the current device, looked up once per device:
+// the queries and attributes cost more host time than a launch.
+struct Device {
+  int sms = 0;
+  int *status = nullptr;
+};
+std::mutex g_devices_mu;
+std::map<int, Device> g_devices;
+
+dash_status_t current_device(int *dev, Device *out) {
   cudaError_t e = cudaGetDevice(dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-  return e == cudaSuccess ? DASH_OK : cuda_error(e, "device query");
+  if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lock(g_devices_mu);
+  Device &d = g_devices[*dev];
+  if (!d.status) {
+    if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, *dev)) != cudaSuccess ||
+        (e = dash::prepare_decode()) != cudaSuccess || (e = dash::ops_status_address(&d.status)) != cudaSuccess) {
+      d.status = nullptr;
+      return cuda_error(e, "device set-up");
+    }
+  }
+  *out = d;
+  return DASH_OK;
 }
 
 dash_status_t cache_strides(const int64_t *s, int n_pages, int page_size, int heads, int D, const char *name,
@@ -161,12 +182,6 @@ dash_status_t cache_strides(const int64_t *s, int n_pages, int page_size, int he
   return DASH_OK;
 }
 
-// The status word of the current device; its first look-up loads the kernels.
-dash_status_t status_word(int **p) {
-  const cudaError_t e = dash::ops_status_address(p);
-  return e == cudaSuccess ? DASH_OK : cuda_error(e, "status word");
-}
-
 dash_status_t check_cache(int Hkv, int D, int n_pages, int page_size) {
   if (n_pages < 1 || page_size < 1) return report(DASH_ERR_INVALID_ARG, "the cache needs pages and tokens in a page");
   if (Hkv < 1) return report(DASH_ERR_INVALID_ARG, "the cache needs heads");
@@ -189,8 +204,10 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
   dash::PackedTables t;
   std::string why = dash::packed_tiles(lengths, n_seqs, &t);
   if (!why.empty()) return report(DASH_ERR_INVALID_ARG, "%s", why.c_str());
-  int dev = 0, sms = 0;
-  if ((st = sm_count(&dev, &sms)) != DASH_OK) return st;
+  int dev = 0;
+  Device device;
+  if ((st = current_device(&dev, &device)) != DASH_OK) return st;
+  const int sms = device.sms;
   std::unique_ptr<dash_packed_plan_st> p(new dash_packed_plan_st());
   p->device = dev;
   p->Hq = Hq;
@@ -212,7 +229,7 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
     cudaError_t e = dash::prepare_packed_fwd(D);
     if (e != cudaSuccess) return cuda_error(e, "packed forward");
     if (backward && (e = dash::prepare_packed_bwd(D)) != cudaSuccess) return cuda_error(e, "packed backward");
-    if ((st = status_word(&p->status)) != DASH_OK) return st;
+    p->status = device.status;
     // one block of device memory, copied once
     Region r;
     const size_t a = r.add(t.seqs.size() * sizeof(int2)), b = r.add(t.tiles.size() * sizeof(int4)),
@@ -479,9 +496,11 @@ dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v
   p.max_pages = max_pages;
   p.hblocks = (p.group + 15) / 16;
   p.scale_log2 = scale * kLog2e;
-  int dev = 0, sms = 0;
-  if ((st = sm_count(&dev, &sms)) || (st = status_word(&p.status))) return st;
-  const cudaError_t e = dash::launch_decode(D, p, sms, reinterpret_cast<cudaStream_t>(stream));
+  int dev = 0;
+  Device device;
+  if ((st = current_device(&dev, &device)) != DASH_OK) return st;
+  p.status = device.status;
+  const cudaError_t e = dash::launch_decode(D, p, device.sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "decode launch");
 }
 
@@ -526,9 +545,11 @@ dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void
   p.n_pages = n_pages;
   p.page_size = page_size;
   p.max_pages = max_pages;
-  int dev = 0, sms = 0;
-  if ((st = sm_count(&dev, &sms)) || (st = status_word(&p.status))) return st;
-  const cudaError_t e = dash::launch_cache_write(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  int dev = 0;
+  Device device;
+  if ((st = current_device(&dev, &device)) != DASH_OK) return st;
+  p.status = device.status;
+  const cudaError_t e = dash::launch_cache_write(p, device.sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "cache write launch");
 }
 
@@ -544,17 +565,18 @@ dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, 
   if ((st = cache_strides(strides, n_pages, page_size, Hkv, D, "k_pages", &p.ks)) ||
       (st = cache_strides(strides ? strides + 3 : nullptr, n_pages, page_size, Hkv, D, "v_pages", &p.vs)))
     return st;
-  std::vector<int32_t> to(dst, dst + n);
-  std::sort(to.begin(), to.end());
-  if (to.front() < 0 || to.back() >= n_pages)
-    return report(DASH_ERR_INVALID_ARG, "destination page outside the cache's %d pages", n_pages);
-  if (std::adjacent_find(to.begin(), to.end()) != to.end())
-    return report(DASH_ERR_INVALID_ARG, "a destination page is named twice");
+  std::vector<bool> to(n_pages);
+  for (int i = 0; i < n; ++i) {
+    if (dst[i] < 0 || dst[i] >= n_pages)
+      return report(DASH_ERR_INVALID_ARG, "destination page %d outside the cache's %d pages", dst[i], n_pages);
+    if (to[dst[i]]) return report(DASH_ERR_INVALID_ARG, "destination page %d is named twice", dst[i]);
+    to[dst[i]] = true;
+  }
   std::vector<int2> pairs(n);
   for (int i = 0; i < n; ++i) {
     if (src[i] < 0 || src[i] >= n_pages)
       return report(DASH_ERR_INVALID_ARG, "source page %d outside the cache's %d pages", src[i], n_pages);
-    if (std::binary_search(to.begin(), to.end(), src[i]))
+    if (to[src[i]])
       return report(DASH_ERR_INVALID_ARG, "page %d is a source and a destination of one call", src[i]);
     pairs[i] = make_int2(src[i], dst[i]);
   }

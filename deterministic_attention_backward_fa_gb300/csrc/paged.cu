@@ -405,13 +405,12 @@ __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
 template <int D>
 cudaError_t launch_decode_t(const DecodeParams &p, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(dash_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
   // at most as many items as the table has room for; two CTAs fit on an SM
   const long long items = (long long)p.B * p.max_splits * p.Hkv * p.hblocks;
   const int grid = (int)(items < 2LL * num_sms ? items : 2LL * num_sms);
   dash_decode_kernel<D><<<grid, kThreads, C::kSmem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.max_splits <= 1) return e;
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.max_splits <= 1) return e;
   dash_decode_join<D><<<dim3(p.Hq, p.B), 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
@@ -525,6 +524,14 @@ void launch_copy_t(const CacheCopyParams &p, const int2 *pairs, int n, cudaStrea
 }
 
 }  // namespace
+
+cudaError_t prepare_decode() {
+  cudaError_t e = cudaFuncSetAttribute(dash_decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       DecCfg<64>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dash_decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<128>::kSmem);
+  return e;
+}
 
 cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_t stream) {
   return D == 64 ? launch_decode_t<64>(p, num_sms, stream) : launch_decode_t<128>(p, num_sms, stream);
