@@ -18,8 +18,8 @@
 // group (or an odd one left over) two neighbouring tiles of a head pair up.
 //
 // Warps: 0-3 softmax and epilogue of tile 0, 4-7 of tile 1 (a thread owns a
-// row), 8 MMA issue, 9 TMA, 10 clears the V rows past the sequence's end in
-// the last KV tile (they belong to the next sequence or to nobody: P is 0
+// row), 8 and 11 MMA issue for tile 0 and 1, 9 TMA, 10 clears the V rows past
+// the sequence's end in the last KV tile (they belong to the next sequence or to nobody: P is 0
 // there, but 0 x NaN is NaN).  K rows past the end are masked after the
 // product, Q rows past the end are computed and not written.
 //
@@ -53,14 +53,14 @@ struct Cfg {
   static constexpr uint32_t oQ = 0;                 // two Q tiles
   static constexpr uint32_t oKV = 2 * kTile;
   static constexpr uint32_t oBAR = oKV + kStages * kTile;
-  static constexpr int kNumBars = 13 + 2 * kStages;
+  static constexpr int kNumBars = 22 + 2 * kStages;
   static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = oMISC + 16;
   static constexpr uint32_t cO = 256;
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory of one CTA");
 
-enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bVFixed = 10, bFinal = 11, bVTail = 12, bKvFull0 = 13 };
+enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bP = 12, bTurn = 20, bKvFull0 = 22 };
 
 __device__ __forceinline__ PackedFwdItem load_item(const PackedFwdItem *p) {
   PackedFwdItem it;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmV, const PackedFwdParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_id(), lane = threadIdx.x & 31;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
   uint64_t *kvFull = bars + bKvFull0, *kvEmpty = kvFull + C::kStages;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
@@ -129,15 +129,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[bQFull + s], 1);
       mbar_init(&bars[bQEmpty + s], 1);
       mbar_init(&bars[bSFull + s], 1);
-      mbar_init(&bars[bPFull + s], 4);
+      for (int c = 0; c < 4; ++c) mbar_init(&bars[bP + 4 * s + c], 4);
       mbar_init(&bars[bOFull + s], 1);
+      mbar_init(&bars[bFinal + s], 1);
+      mbar_init(&bars[bTurn + s], 1);
     }
     mbar_init(&bars[bVFixed], 1);
-    mbar_init(&bars[bFinal], 1);
     mbar_init(&bars[bVTail], 1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&kvFull[s], 1);
-      mbar_init(&kvEmpty[s], 1);
+      mbar_init(&kvEmpty[s], 2);  // both MMA warps
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -202,82 +203,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t f = fills / C::kStages + ((uint32_t)s < fills % C::kStages ? 1u : 0u);
         if (f) mbar_drain(&kvFull[s], (f - 1) & 1, g.limit_ns);
       }
-    } else if (warp == 8 && lane == 0) {
-      // -------------------------------------------------------------- MMA
+    } else if (warp == 8 || warp == 11) {
+      // ----------------------- MMA: a warp for each of the two Q tiles
+      // One warp for both leaves the tensor pipe idle at each of its waits (a
+      // wait queues behind the MMAs just issued, and answers about 100 clocks
+      // later).  The warps take turns, tile 0's PV and next S, then tile 1's, so
+      // that one tile's softmax runs under the other's MMAs; free running, the
+      // two fall into step and softmax and MMAs take place one after the other.
+      const int s = warp == 8 ? 0 : 1;
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
       Ring<C::kStages> rk;              // next K or V tile to be read
-      uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, fix_ph = 0;
-      bool issued = false;
-      auto issue_s = [&](int s, int stage) {
-        const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
-        const uint64_t dk = sw128_desc(smem_u32(smem + C::oKV + stage * C::kTile), 16, 1024);
+      uint32_t q_ph = 0, p_ph = 0, fix_ph = 0;
+      uint32_t lead = elect_one();      // 0 in every lane once a wait has failed: nothing more is issued
+      const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
+      const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oKV), 16, 1024);
+      const uint64_t dv0 = sw128_desc(smem_u32(smem + C::oKV), C::kPanel, 1024);
+      const uint32_t tS = tmem + s * 128, tO = tmem + C::cO + s * D;
+      auto wait = [&](int bar, uint32_t ph) {
+        if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
+      };
+      uint32_t turn_ph = s ? 0 : 1;     // tile 0's first turn is free
+      auto take_turn = [&] {
+        wait(bTurn + s, turn_ph);
+        turn_ph ^= 1;
+      };
+      auto pass_turn = [&] {
+        if (lead) mbar_arrive(&bars[bTurn + (s ^ 1)]);
+      };
+      auto issue_s = [&](int stage, bool pass) {
+        const uint64_t dk = dk0 + ((stage * C::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + s * 128, dq + off, dk + off, idS, kk > 0);
+          if (pass && kk == D / 16 - 2) pass_turn();  // the other warp wakes up under the last MMAs
+          mma_ss_if(lead, tS, dq + off, dk + off, idS, kk > 0);
         }
-        tc_commit(&bars[bSFull + s]);
+        tc_commit_if(lead, &bars[bSFull + s]);
       };
       for (int i = i_begin; i < i_end; ++i) {
         const PackedFwdItem it = load_item(p.items + i);
-        const int n = max(it.nkv[0], it.nkv[1]);
+        const int n = max(it.nkv[0], it.nkv[1]), mine = s ? it.nkv[1] : it.nkv[0];
         const bool fix = n * kPackedTile > it.kv_len;
-        // S of the first KV tile
-        mbar_wait(&kvFull[rk.st], rk.ph, g);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (it.nkv[s] == 0) continue;
-          mbar_wait(&bars[bQFull + s], q_ph[s], g);
-          q_ph[s] ^= 1;
-          if (*g.abort) continue;
+        wait(bKvFull0 + rk.st, rk.ph);
+        if (mine > 0) {  // S of the first KV tile
+          wait(bQFull + s, q_ph);
+          q_ph ^= 1;
           tc_fence_after();
-          issue_s(s, rk.st);
-          issued = true;
-          if (it.nkv[s] == 1) tc_commit(&bars[bQEmpty + s]);
+          issue_s(rk.st, false);
+          if (mine == 1) tc_commit_if(lead, &bars[bQEmpty + s]);
         }
-        if (!*g.abort) tc_commit(&kvEmpty[rk.st]);
+        tc_commit_if(lead, &kvEmpty[rk.st]);
         rk.next();
         for (int j = 0; j < n; ++j) {
           const Ring<C::kStages> rv = rk;  // V tile j; the next K tile follows it in the ring
           rk.next();
-          mbar_wait(&kvFull[rv.st], rv.ph, g);
+          wait(bKvFull0 + rv.st, rv.ph);
           if (fix && j == n - 1) {
-            mbar_arrive(&bars[bVTail]);  // it has landed: its rows past the end may be cleared
-            mbar_wait(&bars[bVFixed], fix_ph, g);
+            if (lead && s == 0) mbar_arrive(&bars[bVTail]);  // it has landed: its rows past the end may be cleared
+            wait(bVFixed, fix_ph);
             fix_ph ^= 1;
           }
-          if (j + 1 < n) mbar_wait(&kvFull[rk.st], rk.ph, g);
-          const uint64_t dv = sw128_desc(smem_u32(smem + C::oKV + rv.st * C::kTile), C::kPanel, 1024);
+          if (j + 1 < n) wait(bKvFull0 + rk.st, rk.ph);
+          const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
+          if (j < mine) {
+            // P stands in tensor memory, quarter by quarter, and O is at its scale
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (j >= it.nkv[s]) continue;
-            mbar_wait(&bars[bPFull + s], p_ph[s], g);  // P stands in tensor memory, O is at its scale
-            p_ph[s] ^= 1;
-            if (*g.abort) continue;
-            tc_fence_after();
+            for (int c = 0; c < 4; ++c) {
+              wait(bP + 4 * s + c, p_ph);
+              if (c == 0) take_turn();
+              tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + C::cO + s * D, tmem + s * 128 + kk * 8, dv + ((kk * 2048) >> 4), idO,
-                     (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 < it.nkv[s]) {
-              issue_s(s, rk.st);  // MMAs run in issue order: PV has read P before S overwrites it
-              if (j + 2 == it.nkv[s]) tc_commit(&bars[bQEmpty + s]);
-            } else {
-              tc_commit(&bars[bOFull + s]);
+              for (int kk = 2 * c; kk < 2 * c + 2; ++kk)
+                mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
             }
+            p_ph ^= 1;
+            if (j + 1 < mine) {
+              issue_s(rk.st, true);  // MMAs run in issue order: PV has read P before S overwrites it
+              if (j + 2 == mine) tc_commit_if(lead, &bars[bQEmpty + s]);
+            } else {
+              pass_turn();
+              tc_commit_if(lead, &bars[bOFull + s]);
+            }
+          } else {
+            take_turn();
+            pass_turn();
           }
-          if (!*g.abort) {
-            tc_commit(&kvEmpty[rv.st]);
-            if (j + 1 < n) tc_commit(&kvEmpty[rk.st]);
+          // each tile is free when both warps' MMAs have read it (a warp that has none arrives at once)
+          tc_commit_if(lead, &kvEmpty[rv.st]);
+          if (j + 1 < n) {
+            tc_commit_if(lead, &kvEmpty[rk.st]);
+            rk.next();
           }
-          if (j + 1 < n) rk.next();
         }
       }
-      if (issued) {  // every MMA has completed before tensor memory is released
-        tc_commit(&bars[bFinal]);
-        mbar_drain(&bars[bFinal], 0, g.limit_ns);
-      }
+      // every MMA has completed before tensor memory is released (at once if none was issued)
+      tc_commit_if(elect_one(), &bars[bFinal + s]);
+      mbar_drain(&bars[bFinal + s], 0, g.limit_ns);
     } else if (warp == 10) {
       // ------------------------------- V rows past the end of the sequence
       uint32_t loads = 0, tail_ph = 0;
@@ -320,77 +342,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int limit = p.causal ? min(it.kv_len, q_pos + 1) : it.kv_len;
       float m = -INFINITY;   // the maximum the row refers to (scaled, log2)
       uint64_t l2 = 0;       // its sum, in two halves
+      // After an abort the loop runs on with whatever tensor memory holds: no
+      // wait blocks any more, and the status word tells that O is not valid.
       for (int j = 0; j < n; ++j) {
         mbar_wait(&bars[bSFull + s], s_ph, g);
         s_ph ^= 1;
-        if (!warp_aborted(g)) {
-          tc_fence_after();
-          uint32_t x[4][32];
+        __syncwarp();
+        tc_fence_after();
+        uint32_t x[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
-          tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
+        tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) reg_order32(x[c]);
-          const int cols = limit - j * kPackedTile;  // valid columns of this tile
-          if (__any_sync(0xffffffffu, cols < kPackedTile)) {
+        for (int c = 0; c < 4; ++c) reg_order32(x[c]);
+        const int cols = limit - j * kPackedTile;  // valid columns of this tile
+        if (__any_sync(0xffffffffu, cols < kPackedTile)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * c + e >= cols) x[c][e] = 0xff800000u;  // -inf
-          }
-          float mx[4];
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= cols) x[c][e] = 0xff800000u;  // -inf
+        }
+        float mx[4];  // four chains side by side
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx[c] = __uint_as_float(x[c][0]);
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
 #pragma unroll
-            for (int e = 1; e < 31; e += 2)
-              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
-            mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          if (j == 0) {
-            m = top == -INFINITY ? 0.f : top;
-          } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
-            // PV(j-1) completed before S(j) did, so O may be rewritten here
-            const float m_new = fmaxf(m, top);
-            const float f = ex2(m - m_new);
-            m = m_new;
-            const uint64_t f2 = pack2(f, f);
-            l2 = mul2(l2, f2);
+        for (int e = 2; e < 32; e += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (j == 0) {
+          m = top == -INFINITY ? 0.f : top;
+        } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          // PV(j-1) completed before S(j) did, so O may be rewritten here
+          const float m_new = fmaxf(m, top);
+          const float f = ex2(m - m_new);
+          m = m_new;
+          const uint64_t f2 = pack2(f, f);
+          l2 = mul2(l2, f2);
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              uint32_t r[16];
-              tmem_ld16(tO + c0, r);
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(tO + c0, r);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tmem_st16(tO + c0, r);
-            }
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            tmem_st16(tO + c0, r);
           }
-          const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nm2 = pack2(-m, -m);
-          uint64_t acc2[2] = {0, 0};
+        }
+        const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nm2 = pack2(-m, -m);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t y2 =
-                  fma2(pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2);
-              float a, b;
-              unpack2(y2, a, b);
-              a = ex2(a);
-              b = ex2(b);
-              acc2[(e >> 1) & 1] = add2(acc2[(e >> 1) & 1], pack2(a, b));
-              pk[e >> 1] = pack_bf16(a, b);
-            }
-            tmem_st16(tS + 16 * c, pk);
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t y2 = fma2(pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2);
+            float a, b;
+            unpack2(y2, a, b);
+            a = ex2(a);
+            b = ex2(b);
+            x[c][e] = __float_as_uint(a);
+            x[c][e + 1] = __float_as_uint(b);
+            pk[e >> 1] = pack_bf16(a, b);
           }
-          l2 = add2(l2, add2(acc2[0], acc2[1]));
+          tmem_st16(tS + 16 * c, pk);
+          // the product starts on the first quarters of P while the others are made
           tmem_st_wait();
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[bP + 4 * s + c]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[bPFull + s]);
+        // the sum is not on the product's path
+        uint64_t acc2[4] = {l2, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc2[c] = add2(acc2[c], pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+        l2 = add2(add2(acc2[0], acc2[1]), add2(acc2[2], acc2[3]));
       }
       // ------------------------------------------------------- epilogue
       mbar_wait(&bars[bOFull + s], o_ph, g);

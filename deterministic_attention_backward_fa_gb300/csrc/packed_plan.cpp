@@ -17,6 +17,9 @@ namespace {
 // Cost of an item of the forward beside its KV tiles (set-up and epilogue), in KV tiles.
 constexpr long long kItemCost = 2;
 
+// Keys (of one K/V head, both tensors, 128 wide) that fill half of the L2.
+constexpr long long kL2Rows = 64LL * 1024 * 1024 / (2 * 128 * 2);
+
 using Slot = std::pair<long long, int>;  // {load, CTA}: the least loaded, lowest CTA first
 using Heap = std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>>;
 
@@ -73,28 +76,30 @@ void packed_forward(const PackedTables &t, int Hq, int Hkv, bool causal, int P, 
   for (int seq : by_length(t)) {
     const int2 sq = t.seqs[seq];
     const int n = (sq.y + kPackedTile - 1) / kPackedTile;
-    for (int hk = 0; hk < Hkv; ++hk) {
-      PackedFwdItem base = {};
-      base.kv_row0 = sq.x;
-      base.kv_len = sq.y;
-      base.kv_head = hk;
-      const int h0 = hk * group;
-      // two tiles of the odd head left over go together every other step
-      for (int qt = n - 1; qt >= 0; --qt) {
-        for (int h = 0; h + 1 < group; h += 2) {
-          PackedFwdItem it = base;
-          tile(it, 0, seq, qt, h0 + h);
-          tile(it, 1, seq, qt, h0 + h + 1);
-          items.push_back(it);
+    // K/V heads side by side whose keys and values stay in L2 together, all their
+    // items the longest first
+    const int batch = (int)std::max<long long>(1, std::min<long long>(Hkv, kL2Rows / std::max(1, sq.y)));
+    for (int b0 = 0; b0 < Hkv; b0 += batch)
+      for (int qt = n - 1; qt >= 0; --qt)
+        for (int hk = b0; hk < std::min(Hkv, b0 + batch); ++hk) {
+          PackedFwdItem base = {};
+          base.kv_row0 = sq.x;
+          base.kv_len = sq.y;
+          base.kv_head = hk;
+          const int h0 = hk * group;
+          for (int h = 0; h + 1 < group; h += 2) {
+            PackedFwdItem it = base;
+            tile(it, 0, seq, qt, h0 + h);
+            tile(it, 1, seq, qt, h0 + h + 1);
+            items.push_back(it);
+          }
+          if ((group & 1) && (n - 1 - qt) % 2 == 0) {  // the odd head's tiles go in pairs
+            PackedFwdItem it = base;
+            tile(it, 0, seq, qt, h0 + group - 1);
+            if (qt > 0) tile(it, 1, seq, qt - 1, h0 + group - 1);
+            items.push_back(it);
+          }
         }
-        if ((group & 1) && (n - 1 - qt) % 2 == 0) {
-          PackedFwdItem it = base;
-          tile(it, 0, seq, qt, h0 + group - 1);
-          if (qt > 0) tile(it, 1, seq, qt - 1, h0 + group - 1);
-          items.push_back(it);
-        }
-      }
-    }
   }
   P = (int)std::max<long long>(1, std::min<long long>(P, (long long)items.size()));
   Heap heap = make_heap(P);
