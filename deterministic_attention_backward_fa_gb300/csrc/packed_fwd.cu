@@ -17,8 +17,8 @@
 // Two heads of a group on the same rows share keys exactly; with one head per
 // group (or an odd one left over) two neighbouring tiles of a head pair up.
 //
-// Warps: 0-3 softmax and epilogue of tile 0, 4-7 of tile 1 (a thread owns a
-// row), 8 and 11 MMA issue for tile 0 and 1, 9 TMA, 10 clears the V rows past
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a thread owns a row), 12-15
+// the epilogue, 8 and 11 MMA issue for tile 0 and 1, 9 TMA, 10 clears the V rows past
 // the sequence's end in the last KV tile (they belong to the next sequence or to nobody: P is 0
 // there, but 0 x NaN is NaN).  K rows past the end are masked after the
 // product, Q rows past the end are computed and not written.
@@ -36,11 +36,12 @@ using namespace dev;
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsLaunch = 168;   // 384 threads x 168 registers
-constexpr int kRegsSoftmax = 208;  // a row of S in registers
+constexpr int kThreads = 512;
+constexpr int kRegsLaunch = 128;   // 512 threads x 128 registers
+constexpr int kRegsSoftmax = 176;  // a row of S in registers
 constexpr int kRegsOther = 88;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= kRegsLaunch * kThreads,
+constexpr int kRegsOut = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsOther + kRegsOut) <= kRegsLaunch * kThreads,
               "register split exceeds the CTA's allocation");
 constexpr float kLazy = 8.f;       // log2 growth of a row's maximum that is left standing
 
@@ -53,14 +54,15 @@ struct Cfg {
   static constexpr uint32_t oQ = 0;                 // two Q tiles
   static constexpr uint32_t oKV = 2 * kTile;
   static constexpr uint32_t oBAR = oKV + kStages * kTile;
-  static constexpr int kNumBars = 22 + 2 * kStages;
+  static constexpr int kNumBars = 20 + 2 * kStages;
   static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
-  static constexpr uint32_t kSmemBytes = oMISC + 16;
+  static constexpr uint32_t oSTAT = oMISC + 16;     // {maximum, sum} of each tile's rows
+  static constexpr uint32_t kSmemBytes = oSTAT + 2 * 128 * 8;
   static constexpr uint32_t cO = 256;
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory of one CTA");
 
-enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bP = 12, bTurn = 20, bKvFull0 = 22 };
+enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bPFull = 12, bTurn = 14, bLFull = 16, bOEmpty = 18, bKvFull0 = 20 };
 
 __device__ __forceinline__ PackedFwdItem load_item(const PackedFwdItem *p) {
   PackedFwdItem it;
@@ -129,7 +131,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[bQFull + s], 1);
       mbar_init(&bars[bQEmpty + s], 1);
       mbar_init(&bars[bSFull + s], 1);
-      for (int c = 0; c < 4; ++c) mbar_init(&bars[bP + 4 * s + c], 4);
+      mbar_init(&bars[bPFull + s], 4);
+      mbar_init(&bars[bLFull + s], 4);
+      mbar_init(&bars[bOEmpty + s], 4);
       mbar_init(&bars[bOFull + s], 1);
       mbar_init(&bars[bFinal + s], 1);
       mbar_init(&bars[bTurn + s], 1);
@@ -152,9 +156,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
+  float2 *stat = reinterpret_cast<float2 *>(smem + C::oSTAT);
   const int i_begin = p.cta_off[blockIdx.x], i_end = p.cta_off[blockIdx.x + 1];
 
-  if (warp >= 8) {
+  if (warp >= 12) {
+    // ---------------------------------------------------------- epilogue
+    // The two tiles' O in turn, while the softmax warps are at the next item.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    const int sub = warp & 3, L = sub * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
+    uint32_t ph[2] = {0, 0};
+    for (int i = i_begin; i < i_end; ++i) {
+      const PackedFwdItem it = load_item(p.items + i);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (it.nkv[s] == 0) continue;
+        bool ok = mbar_wait(&bars[bLFull + s], ph[s], g);
+        ok &= mbar_wait(&bars[bOFull + s], ph[s], g);
+        ph[s] ^= 1;
+        __syncwarp();
+        tc_fence_after();
+        const float2 ml = stat[s * 128 + L];
+        const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+        ok &= L < it.rows[s];
+        const long long row = (long long)it.row0[s] + L;
+        __nv_bfloat16 *orow = p.o + row * p.o_row + it.head[s] * p.o_head;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(tl + C::cO + s * D + c0, r);
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 w;
+              w.x = pack_bf16(inv * __uint_as_float(r[8 * k + 0]), inv * __uint_as_float(r[8 * k + 1]));
+              w.y = pack_bf16(inv * __uint_as_float(r[8 * k + 2]), inv * __uint_as_float(r[8 * k + 3]));
+              w.z = pack_bf16(inv * __uint_as_float(r[8 * k + 4]), inv * __uint_as_float(r[8 * k + 5]));
+              w.w = pack_bf16(inv * __uint_as_float(r[8 * k + 6]), inv * __uint_as_float(r[8 * k + 7]));
+              *reinterpret_cast<uint4 *>(orow + c0 + 8 * k) = w;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[bOEmpty + s]);
+        if (ok) p.lse[it.head[s] * p.lse_head + row] = (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+      }
+    }
+  } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 9 && lane == 0) {
       // -------------------------------------------------------------- TMA
@@ -214,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
       Ring<C::kStages> rk;              // next K or V tile to be read
-      uint32_t q_ph = 0, p_ph = 0, fix_ph = 0;
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0;
       uint32_t lead = elect_one();      // 0 in every lane once a wait has failed: nothing more is issued
       const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
       const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oKV), 16, 1024);
@@ -267,16 +316,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < n) wait(bKvFull0 + rk.st, rk.ph);
           const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
           if (j < mine) {
-            // P stands in tensor memory, quarter by quarter, and O is at its scale
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              wait(bP + 4 * s + c, p_ph);
-              if (c == 0) take_turn();
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 2 * c; kk < 2 * c + 2; ++kk)
-                mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
+            // P stands in tensor memory, O is at its scale and the last item's O has been read
+            wait(bPFull + s, p_ph);
+            if (j == 0) {
+              wait(bOEmpty + s, o_ph);
+              o_ph ^= 1;
             }
+            take_turn();
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
             p_ph ^= 1;
             if (j + 1 < mine) {
               issue_s(rk.st, true);  // MMAs run in issue order: PV has read P before S overwrites it
@@ -406,12 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[e >> 1] = pack_bf16(a, b);
           }
           tmem_st16(tS + 16 * c, pk);
-          // the product starts on the first quarters of P while the others are made
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[bP + 4 * s + c]);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[bPFull + s]);
         // the sum is not on the product's path
         uint64_t acc2[4] = {l2, 0, 0, 0};
 #pragma unroll
@@ -421,38 +470,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc2[c] = add2(acc2[c], pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
         l2 = add2(add2(acc2[0], acc2[1]), add2(acc2[2], acc2[3]));
       }
-      // ------------------------------------------------------- epilogue
+      // The last product's completion also says that the item before has been
+      // written out (the product waited for it), so its row of `stat` is free.
+      // The next S comes later anyway.
       mbar_wait(&bars[bOFull + s], o_ph, g);
       o_ph ^= 1;
-      if (!warp_aborted(g)) {
-        tc_fence_after();
-        float la, lb;
-        unpack2(l2, la, lb);
-        const float l = la + lb;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const bool ok = L < (s ? it.rows[1] : it.rows[0]);
-        const long long row = (long long)(s ? it.row0[1] : it.row0[0]) + L;
-        const int head = s ? it.head[1] : it.head[0];
-        __nv_bfloat16 *orow = p.o + row * p.o_row + head * p.o_head;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t r[32];
-          tmem_ld32(tO + c0, r);
-          if (ok) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 w;
-              w.x = pack_bf16(inv * __uint_as_float(r[8 * k + 0]), inv * __uint_as_float(r[8 * k + 1]));
-              w.y = pack_bf16(inv * __uint_as_float(r[8 * k + 2]), inv * __uint_as_float(r[8 * k + 3]));
-              w.z = pack_bf16(inv * __uint_as_float(r[8 * k + 4]), inv * __uint_as_float(r[8 * k + 5]));
-              w.w = pack_bf16(inv * __uint_as_float(r[8 * k + 6]), inv * __uint_as_float(r[8 * k + 7]));
-              *reinterpret_cast<uint4 *>(orow + c0 + 8 * k) = w;
-            }
-          }
-        }
-        if (ok) p.lse[head * p.lse_head + row] = (m + log2f(l)) * 0.6931471805599453f;
-        tc_fence_before();
-      }
+      float la, lb;
+      unpack2(l2, la, lb);
+      stat[s * 128 + L] = make_float2(m, la + lb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bLFull + s]);
     }
   }
   tc_fence_before();
