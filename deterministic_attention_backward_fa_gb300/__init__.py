@@ -89,7 +89,7 @@ _SIGS = {
     "dash_packed_plan_create": ([_P] + [_I] * 6 + [ctypes.POINTER(_P)], _I),
     "dash_packed_plan_destroy": ([_P], None),
     "dash_packed_bwd_workspace": ([_P], _L),
-    "dash_build_packed_schedule": ([_P] + [_I] * 5 + [_P, _P, ctypes.POINTER(_I), ctypes.POINTER(_L)], _I),
+    "dash_build_packed_items": ([_P] + [_I] * 6 + [_P, _P, ctypes.POINTER(_I), ctypes.POINTER(_L)], _I),
     "dash_attn_packed_fwd": ([_P] * 6 + [_L, _P, _F, _P], _I),
     "dash_attn_packed_bwd": ([_P] * 10 + [_L, _P, _F, _P, _L, _P], _I),
     "dash_attn_decode": ([_P] * 7 + [_I] * 7 + [_P, _F, _P, _L, _P], _I),
@@ -523,16 +523,16 @@ def dash_packed_bwd_workspace(plan) -> int:
     return int(lib().dash_packed_bwd_workspace(_handle(plan)))
 
 
-def dash_build_packed_schedule(lengths, heads: int, kv_heads: int, causal: bool, P: int):
-    """Host-only.  The packed backward's table: (tasks int32 [N, 4], cta_off int32 [CTAs + 1])."""
+def dash_build_packed_items(lengths, heads: int, kv_heads: int, causal: bool, kernel: int, P: int):
+    """Host-only.  The items of the forward (kernel 0), dQ (1) or dK and dV (2): (int32 [N, 16 or 8], cta_off)."""
     arr = (ctypes.c_int32 * max(len(lengths), 1))(*lengths)
     n, ctas = _L(0), _I(0)
-    head = (arr, len(lengths), heads, kv_heads, int(causal), P)
-    _check(lib().dash_build_packed_schedule(*head, None, None, ctypes.byref(ctas), ctypes.byref(n)))
-    tasks = np.zeros((max(n.value, 1), 4), dtype=np.int32)
+    head = (arr, len(lengths), heads, kv_heads, int(causal), kernel, P)
+    _check(lib().dash_build_packed_items(*head, None, None, ctypes.byref(ctas), ctypes.byref(n)))
+    items = np.zeros((max(n.value, 1), 8 if kernel else 16), dtype=np.int32)
     off = np.zeros(ctas.value + 1, dtype=np.int32)
-    _check(lib().dash_build_packed_schedule(*head, tasks.ctypes.data, off.ctypes.data, None, ctypes.byref(n)))
-    return tasks[:n.value], off
+    _check(lib().dash_build_packed_items(*head, items.ctypes.data, off.ctypes.data, None, ctypes.byref(n)))
+    return items[:n.value], off
 
 
 def dash_attn_packed_fwd(plan: PackedPlan, q, k, v, o, lse, scale: float, stream=None):

@@ -143,12 +143,6 @@ __device__ __forceinline__ void regs_set() {
   }
 }
 __device__ __forceinline__ void regs_dec() { regs_set<kRegsProducer>(); }
-// Orders the writes that another kernel made to a tensor map before this
-// thread's copies that read it.
-__device__ __forceinline__ void acquire_tmap(const CUtensorMap *m) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m))
-               : "memory");
-}
 // Phase stamp of the traced kernel (compiled out of the plain one).
 template <bool kTrace>
 __device__ __forceinline__ void trace_put(const BwdMainParams &p, int t, int slot, long long v) {
@@ -169,14 +163,7 @@ __device__ __forceinline__ unsigned smid() {
 __device__ __forceinline__ void regs_softmax() { regs_set<kRegsSoftmax>(); }
 __device__ __forceinline__ void regs_reduce() { regs_set<kRegsReduce>(); }
 
-// kPacked: the tasks are those of a packed problem (kernels.h, PackedBwd): heads
-// are Q heads, tiles are numbered over all sequences, and the loads go through
-// tensor maps of one sequence each, whose bounds fill the rows past its end
-// with zeros.  Tiles of one sequence have consecutive numbers, so differences
-// of tile numbers are distances inside it and the causal test is unchanged.  A
-// KV run holds the tasks of every Q head of its group (or of a part of it), so
-// dK and dV of shared heads are summed in tensor memory.
-template <int D, int T, bool kTrace, bool kPacked>
+template <int D, int T, bool kTrace>
 __global__ void __launch_bounds__(kThreads, 1)
     dash_bwd_main(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -233,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMaxClusterLinks; ++i) turn_count[i] = turns_seen[i] = 0;
     fence_mbar_init();
   }
-  if (!kPacked && warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -275,32 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kv_last = 0, kv_fills = 0;
       int st = 0, runs = 0;
       int4 nxt = t_begin < t_end ? tasks[t_begin] : make_int4(0, 0, 0, 0);
-      [[maybe_unused]] int seq = -1;                      // packed: the sequence of the maps in use
-      [[maybe_unused]] const CUtensorMap *smaps = nullptr;  // its Q, K, V and dO maps
       for (int t = t_begin; t < t_end; ++t) {
         const int4 tk = nxt;
         if (t + 1 < t_end) nxt = tasks[t + 1];
         const int bh = tk.x, kv = tk.y, q = tk.z;
-        int kv_row = kv * T, q_row = q * T, kv_head = bh;
-        if constexpr (kPacked) {
-          const int4 qt = p.packed.tiles[q];
-          if (qt.z != seq) {
-            seq = qt.z;
-            smaps = p.packed.maps + 4 * (size_t)seq;
-            // written by the preprocess kernel: order its writes before the copies that read the maps
-            if (qside) {
-              acquire_tmap(smaps);
-              acquire_tmap(smaps + 1);
-              acquire_tmap(smaps + 2);
-            } else {
-              acquire_tmap(smaps + 3);
-            }
-          }
-          map = smaps + (qside ? 0 : 3);
-          q_row = qt.x;
-          kv_row = qt.x - (q - kv) * T;
-          kv_head = bh / p.packed.group;
-        }
         if (qside && (tk.w & kTaskFirstFlag)) {
           if (runs > 0) {
             mbar_wait(&bars[bKvEmpty], kv_e_phase, g);
@@ -310,10 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!*g.abort) {
             mbar_arrive_expect_tx(&bars[bKvFull], 2 * C::kKvBytes);
             for (int pn = 0; pn < C::kPanels; ++pn) {
-              tma_load_3d(smem + C::oK + pn * C::kKvPanel, kPacked ? smaps + 1 : &tmK, &bars[bKvFull], pn * 64, kv_row,
-                          kv_head);
-              tma_load_3d(smem + C::oV + pn * C::kKvPanel, kPacked ? smaps + 2 : &tmV, &bars[bKvFull], pn * 64, kv_row,
-                          kv_head);
+              tma_load_3d(smem + C::oK + pn * C::kKvPanel, &tmK, &bars[bKvFull], pn * 64, kv * T, bh);
+              tma_load_3d(smem + C::oV + pn * C::kKvPanel, &tmV, &bars[bKvFull], pn * 64, kv * T, bh);
             }
             kv_issued = true;
             kv_last = kv_fills & 1;
@@ -328,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t fill = used[st] ? (f_last[st] ^ 1) : 0;
           mbar_arrive_expect_tx(&full[st], C::kQBytes + T * 4);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_3d(buf0 + st * C::kQBytes + pn * C::kQPanel, map, &full[st], pn * 64, q_row, bh);
+            tma_load_3d(buf0 + st * C::kQBytes + pn * C::kQPanel, map, &full[st], pn * 64, q * T, bh);
           bulk_load(row0p + st * T * 4, rowsrc + ((size_t)bh * p.n + q) * T, T * 4, &full[st]);
           f_last[st] = fill;
           used[st] = true;
@@ -528,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_aborted(g)) {
         tc_fence_after();
         const int kv_g = kv * T + L;
-        const bool row_ok = kPacked ? L < p.packed.tiles[kv].y : (L < T) && (kv_g < p.S);
+        const bool row_ok = (L < T) && (kv_g < p.S);
         const int qbase = q * T;
         // Masking is needed only where a row lies past the sequence or, for a
         // causal mask, the tile reaches above the diagonal; the test is made
@@ -798,19 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_aborted(g)) {
           tc_fence_after();
           const int kv_g = kv * T + L;
-          bool row_ok;
-          __nv_bfloat16 *dv_row, *dk_row;
-          if constexpr (kPacked) {
-            const int4 kt = p.packed.tiles[kv];
-            const long long row = (long long)kt.w + L, head = bh / p.packed.group;
-            row_ok = L < kt.y;
-            dv_row = p.dv + row * p.packed.dv_row + head * p.packed.dv_head;
-            dk_row = p.dk + row * p.packed.dk_row + head * p.packed.dk_head;
-          } else {
-            row_ok = (L < T) && (kv_g < p.S);
-            dv_row = p.dv + ((size_t)bh * p.S + kv_g) * D;
-            dk_row = p.dk + ((size_t)bh * p.S + kv_g) * D;
-          }
+          const bool row_ok = (L < T) && (kv_g < p.S);
+          __nv_bfloat16 *dv_row = p.dv + ((size_t)bh * p.S + kv_g) * D;
+          __nv_bfloat16 *dk_row = p.dk + ((size_t)bh * p.S + kv_g) * D;
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t a[32], b[32];
@@ -967,34 +920,24 @@ __global__ void __launch_bounds__(256) dash_bwd_convert(const float *__restrict_
   }
 }
 
-template <int D, int T>
-int main_smem() {
+template <int D, int T, bool kTrace>
+cudaError_t launch_main_t(const BwdMaps &maps, const BwdMainParams &p, int num_ctas, cudaStream_t stream,
+                          int cluster) {
   using C = BwdCfg<D, T>;
-  return C::kSmemBytes > (uint32_t)kMinSmemOneCtaPerSm ? (int)C::kSmemBytes : kMinSmemOneCtaPerSm;
-}
-
-template <int D, int T, bool kTrace, bool kPacked>
-cudaError_t prepare_main_t() {
-  auto kfn = dash_bwd_main<D, T, kTrace, kPacked>;
+  auto kfn = dash_bwd_main<D, T, kTrace>;
   // The setmaxnreg split above assumes the CTA is launched with exactly
   // kRegsLaunch registers per thread; with fewer, an increase could wait forever.
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kfn);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, main_smem<D, T>());
-}
-
-template <int D, int T, bool kTrace, bool kPacked = false>
-cudaError_t launch_main_t(const BwdMaps &maps, const BwdMainParams &p, int num_ctas, cudaStream_t stream,
-                          int cluster) {
-  auto kfn = dash_bwd_main<D, T, kTrace, kPacked>;
-  cudaError_t e = prepare_main_t<D, T, kTrace, kPacked>();
+  const int smem = C::kSmemBytes > (uint32_t)kMinSmemOneCtaPerSm ? (int)C::kSmemBytes : kMinSmemOneCtaPerSm;
+  e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = main_smem<D, T>();
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs resident: semaphore waits cannot starve
@@ -1018,7 +961,7 @@ cudaError_t launch_main_t(const BwdMaps &maps, const BwdMainParams &p, int num_c
 template <int D, int T>
 int cluster_size_t(int num_ctas) {
   using C = BwdCfg<D, T>;
-  auto kfn = dash_bwd_main<D, T, false, false>;
+  auto kfn = dash_bwd_main<D, T, false>;
   const int smem = C::kSmemBytes > (uint32_t)kMinSmemOneCtaPerSm ? (int)C::kSmemBytes : kMinSmemOneCtaPerSm;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 1;
   for (int cl : {16, 8, 4, 2}) {
@@ -1067,16 +1010,6 @@ cudaError_t launch_bwd_preprocess(const BwdPreParams &a, int num_sms, cudaStream
         (const __nv_bfloat16 *)a.o, (const __nv_bfloat16 *)a.dout, a.lse, a.lse2, a.delta, (float4 *)a.dq_accum,
         a.accum_floats / 4, a.sem, a.sem_count, a.S, a.rows_padded, a.total_rows);
   return cudaGetLastError();
-}
-
-cudaError_t prepare_packed_bwd(int D) {
-  return D == 64 ? prepare_main_t<64, 128, false, true>() : prepare_main_t<128, 128, false, true>();
-}
-
-cudaError_t launch_packed_bwd_main(int D, const BwdMainParams &p, int num_ctas, cudaStream_t stream) {
-  BwdMaps unused = {};  // the packed kernel loads through p.packed.maps
-  if (D == 64) return launch_main_t<64, 128, false, true>(unused, p, num_ctas, stream, 1);
-  return launch_main_t<128, 128, false, true>(unused, p, num_ctas, stream, 1);
 }
 
 cudaError_t launch_bwd_main(int D, int T, const BwdMaps &maps, const BwdMainParams &p, int num_ctas,

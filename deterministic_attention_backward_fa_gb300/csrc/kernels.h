@@ -33,15 +33,6 @@ struct BwdMaps {
   CUtensorMap q, k, v, dout;  // 3-D [BH][S][D] bf16, 128-byte swizzle; Q/dO box T rows, K/V box 128 rows
 };
 
-// A packed problem's backward (bwd.cu): the tiles of all sequences in one
-// numbering, n = their count, and the maps of each sequence.
-struct PackedBwd {
-  const int4 *tiles = nullptr;         // {first row inside the sequence, valid rows, sequence, first packed row}
-  const CUtensorMap *maps = nullptr;   // [sequences][Q, K, V, dO], bounded by the sequence
-  int group = 1;                       // Q heads per K/V head
-  long long dk_row = 0, dk_head = 0, dv_row = 0, dv_head = 0;  // element strides of dK and dV
-};
-
 struct BwdMainParams {
   const int4 *tasks;     // {bh, kv, q, rank | flags}
   const int *cta_off;    // gridDim.x + 1
@@ -72,7 +63,6 @@ struct BwdMainParams {
   // turn from a counter in its own shared memory that the predecessor's CTA
   // raises.
   int linked = 0;
-  PackedBwd packed;  // packed problems only
 };
 constexpr int kMaxClusterLinks = 16;  // cluster sizes up to 16: one counter per CTA of the cluster
 // Link bits of a task word (host cluster_links and the device table of a linked launch)
@@ -138,9 +128,6 @@ cudaError_t launch_bwd_preprocess(const BwdPreParams &a, int num_sms, cudaStream
 // size (then p.linked may be set).
 cudaError_t launch_bwd_main(int D, int T, const BwdMaps &maps, const BwdMainParams &p, int num_ctas,
                             cudaStream_t stream, int cluster = 1);
-// The packed problem's main kernel (128-row tiles): p.packed is set, p.n counts the tiles of all sequences.
-cudaError_t prepare_packed_bwd(int D);  // checks its registers, raises its shared-memory limit, loads it
-cudaError_t launch_packed_bwd_main(int D, const BwdMainParams &p, int num_ctas, cudaStream_t stream);
 // The largest cluster size among 16, 8, 4, 2 that divides num_ctas and lets
 // every CTA of the launch be resident at once; 1 if none.
 int bwd_main_cluster_size(int D, int T, int num_ctas);

@@ -44,33 +44,52 @@ struct PackedFwdParams {
   long long spin_limit_ns;
 };
 
-// Preprocess of the packed backward: per (Q head, tile) the padded rows' lse2
-// and delta, the semaphore's zero, and each sequence's four tensor maps.
-struct PackedPreParams {
-  const __nv_bfloat16 *o, *dout;
-  const float *lse;  // [Hq][lse_head]
-  long long o_row, o_head, do_row, do_head, lse_head;
-  const int4 *tiles;
-  const int2 *seqs;  // {first packed row, length}
-  float *lse2, *delta;
-  int *sem;
-  CUtensorMap *maps;
-  const void *base[4];       // Q, K, V, dO
-  long long base_row[4];     // their row strides in bytes
-  int n_tiles, n_seqs, heads;
+// The packed backward's two kernels (packed_bwd.cu).  dQ: one Q tile of one
+// head against its KV tiles.
+struct PackedDqItem {
+  int row0;      // first packed row of the Q tile
+  int rows;      // valid rows
+  int nkv;       // KV tiles it attends
+  int head;      // Q head
+  int q0;        // position of its first row in the sequence
+  int kv_row0;   // packed row of the sequence's first key
+  int kv_len;    // keys of the sequence
+  int tile;      // number of the Q tile over all sequences
 };
-cudaError_t launch_packed_preprocess(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                                     const CUtensorMap &dout, const PackedPreParams &p, cudaStream_t stream);
+// dK and dV: one KV tile of one K/V head against the Q tiles of its group.
+struct PackedDkvItem {
+  int row0;      // first packed row of the KV tile
+  int rows;      // valid rows
+  int kv;        // number of the tile in its sequence
+  int head;      // K/V head
+  int n;         // tiles of the sequence
+  int seq_row0;  // the sequence's first packed row
+  int seq_len;
+  int tile0;     // number of the sequence's first tile over all sequences
+};
+static_assert(sizeof(PackedDqItem) == 32 && sizeof(PackedDkvItem) == 32, "items are read as two 16-byte words");
 
-struct PackedConvertParams {
-  const float *accum;        // [Hq][n_tiles][D/4][128][4]
-  const int4 *tiles;
-  __nv_bfloat16 *dq;
-  long long dq_row, dq_head;
-  float scale;
-  int n_tiles, heads;
+struct PackedBwdParams {
+  const PackedDqItem *dq_items;
+  const int *dq_off;       // CTA count + 1
+  const PackedDkvItem *dkv_items;
+  const int *dkv_off;
+  const __nv_bfloat16 *o, *dout;
+  const float *lse;        // [Hq][lse_head]
+  long long o_row, o_head, do_row, do_head, lse_head;
+  float *stats;            // [Hq][n_tiles][2][128]: -LSE log2(e) (-inf behind the sequence), -rowsum(dO O)
+  __nv_bfloat16 *dq, *dk, *dv;
+  long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
+  int n_tiles, group, causal;
+  float scale, scale_log2;
+  int *status;
+  long long spin_limit_ns;
 };
-cudaError_t launch_packed_convert(int D, const PackedConvertParams &p, cudaStream_t stream);
+// Both kernels, dQ first: it writes the stats that the other reads.
+cudaError_t launch_packed_bwd(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                              const CUtensorMap &dout, const PackedBwdParams &p, int dq_ctas, int dkv_ctas,
+                              cudaStream_t stream);
+cudaError_t prepare_packed_bwd(int D);
 
 cudaError_t launch_packed_fwd(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                               const PackedFwdParams &p, int num_ctas, cudaStream_t stream);

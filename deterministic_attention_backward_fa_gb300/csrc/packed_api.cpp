@@ -30,14 +30,13 @@ using dash::report;
 struct dash_packed_plan_st {
   int device = 0, Hq = 0, Hkv = 0, D = 0, causal = 0, n_seqs = 0;
   long long rows = 0, n_tiles = 0;
-  int fwd_ctas = 0, bwd_ctas = 0;  // 0: nothing to do, or (backward) not planned
+  int fwd_ctas = 0, dq_ctas = 0, dkv_ctas = 0;
   bool backward = false;
   void *mem = nullptr;
-  const int2 *seqs = nullptr;
-  const int4 *tiles = nullptr;
-  const dash::PackedFwdItem *items = nullptr;
-  const int *fwd_off = nullptr, *bwd_off = nullptr;
-  const int4 *tasks = nullptr;
+  const dash::PackedFwdItem *fwd = nullptr;
+  const dash::PackedDqItem *dq = nullptr;
+  const dash::PackedDkvItem *dkv = nullptr;
+  const int *fwd_off = nullptr, *dq_off = nullptr, *dkv_off = nullptr;
   int *status = nullptr;
 };
 
@@ -92,31 +91,8 @@ dash_status_t check_heads(int Hq, int Hkv, int D) {
   return DASH_OK;
 }
 
-struct Region {
-  size_t bytes = 0;
-  size_t add(size_t n) {
-    const size_t at = bytes;
-    bytes = (bytes + n + 255) / 256 * 256;
-    return at;
-  }
-};
-
-// Workspace of a packed backward.
-struct BwdLayout {
-  size_t accum, lse2, delta, sem, maps, bytes;
-};
-BwdLayout bwd_layout(const dash_packed_plan_st *p) {
-  const size_t tiles = (size_t)p->n_tiles * p->Hq;
-  Region r;
-  BwdLayout l;
-  l.maps = r.add((size_t)p->n_seqs * 4 * sizeof(CUtensorMap));
-  l.sem = r.add(tiles * dash::kSemStride * 4);
-  l.lse2 = r.add(tiles * dash::kPackedTile * 4);
-  l.delta = r.add(tiles * dash::kPackedTile * 4);
-  l.accum = r.add(tiles * dash::kPackedTile * p->D * 4);
-  l.bytes = r.bytes;
-  return l;
-}
+// Workspace of a packed backward: two floats for every row of every tile and head.
+long long stats_bytes(const dash_packed_plan_st *p) { return p->n_tiles * p->Hq * 2 * dash::kPackedTile * 4; }
 
 dash_status_t check_plan(const dash_packed_plan_st *p, long long rows) {
   if (!p) return report(DASH_ERR_INVALID_ARG, "null plan");
@@ -202,12 +178,11 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
   dash_status_t st = check_heads(Hq, Hkv, D);
   if (st != DASH_OK) return st;
   dash::PackedTables t;
-  std::string why = dash::packed_tiles(lengths, n_seqs, &t);
+  std::string why = dash::packed_sequences(lengths, n_seqs, &t);
   if (!why.empty()) return report(DASH_ERR_INVALID_ARG, "%s", why.c_str());
   int dev = 0;
   Device device;
   if ((st = current_device(&dev, &device)) != DASH_OK) return st;
-  const int sms = device.sms;
   std::unique_ptr<dash_packed_plan_st> p(new dash_packed_plan_st());
   p->device = dev;
   p->Hq = Hq;
@@ -216,48 +191,46 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
   p->causal = causal ? 1 : 0;
   p->n_seqs = n_seqs;
   p->rows = t.rows;
-  p->n_tiles = (long long)t.tiles.size();
+  p->n_tiles = t.n_tiles;
   p->backward = backward != 0;
   if (t.rows > 0) {
-    dash::packed_forward(t, Hq, Hkv, causal != 0, sms, &t);
+    if (t.n_tiles * Hq > INT32_MAX / 4)
+      return report(DASH_ERR_UNSUPPORTED, "%lld tiles of %d heads: beyond the 32-bit tables", t.n_tiles, Hq);
+    dash::packed_forward(Hq, Hkv, causal != 0, device.sms, &t);
     p->fwd_ctas = (int)t.fwd_off.size() - 1;
     if (backward) {
-      why = dash::packed_backward(t, Hq, Hkv, causal != 0, sms, &t);
-      if (!why.empty()) return report(DASH_ERR_UNSUPPORTED, "%s", why.c_str());
-      p->bwd_ctas = (int)t.bwd_off.size() - 1;
+      dash::packed_backward(Hq, Hkv, causal != 0, device.sms, &t);
+      p->dq_ctas = (int)t.dq_off.size() - 1;
+      p->dkv_ctas = (int)t.dkv_off.size() - 1;
     }
     cudaError_t e = dash::prepare_packed_fwd(D);
     if (e != cudaSuccess) return cuda_error(e, "packed forward");
     if (backward && (e = dash::prepare_packed_bwd(D)) != cudaSuccess) return cuda_error(e, "packed backward");
     p->status = device.status;
     // one block of device memory, copied once
-    Region r;
-    const size_t a = r.add(t.seqs.size() * sizeof(int2)), b = r.add(t.tiles.size() * sizeof(int4)),
-                 c = r.add(t.items.size() * sizeof(dash::PackedFwdItem)), d = r.add(t.fwd_off.size() * 4),
-                 f = r.add(t.bwd_off.size() * 4), g = r.add(t.tasks.size() * 4);
-    std::vector<uint8_t> host(r.bytes);
-    auto put = [&](size_t at, const void *src, size_t n) {
-      if (n) std::memcpy(host.data() + at, src, n);
+    std::vector<uint8_t> host;
+    auto put = [&](const void *src, size_t bytes) {
+      const size_t at = (host.size() + 255) / 256 * 256;
+      host.resize(at + bytes);
+      if (bytes) std::memcpy(host.data() + at, src, bytes);
+      return at;
     };
-    put(a, t.seqs.data(), t.seqs.size() * sizeof(int2));
-    put(b, t.tiles.data(), t.tiles.size() * sizeof(int4));
-    put(c, t.items.data(), t.items.size() * sizeof(dash::PackedFwdItem));
-    put(d, t.fwd_off.data(), t.fwd_off.size() * 4);
-    put(f, t.bwd_off.data(), t.bwd_off.size() * 4);
-    put(g, t.tasks.data(), t.tasks.size() * 4);
-    if ((e = cudaMalloc(&p->mem, r.bytes)) != cudaSuccess)
-      return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", r.bytes, cudaGetErrorString(e));
-    if ((e = cudaMemcpy(p->mem, host.data(), r.bytes, cudaMemcpyHostToDevice)) != cudaSuccess) {
+    const size_t at[6] = {put(t.fwd.data(), t.fwd.size() * sizeof(t.fwd[0])), put(t.fwd_off.data(), t.fwd_off.size() * 4),
+                          put(t.dq.data(), t.dq.size() * sizeof(t.dq[0])),    put(t.dq_off.data(), t.dq_off.size() * 4),
+                          put(t.dkv.data(), t.dkv.size() * sizeof(t.dkv[0])), put(t.dkv_off.data(), t.dkv_off.size() * 4)};
+    if ((e = cudaMalloc(&p->mem, host.size())) != cudaSuccess)
+      return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", host.size(), cudaGetErrorString(e));
+    if ((e = cudaMemcpy(p->mem, host.data(), host.size(), cudaMemcpyHostToDevice)) != cudaSuccess) {
       cudaFree(p->mem);
       return cuda_error(e, "plan tables");
     }
     uint8_t *m = static_cast<uint8_t *>(p->mem);
-    p->seqs = reinterpret_cast<const int2 *>(m + a);
-    p->tiles = reinterpret_cast<const int4 *>(m + b);
-    p->items = reinterpret_cast<const dash::PackedFwdItem *>(m + c);
-    p->fwd_off = reinterpret_cast<const int *>(m + d);
-    p->bwd_off = reinterpret_cast<const int *>(m + f);
-    p->tasks = reinterpret_cast<const int4 *>(m + g);
+    p->fwd = reinterpret_cast<const dash::PackedFwdItem *>(m + at[0]);
+    p->fwd_off = reinterpret_cast<const int *>(m + at[1]);
+    p->dq = reinterpret_cast<const dash::PackedDqItem *>(m + at[2]);
+    p->dq_off = reinterpret_cast<const int *>(m + at[3]);
+    p->dkv = reinterpret_cast<const dash::PackedDkvItem *>(m + at[4]);
+    p->dkv_off = reinterpret_cast<const int *>(m + at[5]);
   }
   *plan_out = p.release();
   return DASH_OK;
@@ -281,28 +254,35 @@ void dash_packed_plan_destroy(dash_packed_plan_t *plan) {
 
 long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan) {
   if (!plan || !plan->backward) return -1;
-  return plan->rows ? (long long)bwd_layout(plan).bytes : 0;
+  return stats_bytes(plan);
 }
 
-dash_status_t dash_build_packed_schedule(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int P,
-                                         int32_t *tasks_out, int32_t *cta_off_out, int *ctas_out,
-                                         long long *n_tasks_out) try {
-  if (n_seqs < 0 || (n_seqs > 0 && !lengths) || P < 1 || !n_tasks_out)
-    return report(DASH_ERR_INVALID_ARG, "dash_build_packed_schedule: null pointer or sizes out of range");
+dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int kernel,
+                                      int P, int32_t *items_out, int32_t *cta_off_out, int *ctas_out,
+                                      long long *n_items_out) try {
+  if (n_seqs < 0 || (n_seqs > 0 && !lengths) || P < 1 || kernel < 0 || kernel > 2 || !n_items_out)
+    return report(DASH_ERR_INVALID_ARG, "dash_build_packed_items: null pointer or sizes out of range");
   dash_status_t st = check_heads(Hq, Hkv, 64);
   if (st != DASH_OK) return st;
   dash::PackedTables t;
-  std::string why = dash::packed_tiles(lengths, n_seqs, &t);
+  std::string why = dash::packed_sequences(lengths, n_seqs, &t);
   if (!why.empty()) return report(DASH_ERR_INVALID_ARG, "%s", why.c_str());
-  why = dash::packed_backward(t, Hq, Hkv, causal != 0, P, &t);
-  if (!why.empty()) return report(DASH_ERR_UNSUPPORTED, "%s", why.c_str());
-  *n_tasks_out = (long long)t.tasks.size() / 4;
-  if (ctas_out) *ctas_out = (int)t.bwd_off.size() - 1;
-  if (tasks_out && !t.tasks.empty()) std::memcpy(tasks_out, t.tasks.data(), t.tasks.size() * 4);
-  if (cta_off_out) std::memcpy(cta_off_out, t.bwd_off.data(), t.bwd_off.size() * 4);
+  if (t.n_tiles * Hq > INT32_MAX / 4)
+    return report(DASH_ERR_UNSUPPORTED, "%lld tiles of %d heads: beyond the 32-bit tables", t.n_tiles, Hq);
+  if (kernel == 0)
+    dash::packed_forward(Hq, Hkv, causal != 0, P, &t);
+  else
+    dash::packed_backward(Hq, Hkv, causal != 0, P, &t);
+  const std::vector<int32_t> &off = kernel == 0 ? t.fwd_off : kernel == 1 ? t.dq_off : t.dkv_off;
+  const void *items = kernel == 0 ? (const void *)t.fwd.data() : kernel == 1 ? (const void *)t.dq.data() : t.dkv.data();
+  const size_t size = kernel == 0 ? sizeof(dash::PackedFwdItem) : sizeof(dash::PackedDqItem);
+  *n_items_out = off.back();
+  if (ctas_out) *ctas_out = (int)off.size() - 1;
+  if (items_out && off.back()) std::memcpy(items_out, items, off.back() * size);
+  if (cta_off_out) std::memcpy(cta_off_out, off.data(), off.size() * 4);
   return DASH_OK;
 } catch (...) {
-  return report(DASH_ERR_NO_MEMORY, "dash_build_packed_schedule: out of host memory");
+  return report(DASH_ERR_NO_MEMORY, "dash_build_packed_items: out of host memory");
 }
 
 dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
@@ -326,7 +306,7 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
       (st = dash::encode_rows_map(&mv, v, plan->Hkv, rows, D, rv.row, rv.head, dash::kPackedTile)))
     return st;
   dash::PackedFwdParams p;
-  p.items = plan->items;
+  p.items = plan->fwd;
   p.cta_off = plan->fwd_off;
   p.o = static_cast<__nv_bfloat16 *>(o);
   p.o_row = ro.row;
@@ -345,8 +325,7 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
 dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
                                    const void *o, const void *dout, const float *lse, void *dq, void *dk, void *dv,
                                    long long rows, const int64_t *strides, float scale, void *workspace,
-                                   long long workspace_bytes, dash_stream_t stream_) {
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+                                   long long workspace_bytes, dash_stream_t stream) {
   dash_status_t st = check_scale(scale);
   if (st != DASH_OK || (st = check_plan(plan, rows)) != DASH_OK) return st;
   if (!plan->backward) return report(DASH_ERR_INVALID_ARG, "the plan was made without its backward");
@@ -360,83 +339,50 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
       return st;
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return report(DASH_ERR_INVALID_ARG, "lse must be a pointer to floats");
-  const BwdLayout l = bwd_layout(plan);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < (long long)l.bytes)
-    return report(DASH_ERR_INVALID_ARG, "the workspace must hold %zu bytes, 256-byte aligned", l.bytes);
-  uint8_t *w = static_cast<uint8_t *>(workspace);
-
+  const long long need = stats_bytes(plan);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need)
+    return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
   CUtensorMap m[4];
   const int of[4] = {0, 1, 2, 4};  // Q, K, V, dO
-  dash::PackedPreParams pre;
   for (int i = 0; i < 4; ++i) {
     const int x = of[i];
     if ((st = dash::encode_rows_map(&m[i], ptrs[x], heads[x], rows, plan->D, r[x].row, r[x].head,
                                     dash::kPackedTile)) != DASH_OK)
       return st;
-    pre.base[i] = ptrs[x];
-    pre.base_row[i] = r[x].row * 2;
   }
-  pre.o = static_cast<const __nv_bfloat16 *>(o);
-  pre.dout = static_cast<const __nv_bfloat16 *>(dout);
-  pre.lse = lse;
-  pre.o_row = r[3].row;
-  pre.o_head = r[3].head;
-  pre.do_row = r[4].row;
-  pre.do_head = r[4].head;
-  pre.lse_head = rows;
-  pre.tiles = plan->tiles;
-  pre.seqs = plan->seqs;
-  pre.lse2 = reinterpret_cast<float *>(w + l.lse2);
-  pre.delta = reinterpret_cast<float *>(w + l.delta);
-  pre.sem = reinterpret_cast<int *>(w + l.sem);
-  pre.maps = reinterpret_cast<CUtensorMap *>(w + l.maps);
-  pre.n_tiles = (int)plan->n_tiles;
-  pre.n_seqs = plan->n_seqs;
-  pre.heads = plan->Hq;
-  cudaError_t e = dash::launch_packed_preprocess(plan->D, m[0], m[1], m[2], m[3], pre, stream);
-  if (e != cudaSuccess) return cuda_error(e, "packed preprocess launch");
-
-  dash::BwdMainParams mp = {};
-  mp.tasks = plan->tasks;
-  mp.cta_off = plan->bwd_off;
-  mp.lse2 = pre.lse2;
-  mp.delta = pre.delta;
-  mp.dq_accum = reinterpret_cast<float *>(w + l.accum);
-  mp.sem = pre.sem;
-  mp.dk = static_cast<__nv_bfloat16 *>(dk);
-  mp.dv = static_cast<__nv_bfloat16 *>(dv);
-  mp.status = plan->status;
-  mp.S = INT32_MAX;  // the bounds are the tiles' own
-  mp.n = (int)plan->n_tiles;
-  mp.scale = scale;
-  mp.scale_log2 = scale * kLog2e;
-  mp.causal = plan->causal;
-  mp.ordered = 1;
-  mp.spin_limit_ns = kSpinNs;
-  mp.chains = 1;
-  mp.chain_stride = 0;
-  mp.packed.tiles = plan->tiles;
-  mp.packed.maps = pre.maps;
-  mp.packed.group = plan->Hq / plan->Hkv;
-  mp.packed.dk_row = r[6].row;
-  mp.packed.dk_head = r[6].head;
-  mp.packed.dv_row = r[7].row;
-  mp.packed.dv_head = r[7].head;
-  if ((e = dash::launch_packed_bwd_main(plan->D, mp, plan->bwd_ctas, stream)) != cudaSuccess)
-    return cuda_error(e, "packed main launch");
-
-  dash::PackedConvertParams cp;
-  cp.accum = mp.dq_accum;
-  cp.tiles = plan->tiles;
-  cp.dq = static_cast<__nv_bfloat16 *>(dq);
-  cp.dq_row = r[5].row;
-  cp.dq_head = r[5].head;
-  cp.scale = scale;
-  cp.n_tiles = (int)plan->n_tiles;
-  cp.heads = plan->Hq;
-  if ((e = dash::launch_packed_convert(plan->D, cp, stream)) != cudaSuccess)
-    return cuda_error(e, "packed convert launch");
-  return DASH_OK;
+  dash::PackedBwdParams p;
+  p.dq_items = plan->dq;
+  p.dq_off = plan->dq_off;
+  p.dkv_items = plan->dkv;
+  p.dkv_off = plan->dkv_off;
+  p.o = static_cast<const __nv_bfloat16 *>(o);
+  p.dout = static_cast<const __nv_bfloat16 *>(dout);
+  p.lse = lse;
+  p.o_row = r[3].row;
+  p.o_head = r[3].head;
+  p.do_row = r[4].row;
+  p.do_head = r[4].head;
+  p.lse_head = rows;
+  p.stats = static_cast<float *>(workspace);
+  p.dq = static_cast<__nv_bfloat16 *>(dq);
+  p.dk = static_cast<__nv_bfloat16 *>(dk);
+  p.dv = static_cast<__nv_bfloat16 *>(dv);
+  p.dq_row = r[5].row;
+  p.dq_head = r[5].head;
+  p.dk_row = r[6].row;
+  p.dk_head = r[6].head;
+  p.dv_row = r[7].row;
+  p.dv_head = r[7].head;
+  p.n_tiles = (int)plan->n_tiles;
+  p.group = plan->Hq / plan->Hkv;
+  p.causal = plan->causal;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.status = plan->status;
+  p.spin_limit_ns = kSpinNs;
+  const cudaError_t e = dash::launch_packed_bwd(plan->D, m[0], m[1], m[2], m[3], p, plan->dq_ctas, plan->dkv_ctas,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "packed backward launch");
 }
 
 long long dash_decode_workspace(int B, int Hq, int D, int page_size, int max_pages) {

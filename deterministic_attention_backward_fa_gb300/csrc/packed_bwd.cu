@@ -1,9 +1,29 @@
-// Preprocess and convert of the packed backward; its main kernel is
-// dash_bwd_main (bwd.cu) with kPacked.
+// Packed, grouped-head attention backward for sm_103a, deterministic by
+// construction: every gradient element is summed by one CTA in one order.
 //
-// Both are bound by the bytes they move.  A block takes one (tile, Q head), so
-// a packed row is found without a search, and rows past a sequence's end get
-// lse2 = +inf (P = 0) and delta = 0 in the padded row arrays.
+//   P = 2^(scale log2(e) q.k - LSE log2(e)),  delta_i = dO_i . O_i,
+//   dS = P (dO V^T - delta),
+//   dQ = scale dS K,   dK = scale sum_heads dS^T Q,   dV = sum_heads P^T dO.
+//
+// Two kernels, each with its own P and dS: dQ walks the KV tiles of a Q tile,
+// dK/dV the Q tiles (of every Q head of the group) of a KV tile.  That makes
+// seven products of 128 x 128 x D a tile pair where one kernel for all three
+// gradients makes five, but nothing crosses a CTA: no 32-bit dQ accumulator in
+// memory, no order to enforce between CTAs, no wait of one CTA for another, and
+// dQ's place in tensor memory lets the products run under the softmax.  The
+// one-kernel form (tiles of dQ reduced in the order of a schedule) ran the
+// training batch of 16384 tokens in 737 us and long documents at D = 64 in
+// 2151 us; this one takes DQKV_PACKED and DQKV_D64.
+//
+// Warps of both kernels: 0-7 turn scores into P and dS (a thread owns a row of
+// the accumulator and half of its columns), 8 and 9 issue the MMAs (X and Y),
+// 10 loads, 11 clears rows past a sequence's end that take part in a sum, 12-15
+// write the results of the last item (and, for dQ, make the next item's delta).
+// X and Y take turns, as the forward's MMA warps do: a wait answers about 100
+// clocks after the MMAs in front of it, which the other warp's MMAs cover.
+//
+// P and dS are rounded to bf16 as MMA operands, once each; everything else is
+// held in 32 bits until the gradients' own rounding.
 #include <cuda_runtime.h>
 
 #include "packed.h"
@@ -15,122 +35,964 @@ using namespace dev;
 
 namespace {
 
-// A copy of `src` bounded to one sequence: rows past its end lie outside the
-// map, so the copies fill them with zeros instead of another sequence's rows
-// (whose values, times P = 0, could still be NaN).
-__device__ __forceinline__ void bound_map(CUtensorMap *dst, const CUtensorMap *src, const void *base, int rows) {
-  const int4 *s = reinterpret_cast<const int4 *>(src);
-  int4 *d = reinterpret_cast<int4 *>(dst);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] = s[i];
-  const uint64_t at = reinterpret_cast<uint64_t>(dst);
-  asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(at),
-               "l"(reinterpret_cast<uint64_t>(base))
-               : "memory");
-  asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(at), "r"(rows) : "memory");
-  asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+constexpr int kThreads = 512;
+constexpr int kRegsLaunch = 128;  // 512 threads x 128 registers
+constexpr int kRegsSoft = 168;
+constexpr int kRegsOther = 104;
+constexpr int kRegsOut = 72;
+static_assert(2 * kRegsSoft + kRegsOther + kRegsOut <= 4 * kRegsLaunch, "register split exceeds the CTA's allocation");
+
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t dup2(float a) { return pack2(__float_as_uint(a), __float_as_uint(a)); }
+
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <class T>
+__device__ __forceinline__ T load_item(const T *p) {
+  T it;
+  int4 *d = reinterpret_cast<int4 *>(&it);
+  d[0] = __ldg(reinterpret_cast<const int4 *>(p));
+  d[1] = __ldg(reinterpret_cast<const int4 *>(p) + 1);
+  return it;
 }
 
+// Clears the rows first .. 127 of a swizzled tile (a row is 128 bytes of each
+// 64-column panel, whatever the swizzle does inside it).
 template <int D>
-__global__ void __launch_bounds__(256)
-    dash_packed_preprocess(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int first, int lane) {
+  for (int x = first * 8 + lane; x < kPackedTile * 8; x += 32)
+#pragma unroll
+    for (int pn = 0; pn < D / 64; ++pn)
+      *reinterpret_cast<uint4 *>(tile + pn * (128 * 128) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// A row of D accumulator columns, scaled and rounded.
+template <int D>
+__device__ __forceinline__ void write_row(uint32_t taddr, float scale, bool ok, __nv_bfloat16 *out) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t r[32];
+    tmem_ld32(taddr + c0, r);
+    if (ok) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 w;
+        w.x = pack_bf16(scale * __uint_as_float(r[8 * k + 0]), scale * __uint_as_float(r[8 * k + 1]));
+        w.y = pack_bf16(scale * __uint_as_float(r[8 * k + 2]), scale * __uint_as_float(r[8 * k + 3]));
+        w.z = pack_bf16(scale * __uint_as_float(r[8 * k + 4]), scale * __uint_as_float(r[8 * k + 5]));
+        w.w = pack_bf16(scale * __uint_as_float(r[8 * k + 6]), scale * __uint_as_float(r[8 * k + 7]));
+        *reinterpret_cast<uint4 *>(out + c0 + 8 * k) = w;
+      }
+    }
+  }
+}
+
+// P and dS replace the scores they come from: half h of a row's 128 columns
+// (64 h ..) packs into columns 64 h .. 64 h + 31, which the same thread has
+// read, so the halves never race.  K step kk of the MMA that reads them:
+__device__ __forceinline__ constexpr uint32_t packed_col(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }
+
+// Shared parts of the two kernels.
+template <int D>
+struct Tile {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kBytes = 128 * D * 2;
+  static constexpr uint32_t kPanel = 128 * 128;
+  // k-step offset of a K-major operand, in descriptor units
+  static __device__ __forceinline__ constexpr uint32_t kmajor(int kk) {
+    return ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+  }
+  static __device__ __forceinline__ void load(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int row, int head) {
+    for (int pn = 0; pn < kPanels; ++pn) tma_load_3d(dst + pn * kPanel, m, bar, pn * 64, row, head);
+  }
+};
+
+// ------------------------------------------------------------------- dQ
+// Per KV tile j:   X: dP(j+1) = dO V^T     Y: dQ += dS(j) K, S(j+2) = Q K^T
+// once the softmax warps have dP(j) in registers (X) and dS(j) in tensor memory
+// (Y; S(j+2) takes the place of dS(j), and MMAs of one warp run in issue order).
+// Tensor memory: S and dS in two buffers at 0 and 128, dP at 256, dQ at 384.  V rows past the sequence's end reach dP only, whose
+// columns there are replaced; K rows there are summed over and are cleared.
+template <int D>
+struct DqCfg : Tile<D> {
+  static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;  // stages
+  static constexpr uint32_t oQ = 0, oDO = Tile<D>::kBytes, oK = 2 * Tile<D>::kBytes;
+  static constexpr uint32_t oV = oK + kK * Tile<D>::kBytes;
+  static constexpr uint32_t oSTAT = oV + kV * Tile<D>::kBytes;  // [2][128] {-lse2, -delta}
+  static constexpr uint32_t oBAR = oSTAT + 2 * 128 * 8;
+  enum {
+    bQFull, bQEmpty, bSFull, bDpFull = bSFull + 2, bRead, bDsFull, bOFull, bOEmpty, bTail, bFixed, bTurnX, bTurnY, bFinalX, bFinalY, bStat,
+    bKFull = bStat + 2, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV, kBars = bVEmpty + kV
+  };
+  static constexpr uint32_t oMISC = oBAR + kBars * 8;
+  static constexpr uint32_t kSmem = oMISC + 16;
+  static constexpr uint32_t cDP = 256, cDQ = 384;
+};
+static_assert(DqCfg<128>::kSmem <= 232448 && DqCfg<64>::kSmem <= 232448, "shared memory of one CTA");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dash_packed_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                          const PackedBwdParams p) {
+  using C = DqCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = warp_id(), lane = threadIdx.x & 31;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
+  float2 *stat = reinterpret_cast<float2 *>(smem + C::oSTAT);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < C::kBars; ++b)
+      mbar_init(&bars[b], b == C::bRead || b == C::bDsFull                               ? 8
+                          : b == C::bOEmpty || b == C::bStat || b == C::bStat + 1 ? 4
+                          : b == C::bQEmpty                                       ? 2  // X's last dP, Y's last S
+                                                                                  : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
+  const int i_begin = p.dq_off[blockIdx.x], i_end = p.dq_off[blockIdx.x + 1];
+
+  if (warp >= 12) {
+    // ------------------------------------------------- delta and epilogue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    const int sub = warp & 3;
+    // A warp makes the stats of its 32 rows: D / 8 lanes of 16 bytes a row.
+    auto make_stats = [&](int i) {
+      const PackedDqItem it = load_item(p.dq_items + i);
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kU = 4;
+      const int li = lane % kLanes, rs = lane / kLanes;
+      float2 *out = stat + (i & 1) * 128;
+      float *gout = p.stats + ((size_t)it.head * p.n_tiles + it.tile) * 256;
+      const __nv_bfloat16 *o = p.o + it.row0 * p.o_row + it.head * p.o_head + li * 8;
+      const __nv_bfloat16 *d = p.dout + it.row0 * p.do_row + it.head * p.do_head + li * 8;
+#pragma unroll 1
+      for (int r0 = sub * 32; r0 < sub * 32 + 32; r0 += kRows * kU) {
+        uint4 a[kU], b[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int r = r0 + u * kRows + rs;
+          a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < it.rows) {
+            a[u] = *reinterpret_cast<const uint4 *>(o + r * p.o_row);
+            b[u] = *reinterpret_cast<const uint4 *>(d + r * p.do_row);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(&a[u]);
+          const __nv_bfloat162 *pb = reinterpret_cast<const __nv_bfloat162 *>(&b[u]);
+          float sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 fa = __bfloat1622float2(pa[x]), fb = __bfloat1622float2(pb[x]);
+            sum = fmaf(fa.x, fb.x, sum);
+            sum = fmaf(fa.y, fb.y, sum);
+          }
+#pragma unroll
+          for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          const int r = r0 + u * kRows + rs;
+          if (li == 0) {
+            const float nl = r < it.rows
+                                 ? -p.lse[it.head * p.lse_head + it.row0 + r] * 1.4426950408889634f
+                                 : __int_as_float(0xff800000);
+            out[r] = make_float2(nl, -sum);
+            gout[r] = nl;
+            gout[128 + r] = -sum;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[C::bStat + (i & 1)]);
+    };
+    const int L = sub * 32 + lane;
+    const uint32_t tq = tmem + ((uint32_t)(sub * 32) << 16) + C::cDQ;
+    uint32_t ph = 0;
+    if (i_begin < i_end) make_stats(i_begin);
+    for (int i = i_begin; i < i_end; ++i) {
+      // stats (i + 1) & 1 were read when item i - 1 began, which is over
+      if (i + 1 < i_end) make_stats(i + 1);
+      const PackedDqItem it = load_item(p.dq_items + i);
+      bool ok = mbar_wait(&bars[C::bOFull], ph, g);
+      ph ^= 1;
+      __syncwarp();
+      tc_fence_after();
+      ok &= L < it.rows;
+      write_row<D>(tq, p.scale, ok, p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    uint32_t lead = elect_one();
+    auto wait = [&](int bar, uint32_t ph) {
+      if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
+    };
+    if (warp == 10 && lane == 0) {
+      // -------------------------------------------------------------- TMA
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      prefetch_tmap(&tmDO);
+      Ring<C::kK> rk;
+      Ring<C::kV> rv;
+      uint32_t q_ph = 1, nq = 0, nk = 0, nv = 0;
+      bool live = true;
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDqItem it = load_item(p.dq_items + i);
+        const int kvh = it.head / p.group;
+        live = live && mbar_wait(&bars[C::bQEmpty], q_ph, g);
+        q_ph ^= 1;
+        if (live) {
+          mbar_arrive_expect_tx(&bars[C::bQFull], 2 * C::kBytes);
+          C::load(smem + C::oQ, &tmQ, &bars[C::bQFull], it.row0, it.head);
+          C::load(smem + C::oDO, &tmDO, &bars[C::bQFull], it.row0, it.head);
+          ++nq;
+        }
+        for (int j = 0; j < it.nkv; ++j) {
+          live = live && mbar_wait(&bars[C::bKEmpty + rk.st], rk.ph ^ 1, g);
+          if (live) {
+            mbar_arrive_expect_tx(&bars[C::bKFull + rk.st], C::kBytes);
+            C::load(smem + C::oK + rk.st * C::kBytes, &tmK, &bars[C::bKFull + rk.st], it.kv_row0 + j * kPackedTile, kvh);
+            ++nk;
+          }
+          rk.next();
+          live = live && mbar_wait(&bars[C::bVEmpty + rv.st], rv.ph ^ 1, g);
+          if (live) {
+            mbar_arrive_expect_tx(&bars[C::bVFull + rv.st], C::kBytes);
+            C::load(smem + C::oV + rv.st * C::kBytes, &tmV, &bars[C::bVFull + rv.st], it.kv_row0 + j * kPackedTile, kvh);
+            ++nv;
+          }
+          rv.next();
+        }
+      }
+      // copies still in flight land before the CTA exits
+      if (nq) mbar_drain(&bars[C::bQFull], (nq - 1) & 1, g.limit_ns);
+      for (uint32_t s = 0; s < C::kK; ++s) {
+        const uint32_t f = nk / C::kK + (s < nk % C::kK ? 1u : 0u);
+        if (f) mbar_drain(&bars[C::bKFull + s], (f - 1) & 1, g.limit_ns);
+      }
+      for (uint32_t s = 0; s < C::kV; ++s) {
+        const uint32_t f = nv / C::kV + (s < nv % C::kV ? 1u : 0u);
+        if (f) mbar_drain(&bars[C::bVFull + s], (f - 1) & 1, g.limit_ns);
+      }
+    } else if (warp == 8) {
+      // ------------------------------------------------------- X: dP
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      const uint64_t ddo = sw128_desc(smem_u32(smem + C::oDO), 16, 1024);
+      const uint64_t dv0 = sw128_desc(smem_u32(smem + C::oV), 16, 1024);
+      Ring<C::kV> rv;
+      uint32_t q_ph = 0, read_ph = 0, turn_ph = 1;
+      auto issue = [&](bool pass) {
+        tc_fence_after();
+        const uint64_t dv = dv0 + ((rv.st * C::kBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnY]);
+          mma_ss_if(lead, tmem + C::cDP, ddo + C::kmajor(kk), dv + C::kmajor(kk), idS, kk > 0);
+        }
+        tc_commit_if(lead, &bars[C::bDpFull]);
+        tc_commit_if(lead, &bars[C::bVEmpty + rv.st]);
+        rv.next();
+      };
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDqItem it = load_item(p.dq_items + i);
+        wait(C::bQFull, q_ph);
+        q_ph ^= 1;
+        wait(C::bVFull + rv.st, rv.ph);
+        issue(false);
+        if (it.nkv == 1) tc_commit_if(lead, &bars[C::bQEmpty]);
+        for (int j = 0; j < it.nkv; ++j) {
+          const bool more = j + 1 < it.nkv;
+          if (more) wait(C::bVFull + rv.st, rv.ph);
+          wait(C::bRead, read_ph);  // dP(j) is in registers
+          read_ph ^= 1;
+          wait(C::bTurnX, turn_ph);
+          turn_ph ^= 1;
+          if (more) {
+            issue(true);
+            if (j + 2 == it.nkv) tc_commit_if(lead, &bars[C::bQEmpty]);
+          } else if (lead) {
+            mbar_arrive(&bars[C::bTurnY]);
+          }
+        }
+      }
+      // every MMA has completed before tensor memory is released (at once if none was issued)
+      tc_commit_if(elect_one(), &bars[C::bFinalX]);
+      mbar_drain(&bars[C::bFinalX], 0, g.limit_ns);
+    } else if (warp == 9) {
+      // ------------------------------------------------- Y: S and dQ
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idQ = idesc_bf16(128, D, 0, 1);
+      const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ), 16, 1024);
+      const uint64_t dks0 = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
+      const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oK), C::kPanel, 1024);
+      Ring<C::kK> rs, rk;  // next K tile of S and of dQ
+      uint32_t q_ph = 0, ds_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0, sbuf = 0, buf = 0;
+      auto issue_s = [&](bool fix, bool pass) {
+        wait(C::bKFull + rs.st, rs.ph);
+        if (fix) {
+          if (lead) mbar_arrive(&bars[C::bTail]);
+          wait(C::bFixed, fix_ph);
+          fix_ph ^= 1;
+        }
+        tc_fence_after();
+        const uint64_t dk = dks0 + ((rs.st * C::kBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnX]);
+          mma_ss_if(lead, tmem + sbuf * 128, dq + C::kmajor(kk), dk + C::kmajor(kk), idS, kk > 0);
+        }
+        tc_commit_if(lead, &bars[C::bSFull + sbuf]);
+        sbuf ^= 1;
+        rs.next();
+      };
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDqItem it = load_item(p.dq_items + i);
+        const bool ragged = it.nkv * kPackedTile > it.kv_len;
+        wait(C::bQFull, q_ph);
+        q_ph ^= 1;
+        for (int j = 0; j < min(2, it.nkv); ++j) issue_s(ragged && j + 1 == it.nkv, false);
+        if (it.nkv <= 2) tc_commit_if(lead, &bars[C::bQEmpty]);
+        for (int j = 0; j < it.nkv; ++j) {
+          const bool more = j + 2 < it.nkv;
+          wait(C::bDsFull, ds_ph);
+          ds_ph ^= 1;
+          if (j == 0) {  // the item before has been written out
+            wait(C::bOEmpty, o_ph);
+            o_ph ^= 1;
+          }
+          wait(C::bTurnY, turn_ph);
+          turn_ph ^= 1;
+          tc_fence_after();
+          const uint64_t dk = dk0 + ((rk.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            if (!more && kk == 6 && lead) mbar_arrive(&bars[C::bTurnX]);
+            mma_ts_if(lead, tmem + C::cDQ, tmem + buf * 128 + packed_col(kk), dk + ((kk * 2048) >> 4), idQ,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit_if(lead, &bars[C::bKEmpty + rk.st]);
+          if (j + 1 == it.nkv) tc_commit_if(lead, &bars[C::bOFull]);
+          buf ^= 1;
+          rk.next();
+          if (more) {
+            issue_s(ragged && j + 3 == it.nkv, true);
+            if (j + 3 == it.nkv) tc_commit_if(lead, &bars[C::bQEmpty]);
+          }
+        }
+      }
+      tc_commit_if(elect_one(), &bars[C::bFinalY]);
+      mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
+    } else if (warp == 11) {
+      uint32_t loads = 0, tail_ph = 0;
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDqItem it = load_item(p.dq_items + i);
+        loads += it.nkv;
+        if (it.nkv * kPackedTile > it.kv_len) {
+          wait(C::bTail, tail_ph);
+          tail_ph ^= 1;
+          if (!warp_aborted(g))
+            clear_rows<D>(smem + C::oK + (loads - 1) % C::kK * C::kBytes, it.kv_len - (it.nkv - 1) * kPackedTile, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixed]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- dS
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int sub = warp & 3, half = warp >> 2;
+    const int L = sub * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + 64 * half;
+    const uint64_t sc2 = dup2(p.scale_log2);
+    uint32_t s_ph = 0, dp_ph = 0, buf = 0, st_ph = 0;  // st_ph: a bit per stats buffer
+    for (int i = i_begin; i < i_end; ++i) {
+      const PackedDqItem it = load_item(p.dq_items + i);
+      mbar_wait(&bars[C::bStat + (i & 1)], (st_ph >> (i & 1)) & 1, g);
+      st_ph ^= 1u << (i & 1);
+      const float2 ls = stat[(i & 1) * 128 + L];
+      const uint64_t nl2 = dup2(ls.x), nd2 = dup2(ls.y);
+      const int limit = p.causal ? min(it.kv_len, it.q0 + L + 1) : it.kv_len;
+      for (int j = 0; j < it.nkv; ++j) {
+        mbar_wait(&bars[C::bSFull + buf], s_ph, g);
+        mbar_wait(&bars[C::bDpFull], dp_ph, g);
+        s_ph ^= buf;  // both buffers' parity, which changes after the second
+        dp_ph ^= 1;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t x[2][32], y[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tl + buf * 128 + 32 * c, x[c]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tl + C::cDP + 32 * c, y[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          reg_order32(x[c]);
+          reg_order32(y[c]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::bRead]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float a, b;
+            unpack2(fma2(pack2(x[c][e], x[c][e + 1]), sc2, nl2), a, b);
+            const uint64_t p2 = pack2(__float_as_uint(ex2(a)), __float_as_uint(ex2(b)));
+            unpack2(mul2(p2, add2(pack2(y[c][e], y[c][e + 1]), nd2)), a, b);
+            y[c][e] = __float_as_uint(a);
+            y[c][e + 1] = __float_as_uint(b);
+          }
+        const int cols = limit - j * kPackedTile - 64 * half;  // valid columns of this half
+        if (__any_sync(0xffffffffu, cols < 64)) {
+          // selected, not multiplied: dP there may come from rows of another sequence
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= cols) y[c][e] = 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            pk[e >> 1] = pack_bf16(__uint_as_float(y[c][e]), __uint_as_float(y[c][e + 1]));
+          tmem_st16(tl + buf * 128 + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::bDsFull]);
+        buf ^= 1;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------- dK and dV
+// The accumulators' lanes are KV rows.  Per Q tile i (of every head):
+//   X: dV += P^T(i) dO, S^T(i+1) = K Q^T     Y: dK += dS^T(i) Q, dP^T(i+1) = V dO^T
+// P^T and dS^T replace S^T and dP^T in tensor memory (S at 0, dP at 128, dV at
+// 256, dK at 256 + D).  Rows of Q and dO past the sequence's end are summed
+// over and cleared; K and V rows there only reach accumulator rows that are
+// not written.
+template <int D>
+struct DkvCfg : Tile<D> {
+  static constexpr int kQ = D == 128 ? 3 : 4, kDO = D == 128 ? 2 : 4, kSt = D == 128 ? 2 : 4;  // stages
+  static constexpr uint32_t oK = 0, oV = Tile<D>::kBytes, oQ = 2 * Tile<D>::kBytes;
+  static constexpr uint32_t oDO = oQ + kQ * Tile<D>::kBytes;
+  static constexpr uint32_t oSTAT = oDO + kDO * Tile<D>::kBytes;  // [kSt][2][128]
+  static constexpr uint32_t oBAR = oSTAT + kSt * 1024;
+  enum {
+    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bPFull, bDpFull, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
+    bTailDO, bFixedDO, bTurnX, bTurnY, bFinalX, bFinalY,
+    bQFull, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kDO, bStFull = bDOEmpty + kDO,
+    bStEmpty = bStFull + kSt, kBars = bStEmpty + kSt
+  };
+  static constexpr uint32_t oMISC = oBAR + kBars * 8;
+  static constexpr uint32_t kSmem = oMISC + 16;
+  static constexpr uint32_t cDP = 128, cDV = 256, cDK = 256 + D;
+};
+static_assert(DkvCfg<128>::kSmem <= 232448 && DkvCfg<64>::kSmem <= 232448, "shared memory of one CTA");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dash_packed_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                           const PackedPreParams p) {
-  const int gt = blockIdx.x, h = blockIdx.y;
-  const int4 tile = p.tiles[gt];  // {first row inside the sequence, valid rows, sequence, first packed row}
-  if (h == 0 && tile.x == 0 && threadIdx.x < 4) {
-    const int2 sq = p.seqs[tile.z];
-    const CUtensorMap *src = threadIdx.x == 0 ? &tmQ : threadIdx.x == 1 ? &tmK : threadIdx.x == 2 ? &tmV : &tmDO;
-    bound_map(p.maps + 4 * (size_t)tile.z + threadIdx.x, src,
-              static_cast<const uint8_t *>(p.base[threadIdx.x]) + sq.x * p.base_row[threadIdx.x], sq.y);
+                           const PackedBwdParams p) {
+  using C = DkvCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = warp_id(), lane = threadIdx.x & 31;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
+    return;
   }
-  const size_t key = (size_t)h * p.n_tiles + gt;
-  if (threadIdx.x < kSemStride) p.sem[key * kSemStride + threadIdx.x] = 0;
-  // D / 8 lanes of 16 bytes per row; every thread has all its loads in flight at once
-  constexpr int kLanesPerRow = D / 8, kRowsPerPass = 256 / kLanesPerRow, kPasses = kPackedTile / kRowsPerPass;
-  const int r0 = threadIdx.x / kLanesPerRow, li = threadIdx.x % kLanesPerRow;
-  const __nv_bfloat16 *o = p.o + tile.w * p.o_row + h * p.o_head + li * 8;
-  const __nv_bfloat16 *g = p.dout + tile.w * p.do_row + h * p.do_head + li * 8;
-  uint4 a[kPasses], b[kPasses];
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < C::kBars; ++b) {
+      const bool soft = b == C::bPFull || b == C::bDsFull || b >= C::bStEmpty;
+      const bool both = b >= C::bDOEmpty && b < C::bDOEmpty + C::kDO;  // X's dV and Y's dP have read it
+      mbar_init(&bars[b], soft ? 8 : b == C::bOEmpty ? 4 : both ? 2 : 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
+  const int i_begin = p.dkv_off[blockIdx.x], i_end = p.dkv_off[blockIdx.x + 1];
+
+  if (warp >= 12) {
+    // ---------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    const int sub = warp & 3, L = sub * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
+    uint32_t ph = 0;
+    for (int i = i_begin; i < i_end; ++i) {
+      const PackedDkvItem it = load_item(p.dkv_items + i);
+      bool ok = mbar_wait(&bars[C::bDvFull], ph, g);
+      ok &= mbar_wait(&bars[C::bDkFull], ph, g);
+      ph ^= 1;
+      __syncwarp();
+      tc_fence_after();
+      ok &= L < it.rows;
+      const long long row = (long long)it.row0 + L;
+      write_row<D>(tl + C::cDV, 1.f, ok, p.dv + row * p.dv_row + it.head * p.dv_head);
+      write_row<D>(tl + C::cDK, p.scale, ok, p.dk + row * p.dk_row + it.head * p.dk_head);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    uint32_t lead = elect_one();
+    auto wait = [&](int bar, uint32_t ph) {
+      if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
+    };
+    if (warp == 10 && lane == 0) {
+      // -------------------------------------------------------------- TMA
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      prefetch_tmap(&tmDO);
+      Ring<C::kQ> rq;
+      Ring<C::kDO> rd;
+      Ring<C::kSt> rs;
+      uint32_t e_ph = 1, nkv = 0, nt = 0;
+      bool live = true;
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDkvItem it = load_item(p.dkv_items + i);
+        const int q_first = p.causal ? it.kv : 0;
+        for (int h = 0; h < p.group; ++h)
+          for (int q = q_first; q < it.n; ++q) {
+            const bool first = h == 0 && q == q_first;
+            const int row = it.seq_row0 + q * kPackedTile, head = it.head * p.group + h;
+            if (first) {
+              live = live && mbar_wait(&bars[C::bKEmpty], e_ph, g);
+              if (live) {
+                mbar_arrive_expect_tx(&bars[C::bKFull], C::kBytes);
+                C::load(smem + C::oK, &tmK, &bars[C::bKFull], it.row0, it.head);
+              }
+            }
+            live = live && mbar_wait(&bars[C::bQEmpty + rq.st], rq.ph ^ 1, g);
+            if (live) {
+              mbar_arrive_expect_tx(&bars[C::bQFull + rq.st], C::kBytes);
+              C::load(smem + C::oQ + rq.st * C::kBytes, &tmQ, &bars[C::bQFull + rq.st], row, head);
+            }
+            live = live && mbar_wait(&bars[C::bStEmpty + rs.st], rs.ph ^ 1, g);
+            if (live) {
+              mbar_arrive_expect_tx(&bars[C::bStFull + rs.st], 1024);
+              bulk_load(smem + C::oSTAT + rs.st * 1024, p.stats + ((size_t)head * p.n_tiles + it.tile0 + q) * 256, 1024,
+                        &bars[C::bStFull + rs.st]);
+            }
+            if (first) {
+              live = live && mbar_wait(&bars[C::bVEmpty], e_ph, g);
+              e_ph ^= 1;
+              if (live) {
+                mbar_arrive_expect_tx(&bars[C::bVFull], C::kBytes);
+                C::load(smem + C::oV, &tmV, &bars[C::bVFull], it.row0, it.head);
+                ++nkv;
+              }
+            }
+            live = live && mbar_wait(&bars[C::bDOEmpty + rd.st], rd.ph ^ 1, g);
+            if (live) {
+              mbar_arrive_expect_tx(&bars[C::bDOFull + rd.st], C::kBytes);
+              C::load(smem + C::oDO + rd.st * C::kBytes, &tmDO, &bars[C::bDOFull + rd.st], row, head);
+              ++nt;
+            }
+            rq.next();
+            rs.next();
+            rd.next();
+          }
+      }
+      // Copies still in flight land before the CTA exits.  After an abort a tile's loads may
+      // be cut short between its parts, so the drains (bounded) may find nothing to wait for.
+      auto drain = [&](int bar, uint32_t n, uint32_t stages) {
+        for (uint32_t s = 0; s < stages; ++s) {
+          const uint32_t f = n / stages + (s < n % stages ? 1u : 0u);
+          if (f) mbar_drain(&bars[bar + s], (f - 1) & 1, g.limit_ns);
+        }
+      };
+      drain(C::bKFull, nkv, 1);
+      drain(C::bVFull, nkv, 1);
+      drain(C::bQFull, nt, C::kQ);
+      drain(C::bDOFull, nt, C::kDO);
+      drain(C::bStFull, nt, C::kSt);
+    } else if (warp == 8) {
+      // ------------------------------------------------ X: S^T and dV
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idV = idesc_bf16(128, D, 0, 1);
+      const uint64_t dk = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
+      const uint64_t dq0 = sw128_desc(smem_u32(smem + C::oQ), 16, 1024);
+      const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), C::kPanel, 1024);
+      Ring<C::kQ> rq;
+      Ring<C::kDO> rd;
+      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0;
+      auto q_landed = [&](bool fix) {
+        wait(C::bQFull + rq.st, rq.ph);
+        if (fix) {
+          if (lead) mbar_arrive(&bars[C::bTailQ]);
+          wait(C::bFixedQ, fix_ph);
+          fix_ph ^= 1;
+        }
+      };
+      auto issue_s = [&](bool pass) {
+        const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
 #pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int r = r0 + u * kRowsPerPass;
-    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < tile.y) {
-      a[u] = *reinterpret_cast<const uint4 *>(o + r * p.o_row);
-      b[u] = *reinterpret_cast<const uint4 *>(g + r * p.do_row);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnY]);
+          mma_ss_if(lead, tmem, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
+        }
+        tc_commit_if(lead, &bars[C::bSFull]);
+        rq.next();
+      };
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDkvItem it = load_item(p.dkv_items + i);
+        const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
+        const bool ragged = it.n * kPackedTile > it.seq_len;
+        wait(C::bKFull, k_ph);
+        k_ph ^= 1;
+        q_landed(ragged && per == 1);
+        tc_fence_after();
+        issue_s(false);
+        if (total == 1) tc_commit_if(lead, &bars[C::bKEmpty]);
+        int left = per - 1;  // Q tiles of the head behind the one whose S is issued
+        for (int t = 0; t < total; ++t) {
+          const bool more = t + 1 < total;
+          if (more) {
+            left = left == 0 ? per - 1 : left - 1;
+            q_landed(ragged && left == 0);
+          }
+          wait(C::bDOFull + rd.st, rd.ph);
+          wait(C::bPFull, p_ph);
+          p_ph ^= 1;
+          if (t == 0) {  // the item before has been written out
+            wait(C::bOEmpty, o_ph);
+            o_ph ^= 1;
+          }
+          wait(C::bTurnX, turn_ph);
+          turn_ph ^= 1;
+          tc_fence_after();
+          const uint64_t ddo = ddo0 + ((rd.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            if (!more && kk == 6 && lead) mbar_arrive(&bars[C::bTurnY]);
+            mma_ts_if(lead, tmem + C::cDV, tmem + packed_col(kk), ddo + ((kk * 2048) >> 4), idV,
+                      (t > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit_if(lead, &bars[C::bDOEmpty + rd.st]);
+          rd.next();
+          if (more) {
+            issue_s(true);  // dV has read P: MMAs run in issue order
+            if (t + 2 == total) tc_commit_if(lead, &bars[C::bKEmpty]);
+          } else {
+            tc_commit_if(lead, &bars[C::bDvFull]);
+          }
+        }
+      }
+      tc_commit_if(elect_one(), &bars[C::bFinalX]);
+      mbar_drain(&bars[C::bFinalX], 0, g.limit_ns);
+    } else if (warp == 9) {
+      // ----------------------------------------------- Y: dP^T and dK
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idK = idesc_bf16(128, D, 0, 1);
+      const uint64_t dv = sw128_desc(smem_u32(smem + C::oV), 16, 1024);
+      const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), 16, 1024);
+      const uint64_t dq0 = sw128_desc(smem_u32(smem + C::oQ), C::kPanel, 1024);
+      Ring<C::kQ> rq;
+      Ring<C::kDO> rd;
+      uint32_t v_ph = 0, ds_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0;
+      auto do_landed = [&](bool fix) {
+        wait(C::bDOFull + rd.st, rd.ph);
+        if (fix) {
+          if (lead) mbar_arrive(&bars[C::bTailDO]);
+          wait(C::bFixedDO, fix_ph);
+          fix_ph ^= 1;
+        }
+      };
+      auto issue_dp = [&](bool last) {
+        const uint64_t ddo = ddo0 + ((rd.st * C::kBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnX]);
+          mma_ss_if(lead, tmem + C::cDP, dv + C::kmajor(kk), ddo + C::kmajor(kk), idS, kk > 0);
+        }
+        tc_commit_if(lead, &bars[C::bDpFull]);
+        tc_commit_if(lead, &bars[C::bDOEmpty + rd.st]);
+        if (last) tc_commit_if(lead, &bars[C::bVEmpty]);
+        rd.next();
+      };
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDkvItem it = load_item(p.dkv_items + i);
+        const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
+        const bool ragged = it.n * kPackedTile > it.seq_len;
+        wait(C::bVFull, v_ph);
+        v_ph ^= 1;
+        do_landed(ragged && per == 1);
+        tc_fence_after();
+        issue_dp(total == 1);  // hands X its first turn: dV reads a dO tile whose tail is cleared
+        int left = per - 1;
+        for (int t = 0; t < total; ++t) {
+          const bool more = t + 1 < total;
+          if (more) {
+            left = left == 0 ? per - 1 : left - 1;
+            do_landed(ragged && left == 0);
+          }
+          wait(C::bQFull + rq.st, rq.ph);
+          wait(C::bDsFull, ds_ph);
+          ds_ph ^= 1;
+          if (t == 0) {
+            wait(C::bOEmpty, o_ph);
+            o_ph ^= 1;
+          }
+          wait(C::bTurnY, turn_ph);
+          turn_ph ^= 1;
+          tc_fence_after();
+          const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_if(lead, tmem + C::cDK, tmem + C::cDP + packed_col(kk), dq + ((kk * 2048) >> 4), idK,
+                      (t > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_if(lead, &bars[C::bQEmpty + rq.st]);
+          rq.next();
+          if (more)
+            issue_dp(t + 2 == total);  // dK has read dS
+          else
+            tc_commit_if(lead, &bars[C::bDkFull]);
+        }
+      }
+      tc_commit_if(elect_one(), &bars[C::bFinalY]);
+      mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
+    } else if (warp == 11) {
+      uint32_t loads = 0, ph = 0;
+      for (int i = i_begin; i < i_end; ++i) {
+        const PackedDkvItem it = load_item(p.dkv_items + i);
+        const int per = p.causal ? it.n - it.kv : it.n;
+        const bool ragged = it.n * kPackedTile > it.seq_len;
+        for (int h = 0; h < p.group; ++h) {
+          loads += per;
+          if (!ragged) continue;
+          const int first = it.seq_len - (it.n - 1) * kPackedTile;
+          wait(C::bTailQ, ph);
+          if (!warp_aborted(g)) clear_rows<D>(smem + C::oQ + (loads - 1) % C::kQ * C::kBytes, first, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixedQ]);
+          wait(C::bTailDO, ph);
+          if (!warp_aborted(g)) clear_rows<D>(smem + C::oDO + (loads - 1) % C::kDO * C::kBytes, first, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixedDO]);
+          ph ^= 1;
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------- P and dS
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int sub = warp & 3, half = warp >> 2;
+    const int L = sub * 32 + lane;  // KV row
+    const uint32_t tS = tmem + ((uint32_t)(sub * 32) << 16) + 64 * half, tP = tS + C::cDP;
+    const uint64_t sc2 = dup2(p.scale_log2);
+    Ring<C::kSt> rs;
+    uint32_t s_ph = 0, dp_ph = 0;
+    for (int i = i_begin; i < i_end; ++i) {
+      const PackedDkvItem it = load_item(p.dkv_items + i);
+      const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
+      int k = 0;
+      for (int t = 0; t < total; ++t) {
+        // a causal KV tile's first Q tile of each head is on the diagonal
+        const bool diagonal = p.causal && k == 0;
+        k = k + 1 == per ? 0 : k + 1;
+        const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(smem + C::oSTAT + rs.st * 1024 + half * 256);
+        const ulonglong2 *nd = nl + 32;
+        mbar_wait(&bars[C::bStFull + rs.st], rs.ph, g);
+        mbar_wait(&bars[C::bSFull], s_ph, g);
+        s_ph ^= 1;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t x[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) reg_order32(x[c]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 l4 = nl[8 * c + (e >> 2)];
+            float a, b, u, v;
+            unpack2(fma2(pack2(x[c][e], x[c][e + 1]), sc2, l4.x), a, b);
+            unpack2(fma2(pack2(x[c][e + 2], x[c][e + 3]), sc2, l4.y), u, v);
+            x[c][e] = __float_as_uint(ex2(a));
+            x[c][e + 1] = __float_as_uint(ex2(b));
+            x[c][e + 2] = __float_as_uint(ex2(u));
+            x[c][e + 3] = __float_as_uint(ex2(v));
+          }
+        if (diagonal) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (64 * half + 32 * c + e < L) x[c][e] = 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            pk[e >> 1] = pack_bf16(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+          tmem_st16(tS + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::bPFull]);
+
+        mbar_wait(&bars[C::bDpFull], dp_ph, g);
+        dp_ph ^= 1;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t y[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tP + 32 * c, y[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) reg_order32(y[c]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 d4 = nd[8 * c + (e >> 2)];
+            float a, b, u, v;
+            unpack2(mul2(pack2(x[c][e], x[c][e + 1]), add2(pack2(y[c][e], y[c][e + 1]), d4.x)), a, b);
+            unpack2(mul2(pack2(x[c][e + 2], x[c][e + 3]), add2(pack2(y[c][e + 2], y[c][e + 3]), d4.y)), u, v);
+            pk[e >> 1] = pack_bf16(a, b);
+            pk[(e >> 1) + 1] = pack_bf16(u, v);
+          }
+          tmem_st16(tP + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars[C::bDsFull]);
+          mbar_arrive(&bars[C::bStEmpty + rs.st]);
+        }
+        rs.next();
+      }
     }
   }
-#pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int r = r0 + u * kRowsPerPass;
-    const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(&a[u]);
-    const __nv_bfloat162 *pb = reinterpret_cast<const __nv_bfloat162 *>(&b[u]);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 fa = __bfloat1622float2(pa[i]), fb = __bfloat1622float2(pb[i]);
-      sum = fmaf(fa.x, fb.x, sum);
-      sum = fmaf(fa.y, fb.y, sum);
-    }
-#pragma unroll
-    for (int off = kLanesPerRow / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (li == 0) {
-      const bool valid = r < tile.y;
-      p.delta[key * kPackedTile + r] = sum;
-      p.lse2[key * kPackedTile + r] =
-          valid ? p.lse[h * p.lse_head + tile.w + r] * 1.4426950408889634f : __int_as_float(0x7f800000);
-    }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
-// dQ = bf16(scale * accumulator): the only rounding of dQ below 32 bits.
+template <class Cfg>
+constexpr int smem_bytes() {
+  return Cfg::kSmem > (uint32_t)kMinSmemOneCtaPerSm ? (int)Cfg::kSmem : kMinSmemOneCtaPerSm;
+}
+
+template <class K>
+cudaError_t prepare_kernel(K kernel, int smem) {
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) dash_packed_convert(const PackedConvertParams p) {
-  const int gt = blockIdx.x, h = blockIdx.y;
-  const int4 tile = p.tiles[gt];
-  const float *acc = p.accum + ((size_t)h * p.n_tiles + gt) * (size_t)(kPackedTile * D);
-  constexpr int kGroups = D / 16;  // a thread turns 16 columns of a row into 32 bytes
-#pragma unroll
-  for (int i = threadIdx.x; i < kPackedTile * kGroups; i += 256) {
-    const int r = i & (kPackedTile - 1), gidx = i >> 7;
-    if (r >= tile.y) continue;
-    float4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = *reinterpret_cast<const float4 *>(acc + ((size_t)(4 * gidx + k) * kPackedTile + r) * 4);
-    uint4 o[2];
-    uint32_t *w = reinterpret_cast<uint32_t *>(o);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[2 * k] = pack_bf16(p.scale * v[k].x, p.scale * v[k].y);
-      w[2 * k + 1] = pack_bf16(p.scale * v[k].z, p.scale * v[k].w);
-    }
-    uint4 *out = reinterpret_cast<uint4 *>(p.dq + (long long)(tile.w + r) * p.dq_row + h * p.dq_head + 16 * gidx);
-    out[0] = o[0];
-    out[1] = o[1];
-  }
+cudaError_t prepare_t() {
+  cudaError_t e = prepare_kernel(dash_packed_dq_kernel<D>, smem_bytes<DqCfg<D>>());
+  return e == cudaSuccess ? prepare_kernel(dash_packed_dkv_kernel<D>, smem_bytes<DkvCfg<D>>()) : e;
+}
+
+template <int D>
+cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const CUtensorMap &dout,
+                     const PackedBwdParams &p, int dq_ctas, int dkv_ctas, cudaStream_t stream) {
+  dash_packed_dq_kernel<D><<<dq_ctas, kThreads, smem_bytes<DqCfg<D>>(), stream>>>(q, k, v, dout, p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  dash_packed_dkv_kernel<D><<<dkv_ctas, kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_packed_preprocess(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                                     const CUtensorMap &dout, const PackedPreParams &p, cudaStream_t stream) {
-  const dim3 grid(p.n_tiles, p.heads);
-  if (D == 64)
-    dash_packed_preprocess<64><<<grid, 256, 0, stream>>>(q, k, v, dout, p);
-  else
-    dash_packed_preprocess<128><<<grid, 256, 0, stream>>>(q, k, v, dout, p);
-  return cudaGetLastError();
-}
+cudaError_t prepare_packed_bwd(int D) { return D == 64 ? prepare_t<64>() : prepare_t<128>(); }
 
-cudaError_t launch_packed_convert(int D, const PackedConvertParams &p, cudaStream_t stream) {
-  const dim3 grid(p.n_tiles, p.heads);
-  if (D == 64)
-    dash_packed_convert<64><<<grid, 256, 0, stream>>>(p);
-  else
-    dash_packed_convert<128><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_packed_bwd(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                              const CUtensorMap &dout, const PackedBwdParams &p, int dq_ctas, int dkv_ctas,
+                              cudaStream_t stream) {
+  return D == 64 ? launch_t<64>(q, k, v, dout, p, dq_ctas, dkv_ctas, stream)
+                 : launch_t<128>(q, k, v, dout, p, dq_ctas, dkv_ctas, stream);
 }
 
 }  // namespace dash

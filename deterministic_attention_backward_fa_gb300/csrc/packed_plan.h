@@ -12,27 +12,22 @@ namespace dash {
 
 struct PackedTables {
   std::vector<int2> seqs;              // {first packed row, length}
-  std::vector<int4> tiles;             // {first row inside the sequence, valid rows, sequence, first packed row}
-  std::vector<PackedFwdItem> items;    // grouped by CTA
-  std::vector<int32_t> fwd_off;        // CTA count + 1
-  std::vector<int32_t> tasks;          // backward: {Q head, KV tile, Q tile, rank | flags}, grouped by CTA
-  std::vector<int32_t> bwd_off;        // CTA count + 1
-  long long rows = 0;                  // sum of the lengths
+  long long rows = 0, n_tiles = 0;     // sums over the sequences
+  // items grouped by CTA, each with CTA count + 1 offsets
+  std::vector<PackedFwdItem> fwd;
+  std::vector<PackedDqItem> dq;
+  std::vector<PackedDkvItem> dkv;
+  std::vector<int32_t> fwd_off, dq_off, dkv_off;
 };
 
 // Lengths and tiles.  Empty string on success, else the reason.
-std::string packed_tiles(const int32_t *lengths, int n_seqs, PackedTables *out);
+std::string packed_sequences(const int32_t *lengths, int n_seqs, PackedTables *out);
 
-// The forward's items on up to P CTAs: the most work first, each to the CTA
-// that has the least so far.
-void packed_forward(const PackedTables &t, int Hq, int Hkv, bool causal, int P, PackedTables *out);
-
-// The backward's task table on up to P CTAs.  A chain is one KV tile of one
-// K/V head with every Q head of its group; chains go, the longest of a
-// sequence first, to the CTA that is free first, each task taking one step.  A
-// dQ tile's partials are added in the order of those steps (ties by CTA), so
-// the ranks grow along every CTA's list and no cycle of waits can arise.
-// Empty string on success, else the reason.
-std::string packed_backward(const PackedTables &t, int Hq, int Hkv, bool causal, int P, PackedTables *out);
+// The items of the forward and of the backward's two kernels on up to P CTAs:
+// sequences by decreasing length, inside one the K/V heads in batches whose keys
+// and values fit in L2 together, inside a batch the longest items first, each
+// to the CTA that has the least work so far.
+void packed_forward(int Hq, int Hkv, bool causal, int P, PackedTables *t);
+void packed_backward(int Hq, int Hkv, bool causal, int P, PackedTables *t);
 
 }  // namespace dash

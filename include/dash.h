@@ -465,7 +465,7 @@ dash_status_t dash_die_map(dash_stream_t stream, int32_t *group_of_smid_out, int
  * order of the arguments (NULL: contiguous), so that the parts of a fused
  * projection need no copies.  Strides are multiples of 8, at least D, and rows
  * must not overlap; D itself is contiguous.  Outputs must not overlap inputs.
- * K and V must be finite inside their sequence: as in dash_attn_fwd, a
+ * The inputs must be finite inside their sequence: as in dash_attn_fwd, a
  * non-finite value of a key that the causal mask hides can still reach the
  * rows of its own 128-row tile.  Values outside a sequence never reach it. */
 
@@ -488,12 +488,13 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
                                    dash_stream_t stream);
 
 /* Backward: dq, dk, dv from the forward's inputs, o, lse and dout; dk and dv of
- * a shared head are sums over its Q heads, in 32 bits.  The dQ reduction runs
- * in the order of the plan's task table, so the gradients are bit-identical
- * from run to run (for the same lengths on the same GPU model).  strides: q, k,
- * v, o, dout, dq, dk, dv (16 values).  `workspace` is device memory of
- * dash_packed_bwd_workspace(plan) bytes, 256-byte aligned, used until the
- * call's work is done: calls that overlap need one each.  Can be captured. */
+ * a shared head are sums over its Q heads, in 32 bits.  Every gradient element
+ * is summed by one CTA in one order that depends on its own sequence alone (no
+ * schedule is involved), so its bits are the same in every run and in every
+ * batch.  strides: q, k, v, o, dout, dq, dk, dv (16 values).  `workspace` is
+ * device memory of dash_packed_bwd_workspace(plan) bytes, 16-byte aligned, used
+ * until the call's work is done: calls that overlap need one each.  Can be
+ * captured. */
 dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
                                    const void *o, const void *dout, const float *lse, void *dq, void *dk, void *dv,
                                    long long rows, const int64_t *strides, float scale, void *workspace,
@@ -501,17 +502,19 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
 /* Bytes of that workspace; -1 for a plan made without its backward. */
 long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan);
 
-/* The backward's task table for at most P CTAs, as dash_packed_plan_create
- * builds it for the GPU's SM count (host only): {Q head, KV tile, Q tile,
- * word} per task, tiles of 128 rows numbered over all sequences.  A chain is
- * one KV tile of one K/V head with every Q head of its group; list scheduling
- * puts each chain, a sequence's longest first, on the CTA that is free first,
- * and a dQ tile's partials are added in the order in which the schedule
- * reaches the tile (timed ranks).  tasks_out (4 values per task) and
- * cta_off_out (P + 1 values) may be NULL to ask for the counts. */
-dash_status_t dash_build_packed_schedule(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int P,
-                                         int32_t *tasks_out, int32_t *cta_off_out, int *ctas_out,
-                                         long long *n_tasks_out);
+/* The plan's items for at most P CTAs, as dash_packed_plan_create builds them
+ * for the GPU's SM count (host only), grouped by CTA (cta_off_out: P + 1
+ * values).  Tiles have 128 rows and start at their sequence's first row.
+ * kernel 0, the forward, 16 ints per item: {row0, row0', rows, rows', KV tiles,
+ * KV tiles', Q head, Q head', position, position', first key row, keys, K/V
+ * head, 0, 0, 0} of one or two Q tiles (0 KV tiles: no second one); kernel 1,
+ * dQ, 8 ints: {row0, rows, KV tiles, Q head, position, first key row, keys,
+ * number of the tile}; kernel 2, dK and dV, 8 ints: {row0, rows, KV tile, K/V
+ * head, tiles of the sequence, its first row, its length, number of its first
+ * tile}.  items_out and cta_off_out may be NULL to ask for the counts. */
+dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int kernel,
+                                      int P, int32_t *items_out, int32_t *cta_off_out, int *ctas_out,
+                                      long long *n_items_out);
 
 /* ------------------------------------------------------ paged key-value cache
  * k_pages and v_pages are bf16 [n_pages][page_size][Hkv][D] (strides {page,

@@ -23,46 +23,45 @@ LENS = [[1], [128], [129, 1, 127], [0, 5, 0, 300, 0], [], [0], [1000, 3, 257], [
 @pytest.mark.parametrize("lens", LENS, ids=str)
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 2), (6, 2), (8, 1)])
 @pytest.mark.parametrize("causal", [True, False])
-def test_task_table_is_complete_and_can_finish(lens, hq, hkv, causal):
+def test_items_cover_every_tile_once(lens, hq, hkv, causal):
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(int)
+    tiles = [(s, i) for s, n in enumerate(lens) for i in range(-(-n // 128))]
+    first = {s: tiles.index((s, 0)) for s, n in enumerate(lens) if n}
+    rows = lambda s, i: min(128, lens[s] - 128 * i)
     for P in (1, 7, 152):
-        tasks, off = dash.dash_build_packed_schedule(lens, hq, hkv, causal, P)
-        tiles = [(s, i) for s, n in enumerate(lens) for i in range(-(-n // 128))]
-        want = {(h, a, b) for h in range(hq) for a, (sa, ia) in enumerate(tiles) for b, (sb, ib) in enumerate(tiles)
-                if sa == sb and (not causal or ib >= ia)}
-        assert {tuple(t[:3]) for t in tasks.tolist()} == want and len(tasks) == len(want)
-        assert off[0] == 0 and off[-1] == len(tasks) and (np.diff(off) >= 0).all() and len(off) - 1 <= P
-        order = {}
-        for c in range(len(off) - 1):
-            run = None
-            for i in range(off[c], off[c + 1]):
-                h, kv, q, w = (int(x) for x in tasks[i])
-                order.setdefault((h, q), []).append((w & dash.TASK_RANK_MASK, i - off[c], c))
-                if w & dash.TASK_FIRST:
-                    assert run is None
-                    run, heads = kv, set()
-                assert run == kv
-                heads.add(h)
-                if w & dash.TASK_LAST:  # every head of the group, so dK and dV are whole
-                    assert heads == set(range(h // (hq // hkv) * (hq // hkv), h + 1)) and len(heads) == hq // hkv
-                    run = None
-            assert run is None
-        for v in order.values():
-            v.sort()
-            assert [r for r, _, _ in v] == list(range(len(v)))
-            steps = [(i, c) for _, i, c in v]
-            # a rank's step comes before its successor's: (step, CTA) orders all tasks, so no waits form a cycle
-            assert steps == sorted(steps)
+        got = {}
+        for kernel in range(3):
+            items, off = dash.dash_build_packed_items(lens, hq, hkv, causal, kernel, P)
+            assert off[0] == 0 and off[-1] == len(items) and (np.diff(off) >= 0).all() and len(off) - 1 <= P
+            got[kernel] = items.tolist()
+        n_of = {s: -(-lens[s] // 128) for s in range(len(lens))}
+        q_tiles = sorted((starts[s] + 128 * i, rows(s, i), i + 1 if causal else n_of[s], h, 128 * i, starts[s], lens[s])
+                         for s, i in tiles for h in range(hq))
+        fwd = []
+        for it in got[0]:
+            halves = [h for h in range(2) if it[4 + h]]
+            assert halves in ([0], [0, 1])
+            for h in halves:
+                assert it[6 + h] // (hq // hkv) == it[12]
+                fwd.append((it[h], it[2 + h], it[4 + h], it[6 + h], it[8 + h], it[10], it[11]))
+        assert sorted(fwd) == q_tiles
+        assert sorted(tuple(it[:7]) for it in got[1]) == q_tiles
+        assert all(it[7] == next(first[s] + i for s, i in tiles if starts[s] + 128 * i == it[0]) for it in got[1])
+        assert sorted(map(tuple, got[2])) == sorted(
+            (starts[s] + 128 * i, rows(s, i), i, h, n_of[s], starts[s], lens[s], first[s])
+            for s, i in tiles for h in range(hkv))
 
 
-def test_schedule_refusals():
-    for args, word in ((([-1], 4, 2, True, 8), "negative"), (([5], 4, 3, True, 8), "multiple"),
-                       (([5], 4, 0, True, 8), "multiple"), (([5], 4, 2, True, 0), "out of range"),
-                       (([2**31 - 1, 2**31 - 1], 1, 1, True, 8), "rows")):
+def test_item_refusals():
+    for args, word in ((([-1], 4, 2, True, 0, 8), "negative"), (([5], 4, 3, True, 0, 8), "multiple"),
+                       (([5], 4, 0, True, 1, 8), "multiple"), (([5], 4, 2, True, 2, 0), "out of range"),
+                       (([5], 4, 2, True, 3, 8), "out of range"),
+                       (([2**31 - 1, 2**31 - 1], 1, 1, True, 0, 8), "rows")):
         with pytest.raises(dash.DashError, match=word) as ei:
-            dash.dash_build_packed_schedule(*args)
+            dash.dash_build_packed_items(*args)
         assert ei.value.code == 1
     with pytest.raises(dash.DashError, match="32-bit") as ei:
-        dash.dash_build_packed_schedule([1 << 24], 64, 8, True, 152)
+        dash.dash_build_packed_items([1 << 24], 65024, 8, True, 1, 152)
     assert ei.value.code == 2
 
 
