@@ -19,8 +19,8 @@
 // the accumulator and half of its columns), 8 and 9 issue the MMAs (X and Y),
 // 10 loads, 11 clears rows past a sequence's end that take part in a sum, 12-15
 // write the results of the last item (and, for dQ, make the next item's delta).
-// X and Y take turns, as the forward's MMA warps do: a wait answers about 100
-// clocks after the MMAs in front of it, which the other warp's MMAs cover.
+// Two MMA warps, because a wait answers about 100 clocks after the MMAs in
+// front of it, which the other warp's MMAs cover.
 //
 // P and dS are rounded to bf16 as MMA operands, once each; everything else is
 // held in 32 bits until the gradients' own rounding.
@@ -38,8 +38,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kRegsLaunch = 128;  // 512 threads x 128 registers
 constexpr int kRegsSoft = 168;
-constexpr int kRegsOther = 104;
-constexpr int kRegsOut = 72;
+constexpr int kRegsOther = 72;
+constexpr int kRegsOut = 104;     // a packed row of an accumulator, or the rows that make delta
 static_assert(2 * kRegsSoft + kRegsOther + kRegsOut <= 4 * kRegsLaunch, "register split exceeds the CTA's allocation");
 
 __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
@@ -100,31 +100,36 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int first, int lane) {
   __syncwarp();
 }
 
-// A row of D accumulator columns, scaled and rounded.
+// A row of D accumulator columns, scaled and rounded, in registers: tensor
+// memory is free before the row goes to global memory.
 template <int D>
-__device__ __forceinline__ void write_row(uint32_t taddr, float scale, bool ok, __nv_bfloat16 *out) {
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t r[32];
-    tmem_ld32(taddr + c0, r);
-    if (ok) {
+struct OutRow {
+  uint32_t w[D / 2];
+  __device__ __forceinline__ void read(uint32_t taddr, float scale) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint4 w;
-        w.x = pack_bf16(scale * __uint_as_float(r[8 * k + 0]), scale * __uint_as_float(r[8 * k + 1]));
-        w.y = pack_bf16(scale * __uint_as_float(r[8 * k + 2]), scale * __uint_as_float(r[8 * k + 3]));
-        w.z = pack_bf16(scale * __uint_as_float(r[8 * k + 4]), scale * __uint_as_float(r[8 * k + 5]));
-        w.w = pack_bf16(scale * __uint_as_float(r[8 * k + 6]), scale * __uint_as_float(r[8 * k + 7]));
-        *reinterpret_cast<uint4 *>(out + c0 + 8 * k) = w;
-      }
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t r[32];
+      tmem_ld32(taddr + 32 * c, r);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        w[16 * c + (e >> 1)] = pack_bf16(scale * __uint_as_float(r[e]), scale * __uint_as_float(r[e + 1]));
     }
   }
-}
+  __device__ __forceinline__ void write(__nv_bfloat16 *out) const {
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k)
+      *reinterpret_cast<uint4 *>(out + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+};
 
-// P and dS replace the scores they come from: half h of a row's 128 columns
-// (64 h ..) packs into columns 64 h .. 64 h + 31, which the same thread has
-// read, so the halves never race.  K step kk of the MMA that reads them:
-__device__ __forceinline__ constexpr uint32_t packed_col(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }
+// P and dS replace the scores they come from: the kCols columns of a thread
+// pack into the first half of their own place, which the same thread has read,
+// so threads of one row never race.  K step kk (16 columns) of the MMA that
+// reads them:
+template <int kCols>
+__device__ __forceinline__ constexpr uint32_t packed_col(int kk) {
+  return 16 * kk / kCols * kCols + 16 * kk % kCols / 2;
+}
 
 // Shared parts of the two kernels.
 template <int D>
@@ -155,7 +160,9 @@ struct DqCfg : Tile<D> {
   static constexpr uint32_t oSTAT = oV + kV * Tile<D>::kBytes;  // [2][128] {-lse2, -delta}
   static constexpr uint32_t oBAR = oSTAT + 2 * 128 * 8;
   enum {
-    bQFull, bQEmpty, bSFull, bDpFull = bSFull + 2, bRead, bDsFull, bOFull, bOEmpty, bTail, bFixed, bTurnX, bTurnY, bFinalX, bFinalY, bStat,
+    // S and dS have a barrier per buffer: a warp may be a tile ahead of another.  So have the tails: S, which
+    // asks for them, is up to two items ahead of dQ, which waits for them.
+    bQFull, bQEmpty, bSFull, bDpFull = bSFull + 2, bRead, bDsFull, bOFull = bDsFull + 2, bOEmpty, bTail, bFixed = bTail + 2, bFinalX = bFixed + 2, bFinalY, bStat,
     bKFull = bStat + 2, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV, kBars = bVEmpty + kV
   };
   static constexpr uint32_t oMISC = oBAR + kBars * 8;
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::kBars; ++b)
-      mbar_init(&bars[b], b == C::bRead || b == C::bDsFull                               ? 8
+      mbar_init(&bars[b], b >= C::bRead && b < C::bDsFull + 2                            ? 8
                           : b == C::bOEmpty || b == C::bStat || b == C::bStat + 1 ? 4
                           : b == C::bQEmpty                                       ? 2  // X's last dP, Y's last S
                                                                                   : 1);
@@ -204,21 +211,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- delta and epilogue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int sub = warp & 3;
-    // A warp makes the stats of its 32 rows: D / 8 lanes of 16 bytes a row.
+    // A warp makes the stats of its 32 rows: D / 8 lanes of 16 bytes a row, two
+    // rounds of loads.  The rows come from memory (nobody else has read O), so
+    // the item behind asks L2 for them: 18000 clocks an item without that and
+    // with four rounds, longer than a short item takes.
+    auto ask = [&](int i) {
+      const PackedDqItem it = load_item(p.dq_items + i);
+      const int r = sub * 32 + lane;
+      if (r < it.rows) {
+        const __nv_bfloat16 *o = p.o + (it.row0 + r) * p.o_row + it.head * p.o_head;
+        const __nv_bfloat16 *d = p.dout + (it.row0 + r) * p.do_row + it.head * p.do_head;
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(o + c));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(d + c));
+        }
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lse + it.head * p.lse_head + it.row0 + r));
+      }
+    };
     auto make_stats = [&](int i) {
       const PackedDqItem it = load_item(p.dq_items + i);
-      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kU = 4;
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kU = 16 / kRows;
       const int li = lane % kLanes, rs = lane / kLanes;
       float2 *out = stat + (i & 1) * 128;
       float *gout = p.stats + ((size_t)it.head * p.n_tiles + it.tile) * 256;
       const __nv_bfloat16 *o = p.o + it.row0 * p.o_row + it.head * p.o_head + li * 8;
       const __nv_bfloat16 *d = p.dout + it.row0 * p.do_row + it.head * p.do_head + li * 8;
+      const int mine = sub * 32 + lane;
+      float nl = __int_as_float(0xff800000), nd = 0.f;  // of this lane's row
+      if (mine < it.rows) nl = -p.lse[it.head * p.lse_head + it.row0 + mine] * 1.4426950408889634f;
 #pragma unroll 1
-      for (int r0 = sub * 32; r0 < sub * 32 + 32; r0 += kRows * kU) {
+      for (int half = 0; half < 2; ++half) {
         uint4 a[kU], b[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int r = r0 + u * kRows + rs;
+          const int r = sub * 32 + half * 16 + u * kRows + rs;
           a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
           if (r < it.rows) {
             a[u] = *reinterpret_cast<const uint4 *>(o + r * p.o_row);
@@ -238,17 +265,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          const int r = r0 + u * kRows + rs;
-          if (li == 0) {
-            const float nl = r < it.rows
-                                 ? -p.lse[it.head * p.lse_head + it.row0 + r] * 1.4426950408889634f
-                                 : __int_as_float(0xff800000);
-            out[r] = make_float2(nl, -sum);
-            gout[r] = nl;
-            gout[128 + r] = -sum;
-          }
+          // every lane of a row has its sum: hand it to the lane that keeps the row
+          const int at = lane - half * 16 - u * kRows;
+          const float got = __shfl_sync(0xffffffffu, sum, (at & (kRows - 1)) * kLanes);
+          if (at >= 0 && at < kRows) nd = -got;
         }
       }
+      out[mine] = make_float2(nl, nd);
+      gout[mine] = nl;
+      gout[128 + mine] = nd;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[C::bStat + (i & 1)]);
     };
@@ -256,19 +281,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tq = tmem + ((uint32_t)(sub * 32) << 16) + C::cDQ;
     uint32_t ph = 0;
     if (i_begin < i_end) make_stats(i_begin);
+    if (i_begin + 1 < i_end) ask(i_begin + 1);
     for (int i = i_begin; i < i_end; ++i) {
       // stats (i + 1) & 1 were read when item i - 1 began, which is over
       if (i + 1 < i_end) make_stats(i + 1);
+      if (i + 2 < i_end) ask(i + 2);
       const PackedDqItem it = load_item(p.dq_items + i);
       bool ok = mbar_wait(&bars[C::bOFull], ph, g);
       ph ^= 1;
       __syncwarp();
       tc_fence_after();
-      ok &= L < it.rows;
-      write_row<D>(tq, p.scale, ok, p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head);
+      OutRow<D> out;
+      out.read(tq, p.scale);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+      if (ok && L < it.rows) out.write(p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head);
+      __syncwarp();
     }
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -330,40 +359,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t ddo = sw128_desc(smem_u32(smem + C::oDO), 16, 1024);
       const uint64_t dv0 = sw128_desc(smem_u32(smem + C::oV), 16, 1024);
       Ring<C::kV> rv;
-      uint32_t q_ph = 0, read_ph = 0, turn_ph = 1;
-      auto issue = [&](bool pass) {
-        tc_fence_after();
-        const uint64_t dv = dv0 + ((rv.st * C::kBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnY]);
-          mma_ss_if(lead, tmem + C::cDP, ddo + C::kmajor(kk), dv + C::kmajor(kk), idS, kk > 0);
-        }
-        tc_commit_if(lead, &bars[C::bDpFull]);
-        tc_commit_if(lead, &bars[C::bVEmpty + rv.st]);
-        rv.next();
-      };
+      uint32_t q_ph = 0, read_ph = 1;
       for (int i = i_begin; i < i_end; ++i) {
-        const PackedDqItem it = load_item(p.dq_items + i);
+        const int nkv = p.dq_items[i].nkv;
         wait(C::bQFull, q_ph);
         q_ph ^= 1;
-        wait(C::bVFull + rv.st, rv.ph);
-        issue(false);
-        if (it.nkv == 1) tc_commit_if(lead, &bars[C::bQEmpty]);
-        for (int j = 0; j < it.nkv; ++j) {
-          const bool more = j + 1 < it.nkv;
-          if (more) wait(C::bVFull + rv.st, rv.ph);
-          wait(C::bRead, read_ph);  // dP(j) is in registers
+        for (int j = 0; j < nkv; ++j) {
+          wait(C::bVFull + rv.st, rv.ph);
+          wait(C::bRead, read_ph);  // the dP before is in registers
           read_ph ^= 1;
-          wait(C::bTurnX, turn_ph);
-          turn_ph ^= 1;
-          if (more) {
-            issue(true);
-            if (j + 2 == it.nkv) tc_commit_if(lead, &bars[C::bQEmpty]);
-          } else if (lead) {
-            mbar_arrive(&bars[C::bTurnY]);
-          }
+          tc_fence_after();
+          const uint64_t dv = dv0 + ((rv.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_if(lead, tmem + C::cDP, ddo + C::kmajor(kk), dv + C::kmajor(kk), idS, kk > 0);
+          tc_commit_if(lead, &bars[C::bDpFull]);
+          tc_commit_if(lead, &bars[C::bVEmpty + rv.st]);
+          rv.next();
         }
+        tc_commit_if(lead, &bars[C::bQEmpty]);
       }
       // every MMA has completed before tensor memory is released (at once if none was issued)
       tc_commit_if(elect_one(), &bars[C::bFinalX]);
@@ -376,73 +390,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dks0 = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
       const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oK), C::kPanel, 1024);
       Ring<C::kK> rs, rk;  // next K tile of S and of dQ
-      uint32_t q_ph = 0, ds_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0, sbuf = 0, buf = 0;
-      auto issue_s = [&](bool fix, bool pass) {
+      uint32_t q_ph = 0, ds_ph = 0, o_ph = 1, fix_ph = 0, fix = 0, tail = 0, sbuf = 0, buf = 0;
+      // S runs two tiles ahead of dQ, from one item into the next
+      int s_item = i_begin, s_j = 0, s_n = 0, s_len = 0;
+      auto next_s = [&] {
+        if (s_item >= i_end) return;
+        if (s_j == 0) {
+          s_n = p.dq_items[s_item].nkv;
+          s_len = p.dq_items[s_item].kv_len;
+          wait(C::bQFull, q_ph);
+          q_ph ^= 1;
+        }
         wait(C::bKFull + rs.st, rs.ph);
-        if (fix) {
-          if (lead) mbar_arrive(&bars[C::bTail]);
-          wait(C::bFixed, fix_ph);
-          fix_ph ^= 1;
+        const bool last = s_j + 1 == s_n;
+        // it has landed: the rows past the end may be cleared, while S reads them (their columns are replaced)
+        if (last && s_n * kPackedTile > s_len) {
+          if (lead) mbar_arrive(&bars[C::bTail + tail]);
+          tail ^= 1;
         }
         tc_fence_after();
         const uint64_t dk = dks0 + ((rs.st * C::kBytes) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnX]);
+        for (int kk = 0; kk < D / 16; ++kk)
           mma_ss_if(lead, tmem + sbuf * 128, dq + C::kmajor(kk), dk + C::kmajor(kk), idS, kk > 0);
-        }
         tc_commit_if(lead, &bars[C::bSFull + sbuf]);
+        if (last) tc_commit_if(lead, &bars[C::bQEmpty]);
         sbuf ^= 1;
         rs.next();
+        ++s_j;
+        if (last) {
+          s_j = 0;
+          ++s_item;
+        }
       };
+      next_s();
+      next_s();
       for (int i = i_begin; i < i_end; ++i) {
-        const PackedDqItem it = load_item(p.dq_items + i);
-        const bool ragged = it.nkv * kPackedTile > it.kv_len;
-        wait(C::bQFull, q_ph);
-        q_ph ^= 1;
-        for (int j = 0; j < min(2, it.nkv); ++j) issue_s(ragged && j + 1 == it.nkv, false);
-        if (it.nkv <= 2) tc_commit_if(lead, &bars[C::bQEmpty]);
-        for (int j = 0; j < it.nkv; ++j) {
-          const bool more = j + 2 < it.nkv;
-          wait(C::bDsFull, ds_ph);
-          ds_ph ^= 1;
+        const int nkv = p.dq_items[i].nkv;
+        const bool ragged = nkv * kPackedTile > p.dq_items[i].kv_len;
+        for (int j = 0; j < nkv; ++j) {
+          if (ragged && j + 1 == nkv) {
+            wait(C::bFixed + fix, fix_ph);
+            fix_ph ^= fix;
+            fix ^= 1;
+          }
           if (j == 0) {  // the item before has been written out
             wait(C::bOEmpty, o_ph);
             o_ph ^= 1;
           }
-          wait(C::bTurnY, turn_ph);
-          turn_ph ^= 1;
+          wait(C::bDsFull + buf, ds_ph);
+          ds_ph ^= buf;  // both buffers' parity, which changes after the second
           tc_fence_after();
           const uint64_t dk = dk0 + ((rk.st * C::kBytes) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            if (!more && kk == 6 && lead) mbar_arrive(&bars[C::bTurnX]);
-            mma_ts_if(lead, tmem + C::cDQ, tmem + buf * 128 + packed_col(kk), dk + ((kk * 2048) >> 4), idQ,
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_if(lead, tmem + C::cDQ, tmem + buf * 128 + packed_col<64>(kk), dk + ((kk * 2048) >> 4), idQ,
                       (j > 0 || kk > 0) ? 1u : 0u);
-          }
           tc_commit_if(lead, &bars[C::bKEmpty + rk.st]);
-          if (j + 1 == it.nkv) tc_commit_if(lead, &bars[C::bOFull]);
+          if (j + 1 == nkv) tc_commit_if(lead, &bars[C::bOFull]);
           buf ^= 1;
           rk.next();
-          if (more) {
-            issue_s(ragged && j + 3 == it.nkv, true);
-            if (j + 3 == it.nkv) tc_commit_if(lead, &bars[C::bQEmpty]);
-          }
+          next_s();
         }
       }
       tc_commit_if(elect_one(), &bars[C::bFinalY]);
       mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
     } else if (warp == 11) {
-      uint32_t loads = 0, tail_ph = 0;
+      uint32_t loads = 0, tail_ph = 0, tail = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDqItem it = load_item(p.dq_items + i);
         loads += it.nkv;
         if (it.nkv * kPackedTile > it.kv_len) {
-          wait(C::bTail, tail_ph);
-          tail_ph ^= 1;
+          wait(C::bTail + tail, tail_ph);
           if (!warp_aborted(g))
             clear_rows<D>(smem + C::oK + (loads - 1) % C::kK * C::kBytes, it.kv_len - (it.nkv - 1) * kPackedTile, lane);
-          if (lane == 0) mbar_arrive(&bars[C::bFixed]);
+          if (lane == 0) mbar_arrive(&bars[C::bFixed + tail]);
+          tail_ph ^= tail;
+          tail ^= 1;
         }
       }
     }
@@ -464,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < it.nkv; ++j) {
         mbar_wait(&bars[C::bSFull + buf], s_ph, g);
         mbar_wait(&bars[C::bDpFull], dp_ph, g);
-        s_ph ^= buf;  // both buffers' parity, which changes after the second
+        s_ph ^= buf;
         dp_ph ^= 1;
         __syncwarp();
         tc_fence_after();
@@ -513,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[C::bDsFull]);
+        if (lane == 0) mbar_arrive(&bars[C::bDsFull + buf]);
         buf ^= 1;
       }
     }
@@ -530,36 +554,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The accumulators' lanes are KV rows.  Per Q tile i (of every head):
 //   X: dV += P^T(i) dO, S^T(i+1) = K Q^T     Y: dK += dS^T(i) Q, dP^T(i+1) = V dO^T
 // P^T and dS^T replace S^T and dP^T in tensor memory (S at 0, dP at 128, dV at
-// 256, dK at 256 + D).  Rows of Q and dO past the sequence's end are summed
-// over and cleared; K and V rows there only reach accumulator rows that are
+// 256, dK at 256 + D; at D = 64 two S at 0 and 128 and the others behind).
+// Rows of dO (for dV) and of Q (for dK) past the sequence's end are summed over
+// and cleared first; K and V rows there only reach accumulator rows that are
 // not written.
 template <int D>
 struct DkvCfg : Tile<D> {
   static constexpr int kQ = D == 128 ? 3 : 4, kDO = D == 128 ? 2 : 4, kSt = D == 128 ? 2 : 4;  // stages
+  // Buffers of S^T: a second one, where tensor memory has room, lets the next
+  // score run before dV has read this P.
+  static constexpr int kS = D == 128 ? 1 : 2;
+  // With one buffer, S -> P -> dV -> S is the chain that sets the pace, and X
+  // and Y take turns so that each pair of products runs in one piece.
+  static constexpr bool kTurns = kS == 1;
   static constexpr uint32_t oK = 0, oV = Tile<D>::kBytes, oQ = 2 * Tile<D>::kBytes;
   static constexpr uint32_t oDO = oQ + kQ * Tile<D>::kBytes;
   static constexpr uint32_t oSTAT = oDO + kDO * Tile<D>::kBytes;  // [kSt][2][128]
   static constexpr uint32_t oBAR = oSTAT + kSt * 1024;
   enum {
-    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bPFull, bDpFull, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
+    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bPFull = bSFull + kS, bDpFull = bPFull + kS, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
     bTailDO, bFixedDO, bTurnX, bTurnY, bFinalX, bFinalY,
     bQFull, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kDO, bStFull = bDOEmpty + kDO,
     bStEmpty = bStFull + kSt, kBars = bStEmpty + kSt
   };
   static constexpr uint32_t oMISC = oBAR + kBars * 8;
   static constexpr uint32_t kSmem = oMISC + 16;
-  static constexpr uint32_t cDP = 128, cDV = 256, cDK = 256 + D;
+  static constexpr int kSoft = 16, kCols = 128 / (kSoft / 4);  // softmax warps, columns of a thread
+  static constexpr int kThreads = (kSoft + 8) * 32;
+  static constexpr int kRegsLaunch = 80, kRegsSoft = 88, kRegsOther = 64, kRegsOut = 64;
+  static_assert(kRegsSoft * kSoft / 4 + kRegsOther + kRegsOut <= kRegsLaunch * (kSoft + 8) / 4, "register split");
+  static constexpr uint32_t cDP = 128 * kS, cDV = cDP + 128, cDK = cDV + D;
+  static_assert(cDK + D <= 512, "tensor memory");
 };
 static_assert(DkvCfg<128>::kSmem <= 232448 && DkvCfg<64>::kSmem <= 232448, "shared memory of one CTA");
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
     dash_packed_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                            const PackedBwdParams p) {
   using C = DkvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = warp_id(), lane = threadIdx.x & 31;
+  const int role = warp - C::kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 clears, 4-7 write the results
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
@@ -569,14 +606,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::kBars; ++b) {
-      const bool soft = b == C::bPFull || b == C::bDsFull || b >= C::bStEmpty;
+      const bool soft = (b >= C::bPFull && b < C::bDpFull) || b == C::bDsFull || b >= C::bStEmpty;
       const bool both = b >= C::bDOEmpty && b < C::bDOEmpty + C::kDO;  // X's dV and Y's dP have read it
-      mbar_init(&bars[b], soft ? 8 : b == C::bOEmpty ? 4 : both ? 2 : 1);
+      mbar_init(&bars[b], soft ? C::kSoft : b == C::bOEmpty ? 4 : both ? 2 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (role == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -587,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
   const int i_begin = p.dkv_off[blockIdx.x], i_end = p.dkv_off[blockIdx.x + 1];
 
-  if (warp >= 12) {
+  if (role >= 4) {
     // ---------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOut));
     const int sub = warp & 3, L = sub * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
     uint32_t ph = 0;
@@ -602,19 +639,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       ok &= L < it.rows;
       const long long row = (long long)it.row0 + L;
-      write_row<D>(tl + C::cDV, 1.f, ok, p.dv + row * p.dv_row + it.head * p.dv_head);
-      write_row<D>(tl + C::cDK, p.scale, ok, p.dk + row * p.dk_row + it.head * p.dk_head);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+      auto write = [&](uint32_t taddr, float scale, __nv_bfloat16 *to, bool last) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          OutRow<32> out;
+          out.read(taddr + c, scale);
+          if (last && c + 32 == D) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+          }
+          if (ok) out.write(to + c);
+          __syncwarp();
+        }
+      };
+      write(tl + C::cDV, 1.f, p.dv + row * p.dv_row + it.head * p.dv_head, false);
+      write(tl + C::cDK, p.scale, p.dk + row * p.dk_row + it.head * p.dk_head, true);
     }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  } else if (role >= 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     uint32_t lead = elect_one();
     auto wait = [&](int bar, uint32_t ph) {
       if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
     };
-    if (warp == 10 && lane == 0) {
+    if (role == 2 && lane == 0) {
       // -------------------------------------------------------------- TMA
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmK);
@@ -683,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain(C::bQFull, nt, C::kQ);
       drain(C::bDOFull, nt, C::kDO);
       drain(C::bStFull, nt, C::kSt);
-    } else if (warp == 8) {
+    } else if (role == 0) {
       // ------------------------------------------------ X: S^T and dV
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idV = idesc_bf16(128, D, 0, 1);
@@ -692,72 +740,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), C::kPanel, 1024);
       Ring<C::kQ> rq;
       Ring<C::kDO> rd;
-      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0;
-      auto q_landed = [&](bool fix) {
-        wait(C::bQFull + rq.st, rq.ph);
-        if (fix) {
-          if (lead) mbar_arrive(&bars[C::bTailQ]);
-          wait(C::bFixedQ, fix_ph);
-          fix_ph ^= 1;
-        }
-      };
-      auto issue_s = [&](bool pass) {
-        const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnY]);
-          mma_ss_if(lead, tmem, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
-        }
-        tc_commit_if(lead, &bars[C::bSFull]);
-        rq.next();
-      };
+      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0, sbuf = 0, buf = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
         const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
         const bool ragged = it.n * kPackedTile > it.seq_len;
+        int left = per, issued = 0;  // Q tiles of the head from this one on; scores issued
+        auto issue_s = [&](bool pass) {
+          tc_fence_after();
+          const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            if (C::kTurns && pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnY]);
+            mma_ss_if(lead, tmem + sbuf * 128, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
+          }
+          tc_commit_if(lead, &bars[C::bSFull + sbuf]);
+          if (++issued == total) tc_commit_if(lead, &bars[C::bKEmpty]);
+          rq.next();
+          sbuf = (sbuf + 1) % C::kS;
+        };
         wait(C::bKFull, k_ph);
         k_ph ^= 1;
-        q_landed(ragged && per == 1);
-        tc_fence_after();
-        issue_s(false);
-        if (total == 1) tc_commit_if(lead, &bars[C::bKEmpty]);
-        int left = per - 1;  // Q tiles of the head behind the one whose S is issued
+        for (int t = 0; t < min(C::kS, total); ++t) {
+          wait(C::bQFull + rq.st, rq.ph);
+          issue_s(false);
+        }
         for (int t = 0; t < total; ++t) {
-          const bool more = t + 1 < total;
-          if (more) {
-            left = left == 0 ? per - 1 : left - 1;
-            q_landed(ragged && left == 0);
-          }
+          const bool more = t + C::kS < total;
           wait(C::bDOFull + rd.st, rd.ph);
-          wait(C::bPFull, p_ph);
-          p_ph ^= 1;
+          if (ragged && left == 1) {  // the head's last tile: its rows past the end are summed over
+            if (lead) mbar_arrive(&bars[C::bTailDO]);
+            wait(C::bFixedDO, fix_ph);
+            fix_ph ^= 1;
+          }
+          left = left == 1 ? per : left - 1;
           if (t == 0) {  // the item before has been written out
             wait(C::bOEmpty, o_ph);
             o_ph ^= 1;
           }
-          wait(C::bTurnX, turn_ph);
-          turn_ph ^= 1;
+          if (C::kTurns) {
+            if (more) wait(C::bQFull + rq.st, rq.ph);
+            wait(C::bTurnX, turn_ph);
+            turn_ph ^= 1;
+          }
+          wait(C::bPFull + buf, p_ph);
+          p_ph ^= (int)buf == C::kS - 1;  // the buffers' parity changes after the last one
           tc_fence_after();
           const uint64_t ddo = ddo0 + ((rd.st * C::kBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            if (!more && kk == 6 && lead) mbar_arrive(&bars[C::bTurnY]);
-            mma_ts_if(lead, tmem + C::cDV, tmem + packed_col(kk), ddo + ((kk * 2048) >> 4), idV,
+            if (C::kTurns && !more && kk == 6 && lead) mbar_arrive(&bars[C::bTurnY]);
+            mma_ts_if(lead, tmem + C::cDV, tmem + buf * 128 + packed_col<C::kCols>(kk), ddo + ((kk * 2048) >> 4), idV,
                       (t > 0 || kk > 0) ? 1u : 0u);
           }
           tc_commit_if(lead, &bars[C::bDOEmpty + rd.st]);
+          if (t + 1 == total) tc_commit_if(lead, &bars[C::bDvFull]);
           rd.next();
+          buf = (buf + 1) % C::kS;
           if (more) {
-            issue_s(true);  // dV has read P: MMAs run in issue order
-            if (t + 2 == total) tc_commit_if(lead, &bars[C::bKEmpty]);
-          } else {
-            tc_commit_if(lead, &bars[C::bDvFull]);
+            if (!C::kTurns) wait(C::bQFull + rq.st, rq.ph);
+            issue_s(true);  // dV has read P: MMAs of one warp run in issue order
           }
         }
       }
       tc_commit_if(elect_one(), &bars[C::bFinalX]);
       mbar_drain(&bars[C::bFinalX], 0, g.limit_ns);
-    } else if (warp == 9) {
+    } else if (role == 1) {
       // ----------------------------------------------- Y: dP^T and dK
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idK = idesc_bf16(128, D, 0, 1);
@@ -767,19 +815,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<C::kQ> rq;
       Ring<C::kDO> rd;
       uint32_t v_ph = 0, ds_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0;
-      auto do_landed = [&](bool fix) {
-        wait(C::bDOFull + rd.st, rd.ph);
-        if (fix) {
-          if (lead) mbar_arrive(&bars[C::bTailDO]);
-          wait(C::bFixedDO, fix_ph);
-          fix_ph ^= 1;
-        }
-      };
       auto issue_dp = [&](bool last) {
         const uint64_t ddo = ddo0 + ((rd.st * C::kBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          if (kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnX]);
+          if (C::kTurns && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnX]);
           mma_ss_if(lead, tmem + C::cDP, dv + C::kmajor(kk), ddo + C::kmajor(kk), idS, kk > 0);
         }
         tc_commit_if(lead, &bars[C::bDpFull]);
@@ -793,30 +833,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ragged = it.n * kPackedTile > it.seq_len;
         wait(C::bVFull, v_ph);
         v_ph ^= 1;
-        do_landed(ragged && per == 1);
+        wait(C::bDOFull + rd.st, rd.ph);
         tc_fence_after();
-        issue_dp(total == 1);  // hands X its first turn: dV reads a dO tile whose tail is cleared
-        int left = per - 1;
+        issue_dp(total == 1);
+        int left = per;
         for (int t = 0; t < total; ++t) {
           const bool more = t + 1 < total;
-          if (more) {
-            left = left == 0 ? per - 1 : left - 1;
-            do_landed(ragged && left == 0);
-          }
+          if (more) wait(C::bDOFull + rd.st, rd.ph);
           wait(C::bQFull + rq.st, rq.ph);
-          wait(C::bDsFull, ds_ph);
-          ds_ph ^= 1;
+          if (ragged && left == 1) {
+            if (lead) mbar_arrive(&bars[C::bTailQ]);
+            wait(C::bFixedQ, fix_ph);
+            fix_ph ^= 1;
+          }
+          left = left == 1 ? per : left - 1;
           if (t == 0) {
             wait(C::bOEmpty, o_ph);
             o_ph ^= 1;
           }
-          wait(C::bTurnY, turn_ph);
-          turn_ph ^= 1;
+          if (C::kTurns) {
+            wait(C::bTurnY, turn_ph);
+            turn_ph ^= 1;
+          }
+          wait(C::bDsFull, ds_ph);
+          ds_ph ^= 1;
           tc_fence_after();
           const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts_if(lead, tmem + C::cDK, tmem + C::cDP + packed_col(kk), dq + ((kk * 2048) >> 4), idK,
+            mma_ts_if(lead, tmem + C::cDK, tmem + C::cDP + packed_col<C::kCols>(kk), dq + ((kk * 2048) >> 4), idK,
                       (t > 0 || kk > 0) ? 1u : 0u);
           tc_commit_if(lead, &bars[C::bQEmpty + rq.st]);
           rq.next();
@@ -828,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_commit_if(elect_one(), &bars[C::bFinalY]);
       mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
-    } else if (warp == 11) {
+    } else if (role == 3) {
       uint32_t loads = 0, ph = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
@@ -838,25 +883,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           loads += per;
           if (!ragged) continue;
           const int first = it.seq_len - (it.n - 1) * kPackedTile;
-          wait(C::bTailQ, ph);
-          if (!warp_aborted(g)) clear_rows<D>(smem + C::oQ + (loads - 1) % C::kQ * C::kBytes, first, lane);
-          if (lane == 0) mbar_arrive(&bars[C::bFixedQ]);
           wait(C::bTailDO, ph);
           if (!warp_aborted(g)) clear_rows<D>(smem + C::oDO + (loads - 1) % C::kDO * C::kBytes, first, lane);
           if (lane == 0) mbar_arrive(&bars[C::bFixedDO]);
+          wait(C::bTailQ, ph);
+          if (!warp_aborted(g)) clear_rows<D>(smem + C::oQ + (loads - 1) % C::kQ * C::kBytes, first, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixedQ]);
           ph ^= 1;
         }
       }
     }
   } else {
     // -------------------------------------------------------- P and dS
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int sub = warp & 3, half = warp >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
+    const int sub = warp & 3, c0 = (warp >> 2) * C::kCols;  // its columns of S^T and dP^T
     const int L = sub * 32 + lane;  // KV row
-    const uint32_t tS = tmem + ((uint32_t)(sub * 32) << 16) + 64 * half, tP = tS + C::cDP;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + c0, tP = tl + C::cDP;
     const uint64_t sc2 = dup2(p.scale_log2);
     Ring<C::kSt> rs;
-    uint32_t s_ph = 0, dp_ph = 0;
+    uint32_t s_ph = 0, dp_ph = 0, buf = 0;
     for (int i = i_begin; i < i_end; ++i) {
       const PackedDkvItem it = load_item(p.dkv_items + i);
       const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
@@ -865,21 +910,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a causal KV tile's first Q tile of each head is on the diagonal
         const bool diagonal = p.causal && k == 0;
         k = k + 1 == per ? 0 : k + 1;
-        const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(smem + C::oSTAT + rs.st * 1024 + half * 256);
+        // those inside the sequence: fewer in the head's last tile only
+        const int cols = k == 0 ? it.seq_len - (it.n - 1) * kPackedTile - c0 : C::kCols;
+        const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(smem + C::oSTAT + rs.st * 1024 + c0 * 4);
         const ulonglong2 *nd = nl + 32;
         mbar_wait(&bars[C::bStFull + rs.st], rs.ph, g);
-        mbar_wait(&bars[C::bSFull], s_ph, g);
-        s_ph ^= 1;
+        mbar_wait(&bars[C::bSFull + buf], s_ph, g);
+        const uint32_t tS = tl + buf * 128, p_bar = C::bPFull + buf;
+        buf = (buf + 1) % C::kS;
+        s_ph ^= buf == 0;
         __syncwarp();
         tc_fence_after();
-        uint32_t x[2][32];
+        uint32_t x[C::kCols / 32][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
+        for (int c = 0; c < C::kCols / 32; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) reg_order32(x[c]);
+        for (int c = 0; c < C::kCols / 32; ++c) reg_order32(x[c]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < C::kCols / 32; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 l4 = nl[8 * c + (e >> 2)];
@@ -893,13 +942,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         if (diagonal) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < C::kCols / 32; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (64 * half + 32 * c + e < L) x[c][e] = 0u;
+              if (c0 + 32 * c + e < L) x[c][e] = 0u;
+        }
+        if (cols < C::kCols) {  // replaced, as dS below: what Q and dO hold there may not be finite
+#pragma unroll
+          for (int c = 0; c < C::kCols / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= cols) x[c][e] = 0u;
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < C::kCols / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
@@ -909,20 +965,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[C::bPFull]);
+        if (lane == 0) mbar_arrive(&bars[p_bar]);
 
         mbar_wait(&bars[C::bDpFull], dp_ph, g);
         dp_ph ^= 1;
         __syncwarp();
         tc_fence_after();
-        uint32_t y[2][32];
+        uint32_t y[C::kCols / 32][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tP + 32 * c, y[c]);
+        for (int c = 0; c < C::kCols / 32; ++c) tmem_ld32_nowait(tP + 32 * c, y[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) reg_order32(y[c]);
+        for (int c = 0; c < C::kCols / 32; ++c) reg_order32(y[c]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < C::kCols / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -932,6 +988,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             unpack2(mul2(pack2(x[c][e + 2], x[c][e + 3]), add2(pack2(y[c][e + 2], y[c][e + 3]), d4.y)), u, v);
             pk[e >> 1] = pack_bf16(a, b);
             pk[(e >> 1) + 1] = pack_bf16(u, v);
+          }
+          if (cols < C::kCols) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              if (32 * c + e >= cols) pk[e >> 1] = 0u;
+              else if (32 * c + e + 1 >= cols) pk[e >> 1] &= 0xffffu;
+            }
           }
           tmem_st16(tP + 16 * c, pk);
         }
@@ -948,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (role == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -960,18 +1023,18 @@ constexpr int smem_bytes() {
 }
 
 template <class K>
-cudaError_t prepare_kernel(K kernel, int smem) {
+cudaError_t prepare_kernel(K kernel, int smem, int regs) {
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+  if (fa.numRegs != regs) return cudaErrorInvalidConfiguration;  // the register split counts on it
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 template <int D>
 cudaError_t prepare_t() {
-  cudaError_t e = prepare_kernel(dash_packed_dq_kernel<D>, smem_bytes<DqCfg<D>>());
-  return e == cudaSuccess ? prepare_kernel(dash_packed_dkv_kernel<D>, smem_bytes<DkvCfg<D>>()) : e;
+  cudaError_t e = prepare_kernel(dash_packed_dq_kernel<D>, smem_bytes<DqCfg<D>>(), kRegsLaunch);
+  return e == cudaSuccess ? prepare_kernel(dash_packed_dkv_kernel<D>, smem_bytes<DkvCfg<D>>(), DkvCfg<D>::kRegsLaunch) : e;
 }
 
 template <int D>
@@ -980,7 +1043,7 @@ cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorM
   dash_packed_dq_kernel<D><<<dq_ctas, kThreads, smem_bytes<DqCfg<D>>(), stream>>>(q, k, v, dout, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dash_packed_dkv_kernel<D><<<dkv_ctas, kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
+  dash_packed_dkv_kernel<D><<<dkv_ctas, DkvCfg<D>::kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
   return cudaGetLastError();
 }
 

@@ -316,13 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < n) wait(bKvFull0 + rk.st, rk.ph);
           const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
           if (j < mine) {
-            // P stands in tensor memory, O is at its scale and the last item's O has been read
-            wait(bPFull + s, p_ph);
+            // the last wait: P stands in tensor memory and O is at its scale
             if (j == 0) {
               wait(bOEmpty + s, o_ph);
               o_ph ^= 1;
             }
             take_turn();
+            wait(bPFull + s, p_ph);
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
