@@ -565,7 +565,9 @@ struct DkvCfg : Tile<D> {
   // score run before dV has read this P.
   static constexpr int kS = D == 128 ? 1 : 2;
   // With one buffer, S -> P -> dV -> S is the chain that sets the pace, and X
-  // and Y take turns so that each pair of products runs in one piece.
+  // and Y take turns so that each pair of products runs in one piece.  Passing
+  // the turn is an arrival on the barrier that counts P (for X) or dS (for Y):
+  // one wait answers for both.
   static constexpr bool kTurns = kS == 1;
   static constexpr uint32_t oK = 0, oV = Tile<D>::kBytes, oQ = 2 * Tile<D>::kBytes;
   static constexpr uint32_t oDO = oQ + kQ * Tile<D>::kBytes;
@@ -573,7 +575,7 @@ struct DkvCfg : Tile<D> {
   static constexpr uint32_t oBAR = oSTAT + kSt * 1024;
   enum {
     bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bPFull = bSFull + kS, bDpFull = bPFull + kS, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
-    bTailDO, bFixedDO, bTurnX, bTurnY, bFinalX, bFinalY,
+    bTailDO, bFixedDO, bFinalX, bFinalY,
     bQFull, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kDO, bStFull = bDOEmpty + kDO,
     bStEmpty = bStFull + kSt, kBars = bStEmpty + kSt
   };
@@ -606,9 +608,10 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::kBars; ++b) {
-      const bool soft = (b >= C::bPFull && b < C::bDpFull) || b == C::bDsFull || b >= C::bStEmpty;
+      const bool turn = (b >= C::bPFull && b < C::bDpFull) || b == C::bDsFull;
+      const bool soft = turn || b >= C::bStEmpty;
       const bool both = b >= C::bDOEmpty && b < C::bDOEmpty + C::kDO;  // X's dV and Y's dP have read it
-      mbar_init(&bars[b], soft ? C::kSoft : b == C::bOEmpty ? 4 : both ? 2 : 1);
+      mbar_init(&bars[b], soft ? C::kSoft + (turn && C::kTurns ? 1 : 0) : b == C::bOEmpty ? 4 : both ? 2 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), C::kPanel, 1024);
       Ring<C::kQ> rq;
       Ring<C::kDO> rd;
-      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0, sbuf = 0, buf = 0;
+      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0, sbuf = 0, buf = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
         const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
@@ -751,7 +754,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
           const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            if (C::kTurns && pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnY]);
+            if (C::kTurns && pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bDsFull]);
             mma_ss_if(lead, tmem + sbuf * 128, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
           }
           tc_commit_if(lead, &bars[C::bSFull + sbuf]);
@@ -778,18 +781,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
             wait(C::bOEmpty, o_ph);
             o_ph ^= 1;
           }
-          if (C::kTurns) {
-            if (more) wait(C::bQFull + rq.st, rq.ph);
-            wait(C::bTurnX, turn_ph);
-            turn_ph ^= 1;
-          }
+          if (C::kTurns && more) wait(C::bQFull + rq.st, rq.ph);
           wait(C::bPFull + buf, p_ph);
           p_ph ^= (int)buf == C::kS - 1;  // the buffers' parity changes after the last one
           tc_fence_after();
           const uint64_t ddo = ddo0 + ((rd.st * C::kBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            if (C::kTurns && !more && kk == 6 && lead) mbar_arrive(&bars[C::bTurnY]);
+            if (C::kTurns && !more && kk == 6 && lead) mbar_arrive(&bars[C::bDsFull]);
             mma_ts_if(lead, tmem + C::cDV, tmem + buf * 128 + packed_col<C::kCols>(kk), ddo + ((kk * 2048) >> 4), idV,
                       (t > 0 || kk > 0) ? 1u : 0u);
           }
@@ -814,12 +813,12 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       const uint64_t dq0 = sw128_desc(smem_u32(smem + C::oQ), C::kPanel, 1024);
       Ring<C::kQ> rq;
       Ring<C::kDO> rd;
-      uint32_t v_ph = 0, ds_ph = 0, o_ph = 1, turn_ph = 0, fix_ph = 0;
+      uint32_t v_ph = 0, ds_ph = 0, o_ph = 1, fix_ph = 0;
       auto issue_dp = [&](bool last) {
         const uint64_t ddo = ddo0 + ((rd.st * C::kBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          if (C::kTurns && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bTurnX]);
+          if (C::kTurns && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bPFull]);
           mma_ss_if(lead, tmem + C::cDP, dv + C::kmajor(kk), ddo + C::kmajor(kk), idS, kk > 0);
         }
         tc_commit_if(lead, &bars[C::bDpFull]);
@@ -850,10 +849,6 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
           if (t == 0) {
             wait(C::bOEmpty, o_ph);
             o_ph ^= 1;
-          }
-          if (C::kTurns) {
-            wait(C::bTurnY, turn_ph);
-            turn_ph ^= 1;
           }
           wait(C::bDsFull, ds_ph);
           ds_ph ^= 1;

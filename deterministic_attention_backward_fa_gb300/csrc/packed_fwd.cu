@@ -54,7 +54,7 @@ struct Cfg {
   static constexpr uint32_t oQ = 0;                 // two Q tiles
   static constexpr uint32_t oKV = 2 * kTile;
   static constexpr uint32_t oBAR = oKV + kStages * kTile;
-  static constexpr int kNumBars = 20 + 2 * kStages;
+  static constexpr int kNumBars = 18 + 2 * kStages;
   static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
   static constexpr uint32_t oSTAT = oMISC + 16;     // {maximum, sum} of each tile's rows
   static constexpr uint32_t kSmemBytes = oSTAT + 2 * 128 * 8;
@@ -62,7 +62,7 @@ struct Cfg {
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory of one CTA");
 
-enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bPFull = 12, bTurn = 14, bLFull = 16, bOEmpty = 18, bKvFull0 = 20 };
+enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bPFull = 12, bLFull = 14, bOEmpty = 16, bKvFull0 = 18 };
 
 __device__ __forceinline__ PackedFwdItem load_item(const PackedFwdItem *p) {
   PackedFwdItem it;
@@ -131,12 +131,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[bQFull + s], 1);
       mbar_init(&bars[bQEmpty + s], 1);
       mbar_init(&bars[bSFull + s], 1);
-      mbar_init(&bars[bPFull + s], 4);
+      mbar_init(&bars[bPFull + s], 5);  // four softmax warps and the turn
       mbar_init(&bars[bLFull + s], 4);
       mbar_init(&bars[bOEmpty + s], 4);
       mbar_init(&bars[bOFull + s], 1);
       mbar_init(&bars[bFinal + s], 1);
-      mbar_init(&bars[bTurn + s], 1);
     }
     mbar_init(&bars[bVFixed], 1);
     mbar_init(&bars[bVTail], 1);
@@ -272,20 +271,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](int bar, uint32_t ph) {
         if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
       };
-      uint32_t turn_ph = s ? 0 : 1;     // tile 0's first turn is free
-      auto take_turn = [&] {
-        wait(bTurn + s, turn_ph);
-        turn_ph ^= 1;
-      };
-      auto pass_turn = [&] {
-        if (lead) mbar_arrive(&bars[bTurn + (s ^ 1)]);
+      // Passing the turn is an arrival on the barrier that also counts the other
+      // tile's P, so that one wait answers for both.
+      auto give_turn = [&](int to) {
+        if (lead) mbar_arrive(&bars[bPFull + to]);
       };
       auto issue_s = [&](int stage, bool pass) {
         const uint64_t dk = dk0 + ((stage * C::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
-          if (pass && kk == D / 16 - 2) pass_turn();  // the other warp wakes up under the last MMAs
+          if (pass && kk == D / 16 - 2) give_turn(s ^ 1);  // the other warp wakes up under the last MMAs
           mma_ss_if(lead, tS, dq + off, dk + off, idS, kk > 0);
         }
         tc_commit_if(lead, &bars[bSFull + s]);
@@ -293,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = i_begin; i < i_end; ++i) {
         const PackedFwdItem it = load_item(p.items + i);
         const int n = max(it.nkv[0], it.nkv[1]), mine = s ? it.nkv[1] : it.nkv[0];
+        const int both = min(it.nkv[0], it.nkv[1]);  // KV tiles with a turn: those of both tiles
         const bool fix = n * kPackedTile > it.kv_len;
         wait(bKvFull0 + rk.st, rk.ph);
         if (mine > 0) {  // S of the first KV tile
@@ -316,12 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < n) wait(bKvFull0 + rk.st, rk.ph);
           const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
           if (j < mine) {
-            // the last wait: P stands in tensor memory and O is at its scale
             if (j == 0) {
               wait(bOEmpty + s, o_ph);
               o_ph ^= 1;
             }
-            take_turn();
+            // P stands in tensor memory, O is at its scale, and the turn has come: tile 1's behind tile 0's, tile 0's
+            // behind tile 1's of the KV tile before
+            if (j >= both || (s == 0 && j == 0)) give_turn(s);
+            const bool pass = j < both && (s == 0 || j + 1 < both);
             wait(bPFull + s, p_ph);
             tc_fence_after();
 #pragma unroll
@@ -329,15 +328,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
             p_ph ^= 1;
             if (j + 1 < mine) {
-              issue_s(rk.st, true);  // MMAs run in issue order: PV has read P before S overwrites it
+              issue_s(rk.st, pass);  // MMAs run in issue order: PV has read P before S overwrites it
               if (j + 2 == mine) tc_commit_if(lead, &bars[bQEmpty + s]);
             } else {
-              pass_turn();
+              if (pass) give_turn(s ^ 1);
               tc_commit_if(lead, &bars[bOFull + s]);
             }
-          } else {
-            take_turn();
-            pass_turn();
           }
           // each tile is free when both warps' MMAs have read it (a warp that has none arrives at once)
           tc_commit_if(lead, &kvEmpty[rv.st]);
