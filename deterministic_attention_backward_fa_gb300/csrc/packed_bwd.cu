@@ -15,12 +15,13 @@
 // training batch of 16384 tokens in 737 us and long documents at D = 64 in
 // 2151 us; this one takes DQKV_PACKED and DQKV_D64.
 //
-// Warps of both kernels: 0-7 turn scores into P and dS (a thread owns a row of
-// the accumulator and half of its columns), 8 and 9 issue the MMAs (X and Y),
-// 10 loads, 11 clears rows past a sequence's end that take part in a sum, 12-15
-// write the results of the last item (and, for dQ, make the next item's delta).
-// Two MMA warps, because a wait answers about 100 clocks after the MMAs in
-// front of it, which the other warp's MMAs cover.
+// Warps of both kernels: the first turn scores into P and dS (eight for dQ,
+// sixteen for dK and dV; a thread owns columns of a row of the accumulator),
+// then X, Y and Z, which issue the MMAs, one that loads, and four that write the
+// last item's results, clear rows past a sequence's end that a product sums over
+// and, for dQ, make the next item's delta.  Several warps issue, because a wait
+// answers about 100 clocks after the MMAs in front of it, which another warp's
+// MMAs cover.
 //
 // P and dS are rounded to bf16 as MMA operands, once each; everything else is
 // held in 32 bits until the gradients' own rounding.
@@ -147,23 +148,25 @@ struct Tile {
 };
 
 // ------------------------------------------------------------------- dQ
-// Per KV tile j:   X: dP(j+1) = dO V^T     Y: dQ += dS(j) K, S(j+2) = Q K^T
-// once the softmax warps have dP(j) in registers (X) and dS(j) in tensor memory
-// (Y; S(j+2) takes the place of dS(j), and MMAs of one warp run in issue order).
+// Per KV tile j:   X: dP(j+1) = dO V^T     Y: dQ += dS(j) K     Z: S(j+2) = Q K^T
+// once the softmax warps have dP(j) in registers (X), dS(j) is in tensor memory
+// (Y) and dQ(j) has read dS(j), whose place S(j+2) takes (Z).
 // Tensor memory: S and dS in two buffers at 0 and 128, dP at 256, dQ at 384.  V rows past the sequence's end reach dP only, whose
 // columns there are replaced; K rows there are summed over and are cleared.
 template <int D>
 struct DqCfg : Tile<D> {
-  static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;  // stages
-  static constexpr uint32_t oQ = 0, oDO = Tile<D>::kBytes, oK = 2 * Tile<D>::kBytes;
+  static constexpr int kQ = D == 128 ? 1 : 2, kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;  // stages
+  static constexpr uint32_t oQ = 0, oDO = kQ * Tile<D>::kBytes, oK = 2 * kQ * Tile<D>::kBytes;
   static constexpr uint32_t oV = oK + kK * Tile<D>::kBytes;
   static constexpr uint32_t oSTAT = oV + kV * Tile<D>::kBytes;  // [2][128] {-lse2, -delta}
   static constexpr uint32_t oBAR = oSTAT + 2 * 128 * 8;
   enum {
     // S and dS have a barrier per buffer: a warp may be a tile ahead of another.  So have the tails: S, which
     // asks for them, is up to two items ahead of dQ, which waits for them.
-    bQFull, bQEmpty, bSFull, bDpFull = bSFull + 2, bRead, bDsFull, bOFull = bDsFull + 2, bOEmpty, bTail, bFixed = bTail + 2, bFinalX = bFixed + 2, bFinalY, bStat,
-    bKFull = bStat + 2, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV, kBars = bVEmpty + kV
+    bSFull, bSEmpty = bSFull + 2, bDpFull = bSEmpty + 2, bRead, bDsFull, bOFull = bDsFull + 2, bOEmpty, bTail, bFixed = bTail + 2, bFinalX = bFixed + 2, bFinalY, bFinalZ, bStat,
+    bKFull = bStat + 2, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV,
+    bQFull = bVEmpty + kV, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kQ,
+    kBars = bDOEmpty + kQ
   };
   static constexpr uint32_t oMISC = oBAR + kBars * 8;
   static constexpr uint32_t kSmem = oMISC + 16;
@@ -191,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < C::kBars; ++b)
       mbar_init(&bars[b], b >= C::bRead && b < C::bDsFull + 2                            ? 8
                           : b == C::bOEmpty || b == C::bStat || b == C::bStat + 1 ? 4
-                          : b == C::bQEmpty                                       ? 2  // X's last dP, Y's last S
                                                                                   : 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const int L = sub * 32 + lane;
     const uint32_t tq = tmem + ((uint32_t)(sub * 32) << 16) + C::cDQ;
-    uint32_t ph = 0;
+    uint32_t ph = 0, loads = 0, tail_ph = 0, tail = 0;
     if (i_begin < i_end) make_stats(i_begin);
     if (i_begin + 1 < i_end) ask(i_begin + 1);
     for (int i = i_begin; i < i_end; ++i) {
@@ -287,6 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i + 1 < i_end) make_stats(i + 1);
       if (i + 2 < i_end) ask(i + 2);
       const PackedDqItem it = load_item(p.dq_items + i);
+      loads += it.nkv;
+      if (it.nkv * kPackedTile > it.kv_len) {  // K rows past the end in the item's last tile
+        if (sub == 0) {
+          mbar_wait(&bars[C::bTail + tail], tail_ph, g);
+          if (!warp_aborted(g))
+            clear_rows<D>(smem + C::oK + (loads - 1) % C::kK * C::kBytes, it.kv_len - (it.nkv - 1) * kPackedTile, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixed + tail]);
+        }
+        tail_ph ^= tail;
+        tail ^= 1;
+      }
       bool ok = mbar_wait(&bars[C::bOFull], ph, g);
       ph ^= 1;
       __syncwarp();
@@ -313,57 +326,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tmDO);
       Ring<C::kK> rk;
       Ring<C::kV> rv;
-      uint32_t q_ph = 1, nq = 0, nk = 0, nv = 0;
+      Ring<C::kQ> rq;
+      uint32_t nq = 0, nk = 0, nv = 0;
       bool live = true;
+      auto load = [&](int full, int empty, uint32_t ph, uint32_t at, const CUtensorMap *m, int row, int head) {
+        live = live && mbar_wait(&bars[empty], ph ^ 1, g);
+        if (!live) return 0u;
+        mbar_arrive_expect_tx(&bars[full], C::kBytes);
+        C::load(smem + at, m, &bars[full], row, head);
+        return 1u;
+      };
+      uint32_t ndo = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDqItem it = load_item(p.dq_items + i);
         const int kvh = it.head / p.group;
-        live = live && mbar_wait(&bars[C::bQEmpty], q_ph, g);
-        q_ph ^= 1;
-        if (live) {
-          mbar_arrive_expect_tx(&bars[C::bQFull], 2 * C::kBytes);
-          C::load(smem + C::oQ, &tmQ, &bars[C::bQFull], it.row0, it.head);
-          C::load(smem + C::oDO, &tmDO, &bars[C::bQFull], it.row0, it.head);
-          ++nq;
-        }
+        nq += load(C::bQFull + rq.st, C::bQEmpty + rq.st, rq.ph, C::oQ + rq.st * C::kBytes, &tmQ, it.row0, it.head);
         for (int j = 0; j < it.nkv; ++j) {
-          live = live && mbar_wait(&bars[C::bKEmpty + rk.st], rk.ph ^ 1, g);
-          if (live) {
-            mbar_arrive_expect_tx(&bars[C::bKFull + rk.st], C::kBytes);
-            C::load(smem + C::oK + rk.st * C::kBytes, &tmK, &bars[C::bKFull + rk.st], it.kv_row0 + j * kPackedTile, kvh);
-            ++nk;
-          }
+          const int row = it.kv_row0 + j * kPackedTile;
+          nk += load(C::bKFull + rk.st, C::bKEmpty + rk.st, rk.ph, C::oK + rk.st * C::kBytes, &tmK, row, kvh);
           rk.next();
-          live = live && mbar_wait(&bars[C::bVEmpty + rv.st], rv.ph ^ 1, g);
-          if (live) {
-            mbar_arrive_expect_tx(&bars[C::bVFull + rv.st], C::kBytes);
-            C::load(smem + C::oV + rv.st * C::kBytes, &tmV, &bars[C::bVFull + rv.st], it.kv_row0 + j * kPackedTile, kvh);
-            ++nv;
-          }
+          if (j == 0)  // the last dP before needs dO longer than the last S needs Q
+            ndo += load(C::bDOFull + rq.st, C::bDOEmpty + rq.st, rq.ph, C::oDO + rq.st * C::kBytes, &tmDO, it.row0,
+                        it.head);
+          nv += load(C::bVFull + rv.st, C::bVEmpty + rv.st, rv.ph, C::oV + rv.st * C::kBytes, &tmV, row, kvh);
           rv.next();
         }
+        rq.next();
       }
       // copies still in flight land before the CTA exits
-      if (nq) mbar_drain(&bars[C::bQFull], (nq - 1) & 1, g.limit_ns);
-      for (uint32_t s = 0; s < C::kK; ++s) {
-        const uint32_t f = nk / C::kK + (s < nk % C::kK ? 1u : 0u);
-        if (f) mbar_drain(&bars[C::bKFull + s], (f - 1) & 1, g.limit_ns);
-      }
-      for (uint32_t s = 0; s < C::kV; ++s) {
-        const uint32_t f = nv / C::kV + (s < nv % C::kV ? 1u : 0u);
-        if (f) mbar_drain(&bars[C::bVFull + s], (f - 1) & 1, g.limit_ns);
-      }
+      auto drain = [&](int bar, uint32_t n, uint32_t stages) {
+        for (uint32_t s = 0; s < stages; ++s) {
+          const uint32_t f = n / stages + (s < n % stages ? 1u : 0u);
+          if (f) mbar_drain(&bars[bar + s], (f - 1) & 1, g.limit_ns);
+        }
+      };
+      drain(C::bQFull, nq, C::kQ);
+      drain(C::bDOFull, ndo, C::kQ);
+      drain(C::bKFull, nk, C::kK);
+      drain(C::bVFull, nv, C::kV);
     } else if (warp == 8) {
       // ------------------------------------------------------- X: dP
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-      const uint64_t ddo = sw128_desc(smem_u32(smem + C::oDO), 16, 1024);
+      const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), 16, 1024);
       const uint64_t dv0 = sw128_desc(smem_u32(smem + C::oV), 16, 1024);
       Ring<C::kV> rv;
-      uint32_t q_ph = 0, read_ph = 1;
+      Ring<C::kQ> rq;
+      uint32_t read_ph = 1;
       for (int i = i_begin; i < i_end; ++i) {
         const int nkv = p.dq_items[i].nkv;
-        wait(C::bQFull, q_ph);
-        q_ph ^= 1;
+        wait(C::bDOFull + rq.st, rq.ph);
+        const uint64_t ddo = ddo0 + ((rq.st * C::kBytes) >> 4);
         for (int j = 0; j < nkv; ++j) {
           wait(C::bVFull + rv.st, rv.ph);
           wait(C::bRead, read_ph);  // the dP before is in registers
@@ -377,58 +389,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit_if(lead, &bars[C::bVEmpty + rv.st]);
           rv.next();
         }
-        tc_commit_if(lead, &bars[C::bQEmpty]);
+        tc_commit_if(lead, &bars[C::bDOEmpty + rq.st]);
+        rq.next();
       }
       // every MMA has completed before tensor memory is released (at once if none was issued)
       tc_commit_if(elect_one(), &bars[C::bFinalX]);
       mbar_drain(&bars[C::bFinalX], 0, g.limit_ns);
     } else if (warp == 9) {
-      // ------------------------------------------------- Y: S and dQ
-      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      // ------------------------------------------------------- Y: dQ
       constexpr uint32_t idQ = idesc_bf16(128, D, 0, 1);
-      const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ), 16, 1024);
-      const uint64_t dks0 = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
       const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oK), C::kPanel, 1024);
-      Ring<C::kK> rs, rk;  // next K tile of S and of dQ
-      uint32_t q_ph = 0, ds_ph = 0, o_ph = 1, fix_ph = 0, fix = 0, tail = 0, sbuf = 0, buf = 0;
-      // S runs two tiles ahead of dQ, from one item into the next
-      int s_item = i_begin, s_j = 0, s_n = 0, s_len = 0;
-      auto next_s = [&] {
-        if (s_item >= i_end) return;
-        if (s_j == 0) {
-          s_n = p.dq_items[s_item].nkv;
-          s_len = p.dq_items[s_item].kv_len;
-          wait(C::bQFull, q_ph);
-          q_ph ^= 1;
-        }
-        wait(C::bKFull + rs.st, rs.ph);
-        const bool last = s_j + 1 == s_n;
-        // it has landed: the rows past the end may be cleared, while S reads them (their columns are replaced)
-        if (last && s_n * kPackedTile > s_len) {
-          if (lead) mbar_arrive(&bars[C::bTail + tail]);
-          tail ^= 1;
-        }
-        tc_fence_after();
-        const uint64_t dk = dks0 + ((rs.st * C::kBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss_if(lead, tmem + sbuf * 128, dq + C::kmajor(kk), dk + C::kmajor(kk), idS, kk > 0);
-        tc_commit_if(lead, &bars[C::bSFull + sbuf]);
-        if (last) tc_commit_if(lead, &bars[C::bQEmpty]);
-        sbuf ^= 1;
-        rs.next();
-        ++s_j;
-        if (last) {
-          s_j = 0;
-          ++s_item;
-        }
-      };
-      next_s();
-      next_s();
+      Ring<C::kK> rk;
+      uint32_t ds_ph = 0, o_ph = 1, fix_ph = 0, fix = 0, buf = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const int nkv = p.dq_items[i].nkv;
         const bool ragged = nkv * kPackedTile > p.dq_items[i].kv_len;
         for (int j = 0; j < nkv; ++j) {
+          wait(C::bKFull + rk.st, rk.ph);
           if (ragged && j + 1 == nkv) {
             wait(C::bFixed + fix, fix_ph);
             fix_ph ^= fix;
@@ -446,29 +423,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 8; ++kk)
             mma_ts_if(lead, tmem + C::cDQ, tmem + buf * 128 + packed_col<64>(kk), dk + ((kk * 2048) >> 4), idQ,
                       (j > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_if(lead, &bars[C::bSEmpty + buf]);
           tc_commit_if(lead, &bars[C::bKEmpty + rk.st]);
           if (j + 1 == nkv) tc_commit_if(lead, &bars[C::bOFull]);
           buf ^= 1;
           rk.next();
-          next_s();
         }
       }
       tc_commit_if(elect_one(), &bars[C::bFinalY]);
       mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
     } else if (warp == 11) {
-      uint32_t loads = 0, tail_ph = 0, tail = 0;
+      // ------------------------------------- Z: S, from one item into the next
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      const uint64_t dq0 = sw128_desc(smem_u32(smem + C::oQ), 16, 1024);
+      const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
+      Ring<C::kK> rk;
+      Ring<C::kQ> rq;
+      uint32_t e_ph = 1, tail = 0, buf = 0;
       for (int i = i_begin; i < i_end; ++i) {
-        const PackedDqItem it = load_item(p.dq_items + i);
-        loads += it.nkv;
-        if (it.nkv * kPackedTile > it.kv_len) {
-          wait(C::bTail + tail, tail_ph);
-          if (!warp_aborted(g))
-            clear_rows<D>(smem + C::oK + (loads - 1) % C::kK * C::kBytes, it.kv_len - (it.nkv - 1) * kPackedTile, lane);
-          if (lane == 0) mbar_arrive(&bars[C::bFixed + tail]);
-          tail_ph ^= tail;
-          tail ^= 1;
+        const int nkv = p.dq_items[i].nkv;
+        const bool ragged = nkv * kPackedTile > p.dq_items[i].kv_len;
+        wait(C::bQFull + rq.st, rq.ph);
+        const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
+        for (int j = 0; j < nkv; ++j) {
+          wait(C::bKFull + rk.st, rk.ph);
+          // it has landed: the rows past the end may be cleared, while S reads them (their columns are replaced)
+          if (ragged && j + 1 == nkv) {
+            if (lead) mbar_arrive(&bars[C::bTail + tail]);
+            tail ^= 1;
+          }
+          wait(C::bSEmpty + buf, e_ph);
+          e_ph ^= buf;
+          tc_fence_after();
+          const uint64_t dk = dk0 + ((rk.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_if(lead, tmem + buf * 128, dq + C::kmajor(kk), dk + C::kmajor(kk), idS, kk > 0);
+          tc_commit_if(lead, &bars[C::bSFull + buf]);
+          buf ^= 1;
+          rk.next();
         }
+        tc_commit_if(lead, &bars[C::bQEmpty + rq.st]);
+        rq.next();
       }
+      tc_commit_if(elect_one(), &bars[C::bFinalZ]);
+      mbar_drain(&bars[C::bFinalZ], 0, g.limit_ns);
     }
   } else {
     // ------------------------------------------------------------- dS
@@ -553,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------- dK and dV
 // The accumulators' lanes are KV rows.  Per Q tile i (of every head):
 //   X: dV += P^T(i) dO, S^T(i+1) = K Q^T     Y: dK += dS^T(i) Q, dP^T(i+1) = V dO^T
+// (with two S buffers a third warp, Z, issues S^T(i+2) once dV(i) has read P).
 // P^T and dS^T replace S^T and dP^T in tensor memory (S at 0, dP at 128, dV at
 // 256, dK at 256 + D; at D = 64 two S at 0 and 128 and the others behind).
 // Rows of dO (for dV) and of Q (for dK) past the sequence's end are summed over
@@ -574,8 +574,8 @@ struct DkvCfg : Tile<D> {
   static constexpr uint32_t oSTAT = oDO + kDO * Tile<D>::kBytes;  // [kSt][2][128]
   static constexpr uint32_t oBAR = oSTAT + kSt * 1024;
   enum {
-    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bPFull = bSFull + kS, bDpFull = bPFull + kS, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
-    bTailDO, bFixedDO, bFinalX, bFinalY,
+    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bSEmpty = bSFull + kS, bPFull = bSEmpty + kS, bDpFull = bPFull + kS, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
+    bTailDO, bFixedDO, bFinalX, bFinalY, bFinalZ,
     bQFull, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kDO, bStFull = bDOEmpty + kDO,
     bStEmpty = bStFull + kSt, kBars = bStEmpty + kSt
   };
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
   using C = DkvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = warp_id(), lane = threadIdx.x & 31;
-  const int role = warp - C::kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 clears, 4-7 write the results
+  const int role = warp - C::kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 Z, 4-7 write the results
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
@@ -632,9 +632,25 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOut));
     const int sub = warp & 3, L = sub * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
-    uint32_t ph = 0;
+    uint32_t ph = 0, tail_ph = 0;
+    int loads = 0;
     for (int i = i_begin; i < i_end; ++i) {
       const PackedDkvItem it = load_item(p.dkv_items + i);
+      const int per = p.causal ? it.n - it.kv : it.n;
+      if (it.n * kPackedTile > it.seq_len && sub == 0) {  // rows past the end in each head's last tiles
+        const int first = it.seq_len - (it.n - 1) * kPackedTile;
+        for (int h = 1; h <= p.group; ++h) {
+          const int at = loads + h * per - 1;
+          mbar_wait(&bars[C::bTailDO], tail_ph, g);
+          if (!warp_aborted(g)) clear_rows<D>(smem + C::oDO + at % C::kDO * C::kBytes, first, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixedDO]);
+          mbar_wait(&bars[C::bTailQ], tail_ph, g);
+          if (!warp_aborted(g)) clear_rows<D>(smem + C::oQ + at % C::kQ * C::kBytes, first, lane);
+          if (lane == 0) mbar_arrive(&bars[C::bFixedQ]);
+          tail_ph ^= 1;
+        }
+      }
+      loads += per * p.group;
       bool ok = mbar_wait(&bars[C::bDvFull], ph, g);
       ok &= mbar_wait(&bars[C::bDkFull], ph, g);
       ph ^= 1;
@@ -735,7 +751,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       drain(C::bDOFull, nt, C::kDO);
       drain(C::bStFull, nt, C::kSt);
     } else if (role == 0) {
-      // ------------------------------------------------ X: S^T and dV
+      // ------------------------------------------------ X: dV (and S^T)
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idV = idesc_bf16(128, D, 0, 1);
       const uint64_t dk = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
@@ -743,33 +759,32 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), C::kPanel, 1024);
       Ring<C::kQ> rq;
       Ring<C::kDO> rd;
-      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0, sbuf = 0, buf = 0;
+      uint32_t k_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0, buf = 0;
+      auto issue_s = [&](bool pass) {  // kTurns
+        tc_fence_after();
+        const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bDsFull]);
+          mma_ss_if(lead, tmem, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
+        }
+        tc_commit_if(lead, &bars[C::bSFull]);
+        rq.next();
+      };
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
         const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
         const bool ragged = it.n * kPackedTile > it.seq_len;
-        int left = per, issued = 0;  // Q tiles of the head from this one on; scores issued
-        auto issue_s = [&](bool pass) {
-          tc_fence_after();
-          const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            if (C::kTurns && pass && kk == D / 16 - 2 && lead) mbar_arrive(&bars[C::bDsFull]);
-            mma_ss_if(lead, tmem + sbuf * 128, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
-          }
-          tc_commit_if(lead, &bars[C::bSFull + sbuf]);
-          if (++issued == total) tc_commit_if(lead, &bars[C::bKEmpty]);
-          rq.next();
-          sbuf = (sbuf + 1) % C::kS;
-        };
-        wait(C::bKFull, k_ph);
-        k_ph ^= 1;
-        for (int t = 0; t < min(C::kS, total); ++t) {
+        int left = per;  // Q tiles of the head from this one on
+        if (C::kTurns) {
+          wait(C::bKFull, k_ph);
+          k_ph ^= 1;
           wait(C::bQFull + rq.st, rq.ph);
           issue_s(false);
+          if (total == 1) tc_commit_if(lead, &bars[C::bKEmpty]);
         }
         for (int t = 0; t < total; ++t) {
-          const bool more = t + C::kS < total;
+          const bool more = t + 1 < total;
           wait(C::bDOFull + rd.st, rd.ph);
           if (ragged && left == 1) {  // the head's last tile: its rows past the end are summed over
             if (lead) mbar_arrive(&bars[C::bTailDO]);
@@ -792,13 +807,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
             mma_ts_if(lead, tmem + C::cDV, tmem + buf * 128 + packed_col<C::kCols>(kk), ddo + ((kk * 2048) >> 4), idV,
                       (t > 0 || kk > 0) ? 1u : 0u);
           }
+          if (!C::kTurns) tc_commit_if(lead, &bars[C::bSEmpty + buf]);
           tc_commit_if(lead, &bars[C::bDOEmpty + rd.st]);
-          if (t + 1 == total) tc_commit_if(lead, &bars[C::bDvFull]);
+          if (!more) tc_commit_if(lead, &bars[C::bDvFull]);
           rd.next();
           buf = (buf + 1) % C::kS;
-          if (more) {
-            if (!C::kTurns) wait(C::bQFull + rq.st, rq.ph);
+          if (C::kTurns && more) {
             issue_s(true);  // dV has read P: MMAs of one warp run in issue order
+            if (t + 2 == total) tc_commit_if(lead, &bars[C::bKEmpty]);
           }
         }
       }
@@ -868,25 +884,35 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       }
       tc_commit_if(elect_one(), &bars[C::bFinalY]);
       mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
-    } else if (role == 3) {
-      uint32_t loads = 0, ph = 0;
+    } else if (role == 3 && !C::kTurns) {
+      // -------------------------------------------------------- Z: S^T
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      const uint64_t dk = sw128_desc(smem_u32(smem + C::oK), 16, 1024);
+      const uint64_t dq0 = sw128_desc(smem_u32(smem + C::oQ), 16, 1024);
+      Ring<C::kQ> rq;
+      uint32_t k_ph = 0, e_ph = 1, buf = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
-        const int per = p.causal ? it.n - it.kv : it.n;
-        const bool ragged = it.n * kPackedTile > it.seq_len;
-        for (int h = 0; h < p.group; ++h) {
-          loads += per;
-          if (!ragged) continue;
-          const int first = it.seq_len - (it.n - 1) * kPackedTile;
-          wait(C::bTailDO, ph);
-          if (!warp_aborted(g)) clear_rows<D>(smem + C::oDO + (loads - 1) % C::kDO * C::kBytes, first, lane);
-          if (lane == 0) mbar_arrive(&bars[C::bFixedDO]);
-          wait(C::bTailQ, ph);
-          if (!warp_aborted(g)) clear_rows<D>(smem + C::oQ + (loads - 1) % C::kQ * C::kBytes, first, lane);
-          if (lane == 0) mbar_arrive(&bars[C::bFixedQ]);
-          ph ^= 1;
+        const int total = (p.causal ? it.n - it.kv : it.n) * p.group;
+        wait(C::bKFull, k_ph);
+        k_ph ^= 1;
+        for (int t = 0; t < total; ++t) {
+          wait(C::bQFull + rq.st, rq.ph);
+          wait(C::bSEmpty + buf, e_ph);
+          e_ph ^= (int)buf == C::kS - 1;
+          tc_fence_after();
+          const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_if(lead, tmem + buf * 128, dk + C::kmajor(kk), dq + C::kmajor(kk), idS, kk > 0);
+          tc_commit_if(lead, &bars[C::bSFull + buf]);
+          rq.next();
+          buf = (buf + 1) % C::kS;
         }
+        tc_commit_if(lead, &bars[C::bKEmpty]);
       }
+      tc_commit_if(elect_one(), &bars[C::bFinalZ]);
+      mbar_drain(&bars[C::bFinalZ], 0, g.limit_ns);
     }
   } else {
     // -------------------------------------------------------- P and dS
