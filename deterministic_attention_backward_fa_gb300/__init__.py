@@ -737,10 +737,11 @@ def attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, scale: float | None =
 def attn_decode(q, k_pages, v_pages, page_table, lengths, scale: float | None = None, stream=None):
     """O [B, heads, D] (bf16) and LSE [B, heads] (fp32) of one new token per sequence over a paged cache."""
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("attn_decode takes q [B, heads, D], pages [pages, tokens, heads, D] and a table [B, pages]")
+    need = dash_decode_workspace(q.shape[0], q.shape[1], q.shape[2], k_pages.shape[1], page_table.shape[1])
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _cache(k_pages, v_pages)
-    need = dash_decode_workspace(q.shape[0], q.shape[1], q.shape[2], k_pages.shape[1], page_table.shape[1])
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     with _using(stream, o, lse, ws):
         dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale, ws, stream)

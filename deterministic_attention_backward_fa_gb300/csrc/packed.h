@@ -122,9 +122,12 @@ struct DecodeParams {
   int *status;
 };
 // Tokens a split covers, from the sequence's own length alone.
+// Long ones get longer splits (a split's partial result costs as much as eight
+// cached tokens to write and read) but up to 64 of them, so that one sequence
+// on few heads still spreads.
 __host__ __device__ inline int decode_chunk(int len) {
   int c = 256;
-  while ((long long)c * 128 < len) c *= 2;
+  while ((long long)c * 64 < len || (c < 1024 && c * 16 < len)) c *= 2;
   return c;
 }
 __host__ __device__ inline int decode_splits(int len) {
