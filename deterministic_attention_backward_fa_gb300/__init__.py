@@ -15,6 +15,7 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -422,11 +423,8 @@ def dash_die_map(max_sm: int = 1023, stream=None):
 
 
 # ---- packed, grouped-head attention and the paged cache
-def _on(device, stream, tensors):
-    """Checks that the tensors lie on ``device`` and returns the stream to run on (that device's current one)."""
-    for name, t in tensors:
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _stream_on(device, stream):
+    """The raw stream to run on: the given one, or ``device``'s current one."""
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream
     if stream.device != device:
@@ -442,19 +440,17 @@ def _device(dev):
     return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _rows(name, t, heads=None, dim=None, rows=None):
-    """A [rows, heads, D] bf16 CUDA tensor whose last dimension is contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim) or \
-            (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {heads or 'heads'}, {dim or 'D'}], "
-                         f"not {list(t.shape)}")
-    if t.stride(2) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t
+def _rows(name, t, heads, dim, rows, device):
+    """Checks a [rows, heads, D] bf16 tensor whose last dimension is contiguous (None: any extent)."""
+    shape = t.shape
+    if len(shape) != 3 or t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(2) != 1 or \
+            (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim) or \
+            (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be a CUDA torch.bfloat16 tensor [{'rows' if rows is None else rows}, "
+                         f"{heads or 'heads'}, {dim or 'D'}], contiguous in its last dimension, not {t.dtype} "
+                         f"{list(shape)} on {t.device} with strides {t.stride()}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _plain(name, t, dtype, shape, device):
@@ -467,6 +463,9 @@ def _plain(name, t, dtype, shape, device):
 
 
 def _strides(*tensors):
+    """Row and head strides, or None when every tensor is contiguous."""
+    if all([t.is_contiguous() for t in tensors]):
+        return None
     v = [x for t in tensors for x in t.stride()[:2]]
     return (ctypes.c_int64 * len(v))(*v)
 
@@ -535,43 +534,71 @@ def dash_build_packed_items(lengths, heads: int, kv_heads: int, causal: bool, ke
     return items[:n.value], off
 
 
-def dash_attn_packed_fwd(plan: PackedPlan, q, k, v, o, lse, scale: float, stream=None):
-    rows, dev = q.shape[0], plan.device
-    for name, t, h in (("q", q, plan.heads), ("k", k, plan.kv_heads), ("v", v, plan.kv_heads), ("o", o, plan.heads)):
-        _rows(name, t, h, plan.head_dim, rows)
-    _plain("lse", lse, torch.float32, (plan.heads, rows), dev)
-    st = _on(dev, stream, (("q", q), ("k", k), ("v", v), ("o", o)))
+def _packed_fwd(plan, q, k, v, o, lse, scale, stream):
+    dev = plan.device
     with _device(dev):
         _check(lib().dash_attn_packed_fwd(plan._handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                          lse.data_ptr(), rows, _strides(q, k, v, o), float(scale), st))
+                                          lse.data_ptr(), q.shape[0], _strides(q, k, v, o), scale,
+                                          _stream_on(dev, stream)))
 
 
-def dash_attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, stream=None):
-    rows, dev, hq, hk = q.shape[0], plan.device, plan.heads, plan.kv_heads
-    named = (("q", q, hq), ("k", k, hk), ("v", v, hk), ("o", o, hq), ("do", do, hq), ("dq", dq, hq), ("dk", dk, hk),
-             ("dv", dv, hk))
-    for name, t, h in named:
-        _rows(name, t, h, plan.head_dim, rows)
-    _plain("lse", lse, torch.float32, (hq, rows), dev)
-    _plain("workspace", workspace, torch.uint8, (None,), dev)
-    st = _on(dev, stream, [(n, t) for n, t, _ in named])
+def _packed_inputs(plan, q, k, v):
+    dev, dim = plan.device, plan.head_dim
+    _rows("q", q, plan.heads, dim, None, dev)
+    _rows("k", k, plan.kv_heads, dim, q.shape[0], dev)
+    _rows("v", v, plan.kv_heads, dim, q.shape[0], dev)
+
+
+def dash_attn_packed_fwd(plan: PackedPlan, q, k, v, o, lse, scale: float, stream=None):
+    _packed_inputs(plan, q, k, v)
+    _rows("o", o, plan.heads, plan.head_dim, q.shape[0], plan.device)
+    _plain("lse", lse, torch.float32, (plan.heads, q.shape[0]), plan.device)
+    _packed_fwd(plan, q, k, v, o, lse, float(scale), stream)
+
+
+def _packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, scale, workspace, stream):
+    dev = plan.device
     with _device(dev):
         _check(lib().dash_attn_packed_bwd(plan._handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                           do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                          rows, _strides(q, k, v, o, do, dq, dk, dv), float(scale),
-                                          workspace.data_ptr(), workspace.numel(), st))
+                                          q.shape[0], _strides(q, k, v, o, do, dq, dk, dv), scale,
+                                          workspace.data_ptr(), workspace.numel(), _stream_on(dev, stream)))
 
 
-def _cache(k_pages, v_pages):
+def _packed_saved(plan, q, o, do, lse):
+    dev, rows = plan.device, q.shape[0]
+    _rows("o", o, plan.heads, plan.head_dim, rows, dev)
+    _rows("do", do, plan.heads, plan.head_dim, rows, dev)
+    _plain("lse", lse, torch.float32, (plan.heads, rows), dev)
+
+
+def dash_attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, stream=None):
+    dev, rows = plan.device, q.shape[0]
+    _packed_inputs(plan, q, k, v)
+    _packed_saved(plan, q, o, do, lse)
+    _rows("dq", dq, plan.heads, plan.head_dim, rows, dev)
+    _rows("dk", dk, plan.kv_heads, plan.head_dim, rows, dev)
+    _rows("dv", dv, plan.kv_heads, plan.head_dim, rows, dev)
+    _plain("workspace", workspace, torch.uint8, (None,), dev)
+    _packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, float(scale), workspace, stream)
+
+
+def _cache(k_pages, v_pages, device):
+    shape = k_pages.shape
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+        if not t.is_cuda or t.dtype != torch.bfloat16 or len(t.shape) != 4 or t.stride(3) != 1:
             raise ValueError(f"{name} must be a CUDA bfloat16 tensor [pages, tokens, heads, D], contiguous in D")
-    if k_pages.shape != v_pages.shape:
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
-    return k_pages.shape
+    return shape
 
 
 def _cache_strides(a, b, k_pages, v_pages, table):
+    """The strides of two row tensors, the cache and the page table, or None when all are contiguous."""
+    if all([t.is_contiguous() for t in (a, b, k_pages, v_pages, table)]):
+        return None
     v = (*a.stride()[:2], *b.stride()[:2], *k_pages.stride()[:3], *v_pages.stride()[:3], table.stride(0))
     return (ctypes.c_int64 * 11)(*v)
 
@@ -583,62 +610,72 @@ def _table(page_table, n_seqs, device):
         raise ValueError(f"page_table must lie on {device} with contiguous rows")
 
 
+@functools.lru_cache(maxsize=64)
 def dash_decode_workspace(B: int, heads: int, head_dim: int, page_size: int, max_pages: int) -> int:
     return int(lib().dash_decode_workspace(B, heads, head_dim, page_size, max_pages))
 
 
-def dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale: float, workspace=None, stream=None):
-    """``lse`` may be None; ``workspace`` as dash_decode_workspace asks for (uint8)."""
-    n_pages, page, hkv, D = _cache(k_pages, v_pages)
-    _rows("q", q, None, D)
-    B, hq = q.shape[0], q.shape[1]
-    _rows("o", o, hq, D, B)
+def _decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale, workspace, stream):
     dev = q.device
-    _table(page_table, B, dev)
-    _plain("lengths", lengths, torch.int32, (B,), dev)
-    if lse is not None:
-        _plain("lse", lse, torch.float32, (B, hq), dev)
-    if workspace is not None:
-        _plain("workspace", workspace, torch.uint8, (None,), dev)
-    st = _on(dev, stream, (("o", o), ("k_pages", k_pages), ("v_pages", v_pages)))
+    n_pages, page, hkv, D = k_pages.shape
     with _device(dev):
         _check(lib().dash_attn_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                       lengths.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                      B, hq, hkv, D, n_pages, page, page_table.shape[1],
-                                      _cache_strides(q, o, k_pages, v_pages, page_table), float(scale),
+                                      q.shape[0], q.shape[1], hkv, D, n_pages, page, page_table.shape[1],
+                                      _cache_strides(q, o, k_pages, v_pages, page_table), scale,
                                       None if workspace is None else workspace.data_ptr(),
-                                      0 if workspace is None else workspace.numel(), st))
+                                      0 if workspace is None else workspace.numel(), _stream_on(dev, stream)))
+
+
+def _decode_inputs(q, k_pages, v_pages, page_table, lengths):
+    _rows("q", q, None, None, None, None)
+    dev, B = q.device, q.shape[0]
+    if _cache(k_pages, v_pages, dev)[3] != q.shape[2]:
+        raise ValueError(f"q has head dimension {q.shape[2]}, the cache {k_pages.shape[3]}")
+    _table(page_table, B, dev)
+    _plain("lengths", lengths, torch.int32, (B,), dev)
+
+
+def dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale: float, workspace=None, stream=None):
+    """``lse`` may be None; ``workspace`` as dash_decode_workspace asks for (uint8)."""
+    _decode_inputs(q, k_pages, v_pages, page_table, lengths)
+    dev = q.device
+    _rows("o", o, q.shape[1], q.shape[2], q.shape[0], dev)
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (q.shape[0], q.shape[1]), dev)
+    if workspace is not None:
+        _plain("workspace", workspace, torch.uint8, (None,), dev)
+    _decode(q, k_pages, v_pages, page_table, lengths, o, lse, float(scale), workspace, stream)
 
 
 def dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=None):
-    n_pages, page, hkv, D = _cache(k_pages, v_pages)
-    _rows("k", k, hkv, D)
-    _rows("v", v, hkv, D, k.shape[0])
     dev = k.device
+    n_pages, page, hkv, D = _cache(k_pages, v_pages, dev)
+    _rows("k", k, hkv, D, None, None)
+    _rows("v", v, hkv, D, k.shape[0], dev)
     _plain("starts", starts, torch.int32, (None,), dev)
     B = starts.shape[0]
     _plain("cu_new", cu_new, torch.int32, (B + 1,), dev)
     _table(page_table, B, dev)
-    st = _on(dev, stream, (("v", v), ("k_pages", k_pages), ("v_pages", v_pages)))
     with _device(dev):
         _check(lib().dash_cache_write(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                       page_table.data_ptr(), starts.data_ptr(), cu_new.data_ptr(), k.shape[0], B, hkv,
                                       D, n_pages, page, page_table.shape[1],
-                                      _cache_strides(k, v, k_pages, v_pages, page_table), st))
+                                      _cache_strides(k, v, k_pages, v_pages, page_table), _stream_on(dev, stream)))
 
 
 def dash_cache_copy(k_pages, v_pages, src, dst, stream=None):
     """``src``, ``dst``: page numbers on the host (lists, arrays or CPU tensors)."""
-    n_pages, page, hkv, D = _cache(k_pages, v_pages)
+    n_pages, page, hkv, D = _cache(k_pages, v_pages, k_pages.device)
     s, d = (array.array("i", x if isinstance(x, (list, tuple)) else x.tolist()) for x in (src, dst))
     if len(s) != len(d):
         raise ValueError("src and dst must have the same length")
-    dev = k_pages.device
-    st = _on(dev, stream, (("v_pages", v_pages),))
-    strides = (ctypes.c_int64 * 6)(*k_pages.stride()[:3], *v_pages.stride()[:3])
+    dev, strides = k_pages.device, None
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        strides = (ctypes.c_int64 * 6)(*k_pages.stride()[:3], *v_pages.stride()[:3])
     with _device(dev):
-        _check(lib().dash_cache_copy(k_pages.data_ptr(), v_pages.data_ptr(), s.buffer_info()[0], d.buffer_info()[0], len(s),
-                                     hkv, D, n_pages, page, strides, st))
+        _check(lib().dash_cache_copy(k_pages.data_ptr(), v_pages.data_ptr(), s.buffer_info()[0], d.buffer_info()[0],
+                                     len(s), hkv, D, n_pages, page, strides, _stream_on(dev, stream)))
 
 
 def dash_sync_status(stream=None):
@@ -705,13 +742,13 @@ def attn_bwd(q, k, v, o, do, lse, causal: bool, scale: float | None = None, sche
 def attn_packed_fwd(plan: PackedPlan, q, k, v, scale: float | None = None, stream=None):
     """O [rows, heads, D] (bf16) and LSE [heads, rows] (fp32) of attention over the plan's packed sequences.  Rows
     behind the last sequence are zero (-inf in LSE)."""
-    _rows("q", q, plan.heads, plan.head_dim)
-    scale = 1.0 / math.sqrt(plan.head_dim) if scale is None else scale
+    _packed_inputs(plan, q, k, v)
+    scale = 1.0 / math.sqrt(plan.head_dim) if scale is None else float(scale)
     rows = q.shape[0]
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty((plan.heads, rows), dtype=torch.float32, device=q.device)
     with _using(stream, o, lse):
-        dash_attn_packed_fwd(plan, q, k, v, o, lse, scale, stream)
+        _packed_fwd(plan, q, k, v, o, lse, scale, stream)
         if rows > plan.rows:
             o[plan.rows:].zero_()
             lse[:, plan.rows:].fill_(float("-inf"))
@@ -720,14 +757,16 @@ def attn_packed_fwd(plan: PackedPlan, q, k, v, scale: float | None = None, strea
 
 def attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, scale: float | None = None, stream=None):
     """dQ [rows, heads, D], dK, dV [rows, kv_heads, D] (bf16); zero behind the last sequence."""
-    _rows("q", q, plan.heads, plan.head_dim)
-    scale = 1.0 / math.sqrt(plan.head_dim) if scale is None else scale
-    rows = q.shape[0]
+    _packed_inputs(plan, q, k, v)
+    _packed_saved(plan, q, o, do, lse)
+    scale = 1.0 / math.sqrt(plan.head_dim) if scale is None else float(scale)
+    rows, kv_shape = q.shape[0], (q.shape[0], plan.kv_heads, plan.head_dim)
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk, dv = (torch.empty((rows, plan.kv_heads, plan.head_dim), dtype=q.dtype, device=q.device) for _ in range(2))
+    dk = torch.empty(kv_shape, dtype=q.dtype, device=q.device)
+    dv = torch.empty(kv_shape, dtype=q.dtype, device=q.device)
     ws = torch.empty(max(plan.workspace_bytes, 0), dtype=torch.uint8, device=q.device)
     with _using(stream, dq, dk, dv, ws):
-        dash_attn_packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, scale, ws, stream)
+        _packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, scale, ws, stream)
         if rows > plan.rows:
             for t in (dq, dk, dv):
                 t[plan.rows:].zero_()
@@ -736,15 +775,15 @@ def attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, scale: float | None =
 
 def attn_decode(q, k_pages, v_pages, page_table, lengths, scale: float | None = None, stream=None):
     """O [B, heads, D] (bf16) and LSE [B, heads] (fp32) of one new token per sequence over a paged cache."""
-    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("attn_decode takes q [B, heads, D], pages [pages, tokens, heads, D] and a table [B, pages]")
-    need = dash_decode_workspace(q.shape[0], q.shape[1], q.shape[2], k_pages.shape[1], page_table.shape[1])
+    _decode_inputs(q, k_pages, v_pages, page_table, lengths)
+    B, heads, dim = q.shape
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    lse = torch.empty((B, heads), dtype=torch.float32, device=q.device)
+    need = dash_decode_workspace(B, heads, dim, k_pages.shape[1], page_table.shape[1])
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     with _using(stream, o, lse, ws):
-        dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale, ws, stream)
+        _decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale, ws, stream)
     return o, lse
 
 

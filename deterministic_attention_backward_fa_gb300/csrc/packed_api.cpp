@@ -246,7 +246,11 @@ void dash_packed_plan_destroy(dash_packed_plan_t *plan) {
     int dev = 0;
     const bool other = cudaGetDevice(&dev) == cudaSuccess && dev != plan->device;
     if (other) cudaSetDevice(plan->device);
+    // a plan may be dropped while some thread captures a graph; freeing its memory is no part of that graph
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
     cudaFree(plan->mem);
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if (other) cudaSetDevice(dev);
   }
   delete plan;

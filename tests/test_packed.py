@@ -114,7 +114,7 @@ def test_refusals_before_any_device_call():
 def test_binding_refuses_wrong_tensors():
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
-        dash._rows("q", q)
+        dash._rows("q", q, 2, 64, None, None)
     with pytest.raises(ValueError, match="CUDA bfloat16"):
         dash.cache_copy(torch.zeros(2, 3, 4, 64), torch.zeros(2, 3, 4, 64), [0], [1])
     with pytest.raises(ValueError, match="32 bits"):
