@@ -25,8 +25,9 @@ std::string packed_sequences(const int32_t *lengths, int n_seqs, PackedTables *o
 
 // The items of the forward and of the backward's two kernels on up to P CTAs:
 // sequences by decreasing length, inside one the K/V heads in batches whose keys
-// and values fit in L2 together, inside a batch the longest items first, each
-// to the CTA that has the least work so far.
+// and values fit in L2 together, inside a batch the longest items first (dK and
+// dV: the longest items of all first), each to the CTA that has the least work
+// so far.
 void packed_forward(int Hq, int Hkv, bool causal, int P, PackedTables *t);
 void packed_backward(int Hq, int Hkv, bool causal, int P, PackedTables *t);
 
