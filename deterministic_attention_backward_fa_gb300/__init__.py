@@ -523,12 +523,12 @@ def dash_packed_bwd_workspace(plan) -> int:
 
 
 def dash_build_packed_items(lengths, heads: int, kv_heads: int, causal: bool, kernel: int, P: int):
-    """Host-only.  The items of the forward (kernel 0), dQ (1) or dK and dV (2): (int32 [N, 16 or 8], cta_off)."""
+    """Host-only.  The items of the forward (kernel 0), dQ (1) or dK and dV (2): (int32 [N, 16, 8 or 12], cta_off)."""
     arr = (ctypes.c_int32 * max(len(lengths), 1))(*lengths)
     n, ctas = _L(0), _I(0)
     head = (arr, len(lengths), heads, kv_heads, int(causal), kernel, P)
     _check(lib().dash_build_packed_items(*head, None, None, ctypes.byref(ctas), ctypes.byref(n)))
-    items = np.zeros((max(n.value, 1), 8 if kernel else 16), dtype=np.int32)
+    items = np.zeros((max(n.value, 1), (16, 8, 12)[kernel]), dtype=np.int32)
     off = np.zeros(ctas.value + 1, dtype=np.int32)
     _check(lib().dash_build_packed_items(*head, items.ctypes.data, off.ctypes.data, None, ctypes.byref(n)))
     return items[:n.value], off

@@ -56,7 +56,10 @@ struct PackedDqItem {
   int kv_len;    // keys of the sequence
   int tile;      // number of the Q tile over all sequences
 };
-// dK and dV: one KV tile of one K/V head against the Q tiles of its group.
+// dK and dV: one KV tile of one K/V head against the Q tiles of its group, or
+// the part t0 <= t < t1 of them: its Q tiles q_first .. n - 1 (q_first: the KV
+// tile itself, or 0 without the causal mask) of the group's first head, of the
+// second head, and so on.
 struct PackedDkvItem {
   int row0;      // first packed row of the KV tile
   int rows;      // valid rows
@@ -66,8 +69,18 @@ struct PackedDkvItem {
   int seq_row0;  // the sequence's first packed row
   int seq_len;
   int tile0;     // number of the sequence's first tile over all sequences
+  int t0, t1;    // the part
+  int slot;      // -1: the item writes dK and dV; else its sums go to this place of `parts`
+  int pad;
 };
-static_assert(sizeof(PackedDqItem) == 32 && sizeof(PackedDkvItem) == 32, "items are read as two 16-byte words");
+// A KV tile whose dK and dV were summed in parts.
+struct PackedSum {
+  int row0, rows, head;
+  int slot, n;   // its parts, in their order
+  int pad[3];
+};
+static_assert(sizeof(PackedDqItem) == 32 && sizeof(PackedDkvItem) == 48 && sizeof(PackedSum) == 32,
+              "items are read as 16-byte words");
 
 struct PackedBwdParams {
   const PackedDqItem *dq_items;
@@ -78,6 +91,9 @@ struct PackedBwdParams {
   const float *lse;        // [Hq][lse_head]
   long long o_row, o_head, do_row, do_head, lse_head;
   float *stats;            // [Hq][n_tiles][2][128]: -LSE log2(e) (-inf behind the sequence), -rowsum(dO O)
+  const PackedSum *sums;
+  int n_sums;
+  float *parts;            // [slots][2][128][D]: dV and dK (not yet scaled) of a part
   __nv_bfloat16 *dq, *dk, *dv;
   long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
   int n_tiles, group, causal;
@@ -85,7 +101,7 @@ struct PackedBwdParams {
   int *status;
   long long spin_limit_ns;
 };
-// Both kernels, dQ first: it writes the stats that the other reads.
+// The kernels, dQ first: it writes the stats that the other reads; then the sums of parts, if any.
 cudaError_t launch_packed_bwd(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                               const CUtensorMap &dout, const PackedBwdParams &p, int dq_ctas, int dkv_ctas,
                               cudaStream_t stream);

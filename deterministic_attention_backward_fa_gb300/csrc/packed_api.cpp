@@ -36,6 +36,8 @@ struct dash_packed_plan_st {
   const dash::PackedFwdItem *fwd = nullptr;
   const dash::PackedDqItem *dq = nullptr;
   const dash::PackedDkvItem *dkv = nullptr;
+  const dash::PackedSum *sums = nullptr;
+  int n_sums = 0, slots = 0;
   const int *fwd_off = nullptr, *dq_off = nullptr, *dkv_off = nullptr;
   int *status = nullptr;
 };
@@ -91,8 +93,12 @@ dash_status_t check_heads(int Hq, int Hkv, int D) {
   return DASH_OK;
 }
 
-// Workspace of a packed backward: two floats for every row of every tile and head.
+// Workspace of a packed backward: two floats for every row of every tile and
+// head, then dV and dK of the KV tiles that are summed in parts.
 long long stats_bytes(const dash_packed_plan_st *p) { return p->n_tiles * p->Hq * 2 * dash::kPackedTile * 4; }
+long long bwd_bytes(const dash_packed_plan_st *p) {
+  return stats_bytes(p) + (long long)p->slots * 2 * dash::kPackedTile * p->D * 4;
+}
 
 dash_status_t check_plan(const dash_packed_plan_st *p, long long rows) {
   if (!p) return report(DASH_ERR_INVALID_ARG, "null plan");
@@ -202,6 +208,8 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
       dash::packed_backward(Hq, Hkv, causal != 0, device.sms, &t);
       p->dq_ctas = (int)t.dq_off.size() - 1;
       p->dkv_ctas = (int)t.dkv_off.size() - 1;
+      p->n_sums = (int)t.sums.size();
+      p->slots = t.slots;
     }
     cudaError_t e = dash::prepare_packed_fwd(D);
     if (e != cudaSuccess) return cuda_error(e, "packed forward");
@@ -215,9 +223,10 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
       if (bytes) std::memcpy(host.data() + at, src, bytes);
       return at;
     };
-    const size_t at[6] = {put(t.fwd.data(), t.fwd.size() * sizeof(t.fwd[0])), put(t.fwd_off.data(), t.fwd_off.size() * 4),
+    const size_t at[7] = {put(t.fwd.data(), t.fwd.size() * sizeof(t.fwd[0])), put(t.fwd_off.data(), t.fwd_off.size() * 4),
                           put(t.dq.data(), t.dq.size() * sizeof(t.dq[0])),    put(t.dq_off.data(), t.dq_off.size() * 4),
-                          put(t.dkv.data(), t.dkv.size() * sizeof(t.dkv[0])), put(t.dkv_off.data(), t.dkv_off.size() * 4)};
+                          put(t.dkv.data(), t.dkv.size() * sizeof(t.dkv[0])), put(t.dkv_off.data(), t.dkv_off.size() * 4),
+                          put(t.sums.data(), t.sums.size() * sizeof(t.sums[0]))};
     if ((e = cudaMalloc(&p->mem, host.size())) != cudaSuccess)
       return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", host.size(), cudaGetErrorString(e));
     if ((e = cudaMemcpy(p->mem, host.data(), host.size(), cudaMemcpyHostToDevice)) != cudaSuccess) {
@@ -231,6 +240,7 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
     p->dq_off = reinterpret_cast<const int *>(m + at[3]);
     p->dkv = reinterpret_cast<const dash::PackedDkvItem *>(m + at[4]);
     p->dkv_off = reinterpret_cast<const int *>(m + at[5]);
+    p->sums = reinterpret_cast<const dash::PackedSum *>(m + at[6]);
   }
   *plan_out = p.release();
   return DASH_OK;
@@ -258,7 +268,7 @@ void dash_packed_plan_destroy(dash_packed_plan_t *plan) {
 
 long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan) {
   if (!plan || !plan->backward) return -1;
-  return stats_bytes(plan);
+  return bwd_bytes(plan);
 }
 
 dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int kernel,
@@ -279,7 +289,9 @@ dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq
     dash::packed_backward(Hq, Hkv, causal != 0, P, &t);
   const std::vector<int32_t> &off = kernel == 0 ? t.fwd_off : kernel == 1 ? t.dq_off : t.dkv_off;
   const void *items = kernel == 0 ? (const void *)t.fwd.data() : kernel == 1 ? (const void *)t.dq.data() : t.dkv.data();
-  const size_t size = kernel == 0 ? sizeof(dash::PackedFwdItem) : sizeof(dash::PackedDqItem);
+  const size_t size = kernel == 0   ? sizeof(dash::PackedFwdItem)
+                      : kernel == 1 ? sizeof(dash::PackedDqItem)
+                                    : sizeof(dash::PackedDkvItem);
   *n_items_out = off.back();
   if (ctas_out) *ctas_out = (int)off.size() - 1;
   if (items_out && off.back()) std::memcpy(items_out, items, off.back() * size);
@@ -343,7 +355,7 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
       return st;
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return report(DASH_ERR_INVALID_ARG, "lse must be a pointer to floats");
-  const long long need = stats_bytes(plan);
+  const long long need = bwd_bytes(plan);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need)
     return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
   CUtensorMap m[4];
@@ -368,6 +380,9 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
   p.do_head = r[4].head;
   p.lse_head = rows;
   p.stats = static_cast<float *>(workspace);
+  p.parts = p.stats + stats_bytes(plan) / 4;
+  p.sums = plan->sums;
+  p.n_sums = plan->n_sums;
   p.dq = static_cast<__nv_bfloat16 *>(dq);
   p.dk = static_cast<__nv_bfloat16 *>(dk);
   p.dv = static_cast<__nv_bfloat16 *>(dv);

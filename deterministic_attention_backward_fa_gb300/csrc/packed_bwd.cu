@@ -84,8 +84,8 @@ template <class T>
 __device__ __forceinline__ T load_item(const T *p) {
   T it;
   int4 *d = reinterpret_cast<int4 *>(&it);
-  d[0] = __ldg(reinterpret_cast<const int4 *>(p));
-  d[1] = __ldg(reinterpret_cast<const int4 *>(p) + 1);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 16; ++i) d[i] = __ldg(reinterpret_cast<const int4 *>(p) + i);
   return it;
 }
 
@@ -122,6 +122,19 @@ struct OutRow {
       *reinterpret_cast<uint4 *>(out + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
   }
 };
+
+// The same row in 32 bits, as one part of a sum.
+template <int D>
+__device__ __forceinline__ void write_part(uint32_t taddr, float *out) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t r[32];
+    tmem_ld32(taddr + c, r);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+  }
+}
 
 // P and dS replace the scores they come from: the kCols columns of a thread
 // pack into the first half of their own place, which the same thread has read,
@@ -639,8 +652,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       const int per = p.causal ? it.n - it.kv : it.n;
       if (it.n * kPackedTile > it.seq_len && sub == 0) {  // rows past the end in each head's last tiles
         const int first = it.seq_len - (it.n - 1) * kPackedTile;
-        for (int h = 1; h <= p.group; ++h) {
-          const int at = loads + h * per - 1;
+        for (int t = it.t0 + (per - 1 - it.t0 % per); t < it.t1; t += per) {
+          const int at = loads + t - it.t0;
           mbar_wait(&bars[C::bTailDO], tail_ph, g);
           if (!warp_aborted(g)) clear_rows<D>(smem + C::oDO + at % C::kDO * C::kBytes, first, lane);
           if (lane == 0) mbar_arrive(&bars[C::bFixedDO]);
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
           tail_ph ^= 1;
         }
       }
-      loads += per * p.group;
+      loads += it.t1 - it.t0;
       bool ok = mbar_wait(&bars[C::bDvFull], ph, g);
       ok &= mbar_wait(&bars[C::bDkFull], ph, g);
       ph ^= 1;
@@ -672,6 +685,15 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
           __syncwarp();
         }
       };
+      if (it.slot >= 0) {
+        float *part = p.parts + (size_t)it.slot * (2 * 128 * D) + L * D;
+        write_part<D>(tl + C::cDV, part);
+        write_part<D>(tl + C::cDK, part + 128 * D);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+        continue;
+      }
       write(tl + C::cDV, 1.f, p.dv + row * p.dv_row + it.head * p.dv_head, false);
       write(tl + C::cDK, p.scale, p.dk + row * p.dk_row + it.head * p.dk_head, true);
     }
@@ -690,66 +712,56 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       Ring<C::kQ> rq;
       Ring<C::kDO> rd;
       Ring<C::kSt> rs;
-      uint32_t e_ph = 1, nkv = 0, nt = 0;
+      uint32_t e_ph = 1, nk = 0, nv = 0, nq = 0, nst = 0, ndo = 0;
       bool live = true;
+      auto load = [&](int full, int empty, uint32_t ph, uint32_t at, const CUtensorMap *m, int row, int head) {
+        live = live && mbar_wait(&bars[empty], ph ^ 1, g);
+        if (!live) return 0u;
+        mbar_arrive_expect_tx(&bars[full], C::kBytes);
+        C::load(smem + at, m, &bars[full], row, head);
+        return 1u;
+      };
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
-        const int q_first = p.causal ? it.kv : 0;
-        for (int h = 0; h < p.group; ++h)
-          for (int q = q_first; q < it.n; ++q) {
-            const bool first = h == 0 && q == q_first;
-            const int row = it.seq_row0 + q * kPackedTile, head = it.head * p.group + h;
-            if (first) {
-              live = live && mbar_wait(&bars[C::bKEmpty], e_ph, g);
-              if (live) {
-                mbar_arrive_expect_tx(&bars[C::bKFull], C::kBytes);
-                C::load(smem + C::oK, &tmK, &bars[C::bKFull], it.row0, it.head);
-              }
-            }
-            live = live && mbar_wait(&bars[C::bQEmpty + rq.st], rq.ph ^ 1, g);
-            if (live) {
-              mbar_arrive_expect_tx(&bars[C::bQFull + rq.st], C::kBytes);
-              C::load(smem + C::oQ + rq.st * C::kBytes, &tmQ, &bars[C::bQFull + rq.st], row, head);
-            }
-            live = live && mbar_wait(&bars[C::bStEmpty + rs.st], rs.ph ^ 1, g);
-            if (live) {
-              mbar_arrive_expect_tx(&bars[C::bStFull + rs.st], 1024);
-              bulk_load(smem + C::oSTAT + rs.st * 1024, p.stats + ((size_t)head * p.n_tiles + it.tile0 + q) * 256, 1024,
-                        &bars[C::bStFull + rs.st]);
-            }
-            if (first) {
-              live = live && mbar_wait(&bars[C::bVEmpty], e_ph, g);
-              e_ph ^= 1;
-              if (live) {
-                mbar_arrive_expect_tx(&bars[C::bVFull], C::kBytes);
-                C::load(smem + C::oV, &tmV, &bars[C::bVFull], it.row0, it.head);
-                ++nkv;
-              }
-            }
-            live = live && mbar_wait(&bars[C::bDOEmpty + rd.st], rd.ph ^ 1, g);
-            if (live) {
-              mbar_arrive_expect_tx(&bars[C::bDOFull + rd.st], C::kBytes);
-              C::load(smem + C::oDO + rd.st * C::kBytes, &tmDO, &bars[C::bDOFull + rd.st], row, head);
-              ++nt;
-            }
-            rq.next();
-            rs.next();
-            rd.next();
+        const int q_first = p.causal ? it.kv : 0, per = it.n - q_first;
+        int head = it.head * p.group + it.t0 / per, q = q_first + it.t0 % per;
+        for (int t = it.t0; t < it.t1; ++t) {
+          const int row = it.seq_row0 + q * kPackedTile;
+          if (t == it.t0) nk += load(C::bKFull, C::bKEmpty, e_ph ^ 1, C::oK, &tmK, it.row0, it.head);
+          nq += load(C::bQFull + rq.st, C::bQEmpty + rq.st, rq.ph, C::oQ + rq.st * C::kBytes, &tmQ, row, head);
+          live = live && mbar_wait(&bars[C::bStEmpty + rs.st], rs.ph ^ 1, g);
+          if (live) {
+            mbar_arrive_expect_tx(&bars[C::bStFull + rs.st], 1024);
+            bulk_load(smem + C::oSTAT + rs.st * 1024, p.stats + ((size_t)head * p.n_tiles + it.tile0 + q) * 256, 1024,
+                      &bars[C::bStFull + rs.st]);
+            ++nst;
           }
+          if (t == it.t0) {
+            nv += load(C::bVFull, C::bVEmpty, e_ph ^ 1, C::oV, &tmV, it.row0, it.head);
+            e_ph ^= 1;
+          }
+          ndo += load(C::bDOFull + rd.st, C::bDOEmpty + rd.st, rd.ph, C::oDO + rd.st * C::kBytes, &tmDO, row, head);
+          rq.next();
+          rs.next();
+          rd.next();
+          if (++q == it.n) {
+            q = q_first;
+            ++head;
+          }
+        }
       }
-      // Copies still in flight land before the CTA exits.  After an abort a tile's loads may
-      // be cut short between its parts, so the drains (bounded) may find nothing to wait for.
+      // copies still in flight land before the CTA exits
       auto drain = [&](int bar, uint32_t n, uint32_t stages) {
         for (uint32_t s = 0; s < stages; ++s) {
           const uint32_t f = n / stages + (s < n % stages ? 1u : 0u);
           if (f) mbar_drain(&bars[bar + s], (f - 1) & 1, g.limit_ns);
         }
       };
-      drain(C::bKFull, nkv, 1);
-      drain(C::bVFull, nkv, 1);
-      drain(C::bQFull, nt, C::kQ);
-      drain(C::bDOFull, nt, C::kDO);
-      drain(C::bStFull, nt, C::kSt);
+      drain(C::bKFull, nk, 1);
+      drain(C::bVFull, nv, 1);
+      drain(C::bQFull, nq, C::kQ);
+      drain(C::bDOFull, ndo, C::kDO);
+      drain(C::bStFull, nst, C::kSt);
     } else if (role == 0) {
       // ------------------------------------------------ X: dV (and S^T)
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
@@ -773,9 +785,9 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       };
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
-        const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
+        const int per = p.causal ? it.n - it.kv : it.n, total = it.t1 - it.t0;
         const bool ragged = it.n * kPackedTile > it.seq_len;
-        int left = per;  // Q tiles of the head from this one on
+        int left = per - it.t0 % per;  // Q tiles of the head from this one on
         if (C::kTurns) {
           wait(C::bKFull, k_ph);
           k_ph ^= 1;
@@ -844,14 +856,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       };
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
-        const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
+        const int per = p.causal ? it.n - it.kv : it.n, total = it.t1 - it.t0;
         const bool ragged = it.n * kPackedTile > it.seq_len;
         wait(C::bVFull, v_ph);
         v_ph ^= 1;
         wait(C::bDOFull + rd.st, rd.ph);
         tc_fence_after();
         issue_dp(total == 1);
-        int left = per;
+        int left = per - it.t0 % per;
         for (int t = 0; t < total; ++t) {
           const bool more = t + 1 < total;
           if (more) wait(C::bDOFull + rd.st, rd.ph);
@@ -893,7 +905,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       uint32_t k_ph = 0, e_ph = 1, buf = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedDkvItem it = load_item(p.dkv_items + i);
-        const int total = (p.causal ? it.n - it.kv : it.n) * p.group;
+        const int total = it.t1 - it.t0;
         wait(C::bKFull, k_ph);
         k_ph ^= 1;
         for (int t = 0; t < total; ++t) {
@@ -925,8 +937,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
     uint32_t s_ph = 0, dp_ph = 0, buf = 0;
     for (int i = i_begin; i < i_end; ++i) {
       const PackedDkvItem it = load_item(p.dkv_items + i);
-      const int per = p.causal ? it.n - it.kv : it.n, total = per * p.group;
-      int k = 0;
+      const int per = p.causal ? it.n - it.kv : it.n, total = it.t1 - it.t0;
+      int k = it.t0 % per;
       for (int t = 0; t < total; ++t) {
         // a causal KV tile's first Q tile of each head is on the diagonal
         const bool diagonal = p.causal && k == 0;
@@ -1038,6 +1050,34 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
   }
 }
 
+// Adds up the parts of a KV tile's dK and dV in their order.  Bound by the bytes
+// of the parts, which mostly come from L2.
+template <int D>
+__global__ void __launch_bounds__(256) dash_packed_sum(const PackedBwdParams p) {
+  const PackedSum it = load_item(p.sums + blockIdx.x);
+  const bool is_k = blockIdx.y != 0;
+  const float *src = p.parts + (size_t)it.slot * (2 * 128 * D) + (is_k ? 128 * D : 0);
+  __nv_bfloat16 *out = is_k ? p.dk + it.row0 * p.dk_row + it.head * p.dk_head : p.dv + it.row0 * p.dv_row + it.head * p.dv_head;
+  const long long row_stride = is_k ? p.dk_row : p.dv_row;
+  const float scale = is_k ? p.scale : 1.f;
+  // blockIdx.z takes a quarter of the rows
+  for (int x = threadIdx.x; x < 32 * D / 4; x += 256) {
+    const int r = blockIdx.z * 32 + x / (D / 4), c = x % (D / 4) * 4;
+    if (r >= it.rows) break;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < it.n; ++k) {
+      const float4 v = *reinterpret_cast<const float4 *>(src + (size_t)k * (2 * 128 * D) + r * D + c);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    *reinterpret_cast<uint2 *>(out + r * row_stride + c) =
+        make_uint2(pack_bf16(scale * sum.x, scale * sum.y), pack_bf16(scale * sum.z, scale * sum.w));
+  }
+}
+
 template <class Cfg>
 constexpr int smem_bytes() {
   return Cfg::kSmem > (uint32_t)kMinSmemOneCtaPerSm ? (int)Cfg::kSmem : kMinSmemOneCtaPerSm;
@@ -1065,6 +1105,7 @@ cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorM
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   dash_packed_dkv_kernel<D><<<dkv_ctas, DkvCfg<D>::kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
+  if (p.n_sums) dash_packed_sum<D><<<dim3(p.n_sums, 2, 4), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

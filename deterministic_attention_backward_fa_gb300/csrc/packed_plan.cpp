@@ -41,9 +41,9 @@ void for_batches(const PackedTables &t, int Hkv, F f) {
 }
 
 // Deals the items, in their order, to the CTA with the least work (ties to the
-// lowest) and writes them grouped by CTA.
+// lowest) and writes them grouped by CTA.  Returns the work of the last CTA to end.
 template <class Item, class Cost>
-void deal(const std::vector<Item> &items, int P, Cost cost, std::vector<Item> *out, std::vector<int32_t> *off) {
+long long deal(const std::vector<Item> &items, int P, Cost cost, std::vector<Item> *out, std::vector<int32_t> *off) {
   using Slot = std::pair<long long, int>;  // {work, CTA}
   P = (int)std::max<long long>(1, std::min<long long>(P, (long long)items.size()));
   std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>> heap;
@@ -63,6 +63,9 @@ void deal(const std::vector<Item> &items, int P, Cost cost, std::vector<Item> *o
     for (int i : lists[c]) out->push_back(items[i]);
     off->push_back((int32_t)out->size());
   }
+  long long most = 0;
+  for (; !heap.empty(); heap.pop()) most = heap.top().first;
+  return most;
 }
 
 }  // namespace
@@ -134,16 +137,57 @@ void packed_backward(int Hq, int Hkv, bool causal, int P, PackedTables *t) {
                       tile0 + qt});
     for (int kv = 0; kv < n; ++kv)
       for (int hk = h_begin; hk < h_end; ++hk)
-        dkv.push_back({sq.x + kv * kPackedTile, rows(kv), kv, hk, n, sq.x, sq.y, tile0});
+        dkv.push_back({sq.x + kv * kPackedTile, rows(kv), kv, hk, n, sq.x, sq.y, tile0, 0,
+                       group * (causal ? n - kv : n), -1, 0});
   });
   deal(dq, P, [](const PackedDqItem &it) { return (long long)it.nkv; }, &t->dq, &t->dq_off);
-  // The dK/dV items are few and large (a KV tile with every Q tile of its group),
-  // so balance counts for more than what L2 holds: the longest of all first (a
-  // training batch of 16384 tokens 235 us against 246).
-  auto cost = [&](const PackedDkvItem &it) { return (long long)group * (causal ? it.n - it.kv : it.n); };
-  std::stable_sort(dkv.begin(), dkv.end(),
-                   [&](const PackedDkvItem &a, const PackedDkvItem &b) { return cost(a) > cost(b); });
-  deal(dkv, P, cost, &t->dkv, &t->dkv_off);
+
+  // The dK/dV items are few and large (a KV tile with every Q tile of its
+  // group), so balance counts for more than what L2 holds: the longest of all
+  // first (a training batch of 16384 tokens 235 us against 246).  Where that
+  // still leaves CTAs idle, items longer than `cut` go in parts, whose sums a
+  // kernel behind adds up: the cut with the least time, a part costing the bytes
+  // that it writes and reads back (about 1 / 40 of a tile pair's time at D = 128,
+  // and as much at D = 64, where both are half) and the kernel three tile pairs.
+  auto cost = [](const PackedDkvItem &it) { return (long long)it.t1 - it.t0; };
+  auto parts_of = [&](long long cut) {
+    std::vector<PackedDkvItem> out;
+    t->sums.clear();
+    t->slots = 0;
+    for (const PackedDkvItem &it : dkv) {
+      const long long n = (cost(it) + cut - 1) / cut;
+      if (n <= 1) {
+        out.push_back(it);
+        continue;
+      }
+      t->sums.push_back({it.row0, it.rows, it.head, t->slots, (int)n, {0, 0, 0}});
+      for (long long k = 0; k < n; ++k) {
+        PackedDkvItem part = it;
+        part.t0 = (int)(it.t1 * k / n);
+        part.t1 = (int)(it.t1 * (k + 1) / n);
+        part.slot = t->slots++;
+        out.push_back(part);
+      }
+    }
+    std::stable_sort(out.begin(), out.end(),
+                     [&](const PackedDkvItem &a, const PackedDkvItem &b) { return cost(a) > cost(b); });
+    return out;
+  };
+  long long longest = 1, best = -1, best_cut = 0;
+  int worse = 0;
+  for (const PackedDkvItem &it : dkv) longest = std::max(longest, cost(it));
+  for (long long cut = longest; cut >= 4 || cut == longest; cut /= 2) {
+    const std::vector<PackedDkvItem> items = parts_of(cut);
+    long long time = 40 * deal(items, P, cost, &t->dkv, &t->dkv_off);
+    if (t->slots) time += t->slots + 120;
+    if (best < 0 || time < best) {
+      best = time;
+      best_cut = cut;
+    } else if (++worse == 2) {
+      break;
+    }
+  }
+  deal(parts_of(best_cut), P, cost, &t->dkv, &t->dkv_off);
 }
 
 }  // namespace dash

@@ -17,6 +17,8 @@ struct PackedTables {
   std::vector<PackedFwdItem> fwd;
   std::vector<PackedDqItem> dq;
   std::vector<PackedDkvItem> dkv;
+  std::vector<PackedSum> sums;         // KV tiles whose items are parts
+  int slots = 0;                       // parts
   std::vector<int32_t> fwd_off, dq_off, dkv_off;
 };
 

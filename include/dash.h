@@ -489,9 +489,9 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
 
 /* Backward: dq, dk, dv from the forward's inputs, o, lse and dout; dk and dv of
  * a shared head are sums over its Q heads, in 32 bits.  Every gradient element
- * is summed by one CTA in one order that depends on its own sequence alone (no
- * schedule is involved), so its bits are the same in every run and in every
- * batch.  strides: q, k, v, o, dout, dq, dk, dv (16 values).  `workspace` is
+ * is summed in one order that the plan fixes (no schedule, no atomics), so its
+ * bits are the same in every run with the same lengths on the same GPU model;
+ * those of dq are the same in any batch.  strides: q, k, v, o, dout, dq, dk, dv (16 values).  `workspace` is
  * device memory of dash_packed_bwd_workspace(plan) bytes, 16-byte aligned, used
  * until the call's work is done: calls that overlap need one each.  Can be
  * captured. */
@@ -509,9 +509,10 @@ long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan);
  * KV tiles', Q head, Q head', position, position', first key row, keys, K/V
  * head, 0, 0, 0} of one or two Q tiles (0 KV tiles: no second one); kernel 1,
  * dQ, 8 ints: {row0, rows, KV tiles, Q head, position, first key row, keys,
- * number of the tile}; kernel 2, dK and dV, 8 ints: {row0, rows, KV tile, K/V
+ * number of the tile}; kernel 2, dK and dV, 12 ints: {row0, rows, KV tile, K/V
  * head, tiles of the sequence, its first row, its length, number of its first
- * tile}.  items_out and cta_off_out may be NULL to ask for the counts. */
+ * tile, t0, t1, place of its partial sums or -1, 0}: the part t0 <= t < t1 of
+ * the KV tile's Q tiles, those of the group's first head first.  items_out and cta_off_out may be NULL to ask for the counts. */
 dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int kernel,
                                       int P, int32_t *items_out, int32_t *cta_off_out, int *ctas_out,
                                       long long *n_items_out);

@@ -45,7 +45,9 @@ def check_backward(lens, q, k, v, o, do, lse, causal, scale, grads):
 CASES = [([1], 1, 1, 64, True), ([128], 2, 1, 128, True), ([129, 1, 127], 4, 2, 64, True),
          ([0, 5, 0, 300, 0], 6, 2, 128, True), ([257, 64, 0, 1], 4, 4, 64, False), ([1000, 3], 8, 1, 128, True),
          ([200], 5, 1, 64, False), ([700, 513], 2, 2, 128, False), ([1300, 384, 31], 4, 4, 128, True),
-         (list(range(1, 60, 3)), 8, 2, 128, True), ([2049], 16, 4, 64, True), ([640], 3, 3, 128, True)]
+         (list(range(1, 60, 3)), 8, 2, 128, True), ([2049], 16, 4, 64, True), ([640], 3, 3, 128, True),
+         # few, long KV tiles: dK and dV are summed in parts
+         ([1930, 70], 8, 1, 64, True), ([1300], 6, 1, 128, False), ([2000], 4, 2, 128, True)]
 
 
 @pytest.mark.parametrize("lens,hq,hkv,D,causal", CASES, ids=str)

@@ -17,7 +17,7 @@ def built():
     __graft_entry__.build()
 
 
-LENS = [[1], [128], [129, 1, 127], [0, 5, 0, 300, 0], [], [0], [1000, 3, 257], [4000], list(range(1, 40))]
+LENS = [[1], [128], [129, 1, 127], [4096], [0, 5, 0, 300, 0], [], [0], [1000, 3, 257], [4000], list(range(1, 40))]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=str)
@@ -47,9 +47,22 @@ def test_items_cover_every_tile_once(lens, hq, hkv, causal):
         assert sorted(fwd) == q_tiles
         assert sorted(tuple(it[:7]) for it in got[1]) == q_tiles
         assert all(it[7] == next(first[s] + i for s, i in tiles if starts[s] + 128 * i == it[0]) for it in got[1])
-        assert sorted(map(tuple, got[2])) == sorted(
-            (starts[s] + 128 * i, rows(s, i), i, h, n_of[s], starts[s], lens[s], first[s])
-            for s, i in tiles for h in range(hkv))
+        # the parts of every KV tile cover its Q tiles once, and parts have places of their own
+        parts, places = {}, []
+        for it in got[2]:
+            parts.setdefault(tuple(it[:8]), []).append((it[8], it[9], it[10]))
+        assert set(parts) == {(starts[s] + 128 * i, rows(s, i), i, h, n_of[s], starts[s], lens[s], first[s])
+                              for s, i in tiles for h in range(hkv)}
+        for key, v in parts.items():
+            v.sort()
+            assert v[0][0] == 0 and v[-1][1] == (hq // hkv) * (key[4] - (key[2] if causal else 0))
+            assert all(a[1] == b[0] for a, b in zip(v, v[1:])) and all(a < b for a, b, _ in v)
+            if len(v) == 1:
+                assert v[0][2] == -1
+            else:  # in their order, side by side
+                assert [x[2] for x in v] == list(range(v[0][2], v[0][2] + len(v)))
+                places += [x[2] for x in v]
+        assert sorted(places) == list(range(len(places)))
 
 
 def test_item_refusals():
