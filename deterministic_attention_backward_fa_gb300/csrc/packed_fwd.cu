@@ -23,8 +23,12 @@
 // there, but 0 x NaN is NaN).  K rows past the end are masked after the
 // product, Q rows past the end are computed and not written.
 //
-// Tensor memory: S0 at 0, S1 at 128 (P overwrites the first half of its S as
-// packed bf16, rounded once to the MMA's operand type), O0 at 256, O1 at 256+D.
+// Tensor memory: S0 at 0, S1 at 128, O0 at 256, O1 at 256+D; P, packed bf16 and
+// rounded once as the MMA's operand, overwrites the first half of its S.  At
+// D = 64 there is room for P beside S (at 384 and 448): the next score then runs
+// as soon as this one is in registers, so that the softmax, which takes longer
+// than the products there, never waits for them (16 heads of 4096 tokens:
+// 707 TFLOPS against 670).
 #include <cuda_runtime.h>
 
 #include "packed.h"
@@ -54,15 +58,17 @@ struct Cfg {
   static constexpr uint32_t oQ = 0;                 // two Q tiles
   static constexpr uint32_t oKV = 2 * kTile;
   static constexpr uint32_t oBAR = oKV + kStages * kTile;
-  static constexpr int kNumBars = 18 + 2 * kStages;
+  static constexpr int kNumBars = 22 + 2 * kStages;
   static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
   static constexpr uint32_t oSTAT = oMISC + 16;     // {maximum, sum} of each tile's rows
   static constexpr uint32_t kSmemBytes = oSTAT + 2 * 128 * 8;
   static constexpr uint32_t cO = 256;
+  static constexpr bool kApart = D == 64;  // P beside S
+  static __device__ __forceinline__ constexpr uint32_t cP(int s) { return kApart ? 384 + 64 * s : 128 * s; }
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory of one CTA");
 
-enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bPFull = 12, bLFull = 14, bOEmpty = 16, bKvFull0 = 18 };
+enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bPFull = 12, bLFull = 14, bOEmpty = 16, bSRead = 18, bPvDone = 20, bKvFull0 = 22 };
 
 __device__ __forceinline__ PackedFwdItem load_item(const PackedFwdItem *p) {
   PackedFwdItem it;
@@ -131,7 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[bQFull + s], 1);
       mbar_init(&bars[bQEmpty + s], 1);
       mbar_init(&bars[bSFull + s], 1);
-      mbar_init(&bars[bPFull + s], 5);  // four softmax warps and the turn
+      mbar_init(&bars[bPFull + s], C::kApart ? 4 : 5);  // four softmax warps and the turn
+      mbar_init(&bars[bSRead + s], 4);
+      mbar_init(&bars[bPvDone + s], 1);
       mbar_init(&bars[bLFull + s], 4);
       mbar_init(&bars[bOEmpty + s], 4);
       mbar_init(&bars[bOFull + s], 1);
@@ -258,16 +266,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // later).  The warps take turns, tile 0's PV and next S, then tile 1's, so
       // that one tile's softmax runs under the other's MMAs; free running, the
       // two fall into step and softmax and MMAs take place one after the other.
+      // (With P apart the softmax sets the pace and there are no turns.)
       const int s = warp == 8 ? 0 : 1;
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
       Ring<C::kStages> rk;              // next K or V tile to be read
-      uint32_t q_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0;
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0, r_ph = 1;
       uint32_t lead = elect_one();      // 0 in every lane once a wait has failed: nothing more is issued
       const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
       const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oKV), 16, 1024);
       const uint64_t dv0 = sw128_desc(smem_u32(smem + C::oKV), C::kPanel, 1024);
-      const uint32_t tS = tmem + s * 128, tO = tmem + C::cO + s * D;
+      const uint32_t tS = tmem + s * 128, tP = tmem + C::cP(s), tO = tmem + C::cO + s * D;
       auto wait = [&](int bar, uint32_t ph) {
         if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
       };
@@ -277,6 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lead) mbar_arrive(&bars[bPFull + to]);
       };
       auto issue_s = [&](int stage, bool pass) {
+        if (C::kApart) {
+          wait(bSRead + s, r_ph);  // the S before is in registers
+          r_ph ^= 1;
+        }
+        tc_fence_after();
         const uint64_t dk = dk0 + ((stage * C::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -295,7 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine > 0) {  // S of the first KV tile
           wait(bQFull + s, q_ph);
           q_ph ^= 1;
-          tc_fence_after();
           issue_s(rk.st, false);
           if (mine == 1) tc_commit_if(lead, &bars[bQEmpty + s]);
         }
@@ -317,18 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               wait(bOEmpty + s, o_ph);
               o_ph ^= 1;
             }
+            const bool more = j + 1 < mine;
+            if (C::kApart && more) issue_s(rk.st, false);
             // P stands in tensor memory, O is at its scale, and the turn has come: tile 1's behind tile 0's, tile 0's
             // behind tile 1's of the KV tile before
-            if (j >= both || (s == 0 && j == 0)) give_turn(s);
-            const bool pass = j < both && (s == 0 || j + 1 < both);
+            if (!C::kApart && (j >= both || (s == 0 && j == 0))) give_turn(s);
+            const bool pass = !C::kApart && j < both && (s == 0 || j + 1 < both);
             wait(bPFull + s, p_ph);
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
+              mma_ts_if(lead, tO, tP + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
             p_ph ^= 1;
-            if (j + 1 < mine) {
-              issue_s(rk.st, pass);  // MMAs run in issue order: PV has read P before S overwrites it
+            if (C::kApart) tc_commit_if(lead, &bars[bPvDone + s]);
+            if (more) {
+              if (!C::kApart) issue_s(rk.st, pass);  // MMAs run in issue order: PV has read P before S overwrites it
               if (j + 2 == mine) tc_commit_if(lead, &bars[bQEmpty + s]);
             } else {
               if (pass) give_turn(s ^ 1);
@@ -377,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp >> 2, sub = warp & 3;
     const int L = sub * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
-    const uint32_t tS = tl + s * 128, tO = tl + C::cO + s * D;
-    uint32_t s_ph = 0, o_ph = 0;
+    const uint32_t tS = tl + s * 128, tP = tl + C::cP(s), tO = tl + C::cO + s * D;
+    uint32_t s_ph = 0, o_ph = 0, v_ph = 0;
     for (int i = i_begin; i < i_end; ++i) {
       const PackedFwdItem it = load_item(p.items + i);
       const int n = s ? it.nkv[1] : it.nkv[0];
@@ -401,6 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_order32(x[c]);
+        if (C::kApart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[bSRead + s]);
+        }
         const int cols = limit - j * kPackedTile;  // valid columns of this tile
         if (__any_sync(0xffffffffu, cols < kPackedTile)) {
 #pragma unroll
@@ -418,10 +439,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c)
             mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (C::kApart && j > 0) {  // the last PV has read P
+          mbar_wait(&bars[bPvDone + s], v_ph, g);
+          v_ph ^= 1;
+          __syncwarp();
+          tc_fence_after();
+        }
         if (j == 0) {
           m = top == -INFINITY ? 0.f : top;
         } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          // PV(j-1) completed before S(j) did, so O may be rewritten here
+          // PV(j-1) is complete (with P in S's place it completed before S(j) did), so O may be rewritten here
           const float m_new = fmaxf(m, top);
           const float f = ex2(m - m_new);
           m = m_new;
@@ -451,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[c][e + 1] = __float_as_uint(b);
             pk[e >> 1] = pack_bf16(a, b);
           }
-          tmem_st16(tS + 16 * c, pk);
+          tmem_st16(tP + 16 * c, pk);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -468,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The last product's completion also says that the item before has been
       // written out (the product waited for it), so its row of `stat` is free.
-      // The next S comes later anyway.
-      mbar_wait(&bars[bOFull + s], o_ph, g);
+      mbar_wait(&bars[(C::kApart ? bPvDone : bOFull) + s], C::kApart ? v_ph : o_ph, g);
       o_ph ^= 1;
+      v_ph ^= 1;
       float la, lb;
       unpack2(l2, la, lb);
       stat[s * 128 + L] = make_float2(m, la + lb);
