@@ -128,11 +128,14 @@ dash_status_t current_device(int *dev, Device *out) {
   std::lock_guard<std::mutex> lock(g_devices_mu);
   Device &d = g_devices[*dev];
   if (!d.status) {
+    // the first call may come inside a capture, which loading the kernels is no part of
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, *dev)) != cudaSuccess ||
-        (e = dash::prepare_decode()) != cudaSuccess || (e = dash::ops_status_address(&d.status)) != cudaSuccess) {
+        (e = dash::prepare_decode()) != cudaSuccess || (e = dash::ops_status_address(&d.status)) != cudaSuccess)
       d.status = nullptr;
-      return cuda_error(e, "device set-up");
-    }
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return cuda_error(e, "device set-up");
   }
   *out = d;
   return DASH_OK;

@@ -11,9 +11,13 @@
 // gradients makes five, but nothing crosses a CTA: no 32-bit dQ accumulator in
 // memory, no order to enforce between CTAs, no wait of one CTA for another, and
 // dQ's place in tensor memory lets the products run under the softmax.  The
-// one-kernel form (tiles of dQ reduced in the order of a schedule) ran the
-// training batch of 16384 tokens in 737 us and long documents at D = 64 in
-// 2151 us; this one takes DQKV_PACKED and DQKV_D64.
+// one-kernel form (tiles of dQ reduced in the order of a schedule) ran a
+// training batch of 16384 tokens (16 heads on 4, D = 128) in 737 us and long
+// documents at D = 64 (32 heads on 8) in 2151 us; this one takes 437 (dQ 190,
+// dK and dV 241) and 1220 (490 and 730).  The MMAs keep the tensor pipe two
+// thirds busy at D = 128; what is left is the chain from one tile's scores to
+// the next tile's (waits, exponentials), and at D = 64 the exponentials' and
+// the conversions' latency in sixteen warps.
 //
 // Warps of both kernels: the first turn scores into P and dS (eight for dQ,
 // sixteen for dK and dV; a thread owns columns of a row of the accumulator),

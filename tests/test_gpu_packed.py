@@ -200,6 +200,67 @@ def test_streams_and_captured_graphs():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def test_a_long_sequence():
+    # many KV tiles per row, several items per CTA, tails inside tiles
+    lens, hq, hkv, D = [9001, 517], 4, 2, 128
+    q, k, v, do = problem(lens, hq, hkv, D, seed=95)
+    scale = 1 / math.sqrt(D)
+    plan = dash.PackedPlan(lens, hq, hkv, D, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    g = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    dash.dash_sync_status()
+    check_forward(lens, q, k, v, True, scale, o, lse)
+    check_backward(lens, q, k, v, o, do, lse, True, scale, g)
+
+
+def test_a_backward_captured_while_plans_come_and_go():
+    # a plan that is dropped during a capture, and gradients of the same inputs in an eager call and in the graph
+    lens, hq, hkv, D = [260], 4, 2, 128
+    q, k, v, do = problem(lens, hq, hkv, D, seed=97)
+    plan = dash.PackedPlan(lens, hq, hkv, D, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    eager = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    dropped = dash.PackedPlan([5, 6], hq, hkv, D, backward=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        del dropped
+        captured = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, captured))
+    # new values in the same tensors
+    for t, i in ((q, 1), (k, 2), (v, 3)):
+        t.copy_(R.normal(200 + i, *t.shape))
+    o2, lse2 = dash.attn_packed_fwd(plan, q, k, v)
+    o.copy_(o2)
+    lse.copy_(lse2)
+    graph.replay()
+    torch.cuda.synchronize()
+    again = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    assert all(torch.equal(a, b) for a, b in zip(again, captured))
+    assert not torch.equal(eager[0], again[0])
+
+
+def test_two_plans_on_two_streams():
+    probs = [([700, 33], 4, 2, 64, 1), ([128, 1, 390], 6, 3, 64, 2)]
+    data = [(dash.PackedPlan(l, hq, hkv, D, backward=True), *problem(l, hq, hkv, D, seed=300 + s))
+            for l, hq, hkv, D, s in probs]
+
+    def run(p, q, k, v, do, stream=None):
+        o, lse = dash.attn_packed_fwd(p, q, k, v, stream=stream)
+        return (o, lse, *dash.attn_packed_bwd(p, q, k, v, o, do, lse, stream=stream))
+
+    want = [run(*d) for d in data]
+    streams = [torch.cuda.Stream() for _ in data]
+    torch.cuda.synchronize()
+    got = [[run(*d, stream=s) for d, s in zip(data, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    dash.dash_sync_status()
+    for row in got:
+        for w, g in zip(want, row):
+            assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
 def test_empty_problems():
     for lens in ([], [0, 0]):
         plan = dash.PackedPlan(lens, 2, 1, 64, backward=True)

@@ -284,3 +284,29 @@ def test_decode_in_captured_graphs():
     torch.cuda.synchronize()
     dash.dash_sync_status()
     check(q, kp, vp, table, [x - 5 for x in lens], 1 / math.sqrt(D), *n2)
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, deterministic_attention_backward_fa_gb300 as dash
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kp = torch.randn(4, 16, 2, 64, device="cuda").bfloat16()
+vp = torch.randn(4, 16, 2, 64, device="cuda").bfloat16()
+q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+table, n = i([[2, 0, 1]]), i([40])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dash.cache_copy(kp, vp, [2], [3])
+    o, lse = dash.attn_decode(q, kp, vp, table, n)
+g.replay()
+torch.cuda.synchronize()
+o2, lse2 = dash.attn_decode(q, kp, vp, table, n)
+dash.dash_sync_status()
+assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(kp[2], kp[3])
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
