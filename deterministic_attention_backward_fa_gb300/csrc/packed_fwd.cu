@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr uint32_t oQ = 0;                 // two Q tiles
   static constexpr uint32_t oKV = 2 * kTile;
   static constexpr uint32_t oBAR = oKV + kStages * kTile;
-  static constexpr int kNumBars = 22 + 2 * kStages;
+  static constexpr int kNumBars = 25 + 2 * kStages;
   static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
   static constexpr uint32_t oSTAT = oMISC + 16;     // {maximum, sum} of each tile's rows
   static constexpr uint32_t kSmemBytes = oSTAT + 2 * 128 * 8;
@@ -68,7 +68,15 @@ struct Cfg {
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448 && Cfg<64>::kSmemBytes <= 232448, "shared memory of one CTA");
 
-enum { bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVFixed = 10, bVTail = 11, bPFull = 12, bLFull = 14, bOEmpty = 16, bSRead = 18, bPvDone = 20, bKvFull0 = 22 };
+enum {
+  bQFull = 0, bQEmpty = 2, bSFull = 4, bOFull = 6, bFinal = 8, bVTail = 10, bPFull = 11, bLFull = 13, bOEmpty = 15,
+  bSRead = 17, bPvDone = 19, bVFixed = 21, bKvFull0 = 25
+};
+// Cleared V tails that one MMA warp may be ahead of the other by: an item holds
+// at least two stages of the ring until both have read it.
+constexpr int kFixed = 4;
+static_assert(Cfg<128>::kStages <= 2 * kFixed && Cfg<64>::kStages <= 2 * kFixed && bVFixed + kFixed == bKvFull0,
+              "a warp could miss a cleared tail");
 
 __device__ __forceinline__ PackedFwdItem load_item(const PackedFwdItem *p) {
   PackedFwdItem it;
@@ -145,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[bOFull + s], 1);
       mbar_init(&bars[bFinal + s], 1);
     }
-    mbar_init(&bars[bVFixed], 1);
+    for (int k = 0; k < kFixed; ++k) mbar_init(&bars[bVFixed + k], 1);
     mbar_init(&bars[bVTail], 1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&kvFull[s], 1);
@@ -271,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
       Ring<C::kStages> rk;              // next K or V tile to be read
-      uint32_t q_ph = 0, p_ph = 0, o_ph = 1, fix_ph = 0, r_ph = 1;
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 1, r_ph = 1, fixes = 0;
+      bool owed = false;                // the other warp passes the turn to this one's next P
       uint32_t lead = elect_one();      // 0 in every lane once a wait has failed: nothing more is issued
       const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
       const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oKV), 16, 1024);
@@ -320,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(bKvFull0 + rv.st, rv.ph);
           if (fix && j == n - 1) {
             if (lead && s == 0) mbar_arrive(&bars[bVTail]);  // it has landed: its rows past the end may be cleared
-            wait(bVFixed, fix_ph);
-            fix_ph ^= 1;
+            wait(bVFixed + fixes % kFixed, fixes / kFixed & 1);
+            ++fixes;
           }
           if (j + 1 < n) wait(bKvFull0 + rk.st, rk.ph);
           const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
@@ -332,10 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool more = j + 1 < mine;
             if (C::kApart && more) issue_s(rk.st, false);
-            // P stands in tensor memory, O is at its scale, and the turn has come: tile 1's behind tile 0's, tile 0's
-            // behind tile 1's of the KV tile before
-            if (!C::kApart && (j >= both || (s == 0 && j == 0))) give_turn(s);
-            const bool pass = !C::kApart && j < both && (s == 0 || j + 1 < both);
+            // P stands in tensor memory, O is at its scale, and the turn has come: tile 1's from tile 0's warp at the
+            // same KV tile, tile 0's from tile 1's warp at the KV tile before, or, where tile 1 had none, from itself.
+            // So no turn is passed to a warp before it has taken its last one.  (Tile 1 never has more KV tiles.)
+            const bool pass = !C::kApart && j < both;
+            if (!C::kApart && s == 0 && !owed) give_turn(0);
+            owed = pass;
             wait(bPFull + s, p_ph);
             tc_fence_after();
 #pragma unroll
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain(&bars[bFinal + s], 0, g.limit_ns);
     } else if (warp == 10) {
       // ------------------------------- V rows past the end of the sequence
-      uint32_t loads = 0, tail_ph = 0;
+      uint32_t loads = 0, tail_ph = 0, fixes = 0;
       for (int i = i_begin; i < i_end; ++i) {
         const PackedFwdItem it = load_item(p.items + i);
         const int n = max(it.nkv[0], it.nkv[1]);
@@ -383,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[bVFixed]);
+          if (lane == 0) mbar_arrive(&bars[bVFixed + fixes % kFixed]);
+          ++fixes;
         }
       }
     }

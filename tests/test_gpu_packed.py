@@ -200,6 +200,32 @@ def test_streams_and_captured_graphs():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("hq,hkv,D,causal", [(8, 2, 128, True), (8, 2, 64, True), (3, 1, 128, False), (5, 5, 64, False),
+                                             (5, 5, 128, True)])
+def test_many_short_sequences(hq, hkv, D, causal):
+    # dozens of one-tile items per CTA, each with a tail, so that warps run items ahead of each other; and the same
+    # lengths with longer ones between, so that items of one and two tiles, with and without a second Q tile, alternate
+    for lens in ([1 + (37 * i) % 127 for i in range(700)], [1 + (53 * i) % 300 for i in range(300)]):
+        q, k, v, do = problem(lens, hq, hkv, D, seed=93)
+        plan = dash.PackedPlan(lens, hq, hkv, D, causal=causal, backward=True)
+        first = None
+        for _ in range(5):
+            o, lse = dash.attn_packed_fwd(plan, q, k, v)
+            got = (o, lse, *dash.attn_packed_bwd(plan, q, k, v, o, do, lse))
+            dash.dash_sync_status()
+            first = first or got
+            assert all(torch.equal(a, b) for a, b in zip(first, got))
+        scale, few, n = 1 / math.sqrt(D), lens[:40], sum(lens[:40])
+        cut = lambda *t: [x[:n].contiguous() for x in t]
+        check_forward(few, *cut(q, k, v), causal, scale, o[:n], lse[:, :n])
+        check_backward(few, *cut(q, k, v, o, do), lse[:, :n], causal, scale, [x[:n] for x in got[2:]])
+        # the last ones, which end the CTAs' lists
+        few, n = lens[-40:], sum(lens[-40:])
+        cut = lambda *t: [x[-n:].contiguous() for x in t]
+        check_forward(few, *cut(q, k, v), causal, scale, o[-n:], lse[:, -n:])
+        check_backward(few, *cut(q, k, v, o, do), lse[:, -n:], causal, scale, [x[-n:] for x in got[2:]])
+
+
 def test_a_long_sequence():
     # many KV tiles per row, several items per CTA, tails inside tiles
     lens, hq, hkv, D = [9001, 517], 4, 2, 128
