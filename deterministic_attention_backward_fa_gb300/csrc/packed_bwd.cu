@@ -168,8 +168,9 @@ struct Tile {
 // Per KV tile j:   X: dP(j+1) = dO V^T     Y: dQ += dS(j) K     Z: S(j+2) = Q K^T
 // once the softmax warps have dP(j) in registers (X), dS(j) is in tensor memory
 // (Y) and dQ(j) has read dS(j), whose place S(j+2) takes (Z).
-// Tensor memory: S and dS in two buffers at 0 and 128, dP at 256, dQ at 384.  V rows past the sequence's end reach dP only, whose
-// columns there are replaced; K rows there are summed over and are cleared.
+// Tensor memory: S and dS in two buffers at 0 and 128, dP at 256, dQ at 384.  V
+// rows past the sequence's end reach dP only, whose columns there are replaced;
+// K rows there are summed over and are cleared.
 template <int D>
 struct DqCfg : Tile<D> {
   static constexpr int kQ = D == 128 ? 1 : 2, kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;  // stages
@@ -179,8 +180,9 @@ struct DqCfg : Tile<D> {
   static constexpr uint32_t oBAR = oSTAT + 2 * 128 * 8;
   enum {
     // S and dS have a barrier per buffer: a warp may be a tile ahead of another.  So have the tails: S, which
-    // asks for them, is up to two items ahead of dQ, which waits for them.
-    bSFull, bSEmpty = bSFull + 2, bDpFull = bSEmpty + 2, bRead, bDsFull, bOFull = bDsFull + 2, bOEmpty, bTail, bFixed = bTail + 2, bFinalX = bFixed + 2, bFinalY, bFinalZ, bStat,
+    // asks for them, is up to two tiles (and items) ahead of dQ, which waits for them.
+    bSFull, bSEmpty = bSFull + 2, bDpFull = bSEmpty + 2, bRead, bDsFull, bOFull = bDsFull + 2, bOEmpty, bTail,
+    bFixed = bTail + 2, bFinalX = bFixed + 2, bFinalY, bFinalZ, bStat,
     bKFull = bStat + 2, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV,
     bQFull = bVEmpty + kV, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kQ,
     kBars = bDOEmpty + kQ
@@ -464,13 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
         for (int j = 0; j < nkv; ++j) {
           wait(C::bKFull + rk.st, rk.ph);
-          // it has landed: the rows past the end may be cleared, while S reads them (their columns are replaced)
+          wait(C::bSEmpty + buf, e_ph);
+          e_ph ^= buf;
+          // it has landed: the rows past the end may be cleared, while S reads them (their columns are replaced).
+          // Not before the wait, by which the tail before the last has been dealt with: two barriers hold two.
           if (ragged && j + 1 == nkv) {
             if (lead) mbar_arrive(&bars[C::bTail + tail]);
             tail ^= 1;
           }
-          wait(C::bSEmpty + buf, e_ph);
-          e_ph ^= buf;
           tc_fence_after();
           const uint64_t dk = dk0 + ((rk.st * C::kBytes) >> 4);
 #pragma unroll
