@@ -150,6 +150,17 @@ __host__ __device__ inline int decode_splits(int len) {
   const int c = decode_chunk(len);
   return (int)(((long long)len + c - 1) / c);
 }
+// The most splits that a sequence of up to `cap` tokens can have: a length from
+// which splits get longer has more of them than the ones just above it, and
+// those lengths are powers of two.
+inline int decode_max_splits(int cap) {
+  int most = decode_splits(cap);
+  for (long long len = 256; len <= cap; len *= 2) {
+    const int n = decode_splits((int)len);
+    if (n > most) most = n;
+  }
+  return most;
+}
 cudaError_t prepare_decode();  // loads the decode kernels on the current device and raises their shared-memory limit
 cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_t stream);
 

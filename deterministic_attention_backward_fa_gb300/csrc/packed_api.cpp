@@ -411,7 +411,7 @@ long long dash_decode_workspace(int B, int Hq, int D, int page_size, int max_pag
   if (B < 0 || Hq < 1 || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 ||
       (long long)page_size * max_pages > INT32_MAX)
     return -1;
-  const long long splits = dash::decode_splits(page_size * max_pages);
+  const long long splits = dash::decode_max_splits(page_size * max_pages);
   return splits <= 1 ? 0 : (long long)B * Hq * splits * (D * 4 + 8) + 256;
 }
 
@@ -438,7 +438,7 @@ dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v
     return st;
   p.table_row = strides ? strides[10] : max_pages;
   if (B > 1 && p.table_row < max_pages) return report(DASH_ERR_INVALID_ARG, "page table rows overlap");
-  p.max_splits = std::max(1, dash::decode_splits(page_size * max_pages));
+  p.max_splits = std::max(1, dash::decode_max_splits(page_size * max_pages));
   const long long need = dash_decode_workspace(B, Hq, D, page_size, max_pages);
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
     return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);

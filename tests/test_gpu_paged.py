@@ -79,6 +79,20 @@ def test_decode_does_not_depend_on_the_batch():
         assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0])
 
 
+@pytest.mark.parametrize("at,width", [(4096, 4200), (8192, 8300), (65536, 65600)])
+def test_decode_beside_the_lengths_where_splits_grow(at, width):
+    # shorter sequences may have more splits than the longest that the table has room for
+    hq, hkv, D, page = 4, 2, 64, 4
+    lens = [at, width, at - 1, at + 1, 5] * 3
+    kp, vp, table = cache(lens, hkv, D, page, width=-(-width // page))
+    q = R.normal(5, len(lens), hq, D)
+    o, lse = dash.attn_decode(q, kp, vp, table, i32(lens))
+    dash.dash_sync_status()
+    check(q, kp, vp, table, lens, 1 / math.sqrt(D), o, lse)
+    one, l1 = dash.attn_decode(q[:1], kp, vp, table[:1], i32(lens[:1]))
+    assert torch.equal(o[:1], one) and torch.equal(lse[:1], l1)
+
+
 def test_decode_strides_and_lengths_out_of_range():
     lens, hq, hkv, D, page = [100, 700, 31], 8, 2, 64, 16
     kp, vp, table = cache(lens, hkv, D, page)

@@ -124,6 +124,16 @@ def test_refusals_before_any_device_call():
     assert write(n=-1) == 1 and write(D=80) == 2 and write(page=0) == 1 and write(n=0) == 0 and write(B=0) == 0
 
 
+def test_decode_workspace_holds_every_length_a_table_has_room_for():
+    # longer splits past a limit make fewer of them: a table just past it still has room for sequences at it
+    for page in (1, 16):
+        most = 0
+        for pages in sorted({max(1, (1 << n) // page + d) for n in range(6, 20) for d in (-1, 0, 1, 2, 40)}):
+            need = dash.dash_decode_workspace(2, 8, 64, page, pages)
+            assert need >= most
+            most = need
+
+
 def test_binding_refuses_wrong_tensors():
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
