@@ -1,11 +1,13 @@
 // Packed, grouped-head attention backward for sm_103a, deterministic by
-// construction: every gradient element is summed by one CTA in one order.
+// construction: every gradient element is summed in one order, by one CTA, or,
+// where a KV tile's Q tiles are dealt to several, by each over its part and then
+// over the parts in turn.
 //
 //   P = 2^(scale log2(e) q.k - LSE log2(e)),  delta_i = dO_i . O_i,
 //   dS = P (dO V^T - delta),
 //   dQ = scale dS K,   dK = scale sum_heads dS^T Q,   dV = sum_heads P^T dO.
 //
-// Two kernels, each with its own P and dS: dQ walks the KV tiles of a Q tile,
+// Two kernels (and a third that adds up parts), each with its own P and dS: dQ walks the KV tiles of a Q tile,
 // dK/dV the Q tiles (of every Q head of the group) of a KV tile.  That makes
 // seven products of 128 x 128 x D a tile pair where one kernel for all three
 // gradients makes five, but nothing crosses a CTA: no 32-bit dQ accumulator in
@@ -594,8 +596,8 @@ struct DkvCfg : Tile<D> {
   static constexpr uint32_t oSTAT = oDO + kDO * Tile<D>::kBytes;  // [kSt][2][128]
   static constexpr uint32_t oBAR = oSTAT + kSt * 1024;
   enum {
-    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bSEmpty = bSFull + kS, bPFull = bSEmpty + kS, bDpFull = bPFull + kS, bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ,
-    bTailDO, bFixedDO, bFinalX, bFinalY, bFinalZ,
+    bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bSEmpty = bSFull + kS, bPFull = bSEmpty + kS, bDpFull = bPFull + kS,
+    bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ, bTailDO, bFixedDO, bFinalX, bFinalY, bFinalZ,
     bQFull, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kDO, bStFull = bDOEmpty + kDO,
     bStEmpty = bStFull + kSt, kBars = bStEmpty + kSt
   };
@@ -1064,7 +1066,8 @@ __global__ void __launch_bounds__(256) dash_packed_sum(const PackedBwdParams p) 
   const PackedSum it = load_item(p.sums + blockIdx.x);
   const bool is_k = blockIdx.y != 0;
   const float *src = p.parts + (size_t)it.slot * (2 * 128 * D) + (is_k ? 128 * D : 0);
-  __nv_bfloat16 *out = is_k ? p.dk + it.row0 * p.dk_row + it.head * p.dk_head : p.dv + it.row0 * p.dv_row + it.head * p.dv_head;
+  __nv_bfloat16 *out = is_k ? p.dk + it.row0 * p.dk_row + it.head * p.dk_head
+                            : p.dv + it.row0 * p.dv_row + it.head * p.dv_head;
   const long long row_stride = is_k ? p.dk_row : p.dv_row;
   const float scale = is_k ? p.scale : 1.f;
   // blockIdx.z takes a quarter of the rows
