@@ -62,6 +62,17 @@ dash_status_t check_ptr(const void *p, const char *name) {
   return DASH_OK;
 }
 
+// 32-bit values; `optional` ones may be null.
+dash_status_t check_words(const void *p, const char *name, bool optional = false) {
+  if (!p && !optional) return report(DASH_ERR_INVALID_ARG, "%s is a null pointer", name);
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return report(DASH_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
+  return DASH_OK;
+}
+
+// Tokens of a page table row: the end of the last split and the loads ahead of
+// it are counted in 32 bits.
+constexpr long long kMaxCached = INT32_MAX - (1 << 26);
+
 // Strides of a [rows][heads][D] tensor, in elements.
 struct Rows {
   long long row, head;
@@ -69,18 +80,18 @@ struct Rows {
 
 // Takes strides {row, head} (null: contiguous) and checks that 16-byte vectors
 // are aligned and that no two rows share elements.  A stride along an extent of
-// one is never used and set to its contiguous value.
+// one is never used, and set to one that a tensor map takes.
 dash_status_t rows_of(const int64_t *s, int i, long long rows, int heads, int D, const char *name, Rows *out) {
   Rows r{s ? (long long)s[2 * i] : (long long)heads * D, s ? (long long)s[2 * i + 1] : D};
-  if (rows == 1) r.row = (long long)heads * (heads > 1 ? std::max<long long>(r.head, D) : D);
-  if (heads == 1) r.head = rows > 1 ? std::max<long long>(rows * std::max<long long>(r.row, D), D) : D;
+  if ((rows > 1 && r.row >= (1LL << 38)) || (heads > 1 && r.head >= (1LL << 38)))
+    return report(DASH_ERR_UNSUPPORTED, "%s: strides of 2^38 elements and more", name);
+  if (rows == 1) r.row = heads > 1 ? std::max<long long>(r.head, D) : D;
+  if (heads == 1) r.head = std::max<long long>(r.row, D);
   if (r.row < D || r.head < D || (r.row & 7) || (r.head & 7))
     return report(DASH_ERR_INVALID_ARG, "%s: strides (%lld, %lld) must be multiples of 8 of at least D", name,
                   r.row, r.head);
   if (rows > 1 && heads > 1 && r.row < (heads - 1) * r.head + D && r.head < (rows - 1) * r.row + D)
     return report(DASH_ERR_INVALID_ARG, "%s: its rows overlap", name);
-  if (r.row >= (1LL << 38) || r.head >= (1LL << 38))
-    return report(DASH_ERR_UNSUPPORTED, "%s: strides of 2^38 elements and more", name);
   *out = r;
   return DASH_OK;
 }
@@ -171,7 +182,8 @@ dash_status_t check_cache(int Hkv, int D, int n_pages, int page_size) {
   if (n_pages < 1 || page_size < 1) return report(DASH_ERR_INVALID_ARG, "the cache needs pages and tokens in a page");
   if (Hkv < 1) return report(DASH_ERR_INVALID_ARG, "the cache needs heads");
   if (D != 64 && D != 128) return report(DASH_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", D);
-  if ((long long)page_size * Hkv * (D / 8) > INT32_MAX) return report(DASH_ERR_UNSUPPORTED, "pages too large");
+  // a page's 16-byte vectors, with the strides of the loops over them, are counted in 32 bits
+  if ((long long)page_size * Hkv * (D / 8) > INT32_MAX / 2) return report(DASH_ERR_UNSUPPORTED, "pages too large");
   return DASH_OK;
 }
 
@@ -232,7 +244,10 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
                           put(t.sums.data(), t.sums.size() * sizeof(t.sums[0]))};
     if ((e = cudaMalloc(&p->mem, host.size())) != cudaSuccess)
       return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", host.size(), cudaGetErrorString(e));
-    if ((e = cudaMemcpy(p->mem, host.data(), host.size(), cudaMemcpyHostToDevice)) != cudaSuccess) {
+    // pageable memory: cudaMemcpy may return with the copy's last step on its way, and the streams that use the
+    // plan need not wait for this one
+    if ((e = cudaMemcpy(p->mem, host.data(), host.size(), cudaMemcpyHostToDevice)) != cudaSuccess ||
+        (e = cudaStreamSynchronize(cudaStreamLegacy)) != cudaSuccess) {
       cudaFree(p->mem);
       return cuda_error(e, "plan tables");
     }
@@ -312,8 +327,7 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
   if (plan->rows == 0) return DASH_OK;
   if ((st = check_ptr(q, "q")) || (st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) || (st = check_ptr(o, "o")))
     return st;
-  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return report(DASH_ERR_INVALID_ARG, "lse must be a pointer to floats");
+  if ((st = check_words(lse, "lse")) != DASH_OK) return st;
   const int D = plan->D;
   Rows rq, rk, rv, ro;
   if ((st = rows_of(strides, 0, rows, plan->Hq, D, "q", &rq)) || (st = rows_of(strides, 1, rows, plan->Hkv, D, "k", &rk)) ||
@@ -356,8 +370,7 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
   for (int i = 0; i < 8; ++i)
     if ((st = check_ptr(ptrs[i], names[i])) || (st = rows_of(strides, i, rows, heads[i], plan->D, names[i], &r[i])))
       return st;
-  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return report(DASH_ERR_INVALID_ARG, "lse must be a pointer to floats");
+  if ((st = check_words(lse, "lse")) != DASH_OK) return st;
   const long long need = bwd_bytes(plan);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need)
     return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
@@ -409,7 +422,7 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
 
 long long dash_decode_workspace(int B, int Hq, int D, int page_size, int max_pages) {
   if (B < 0 || Hq < 1 || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 ||
-      (long long)page_size * max_pages > INT32_MAX)
+      (long long)page_size * max_pages > kMaxCached)
     return -1;
   const long long splits = dash::decode_max_splits(page_size * max_pages);
   return splits <= 1 ? 0 : (long long)B * Hq * splits * (D * 4 + 8) + 256;
@@ -422,14 +435,16 @@ dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v
   dash_status_t st = check_scale(scale);
   if (st != DASH_OK || (st = check_heads(Hq, Hkv, D)) || (st = check_cache(Hkv, D, n_pages, page_size))) return st;
   if (B < 0 || max_pages < 0) return report(DASH_ERR_INVALID_ARG, "B and max_pages must be >= 0");
-  if ((long long)page_size * max_pages > INT32_MAX)
-    return report(DASH_ERR_UNSUPPORTED, "a page table row covers more than 2^31 tokens");
+  if ((long long)page_size * max_pages > kMaxCached)
+    return report(DASH_ERR_UNSUPPORTED, "a page table row covers more than %lld tokens (2^31 less 2^26)", kMaxCached);
   if (B > 65535) return report(DASH_ERR_UNSUPPORTED, "more than 65535 sequences");
   if (B == 0) return DASH_OK;
   if ((st = check_ptr(q, "q")) || (st = check_ptr(k_pages, "k_pages")) || (st = check_ptr(v_pages, "v_pages")) ||
       (st = check_ptr(o, "o")))
     return st;
-  if ((max_pages > 0 && !page_table) || !lengths) return report(DASH_ERR_INVALID_ARG, "null page table or lengths");
+  if ((st = check_words(page_table, "page_table", max_pages == 0)) || (st = check_words(lengths, "lengths")) ||
+      (st = check_words(lse, "lse", true)))
+    return st;
   Rows rq, ro;
   if ((st = rows_of(strides, 0, B, Hq, D, "q", &rq)) || (st = rows_of(strides, 1, B, Hq, D, "o", &ro))) return st;
   dash::DecodeParams p;
@@ -484,8 +499,9 @@ dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void
   if ((st = check_ptr(k, "k")) || (st = check_ptr(v, "v")) || (st = check_ptr(k_pages, "k_pages")) ||
       (st = check_ptr(v_pages, "v_pages")))
     return st;
-  if ((max_pages > 0 && !page_table) || !starts || !cu_new)
-    return report(DASH_ERR_INVALID_ARG, "null page table, starts or cu_new");
+  if ((st = check_words(page_table, "page_table", max_pages == 0)) || (st = check_words(starts, "starts")) ||
+      (st = check_words(cu_new, "cu_new")))
+    return st;
   Rows rk, rv;
   if ((st = rows_of(strides, 0, n_tokens, Hkv, D, "k", &rk)) || (st = rows_of(strides, 1, n_tokens, Hkv, D, "v", &rv)))
     return st;

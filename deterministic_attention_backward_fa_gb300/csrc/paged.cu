@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(256)
   const __nv_bfloat16 *src = base + pr.x * st.page;
   __nv_bfloat16 *dst = base + pr.y * st.page;
   constexpr int kU = 8;
-  const bool flat = st.head == p.D && st.token == (long long)p.heads * p.D;  // the page is one run of bytes
+  // the page is one run of bytes
+  const bool flat = (st.head == p.D || p.heads == 1) && (st.token == (long long)p.heads * p.D || p.page_size == 1);
   for (int x0 = piece * 256 * kU + threadIdx.x; x0 < total; x0 += pieces * 256 * kU) {
     uint4 a[kU];
     long long at[kU];

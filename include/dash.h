@@ -491,10 +491,10 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
  * a shared head are sums over its Q heads, in 32 bits.  Every gradient element
  * is summed in one order that the plan fixes (no schedule, no atomics), so its
  * bits are the same in every run with the same lengths on the same GPU model;
- * those of dq are the same in any batch.  strides: q, k, v, o, dout, dq, dk, dv (16 values).  `workspace` is
- * device memory of dash_packed_bwd_workspace(plan) bytes, 16-byte aligned, used
- * until the call's work is done: calls that overlap need one each.  Can be
- * captured. */
+ * those of dq are the same in any batch.  strides: q, k, v, o, dout, dq, dk, dv
+ * (16 values).  `workspace` is device memory of dash_packed_bwd_workspace(plan)
+ * bytes, 16-byte aligned, used until the call's work is done: calls that
+ * overlap need one each.  Can be captured. */
 dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q, const void *k, const void *v,
                                    const void *o, const void *dout, const float *lse, void *dq, void *dk, void *dv,
                                    long long rows, const int64_t *strides, float scale, void *workspace,
@@ -512,7 +512,8 @@ long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan);
  * number of the tile}; kernel 2, dK and dV, 12 ints: {row0, rows, KV tile, K/V
  * head, tiles of the sequence, its first row, its length, number of its first
  * tile, t0, t1, place of its partial sums or -1, 0}: the part t0 <= t < t1 of
- * the KV tile's Q tiles, those of the group's first head first.  items_out and cta_off_out may be NULL to ask for the counts. */
+ * the KV tile's Q tiles, those of the group's first head first.  items_out and
+ * cta_off_out may be NULL to ask for the counts. */
 dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int causal, int kernel,
                                       int P, int32_t *items_out, int32_t *cta_off_out, int *ctas_out,
                                       long long *n_items_out);
@@ -529,7 +530,7 @@ dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq
 /* Attention of one new token per sequence over its cached tokens: q, o
  * [B][Hq][D], lengths int32 [B] on the device (the tokens to attend, the new
  * one's among them if it was written; values are clipped to [0, max_pages *
- * page_size]).  lse, if not NULL, is fp32 [B][Hq].  A sequence of length 0
+ * page_size], which must be below 2^31 - 2^26).  lse, if not NULL, is fp32 [B][Hq].  A sequence of length 0
  * gets o = 0 and lse = -inf.  Long sequences are split and joined; the split
  * depends on the sequence's own length alone, so its results are the same
  * bits in any batch.  strides (NULL: contiguous), 11 values: q {batch, head},

@@ -124,6 +124,35 @@ def test_refusals_before_any_device_call():
     assert write(n=-1) == 1 and write(D=80) == 2 and write(page=0) == 1 and write(n=0) == 0 and write(B=0) == 0
 
 
+def test_refusals_of_words_and_sizes_beyond_32_bits():
+    L, nul, fake, odd = dash.lib(), ctypes.c_void_p(0), ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 2)
+
+    def decode(table=fake, lengths=fake, lse=nul, hkv=2, page=16, width=4, strides=None):
+        return L.dash_attn_decode(fake, fake, fake, table, lengths, fake, lse, 2, 4, hkv, 64, 8, page, width, strides,
+                                  0.1, fake, 1 << 40, nul)
+
+    def write(table=fake, starts=fake, cu=fake):
+        return L.dash_cache_write(*[fake] * 4, table, starts, cu, 4, 2, 2, 64, 8, 16, 4, None, nul)
+
+    for call, name in ((decode, "lengths"), (decode, "table"), (decode, "lse"), (write, "table"), (write, "starts"),
+                       (write, "cu")):
+        assert call(**{name: odd}) == 1 and "aligned" in dash.dash_last_error()
+        if name != "lse":
+            assert call(**{name: nul}) == 1 and "null" in dash.dash_last_error()
+    big = 1 << 60
+    wide = (ctypes.c_int64 * 11)(big, 64, 256, 64, 2048, 128, 64, 2048, 128, 64, 4)
+    assert decode(strides=wide) == 2 and "2^38" in dash.dash_last_error()
+    wide = (ctypes.c_int64 * 11)(256, 64, 64, big, 2048, 128, 64, 2048, 128, 64, 4)
+    assert decode(strides=wide) == 2 and "2^38" in dash.dash_last_error()
+    # pages of 2^30 vectors of 16 bytes, tables of nearly 2^31 tokens
+    assert decode(page=1 << 26) == 2 and "pages" in dash.dash_last_error()
+    top = (2**31 - 1 - 2**26) // 16
+    assert decode(width=top + 1) == 2 and "tokens" in dash.dash_last_error()
+    assert dash.dash_decode_workspace(2, 4, 64, 16, top) > 0 > dash.dash_decode_workspace(2, 4, 64, 16, top + 1)
+    assert L.dash_cache_copy(fake, fake, (ctypes.c_int32 * 1)(0), (ctypes.c_int32 * 1)(1), 1, 2, 64, 8, 1 << 26, None,
+                             nul) == 2
+
+
 def test_decode_workspace_holds_every_length_a_table_has_room_for():
     # longer splits past a limit make fewer of them: a table just past it still has room for sequences at it
     for page in (1, 16):
