@@ -41,6 +41,7 @@ struct PackedFwdParams {
   int *status;
   float scale_log2;
   int causal;
+  bool wide;             // every 32 bytes of a row of O start at a multiple of 32
   long long spin_limit_ns;
 };
 
@@ -97,6 +98,7 @@ struct PackedBwdParams {
   __nv_bfloat16 *dq, *dk, *dv;
   long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
   int n_tiles, group, causal;
+  bool wide_in, wide_dq, wide_dkv;  // as above, of o and dout, dq, and dk, dv and parts
   float scale, scale_log2;
   int *status;
   long long spin_limit_ns;

@@ -62,6 +62,11 @@ dash_status_t check_ptr(const void *p, const char *name) {
   return DASH_OK;
 }
 
+// Whether every 32-byte piece of a row (of D elements) starts at a multiple of 32.
+bool wide(const void *p, long long row, long long head) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(row * 2) | (uintptr_t)(head * 2)) & 31u) == 0;
+}
+
 // 32-bit values; `optional` ones may be null.
 dash_status_t check_words(const void *p, const char *name, bool optional = false) {
   if (!p && !optional) return report(DASH_ERR_INVALID_ARG, "%s is a null pointer", name);
@@ -349,6 +354,7 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
   p.status = plan->status;
   p.scale_log2 = scale * kLog2e;
   p.causal = plan->causal;
+  p.wide = wide(o, ro.row, ro.head);
   p.spin_limit_ns = kSpinNs;
   const cudaError_t e =
       dash::launch_packed_fwd(D, mq, mk, mv, p, plan->fwd_ctas, reinterpret_cast<cudaStream_t>(stream));
@@ -411,6 +417,11 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
   p.n_tiles = (int)plan->n_tiles;
   p.group = plan->Hq / plan->Hkv;
   p.causal = plan->causal;
+  bool w[8];
+  for (int i = 0; i < 8; ++i) w[i] = wide(ptrs[i], r[i].row, r[i].head);
+  p.wide_in = w[3] && w[4];
+  p.wide_dq = w[5];
+  p.wide_dkv = w[6] && w[7] && wide(p.parts, 0, 0);
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.status = plan->status;

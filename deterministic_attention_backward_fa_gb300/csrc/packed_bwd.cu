@@ -122,23 +122,21 @@ struct OutRow {
         w[16 * c + (e >> 1)] = pack_bf16(scale * __uint_as_float(r[e]), scale * __uint_as_float(r[e + 1]));
     }
   }
-  __device__ __forceinline__ void write(__nv_bfloat16 *out) const {
+  __device__ __forceinline__ void write(__nv_bfloat16 *out, bool wide) const {
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k)
-      *reinterpret_cast<uint4 *>(out + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int k = 0; k < D / 16; ++k) st_32b(out + 16 * k, w + 8 * k, wide);
   }
 };
 
 // The same row in 32 bits, as one part of a sum.
 template <int D>
-__device__ __forceinline__ void write_part(uint32_t taddr, float *out) {
+__device__ __forceinline__ void write_part(uint32_t taddr, float *out, bool wide) {
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     uint32_t r[32];
     tmem_ld32(taddr + c, r);
 #pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+    for (int e = 0; e < 32; e += 8) st_32b(out + c + e, r + e, wide);
   }
 }
 
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- delta and epilogue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int sub = warp & 3;
-    // A warp makes the stats of its 32 rows: D / 8 lanes of 16 bytes a row, two
+    // A warp makes the stats of its 32 rows: D / 16 lanes of 32 bytes a row, two
     // rounds of loads.  The rows come from memory (nobody else has read O), so
     // the item behind asks L2 for them: 18000 clocks an item without that and
     // with four rounds, longer than a short item takes.
@@ -254,34 +252,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto make_stats = [&](int i) {
       const PackedDqItem it = load_item(p.dq_items + i);
-      constexpr int kLanes = D / 8, kRows = 32 / kLanes, kU = 16 / kRows;
+      constexpr int kLanes = D / 16, kRows = 32 / kLanes, kU = 16 / kRows;
       const int li = lane % kLanes, rs = lane / kLanes;
       float2 *out = stat + (i & 1) * 128;
       float *gout = p.stats + ((size_t)it.head * p.n_tiles + it.tile) * 256;
-      const __nv_bfloat16 *o = p.o + it.row0 * p.o_row + it.head * p.o_head + li * 8;
-      const __nv_bfloat16 *d = p.dout + it.row0 * p.do_row + it.head * p.do_head + li * 8;
+      const __nv_bfloat16 *o = p.o + it.row0 * p.o_row + it.head * p.o_head + li * 16;
+      const __nv_bfloat16 *d = p.dout + it.row0 * p.do_row + it.head * p.do_head + li * 16;
       const int mine = sub * 32 + lane;
       float nl = __int_as_float(0xff800000), nd = 0.f;  // of this lane's row
       if (mine < it.rows) nl = -p.lse[it.head * p.lse_head + it.row0 + mine] * 1.4426950408889634f;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint4 a[kU], b[kU];
+        uint32_t a[kU][8], b[kU][8];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int r = sub * 32 + half * 16 + u * kRows + rs;
-          a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
           if (r < it.rows) {
-            a[u] = *reinterpret_cast<const uint4 *>(o + r * p.o_row);
-            b[u] = *reinterpret_cast<const uint4 *>(d + r * p.do_row);
+            ld_32b(o + r * p.o_row, a[u], p.wide_in);
+            ld_32b(d + r * p.do_row, b[u], p.wide_in);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) a[u][x] = b[u][x] = 0u;
           }
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(&a[u]);
-          const __nv_bfloat162 *pb = reinterpret_cast<const __nv_bfloat162 *>(&b[u]);
+          const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162 *>(a[u]);
+          const __nv_bfloat162 *pb = reinterpret_cast<const __nv_bfloat162 *>(b[u]);
           float sum = 0.f;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 8; ++x) {
             const float2 fa = __bfloat1622float2(pa[x]), fb = __bfloat1622float2(pb[x]);
             sum = fmaf(fa.x, fb.x, sum);
             sum = fmaf(fa.y, fb.y, sum);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
-      if (ok && L < it.rows) out.write(p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head);
+      if (ok && L < it.rows) out.write(p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head, p.wide_dq);
       __syncwarp();
     }
   } else if (warp >= 8) {
@@ -690,14 +690,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
           }
-          if (ok) out.write(to + c);
+          if (ok) out.write(to + c, p.wide_dkv);
           __syncwarp();
         }
       };
       if (it.slot >= 0) {
         float *part = p.parts + (size_t)it.slot * (2 * 128 * D) + L * D;
-        write_part<D>(tl + C::cDV, part);
-        write_part<D>(tl + C::cDK, part + 128 * D);
+        write_part<D>(tl + C::cDV, part, p.wide_dkv);
+        write_part<D>(tl + C::cDK, part + 128 * D, p.wide_dkv);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);

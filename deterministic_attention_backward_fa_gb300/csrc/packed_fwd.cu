@@ -202,13 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tl + C::cO + s * D + c0, r);
           if (ok) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 w;
-              w.x = pack_bf16(inv * __uint_as_float(r[8 * k + 0]), inv * __uint_as_float(r[8 * k + 1]));
-              w.y = pack_bf16(inv * __uint_as_float(r[8 * k + 2]), inv * __uint_as_float(r[8 * k + 3]));
-              w.z = pack_bf16(inv * __uint_as_float(r[8 * k + 4]), inv * __uint_as_float(r[8 * k + 5]));
-              w.w = pack_bf16(inv * __uint_as_float(r[8 * k + 6]), inv * __uint_as_float(r[8 * k + 7]));
-              *reinterpret_cast<uint4 *>(orow + c0 + 8 * k) = w;
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack_bf16(inv * __uint_as_float(r[16 * k + 2 * e]), inv * __uint_as_float(r[16 * k + 2 * e + 1]));
+              st_32b(orow + c0 + 16 * k, w, p.wide);
             }
           }
         }

@@ -165,6 +165,37 @@ def test_against_the_dense_attention():
     assert (lse.reshape(H, B, S).transpose(0, 1) - lse_).abs().max() <= 1e-4
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_at_odd_multiples_of_16_bytes(D):
+    # the same bits as with rows at multiples of 32 bytes, and nothing written beside the rows; few K/V heads of a
+    # long sequence, whose dK and dV are summed in parts
+    lens, hq, hkv = [2500, 3], 4, 1
+    q, k, v, do = problem(lens, hq, hkv, D, seed=83)
+    plan = dash.PackedPlan(lens, hq, hkv, D, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    want = (o, *dash.attn_packed_bwd(plan, q, k, v, o, do, lse))
+
+    def odd(t):
+        big = torch.full((t.shape[0], t.shape[1] * D + 24), 7.0, dtype=t.dtype, device="cuda")
+        part = big[:, 8:8 + t.shape[1] * D].unflatten(1, t.shape[1:])
+        assert part.data_ptr() % 32 == 16 and part.stride(0) % 16 == 8
+        part.copy_(t)
+        return big, part
+
+    (_, o2), (_, do2), (_, q2), (_, k2), (_, v2) = (odd(t) for t in (o, do, q, k, v))
+    outs = [odd(torch.zeros_like(t)) for t in want]
+    lse2 = torch.empty_like(lse)
+    ws = torch.empty(plan.workspace_bytes + 16, dtype=torch.uint8, device="cuda")[16:]
+    scale = 1 / math.sqrt(D)
+    dash.dash_attn_packed_fwd(plan, q2, k2, v2, outs[0][1], lse2, scale)
+    dash.dash_attn_packed_bwd(plan, q2, k2, v2, o2, do2, lse, *(t for _, t in outs[1:]), scale, ws)
+    dash.dash_sync_status()
+    assert torch.equal(lse, lse2)
+    for w, (big, got) in zip(want, outs):
+        assert torch.equal(w, got)
+        assert (big[:, :8] == 7).all() and (big[:, 8 + got.shape[1] * D:] == 7).all()
+
+
 def test_streams_and_captured_graphs():
     lens, hq, hkv, D = [300, 77], 4, 2, 64
     q, k, v, do = problem(lens, hq, hkv, D, seed=81)
