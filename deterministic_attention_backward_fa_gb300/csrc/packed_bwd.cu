@@ -7,9 +7,9 @@
 //   dS = P (dO V^T - delta),
 //   dQ = scale dS K,   dK = scale sum_heads dS^T Q,   dV = sum_heads P^T dO.
 //
-// Two kernels (and a third that adds up parts), each with its own P and dS: dQ walks the KV tiles of a Q tile,
-// dK/dV the Q tiles (of every Q head of the group) of a KV tile.  That makes
-// seven products of 128 x 128 x D a tile pair where one kernel for all three
+// Two kernels (and a third that adds up parts), each with its own P and dS: dQ
+// walks the KV tiles of a Q tile, dK/dV the Q tiles (of every Q head of the
+// group) of a KV tile.  That makes seven products of 128 x 128 x D a tile pair where one kernel for all three
 // gradients makes five, but nothing crosses a CTA: no 32-bit dQ accumulator in
 // memory, no order to enforce between CTAs, no wait of one CTA for another, and
 // dQ's place in tensor memory lets the products run under the softmax.  The
@@ -21,9 +21,8 @@
 // the next tile's (waits, exponentials), and at D = 64 the exponentials' and
 // the conversions' latency in sixteen warps.
 //
-// Warps of both kernels: the first turn scores into P and dS (eight for dQ,
-// sixteen for dK and dV; a thread owns columns of a row of the accumulator),
-// then X, Y and Z, which issue the MMAs, one that loads, and four that write the
+// Warps of both kernels: sixteen turn scores into P and dS (a thread owns 32
+// columns of a row of the accumulator), then X, Y and Z, which issue the MMAs, one that loads, and four that write the
 // last item's results, clear rows past a sequence's end that a product sums over
 // and, for dQ, make the next item's delta.  Several warps issue, because a wait
 // answers about 100 clocks after the MMAs in front of it, which another warp's
@@ -42,12 +41,12 @@ using namespace dev;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kRegsLaunch = 128;  // 512 threads x 128 registers
-constexpr int kRegsSoft = 168;
-constexpr int kRegsOther = 72;
-constexpr int kRegsOut = 104;     // a packed row of an accumulator, or the rows that make delta
-static_assert(2 * kRegsSoft + kRegsOther + kRegsOut <= 4 * kRegsLaunch, "register split exceeds the CTA's allocation");
+constexpr int kSoft = 16;                // softmax warps
+constexpr int kThreads = (kSoft + 8) * 32;
+constexpr int kCols = 128 / (kSoft / 4);  // columns of a softmax thread
+constexpr int kRegsLaunch = 80, kRegsSoft = 88, kRegsOther = 64, kRegsOut = 64;
+static_assert(kCols == 32 && kRegsSoft * kSoft / 4 + kRegsOther + kRegsOut <= kRegsLaunch * (kSoft + 8) / 4,
+              "register split exceeds the CTA's allocation");
 
 __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
   uint64_t r;
@@ -107,28 +106,24 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int first, int lane) {
   __syncwarp();
 }
 
-// A row of D accumulator columns, scaled and rounded, in registers: tensor
-// memory is free before the row goes to global memory.
-template <int D>
+// 32 accumulator columns of a row, scaled and rounded, in registers: tensor
+// memory is free before the last of them go to global memory.
 struct OutRow {
-  uint32_t w[D / 2];
+  uint32_t w[16];
   __device__ __forceinline__ void read(uint32_t taddr, float scale) {
+    uint32_t r[32];
+    tmem_ld32(taddr, r);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t r[32];
-      tmem_ld32(taddr + 32 * c, r);
-#pragma unroll
-      for (int e = 0; e < 32; e += 2)
-        w[16 * c + (e >> 1)] = pack_bf16(scale * __uint_as_float(r[e]), scale * __uint_as_float(r[e + 1]));
-    }
+    for (int e = 0; e < 32; e += 2)
+      w[e >> 1] = pack_bf16(scale * __uint_as_float(r[e]), scale * __uint_as_float(r[e + 1]));
   }
   __device__ __forceinline__ void write(__nv_bfloat16 *out, bool wide) const {
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) st_32b(out + 16 * k, w + 8 * k, wide);
+    st_32b(out, w, wide);
+    st_32b(out + 16, w + 8, wide);
   }
 };
 
-// The same row in 32 bits, as one part of a sum.
+// A whole row in 32 bits, as one part of a sum.
 template <int D>
 __device__ __forceinline__ void write_part(uint32_t taddr, float *out, bool wide) {
 #pragma unroll 1
@@ -144,7 +139,6 @@ __device__ __forceinline__ void write_part(uint32_t taddr, float *out, bool wide
 // pack into the first half of their own place, which the same thread has read,
 // so threads of one row never race.  K step kk (16 columns) of the MMA that
 // reads them:
-template <int kCols>
 __device__ __forceinline__ constexpr uint32_t packed_col(int kk) {
   return 16 * kk / kCols * kCols + 16 * kk % kCols / 2;
 }
@@ -201,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = warp_id(), lane = threadIdx.x & 31;
+  const int role = warp - kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 Z, 4-7 delta and the results
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
   float2 *stat = reinterpret_cast<float2 *>(smem + C::oSTAT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
@@ -211,13 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::kBars; ++b)
-      mbar_init(&bars[b], b >= C::bRead && b < C::bDsFull + 2                            ? 8
+      mbar_init(&bars[b], b >= C::bRead && b < C::bDsFull + 2                     ? kSoft
                           : b == C::bOEmpty || b == C::bStat || b == C::bStat + 1 ? 4
                                                                                   : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (role == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -228,14 +223,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
   const int i_begin = p.dq_off[blockIdx.x], i_end = p.dq_off[blockIdx.x + 1];
 
-  if (warp >= 12) {
+  if (role >= 4) {
     // ------------------------------------------------- delta and epilogue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int sub = warp & 3;
-    // A warp makes the stats of its 32 rows: D / 16 lanes of 32 bytes a row, two
-    // rounds of loads.  The rows come from memory (nobody else has read O), so
-    // the item behind asks L2 for them: 18000 clocks an item without that and
-    // with four rounds, longer than a short item takes.
+    // A warp makes the stats of its 32 rows: D / 16 lanes of 32 bytes a row, in
+    // rounds of loads that the registers hold.  The rows come from memory (nobody
+    // else has read O), so the item behind asks L2 for them (128 documents of 128
+    // tokens at D = 128: 75 us in all, 81 without that).
     auto ask = [&](int i) {
       const PackedDqItem it = load_item(p.dq_items + i);
       const int r = sub * 32 + lane;
@@ -252,24 +247,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto make_stats = [&](int i) {
       const PackedDqItem it = load_item(p.dq_items + i);
-      constexpr int kLanes = D / 16, kRows = 32 / kLanes, kU = 16 / kRows;
+      constexpr int kLanes = D / 16, kRows = 32 / kLanes, kU = 2, kRound = kRows * kU;
       const int li = lane % kLanes, rs = lane / kLanes;
-      float2 *out = stat + (i & 1) * 128;
-      float *gout = p.stats + ((size_t)it.head * p.n_tiles + it.tile) * 256;
-      const __nv_bfloat16 *o = p.o + it.row0 * p.o_row + it.head * p.o_head + li * 16;
-      const __nv_bfloat16 *d = p.dout + it.row0 * p.do_row + it.head * p.do_head + li * 16;
-      const int mine = sub * 32 + lane;
+      const int mine = sub * 32 + lane, first = sub * 32 + rs;
+      const __nv_bfloat16 *o = p.o + (it.row0 + first) * p.o_row + it.head * p.o_head + li * 16;
+      const __nv_bfloat16 *d = p.dout + (it.row0 + first) * p.do_row + it.head * p.do_head + li * 16;
       float nl = __int_as_float(0xff800000), nd = 0.f;  // of this lane's row
       if (mine < it.rows) nl = -p.lse[it.head * p.lse_head + it.row0 + mine] * 1.4426950408889634f;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
+      for (int row = 0; row < 32; row += kRound, o += kRound * p.o_row, d += kRound * p.do_row) {
         uint32_t a[kU][8], b[kU][8];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int r = sub * 32 + half * 16 + u * kRows + rs;
-          if (r < it.rows) {
-            ld_32b(o + r * p.o_row, a[u], p.wide_in);
-            ld_32b(d + r * p.do_row, b[u], p.wide_in);
+          if (first + row + u * kRows < it.rows) {
+            ld_32b(o + u * kRows * p.o_row, a[u], p.wide_in);
+            ld_32b(d + u * kRows * p.do_row, b[u], p.wide_in);
           } else {
 #pragma unroll
             for (int x = 0; x < 8; ++x) a[u][x] = b[u][x] = 0u;
@@ -289,14 +281,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
           // every lane of a row has its sum: hand it to the lane that keeps the row
-          const int at = lane - half * 16 - u * kRows;
+          const int at = lane - row - u * kRows;
           const float got = __shfl_sync(0xffffffffu, sum, (at & (kRows - 1)) * kLanes);
           if (at >= 0 && at < kRows) nd = -got;
         }
       }
-      out[mine] = make_float2(nl, nd);
-      gout[mine] = nl;
-      gout[128 + mine] = nd;
+      stat[(i & 1) * 128 + mine] = make_float2(nl, nd);
+      float *out = p.stats + ((size_t)it.head * p.n_tiles + it.tile) * 256;
+      out[mine] = nl;
+      out[128 + mine] = nd;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[C::bStat + (i & 1)]);
     };
@@ -325,21 +318,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       ph ^= 1;
       __syncwarp();
       tc_fence_after();
-      OutRow<D> out;
-      out.read(tq, p.scale);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
-      if (ok && L < it.rows) out.write(p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head, p.wide_dq);
-      __syncwarp();
+      ok &= L < it.rows;
+      __nv_bfloat16 *to = p.dq + ((long long)it.row0 + L) * p.dq_row + it.head * p.dq_head;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        OutRow out;
+        out.read(tq + c, p.scale);
+        if (c + 32 == D) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+        }
+        if (ok) out.write(to + c, p.wide_dq);
+        __syncwarp();
+      }
     }
-  } else if (warp >= 8) {
+  } else if (role >= 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     uint32_t lead = elect_one();
     auto wait = [&](int bar, uint32_t ph) {
       if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
     };
-    if (warp == 10 && lane == 0) {
+    if (role == 2 && lane == 0) {
       // -------------------------------------------------------------- TMA
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmK);
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain(C::bDOFull, ndo, C::kQ);
       drain(C::bKFull, nk, C::kK);
       drain(C::bVFull, nv, C::kV);
-    } else if (warp == 8) {
+    } else if (role == 0) {
       // ------------------------------------------------------- X: dP
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       const uint64_t ddo0 = sw128_desc(smem_u32(smem + C::oDO), 16, 1024);
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every MMA has completed before tensor memory is released (at once if none was issued)
       tc_commit_if(elect_one(), &bars[C::bFinalX]);
       mbar_drain(&bars[C::bFinalX], 0, g.limit_ns);
-    } else if (warp == 9) {
+    } else if (role == 1) {
       // ------------------------------------------------------- Y: dQ
       constexpr uint32_t idQ = idesc_bf16(128, D, 0, 1);
       const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oK), C::kPanel, 1024);
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t dk = dk0 + ((rk.st * C::kBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts_if(lead, tmem + C::cDQ, tmem + buf * 128 + packed_col<64>(kk), dk + ((kk * 2048) >> 4), idQ,
+            mma_ts_if(lead, tmem + C::cDQ, tmem + buf * 128 + packed_col(kk), dk + ((kk * 2048) >> 4), idQ,
                       (j > 0 || kk > 0) ? 1u : 0u);
           tc_commit_if(lead, &bars[C::bSEmpty + buf]);
           tc_commit_if(lead, &bars[C::bKEmpty + rk.st]);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_commit_if(elect_one(), &bars[C::bFinalY]);
       mbar_drain(&bars[C::bFinalY], 0, g.limit_ns);
-    } else if (warp == 11) {
+    } else if (role == 3) {
       // ------------------------------------- Z: S, from one item into the next
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       const uint64_t dq0 = sw128_desc(smem_u32(smem + C::oQ), 16, 1024);
@@ -494,78 +494,80 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------- dS
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int sub = warp & 3, half = warp >> 2;
+    const int sub = warp & 3, c0 = (warp >> 2) * kCols;  // its columns of S and dP
     const int L = sub * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + 64 * half;
+    const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + c0;
     const uint64_t sc2 = dup2(p.scale_log2);
-    uint32_t s_ph = 0, dp_ph = 0, buf = 0, st_ph = 0;  // st_ph: a bit per stats buffer
+    uint32_t n = 0;       // tiles before this one; its parities give the buffers and the phases
+    uint32_t st_ph = 0;   // a bit per stats buffer
     for (int i = i_begin; i < i_end; ++i) {
       const PackedDqItem it = load_item(p.dq_items + i);
       mbar_wait(&bars[C::bStat + (i & 1)], (st_ph >> (i & 1)) & 1, g);
       st_ph ^= 1u << (i & 1);
       const float2 ls = stat[(i & 1) * 128 + L];
       const uint64_t nl2 = dup2(ls.x), nd2 = dup2(ls.y);
-      const int limit = p.causal ? min(it.kv_len, it.q0 + L + 1) : it.kv_len;
-      for (int j = 0; j < it.nkv; ++j) {
-        mbar_wait(&bars[C::bSFull + buf], s_ph, g);
-        mbar_wait(&bars[C::bDpFull], dp_ph, g);
-        s_ph ^= buf;
-        dp_ph ^= 1;
+      // the columns of this thread that are valid, counted on through the tiles
+      int cols = (p.causal ? min(it.kv_len, it.q0 + L + 1) : it.kv_len) - c0;
+      for (int left = it.nkv; left > 0; --left, ++n, cols -= kPackedTile) {
+        const uint32_t buf = n & 1;
+        mbar_wait(&bars[C::bSFull + buf], n >> 1 & 1, g);
+        mbar_wait(&bars[C::bDpFull], n & 1, g);
         __syncwarp();
         tc_fence_after();
-        uint32_t x[2][32], y[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tl + buf * 128 + 32 * c, x[c]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(tl + C::cDP + 32 * c, y[c]);
+        uint32_t x[32], y[32];
+        tmem_ld32_nowait(tl + buf * 128, x);
+        tmem_ld32_nowait(tl + C::cDP, y);
         tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          reg_order32(x[c]);
-          reg_order32(y[c]);
-        }
+        reg_order32(x);
+        reg_order32(y);
         tc_fence_before();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float a, b;
+          unpack2(fma2(pack2(x[e], x[e + 1]), sc2, nl2), a, b);
+          x[e] = __float_as_uint(ex2(a));
+          x[e + 1] = __float_as_uint(ex2(b));
+        }
+        auto make_ds = [&](int from) {
+#pragma unroll
+          for (int e = from; e < from + 16; e += 2) {
+            float a, b;
+            unpack2(mul2(pack2(x[e], x[e + 1]), add2(pack2(y[e], y[e + 1]), nd2)), a, b);
+            y[e] = __float_as_uint(a);
+            y[e + 1] = __float_as_uint(b);
+          }
+        };
+        make_ds(0);
+        // S and dP have been in registers for long, but X is told now: the next dP
+        // then starts shortly before dQ, not in the middle of the exponentials
+        // (16384 tokens, 16 heads on 4: 861 us against 930 at D = 128, 594
+        // against 642 at D = 64; behind the rounding it is too late, 1058 and
+        // 750).  The registers pass through the statements in this order.
+        reg_order32(x);
+        reg_order32(y);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[C::bRead]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float a, b;
-            unpack2(fma2(pack2(x[c][e], x[c][e + 1]), sc2, nl2), a, b);
-            const uint64_t p2 = pack2(__float_as_uint(ex2(a)), __float_as_uint(ex2(b)));
-            unpack2(mul2(p2, add2(pack2(y[c][e], y[c][e + 1]), nd2)), a, b);
-            y[c][e] = __float_as_uint(a);
-            y[c][e + 1] = __float_as_uint(b);
-          }
-        const int cols = limit - j * kPackedTile - 64 * half;  // valid columns of this half
-        if (__any_sync(0xffffffffu, cols < 64)) {
+        make_ds(16);
+        if (__any_sync(0xffffffffu, cols < kCols)) {
           // selected, not multiplied: dP there may come from rows of another sequence
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= cols) y[c][e] = 0u;
+          for (int e = 0; e < 32; ++e)
+            if (e >= cols) y[e] = 0u;
         }
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            pk[e >> 1] = pack_bf16(__uint_as_float(y[c][e]), __uint_as_float(y[c][e + 1]));
-          tmem_st16(tl + buf * 128 + 16 * c, pk);
-        }
+        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack_bf16(__uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+        tmem_st16(tl + buf * 128, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[C::bDsFull + buf]);
-        buf ^= 1;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (role == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -603,24 +605,20 @@ struct DkvCfg : Tile<D> {
   };
   static constexpr uint32_t oMISC = oBAR + kBars * 8;
   static constexpr uint32_t kSmem = oMISC + 16;
-  static constexpr int kSoft = 16, kCols = 128 / (kSoft / 4);  // softmax warps, columns of a thread
-  static constexpr int kThreads = (kSoft + 8) * 32;
-  static constexpr int kRegsLaunch = 80, kRegsSoft = 88, kRegsOther = 64, kRegsOut = 64;
-  static_assert(kRegsSoft * kSoft / 4 + kRegsOther + kRegsOut <= kRegsLaunch * (kSoft + 8) / 4, "register split");
   static constexpr uint32_t cDP = 128 * kS, cDV = cDP + 128, cDK = cDV + D;
   static_assert(cDK + D <= 512, "tensor memory");
 };
 static_assert(DkvCfg<128>::kSmem <= 232448 && DkvCfg<64>::kSmem <= 232448, "shared memory of one CTA");
 
 template <int D>
-__global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     dash_packed_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                            const PackedBwdParams p) {
   using C = DkvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = warp_id(), lane = threadIdx.x & 31;
-  const int role = warp - C::kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 Z, 4-7 write the results
+  const int role = warp - kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 Z, 4-7 write the results
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
@@ -633,7 +631,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       const bool turn = (b >= C::bPFull && b < C::bDpFull) || b == C::bDsFull;
       const bool soft = turn || b >= C::bStEmpty;
       const bool both = b >= C::bDOEmpty && b < C::bDOEmpty + C::kDO;  // X's dV and Y's dP have read it
-      mbar_init(&bars[b], soft ? C::kSoft + (turn && C::kTurns ? 1 : 0) : b == C::bOEmpty ? 4 : both ? 2 : 1);
+      mbar_init(&bars[b], soft ? kSoft + (turn && C::kTurns ? 1 : 0) : b == C::bOEmpty ? 4 : both ? 2 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
 
   if (role >= 4) {
     // ---------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOut));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     const int sub = warp & 3, L = sub * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
     uint32_t ph = 0, tail_ph = 0;
@@ -683,7 +681,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       auto write = [&](uint32_t taddr, float scale, __nv_bfloat16 *to, bool last) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          OutRow<32> out;
+          OutRow out;
           out.read(taddr + c, scale);
           if (last && c + 32 == D) {
             tc_fence_before();
@@ -707,7 +705,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       write(tl + C::cDK, p.scale, p.dk + row * p.dk_row + it.head * p.dk_head, true);
     }
   } else if (role >= 0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     uint32_t lead = elect_one();
     auto wait = [&](int bar, uint32_t ph) {
       if (!mbar_wait(&bars[bar], ph, g)) lead = 0;
@@ -825,7 +823,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             if (C::kTurns && !more && kk == 6 && lead) mbar_arrive(&bars[C::bDsFull]);
-            mma_ts_if(lead, tmem + C::cDV, tmem + buf * 128 + packed_col<C::kCols>(kk), ddo + ((kk * 2048) >> 4), idV,
+            mma_ts_if(lead, tmem + C::cDV, tmem + buf * 128 + packed_col(kk), ddo + ((kk * 2048) >> 4), idV,
                       (t > 0 || kk > 0) ? 1u : 0u);
           }
           if (!C::kTurns) tc_commit_if(lead, &bars[C::bSEmpty + buf]);
@@ -893,7 +891,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
           const uint64_t dq = dq0 + ((rq.st * C::kBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts_if(lead, tmem + C::cDK, tmem + C::cDP + packed_col<C::kCols>(kk), dq + ((kk * 2048) >> 4), idK,
+            mma_ts_if(lead, tmem + C::cDK, tmem + C::cDP + packed_col(kk), dq + ((kk * 2048) >> 4), idK,
                       (t > 0 || kk > 0) ? 1u : 0u);
           tc_commit_if(lead, &bars[C::bQEmpty + rq.st]);
           rq.next();
@@ -937,9 +935,10 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
     }
   } else {
     // -------------------------------------------------------- P and dS
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
-    const int sub = warp & 3, c0 = (warp >> 2) * C::kCols;  // its columns of S^T and dP^T
-    const int L = sub * 32 + lane;  // KV row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int sub = warp & 3, c0 = (warp >> 2) * kCols;  // its columns of S^T and dP^T
+    const int before = sub * 32 + lane - c0;  // of its columns, those ahead of its KV row
+    const uint8_t *stats = smem + C::oSTAT + c0 * 4;
     const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16) + c0, tP = tl + C::cDP;
     const uint64_t sc2 = dup2(p.scale_log2);
     Ring<C::kSt> rs;
@@ -948,13 +947,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
       const PackedDkvItem it = load_item(p.dkv_items + i);
       const int per = p.causal ? it.n - it.kv : it.n, total = it.t1 - it.t0;
       int k = it.t0 % per;
+      const int last = it.seq_len - (it.n - 1) * kPackedTile - c0;
       for (int t = 0; t < total; ++t) {
         // a causal KV tile's first Q tile of each head is on the diagonal
         const bool diagonal = p.causal && k == 0;
         k = k + 1 == per ? 0 : k + 1;
         // those inside the sequence: fewer in the head's last tile only
-        const int cols = k == 0 ? it.seq_len - (it.n - 1) * kPackedTile - c0 : C::kCols;
-        const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(smem + C::oSTAT + rs.st * 1024 + c0 * 4);
+        const int cols = k == 0 ? last : kCols;
+        const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(stats + rs.st * 1024);
         const ulonglong2 *nd = nl + 32;
         mbar_wait(&bars[C::bStFull + rs.st], rs.ph, g);
         mbar_wait(&bars[C::bSFull + buf], s_ph, g);
@@ -963,14 +963,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
         s_ph ^= buf == 0;
         __syncwarp();
         tc_fence_after();
-        uint32_t x[C::kCols / 32][32];
+        uint32_t x[kCols / 32][32];
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
+        for (int c = 0; c < kCols / 32; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) reg_order32(x[c]);
+        for (int c = 0; c < kCols / 32; ++c) reg_order32(x[c]);
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c)
+        for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 l4 = nl[8 * c + (e >> 2)];
@@ -984,20 +984,20 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
           }
         if (diagonal) {
 #pragma unroll
-          for (int c = 0; c < C::kCols / 32; ++c)
+          for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (c0 + 32 * c + e < L) x[c][e] = 0u;
+              if (32 * c + e < before) x[c][e] = 0u;
         }
-        if (cols < C::kCols) {  // replaced, as dS below: what Q and dO hold there may not be finite
+        if (cols < kCols) {  // replaced, as dS below: what Q and dO hold there may not be finite
 #pragma unroll
-          for (int c = 0; c < C::kCols / 32; ++c)
+          for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (32 * c + e >= cols) x[c][e] = 0u;
         }
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) {
+        for (int c = 0; c < kCols / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
@@ -1013,14 +1013,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
         dp_ph ^= 1;
         __syncwarp();
         tc_fence_after();
-        uint32_t y[C::kCols / 32][32];
+        uint32_t y[kCols / 32][32];
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) tmem_ld32_nowait(tP + 32 * c, y[c]);
+        for (int c = 0; c < kCols / 32; ++c) tmem_ld32_nowait(tP + 32 * c, y[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) reg_order32(y[c]);
+        for (int c = 0; c < kCols / 32; ++c) reg_order32(y[c]);
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) {
+        for (int c = 0; c < kCols / 32; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::kThreads, 1)
             pk[e >> 1] = pack_bf16(a, b);
             pk[(e >> 1) + 1] = pack_bf16(u, v);
           }
-          if (cols < C::kCols) {
+          if (cols < kCols) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               if (32 * c + e >= cols) pk[e >> 1] = 0u;
@@ -1105,7 +1105,7 @@ cudaError_t prepare_kernel(K kernel, int smem, int regs) {
 template <int D>
 cudaError_t prepare_t() {
   cudaError_t e = prepare_kernel(dash_packed_dq_kernel<D>, smem_bytes<DqCfg<D>>(), kRegsLaunch);
-  return e == cudaSuccess ? prepare_kernel(dash_packed_dkv_kernel<D>, smem_bytes<DkvCfg<D>>(), DkvCfg<D>::kRegsLaunch) : e;
+  return e == cudaSuccess ? prepare_kernel(dash_packed_dkv_kernel<D>, smem_bytes<DkvCfg<D>>(), kRegsLaunch) : e;
 }
 
 template <int D>
@@ -1114,7 +1114,7 @@ cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorM
   dash_packed_dq_kernel<D><<<dq_ctas, kThreads, smem_bytes<DqCfg<D>>(), stream>>>(q, k, v, dout, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dash_packed_dkv_kernel<D><<<dkv_ctas, DkvCfg<D>::kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
+  dash_packed_dkv_kernel<D><<<dkv_ctas, kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
   if (p.n_sums) dash_packed_sum<D><<<dim3(p.n_sums, 2, 4), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
