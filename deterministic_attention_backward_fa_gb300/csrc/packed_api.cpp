@@ -243,10 +243,9 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
       if (bytes) std::memcpy(host.data() + at, src, bytes);
       return at;
     };
-    const size_t at[7] = {put(t.fwd.data(), t.fwd.size() * sizeof(t.fwd[0])), put(t.fwd_off.data(), t.fwd_off.size() * 4),
-                          put(t.dq.data(), t.dq.size() * sizeof(t.dq[0])),    put(t.dq_off.data(), t.dq_off.size() * 4),
-                          put(t.dkv.data(), t.dkv.size() * sizeof(t.dkv[0])), put(t.dkv_off.data(), t.dkv_off.size() * 4),
-                          put(t.sums.data(), t.sums.size() * sizeof(t.sums[0]))};
+    auto table = [&](const auto &v) { return put(v.data(), v.size() * sizeof(v[0])); };
+    const size_t at[7] = {table(t.fwd), table(t.fwd_off), table(t.dq),  table(t.dq_off),
+                          table(t.dkv), table(t.dkv_off), table(t.sums)};
     if ((e = cudaMalloc(&p->mem, host.size())) != cudaSuccess)
       return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", host.size(), cudaGetErrorString(e));
     // pageable memory: cudaMemcpy may return with the copy's last step on its way, and the streams that use the
@@ -335,8 +334,10 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
   if ((st = check_words(lse, "lse")) != DASH_OK) return st;
   const int D = plan->D;
   Rows rq, rk, rv, ro;
-  if ((st = rows_of(strides, 0, rows, plan->Hq, D, "q", &rq)) || (st = rows_of(strides, 1, rows, plan->Hkv, D, "k", &rk)) ||
-      (st = rows_of(strides, 2, rows, plan->Hkv, D, "v", &rv)) || (st = rows_of(strides, 3, rows, plan->Hq, D, "o", &ro)))
+  if ((st = rows_of(strides, 0, rows, plan->Hq, D, "q", &rq)) ||
+      (st = rows_of(strides, 1, rows, plan->Hkv, D, "k", &rk)) ||
+      (st = rows_of(strides, 2, rows, plan->Hkv, D, "v", &rv)) ||
+      (st = rows_of(strides, 3, rows, plan->Hq, D, "o", &ro)))
     return st;
   CUtensorMap mq, mk, mv;
   if ((st = dash::encode_rows_map(&mq, q, plan->Hq, rows, D, rq.row, rq.head, dash::kPackedTile)) ||

@@ -205,8 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 2; ++k) {
               uint32_t w[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                w[e] = pack_bf16(inv * __uint_as_float(r[16 * k + 2 * e]), inv * __uint_as_float(r[16 * k + 2 * e + 1]));
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t *a = r + 16 * k + 2 * e;
+                w[e] = pack_bf16(inv * __uint_as_float(a[0]), inv * __uint_as_float(a[1]));
+              }
               st_32b(orow + c0 + 16 * k, w, p.wide);
             }
           }

@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
           p.lse[(size_t)b * p.Hq + h] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
       } else {
         const size_t at = ((size_t)b * p.Hq + h) * p.max_splits + split;
-        *reinterpret_cast<float4 *>(p.part_o + at * D + c) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        *reinterpret_cast<float4 *>(p.part_o + at * D + c) =
+            make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
         if (c == 0) p.part_ml[at] = make_float2(mm, ll);
       }
     }
