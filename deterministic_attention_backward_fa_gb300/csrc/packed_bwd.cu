@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = warp_id(), lane = threadIdx.x & 31;
   const int role = warp - kSoft;  // below 0: softmax; 0 X, 1 Y, 2 loads, 3 Z, 4-7 delta and the results
+  // dK/dV's CTAs may take the SMs that this kernel leaves; they wait for its end before they read the stats
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
   float2 *stat = reinterpret_cast<float2 *>(smem + C::oSTAT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
@@ -736,6 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = it.seq_row0 + q * kPackedTile;
           if (t == it.t0) nk += load(C::bKFull, C::bKEmpty, e_ph ^ 1, C::oK, &tmK, it.row0, it.head);
           nq += load(C::bQFull + rq.st, C::bQEmpty + rq.st, rq.ph, C::oQ + rq.st * C::kBytes, &tmQ, row, head);
+          if (i == i_begin && t == it.t0) {  // every CTA has an item, so this grid ends behind dQ's
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+          }
           live = live && mbar_wait(&bars[C::bStEmpty + rs.st], rs.ph ^ 1, g);
           if (live) {
             mbar_arrive_expect_tx(&bars[C::bStFull + rs.st], 1024);
@@ -1112,9 +1118,20 @@ template <int D>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const CUtensorMap &dout,
                      const PackedBwdParams &p, int dq_ctas, int dkv_ctas, cudaStream_t stream) {
   dash_packed_dq_kernel<D><<<dq_ctas, kThreads, smem_bytes<DqCfg<D>>(), stream>>>(q, k, v, dout, p);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dash_packed_dkv_kernel<D><<<dkv_ctas, kThreads, smem_bytes<DkvCfg<D>>(), stream>>>(q, k, v, dout, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(dkv_ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<DkvCfg<D>>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, dash_packed_dkv_kernel<D>, q, k, v, dout, p);
+  if (e != cudaSuccess) return e;
   if (p.n_sums) dash_packed_sum<D><<<dim3(p.n_sums, 2, 4), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
