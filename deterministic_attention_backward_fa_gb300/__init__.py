@@ -425,8 +425,8 @@ def dash_die_map(max_sm: int = 1023, stream=None):
 # ---- packed, grouped-head attention and the paged cache
 def _stream_on(device, stream):
     """The raw stream to run on: the given one, or ``device``'s current one."""
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+    if stream is None:  # without the Stream object that torch.cuda.current_stream makes: 0.1 us a call against 2
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, not to {device}")
     return stream.cuda_stream
@@ -455,7 +455,8 @@ def _rows(name, t, heads, dim, rows, device):
 
 def _plain(name, t, dtype, shape, device):
     """A contiguous CUDA tensor of the given type and shape (None: any extent)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+    if t.dtype != dtype or (t.shape != shape and (
+            len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)))):
         raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous on {device}")
