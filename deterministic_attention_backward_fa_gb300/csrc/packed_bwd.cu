@@ -601,7 +601,7 @@ struct DkvCfg : Tile<D> {
   static constexpr uint32_t oBAR = oSTAT + kSt * 1024;
   enum {
     bKFull, bKEmpty, bVFull, bVEmpty, bSFull, bSEmpty = bSFull + kS, bPFull = bSEmpty + kS, bDpFull = bPFull + kS,
-    bDsFull, bDvFull, bDkFull, bOEmpty, bTailQ, bFixedQ, bTailDO, bFixedDO, bFinalX, bFinalY, bFinalZ,
+    bDsFull, bDvFull, bDkFull, bDvEmpty, bDkEmpty, bTailQ, bFixedQ, bTailDO, bFixedDO, bFinalX, bFinalY, bFinalZ,
     bQFull, bQEmpty = bQFull + kQ, bDOFull = bQEmpty + kQ, bDOEmpty = bDOFull + kDO, bStFull = bDOEmpty + kDO,
     bStEmpty = bStFull + kSt, kBars = bStEmpty + kSt
   };
@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool turn = (b >= C::bPFull && b < C::bDpFull) || b == C::bDsFull;
       const bool soft = turn || b >= C::bStEmpty;
       const bool both = b >= C::bDOEmpty && b < C::bDOEmpty + C::kDO;  // X's dV and Y's dP have read it
-      mbar_init(&bars[b], soft ? kSoft + (turn && C::kTurns ? 1 : 0) : b == C::bOEmpty ? 4 : both ? 2 : 1);
+      const int out = b == C::bDvEmpty || b == C::bDkEmpty ? 4 : 1;
+      mbar_init(&bars[b], soft ? kSoft + (turn && C::kTurns ? 1 : 0) : both ? 2 : out);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -673,38 +674,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       loads += it.t1 - it.t0;
-      bool ok = mbar_wait(&bars[C::bDvFull], ph, g);
-      ok &= mbar_wait(&bars[C::bDkFull], ph, g);
-      ph ^= 1;
-      __syncwarp();
-      tc_fence_after();
-      ok &= L < it.rows;
+      // dV is complete before dK, and its place is free for the next item while dK is written
       const long long row = (long long)it.row0 + L;
-      auto write = [&](uint32_t taddr, float scale, __nv_bfloat16 *to, bool last) {
+      float *part = p.parts + (it.slot >= 0 ? (size_t)it.slot * (2 * 128 * D) + L * D : 0);
+#pragma unroll
+      for (int is_k = 0; is_k < 2; ++is_k) {
+        bool ok = mbar_wait(&bars[is_k ? C::bDkFull : C::bDvFull], ph, g);
+        __syncwarp();
+        tc_fence_after();
+        ok &= L < it.rows;
+        const uint32_t acc = tl + (is_k ? C::cDK : C::cDV);
+        uint64_t *empty = &bars[is_k ? C::bDkEmpty : C::bDvEmpty];
+        if (it.slot >= 0) {
+          write_part<D>(acc, part + is_k * 128 * D, p.wide_dkv);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty);
+          continue;
+        }
+        __nv_bfloat16 *to = is_k ? p.dk + row * p.dk_row + it.head * p.dk_head
+                                 : p.dv + row * p.dv_row + it.head * p.dv_head;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           OutRow out;
-          out.read(taddr + c, scale);
-          if (last && c + 32 == D) {
+          out.read(acc + c, is_k ? p.scale : 1.f);
+          if (c + 32 == D) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
+            if (lane == 0) mbar_arrive(empty);
           }
           if (ok) out.write(to + c, p.wide_dkv);
           __syncwarp();
         }
-      };
-      if (it.slot >= 0) {
-        float *part = p.parts + (size_t)it.slot * (2 * 128 * D) + L * D;
-        write_part<D>(tl + C::cDV, part, p.wide_dkv);
-        write_part<D>(tl + C::cDK, part + 128 * D, p.wide_dkv);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[C::bOEmpty]);
-        continue;
       }
-      write(tl + C::cDV, 1.f, p.dv + row * p.dv_row + it.head * p.dv_head, false);
-      write(tl + C::cDK, p.scale, p.dk + row * p.dk_row + it.head * p.dk_head, true);
+      ph ^= 1;
     }
   } else if (role >= 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           left = left == 1 ? per : left - 1;
           if (t == 0) {  // the item before has been written out
-            wait(C::bOEmpty, o_ph);
+            wait(C::bDvEmpty, o_ph);
             o_ph ^= 1;
           }
           if (C::kTurns && more) wait(C::bQFull + rq.st, rq.ph);
@@ -888,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           left = left == 1 ? per : left - 1;
           if (t == 0) {
-            wait(C::bOEmpty, o_ph);
+            wait(C::bDkEmpty, o_ph);
             o_ph ^= 1;
           }
           wait(C::bDsFull, ds_ph);
