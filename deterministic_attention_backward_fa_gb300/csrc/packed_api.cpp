@@ -436,8 +436,8 @@ long long dash_decode_workspace(int B, int Hq, int D, int page_size, int max_pag
   if (B < 0 || Hq < 1 || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 ||
       (long long)page_size * max_pages > kMaxCached)
     return -1;
-  const long long splits = dash::decode_max_splits(page_size * max_pages);
-  return splits <= 1 ? 0 : (long long)B * Hq * splits * (D * 4 + 8) + 256;
+  const int splits = dash::decode_max_splits(page_size * max_pages);
+  return splits <= 1 || dash::decode_clustered(B, Hq, splits) ? 0 : (long long)B * Hq * splits * (D * 4 + 8) + 256;
 }
 
 dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,

@@ -16,7 +16,9 @@
 // pipe stays far from its limit, while the plain pipe would bound groups of 8).
 // P is rounded to bf16 as the product's operand, with l summed from the same
 // 32-bit values before the rounding.  A second kernel joins the splits of a
-// sequence in their order; calls whose table holds at most one split skip it.
+// sequence in their order; calls whose table holds at most one split skip it,
+// and in small calls the splits of a sequence are a cluster, which joins them
+// through its CTAs' shared memory, with the same bits.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -54,8 +56,53 @@ struct DecCfg {
   static constexpr int kStage = 2 * kTile;
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kSmem = kWarps * kWarpBytes;          // the ring; reused to join the warps
-  static_assert(kSmem >= kWarps * 16 * D * 4 + kWarps * 16 * 8, "the join fits in the ring");
+  static constexpr int oPart = kWarps * 16 * (D * 4 + 8);    // the split's own result, for its cluster
+  static_assert(kSmem >= oPart + 16 * (D * 4 + 8), "the joins fit in the ring");
 };
+
+// How a CTA finds its items.
+enum Deal {
+  kPlain,    // every sequence has max_splits numbers, those it does not need return at once
+  kScan,     // only the splits that a sequence has are numbered
+  kCluster,  // as kPlain, and the splits are a cluster
+};
+
+// The join of a sequence's splits, in one order whoever makes it: weights
+// l 2^(m - max), their sum over the splits in turn, and the weighted rows in
+// kPart sums of every kPart-th split, added in turn.
+template <int D>
+struct Join {
+  static constexpr int kVec = D / 4, kPart = 128 / kVec;  // float4 of a row, sums
+  static __device__ __forceinline__ float weight(float2 ml, float ref) {
+    return ml.y > 0.f ? ml.y * ex2(ml.x - ref) : 0.f;
+  }
+  static __device__ __forceinline__ void add(float4 &o, float w, float4 v) {
+    if (w > 0.f) o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+  }
+  static __device__ __forceinline__ void write(const DecodeParams &p, int b, int h, int c, float4 o, float m, float l) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint2 w;
+    w.x = pack_bf16(o.x * inv, o.y * inv);
+    w.y = pack_bf16(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2 *>(p.o + b * p.o_batch + h * p.o_head + c) = w;
+    if (c == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+};
+
+// Loads from the shared memory of any CTA of the cluster.
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
   const int n = valid ? 16 : 0;  // 0: fills with zeros, reads nothing
@@ -85,7 +132,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, bool kScan>
+template <int D, Deal kDeal>
 __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodeParams p) {
   using C = DecCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -98,24 +145,28 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
   const int per_split = p.Hkv * p.hblocks;
   const int g = lane >> 2, t4 = lane & 3;
 
-  // Items are numbered (sequence, split, K/V head, block of Q heads).  With
-  // kScan only the splits that a sequence has are numbered, and the item's
-  // sequence is found by scanning the splits of kThreads sequences at a time;
-  // `base` and `base_b` remember the block of sequences reached so far.
-  // Without it every sequence has max_splits numbers and those it does not
-  // need return at once.
+  // Items are numbered (sequence, split, K/V head, block of Q heads), the split
+  // last in clusters.  With kScan the item's sequence is found by scanning the
+  // splits of kThreads sequences at a time; `base` and `base_b` remember the
+  // block of sequences reached so far.
   long long base = 0;  // splits before sequence base_b
   int base_b = 0, in_block = -1;
   for (long long item = blockIdx.x;; item += gridDim.x) {
     const long long want = item / per_split;
-    int b = -1, split = 0;
-    if (!kScan) {
+    int b = -1, split = 0, rest = (int)(item - want * per_split);
+    if (kDeal == kCluster) {
+      if (item >= (long long)p.B * p.max_splits * per_split) break;
+      const int group = (int)(item / p.max_splits);
+      b = group / per_split;
+      rest = group - b * per_split;
+      split = (int)item - group * p.max_splits;
+    } else if (kDeal == kPlain) {
       if (want >= (long long)p.B * p.max_splits) break;
       b = (int)(want / p.max_splits);
       split = (int)(want - (long long)b * p.max_splits);
       if (split > 0 && split >= decode_splits(max(0, min(p.lengths[b], p.max_pages * p.page_size)))) continue;
     }
-    while (kScan) {
+    while (kDeal == kScan) {
       if (in_block != base_b) {  // the block's prefix sums
         __syncthreads();
         const int mine = base_b + (int)threadIdx.x;
@@ -156,13 +207,13 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
       base_b += kThreads;
     }
     if (b < 0) break;
-    const int rest = (int)(item - want * per_split);
     const int hk = rest / p.hblocks, hb = rest - hk * p.hblocks;
     const int h0 = hk * p.group + hb * 16, nh = min(16, p.group - hb * 16);
     const int len = max(0, min(p.lengths[b], p.max_pages * p.page_size));
     const int chunk = decode_chunk(len), n_splits = max(1, decode_splits(len));
+    const bool mine = kDeal != kCluster || split < n_splits;  // or the sequence does not have this split of the cluster
     const int begin = split * chunk, end = min(len, begin + chunk);
-    const int steps = (end - begin + kStep - 1) / kStep;
+    const int steps = mine ? (end - begin + kStep - 1) / kStep : 0;
     const int *table = p.table + b * p.table_row;
 
     // Q fragments: rows g and g + 8 of the block's 16 heads
@@ -319,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
     }
     __syncthreads();
     constexpr int kVec = D / 4;  // float4 per row
-    for (int x = threadIdx.x; x < nh * kVec; x += kThreads) {
+    for (int x = threadIdx.x; mine && x < nh * kVec; x += kThreads) {
       const int row = x / kVec, c = (x - row * kVec) * 4;
       float mm = -INFINITY;
 #pragma unroll
@@ -346,12 +397,57 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
         *reinterpret_cast<uint2 *>(p.o + b * p.o_batch + h * p.o_head + c) = w;
         if (c == 0 && p.lse)
           p.lse[(size_t)b * p.Hq + h] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+      } else if (kDeal == kCluster) {
+        float *part = reinterpret_cast<float *>(smem + C::oPart);  // [16][D], then [16] {maximum, sum}
+        *reinterpret_cast<float4 *>(part + row * D + c) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        if (c == 0) reinterpret_cast<float2 *>(part + 16 * D)[row] = make_float2(mm, ll);
       } else {
         const size_t at = ((size_t)b * p.Hq + h) * p.max_splits + split;
         *reinterpret_cast<float4 *>(p.part_o + at * D + c) =
             make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
         if (c == 0) p.part_ml[at] = make_float2(mm, ll);
       }
+    }
+    if (kDeal == kCluster) {
+      if (n_splits > 1) {  // the same in every CTA of the cluster
+        using J = Join<D>;
+        __syncwarp();
+        cluster_sync_all();
+        const float *part = reinterpret_cast<const float *>(smem + C::oPart);
+        const float2 *mls = reinterpret_cast<const float2 *>(part + 16 * D);
+        for (int x = split * kThreads + threadIdx.x; x < nh * kVec; x += p.max_splits * kThreads) {
+          const int row = x / kVec, c = (x - row * kVec) * 4;
+          float2 ml[kMaxCluster];
+          float4 v[kMaxCluster];
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (i < n_splits) {
+              ml[i] = ld_cluster2(mapa_rank(mls + row, i));
+              v[i] = ld_cluster4(mapa_rank(part + row * D + c, i));
+            }
+          }
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i) m = fmaxf(m, ml[i].x);
+          const float ref = m == -INFINITY ? 0.f : m;
+          float4 o[J::kPart] = {};
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i)
+            if (i < n_splits) {
+              const float w = J::weight(ml[i], ref);
+              l += w;
+              J::add(o[i % J::kPart], w, v[i]);
+            }
+#pragma unroll
+          for (int k = 1; k < J::kPart; ++k)
+            o[0] = make_float4(o[0].x + o[k].x, o[0].y + o[k].y, o[0].z + o[k].z, o[0].w + o[k].w);
+          J::write(p, b, h0 + row, c, o[0], m, l);
+        }
+        __syncwarp();
+        cluster_sync_all();  // nobody leaves while its results are read
+      }
+      break;
     }
     __syncthreads();  // the ring is free for the next item
   }
@@ -378,55 +474,53 @@ __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
   for (int i = 0; i < n; ++i) m = fmaxf(m, s_w[i]);
   __syncthreads();
   const float ref = m == -INFINITY ? 0.f : m;
-  s_w[tid] = ml.y > 0.f ? ml.y * ex2(ml.x - ref) : 0.f;
+  using J = Join<D>;
+  s_w[tid] = J::weight(ml, ref);
   __syncthreads();
   float l = 0.f;
   for (int i = 0; i < n; ++i) l += s_w[i];
-  constexpr int kVec = D / 4, kPart = 128 / kVec;  // threads per row of floats, splits in step
-  const int c = tid % kVec, part = tid / kVec;
+  const int c = tid % J::kVec, part = tid / J::kVec;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = part; i < n; i += kPart) {
-    const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (at + i) * D + 4 * c);
-    const float w = s_w[i];
-    if (w > 0.f) {
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
-    }
-  }
+  for (int i = part; i < n; i += J::kPart)
+    J::add(o, s_w[i], *reinterpret_cast<const float4 *>(p.part_o + (at + i) * D + 4 * c));
   s_o[tid] = o;
   __syncthreads();
   if (part == 0) {
 #pragma unroll
-    for (int k = 1; k < kPart; ++k) {
-      const float4 v = s_o[k * kVec + c];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
+    for (int k = 1; k < J::kPart; ++k) {
+      const float4 v = s_o[k * J::kVec + c];
+      o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2 w;
-    w.x = pack_bf16(o.x * inv, o.y * inv);
-    w.y = pack_bf16(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2 *>(p.o + b * p.o_batch + h * p.o_head + 4 * c) = w;
-    if (c == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    J::write(p, b, h, 4 * c, o, m, l);
   }
 }
 
 template <int D>
 cudaError_t launch_decode_t(const DecodeParams &p, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D>;
-  // Two CTAs fit on an SM.  Where they hold every item that the table has room
-  // for, the scan is left out (6.3 us against 7.0 for one sequence of 701
-  // tokens on 4 K/V heads).
   const long long items = (long long)p.B * p.max_splits * p.Hkv * p.hblocks;
+  if (decode_clustered(p.B, p.Hq, p.max_splits)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((int)items);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.max_splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dash_decode_kernel<D, kCluster>, p);
+  }
+  // Two CTAs fit on an SM.  Where they hold every item that the table has room
+  // for, the scan is left out (one sequence of 701 tokens on 4 K/V heads, before
+  // it was a cluster's: 6.3 us against 7.0).
   if (items <= 2LL * num_sms)
-    dash_decode_kernel<D, false><<<(int)items, kThreads, C::kSmem, stream>>>(p);
+    dash_decode_kernel<D, kPlain><<<(int)items, kThreads, C::kSmem, stream>>>(p);
   else
-    dash_decode_kernel<D, true><<<2 * num_sms, kThreads, C::kSmem, stream>>>(p);
+    dash_decode_kernel<D, kScan><<<2 * num_sms, kThreads, C::kSmem, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.max_splits <= 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -554,11 +648,11 @@ void launch_copy_t(const CacheCopyParams &p, const int2 *pairs, int n, cudaStrea
 
 template <int D>
 static cudaError_t prepare_decode_t() {
-  const cudaError_t e = cudaFuncSetAttribute(dash_decode_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             DecCfg<D>::kSmem);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(dash_decode_kernel<D, true>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::kSmem);
+  cudaError_t e = cudaSuccess;
+  for (auto kernel : {dash_decode_kernel<D, kPlain>, dash_decode_kernel<D, kScan>, dash_decode_kernel<D, kCluster>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::kSmem);
+  return e;
 }
 cudaError_t prepare_decode() {
   const cudaError_t e = prepare_decode_t<64>();

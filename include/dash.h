@@ -536,8 +536,8 @@ dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq
  * bits in any batch.  strides (NULL: contiguous), 11 values: q {batch, head},
  * o {batch, head}, k_pages {page, token, head}, v_pages, page_table row.
  * `workspace`: dash_decode_workspace() bytes of device memory, 16-byte
- * aligned, one per call in flight (0 bytes, NULL allowed, when the table has
- * room for one split only).  Can be captured. */
+ * aligned, one per call in flight (0 bytes, NULL allowed, for small calls and
+ * when the table has room for one split only).  Can be captured. */
 dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
                                const int32_t *lengths, void *o, float *lse, int B, int Hq, int Hkv, int D,
                                int n_pages, int page_size, int max_pages, const int64_t *strides, float scale,

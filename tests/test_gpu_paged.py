@@ -93,6 +93,33 @@ def test_decode_beside_the_lengths_where_splits_grow(at, width):
     assert torch.equal(o[:1], one) and torch.equal(lse[:1], l1)
 
 
+@pytest.mark.parametrize("hq,hkv,D,page,width", [(16, 4, 128, 16, 44), (8, 1, 64, 16, 64), (20, 1, 128, 7, 90),
+                                                 (2, 2, 64, 1, 2000), (16, 16, 128, 64, 30), (6, 3, 64, 32, 512)])
+def test_decode_small_calls_join_with_the_same_bits(hq, hkv, D, page, width):
+    # one sequence at a time (its splits are joined in the call's only kernel) and in a batch (by a second one)
+    cap = page * width
+    lens = sorted({0, 1, 255, 256, 257, 512, 513, 777, cap // 2 + 1, cap - 1, cap} & set(range(cap + 1))) * 6
+    kp, vp, table = cache(lens, hkv, D, page, width=width)
+    q = R.normal(15, len(lens), hq, D)
+    o, lse = dash.attn_decode(q, kp, vp, table, i32(lens))
+    dash.dash_sync_status()
+    check(q, kp, vp, table, lens, 1 / math.sqrt(D), o, lse)
+    assert dash.dash_decode_workspace(len(lens), hq, D, page, width) > 0
+    for b, n in enumerate(lens):
+        ob, lb = dash.attn_decode(q[b:b + 1], kp, vp, table[b:b + 1], i32([n]))
+        assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0]), n
+    # captured, its length read when it is replayed
+    if dash.dash_decode_workspace(1, hq, D, page, width) == 0:
+        length, graph = i32([1]), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            og, lg = dash.attn_decode(q[-1:], kp, vp, table[-1:], length)
+        length.copy_(i32(lens[-1:]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(og[0], o[-1]) and torch.equal(lg[0], lse[-1])
+    dash.dash_sync_status()
+
+
 def test_decode_strides_and_lengths_out_of_range():
     lens, hq, hkv, D, page = [100, 700, 31], 8, 2, 64, 16
     kp, vp, table = cache(lens, hkv, D, page)
