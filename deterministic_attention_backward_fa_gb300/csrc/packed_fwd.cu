@@ -461,8 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == 0) {
           m = top == -INFINITY ? 0.f : top;
         } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          // PV(j-1) is complete (with P in S's place it completed before S(j) did), so O may be rewritten here
-          const float m_new = fmaxf(m, top);
+          // PV(j-1) is complete (with P in S's place it completed before S(j) did), so O may be rewritten here.
+          // The vote decides whether the warp does, each row for itself whether it moves (else its factor is 1):
+          // its bits do not depend on the warp's other rows, which may belong to another sequence or to nobody.
+          const float m_new = top > m + kLazy ? top : m;
           const float f = ex2(m - m_new);
           m = m_new;
           const uint64_t f2 = pack2(f, f);

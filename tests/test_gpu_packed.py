@@ -351,3 +351,39 @@ def test_refusals():
     with pytest.raises(dash.DashError, match="workspace"):
         dash.dash_attn_packed_bwd(bp, q, k, v, o, do, lse, torch.empty_like(q), torch.empty_like(k),
                                   torch.empty_like(v), 0.1, ws)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [500, 805])
+def test_large_rows_outside_a_sequence_leave_its_bits(D, causal, n):
+    # A sequence of several KV tiles that ends inside a warp's 32 rows.  The warp also computes the rows behind it,
+    # whose scores here grow from tile to tile by far more than what makes it rescale: those of the next sequence,
+    # then rows behind the last one.
+    hq, hkv, more = 3, 1, 60
+    q, k, v, do = problem([n], hq, hkv, D, seed=131)
+    k = (k.float() * torch.linspace(0.2, 1.0, n, device="cuda")[:, None, None]).bfloat16()
+    plan = dash.PackedPlan([n], hq, hkv, D, causal=causal, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    grads = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    check_forward([n], q, k, v, causal, 1 / math.sqrt(D), o, lse)
+    behind = [torch.cat([t, (R.normal(140 + i, more, t.shape[1], D) * 100).bfloat16()])
+              for i, t in enumerate((q, k, v))]
+    # what the test is about: a row behind the sequence in the same 32 rows whose maximum moves, one inside that does
+    # not but has grown (in powers of two, as far as 2^8)
+    scores = torch.einsum("qhd,kd->hqk", behind[0][:(n + 31) // 32 * 32].float(), k[:, 0].float())
+    scores = scores[:, n // 32 * 32:] / math.sqrt(D) * math.log2(math.e)
+    grown = torch.stack([t.amax(-1) for t in scores.split(128, -1)], -1).diff(dim=-1)
+    assert n % 32 and (grown[:, n % 32:] > 8).any() and ((grown[:, :n % 32] > 0) & (grown[:, :n % 32] < 8)).any()
+    pad = torch.zeros_like(behind[0][n:])
+    for lens in ([n, more], [n]):
+        both = dash.PackedPlan(lens, hq, hkv, D, causal=causal, backward=True)
+        o2, lse2 = dash.attn_packed_fwd(both, *behind)
+        dash.dash_sync_status()
+        assert torch.equal(o, o2[:n]) and torch.equal(lse, lse2[:, :n])
+        g2 = dash.attn_packed_bwd(both, *behind, torch.cat([o, pad]), torch.cat([do, pad + 100]),
+                                  torch.cat([lse, lse2[:, n:]], 1).contiguous())
+        dash.dash_sync_status()
+        assert torch.equal(grads[0], g2[0][:n])
+        if len(lens) == 1:  # dK and dV too: the same lengths
+            assert all(torch.equal(a, b[:n]) for a, b in zip(grads, g2))
