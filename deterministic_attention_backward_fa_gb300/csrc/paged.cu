@@ -67,25 +67,33 @@ enum Deal {
   kCluster,  // as kPlain, and the splits are a cluster
 };
 
+// A row's 1 / l and LSE.  l is 0 for a row that attends nothing (o = 0, LSE =
+// -inf) and NaN where a score is NaN or +inf: the row's results are then NaN, as
+// softmax makes them.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // The join of a sequence's splits, in one order whoever makes it: weights
 // l 2^(m - max), their sum over the splits in turn, and the weighted rows in
-// kPart sums of every kPart-th split, added in turn.
+// kPart sums of every kPart-th split, added in turn.  A split that attends
+// nothing weighs 0 (m = -inf, l = 0) and its row is 0; nothing is left out by a
+// comparison, which would lose a split whose l is NaN.
 template <int D>
 struct Join {
   static constexpr int kVec = D / 4, kPart = 128 / kVec;  // float4 of a row, sums
-  static __device__ __forceinline__ float weight(float2 ml, float ref) {
-    return ml.y > 0.f ? ml.y * ex2(ml.x - ref) : 0.f;
-  }
+  static __device__ __forceinline__ float weight(float2 ml, float ref) { return ml.y * ex2(ml.x - ref); }
   static __device__ __forceinline__ void add(float4 &o, float w, float4 v) {
-    if (w > 0.f) o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+    o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
   }
   static __device__ __forceinline__ void write(const DecodeParams &p, int b, int h, int c, float4 o, float m, float l) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
     uint2 w;
     w.x = pack_bf16(o.x * inv, o.y * inv);
     w.y = pack_bf16(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2 *>(p.o + b * p.o_batch + h * p.o_head + c) = w;
-    if (c == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (c == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = log_sum(m, l);
   }
 };
 
@@ -388,15 +396,14 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
         o[2] += fw * v.z;
         o[3] += fw * v.w;
       }
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      const float inv = inverse_sum(ll);
       const int h = h0 + row;
       if (n_splits == 1) {
         uint2 w;
         w.x = pack_bf16(o[0] * inv, o[1] * inv);
         w.y = pack_bf16(o[2] * inv, o[3] * inv);
         *reinterpret_cast<uint2 *>(p.o + b * p.o_batch + h * p.o_head + c) = w;
-        if (c == 0 && p.lse)
-          p.lse[(size_t)b * p.Hq + h] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        if (c == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = log_sum(mm, ll);
       } else if (kDeal == kCluster) {
         float *part = reinterpret_cast<float *>(smem + C::oPart);  // [16][D], then [16] {maximum, sum}
         *reinterpret_cast<float4 *>(part + row * D + c) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);

@@ -530,10 +530,11 @@ dash_status_t dash_build_packed_items(const int32_t *lengths, int n_seqs, int Hq
 /* Attention of one new token per sequence over its cached tokens: q, o
  * [B][Hq][D], lengths int32 [B] on the device (the tokens to attend, the new
  * one's among them if it was written; values are clipped to [0, max_pages *
- * page_size], which must be below 2^31 - 2^26).  lse, if not NULL, is fp32 [B][Hq].  A sequence of length 0
- * gets o = 0 and lse = -inf.  Long sequences are split and joined; the split
- * depends on the sequence's own length alone, so its results are the same
- * bits in any batch.  strides (NULL: contiguous), 11 values: q {batch, head},
+ * page_size], which must be below 2^31 - 2^26).  lse, if not NULL, is fp32
+ * [B][Hq].  A sequence of length 0 gets o = 0 and lse = -inf, as does a head
+ * whose every score is -inf; a score of NaN or +inf makes its head's row NaN.
+ * Long sequences are split and joined; the split depends on the sequence's own
+ * length alone, so its results are the same bits in any batch.  strides (NULL: contiguous), 11 values: q {batch, head},
  * o {batch, head}, k_pages {page, token, head}, v_pages, page_table row.
  * `workspace`: dash_decode_workspace() bytes of device memory, 16-byte
  * aligned, one per call in flight (0 bytes, NULL allowed, for small calls and

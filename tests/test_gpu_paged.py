@@ -351,3 +351,45 @@ assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(kp[2], kp[3
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n", [200, 2000])
+@pytest.mark.parametrize("form", ["one kernel", "two kernels", "scanned"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_keeps_non_finite_scores(n, form, D):
+    # one cached key of NaN, one that makes a score of +inf, a query of NaN, a value of NaN: the rows that attend them
+    # are NaN, as softmax makes them, and every other row keeps its bits
+    B, hq, hkv = {"one kernel": (1, 4, 2), "two kernels": (1, 128, 2), "scanned": (40, 8, 2)}[form]
+    page, lens = 16, [n] * B
+    kp, vp, table = cache(lens, hkv, D, page, width=2048 // page)
+    assert (dash.dash_decode_workspace(B, hq, D, page, 2048 // page) == 0) == (form == "one kernel")
+    q = R.normal(9, B, hq, D).abs() + 0.1
+    o, lse = dash.attn_decode(q, kp, vp, table, i32(lens))
+    check(q, kp, vp, table, lens, 1 / math.sqrt(D), o, lse)
+    b, head, t = B // 2, 1, n // 2 + 3
+    where = (table[b, t // page].long(), t % page, head)
+    group = slice(head * hq // hkv, (head + 1) * hq // hkv)
+    bad = torch.zeros(B, hq, dtype=torch.bool, device="cuda")
+    bad[b, group] = True
+
+    def others(o2, lse2, wrong):
+        assert torch.equal(o2[~wrong], o[~wrong]) and torch.equal(lse2[~wrong], lse[~wrong])
+
+    for x in (NAN, float("inf")):
+        k2 = kp.clone()
+        k2[where] = x
+        o2, lse2 = dash.attn_decode(q, k2, vp, table, i32(lens))
+        assert o2[bad].isnan().all() and not (lse2[bad] < float("inf")).any()
+        others(o2, lse2, bad)
+    q2, wrong = q.clone(), torch.zeros_like(bad)
+    q2[b, hq - 1], wrong[b, hq - 1] = NAN, True
+    o2, lse2 = dash.attn_decode(q2, kp, vp, table, i32(lens))
+    assert o2[wrong].isnan().all() and lse2[wrong].isnan().all()
+    others(o2, lse2, wrong)
+    v2 = vp.clone()
+    v2[where][5] = NAN
+    o2, lse2 = dash.attn_decode(q, kp, v2, table, i32(lens))
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[b, group, 5] = True
+    assert o2[hit].isnan().all() and torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2, lse)
+    dash.dash_sync_status()
