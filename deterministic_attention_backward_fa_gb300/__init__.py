@@ -89,6 +89,7 @@ _SIGS = {
     "dash_cluster_links": ([_P, _P] + [_I] * 5 + [_P, ctypes.POINTER(ctypes.c_longlong)], _I),
     "dash_packed_plan_create": ([_P] + [_I] * 6 + [ctypes.POINTER(_P)], _I),
     "dash_packed_plan_destroy": ([_P], None),
+    "dash_packed_plan_spin_limit": ([_P, _L], _I),
     "dash_packed_bwd_workspace": ([_P], _L),
     "dash_build_packed_items": ([_P] + [_I] * 6 + [_P, _P, ctypes.POINTER(_I), ctypes.POINTER(_L)], _I),
     "dash_attn_packed_fwd": ([_P] * 6 + [_L, _P, _F, _P], _I),
@@ -475,10 +476,10 @@ class PackedPlan:
     """Tables of one set of sequence lengths (host ints) on a GPU, for ``heads`` Q heads that share ``kv_heads``
     K/V heads: made once per batch, used by every layer's ``attn_packed_fwd`` and, with ``backward=True``,
     ``attn_packed_bwd``.  Read-only once made; keep it while work that uses it (replays of captured graphs
-    included) may still run."""
+    included) may still run.  ``spin_limit_ns`` bounds each device wait (0: 2 s)."""
 
     def __init__(self, lengths, heads: int, kv_heads: int, head_dim: int, causal: bool = True,
-                 backward: bool = False, device=None):
+                 backward: bool = False, device=None, spin_limit_ns: int = 0):
         self._handle = None
         values = lengths.tolist() if hasattr(lengths, "tolist") else list(lengths)
         self.lengths = tuple(int(x) for x in values)
@@ -491,6 +492,7 @@ class PackedPlan:
         with torch.cuda.device(self.device):
             self._handle = dash_packed_plan_create(self.lengths, self.heads, self.kv_heads, self.head_dim,
                                                    self.causal, backward)
+        dash_packed_plan_spin_limit(self._handle, spin_limit_ns)
         self.rows = sum(self.lengths)
         self.workspace_bytes = dash_packed_bwd_workspace(self._handle) if backward else -1
 
@@ -517,6 +519,10 @@ def dash_packed_plan_create(lengths, heads: int, kv_heads: int, head_dim: int, c
 
 def dash_packed_plan_destroy(plan):
     lib().dash_packed_plan_destroy(_handle(plan))
+
+
+def dash_packed_plan_spin_limit(plan, ns: int):
+    _check(lib().dash_packed_plan_spin_limit(_handle(plan), ns))
 
 
 def dash_packed_bwd_workspace(plan) -> int:

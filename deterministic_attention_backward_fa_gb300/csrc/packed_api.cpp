@@ -27,7 +27,9 @@ dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long 
 using dash::report;
 
 // A plan: the tables of one set of lengths on the device it was made on.
+constexpr long long kSpinNs = 2000000000LL;  // 2 s bound on every device wait
 struct dash_packed_plan_st {
+  long long spin_ns = kSpinNs;
   int device = 0, Hq = 0, Hkv = 0, D = 0, causal = 0, n_seqs = 0;
   long long rows = 0, n_tiles = 0;
   int fwd_ctas = 0, dq_ctas = 0, dkv_ctas = 0;
@@ -44,7 +46,6 @@ struct dash_packed_plan_st {
 
 namespace {
 
-constexpr long long kSpinNs = 2000000000LL;  // 2 s bound on every device wait
 constexpr float kLog2e = 1.4426950408889634f;
 
 dash_status_t cuda_error(cudaError_t e, const char *what) {
@@ -288,6 +289,13 @@ void dash_packed_plan_destroy(dash_packed_plan_t *plan) {
   delete plan;
 }
 
+dash_status_t dash_packed_plan_spin_limit(dash_packed_plan_t *plan, long long ns) {
+  if (!plan) return report(DASH_ERR_INVALID_ARG, "null plan");
+  if (ns < 0) return report(DASH_ERR_INVALID_ARG, "the spin limit must be >= 0");
+  plan->spin_ns = ns ? ns : kSpinNs;
+  return DASH_OK;
+}
+
 long long dash_packed_bwd_workspace(const dash_packed_plan_t *plan) {
   if (!plan || !plan->backward) return -1;
   return bwd_bytes(plan);
@@ -356,7 +364,7 @@ dash_status_t dash_attn_packed_fwd(const dash_packed_plan_t *plan, const void *q
   p.scale_log2 = scale * kLog2e;
   p.causal = plan->causal;
   p.wide = wide(o, ro.row, ro.head);
-  p.spin_limit_ns = kSpinNs;
+  p.spin_limit_ns = plan->spin_ns;
   const cudaError_t e =
       dash::launch_packed_fwd(D, mq, mk, mv, p, plan->fwd_ctas, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "packed forward launch");
@@ -426,7 +434,7 @@ dash_status_t dash_attn_packed_bwd(const dash_packed_plan_t *plan, const void *q
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.status = plan->status;
-  p.spin_limit_ns = kSpinNs;
+  p.spin_limit_ns = plan->spin_ns;
   const cudaError_t e = dash::launch_packed_bwd(plan->D, m[0], m[1], m[2], m[3], p, plan->dq_ctas, plan->dkv_ctas,
                                                 reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "packed backward launch");

@@ -650,6 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
   const int i_begin = p.dkv_off[blockIdx.x], i_end = p.dkv_off[blockIdx.x + 1];
+  // Only the first K and Q tiles are asked for before dQ has ended (by the loads' warp, whose waits up to there
+  // are for places that are free).  All others stand here until then, since the waits below are bounded and how
+  // long dQ takes is not: where other work holds some SMs, dQ's last CTAs run a whole share behind the first.
+  if (role != 2 && lane == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncwarp();
 
   if (role >= 4) {
     // ---------------------------------------------------------- epilogue

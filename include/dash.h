@@ -479,6 +479,10 @@ typedef struct dash_packed_plan_st dash_packed_plan_t;
 dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq, int Hkv, int D, int causal,
                                       int backward, dash_packed_plan_t **plan_out);
 void dash_packed_plan_destroy(dash_packed_plan_t *plan);
+/* Bound on each device wait of the calls made with the plan from now on (0 = 2
+ * s, as a new plan has it).  A wait lasts as long as an item of the plan at
+ * most: it never counts the time that a kernel waits for another to end. */
+dash_status_t dash_packed_plan_spin_limit(dash_packed_plan_t *plan, long long ns);
 
 /* Forward: o and lse (as dash_attn_fwd defines them, per sequence).  `rows` is
  * the row count of every tensor, at least the sum of the lengths; strides: q,

@@ -387,3 +387,47 @@ def test_large_rows_outside_a_sequence_leave_its_bits(D, causal, n):
         assert torch.equal(grads[0], g2[0][:n])
         if len(lens) == 1:  # dK and dV too: the same lengths
             assert all(torch.equal(a, b[:n]) for a, b in zip(grads, g2))
+
+
+def test_the_wait_for_dq_is_not_bounded():
+    # Other work holds some SMs, so that dQ's CTAs for them start late and run their share after all others have
+    # ended: dK and dV's CTAs on the freed SMs stand still for longer than any single wait may last, in a run where
+    # nothing is stuck.  The held SMs belong to a dense backward on eight CTAs, which waits for nothing of this.
+    limit_ms = 1
+    lens, hq, hkv, D = [8192] * 16, 16, 4, 128
+    q, k, v, do = problem(lens, hq, hkv, D, seed=151)
+    plan = dash.PackedPlan(lens, hq, hkv, D, backward=True, spin_limit_ns=limit_ms * 10**6)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    want = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    dash.dash_sync_status()
+    x = [R.normal(160 + i, 1, 8, 8192, D) for i in range(4)]
+    xo, xl = dash.attn_fwd(*x[:3], False)
+    grads = [torch.empty_like(x[0]) for _ in range(3)]
+    held = torch.cuda.Stream()
+    event = lambda: torch.cuda.Event(enable_timing=True)
+    main, begin = (event(), event()), event()
+    hold = lambda **kw: dash.dash_attn_bwd_ex(*x[:3], xo, x[3], xl, *grads, False, 1 / math.sqrt(D), "serial",
+                                              num_ctas=8, stream=held, **kw)
+    hold()  # its workspace and tables
+    for e in main:
+        e.record(held)
+
+    def held_for(side, call):
+        torch.cuda.synchronize()
+        hold(main_events=main)
+        side.wait_event(main[0])
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000)  # 0.2 ms: the eight CTAs stand
+            begin.record(side)
+        out = call()
+        torch.cuda.synchronize()
+        return begin.elapsed_time(main[1]), out
+
+    # streams may share a hardware queue, where one waits for the other's kernel to end: one that does not
+    streams = [torch.cuda.Stream(priority=-(i % 2)) for i in range(32)]
+    side = next((s for s in streams if held_for(s, lambda: None)[0] > 2 * limit_ms), None)
+    assert side is not None, "no stream runs beside the other"
+    ms, got = held_for(side, lambda: dash.attn_packed_bwd(plan, q, k, v, o, do, lse, stream=side))
+    assert ms > 2 * limit_ms, "the SMs were not held for long enough"
+    dash.dash_sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

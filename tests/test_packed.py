@@ -188,3 +188,8 @@ def test_plain_backward_against_differences(causal):
         args = lambda s: [t + s * h * d if j == i else t for j, t in enumerate((q, k, v))]
         diff = (loss(*args(1)) - loss(*args(-1))) / (2 * h)
         assert abs(diff - (grads[i] * d).sum()) <= 1e-7 * (1 + abs(diff))
+
+
+def test_refusals_of_a_spin_limit():
+    L, nul = dash.lib(), ctypes.c_void_p(0)
+    assert L.dash_packed_plan_spin_limit(nul, 0) == 1 and "null plan" in dash.dash_last_error()
