@@ -702,6 +702,8 @@ def dash_version() -> int:
 
 
 # ------------------------------------------------------------ conveniences
+# The packed and paged ones take a ``stream`` to run on that waits for what the current stream holds by then; the
+# caller makes the current stream wait for it before it uses the results.  The dash_ forms do not wait.
 @contextlib.contextmanager
 def _side(stream, tensors):
     stream.wait_stream(torch.cuda.current_stream(stream.device))
@@ -796,9 +798,11 @@ def attn_decode(q, k_pages, v_pages, page_table, lengths, scale: float | None = 
 
 def cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=None):
     """Writes new tokens' K and V rows into the pages of their sequences, in place (see dash_cache_write)."""
-    dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream)
+    with _using(stream):
+        dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream)
 
 
 def cache_copy(k_pages, v_pages, src, dst, stream=None):
     """Copies pages ``src`` to pages ``dst`` (host page numbers) inside the cache, in place."""
-    dash_cache_copy(k_pages, v_pages, src, dst, stream)
+    with _using(stream):
+        dash_cache_copy(k_pages, v_pages, src, dst, stream)

@@ -393,3 +393,30 @@ def test_decode_keeps_non_finite_scores(n, form, D):
     hit[b, group, 5] = True
     assert o2[hit].isnan().all() and torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2, lse)
     dash.dash_sync_status()
+
+
+def test_writes_and_copies_on_a_stream_wait_for_the_current_one():
+    # the rows and pages are still being made on the current stream when the calls are
+    hkv, D, page, side = 2, 64, 16, torch.cuda.Stream()
+    kp, vp, table = cache([40], hkv, D, page)
+    new = R.normal(21, 40, 2 * hkv, D)
+    k, v = torch.zeros_like(new[:, :hkv]), torch.zeros_like(new[:, hkv:])
+    pages, free = table[0].tolist(), sorted(set(range(kp.shape[0])) - set(table[0].tolist()))
+    starts, cu = i32([0]), i32([0, 40])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # 10 ms
+    k.copy_(new[:, :hkv])
+    v.copy_(new[:, hkv:])
+    dash.cache_write(k, v, kp, vp, table, starts, cu, stream=side)
+    side.synchronize()
+    at = lambda c: c[table[0].long()].flatten(0, 1)[:40]
+    assert torch.equal(at(kp), new[:, :hkv]) and torch.equal(at(vp), new[:, hkv:])
+    fresh = R.normal(22, 2, page, hkv, D)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    kp[pages[0]].copy_(fresh[0])
+    vp[pages[1]].copy_(fresh[1])
+    dash.cache_copy(kp, vp, pages[:2], free[:2], stream=side)
+    side.synchronize()
+    assert torch.equal(kp[free[0]], fresh[0]) and torch.equal(vp[free[1]], fresh[1])
+    dash.dash_sync_status()
