@@ -715,8 +715,9 @@ def _side(stream, tensors):
 
 
 def _using(stream, *tensors):
-    """Runs torch's own work on ``stream`` if one is given, and tells the allocator that it uses the tensors (made
-    on the current stream, whose work so far it waits for)."""
+    """Runs torch's own work on ``stream`` if one is given, which waits for the current stream's work so far, and
+    tells the allocator that it uses the tensors, inputs and outputs: what the caller drops once the call has
+    returned is not handed out again before the stream has passed."""
     return _HERE if stream is None else _side(stream, tensors)
 
 
@@ -756,7 +757,7 @@ def attn_packed_fwd(plan: PackedPlan, q, k, v, scale: float | None = None, strea
     rows = q.shape[0]
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty((plan.heads, rows), dtype=torch.float32, device=q.device)
-    with _using(stream, o, lse):
+    with _using(stream, q, k, v, o, lse):
         _packed_fwd(plan, q, k, v, o, lse, scale, stream)
         if rows > plan.rows:
             o[plan.rows:].zero_()
@@ -774,7 +775,7 @@ def attn_packed_bwd(plan: PackedPlan, q, k, v, o, do, lse, scale: float | None =
     dk = torch.empty(kv_shape, dtype=q.dtype, device=q.device)
     dv = torch.empty(kv_shape, dtype=q.dtype, device=q.device)
     ws = torch.empty(max(plan.workspace_bytes, 0), dtype=torch.uint8, device=q.device)
-    with _using(stream, dq, dk, dv, ws):
+    with _using(stream, q, k, v, o, do, lse, dq, dk, dv, ws):
         _packed_bwd(plan, q, k, v, o, do, lse, dq, dk, dv, scale, ws, stream)
         if rows > plan.rows:
             for t in (dq, dk, dv):
@@ -791,18 +792,18 @@ def attn_decode(q, k_pages, v_pages, page_table, lengths, scale: float | None = 
     lse = torch.empty((B, heads), dtype=torch.float32, device=q.device)
     need = dash_decode_workspace(B, heads, dim, k_pages.shape[1], page_table.shape[1])
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-    with _using(stream, o, lse, ws):
+    with _using(stream, q, k_pages, v_pages, page_table, lengths, o, lse, ws):
         _decode(q, k_pages, v_pages, page_table, lengths, o, lse, scale, ws, stream)
     return o, lse
 
 
 def cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream=None):
     """Writes new tokens' K and V rows into the pages of their sequences, in place (see dash_cache_write)."""
-    with _using(stream):
+    with _using(stream, k, v, k_pages, v_pages, page_table, starts, cu_new):
         dash_cache_write(k, v, k_pages, v_pages, page_table, starts, cu_new, stream)
 
 
 def cache_copy(k_pages, v_pages, src, dst, stream=None):
     """Copies pages ``src`` to pages ``dst`` (host page numbers) inside the cache, in place."""
-    with _using(stream):
+    with _using(stream, k_pages, v_pages):
         dash_cache_copy(k_pages, v_pages, src, dst, stream)

@@ -420,3 +420,44 @@ def test_writes_and_copies_on_a_stream_wait_for_the_current_one():
     side.synchronize()
     assert torch.equal(kp[free[0]], fresh[0]) and torch.equal(vp[free[1]], fresh[1])
     dash.dash_sync_status()
+
+
+def test_inputs_dropped_after_a_call_on_a_stream():
+    # The caller's inputs go out of scope while the stream that reads them is still busy with other work: their
+    # memory must not be handed to the current stream's next tensors before.
+    hq, hkv, D, page, n, side = 4, 2, 64, 16, 300, torch.cuda.Stream()
+    q, k, v, do = (R.normal(30 + i, n, h, D) for i, h in enumerate((hq, hkv, hkv, hq)))
+    plan = dash.PackedPlan([n], hq, hkv, D, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    kp, vp, table = cache([n], hkv, D, page)
+    one, length, starts, cu = q[:1].clone(), i32([n]), i32([0]), i32([0, n])
+
+    def run(call, *tensors, stream=None):
+        """The call on copies of the tensors, whose memory is overwritten as soon as the allocator gives it out."""
+        copies = [t.clone() for t in tensors]
+        if stream:
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)  # 10 ms
+        got = call(*copies, stream=stream)
+        shapes = [(t.shape, t.dtype) for t in copies]
+        del copies
+        junk = [torch.empty(s, dtype=d, device="cuda").fill_(77) for s, d in shapes for _ in range(2)]
+        torch.cuda.synchronize()
+        del junk
+        return got
+
+    # the pages are copies too, and kept: what is written has to come from the inputs
+    def write(k, v, table, starts, cu, stream):
+        a, b = torch.zeros_like(kp), torch.zeros_like(vp)
+        dash.cache_write(k, v, a, b, table, starts, cu, stream=stream)
+        return a, b
+
+    for call, tensors in ((lambda *t, stream: dash.attn_packed_fwd(plan, *t, stream=stream), (q, k, v)),
+                          (lambda *t, stream: dash.attn_packed_bwd(plan, *t, stream=stream), (q, k, v, o, do, lse)),
+                          (lambda *t, stream: dash.attn_decode(*t, stream=stream), (one, kp, vp, table, length)),
+                          (write, (k, v, table, starts, cu))):
+        want = run(call, *tensors)
+        got = run(call, *tensors, stream=side)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    dash.dash_sync_status()
