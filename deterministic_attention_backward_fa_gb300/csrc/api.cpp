@@ -43,6 +43,7 @@ dash_status_t fail(dash_status_t code, const char *fmt, ...) {
 }
 
 dash_status_t cuda_fail(cudaError_t e, const char *what) {
+  cudaGetLastError();  // taken, or the next launch's check would find it
   return fail(DASH_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

@@ -13,6 +13,36 @@
 
 namespace dash {
 
+#ifdef __CUDACC__
+template <class T>
+struct SameType {
+  using type = T;
+};
+// Launches a kernel and returns the launch's own status.  (What cudaGetLastError
+// returns behind <<<>>> may be the error of an earlier call, of a launch that
+// went through.)
+template <class... P>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                   cudaLaunchAttribute *attr, const typename SameType<P>::type &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = attr ? 1 : 0;
+  void *ptrs[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), ptrs);
+}
+// The kernel may be set up while the one before it runs; it waits for that one's end itself.
+inline cudaLaunchAttribute overlap_attr() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+#endif
+
 constexpr int kPackedTile = 128;  // rows of a Q or KV tile; a sequence's tiles start at its first row
 
 // One unit of the packed forward: up to two 128-row Q tiles that read the same

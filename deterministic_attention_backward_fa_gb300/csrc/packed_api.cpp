@@ -48,7 +48,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A failed call's error stays with the thread until it is taken: left there, a
+// later call's check of its launch would find it.
 dash_status_t cuda_error(cudaError_t e, const char *what) {
+  cudaGetLastError();
   return report(DASH_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -247,8 +250,11 @@ dash_status_t dash_packed_plan_create(const int32_t *lengths, int n_seqs, int Hq
     auto table = [&](const auto &v) { return put(v.data(), v.size() * sizeof(v[0])); };
     const size_t at[7] = {table(t.fwd), table(t.fwd_off), table(t.dq),  table(t.dq_off),
                           table(t.dkv), table(t.dkv_off), table(t.sums)};
-    if ((e = cudaMalloc(&p->mem, host.size())) != cudaSuccess)
-      return report(DASH_ERR_NO_MEMORY, "plan of %zu bytes: %s", host.size(), cudaGetErrorString(e));
+    if ((e = cudaMalloc(&p->mem, host.size())) != cudaSuccess) {
+      cudaGetLastError();
+      return report(e == cudaErrorMemoryAllocation ? DASH_ERR_NO_MEMORY : DASH_ERR_CUDA, "plan of %zu bytes: %s",
+                    host.size(), cudaGetErrorString(e));
+    }
     // pageable memory: cudaMemcpy may return with the copy's last step on its way, and the streams that use the
     // plan need not wait for this one
     if ((e = cudaMemcpy(p->mem, host.data(), host.size(), cudaMemcpyHostToDevice)) != cudaSuccess ||

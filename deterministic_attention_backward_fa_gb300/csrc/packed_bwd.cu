@@ -1126,23 +1126,13 @@ cudaError_t prepare_t() {
 template <int D>
 cudaError_t launch_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const CUtensorMap &dout,
                      const PackedBwdParams &p, int dq_ctas, int dkv_ctas, cudaStream_t stream) {
-  dash_packed_dq_kernel<D><<<dq_ctas, kThreads, smem_bytes<DqCfg<D>>(), stream>>>(q, k, v, dout, p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e =
+      launch(dash_packed_dq_kernel<D>, dq_ctas, kThreads, smem_bytes<DqCfg<D>>(), stream, nullptr, q, k, v, dout, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(dkv_ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<DkvCfg<D>>();
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, dash_packed_dkv_kernel<D>, q, k, v, dout, p);
-  if (e != cudaSuccess) return e;
-  if (p.n_sums) dash_packed_sum<D><<<dim3(p.n_sums, 2, 4), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = overlap_attr();
+  e = launch(dash_packed_dkv_kernel<D>, dkv_ctas, kThreads, smem_bytes<DkvCfg<D>>(), stream, &attr, q, k, v, dout, p);
+  if (e != cudaSuccess || !p.n_sums) return e;
+  return launch(dash_packed_sum<D>, dim3(p.n_sums, 2, 4), 256, 0, stream, nullptr, p);
 }
 
 }  // namespace

@@ -549,11 +549,8 @@ cudaError_t prepare_packed_fwd(int D) { return D == 64 ? prepare_t<64>() : prepa
 
 cudaError_t launch_packed_fwd(int D, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                               const PackedFwdParams &p, int num_ctas, cudaStream_t stream) {
-  if (D == 64)
-    dash_packed_fwd_kernel<64><<<num_ctas, kThreads, smem_bytes<64>(), stream>>>(q, k, v, p);
-  else
-    dash_packed_fwd_kernel<128><<<num_ctas, kThreads, smem_bytes<128>(), stream>>>(q, k, v, p);
-  return cudaGetLastError();
+  return D == 64 ? launch(dash_packed_fwd_kernel<64>, num_ctas, kThreads, smem_bytes<64>(), stream, nullptr, q, k, v, p)
+                 : launch(dash_packed_fwd_kernel<128>, num_ctas, kThreads, smem_bytes<128>(), stream, nullptr, q, k, v, p);
 }
 
 }  // namespace dash

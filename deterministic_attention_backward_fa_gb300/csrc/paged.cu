@@ -508,38 +508,21 @@ cudaError_t launch_decode_t(const DecodeParams &p, int num_sms, cudaStream_t str
   using C = DecCfg<D>;
   const long long items = (long long)p.B * p.max_splits * p.Hkv * p.hblocks;
   if (decode_clustered(p.B, p.Hq, p.max_splits)) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((int)items);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.max_splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dash_decode_kernel<D, kCluster>, p);
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.max_splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    return launch(dash_decode_kernel<D, kCluster>, (int)items, kThreads, C::kSmem, stream, &attr, p);
   }
   // Two CTAs fit on an SM.  Where they hold every item that the table has room
   // for, the scan is left out (one sequence of 701 tokens on 4 K/V heads, before
   // it was a cluster's: 6.3 us against 7.0).
-  if (items <= 2LL * num_sms)
-    dash_decode_kernel<D, kPlain><<<(int)items, kThreads, C::kSmem, stream>>>(p);
-  else
-    dash_decode_kernel<D, kScan><<<2 * num_sms, kThreads, C::kSmem, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const bool all = items <= 2LL * num_sms;
+  const cudaError_t e = launch(all ? dash_decode_kernel<D, kPlain> : dash_decode_kernel<D, kScan>,
+                               all ? (int)items : 2 * num_sms, kThreads, C::kSmem, stream, nullptr, p);
   if (e != cudaSuccess || p.max_splits <= 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.Hq, p.B);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dash_decode_join<D>, p);
+  cudaLaunchAttribute attr = overlap_attr();
+  return launch(dash_decode_join<D>, dim3(p.Hq, p.B), 128, 0, stream, &attr, p);
 }
 
 // ------------------------------------------------------------------ write
@@ -643,12 +626,12 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int N>
-void launch_copy_t(const CacheCopyParams &p, const int2 *pairs, int n, cudaStream_t stream) {
+cudaError_t launch_copy_t(const CacheCopyParams &p, const int2 *pairs, int n, cudaStream_t stream) {
   PairList<N> list;
   for (int i = 0; i < n; ++i) list.p[i] = pairs[i];
   const long long total = (long long)p.page_size * p.heads * (p.D / 8);
   const int pieces = (int)((total + 2047) / 2048 < 64 ? (total + 2047) / 2048 : 64);
-  dash_cache_copy_kernel<N><<<dim3(n * pieces, 2), 256, 0, stream>>>(list, p, pieces);
+  return launch(dash_cache_copy_kernel<N>, dim3(n * pieces, 2), 256, 0, stream, nullptr, list, p, pieces);
 }
 
 }  // namespace
@@ -672,18 +655,14 @@ cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_
 
 cudaError_t launch_cache_write(const CacheWriteParams &p, int num_sms, cudaStream_t stream) {
   const int want = (p.n_tokens + 7) / 8;
-  dash_cache_write_kernel<<<want < 8 * num_sms ? want : 8 * num_sms, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(dash_cache_write_kernel, want < 8 * num_sms ? want : 8 * num_sms, 256, 0, stream, nullptr, p);
 }
 
 cudaError_t launch_cache_copy(const CacheCopyParams &p, const int2 *pairs, int n, cudaStream_t stream) {
   for (int i = 0; i < n; i += kCopyPairs) {
     const int k = n - i < kCopyPairs ? n - i : kCopyPairs;
-    if (k <= 64)
-      launch_copy_t<64>(p, pairs + i, k, stream);
-    else
-      launch_copy_t<kCopyPairs>(p, pairs + i, k, stream);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        k <= 64 ? launch_copy_t<64>(p, pairs + i, k, stream) : launch_copy_t<kCopyPairs>(p, pairs + i, k, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

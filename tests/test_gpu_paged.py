@@ -461,3 +461,50 @@ def test_inputs_dropped_after_a_call_on_a_stream():
         got = run(call, *tensors, stream=side)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     dash.dash_sync_status()
+
+
+def test_a_failed_call_does_not_fail_the_next():
+    # a plan asked for inside a capture is refused (it allocates); the calls after it are none the worse for it
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import os
+import torch, deterministic_attention_backward_fa_gb300 as dash
+rand = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kp, vp, q, table, n, o = rand(4, 16, 2, 64), rand(4, 16, 2, 64), rand(1, 4, 64), i([[2, 0, 1]]), i([40]), rand(1, 4, 64)
+kn, starts, cu = rand(1, 2, 64), i([39]), i([0, 1])
+plan = dash.PackedPlan([40], 4, 2, 64, backward=True)
+x, xo, xl = [rand(40, h, 64) for h in (4, 2, 2, 4)], rand(40, 4, 64), torch.empty(4, 40, device="cuda")
+g, ws = [torch.empty_like(t) for t in x[:3]], torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+y, yo, yl = [rand(1, 2, 128, 64) for _ in range(3)], rand(1, 2, 128, 64), torch.empty(1, 2, 128, device="cuda")
+calls = [lambda: dash.dash_attn_decode(q, kp, vp, table, n, o, None, 0.125),
+         lambda: dash.dash_cache_write(kn, kn, kp, vp, table, starts, cu),
+         lambda: dash.dash_cache_copy(kp, vp, [2], [3]),
+         lambda: dash.dash_attn_packed_fwd(plan, *x[:3], xo, xl, 0.125),
+         lambda: dash.dash_attn_packed_bwd(plan, *x[:3], xo, x[3], xl, *g, 0.125, ws),
+         lambda: dash.dash_attn_fwd(*y, yo, yl, True, 0.125)]
+for call in calls:
+    call()
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph.capture_begin()
+        try:
+            dash.PackedPlan([5], 4, 2, 64)
+            os._exit(3)
+        except dash.DashError as e:
+            assert "capturing" in str(e), e
+        try:
+            graph.capture_end()
+        except RuntimeError:
+            pass
+    call()
+    torch.cuda.synchronize()
+dash.dash_sync_status()
+os._exit(0)  # without the destructors of captures that failed
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
