@@ -30,15 +30,22 @@
 
 namespace {
 
-thread_local std::string g_last_error;
+// The thread's last message, in place: reporting allocates nothing, so it does
+// not throw, not even where it is memory that has run out.
+thread_local char g_last_error[512];
+
+dash_status_t vfail(dash_status_t code, const char *fmt, va_list ap) {
+  char buf[sizeof(g_last_error)];  // an argument may be the message before
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  std::memcpy(g_last_error, buf, std::strlen(buf) + 1);
+  return code;
+}
 
 dash_status_t fail(dash_status_t code, const char *fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vfail(code, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
 
@@ -637,15 +644,13 @@ namespace dash {
 // Lets other translation units of the library report through dash_last_error():
 // formats the message, keeps it for this thread and returns the code.
 dash_status_t report(dash_status_t code, const char *fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vfail(code, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
-void set_last_error(const char *msg) { g_last_error = msg; }
+void set_last_error(const char *msg) { fail(DASH_OK, "%s", msg); }
 // The backward's tensor maps for other translation units of the library.
 bool encode_bhsd_map(CUtensorMap *m, const void *base, int BH, int S, int D, int box_rows) {
   return make_map(m, base, BH, S, D, box_rows) == DASH_OK;
@@ -1041,7 +1046,7 @@ void dash_release_workspace(void) {
     it = (std::get<0>(it->first) == dev) ? g_sched.erase(it) : std::next(it);
 }
 
-const char *dash_last_error(void) { return g_last_error.c_str(); }
+const char *dash_last_error(void) { return g_last_error; }
 
 int dash_version(void) { return 200; }
 

@@ -142,7 +142,7 @@ struct Device {
 std::mutex g_devices_mu;
 std::map<int, Device> g_devices;
 
-dash_status_t current_device(int *dev, Device *out) {
+dash_status_t current_device(int *dev, Device *out) try {
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_devices_mu);
@@ -159,6 +159,8 @@ dash_status_t current_device(int *dev, Device *out) {
   }
   *out = d;
   return DASH_OK;
+} catch (...) {
+  return report(DASH_ERR_NO_MEMORY, "device set-up: out of host memory");
 }
 
 dash_status_t cache_strides(const int64_t *s, int n_pages, int page_size, int heads, int D, const char *name,

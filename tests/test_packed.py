@@ -193,3 +193,49 @@ def test_plain_backward_against_differences(causal):
 def test_refusals_of_a_spin_limit():
     L, nul = dash.lib(), ctypes.c_void_p(0)
     assert L.dash_packed_plan_spin_limit(nul, 0) == 1 and "null plan" in dash.dash_last_error()
+
+
+def test_no_exception_leaves_a_c_entry(tmp_path):
+    # every allocation of the library fails while a flag is set: calls return a code and a message
+    import subprocess
+    import sys
+    (tmp_path / "f.cpp").write_text("""
+#include <cstdlib>
+#include <new>
+extern "C" { int fail_new = 0; }
+void *operator new(std::size_t n) {
+  void *p = fail_new ? nullptr : std::malloc(n ? n : 1);
+  if (!p) throw std::bad_alloc();
+  return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
+""")
+    so = str(tmp_path / "f.so")
+    subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-o", so, str(tmp_path / "f.cpp")], check=True)
+    code = """
+import ctypes, sys
+new, L = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+flag = ctypes.c_int.in_dll(new, "fail_new")
+L.dash_last_error.restype = ctypes.c_char_p
+nul, n, F, I64 = ctypes.c_void_p(0), ctypes.c_longlong(), ctypes.c_float, ctypes.c_longlong
+lens, out = (ctypes.c_int32 * 2)(300, 40), ctypes.c_void_p()
+flag.value = 1
+calls = [(1, lambda: L.dash_attn_decode(*[nul] * 7, 1, 4, 2, 64, 8, 16, 4, nul, F(-1.0), nul, I64(0), nul)),
+         (1, lambda: L.dash_cache_write(*[nul] * 7, I64(4), 1, 2, 64, 8, 0, 4, nul, nul)),
+         (1, lambda: L.dash_cache_copy(*[nul] * 4, -1, 2, 64, 8, 16, nul, nul)),
+         (5, lambda: L.dash_cache_copy(*[ctypes.c_void_p(1 << 20)] * 2, lens, lens, 1, 2, 64, 400, 16, nul, nul)),
+         (1, lambda: L.dash_attn_packed_fwd(*[nul] * 6, I64(5), nul, F(-1.0), nul)),
+         (1, lambda: L.dash_attn_packed_bwd(*[nul] * 10, I64(5), nul, F(-1.0), nul, I64(0), nul)),
+         (5, lambda: L.dash_packed_plan_create(lens, 2, 4, 2, 64, 1, 1, ctypes.byref(out))),
+         (5, lambda: L.dash_build_packed_items(lens, 2, 4, 2, 1, 0, 8, nul, nul, nul, ctypes.byref(n))),
+         (1, lambda: L.dash_attn_fwd(*[nul] * 5, 1, 1, 128, 64, 1, F(-1.0), nul))]
+for want, call in calls:
+    assert call() == want, (want, L.dash_last_error())
+    assert len(L.dash_last_error()) > 10
+flag.value = 0
+"""
+    import os
+    r = subprocess.run([sys.executable, "-c", code, so, dash.library_path()], capture_output=True, text=True,
+                       env=dict(os.environ, LD_PRELOAD=so), timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
