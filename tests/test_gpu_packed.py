@@ -431,3 +431,27 @@ def test_the_wait_for_dq_is_not_bounded():
     assert ms > 2 * limit_ms, "the SMs were not held for long enough"
     dash.dash_sync_status()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_each_value_against_the_dense_attention(D, causal):
+    # Equal lengths: the dense forward and backward on the same values.  Both sides round P, dS and the result to
+    # bf16 once, so each value of either is within R.bound of the exact one, and the two within twice that.
+    B, H, S, scale = 2, 3, 384, 1 / math.sqrt(D)
+    q, k, v, do = problem([S] * B, H, H, D, seed=171)
+    plan = dash.PackedPlan([S] * B, H, H, D, causal=causal, backward=True)
+    o, lse = dash.attn_packed_fwd(plan, q, k, v)
+    g = dash.attn_packed_bwd(plan, q, k, v, o, do, lse)
+    dense = lambda t: t.reshape(B, S, H, D).transpose(1, 2).contiguous()
+    packed = lambda t: t.transpose(1, 2).reshape(B * S, H, D)
+    xo, xl = dash.attn_fwd(dense(q), dense(k), dense(v), causal)
+    xg = dash.attn_bwd(dense(q), dense(k), dense(v), dense(o), dense(do),
+                       lse.reshape(H, B, S).transpose(0, 1).contiguous(), causal, schedule="serial")
+    dash.dash_sync_status()
+    ro, _, mag = R.forward([S] * B, q, k, v, causal, scale)
+    ref, mags = R.backward([S] * B, q, k, v, o, do, lse, causal, scale)
+    for name, a, b, r, m in zip(("O", "dQ", "dK", "dV"), (o, *g), (xo, *xg), (ro, *ref), (mag, *mags)):
+        far = (a.double() - packed(b).double()).abs() > 2 * R.bound(r, m)
+        assert not far.any(), f"{name}: {int(far.sum())} of {far.numel()}"
+    assert (lse.reshape(H, B, S).transpose(0, 1) - xl).abs().max() <= 1e-4
