@@ -1,6 +1,6 @@
 // Packed, grouped-head attention and the paged cache: what the host side
-// (packed.cpp) and the kernels (packed_fwd.cu, bwd.cu, packed_bwd.cu,
-// paged.cu) share.
+// (packed_api.cpp, packed_plan.cpp) and the kernels (packed_fwd.cu,
+// packed_bwd.cu, paged.cu) share; api.cpp reads the status word.
 #pragma once
 
 #include <cuda.h>

@@ -26,8 +26,9 @@ dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long 
 
 using dash::report;
 
-// A plan: the tables of one set of lengths on the device it was made on.
 constexpr long long kSpinNs = 2000000000LL;  // 2 s bound on every device wait
+
+// A plan: the tables of one set of lengths on the device it was made on.
 struct dash_packed_plan_st {
   long long spin_ns = kSpinNs;
   int device = 0, Hq = 0, Hkv = 0, D = 0, causal = 0, n_seqs = 0;

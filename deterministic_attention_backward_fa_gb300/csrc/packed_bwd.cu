@@ -15,8 +15,9 @@
 // dQ's place in tensor memory lets the products run under the softmax.  The
 // one-kernel form (tiles of dQ reduced in the order of a schedule) ran a
 // training batch of 16384 tokens (16 heads on 4, D = 128) in 737 us and long
-// documents at D = 64 (32 heads on 8) in 2151 us; this one takes 412 (dQ 176,
-// dK and dV 240) and 1188 (480 and 715).  The MMAs keep the tensor pipe 70 %
+// documents at D = 64 (32 heads on 8) in 2151 us; this one takes 416 (dQ 176,
+// dK and dV 240) and 1216 (480 and 715), each replayed from a graph, and 444 and
+// 1238 through the call with fresh inputs.  The MMAs keep the tensor pipe 70 %
 // busy at D = 128; what is left is the chain from one tile's scores to the next
 // tile's (waits, exponentials) and, for dQ, shared memory's bandwidth, and at
 // D = 64 the softmax warps' instructions and waits: with next to no MMAs dK/dV

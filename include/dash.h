@@ -472,7 +472,8 @@ dash_status_t dash_die_map(dash_stream_t stream, int32_t *group_of_smid_out, int
 /* The tables of one set of lengths (host pointer, n_seqs values >= 0) on the
  * current device: made once per batch, used by every layer's forward and, with
  * backward != 0, backward.  Allocates device memory and copies (not to be
- * called during a stream capture); read-only afterwards, so concurrent calls
+ * called during a stream capture), and so waits for the work queued on the
+ * device, as destroying it does; read-only afterwards, so concurrent calls
  * on any streams and captured graphs may share a plan.  It must outlive the
  * work enqueued with it, replays of graphs included. */
 typedef struct dash_packed_plan_st dash_packed_plan_t;
