@@ -98,6 +98,9 @@ _SIGS = {
     "dash_decode_workspace": ([_I] * 5, _L),
     "dash_cache_write": ([_P] * 7 + [_L] + [_I] * 6 + [_P, _P], _I),
     "dash_cache_copy": ([_P] * 4 + [_I] * 5 + [_P, _P], _I),
+    "dash_qk_norm_rope": ([_P] * 6 + [_I] + [_P] * 2 + [_L] + [_I] * 6 + [_F, _P, _P], _I),
+    "dash_qk_norm_rope_bwd": ([_P] * 8 + [_I] + [_P] * 4 + [_L] + [_I] * 6 + [_F, _P, _P, _L, _P], _I),
+    "dash_norm_rope_workspace": ([_L, _I], _L),
     "dash_sync_status": ([_P], _I),
     "dash_release_workspace": ([], None),
     "dash_last_error": ([], ctypes.c_char_p),
@@ -685,6 +688,77 @@ def dash_cache_copy(k_pages, v_pages, src, dst, stream=None):
                                      len(s), hkv, D, n_pages, page, strides, _stream_on(dev, stream)))
 
 
+# ---- norms of queries and keys, and their rotation
+def _norm_inputs(q, k, q_weight, k_weight, rope, positions):
+    """Checks the inputs and returns their sizes as dash_qk_norm_rope takes them: rows, Hq, Hkv, D, rot, positions."""
+    _rows("q", q, None, None, None, None)
+    (rows, heads, dim), dev = q.shape, q.device
+    _rows("k", k, None, dim, rows, dev)
+    dtype = q_weight.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise ValueError(f"q_weight must be torch.bfloat16 or torch.float32, not {dtype}")
+    _plain("q_weight", q_weight, dtype, (dim,), dev)
+    _plain("k_weight", k_weight, dtype, (dim,), dev)
+    _plain("rope", rope, torch.float32, (None, None), dev)
+    _plain("positions", positions, torch.int32, (rows,), dev)
+    most, rot = rope.shape
+    return rows, heads, k.shape[1], dim, rot, most
+
+
+def _norm(q, k, q_out, k_out, q_weight, k_weight, rope, positions, sizes, eps, pairs, stream):
+    dev = q.device
+    with _device(dev):
+        _check(lib().dash_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                                       q_weight.data_ptr(), k_weight.data_ptr(), q_weight.dtype == torch.float32,
+                                       rope.data_ptr(), positions.data_ptr(), *sizes, pairs, eps,
+                                       _strides(q, k, q_out, k_out), _stream_on(dev, stream)))
+
+
+def dash_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, rope, positions, eps: float, pairs: bool = False,
+                      stream=None):
+    """``q_out`` may be ``q`` itself and ``k_out`` ``k``."""
+    sizes = _norm_inputs(q, k, q_weight, k_weight, rope, positions)
+    _rows("q_out", q_out, sizes[1], sizes[3], sizes[0], q.device)
+    _rows("k_out", k_out, sizes[2], sizes[3], sizes[0], q.device)
+    _norm(q, k, q_out, k_out, q_weight, k_weight, rope, positions, sizes, eps, pairs, stream)
+
+
+@functools.lru_cache(maxsize=64)
+def dash_norm_rope_workspace(rows: int, head_dim: int) -> int:
+    return int(lib().dash_norm_rope_workspace(rows, head_dim))
+
+
+def _norm_bwd(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, sizes, eps,
+              pairs, workspace, stream):
+    dev = q.device
+    with _device(dev):
+        _check(lib().dash_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+                                           dq.data_ptr(), dk.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+                                           q_weight.dtype == torch.float32, dq_weight.data_ptr(),
+                                           dk_weight.data_ptr(), rope.data_ptr(), positions.data_ptr(), *sizes, pairs,
+                                           eps, _strides(q, k, dq_out, dk_out, dq, dk), workspace.data_ptr(),
+                                           workspace.numel(), _stream_on(dev, stream)))
+
+
+def _norm_grads(q, k, dq_out, dk_out):
+    _rows("dq_out", dq_out, q.shape[1], q.shape[2], q.shape[0], q.device)
+    _rows("dk_out", dk_out, k.shape[1], q.shape[2], q.shape[0], q.device)
+
+
+def dash_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions,
+                          eps: float, workspace, pairs: bool = False, stream=None):
+    """``dq`` may be ``dq_out`` itself and ``dk`` ``dk_out``; ``workspace`` as dash_norm_rope_workspace asks for."""
+    sizes = _norm_inputs(q, k, q_weight, k_weight, rope, positions)
+    _norm_grads(q, k, dq_out, dk_out)
+    _rows("dq", dq, sizes[1], sizes[3], sizes[0], q.device)
+    _rows("dk", dk, sizes[2], sizes[3], sizes[0], q.device)
+    _plain("dq_weight", dq_weight, torch.float32, (sizes[3],), q.device)
+    _plain("dk_weight", dk_weight, torch.float32, (sizes[3],), q.device)
+    _plain("workspace", workspace, torch.uint8, (None,), q.device)
+    _norm_bwd(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, sizes, eps,
+              pairs, workspace, stream)
+
+
 def dash_sync_status(stream=None):
     _check(lib().dash_sync_status(_stream(stream)))
 
@@ -807,3 +881,42 @@ def cache_copy(k_pages, v_pages, src, dst, stream=None):
     """Copies pages ``src`` to pages ``dst`` (host page numbers) inside the cache, in place."""
     with _using(stream, k_pages, v_pages):
         dash_cache_copy(k_pages, v_pages, src, dst, stream)
+
+
+def rope_table(max_positions: int, rot: int, base: float = 10000.0, device=None):
+    """fp32 [max_positions, rot]: the cosines, then the sines of position * base^(-2i / rot), i < rot / 2, as
+    ``qk_norm_rope`` takes them.  The angles are formed in 64 bits: in 32, those of far positions are off by whole
+    digits.  Other frequencies (scaled ones, say) go into a table of the caller's own."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    freq = torch.pow(base, -2.0 * torch.arange(rot // 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(max_positions, dtype=torch.float64, device=device).unsqueeze(1) * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps: float = 1e-6, pairs: bool = False, stream=None):
+    """Norms of queries [rows, heads, D] and keys [rows, kv_heads, D], head by head, times their weights, and turned by
+    ``positions`` (int32 [rows]) with the angles of ``rope`` (see rope_table): what attn_packed_fwd, attn_decode and
+    cache_write take.  Value i turns with value i + rot / 2, or with its neighbour (``pairs``).  New bf16 tensors."""
+    sizes = _norm_inputs(q, k, q_weight, k_weight, rope, positions)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    with _using(stream, q, k, q_out, k_out, q_weight, k_weight, rope, positions):
+        _norm(q, k, q_out, k_out, q_weight, k_weight, rope, positions, sizes, eps, pairs, stream)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps: float = 1e-6,
+                     pairs: bool = False, stream=None):
+    """dq, dk (bf16) and the weights' gradients (fp32 [D]) from ``qk_norm_rope``'s inputs and its outputs' gradients."""
+    sizes = _norm_inputs(q, k, q_weight, k_weight, rope, positions)
+    _norm_grads(q, k, dq_out, dk_out)
+    dev, dim = q.device, sizes[3]
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    dq_weight = torch.empty(dim, dtype=torch.float32, device=dev)
+    dk_weight = torch.empty(dim, dtype=torch.float32, device=dev)
+    ws = torch.empty(max(0, dash_norm_rope_workspace(sizes[0], dim)), dtype=torch.uint8, device=dev)
+    with _using(stream, q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, ws):
+        _norm_bwd(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, sizes, eps,
+                  pairs, ws, stream)
+    return dq, dk, dq_weight, dk_weight

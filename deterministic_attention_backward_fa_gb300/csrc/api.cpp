@@ -1030,6 +1030,8 @@ dash_status_t dash_sync_status(dash_stream_t stream_) {
   if (word == 0) return DASH_OK;
   if (word == dash::kStatusBadPage)
     return fail(DASH_ERR_INVALID_ARG, "a page table entry or token position lies outside the cache");
+  if (word == dash::kStatusBadPosition)
+    return fail(DASH_ERR_INVALID_ARG, "a position lies outside the rotation table");
   if (word == dash::kStatusSmemMisaligned)
     return fail(DASH_ERR_CUDA, "device status %d: dynamic shared memory not 1024-byte aligned", word);
   return fail(DASH_ERR_TIMEOUT, "device status %d: a bounded wait ran out (%s)", word,

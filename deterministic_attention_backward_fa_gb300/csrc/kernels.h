@@ -18,6 +18,7 @@ constexpr int kStatusSemTimeout = 2;      // a dQ semaphore wait ran out
 // sector serialises those accesses at the L2 slice.
 constexpr int kSemStride = 8;
 constexpr int kStatusBadPage = 4;         // a page table entry or a token position outside the cache
+constexpr int kStatusBadPosition = 5;     // a position outside the rotation table
 constexpr int kStatusSmemMisaligned = 3;  // dynamic shared memory not 1024-byte aligned
 
 // Dynamic shared memory requested by every kernel that allocates all 512

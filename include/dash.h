@@ -571,12 +571,48 @@ dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void
 dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, const int32_t *dst, int n, int Hkv,
                               int D, int n_pages, int page_size, const int64_t *strides, dash_stream_t stream);
 
+/* ------------------------------------------------ norms and rotation
+ * What stands between a model's projection and the packed attention or the
+ * decode: every head row x of q [rows][Hq][D] and k [rows][Hkv][D] (bf16) is
+ * normed, multiplied by its tensor's weight and turned by its row's position,
+ *   y = weight x / sqrt(mean(x^2) + eps),
+ *   z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin,
+ * over pairs (a, b) of the first `rot` of its D values: (i, i + rot / 2), or
+ * with pairs != 0 neighbours (2i, 2i + 1).  `rope` is fp32
+ * [max_positions][rot]: the cosines of a position's rot / 2 angles, then their
+ * sines; `positions` is int32 [rows].  rot is a multiple of 8 up to D; D 64 or
+ * 128.  Weights are [D], 16-byte aligned, bf16 or (weight_fp32 != 0) fp32.
+ * A row whose position lies outside the table becomes NaN, and
+ * dash_sync_status reports DASH_ERR_INVALID_ARG.  strides (NULL: contiguous),
+ * {row, head} in elements of q, k, q_out, k_out (8 values), multiples of 8 of
+ * at least D.  q_out may be q itself, with q's strides, and k_out k; otherwise
+ * outputs must not overlap inputs.  Can be captured. */
+dash_status_t dash_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const void *q_weight,
+                                const void *k_weight, int weight_fp32, const float *rope, const int32_t *positions,
+                                long long rows, int Hq, int Hkv, int D, int rot, int max_positions, int pairs,
+                                float eps, const int64_t *strides, dash_stream_t stream);
+
+/* Its backward: dq, dk and the weights' gradients (fp32 [D], sums over all rows
+ * and heads in one order that the sizes alone fix, no atomics) from the
+ * forward's inputs and the gradients dq_out, dk_out of its outputs.  strides:
+ * q, k, dq_out, dk_out, dq, dk (12 values).  dq may be dq_out itself, with its
+ * strides, and dk dk_out.  `workspace`: dash_norm_rope_workspace() bytes of
+ * device memory, 16-byte aligned, one per call in flight. */
+dash_status_t dash_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq,
+                                    void *dk, const void *q_weight, const void *k_weight, int weight_fp32,
+                                    float *dq_weight, float *dk_weight, const float *rope, const int32_t *positions,
+                                    long long rows, int Hq, int Hkv, int D, int rot, int max_positions, int pairs,
+                                    float eps, const int64_t *strides, void *workspace, long long workspace_bytes,
+                                    dash_stream_t stream);
+long long dash_norm_rope_workspace(long long rows, int D);
+
 /* Synchronises `stream` and returns the device status of the calling
  * thread's current device workspace for that stream: DASH_OK, or
  * DASH_ERR_TIMEOUT if a bounded wait ran out since the last call (the word is
- * then cleared).  The packed and paged operators share one such word per
- * device, read and cleared here too: DASH_ERR_TIMEOUT, or
- * DASH_ERR_INVALID_ARG for a page outside the cache. */
+ * then cleared).  The packed and paged operators and the norms share one such
+ * word per device, read and cleared here too: DASH_ERR_TIMEOUT, or
+ * DASH_ERR_INVALID_ARG for a page outside the cache or a position outside the
+ * rotation table. */
 dash_status_t dash_sync_status(dash_stream_t stream);
 
 /* Frees the workspaces and cached schedule tables of the current device. */
