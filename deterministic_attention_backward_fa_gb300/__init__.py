@@ -98,6 +98,10 @@ _SIGS = {
     "dash_decode_workspace": ([_I] * 5, _L),
     "dash_cache_write": ([_P] * 7 + [_L] + [_I] * 6 + [_P, _P], _I),
     "dash_cache_copy": ([_P] * 4 + [_I] * 5 + [_P, _P], _I),
+    "dash_attn_decode_fp8": ([_P] * 9 + [_I] * 7 + [_P, _F, _P, _L, _P], _I),
+    "dash_cache_write_fp8": ([_P] * 9 + [_L] + [_I] * 6 + [_P, _P], _I),
+    "dash_cache_read_fp8": ([_P] * 9 + [_L] + [_I] * 6 + [_P, _P], _I),
+    "dash_cache_copy_fp8": ([_P] * 6 + [_I] * 5 + [_P, _P], _I),
     "dash_qk_norm_rope": ([_P] * 6 + [_I] + [_P] * 2 + [_L] + [_I] * 6 + [_F, _P, _P], _I),
     "dash_qk_norm_rope_bwd": ([_P] * 8 + [_I] + [_P] * 4 + [_L] + [_I] * 6 + [_F, _P, _P, _L, _P], _I),
     "dash_norm_rope_workspace": ([_L, _I], _L),
@@ -688,6 +692,109 @@ def dash_cache_copy(k_pages, v_pages, src, dst, stream=None):
                                      len(s), hkv, D, n_pages, page, strides, _stream_on(dev, stream)))
 
 
+# ---- the 8-bit paged cache
+def _cache8(k_pages, v_pages, k_scales, v_scales, device):
+    shape = k_pages.shape
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.float8_e4m3fn or not t.is_cuda or len(t.shape) != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a CUDA float8_e4m3fn tensor [pages, tokens, heads, D], contiguous in D")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t.dtype != torch.float32 or t.shape != shape[:3] or t.device != device:
+            raise ValueError(f"{name} must be float32 {list(shape[:3])} on {device}, not {t.dtype} {list(t.shape)} on "
+                             f"{t.device}")
+    return shape
+
+
+def _cache8_strides(rows, k_pages, v_pages, k_scales, v_scales, table=None):
+    """Row and head strides of ``rows``, those of the cache, and the page table's; None when all are contiguous."""
+    last = () if table is None else (table,)
+    if all([t.is_contiguous() for t in (k_scales, v_scales, k_pages, v_pages, *rows, *last)]):
+        return None
+    v = [x for t in rows for x in t.stride()[:2]]
+    v += (*k_pages.stride()[:3], *v_pages.stride()[:3], *k_scales.stride(), *v_scales.stride())
+    v += [t.stride(0) for t in last]
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def _cache8_rows(call, k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, stream):
+    dev = k.device
+    n_pages, page, hkv, D = _cache8(k_pages, v_pages, k_scales, v_scales, dev)
+    _rows("k", k, hkv, D, None, None)
+    _rows("v", v, hkv, D, k.shape[0], dev)
+    _plain("starts", starts, torch.int32, (None,), dev)
+    B = starts.shape[0]
+    _plain("cu", cu, torch.int32, (B + 1,), dev)
+    _table(page_table, B, dev)
+    with _device(dev):
+        _check(call(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                    v_scales.data_ptr(), page_table.data_ptr(), starts.data_ptr(), cu.data_ptr(), k.shape[0], B, hkv,
+                    D, n_pages, page, page_table.shape[1],
+                    _cache8_strides((k, v), k_pages, v_pages, k_scales, v_scales, page_table),
+                    _stream_on(dev, stream)))
+
+
+def dash_cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new, stream=None):
+    _cache8_rows(lib().dash_cache_write_fp8, k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new,
+                 stream)
+
+
+def dash_cache_read_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, stream=None):
+    _cache8_rows(lib().dash_cache_read_fp8, k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, stream)
+
+
+def dash_cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None):
+    """``src``, ``dst``: page numbers on the host (lists, arrays or CPU tensors)."""
+    dev = k_pages.device
+    n_pages, page, hkv, D = _cache8(k_pages, v_pages, k_scales, v_scales, dev)
+    s, d = (array.array("i", x if isinstance(x, (list, tuple)) else x.tolist()) for x in (src, dst))
+    if len(s) != len(d):
+        raise ValueError("src and dst must have the same length")
+    with _device(dev):
+        _check(lib().dash_cache_copy_fp8(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                         v_scales.data_ptr(), s.buffer_info()[0], d.buffer_info()[0], len(s), hkv, D,
+                                         n_pages, page, _cache8_strides((), k_pages, v_pages, k_scales, v_scales),
+                                         _stream_on(dev, stream)))
+
+
+def _decode8_inputs(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths):
+    _rows("q", q, None, None, None, None)
+    dev, B = q.device, q.shape[0]
+    if _cache8(k_pages, v_pages, k_scales, v_scales, dev)[3] != q.shape[2]:
+        raise ValueError(f"q has head dimension {q.shape[2]}, the cache {k_pages.shape[3]}")
+    _table(page_table, B, dev)
+    _plain("lengths", lengths, torch.int32, (B,), dev)
+
+
+def _decode8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, o, lse, scale, workspace, stream):
+    dev = q.device
+    n_pages, page, hkv, D = k_pages.shape
+    with _device(dev):
+        _check(lib().dash_attn_decode_fp8(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+            q.shape[0], q.shape[1], hkv, D, n_pages, page, page_table.shape[1],
+            _cache8_strides((q, o), k_pages, v_pages, k_scales, v_scales, page_table), scale,
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+            _stream_on(dev, stream)))
+
+
+def dash_attn_decode_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, o, lse, scale: float,
+                         workspace=None, stream=None):
+    """``lse`` may be None; ``workspace`` as dash_decode_workspace asks for (uint8)."""
+    _decode8_inputs(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths)
+    dev = q.device
+    _rows("o", o, q.shape[1], q.shape[2], q.shape[0], dev)
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (q.shape[0], q.shape[1]), dev)
+    if workspace is not None:
+        _plain("workspace", workspace, torch.uint8, (None,), dev)
+    _decode8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, o, lse, float(scale), workspace, stream)
+
+
 # ---- norms of queries and keys, and their rotation
 def _norm_inputs(q, k, q_weight, k_weight, rope, positions):
     """Checks the inputs and returns their sizes as dash_qk_norm_rope takes them: rows, Hq, Hkv, D, rot, positions."""
@@ -881,6 +988,45 @@ def cache_copy(k_pages, v_pages, src, dst, stream=None):
     """Copies pages ``src`` to pages ``dst`` (host page numbers) inside the cache, in place."""
     with _using(stream, k_pages, v_pages):
         dash_cache_copy(k_pages, v_pages, src, dst, stream)
+
+
+def cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new, stream=None):
+    """``cache_write`` into an 8-bit cache: pages in float8_e4m3fn, and a power-of-two scale (fp32) for each token and
+    head, ``k_scales`` and ``v_scales`` [pages, tokens, heads] (see dash_cache_write_fp8)."""
+    with _using(stream, k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new):
+        dash_cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new, stream)
+
+
+def cache_read_fp8(k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, rows: int, stream=None):
+    """K and V [rows, heads, D] (bf16) of tokens starts[b] .. of each sequence, packed: sequence b has rows cu[b] ..
+    cu[b + 1] - 1.  Rows behind the last sequence are zero."""
+    shape = (int(rows), *k_pages.shape[2:])
+    k = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    v = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    with _using(stream, k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu):
+        dash_cache_read_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, stream)
+    return k, v
+
+
+def cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None):
+    """Copies pages ``src`` to pages ``dst`` (host page numbers) inside an 8-bit cache, their scales with them."""
+    with _using(stream, k_pages, v_pages, k_scales, v_scales):
+        dash_cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, stream)
+
+
+def attn_decode_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, scale: float | None = None,
+                    stream=None):
+    """``attn_decode`` over an 8-bit cache: O [B, heads, D] (bf16) and LSE [B, heads] (fp32)."""
+    _decode8_inputs(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths)
+    B, heads, dim = q.shape
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, heads), dtype=torch.float32, device=q.device)
+    need = dash_decode_workspace(B, heads, dim, k_pages.shape[1], page_table.shape[1])
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    with _using(stream, q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, o, lse, ws):
+        _decode8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, o, lse, scale, ws, stream)
+    return o, lse
 
 
 def rope_table(max_positions: int, rot: int, base: float = 10000.0, device=None):

@@ -1,0 +1,657 @@
+// The 8-bit paged key-value cache for sm_103a: writing and reading rows, copying
+// pages, attention of one new token per sequence.  All are bound by bytes.
+//
+// A row (one token of one K/V head) is D codes in e4m3 and a scale, its values
+// code x scale.  The scale is the smallest power of two (2^-126 at least) with
+// |x| <= 448 scale for the whole row, so that x / scale is exact and each value
+// is rounded once, to the nearest code (ties to even); and a row read back in
+// bf16 is exact.  (With floating-point codes a finer scale gains nothing: the
+// step of a value goes with the value's own power of two.)  A row that holds a
+// NaN or an infinity gets a NaN as its scale, and reads as NaN.
+//
+// Decode.  As in paged.cu, with the rows' scales a_t of K and c_t of V:
+//   x_t = scale log2(e) a_t (q . k_t),  o = (1/l) sum 2^(x_t - m) c_t v_t.
+// The codes are widened to f16, which holds them exactly, and multiplied there:
+//   S^T [16 tokens x 8 heads] = K Q^T,   O^T [16 dims x 8 heads] += V^T P^T
+// so that the codes are the large operand, read straight from global memory into
+// the lanes that need them (16 tokens' K and V are 8 loads of 16 bytes a lane),
+// and the 8 columns are the heads of a group: no shared memory stands between.
+// Contraction order is free, so a lane takes what lies side by side: of K the
+// 16 bytes at 16 (lane % 4) of two tokens, of V the same D / 8 dims of four.
+// Q is multiplied by a power of two first (its largest value lands at 2^14), so
+// that f16 holds its 8 bits down to 2^-29 of that.
+// P goes to f16 as 2^(x_t - M) c_t with M the maximum of x_t + log2 c_t of its
+// head, not of x_t: what counts in O keeps f16's 11 bits whatever the scales
+// of V are.  l and O are 32-bit sums, l of the unrounded 2^(x_t - m).
+// m and M move only when a term has grown past 2^8 of them (most steps need no
+// reduction across lanes and no rescaling).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "cache8.h"
+#include "decode.cuh"
+#include "packed.h"
+#include "sm103.cuh"
+
+namespace dash {
+
+using namespace dev;
+
+namespace {
+
+// ------------------------------------------------------------------ codes
+// 2^(e - 127) of an exponent field 1 <= e <= 254
+__device__ __forceinline__ float pow2_field(int e) { return __uint_as_float((uint32_t)e << 23); }
+
+// Two e4m3 codes as two f16 of the same values.
+__device__ __forceinline__ uint32_t widen8(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ uint32_t narrow8(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The scale's exponent field for a row whose largest magnitude has the bf16 bits
+// `top` (below 0x7f80): 448 = 1.75 x 2^8, so a mantissa of up to 0x60 fits with
+// 8 less, and one above it needs 7 less.
+__device__ __forceinline__ int scale_field(uint32_t top) {
+  return max(1, (int)(top >> 7) - 8 + ((top & 0x7fu) > 0x60u));
+}
+
+// ---------------------------------------------------------- write and read
+// Where token t of the call lies: its page and place, or -1.
+struct Place {
+  int page, off;
+};
+__device__ __forceinline__ Place place_of(const Cache8RowsParams &p, int t, bool &behind) {
+  int lo = 0, hi = p.B;  // the sequence of the token: the last b with cu[b] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu[mid + 1] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  behind = lo >= p.B;  // rows behind the last sequence
+  Place at{-1, 0};
+  if (behind) return at;
+  const int first = p.cu[lo];
+  const long long pos = (long long)p.starts[lo] + (t - first);
+  const long long slot = pos / p.page_size;
+  if (t >= first && pos >= 0 && slot < p.max_pages) at.page = p.table[lo * p.table_row + slot];
+  at.off = (int)(pos - slot * p.page_size);
+  if (at.page < 0 || at.page >= p.n_pages) at.page = -1;
+  return at;
+}
+
+// A warp takes a token: D / 8 lanes a row of a head, 8 values a lane.
+template <int D>
+__global__ void __launch_bounds__(256) dash_cache8_write_kernel(const __grid_constant__ Cache8RowsParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, e = (lane % kLanes) * 8;
+  const int nwarps = gridDim.x * 8;
+  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.n_tokens; t += nwarps) {
+    bool behind;
+    const Place at = place_of(p, t, behind);
+    if (behind) break;  // and so are the rows after it
+    if (at.page < 0) {
+      if (lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
+      continue;
+    }
+    const int rows = 2 * p.heads;  // K's, then V's
+    constexpr int kU = 4;
+    for (int r0 = 0; r0 < rows; r0 += kRows * kU) {
+      uint4 x[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int r = r0 + u * kRows + sub;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const __nv_bfloat16 *src = r < p.heads ? p.k + t * p.k_row + r * p.k_head
+                                                 : p.v + t * p.v_row + (r - p.heads) * p.v_head;
+          x[u] = *reinterpret_cast<const uint4 *>(src + e);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t top = 0;  // magnitudes in order are bits in order, infinities and NaN above all others
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool finite = top < 0x7f80u;
+        const int f = finite ? scale_field(top) : 1;
+        const float inv = pow2_field(254 - f);
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+        const int r = r0 + u * kRows + sub;
+        if (r >= rows) continue;
+        const bool is_v = r >= p.heads;
+        const int h = is_v ? r - p.heads : r;
+        const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
+        uint2 codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        if (!finite) codes = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2 *>((is_v ? p.c.v : p.c.k) + at.page * st.page + at.off * st.token + h * st.head + e) =
+            codes;
+        if (e == 0)
+          (is_v ? p.c.v_scale : p.c.k_scale)[at.page * ss.page + at.off * ss.token + h * ss.head] =
+              finite ? pow2_field(f) : NAN;
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) dash_cache8_read_kernel(const __grid_constant__ Cache8RowsParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, e = (lane % kLanes) * 8;
+  const int nwarps = gridDim.x * 8;
+  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.n_tokens; t += nwarps) {
+    bool behind;
+    const Place at = place_of(p, t, behind);
+    const bool none = at.page < 0;  // such rows are zero
+    if (none && !behind && lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
+    const int rows = 2 * p.heads;
+    constexpr int kU = 4;
+    for (int r0 = 0; r0 < rows; r0 += kRows * kU) {
+      uint2 x[kU];
+      float s[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int r = r0 + u * kRows + sub;
+        x[u] = make_uint2(0u, 0u);
+        s[u] = 0.f;
+        if (r < rows && !none) {
+          const bool is_v = r >= p.heads;
+          const int h = is_v ? r - p.heads : r;
+          const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
+          x[u] = *reinterpret_cast<const uint2 *>((is_v ? p.c.v : p.c.k) + at.page * st.page + at.off * st.token +
+                                                  h * st.head + e);
+          s[u] = (is_v ? p.c.v_scale : p.c.k_scale)[at.page * ss.page + at.off * ss.token + h * ss.head];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int r = r0 + u * kRows + sub;
+        if (r >= rows) continue;
+        uint4 w;
+        uint32_t *out = &w.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = widen8((i < 2 ? x[u].x : x[u].y) >> (16 * (i & 1)));
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+          out[i] = pack_bf16(v.x * s[u], v.y * s[u]);
+        }
+        __nv_bfloat16 *dst =
+            r < p.heads ? p.k + t * p.k_row + r * p.k_head : p.v + t * p.v_row + (r - p.heads) * p.v_head;
+        *reinterpret_cast<uint4 *>(dst + e) = w;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- copy
+// As in paged.cu: the pairs travel in the launch's arguments.  Blocks (pair,
+// piece) in x, K or V in y; a page's rows are walked 16 bytes a thread, its
+// scales one.
+template <int N>
+struct PairList8 {
+  int2 p[N];
+};
+constexpr int kCopyPairs8 = 3400;  // at most 32764 bytes of arguments
+
+template <int N>
+__global__ void __launch_bounds__(256)
+    dash_cache8_copy_kernel(const __grid_constant__ PairList8<N> pairs, const Cache8CopyParams p, int pieces) {
+  const int vecs = p.D >> 4, rows = p.page_size * p.heads, total = rows * vecs;
+  const int pair = blockIdx.x / pieces, piece = blockIdx.x - pair * pieces;
+  const int2 pr = pairs.p[pair];
+  const bool is_v = blockIdx.y != 0;
+  uint8_t *base = is_v ? p.c.v : p.c.k;
+  float *scale = is_v ? p.c.v_scale : p.c.k_scale;
+  const CacheStrides st = is_v ? p.c.vs : p.c.ks, ss = is_v ? p.c.vss : p.c.kss;
+  constexpr int kU = 8;
+  for (int x0 = piece * 256 * kU + threadIdx.x; x0 < total; x0 += pieces * 256 * kU) {
+    uint4 a[kU];
+    long long at[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int x = x0 + 256 * u;
+      if (x < total) {
+        const int row = x / vecs, tok = row / p.heads;
+        at[u] = tok * st.token + (row - tok * p.heads) * st.head + (x - row * vecs) * 16;
+        a[u] = *reinterpret_cast<const uint4 *>(base + pr.x * st.page + at[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (x0 + 256 * u < total) *reinterpret_cast<uint4 *>(base + pr.y * st.page + at[u]) = a[u];
+  }
+  for (int x = piece * 256 + threadIdx.x; x < rows; x += pieces * 256) {
+    // the shorter of the two inner strides innermost, so that neighbours stay neighbours
+    const bool heads_in = ss.head <= ss.token;
+    const int in = heads_in ? p.heads : p.page_size, a = x / in, b = x - a * in;
+    const long long at = (heads_in ? a : b) * ss.token + (heads_in ? b : a) * ss.head;
+    scale[pr.y * ss.page + at] = scale[pr.x * ss.page + at];
+  }
+}
+
+template <int N>
+cudaError_t launch_copy_t(const Cache8CopyParams &p, const int2 *pairs, int n, cudaStream_t stream) {
+  PairList8<N> list;
+  for (int i = 0; i < n; ++i) list.p[i] = pairs[i];
+  const long long total = (long long)p.page_size * p.heads * (p.D / 16);
+  const int pieces = (int)((total + 2047) / 2048 < 64 ? (total + 2047) / 2048 : 64);
+  return launch(dash_cache8_copy_kernel<N>, dim3(n * pieces, 2), 256, 0, stream, nullptr, list, p, pieces);
+}
+
+// ----------------------------------------------------------------- decode
+constexpr int kWarps = kDecodeThreads / 32;
+constexpr int kTok = 16;              // tokens of a warp's step
+constexpr int kStep = kWarps * kTok;  // tokens of the CTA's step
+constexpr float kLazy = 256.f;        // growth of a term past its maximum that is left standing
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 ld16(const uint8_t *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld8(const uint8_t *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// Sixteen tokens as a lane holds them: of tokens g and g + 8 its 16-byte pieces
+// of K and both scales, of tokens 2t, 2t + 1, 2t + 8, 2t + 9 its dims of V
+// (g = lane / 4, t = lane % 4).
+template <int D>
+struct Tokens {
+  static constexpr int kK = D / 64, kV = D / 32;  // 16-byte pieces of a K row, words of V
+  uint4 k[2][kK];
+  uint32_t v[4][kV];
+  float ks[2], vs[2];
+  uint32_t valid;
+};
+
+// NT tiles of 8 Q heads.
+template <int D, int NT, Deal kDeal>
+__global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
+    dash_decode8_kernel(const __grid_constant__ Decode8Params p) {
+  using T = Tokens<D>;
+  constexpr int kRowF = 8 * NT * D;                         // floats of a warp's result
+  __shared__ __align__(16) float s_o[kWarps * kRowF];       // [warp][head][D]
+  __shared__ float2 s_ml[kWarps * 8 * NT];
+  __shared__ __align__(16) uint8_t s_part[kDeal == kCluster ? 16 * (D * 4 + 8) : 16];
+  // the join may be set up now; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  Items<kDeal> it;
+  for (long long item = blockIdx.x;; item += gridDim.x) {
+    const int found = it.find(p, item);
+    if (found == 0) break;
+    if (found < 0) continue;
+    const int b = it.b, split = it.split;
+    const int hk = it.rest / p.hblocks, hb = it.rest - hk * p.hblocks;
+    const int h0 = hk * p.group + hb * 8 * NT, nh = min(8 * NT, p.group - hb * 8 * NT);
+    const int len = decode_len(p, b);
+    const int chunk = decode_chunk(len), n_splits = max(1, decode_splits(len));
+    const bool mine = kDeal != kCluster || split < n_splits;  // or the sequence does not have this split of the cluster
+    const int begin = split * chunk, end = min(len, begin + chunk);
+    const int steps = mine ? (end - begin + kStep - 1) / kStep : 0;
+    const int *table = p.table + b * p.table_row;
+    const uint8_t *kbase = p.c.k + hk * p.c.ks.head, *vbase = p.c.v + hk * p.c.vs.head;
+    const float *ksbase = p.c.k_scale + hk * p.c.kss.head, *vsbase = p.c.v_scale + hk * p.c.vss.head;
+
+    // Lanes 0-15 know where a token of the step lies, lanes 16-31 likewise.
+    auto page_of = [&](int step) -> int {
+      const int t = begin + step * kStep + warp * kTok + (lane & 15);
+      return t < end ? table[t / p.page_size] : -1;
+    };
+    auto load = [&](T &x, int step, int page) {
+      const int t = begin + step * kStep + warp * kTok + (lane & 15);
+      const bool inside = step < steps && t < end;
+      const bool ok = inside && page >= 0 && page < p.n_pages;
+      if (inside && !ok) atomicCAS(p.status, 0, kStatusBadPage);
+      const int off = t % p.page_size;
+      x.valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int tok = g + 8 * r;
+        const long long pg = __shfl_sync(0xffffffffu, page, tok);
+        const int of = __shfl_sync(0xffffffffu, off, tok);
+        const bool v = (x.valid >> tok) & 1u;
+        const uint8_t *row = kbase + pg * p.c.ks.page + of * p.c.ks.token + 16 * t4;
+#pragma unroll
+        for (int i = 0; i < T::kK; ++i) x.k[r][i] = v ? ld16(row + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
+        x.ks[r] = v ? __ldg(ksbase + pg * p.c.kss.page + of * p.c.kss.token) : 0.f;
+        x.vs[r] = v ? __ldg(vsbase + pg * p.c.vss.page + of * p.c.vss.token) : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tok = 2 * t4 + (r & 1) + 8 * (r >> 1);
+        const long long pg = __shfl_sync(0xffffffffu, page, tok);
+        const int of = __shfl_sync(0xffffffffu, off, tok);
+        const bool v = (x.valid >> tok) & 1u;
+        const uint8_t *row = vbase + pg * p.c.vs.page + of * p.c.vs.token + (D / 8) * g;
+        if (D == 128) {
+          const uint4 w = v ? ld16(row) : make_uint4(0u, 0u, 0u, 0u);
+          x.v[r][0] = w.x, x.v[r][1] = w.y, x.v[r][T::kV - 2] = w.z, x.v[r][T::kV - 1] = w.w;
+        } else {
+          const uint2 w = v ? ld8(row) : make_uint2(0u, 0u);
+          x.v[r][0] = w.x, x.v[r][1] = w.y;
+        }
+      }
+    };
+
+    T x[2];
+    int page = page_of(0);
+    load(x[0], 0, page);
+    page = page_of(1);
+
+    // Q: head g of each tile, the 16 values of each K piece; its power of two goes into the score's factor
+    uint32_t qf[NT][D / 16][2];
+    float sc[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = 8 * nt + g;
+      const __nv_bfloat16 *q = p.q + b * p.q_batch + (long long)(h0 + row) * p.q_head;
+      uint32_t raw[D / 16][2], top = 0;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const uint2 w = row < nh ? *reinterpret_cast<const uint2 *>(q + 64 * (j >> 2) + 16 * t4 + 4 * (j & 3))
+                                 : make_uint2(0u, 0u);
+        raw[j][0] = w.x, raw[j][1] = w.y;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top = max(top, max(raw[j][i] & 0x7fffu, (raw[j][i] >> 16) & 0x7fffu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int f = min(253, 268 - (int)(top >> 7));  // the largest magnitude becomes 2^14 to 2^15
+      const float up = pow2_field(f);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          qf[nt][j][i] = pack_f16(__uint_as_float(raw[j][i] << 16) * up, __uint_as_float(raw[j][i] & 0xffff0000u) * up);
+      const float down = p.scale_log2 * pow2_field(254 - f);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) sc[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t4 + c) * 4);
+    }
+
+    float acc[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.f;
+    // of heads 2 t4 and 2 t4 + 1 of each tile: m, M (-inf: nothing counted yet), 2^(m - M), l of the lane's tokens
+    float m[NT][2], M[NT][2], up[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = M[nt][c] = -INFINITY;
+        up[nt][c] = NAN;
+        l[nt][c] = 0.f;
+      }
+
+    auto compute = [&](const T &x) {
+      float s[NT][4] = {};
+#pragma unroll
+      for (int i = 0; i < T::kK; ++i) {
+        const uint32_t w0[4] = {x.k[0][i].x, x.k[0][i].y, x.k[0][i].z, x.k[0][i].w};
+        const uint32_t w1[4] = {x.k[1][i].x, x.k[1][i].y, x.k[1][i].z, x.k[1][i].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = widen8(w0[w]), a1 = widen8(w1[w]), a2 = widen8(w0[w] >> 16), a3 = widen8(w1[w] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
+        }
+      }
+      // s[nt][2 r + c]: token g + 8 r, head 2 t4 + c
+      float pv[NT][4];
+      bool fast = true;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1, c = e & 1;
+          const float y = s[nt][e] * sc[nt][c] * x.ks[r];
+          s[nt][e] = (x.valid >> (g + 8 * r)) & 1u ? y : -INFINITY;
+        }
+      float pr[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1, c = e & 1;
+          pr[nt][e] = ex2(s[nt][e] - m[nt][c]);
+          pv[nt][e] = pr[nt][e] * (x.vs[r] * up[nt][c]);
+          fast = fast && pr[nt][e] <= kLazy && pv[nt][e] <= kLazy;  // false for NaN
+        }
+      if (!__all_sync(0xffffffffu, fast)) {
+        const float lv[2] = {lg2(x.vs[0]), lg2(x.vs[1])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float fo[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float tm = fmaxf(s[nt][c], s[nt][2 + c]), tM = fmaxf(s[nt][c] + lv[0], s[nt][2 + c] + lv[1]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+              tM = fmaxf(tM, __shfl_xor_sync(0xffffffffu, tM, o));
+            }
+            const float m1 = fmaxf(m[nt][c], tm), M1 = fmaxf(M[nt][c], tM);
+            const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
+            l[nt][c] *= ex2(m[nt][c] - mr);
+            fo[c] = ex2(M[nt][c] - Mr);
+            m[nt][c] = m1;
+            M[nt][c] = M1;
+            // a factor that 32 bits cannot hold stays NaN, and every step comes here
+            up[nt][c] = fabsf(m1 - M1) < 100.f ? ex2(m1 - M1) : NAN;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              pr[nt][2 * r + c] = ex2(s[nt][2 * r + c] - mr);
+              pv[nt][2 * r + c] = ex2(s[nt][2 * r + c] + lv[r] - Mr);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][i][e] *= fo[e & 1];
+        }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) l[nt][c] += pr[nt][c] + pr[nt][2 + c];
+        pb[nt][0] = transpose8x8(pack_f16(pv[nt][0], pv[nt][1]));
+        pb[nt][1] = transpose8x8(pack_f16(pv[nt][2], pv[nt][3]));
+      }
+#pragma unroll
+      for (int w = 0; w < T::kV; ++w)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // dims 2 half, 2 half + 1 of the word: {first, second token} pairs of codes
+          const uint32_t y0 = __byte_perm(x.v[0][w], x.v[1][w], half ? 0x7362 : 0x5140);
+          const uint32_t y1 = __byte_perm(x.v[2][w], x.v[3][w], half ? 0x7362 : 0x5140);
+          const uint32_t a0 = widen8(y0), a1 = widen8(y0 >> 16), a2 = widen8(y1), a3 = widen8(y1 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][2 * w + half], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+    };
+
+    for (int step = 0; step < steps; step += 2) {
+      load(x[1], step + 1, page);
+      page = page_of(step + 2);
+      compute(x[0]);
+      if (step + 1 >= steps) break;
+      load(x[0], step + 2, page);
+      page = page_of(step + 3);
+      compute(x[1]);
+    }
+
+    // ---- each warp's average with its maximum and sum, then their join
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+        const int row = 8 * nt + 2 * t4 + c;
+        const float f = l[nt][c] == 0.f ? 0.f : ex2(M[nt][c] - m[nt][c]), inv = inverse_sum(l[nt][c]);
+        float *o = s_o + (warp * 8 * NT + row) * D + (D / 8) * g;
+#pragma unroll
+        for (int w = 0; w < T::kV; ++w)
+          *reinterpret_cast<float4 *>(o + 4 * w) =
+              make_float4(acc[nt][2 * w][c] * inv * f, acc[nt][2 * w][2 + c] * inv * f,
+                          acc[nt][2 * w + 1][c] * inv * f, acc[nt][2 * w + 1][2 + c] * inv * f);
+        if (g == 0) s_ml[warp * 8 * NT + row] = make_float2(m[nt][c], l[nt][c]);
+      }
+    __syncthreads();
+    constexpr int kVec = D / 4;
+    using J = Join<D>;
+    for (int y = threadIdx.x; mine && y < nh * kVec; y += kDecodeThreads) {
+      const int row = y / kVec, c = (y - row * kVec) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w * 8 * NT + row].x);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float fw = J::weight(s_ml[w * 8 * NT + row], ref);
+        ll += fw;
+        J::add(o, fw, *reinterpret_cast<const float4 *>(s_o + (w * 8 * NT + row) * D + c));
+      }
+      const int h = h0 + row;
+      if (n_splits == 1) {
+        J::write(p, b, h, c, o, mm, ll);
+      } else {
+        const float inv = inverse_sum(ll);
+        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (kDeal == kCluster) {
+          float *part = reinterpret_cast<float *>(s_part);  // [16][D], then [16] {maximum, sum}
+          *reinterpret_cast<float4 *>(part + row * D + c) = o;
+          if (c == 0) reinterpret_cast<float2 *>(part + 16 * D)[row] = make_float2(mm, ll);
+        } else {
+          const size_t at = ((size_t)b * p.Hq + h) * p.max_splits + split;
+          *reinterpret_cast<float4 *>(p.part_o + at * D + c) = o;
+          if (c == 0) p.part_ml[at] = make_float2(mm, ll);
+        }
+      }
+    }
+    if (kDeal == kCluster) {
+      if (n_splits > 1) join_cluster<D>(p, s_part, b, h0, nh, split, n_splits);  // the same in every CTA of the cluster
+      break;
+    }
+    __syncthreads();  // shared memory is free for the next item
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_decode_t(const Decode8Params &p, int num_sms, cudaStream_t stream) {
+  const long long items = (long long)p.B * p.max_splits * p.Hkv * p.hblocks;
+  if (decode_clustered(p.B, p.Hq, p.max_splits)) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.max_splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    return launch(dash_decode8_kernel<D, NT, kCluster>, (int)items, kDecodeThreads, 0, stream, &attr, p);
+  }
+  const int resident = (NT == 1 ? 3 : 2) * num_sms;
+  const bool all = items <= resident;
+  const cudaError_t e = launch(all ? dash_decode8_kernel<D, NT, kPlain> : dash_decode8_kernel<D, NT, kScan>,
+                               all ? (int)items : resident, kDecodeThreads, 0, stream, nullptr, p);
+  return e != cudaSuccess || p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
+}
+
+template <int D, int NT>
+cudaError_t prepare_t() {
+  cudaFuncAttributes fa;
+  for (auto kernel : {dash_decode8_kernel<D, NT, kPlain>, dash_decode8_kernel<D, NT, kScan>,
+                      dash_decode8_kernel<D, NT, kCluster>})
+    if (const cudaError_t e = cudaFuncGetAttributes(&fa, kernel)) return e;
+  return cudaSuccess;
+}
+
+int rows_grid(int n_tokens, int num_sms) {
+  const int want = (n_tokens + 7) / 8;
+  return want < 8 * num_sms ? want : 8 * num_sms;
+}
+
+}  // namespace
+
+cudaError_t prepare_cache8() {
+  cudaFuncAttributes fa;
+  for (auto kernel : {dash_cache8_write_kernel<64>, dash_cache8_write_kernel<128>, dash_cache8_read_kernel<64>,
+                      dash_cache8_read_kernel<128>})
+    if (const cudaError_t e = cudaFuncGetAttributes(&fa, kernel)) return e;
+  cudaError_t e = cudaFuncGetAttributes(&fa, dash_cache8_copy_kernel<64>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, dash_cache8_copy_kernel<kCopyPairs8>);
+  if (e == cudaSuccess) e = prepare_t<64, 1>();
+  if (e == cudaSuccess) e = prepare_t<64, 2>();
+  if (e == cudaSuccess) e = prepare_t<128, 1>();
+  return e != cudaSuccess ? e : prepare_t<128, 2>();
+}
+
+cudaError_t launch_decode8(int D, const Decode8Params &p, int num_sms, cudaStream_t stream) {
+  const bool small = p.group <= 8;
+  if (D == 64) return small ? launch_decode_t<64, 1>(p, num_sms, stream) : launch_decode_t<64, 2>(p, num_sms, stream);
+  return small ? launch_decode_t<128, 1>(p, num_sms, stream) : launch_decode_t<128, 2>(p, num_sms, stream);
+}
+
+cudaError_t launch_cache8_write(const Cache8RowsParams &p, int num_sms, cudaStream_t stream) {
+  return launch(p.D == 64 ? dash_cache8_write_kernel<64> : dash_cache8_write_kernel<128>,
+                rows_grid(p.n_tokens, num_sms), 256, 0, stream, nullptr, p);
+}
+
+cudaError_t launch_cache8_read(const Cache8RowsParams &p, int num_sms, cudaStream_t stream) {
+  return launch(p.D == 64 ? dash_cache8_read_kernel<64> : dash_cache8_read_kernel<128>,
+                rows_grid(p.n_tokens, num_sms), 256, 0, stream, nullptr, p);
+}
+
+cudaError_t launch_cache8_copy(const Cache8CopyParams &p, const int2 *pairs, int n, cudaStream_t stream) {
+  for (int i = 0; i < n; i += kCopyPairs8) {
+    const int k = n - i < kCopyPairs8 ? n - i : kCopyPairs8;
+    const cudaError_t e =
+        k <= 64 ? launch_copy_t<64>(p, pairs + i, k, stream) : launch_copy_t<kCopyPairs8>(p, pairs + i, k, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace dash

@@ -160,12 +160,14 @@ struct DecodeParams {
   const int *table, *lengths;
   __nv_bfloat16 *o;
   float *lse;                 // [B][Hq] or null
-  float *part_o;              // [B][Hq][max_splits][D], each split's own softmax average
-  float2 *part_ml;            // [B][Hq][max_splits] {maximum (scaled, log2), sum}
+  float *part_o;              // [B][Hq][parts][D], each split's own softmax average; parts: parts_before + max_splits
+  float2 *part_ml;            // [B][Hq][parts] {maximum (scaled, log2), sum}
   long long q_batch, q_head, o_batch, o_head, table_row;
   CacheStrides ks, vs;
   int B, Hq, Hkv, group, n_pages, page_size, max_pages, max_splits;
   int hblocks;                // blocks of 16 Q heads in a group
+  int first;                  // the tokens before this one are attended elsewhere ...
+  int parts_before;           // ... and have left that many parts
   float scale_log2;
   int *status;
 };
@@ -205,6 +207,8 @@ inline bool decode_clustered(int B, int Hq, int max_splits) {
 }
 cudaError_t prepare_decode();  // loads the decode kernels on the current device and raises their shared-memory limit
 cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_t stream);
+// Joins the parts of every (sequence, Q head); the kernel before it in the stream is the last that writes them.
+cudaError_t launch_decode_join(int D, const DecodeParams &p, cudaStream_t stream);
 
 struct CacheWriteParams {
   const __nv_bfloat16 *k, *v;

@@ -14,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "cache8.h"
 #include "dash.h"
 #include "norm_rope.h"
 #include "packed.h"
@@ -85,7 +86,7 @@ dash_status_t dash::host::current_device(int *dev, Device *out) try {
     cudaThreadExchangeStreamCaptureMode(&mode);
     if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, *dev)) != cudaSuccess ||
         (e = dash::prepare_decode()) != cudaSuccess || (e = dash::prepare_norm_rope()) != cudaSuccess ||
-        (e = dash::ops_status_address(&d.status)) != cudaSuccess)
+        (e = dash::prepare_cache8()) != cudaSuccess || (e = dash::ops_status_address(&d.status)) != cudaSuccess)
       d.status = nullptr;
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return cuda_error(e, "device set-up");
@@ -356,53 +357,11 @@ dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v
                                const int32_t *lengths, void *o, float *lse, int B, int Hq, int Hkv, int D,
                                int n_pages, int page_size, int max_pages, const int64_t *strides, float scale,
                                void *workspace, long long workspace_bytes, dash_stream_t stream) {
-  dash_status_t st = check_scale(scale);
-  if (st != DASH_OK || (st = check_heads(Hq, Hkv, D)) || (st = check_cache(Hkv, D, n_pages, page_size))) return st;
-  if (B < 0 || max_pages < 0) return report(DASH_ERR_INVALID_ARG, "B and max_pages must be >= 0");
-  if ((long long)page_size * max_pages > kMaxCached)
-    return report(DASH_ERR_UNSUPPORTED, "a page table row covers more than %lld tokens (2^31 less 2^26)", kMaxCached);
-  if (B > 65535) return report(DASH_ERR_UNSUPPORTED, "more than 65535 sequences");
-  if (B == 0) return DASH_OK;
-  if ((st = check_ptr(q, "q")) || (st = check_ptr(k_pages, "k_pages")) || (st = check_ptr(v_pages, "v_pages")) ||
-      (st = check_ptr(o, "o")))
-    return st;
-  if ((st = check_words(page_table, "page_table", max_pages == 0)) || (st = check_words(lengths, "lengths")) ||
-      (st = check_words(lse, "lse", true)))
-    return st;
-  Rows rq, ro;
-  if ((st = rows_of(strides, 0, B, Hq, D, "q", &rq)) || (st = rows_of(strides, 1, B, Hq, D, "o", &ro))) return st;
   dash::DecodeParams p;
-  if ((st = cache_strides(strides ? strides + 4 : nullptr, n_pages, page_size, Hkv, D, "k_pages", &p.ks)) ||
-      (st = cache_strides(strides ? strides + 7 : nullptr, n_pages, page_size, Hkv, D, "v_pages", &p.vs)))
-    return st;
-  p.table_row = strides ? strides[10] : max_pages;
-  if (B > 1 && p.table_row < max_pages) return report(DASH_ERR_INVALID_ARG, "page table rows overlap");
-  p.max_splits = std::max(1, dash::decode_max_splits(page_size * max_pages));
-  const long long need = dash_decode_workspace(B, Hq, D, page_size, max_pages);
-  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
-    return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
-  p.q = static_cast<const __nv_bfloat16 *>(q);
-  p.k = static_cast<const __nv_bfloat16 *>(k_pages);
-  p.v = static_cast<const __nv_bfloat16 *>(v_pages);
-  p.table = page_table;
-  p.lengths = lengths;
-  p.o = static_cast<__nv_bfloat16 *>(o);
-  p.lse = lse;
-  p.part_o = static_cast<float *>(workspace);
-  p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)B * Hq * p.max_splits * D);
-  p.q_batch = rq.row;
-  p.q_head = rq.head;
-  p.o_batch = ro.row;
-  p.o_head = ro.head;
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.group = Hq / Hkv;
-  p.n_pages = n_pages;
-  p.page_size = page_size;
-  p.max_pages = max_pages;
-  p.hblocks = (p.group + 15) / 16;
-  p.scale_log2 = scale * kLog2e;
+  dash_status_t st = decode_params(q, page_table, lengths, o, lse, B, Hq, Hkv, D, n_pages, page_size, max_pages,
+                                   strides, strides ? strides + 10 : nullptr, scale, workspace, workspace_bytes, &p);
+  if (st != DASH_OK || B == 0) return st;
+  if ((st = decode_cache(k_pages, v_pages, Hkv, D, n_pages, page_size, strides, &p)) != DASH_OK) return st;
   int dev = 0;
   Device device;
   if ((st = current_device(&dev, &device)) != DASH_OK) return st;
@@ -473,21 +432,8 @@ dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, 
   if ((st = cache_strides(strides, n_pages, page_size, Hkv, D, "k_pages", &p.ks)) ||
       (st = cache_strides(strides ? strides + 3 : nullptr, n_pages, page_size, Hkv, D, "v_pages", &p.vs)))
     return st;
-  std::vector<bool> to(n_pages);
-  for (int i = 0; i < n; ++i) {
-    if (dst[i] < 0 || dst[i] >= n_pages)
-      return report(DASH_ERR_INVALID_ARG, "destination page %d outside the cache's %d pages", dst[i], n_pages);
-    if (to[dst[i]]) return report(DASH_ERR_INVALID_ARG, "destination page %d is named twice", dst[i]);
-    to[dst[i]] = true;
-  }
-  std::vector<int2> pairs(n);
-  for (int i = 0; i < n; ++i) {
-    if (src[i] < 0 || src[i] >= n_pages)
-      return report(DASH_ERR_INVALID_ARG, "source page %d outside the cache's %d pages", src[i], n_pages);
-    if (to[src[i]])
-      return report(DASH_ERR_INVALID_ARG, "page %d is a source and a destination of one call", src[i]);
-    pairs[i] = make_int2(src[i], dst[i]);
-  }
+  std::vector<int2> pairs;
+  if ((st = copy_pairs(src, dst, n, n_pages, &pairs)) != DASH_OK) return st;
   p.kp = static_cast<__nv_bfloat16 *>(k_pages);
   p.vp = static_cast<__nv_bfloat16 *>(v_pages);
   p.page_size = page_size;

@@ -23,6 +23,7 @@
 
 #include <atomic>
 
+#include "decode.cuh"
 #include "packed.h"
 #include "sm103.cuh"
 
@@ -45,6 +46,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+static_assert(kThreads == kDecodeThreads, "the items are found by all threads");
 constexpr int kTok = 16;               // tokens of a warp per step
 constexpr int kStep = kWarps * kTok;   // tokens of the CTA per step
 constexpr int kStages = 3;
@@ -59,58 +61,6 @@ struct DecCfg {
   static constexpr int oPart = kWarps * 16 * (D * 4 + 8);    // the split's own result, for its cluster
   static_assert(kSmem >= oPart + 16 * (D * 4 + 8), "the joins fit in the ring");
 };
-
-// How a CTA finds its items.
-enum Deal {
-  kPlain,    // every sequence has max_splits numbers, those it does not need return at once
-  kScan,     // only the splits that a sequence has are numbered
-  kCluster,  // as kPlain, and the splits are a cluster
-};
-
-// A row's 1 / l and LSE.  l is 0 for a row that attends nothing (o = 0, LSE =
-// -inf) and NaN where a score is NaN or +inf: the row's results are then NaN, as
-// softmax makes them.
-__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
-__device__ __forceinline__ float log_sum(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
-// The join of a sequence's splits, in one order whoever makes it: weights
-// l 2^(m - max), their sum over the splits in turn, and the weighted rows in
-// kPart sums of every kPart-th split, added in turn.  A split that attends
-// nothing weighs 0 (m = -inf, l = 0) and its row is 0; nothing is left out by a
-// comparison, which would lose a split whose l is NaN.
-template <int D>
-struct Join {
-  static constexpr int kVec = D / 4, kPart = 128 / kVec;  // float4 of a row, sums
-  static __device__ __forceinline__ float weight(float2 ml, float ref) { return ml.y * ex2(ml.x - ref); }
-  static __device__ __forceinline__ void add(float4 &o, float w, float4 v) {
-    o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
-  }
-  static __device__ __forceinline__ void write(const DecodeParams &p, int b, int h, int c, float4 o, float m, float l) {
-    const float inv = inverse_sum(l);
-    uint2 w;
-    w.x = pack_bf16(o.x * inv, o.y * inv);
-    w.y = pack_bf16(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2 *>(p.o + b * p.o_batch + h * p.o_head + c) = w;
-    if (c == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = log_sum(m, l);
-  }
-};
-
-// Loads from the shared memory of any CTA of the cluster.
-__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
   const int n = valid ? 16 : 0;  // 0: fills with zeros, reads nothing
@@ -144,80 +94,21 @@ template <int D, Deal kDeal>
 __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodeParams p) {
   using C = DecCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_prefix[kThreads + 1];
-  __shared__ int s_find[2];  // {sequence, splits before it}
   // the join may be set up now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-  const int per_split = p.Hkv * p.hblocks;
   const int g = lane >> 2, t4 = lane & 3;
 
-  // Items are numbered (sequence, split, K/V head, block of Q heads), the split
-  // last in clusters.  With kScan the item's sequence is found by scanning the
-  // splits of kThreads sequences at a time; `base` and `base_b` remember the
-  // block of sequences reached so far.
-  long long base = 0;  // splits before sequence base_b
-  int base_b = 0, in_block = -1;
+  Items<kDeal> it;
   for (long long item = blockIdx.x;; item += gridDim.x) {
-    const long long want = item / per_split;
-    int b = -1, split = 0, rest = (int)(item - want * per_split);
-    if (kDeal == kCluster) {
-      if (item >= (long long)p.B * p.max_splits * per_split) break;
-      const int group = (int)(item / p.max_splits);
-      b = group / per_split;
-      rest = group - b * per_split;
-      split = (int)item - group * p.max_splits;
-    } else if (kDeal == kPlain) {
-      if (want >= (long long)p.B * p.max_splits) break;
-      b = (int)(want / p.max_splits);
-      split = (int)(want - (long long)b * p.max_splits);
-      if (split > 0 && split >= decode_splits(max(0, min(p.lengths[b], p.max_pages * p.page_size)))) continue;
-    }
-    while (kDeal == kScan) {
-      if (in_block != base_b) {  // the block's prefix sums
-        __syncthreads();
-        const int mine = base_b + (int)threadIdx.x;
-        int n = 0;
-        if (mine < p.B) n = decode_splits(max(0, min(p.lengths[mine], p.max_pages * p.page_size)));
-        // an empty sequence still has an item, which writes its zero row
-        if (mine < p.B && n == 0) n = 1;
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        s_prefix[threadIdx.x + 1] = x;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += s_prefix[(w + 1) * 32];
-        __syncthreads();
-        s_prefix[threadIdx.x + 1] = x + before;
-        if (threadIdx.x == 0) s_prefix[0] = 0;
-        __syncthreads();
-        in_block = base_b;
-      }
-      const int total = s_prefix[kThreads];
-      if (want < base + total) {
-        const int off = (int)(want - base);
-        if (off >= s_prefix[threadIdx.x] && off < s_prefix[threadIdx.x + 1]) {
-          s_find[0] = base_b + threadIdx.x;
-          s_find[1] = off - s_prefix[threadIdx.x];
-        }
-        __syncthreads();
-        b = s_find[0];
-        split = s_find[1];
-        break;
-      }
-      if (base_b + kThreads >= p.B) break;
-      base += total;
-      base_b += kThreads;
-    }
-    if (b < 0) break;
+    const int found = it.find(p, item);
+    if (found == 0) break;
+    if (found < 0) continue;
+    const int b = it.b, split = it.split, rest = it.rest;
     const int hk = rest / p.hblocks, hb = rest - hk * p.hblocks;
     const int h0 = hk * p.group + hb * 16, nh = min(16, p.group - hb * 16);
-    const int len = max(0, min(p.lengths[b], p.max_pages * p.page_size));
+    const int len = decode_len(p, b);
     const int chunk = decode_chunk(len), n_splits = max(1, decode_splits(len));
     const bool mine = kDeal != kCluster || split < n_splits;  // or the sequence does not have this split of the cluster
     const int begin = split * chunk, end = min(len, begin + chunk);
@@ -240,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
     // A lane below 16 keeps the row of one of the warp's tokens.
     auto page_of = [&](int step) -> int {
       const int t = begin + step * kStep + warp * kTok + (lane & 15);
-      return t < end ? table[t / p.page_size] : -1;
+      return t < end ? table[(p.first + t) / p.page_size] : -1;
     };
     uint32_t valid_ring[kStages];  // the tokens of each stage that count
     auto load = [&](int step, int page, int slot) -> uint32_t {
@@ -248,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
       const bool inside = step < steps && t < end;
       const bool ok = inside && page >= 0 && page < p.n_pages;
       if (inside && !ok) atomicCAS(p.status, 0, kStatusBadPage);
-      const int off = t - t / p.page_size * p.page_size;
+      const int off = (p.first + t) % p.page_size;
       const long long pg = ok ? page : 0;
       const long long ka = ok ? pg * p.ks.page + off * p.ks.token + hk * p.ks.head : 0;
       const long long va = ok ? pg * p.vs.page + off * p.vs.token + hk * p.vs.head : 0;
@@ -398,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
       }
       const float inv = inverse_sum(ll);
       const int h = h0 + row;
-      if (n_splits == 1) {
+      if (p.parts_before + n_splits == 1) {
         uint2 w;
         w.x = pack_bf16(o[0] * inv, o[1] * inv);
         w.y = pack_bf16(o[2] * inv, o[3] * inv);
@@ -409,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
         *reinterpret_cast<float4 *>(part + row * D + c) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
         if (c == 0) reinterpret_cast<float2 *>(part + 16 * D)[row] = make_float2(mm, ll);
       } else {
-        const size_t at = ((size_t)b * p.Hq + h) * p.max_splits + split;
+        const size_t at = ((size_t)b * p.Hq + h) * (p.parts_before + p.max_splits) + p.parts_before + split;
         *reinterpret_cast<float4 *>(p.part_o + at * D + c) =
             make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
         if (c == 0) p.part_ml[at] = make_float2(mm, ll);
@@ -417,42 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
     }
     if (kDeal == kCluster) {
       if (n_splits > 1) {  // the same in every CTA of the cluster
-        using J = Join<D>;
-        __syncwarp();
-        cluster_sync_all();
-        const float *part = reinterpret_cast<const float *>(smem + C::oPart);
-        const float2 *mls = reinterpret_cast<const float2 *>(part + 16 * D);
-        for (int x = split * kThreads + threadIdx.x; x < nh * kVec; x += p.max_splits * kThreads) {
-          const int row = x / kVec, c = (x - row * kVec) * 4;
-          float2 ml[kMaxCluster];
-          float4 v[kMaxCluster];
-#pragma unroll
-          for (int i = 0; i < kMaxCluster; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.f);
-            if (i < n_splits) {
-              ml[i] = ld_cluster2(mapa_rank(mls + row, i));
-              v[i] = ld_cluster4(mapa_rank(part + row * D + c, i));
-            }
-          }
-          float m = -INFINITY, l = 0.f;
-#pragma unroll
-          for (int i = 0; i < kMaxCluster; ++i) m = fmaxf(m, ml[i].x);
-          const float ref = m == -INFINITY ? 0.f : m;
-          float4 o[J::kPart] = {};
-#pragma unroll
-          for (int i = 0; i < kMaxCluster; ++i)
-            if (i < n_splits) {
-              const float w = J::weight(ml[i], ref);
-              l += w;
-              J::add(o[i % J::kPart], w, v[i]);
-            }
-#pragma unroll
-          for (int k = 1; k < J::kPart; ++k)
-            o[0] = make_float4(o[0].x + o[k].x, o[0].y + o[k].y, o[0].z + o[k].z, o[0].w + o[k].w);
-          J::write(p, b, h0 + row, c, o[0], m, l);
-        }
-        __syncwarp();
-        cluster_sync_all();  // nobody leaves while its results are read
+        join_cluster<D>(p, smem + C::oPart, b, h0, nh, split, n_splits);
       }
       break;
     }
@@ -466,10 +322,9 @@ __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
   // every block waits, so that this grid never ends before the first one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int h = blockIdx.x, b = blockIdx.y;
-  const int len = max(0, min(p.lengths[b], p.max_pages * p.page_size));
-  const int n = decode_splits(len);
-  if (n <= 1) return;  // written by the first kernel
-  const size_t at = ((size_t)b * p.Hq + h) * p.max_splits;
+  const int n = p.parts_before + decode_splits(decode_len(p, b));
+  if (n <= 1 && p.parts_before == 0) return;  // written by the first kernel
+  const size_t at = ((size_t)b * p.Hq + h) * (p.parts_before + p.max_splits);
   __shared__ float s_w[128];
   __shared__ float4 s_o[128];
   const int tid = threadIdx.x;
@@ -520,9 +375,7 @@ cudaError_t launch_decode_t(const DecodeParams &p, int num_sms, cudaStream_t str
   const bool all = items <= 2LL * num_sms;
   const cudaError_t e = launch(all ? dash_decode_kernel<D, kPlain> : dash_decode_kernel<D, kScan>,
                                all ? (int)items : 2 * num_sms, kThreads, C::kSmem, stream, nullptr, p);
-  if (e != cudaSuccess || p.max_splits <= 1) return e;
-  cudaLaunchAttribute attr = overlap_attr();
-  return launch(dash_decode_join<D>, dim3(p.Hq, p.B), 128, 0, stream, &attr, p);
+  return e != cudaSuccess || p.parts_before + p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
 }
 
 // ------------------------------------------------------------------ write
@@ -647,6 +500,11 @@ static cudaError_t prepare_decode_t() {
 cudaError_t prepare_decode() {
   const cudaError_t e = prepare_decode_t<64>();
   return e != cudaSuccess ? e : prepare_decode_t<128>();
+}
+
+cudaError_t launch_decode_join(int D, const DecodeParams &p, cudaStream_t stream) {
+  cudaLaunchAttribute attr = overlap_attr();
+  return launch(D == 64 ? dash_decode_join<64> : dash_decode_join<128>, dim3(p.Hq, p.B), 128, 0, stream, &attr, p);
 }
 
 cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_t stream) {

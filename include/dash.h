@@ -571,6 +571,53 @@ dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void
 dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, const int32_t *dst, int n, int Hkv,
                               int D, int n_pages, int page_size, const int64_t *strides, dash_stream_t stream);
 
+/* -------------------------------------------- 8-bit paged key-value cache
+ * The paged cache in half the bytes.  k_pages and v_pages are e4m3
+ * [n_pages][page_size][Hkv][D] (strides {page, token, head}, multiples of 16 of
+ * at least D), k_scales and v_scales fp32 [n_pages][page_size][Hkv], one for
+ * each row of D values (any strides without overlap; a head's scales side by
+ * side along a page's tokens are read with the fewest transactions).  A value
+ * is its code times its row's scale.  Page tables and pages outside the cache
+ * are as above.
+ *
+ * Writing quantises: a row's scale is the smallest power of two, 2^-126 at
+ * least, with |x| <= 448 scale for all of the row, and each x / scale is
+ * rounded to the nearest code, ties to even.  A row that holds a NaN or an
+ * infinity gets codes of 0 and a NaN for its scale: it reads as NaN.  Otherwise
+ * as dash_cache_write.  strides, 17 values: k {token, head}, v {token, head},
+ * k_pages, v_pages, k_scales, v_scales, page_table row. */
+dash_status_t dash_cache_write_fp8(const void *k, const void *v, void *k_pages, void *v_pages, float *k_scales,
+                                   float *v_scales, const int32_t *page_table, const int32_t *starts,
+                                   const int32_t *cu_new, long long n_tokens, int B, int Hkv, int D, int n_pages,
+                                   int page_size, int max_pages, const int64_t *strides, dash_stream_t stream);
+
+/* The reverse: tokens starts[b] .. of sequence b as packed bf16 rows cu[b] ..
+ * cu[b + 1] - 1 of k and v, each value its code times its scale, rounded to
+ * bf16 (exact for rows that dash_cache_write_fp8 wrote, unless they fall below
+ * bf16's range).  Rows behind cu[B], and those of pages outside the cache
+ * (reported), are zero.  strides as for writing. */
+dash_status_t dash_cache_read_fp8(void *k, void *v, const void *k_pages, const void *v_pages, const float *k_scales,
+                                  const float *v_scales, const int32_t *page_table, const int32_t *starts,
+                                  const int32_t *cu, long long n_tokens, int B, int Hkv, int D, int n_pages,
+                                  int page_size, int max_pages, const int64_t *strides, dash_stream_t stream);
+
+/* As dash_cache_copy, the pages' scales with them.  strides, 12 values: k_pages, v_pages, k_scales, v_scales. */
+dash_status_t dash_cache_copy_fp8(void *k_pages, void *v_pages, float *k_scales, float *v_scales, const int32_t *src,
+                                  const int32_t *dst, int n, int Hkv, int D, int n_pages, int page_size,
+                                  const int64_t *strides, dash_stream_t stream);
+
+/* As dash_attn_decode, over the 8-bit cache, whose scales may be any finite
+ * values >= 0, or NaN: o is then NaN for the heads that attend the row (lse too,
+ * if it is a K row).
+ * Workspace: dash_decode_workspace() bytes.  strides, 17 values: q {batch,
+ * head}, o {batch, head}, k_pages, v_pages, k_scales, v_scales, page_table
+ * row. */
+dash_status_t dash_attn_decode_fp8(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                                   const float *v_scales, const int32_t *page_table, const int32_t *lengths, void *o,
+                                   float *lse, int B, int Hq, int Hkv, int D, int n_pages, int page_size,
+                                   int max_pages, const int64_t *strides, float scale, void *workspace,
+                                   long long workspace_bytes, dash_stream_t stream);
+
 /* ------------------------------------------------ norms and rotation
  * What stands between a model's projection and the packed attention or the
  * decode: every head row x of q [rows][Hq][D] and k [rows][Hkv][D] (bf16) is

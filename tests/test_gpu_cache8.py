@@ -1,0 +1,435 @@
+"""The 8-bit paged cache on the GPU: writing, reading, copying, and decode
+attention, against 64-bit plain forms."""
+import math
+
+import pytest
+import torch
+
+import deterministic_attention_backward_fa_gb300 as dash
+
+import _cache8 as R
+import _packed as P
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+FP8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def bits(t):
+    return t.view(torch.uint8) if t.dtype == FP8 else t.view(torch.int32)
+
+
+def pages_of(lens, page, seed=1, spare=3, width=None):
+    need = [-(-n // page) for n in lens]
+    n_pages = sum(need) + spare
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    order = torch.randperm(n_pages, generator=g, device="cuda").int()
+    table = torch.full((len(lens), width or max(need + [1])), 2**31 - 1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return table, n_pages
+
+
+def cache(lens, hkv, D, page, seed=1, width=None, spread=0.0, heads_first=True):
+    """A filled 8-bit cache; ``spread``: standard deviation of the rows' own scales, in powers of two."""
+    table, n_pages = pages_of(lens, page, seed, width=width)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed + 10)
+    out = []
+    for _ in range(2):
+        x = torch.randn(n_pages, page, hkv, D, generator=g, device="cuda", dtype=torch.float64)
+        x = x * torch.exp2(spread * torch.randn(n_pages, page, hkv, 1, generator=g, device="cuda", dtype=torch.float64))
+        codes, scale = R.quantise(x)
+        scale = scale.float()
+        if heads_first:
+            scale = scale.transpose(1, 2).contiguous().transpose(1, 2)
+        out.append((codes.to(FP8), scale))
+    (kp, ks), (vp, vs) = out
+    return kp, vp, ks, vs, table
+
+
+def check(q, c, lengths, scale, o, lse, lse_tol=1e-4):
+    kp, vp, ks, vs, table = c
+    ro, rl, mag, top = R.decode(q, (kp, vp), (ks, vs), table, lengths, scale)
+    R.within("O", o, ro, mag, top)
+    none = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), none)
+    assert (lse.double() - rl)[~none].abs().max() <= lse_tol if (~none).any() else True
+
+
+# ------------------------------------------------------------ write, read
+@pytest.mark.parametrize("hkv,D,page", [(1, 64, 16), (8, 128, 16), (3, 64, 1), (5, 128, 7)])
+def test_write_and_read(hkv, D, page):
+    starts, news = [0, 5, 31, 0, 16], [1, 40, 0, 33, 16]
+    lens = [a + b for a, b in zip(starts, news)]
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page, seed=3, heads_first=page != 7)
+    cu = [sum(news[:i]) for i in range(len(news) + 1)]
+    extra = 4  # tokens behind the last sequence
+    fused = P.normal(4, cu[-1] + extra, 2 * hkv + 1, D) * torch.exp2(
+        torch.randint(-20, 20, (cu[-1] + extra, 2 * hkv + 1, 1), device="cuda").float()).bfloat16()
+    k, v = fused[:, 1:1 + hkv], fused[:, 1 + hkv:]
+    want = []
+    for x, pages, scales in ((k, kp, ks), (v, vp, vs)):
+        codes, scale = R.quantise(x)
+        wp, ws = bits(pages).clone(), scales.clone()
+        for b, n in enumerate(news):
+            for i in range(n):
+                pos = starts[b] + i
+                at = (table[b, pos // page].long(), pos % page)
+                wp[at], ws[at] = bits(codes[cu[b] + i].to(FP8)), scale[cu[b] + i].float()
+        want += [wp, ws]
+    dash.cache_write_fp8(k, v, kp, vp, ks, vs, table, i32(starts), i32(cu))
+    dash.dash_sync_status()
+    for got, ref in zip((bits(kp), ks, bits(vp), vs), want):
+        assert torch.equal(got, ref)
+    # what was written reads back as code times scale, exactly; rows behind the last sequence are zero
+    rk, rv = dash.cache_read_fp8(kp, vp, ks, vs, table, i32(starts), i32(cu), cu[-1] + extra)
+    dash.dash_sync_status()
+    for x, back in ((k, rk), (v, rv)):
+        codes, scale = R.quantise(x[:cu[-1]])
+        assert torch.equal(back[:cu[-1]].double(), codes * scale[..., None]) and not back[cu[-1]:].any()
+        # within half a step of what went in: 2^-4 of a value, or 2^-10 of the scale below the normal codes
+        err = (back[:cu[-1]].double() - x[:cu[-1]].double()).abs()
+        assert (err <= torch.maximum(2.0 ** -4 * x[:cu[-1]].double().abs(), 2.0 ** -10 * scale[..., None])).all()
+    # from the middle of the sequences on
+    mid = [min(3, n) for n in lens]
+    left = [n - m for n, m in zip(lens, mid)]
+    cu2 = [sum(left[:i]) for i in range(len(left) + 1)]
+    rk, _ = dash.cache_read_fp8(kp, vp, ks, vs, table, i32(mid), i32(cu2), cu2[-1])
+    vals = R.values(kp, ks)
+    for b, n in enumerate(left):
+        t = torch.arange(mid[b], lens[b], device="cuda")
+        assert torch.equal(rk[cu2[b]:cu2[b + 1]].double(), vals[table[b].long()[t // page], t % page].bfloat16().double())
+
+
+def test_quantisation_of_every_magnitude():
+    # one row for each exponent of bf16 and for mantissas beside the limit of 448 = 1.75 x 2^8; zero, NaN, infinities
+    D = 64
+    raw = torch.arange(0, 0x7f80, 0x10, dtype=torch.int16, device="cuda")
+    edge = torch.tensor([e << 7 | m for e in range(255) for m in (0x5f, 0x60, 0x61, 0x7f)], dtype=torch.int16,
+                        device="cuda")
+    tops = torch.cat([raw, edge]).view(torch.bfloat16)
+    x = P.normal(7, tops.numel(), 1, D).clamp(-1, 1) * tops[:, None, None] / 2
+    x[:, 0, 5] = tops * torch.where(torch.arange(tops.numel(), device="cuda") % 2 == 0, 1, -1).bfloat16()
+    bad = torch.zeros(4, 1, D, dtype=torch.bfloat16, device="cuda")
+    bad[1, 0, 9], bad[2, 0, 0], bad[3, 0, 63] = NAN, INF, -INF
+    x = torch.cat([x, bad])
+    n = x.shape[0]
+    kp, vp = (torch.zeros(1, n, 1, D, device="cuda").to(FP8) for _ in range(2))
+    ks, vs = (torch.full((1, n, 1), 5.0, device="cuda") for _ in range(2))
+    dash.cache_write_fp8(x, -x, kp, vp, ks, vs, i32([[0]]), i32([0]), i32([0, n]))
+    codes, scale = R.quantise(x)
+    assert torch.equal(kp[0].double(), codes) and torch.equal(vp[0].double(), -codes)
+    assert torch.equal(ks[0].nan_to_num(7), scale.float().nan_to_num(7)) and torch.equal(vs.nan_to_num(7), ks.nan_to_num(7))
+    rk, rv = dash.cache_read_fp8(kp, vp, ks, vs, i32([[0]]), i32([0]), i32([0, n]), n)
+    assert torch.equal(rk[:-3].double(), (codes * scale[..., None]).bfloat16().double()[:-3])
+    assert rk[-3:].isnan().all() and rv[-3:].isnan().all()
+
+
+def test_write_and_read_outside_the_cache_are_reported():
+    kp, vp, ks, vs, table = cache([32, 32], 2, 64, 16)
+    k = P.normal(2, 4, 2, 64)
+    codes, scale = R.quantise(k)
+    table[1, 1] = -1
+    for starts in ([0, 15], [0, 40], [0, -3]):
+        wk = bits(kp).clone()
+        dash.cache_write_fp8(k, k, kp, vp, ks, vs, table, i32(starts), i32([0, 2, 4]))
+        with pytest.raises(dash.DashError, match="outside the cache"):
+            dash.dash_sync_status()
+        wk[table[0, 0].long(), :2] = bits(codes[:2].to(FP8))
+        for i in (2, 3):
+            pos = starts[1] + i - 2
+            if 0 <= pos < 16:
+                wk[table[1, 0].long(), pos] = bits(codes[i].to(FP8))
+        assert torch.equal(bits(kp), wk)
+        rk, rv = dash.cache_read_fp8(kp, vp, ks, vs, table, i32(starts), i32([0, 2, 4]), 4)
+        with pytest.raises(dash.DashError, match="outside the cache"):
+            dash.dash_sync_status()
+        for i in range(4):
+            pos = starts[i // 2] + i % 2
+            inside = i < 2 or 0 <= pos < 16
+            assert torch.equal(rk[i].double(), codes[i] * scale[i][:, None]) if inside else not rk[i].any()
+    assert not dash.cache_read_fp8(kp, vp, ks, vs, table[:0], i32([]), i32([0]), 3)[0].any()
+    dash.dash_sync_status()
+
+
+@pytest.mark.parametrize("hkv,D,page,n", [(1, 64, 1, 5), (2, 128, 16, 64), (3, 64, 24, 65), (8, 128, 16, 3600)])
+def test_copy(hkv, D, page, n):
+    n_pages = 2 * n + 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    pages = [torch.randint(0, 256, (n_pages, page, hkv, D), generator=g, device="cuda", dtype=torch.uint8).view(FP8)
+             for _ in range(2)]
+    scales = [torch.rand(n_pages, page, hkv, generator=g, device="cuda") for _ in range(2)]
+    perm = torch.randperm(n_pages, generator=torch.Generator().manual_seed(5))
+    src, dst = perm[:n], perm[n:2 * n]
+    src[n // 2] = src[0]  # a page may be copied to several
+    want = [bits(t).clone() for t in (*pages, *scales)]
+    for t, w in zip((*pages, *scales), want):
+        w[dst] = bits(t)[src]
+    first = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in (*pages, *scales)]
+    dash.cache_copy_fp8(*pages, *scales, src, dst)
+    dash.cache_copy_fp8(*first, src.tolist(), dst.tolist())
+    dash.cache_copy_fp8(*pages, *scales, [], [])
+    dash.dash_sync_status()
+    for t, f, w in zip((*pages, *scales), first, want):
+        assert torch.equal(bits(t), w) and torch.equal(bits(f.contiguous()), w)
+
+
+# ----------------------------------------------------------------- decode
+CASES = [([1], 1, 1, 64, 16), ([0, 5, 0], 4, 2, 128, 16), ([64, 63, 65, 256, 257, 255], 8, 2, 128, 16),
+         ([300, 1000, 17], 6, 2, 64, 24), ([2000, 1], 32, 1, 128, 64), ([777] * 3, 20, 1, 64, 1), ([90, 513], 16, 1, 128, 16),
+         ([40000, 3], 4, 4, 128, 128), ([33000, 65], 3, 1, 64, 7), (list(range(0, 900, 5)), 2, 1, 64, 32),
+         (list(range(0, 900, 7)), 9, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,D,page", CASES, ids=lambda x: str(x)[:40])
+def test_decode(lens, hq, hkv, D, page):
+    c = cache(lens, hkv, D, page, heads_first=hq != 3)
+    kp, vp, ks, vs, table = c
+    # whatever stands behind a sequence's last token is not read into its result
+    for b, n in enumerate(lens):
+        if n % page:
+            last = table[b, n // page].long()
+            for pages, scales in ((kp, ks), (vp, vs)):
+                bits(pages)[last, n % page:], scales[last, n % page:] = 0x7f, NAN
+    q = P.normal(9, len(lens), hq, D)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    dash.dash_sync_status()
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
+    o2, lse2 = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("spread", [3.0, 20.0])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (12, 1)])
+def test_decode_of_rows_of_very_different_scales(hq, hkv, spread):
+    # K's scale far down as well, so that scores stay small whatever the rows' scales are; V's as they come
+    lens, D, page = [700, 65, 3000], 128, 16
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page, spread=spread)
+    ks = torch.ones_like(ks) * 2.0 ** -8
+    # the largest V rows first, in the middle, and on tokens that hardly count
+    c = (kp, vp, ks, vs, table)
+    for seed in (1, 2):
+        q = P.normal(seed, 3, hq, D)
+        o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+        check(q, c, lens, 1 / math.sqrt(D), o, lse)
+    # scales of zero weigh nothing in O and count in the sum; arbitrary (not power of two) scales
+    vs[table[0, 3].long(), 2:9] = 0.0
+    ks.mul_(1.37)
+    vs.mul_(0.77)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
+    vs.zero_()
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    assert not o.any() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -100, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100])
+def test_decode_of_queries_of_any_magnitude(gain):
+    lens, hq, hkv, D, page = [300, 40], 4, 2, 64, 16
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page)
+    q = (P.normal(3, 2, hq, D).double() * gain).bfloat16()
+    ks = (ks.double() / gain).float()
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    check(q, (kp, vp, ks, vs, table), lens, 1 / math.sqrt(D), o, lse)
+    o, lse = dash.attn_decode_fp8(torch.zeros_like(q), kp, vp, ks, vs, table, i32(lens))
+    check(torch.zeros_like(q), (kp, vp, ks, vs, table), lens, 1 / math.sqrt(D), o, lse)
+
+
+def test_decode_does_not_depend_on_the_batch():
+    lens, hq, hkv, D, page = [5000, 130, 20000, 1, 700], 8, 2, 128, 16
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page, width=4000)
+    q = P.normal(5, 5, hq, D)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    for b, n in enumerate(lens):
+        w = -(-n // page)
+        ob, lb = dash.attn_decode_fp8(q[b:b + 1], kp, vp, ks, vs, table[b:b + 1, :w].contiguous(), i32([n]))
+        assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0])
+
+
+@pytest.mark.parametrize("hq,hkv,D,page,width", [(16, 4, 128, 16, 44), (8, 1, 64, 16, 64), (20, 1, 128, 7, 90),
+                                                 (2, 2, 64, 1, 2000), (12, 1, 128, 64, 30)])
+def test_decode_small_calls_and_captures(hq, hkv, D, page, width):
+    cap = page * width
+    lens = sorted({0, 1, 255, 256, 257, 512, 513, 777, cap // 2 + 1, cap - 1, cap} & set(range(cap + 1))) * 6
+    c = cache(lens, hkv, D, page, width=width)
+    kp, vp, ks, vs, table = c
+    q = P.normal(15, len(lens), hq, D)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    dash.dash_sync_status()
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
+    for b, n in enumerate(lens):
+        ob, lb = dash.attn_decode_fp8(q[b:b + 1], kp, vp, ks, vs, table[b:b + 1], i32([n]))
+        assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0]), n
+    length, graph = i32([1]), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og, lg = dash.attn_decode_fp8(q[-1:], kp, vp, ks, vs, table[-1:], length)
+    length.copy_(i32(lens[-1:]))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(og[0], o[-1]) and torch.equal(lg[0], lse[-1])
+    dash.dash_sync_status()
+
+
+def test_decode_strides_streams_and_lengths_out_of_range():
+    lens, hq, hkv, D, page = [100, 700, 31], 8, 2, 64, 16
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page)
+    q = P.normal(6, 3, hq, D)
+    want = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    # a head-first cache, K and V side by side, Q a part of a fused row, a table inside a larger one
+    both = torch.zeros((kp.shape[0], 2, hkv, page, D), dtype=torch.uint8, device="cuda")
+    both[:, 0], both[:, 1] = bits(kp).transpose(1, 2), bits(vp).transpose(1, 2)
+    k2, v2 = both[:, 0].transpose(1, 2).view(FP8), both[:, 1].transpose(1, 2).view(FP8)
+    s2 = torch.stack([ks, vs], 3)
+    fused = torch.full((3, hq + 4, D), NAN, dtype=torch.bfloat16, device="cuda")
+    q2 = fused[:, 2:2 + hq]
+    q2.copy_(q)
+    t2 = torch.full((3, table.shape[1] + 9), -5, dtype=torch.int32, device="cuda")
+    t2[:, :table.shape[1]] = table
+    side = torch.cuda.Stream()
+    got = dash.attn_decode_fp8(q2, k2, v2, s2[..., 0], s2[..., 1], t2[:, :table.shape[1]], i32(lens), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    small, full = table[:, :2].contiguous(), i32([32, 32, 31])
+    a = dash.attn_decode_fp8(q2, kp, vp, ks, vs, small, i32([-4, 10**9, 31]))
+    b = dash.attn_decode_fp8(q2, kp, vp, ks, vs, small, full)
+    dash.dash_sync_status()
+    assert torch.equal(a[0][1:], b[0][1:]) and not a[0][0].any() and (a[1][0] == -INF).all()
+    # without lse, into a given o
+    o = torch.empty_like(q)
+    ws = torch.empty(dash.dash_decode_workspace(3, hq, D, page, table.shape[1]), dtype=torch.uint8, device="cuda")
+    dash.dash_attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens), o, None, 1 / math.sqrt(D), ws)
+    assert torch.equal(o, want[0])
+
+
+def test_decode_of_bad_pages_nan_and_infinite_scores():
+    lens, hq, hkv, D, page = [70, 40], 4, 2, 128, 16
+    c = cache(lens, hkv, D, page)
+    kp, vp, ks, vs, table = c
+    q = P.normal(7, 2, hq, D)
+    for bad in (-1, kp.shape[0], 2**31 - 1):
+        t = table.clone()
+        t[0, 1] = bad
+        o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, t, i32(lens))
+        with pytest.raises(dash.DashError, match="outside the cache"):
+            dash.dash_sync_status()
+        dash.dash_sync_status()  # cleared
+        check(q, (kp, vp, ks, vs, t), lens, 1 / math.sqrt(D), o, lse)
+    good = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    # a NaN row of K, a NaN row of V, a NaN code of V: heads of that K/V head and sequence alone
+    for what, where in (("k", ks), ("v", vs), ("code", vp)):
+        kept = where.clone()
+        at = (table[0, 2].long(), 5, 1)
+        if what == "code":
+            bits(where)[(*at, 17)] = 0x7f
+        else:
+            where[at] = NAN
+        o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+        assert torch.equal(o[1], good[0][1]) and torch.equal(o[0, :2], good[0][0, :2])
+        if what == "code":
+            assert o[0, 2:, 17].isnan().all() and o[0, 2:, 16].isfinite().all()
+        else:
+            assert o[0, 2:].isnan().all() and (lse[0, 2:].isnan().all() if what == "k" else lse[0, 2:].isfinite().all())
+        bits(where).copy_(bits(kept))
+    # queries: NaN and +inf make the row NaN; scores of -inf weigh nothing
+    one = q.clone()
+    one[0, 0, 3] = NAN
+    o, lse = dash.attn_decode_fp8(one, kp, vp, ks, vs, table, i32(lens))
+    assert o[0, 0].isnan().all() and lse[0, 0].isnan() and torch.equal(o[0, 1:], good[0][0, 1:])
+    bits(kp)[:, :, :, 0] = 0x38  # 1.0
+    one = q.clone()
+    one[0, 0, 0], one[0, 1, 0] = INF, -INF
+    o, lse = dash.attn_decode_fp8(one, kp, vp, ks, vs, table, i32(lens))
+    assert o[0, 0].isnan().all() and not o[0, 1].any() and lse[0, 1] == -INF
+    dash.dash_sync_status()
+
+
+def test_large_offsets():
+    # a cache of more than 2^32 bytes
+    hq, hkv, D, page = 4, 4, 128, 64
+    n_pages = (2**32 // (page * hkv * D)) + 40
+    kp, vp = (torch.zeros(n_pages, page, hkv, D, dtype=torch.uint8, device="cuda").view(FP8) for _ in range(2))
+    ks, vs = (torch.ones(n_pages, page, hkv, device="cuda") for _ in range(2))
+    table = i32([[n_pages - 1, 3, n_pages - 20, n_pages - 2]])
+    k, v = P.normal(1, 250, hkv, D), P.normal(2, 250, hkv, D)
+    dash.cache_write_fp8(k, v, kp, vp, ks, vs, table, i32([0]), i32([0, 250]))
+    q = P.normal(8, 1, hq, D)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32([250]))
+    dash.cache_copy_fp8(kp, vp, ks, vs, [n_pages - 1, n_pages - 2], [0, n_pages - 5])
+    rk, rv = dash.cache_read_fp8(kp, vp, ks, vs, i32([[0, 3, n_pages - 20, n_pages - 5]]), i32([0]), i32([0, 250]), 250)
+    dash.dash_sync_status()
+    small = [t[table[0].long()] for t in (bits(kp), bits(vp), ks, vs)]
+    check(q, (small[0].view(FP8), small[1].view(FP8), small[2], small[3], i32([[0, 1, 2, 3]])), [250], 1 / math.sqrt(D),
+          o, lse)
+    for x, back in ((k, rk), (v, rv)):
+        codes, scale = R.quantise(x)
+        assert torch.equal(back.double(), codes * scale[..., None])
+
+
+def test_refusals():
+    kp, vp, ks, vs, table = cache([32], 2, 64, 16)
+    q, n = P.normal(1, 1, 4, 64), i32([32])
+    f = dash.attn_decode_fp8
+    for bad in (lambda: f(q.float(), kp, vp, ks, vs, table, n), lambda: f(q, kp, vp[1:], ks, vs, table, n),
+                lambda: f(q, kp.float().bfloat16(), vp, ks, vs, table, n), lambda: f(q, kp, vp, ks.double(), vs, table, n),
+                lambda: f(q, kp, vp, ks, vs[1:], table, n), lambda: f(q, kp, vp, ks, vs, table.long(), n),
+                lambda: f(q, kp, vp, ks.cpu(), vs, table, n), lambda: f(q, kp, vp, ks, vs, table, n.long()),
+                lambda: f(P.normal(1, 1, 4, 128), kp, vp, ks, vs, table, n),
+                lambda: dash.cache_copy_fp8(kp, vp, ks, vs, [0], [1, 2]),
+                lambda: dash.cache_write_fp8(q, q, kp, vp, ks, vs, table, i32([0]), i32([0, 1])),
+                lambda: dash.cache_read_fp8(kp, vp, ks, vs, table, i32([0]), i32([0]), 1),
+                lambda: dash.attn_decode(q, kp, vp, table, n)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(dash.DashError, match="overlap|strides"):
+        f(q, kp, vp, ks[:, :, :1].expand(-1, -1, 2), vs, table, n)
+    with pytest.raises(dash.DashError, match="twice"):
+        dash.cache_copy_fp8(kp, vp, ks, vs, [0, 1], [2, 2])
+
+
+def test_prompt_fork_and_decode_together():
+    # two prompts go through the norms and into the 8-bit cache, the first is forked, all take a new token, and the
+    # context read back gives the packed forward the same answer as the decode
+    hq, hkv, D, page, lens = 8, 2, 128, 16, [150, 37]
+    rows = sum(lens)
+    fused = P.normal(3, rows + 3, hq + 2 * hkv, D)
+    w = [torch.ones(D, device="cuda")] * 2
+    rope = dash.rope_table(200, D)
+    positions = torch.cat([torch.arange(n, dtype=torch.int32, device="cuda") for n in lens] + [i32([150, 37, 150])])
+    q, k = dash.qk_norm_rope(fused[:, :hq], fused[:, hq:hq + hkv], *w, rope, positions)
+    v = fused[:, hq + hkv:]
+    kp, vp = (torch.zeros(40, page, hkv, D, dtype=torch.uint8, device="cuda").view(FP8) for _ in range(2))
+    ks, vs = (torch.zeros(40, hkv, page, device="cuda").transpose(1, 2) for _ in range(2))
+    c = (kp, vp, ks, vs)
+    table = torch.arange(36, dtype=torch.int32, device="cuda").reshape(3, 12)
+    dash.cache_write_fp8(k[:rows], v[:rows], *c, table[:2], i32([0, 0]), i32([0, 150, 187]))
+    table[2, :9] = table[0, :9]
+    dash.cache_copy_fp8(*c, [int(table[0, 9])], [int(table[2, 9])])
+    dash.cache_write_fp8(k[rows:], v[rows:], *c, table, i32([150, 37, 150]), i32([0, 1, 2, 3]))
+    now = [151, 38, 151]
+    o, lse = dash.attn_decode_fp8(q[rows:], *c, table, i32(now))
+    dash.dash_sync_status()
+    check(q[rows:], (*c, table), now, D ** -0.5, o, lse)
+    cu = [0, 151, 189, 340]
+    rk, rv = dash.cache_read_fp8(*c, table, i32([0, 0, 0]), i32(cu), 340)
+    fq = torch.zeros(340, hq, D, dtype=torch.bfloat16, device="cuda")
+    last = torch.tensor([150, 188, 339], device="cuda")
+    fq[last] = q[rows:]
+    po, pl = dash.attn_packed_fwd(dash.PackedPlan(now, hq, hkv, D), fq, rk, rv)
+    ro, _, mag = P.decode(q[rows:], R.values(kp, ks), R.values(vp, vs), table, now, D ** -0.5)
+    P.within("packed", po[last], ro, mag)
+    assert (pl[:, last].T - lse).abs().max() <= 2e-4
