@@ -98,6 +98,8 @@ _SIGS = {
     "dash_decode_workspace": ([_I] * 5, _L),
     "dash_cache_write": ([_P] * 7 + [_L] + [_I] * 6 + [_P, _P], _I),
     "dash_cache_copy": ([_P] * 4 + [_I] * 5 + [_P, _P], _I),
+    "dash_attn_decode_shared": ([_P] * 5 + [_I] + [_P] * 2 + [_I] * 7 + [_P, _F, _P, _L, _P], _I),
+    "dash_decode_shared_workspace": ([_I] * 7, _L),
     "dash_attn_decode_fp8": ([_P] * 9 + [_I] * 7 + [_P, _F, _P, _L, _P], _I),
     "dash_cache_write_fp8": ([_P] * 9 + [_L] + [_I] * 6 + [_P, _P], _I),
     "dash_cache_read_fp8": ([_P] * 9 + [_L] + [_I] * 6 + [_P, _P], _I),
@@ -692,6 +694,43 @@ def dash_cache_copy(k_pages, v_pages, src, dst, stream=None):
                                      len(s), hkv, D, n_pages, page, strides, _stream_on(dev, stream)))
 
 
+@functools.lru_cache(maxsize=64)
+def dash_decode_shared_workspace(B: int, heads: int, kv_heads: int, head_dim: int, page_size: int, max_pages: int,
+                                 prefix: int) -> int:
+    return int(lib().dash_decode_shared_workspace(B, heads, kv_heads, head_dim, page_size, max_pages, prefix))
+
+
+def _decode_shared(q, k_pages, v_pages, page_table, lengths, prefix, o, lse, scale, workspace, stream):
+    dev = q.device
+    n_pages, page, hkv, D = k_pages.shape
+    with _device(dev):
+        _check(lib().dash_attn_decode_shared(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), prefix,
+            o.data_ptr(), None if lse is None else lse.data_ptr(), q.shape[0], q.shape[1], hkv, D, n_pages, page,
+            page_table.shape[1], _cache_strides(q, o, k_pages, v_pages, page_table), scale,
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+            _stream_on(dev, stream)))
+
+
+def _prefix(prefix):
+    if not 0 <= prefix < 2**31:
+        raise ValueError("prefix must be a host number of tokens >= 0 that fits 32 bits")
+    return int(prefix)
+
+
+def dash_attn_decode_shared(q, k_pages, v_pages, page_table, lengths, prefix: int, o, lse, scale: float,
+                            workspace=None, stream=None):
+    """``lse`` may be None; ``workspace`` as dash_decode_shared_workspace asks for (uint8)."""
+    _decode_inputs(q, k_pages, v_pages, page_table, lengths)
+    dev = q.device
+    _rows("o", o, q.shape[1], q.shape[2], q.shape[0], dev)
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (q.shape[0], q.shape[1]), dev)
+    if workspace is not None:
+        _plain("workspace", workspace, torch.uint8, (None,), dev)
+    _decode_shared(q, k_pages, v_pages, page_table, lengths, _prefix(prefix), o, lse, float(scale), workspace, stream)
+
+
 # ---- the 8-bit paged cache
 def _cache8(k_pages, v_pages, k_scales, v_scales, device):
     shape = k_pages.shape
@@ -988,6 +1027,22 @@ def cache_copy(k_pages, v_pages, src, dst, stream=None):
     """Copies pages ``src`` to pages ``dst`` (host page numbers) inside the cache, in place."""
     with _using(stream, k_pages, v_pages):
         dash_cache_copy(k_pages, v_pages, src, dst, stream)
+
+
+def attn_decode_shared(q, k_pages, v_pages, page_table, lengths, prefix: int, scale: float | None = None, stream=None):
+    """``attn_decode`` for a batch whose sequences begin with the same ``prefix`` tokens, in the pages that the table's
+    first row names: their K and V are read once for the batch (see dash_attn_decode_shared)."""
+    _decode_inputs(q, k_pages, v_pages, page_table, lengths)
+    B, heads, dim = q.shape
+    prefix = _prefix(prefix)
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, heads), dtype=torch.float32, device=q.device)
+    need = dash_decode_shared_workspace(B, heads, k_pages.shape[2], dim, k_pages.shape[1], page_table.shape[1], prefix)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    with _using(stream, q, k_pages, v_pages, page_table, lengths, o, lse, ws):
+        _decode_shared(q, k_pages, v_pages, page_table, lengths, prefix, o, lse, scale, ws, stream)
+    return o, lse
 
 
 def cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new, stream=None):

@@ -126,7 +126,8 @@ dash_status_t dash_attn_decode_fp8(const void *q, const void *k_pages, const voi
                                    long long workspace_bytes, dash_stream_t stream) {
   dash::Decode8Params p = {};
   dash_status_t st = decode_params(q, page_table, lengths, o, lse, B, Hq, Hkv, D, n_pages, page_size, max_pages,
-                                   strides, strides ? strides + 16 : nullptr, scale, workspace, workspace_bytes, &p);
+                                   strides, strides ? strides + 16 : nullptr, scale, workspace, workspace_bytes,
+                                   dash_decode_workspace(B, Hq, D, page_size, max_pages), 0, 0, &p);
   if (st != DASH_OK || B == 0) return st;
   if ((st = cache8_of(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, Hkv, D,
                       strides ? strides + 4 : nullptr, &p.c)))

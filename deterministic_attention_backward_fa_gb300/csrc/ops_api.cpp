@@ -1,7 +1,9 @@
 // C ABI of the operators around the attention (declared in include/dash.h): the
-// norms of queries and keys with their rotation.
+// norms of queries and keys with their rotation, and the decode of a batch that
+// shares a prefix.
 #include "norm_rope.h"
 #include "ops_host.h"
+#include "shared.h"
 
 using dash::report;
 using namespace dash::host;
@@ -123,6 +125,52 @@ dash_status_t dash_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
   p.status = device.status;
   const cudaError_t e = dash::launch_norm_rope_bwd(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "norm backward launch");
+}
+
+long long dash_decode_shared_workspace(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int prefix) {
+  if (prefix == 0) return dash_decode_workspace(B, Hq, D, page_size, max_pages);
+  if (B < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 || prefix < 0 ||
+      (long long)page_size * max_pages > kMaxCached || prefix > (long long)page_size * max_pages)
+    return -1;
+  const int parts = dash::prefix_cut(std::max(B, 1), Hq, Hkv, prefix).splits +
+                    std::max(1, dash::decode_max_splits(page_size * max_pages - prefix));
+  return (long long)B * Hq * parts * (D * 4 + 8) + 256;
+}
+
+dash_status_t dash_attn_decode_shared(const void *q, const void *k_pages, const void *v_pages,
+                                      const int32_t *page_table, const int32_t *lengths, int prefix, void *o,
+                                      float *lse, int B, int Hq, int Hkv, int D, int n_pages, int page_size,
+                                      int max_pages, const int64_t *strides, float scale, void *workspace,
+                                      long long workspace_bytes, dash_stream_t stream) {
+  if (prefix < 0 || (page_size > 0 && max_pages >= 0 && prefix > (long long)page_size * max_pages))
+    return report(DASH_ERR_INVALID_ARG, "a prefix of %d tokens does not fit %d pages of %d", prefix, max_pages,
+                  page_size);
+  if (prefix == 0)
+    return dash_attn_decode(q, k_pages, v_pages, page_table, lengths, o, lse, B, Hq, Hkv, D, n_pages, page_size,
+                            max_pages, strides, scale, workspace, workspace_bytes, stream);
+  dash_status_t st = check_heads(Hq, Hkv, D);
+  if (st != DASH_OK) return st;
+  if ((long long)B * (Hq / Hkv) > 65535LL * 2 * dash::kPackedTile)
+    return report(DASH_ERR_UNSUPPORTED, "more than %lld rows on one K/V head", 65535LL * 2 * dash::kPackedTile);
+  dash::SharedParams p = {};
+  const dash::PrefixCut cut = dash::prefix_cut(std::max(B, 1), Hq, Hkv, prefix);
+  if ((st = decode_params(q, page_table, lengths, o, lse, B, Hq, Hkv, D, n_pages, page_size, max_pages, strides,
+                          strides ? strides + 10 : nullptr, scale, workspace, workspace_bytes,
+                          dash_decode_shared_workspace(B, Hq, Hkv, D, page_size, max_pages, prefix), prefix,
+                          cut.splits, &p)) != DASH_OK ||
+      B == 0)
+    return st;
+  if ((st = decode_cache(k_pages, v_pages, Hkv, D, n_pages, page_size, strides, &p)) != DASH_OK) return st;
+  p.prefix_tiles = (prefix + dash::kPackedTile - 1) / dash::kPackedTile;
+  p.tiles_per_split = cut.tiles;
+  p.wide = (reinterpret_cast<uintptr_t>(workspace) & 31u) == 0;
+  p.spin_limit_ns = kSpinNs;
+  int dev = 0;
+  Device device;
+  if ((st = current_device(&dev, &device)) != DASH_OK) return st;
+  p.status = device.status;
+  const cudaError_t e = dash::launch_decode_shared(D, p, device.sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DASH_OK : cuda_error(e, "decode launch");
 }
 
 }  // extern "C"

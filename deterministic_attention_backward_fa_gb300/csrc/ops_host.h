@@ -19,6 +19,7 @@ dash_status_t report(dash_status_t code, const char *fmt, ...);  // api.cpp
 
 namespace host {
 
+constexpr long long kSpinNs = 2000000000LL;  // 2 s bound on every device wait
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A failed call's error stays with the thread until it is taken: left there, a
@@ -151,11 +152,13 @@ inline dash_status_t copy_pairs(const int32_t *src, const int32_t *dst, int n, i
 }
 
 // All of a decode's parameters but those of the cache itself.  strides: q
-// {batch, head}, o {batch, head}, then others; table_row: the page table's.
+// {batch, head}, o {batch, head}, then others; table_row: the page table's;
+// `need`: bytes of workspace; the first `first` tokens leave `parts_before` parts.
 inline dash_status_t decode_params(const void *q, const int32_t *page_table, const int32_t *lengths, void *o,
                                    float *lse, int B, int Hq, int Hkv, int D, int n_pages, int page_size,
                                    int max_pages, const int64_t *strides, const int64_t *table_row, float scale,
-                                   void *workspace, long long workspace_bytes, DecodeParams *out) {
+                                   void *workspace, long long workspace_bytes, long long need, int first,
+                                   int parts_before, DecodeParams *out) {
   dash_status_t st = check_scale(scale);
   if (st != DASH_OK || (st = check_heads(Hq, Hkv, D)) || (st = check_cache(Hkv, D, n_pages, page_size))) return st;
   if (B < 0 || max_pages < 0) return report(DASH_ERR_INVALID_ARG, "B and max_pages must be >= 0");
@@ -172,8 +175,7 @@ inline dash_status_t decode_params(const void *q, const int32_t *page_table, con
   DecodeParams &p = *out;
   p.table_row = table_row ? *table_row : max_pages;
   if (B > 1 && p.table_row < max_pages) return report(DASH_ERR_INVALID_ARG, "page table rows overlap");
-  p.max_splits = std::max(1, decode_max_splits(page_size * max_pages));
-  const long long need = dash_decode_workspace(B, Hq, D, page_size, max_pages);
+  p.max_splits = std::max(1, decode_max_splits(page_size * max_pages - first));
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
     return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -183,7 +185,7 @@ inline dash_status_t decode_params(const void *q, const int32_t *page_table, con
   p.o = static_cast<__nv_bfloat16 *>(o);
   p.lse = lse;
   p.part_o = static_cast<float *>(workspace);
-  p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)B * Hq * p.max_splits * D);
+  p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)B * Hq * (parts_before + p.max_splits) * D);
   p.q_batch = rq.row;
   p.q_head = rq.head;
   p.o_batch = ro.row;
@@ -196,7 +198,8 @@ inline dash_status_t decode_params(const void *q, const int32_t *page_table, con
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.hblocks = (p.group + 15) / 16;
-  p.first = p.parts_before = 0;
+  p.first = first;
+  p.parts_before = parts_before;
   p.scale_log2 = scale * kLog2e;
   return DASH_OK;
 }

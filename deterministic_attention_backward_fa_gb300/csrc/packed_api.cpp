@@ -20,6 +20,7 @@
 #include "packed.h"
 #include "ops_host.h"
 #include "packed_plan.h"
+#include "shared.h"
 
 namespace dash {
 dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long long rows, int D,
@@ -28,8 +29,6 @@ dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long 
 
 using dash::report;
 using namespace dash::host;
-
-constexpr long long kSpinNs = 2000000000LL;  // 2 s bound on every device wait
 
 // A plan: the tables of one set of lengths on the device it was made on.
 struct dash_packed_plan_st {
@@ -86,7 +85,8 @@ dash_status_t dash::host::current_device(int *dev, Device *out) try {
     cudaThreadExchangeStreamCaptureMode(&mode);
     if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, *dev)) != cudaSuccess ||
         (e = dash::prepare_decode()) != cudaSuccess || (e = dash::prepare_norm_rope()) != cudaSuccess ||
-        (e = dash::prepare_cache8()) != cudaSuccess || (e = dash::ops_status_address(&d.status)) != cudaSuccess)
+        (e = dash::prepare_cache8()) != cudaSuccess || (e = dash::prepare_shared()) != cudaSuccess ||
+        (e = dash::ops_status_address(&d.status)) != cudaSuccess)
       d.status = nullptr;
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return cuda_error(e, "device set-up");
@@ -359,7 +359,8 @@ dash_status_t dash_attn_decode(const void *q, const void *k_pages, const void *v
                                void *workspace, long long workspace_bytes, dash_stream_t stream) {
   dash::DecodeParams p;
   dash_status_t st = decode_params(q, page_table, lengths, o, lse, B, Hq, Hkv, D, n_pages, page_size, max_pages,
-                                   strides, strides ? strides + 10 : nullptr, scale, workspace, workspace_bytes, &p);
+                                   strides, strides ? strides + 10 : nullptr, scale, workspace, workspace_bytes,
+                                   dash_decode_workspace(B, Hq, D, page_size, max_pages), 0, 0, &p);
   if (st != DASH_OK || B == 0) return st;
   if ((st = decode_cache(k_pages, v_pages, Hkv, D, n_pages, page_size, strides, &p)) != DASH_OK) return st;
   int dev = 0;

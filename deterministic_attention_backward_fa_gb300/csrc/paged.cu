@@ -362,7 +362,7 @@ template <int D>
 cudaError_t launch_decode_t(const DecodeParams &p, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D>;
   const long long items = (long long)p.B * p.max_splits * p.Hkv * p.hblocks;
-  if (decode_clustered(p.B, p.Hq, p.max_splits)) {
+  if (p.parts_before == 0 && decode_clustered(p.B, p.Hq, p.max_splits)) {
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = p.max_splits;

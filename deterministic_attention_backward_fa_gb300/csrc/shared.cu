@@ -1,0 +1,408 @@
+// Decode attention over a prefix that all sequences of a batch share, computed
+// once for all.  The rows (sequence, Q head) of a K/V head's group form one
+// matrix: B x group rows attend the same tokens, which is attention of many
+// queries on one key sequence, so the tensor cores take it and K and V are read
+// once per 256 rows.  Each CTA has (split of the prefix, up to two tiles of 128
+// rows, K/V head) and leaves per row its softmax average with maximum and sum,
+// as a split of dash_decode_kernel does; that kernel attends the tokens behind
+// the prefix, and the same join adds all parts.
+//
+// Per row one pass over the split's KV tiles of 128 tokens:
+//   m' = max(m, max_j x_j),  l' = l 2^(m-m') + sum_j 2^(x_j - m'),
+//   O' = O 2^(m-m') + P V,   x = scale log2(e) q.k,  P = 2^(x - m'),
+// with S, P (bf16, in S's place) and O in tensor memory.  The maximum moves when
+// it has grown by 2^8 (kLazy), or from nothing.
+//
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a thread owns a row), 8 and 9 MMA
+// issue for tile 0 and 1, 12-15 fetch K and V: a token's row lies wherever its
+// page does, so rows are fetched with 16-byte asynchronous copies (16 lanes a
+// row at D = 128) into the swizzled layout that the MMAs read, three tiles ahead
+// of the one that is handed over.
+#include <cuda_runtime.h>
+
+#include "packed.h"
+#include "shared.h"
+#include "sm103.cuh"
+
+namespace dash {
+
+using namespace dev;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRegsLaunch = 128;   // 512 threads x 128 registers
+constexpr int kRegsSoftmax = 176;  // a row of S in registers
+constexpr int kRegsOther = 80;
+static_assert(2 * 128 * kRegsSoftmax + 2 * 128 * kRegsOther <= kRegsLaunch * kThreads,
+              "register split exceeds the CTA's allocation");
+constexpr float kLazy = 8.f;
+constexpr int kLag = 3;    // loads in flight; see the producer
+constexpr int kMasks = 4;  // tiles whose masks are held
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kTile = 128 * D * 2;
+  static constexpr uint32_t kPanel = 128 * 128;
+  static constexpr int kStages = 5;  // K and V tiles in turn
+  static constexpr uint32_t oQ = 0;  // two Q tiles
+  static constexpr uint32_t oKV = 2 * kTile;
+  static constexpr uint32_t oBAR = oKV + kStages * kTile;
+  static constexpr int kNumBars = 8 + kMasks + 2 * kStages;
+  static constexpr uint32_t oMISC = oBAR + kNumBars * 8;
+  static constexpr uint32_t oMASK = oMISC + 16;
+  static constexpr uint32_t kSmemBytes = oMASK + kMasks * 16;
+  static constexpr uint32_t cO = 256;
+};
+static_assert(Cfg<128>::kSmemBytes <= 232448, "shared memory of one CTA");
+// A stage is filled again when the load kStages before has been read.  V of tile
+// j is read once K of j + 1 has been handed over, one load on, which happens
+// kLag loads later: kLag + 1 < kStages, or the producer would wait for itself.
+static_assert(kLag + 1 < Cfg<128>::kStages, "loads ahead");
+
+enum { bSFull = 0, bPFull = 2, bOFull = 4, bFinal = 6, bMask = 8, bKvFull0 = 8 + kMasks };
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: fills with zeros, reads nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_constant__ SharedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = warp_id(), lane = threadIdx.x & 31;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBAR);
+  uint64_t *kvFull = bars + bKvFull0, *kvEmpty = kvFull + C::kStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::oMISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + C::oMASK);  // [kMasks][4]: tokens that count
+
+  const int split = blockIdx.x, hk = blockIdx.z;
+  const int rows = p.B * p.group, row0 = blockIdx.y * 2 * kPackedTile;
+  const int tiles = rows - row0 > kPackedTile ? 2 : 1;  // Q tiles
+  const int j0 = split * p.tiles_per_split, n = min(p.tiles_per_split, p.prefix_tiles - j0);
+
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[bSFull + s], 1);
+      mbar_init(&bars[bPFull + s], 4);
+      mbar_init(&bars[bOFull + s], 1);
+      mbar_init(&bars[bFinal + s], 1);
+    }
+    for (int i = 0; i < kMasks; ++i) mbar_init(&bars[bMask + i], 4);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&kvFull[s], 4);       // the producer's warps
+      mbar_init(&kvEmpty[s], tiles);  // the MMA warps
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
+
+  if (warp >= 12) {
+    // -------------------------------------------------------------- loads
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    const int w = warp - 12;
+    constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;  // 16-byte pieces of a row, rows of a warp's copy
+    const int c = lane % kChunks, rsub = lane / kChunks;
+    const uint32_t col = (uint32_t)(c >> 3) * C::kPanel;
+    // Q, with the first K tile's group; rows past the last are zero
+    for (int s = 0; s < tiles; ++s)
+#pragma unroll 4
+      for (int i = 0; i < 32 / kRowsPer; ++i) {
+        const int r = w * 32 + i * kRowsPer + rsub, row = row0 + s * kPackedTile + r;
+        const bool ok = row < rows;
+        const int b = ok ? row / p.group : 0, h = hk * p.group + (ok ? row - b * p.group : 0);
+        cp16(smem_u32(smem + C::oQ + s * C::kTile) + col + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+             p.q + b * p.q_batch + h * p.q_head + 8 * c, ok);
+      }
+    const int *table = p.table;  // the prefix's pages are those of the first sequence
+    auto page_of = [&](int j) -> int {
+      const int t = (j0 + j) * kPackedTile + w * 32 + lane;
+      return j < n && t < p.first ? table[t / p.page_size] : -1;
+    };
+    Ring<C::kStages> r, done;
+    int loads = 0, page = page_of(0);
+    auto hand_over = [&]() {
+      fence_proxy_async_smem();  // the copies' writes, before the MMAs read them
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kvFull[done.st]);
+      done.next();
+    };
+    for (int j = 0; j < n; ++j) {
+      const int t = (j0 + j) * kPackedTile + w * 32 + lane;
+      const bool ok = page >= 0 && page < p.n_pages;
+      if (t < p.first && !ok) atomicCAS(p.status, 0, kStatusBadPage);
+      const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+      const int off = t % p.page_size;
+      const long long ka = ok ? page * p.ks.page + off * p.ks.token + hk * p.ks.head : 0;
+      const long long va = ok ? page * p.vs.page + off * p.vs.token + hk * p.vs.head : 0;
+      page = page_of(j + 1);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        mbar_wait(&kvEmpty[r.st], r.ph ^ 1, g);
+        __syncwarp();
+        if (which == 0) {
+          // the masks kMasks tiles before have been read: their P was, by the products that freed this stage
+          if (lane == 0) {
+            masks[(j % kMasks) * 4 + w] = valid;
+            mbar_arrive(&bars[bMask + j % kMasks]);
+          }
+        }
+        const __nv_bfloat16 *base = which ? p.v : p.k;
+        const uint32_t dst = smem_u32(smem + C::oKV + r.st * C::kTile) + col;
+        if (!warp_aborted(g)) {
+#pragma unroll
+          for (int i = 0; i < 32 / kRowsPer; ++i) {
+            const int from = i * kRowsPer + rsub, rr = w * 32 + from;
+            const long long a = __shfl_sync(0xffffffffu, which ? va : ka, from);
+            cp16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), base + a + 8 * c, (valid >> from) & 1u);
+          }
+        }
+        cp_commit();
+        r.next();
+        if (++loads > kLag) {
+          cp_wait<kLag>();
+          hand_over();
+        }
+      }
+    }
+    cp_wait<0>();
+    for (int i = min(loads, kLag); i > 0; --i) hand_over();
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    const int s = warp - 8;
+    if (s < tiles) {
+      // --------------------------------------- MMA: a warp for each Q tile
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
+      Ring<C::kStages> rk;          // next K or V tile to be read
+      uint32_t p_ph = 0;
+      uint32_t lead = elect_one();  // 0 in every lane once a wait has failed: nothing more is issued
+      const uint64_t dq = sw128_desc(smem_u32(smem + C::oQ + s * C::kTile), 16, 1024);
+      const uint64_t dk0 = sw128_desc(smem_u32(smem + C::oKV), 16, 1024);
+      const uint64_t dv0 = sw128_desc(smem_u32(smem + C::oKV), C::kPanel, 1024);
+      const uint32_t tS = tmem + s * 128, tO = tmem + C::cO + s * D;
+      auto wait = [&](uint64_t *bar, uint32_t ph) {
+        if (!mbar_wait(bar, ph, g)) lead = 0;
+      };
+      auto issue_s = [&](int stage) {
+        tc_fence_after();
+        const uint64_t dk = dk0 + ((stage * C::kTile) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
+          mma_ss_if(lead, tS, dq + off, dk + off, idS, kk > 0);
+        }
+        tc_commit_if(lead, &bars[bSFull + s]);
+      };
+      wait(&kvFull[rk.st], rk.ph);  // Q and the first K tile
+      issue_s(rk.st);
+      tc_commit_if(lead, &kvEmpty[rk.st]);
+      rk.next();
+      for (int j = 0; j < n; ++j) {
+        const Ring<C::kStages> rv = rk;  // V tile j; the next K tile follows it in the ring
+        rk.next();
+        wait(&kvFull[rv.st], rv.ph);
+        if (j + 1 < n) wait(&kvFull[rk.st], rk.ph);
+        const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
+        wait(&bars[bPFull + s], p_ph);
+        p_ph ^= 1;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
+        tc_commit_if(lead, &kvEmpty[rv.st]);
+        if (j + 1 < n) {
+          issue_s(rk.st);  // MMAs run in issue order: PV has read P before S overwrites it
+          tc_commit_if(lead, &kvEmpty[rk.st]);
+          rk.next();
+        } else {
+          tc_commit_if(lead, &bars[bOFull + s]);
+        }
+      }
+      // every MMA has completed before tensor memory is released (at once if none was issued)
+      tc_commit_if(elect_one(), &bars[bFinal + s]);
+      mbar_drain(&bars[bFinal + s], 0, g.limit_ns);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int s = warp >> 2, sub = warp & 3;
+    if (s < tiles) {
+      const int row = row0 + s * kPackedTile + sub * 32 + lane;
+      const bool real = row < rows;
+      const int b = real ? row / p.group : 0, h = hk * p.group + (real ? row - b * p.group : 0);
+      const uint32_t tl = tmem + ((uint32_t)(sub * 32) << 16);
+      const uint32_t tS = tl + s * 128, tO = tl + C::cO + s * D;
+      // tokens of the split that this row attends: a sequence may end inside the prefix
+      const int limit =
+          (real ? max(0, min(min(p.lengths[b], p.max_pages * p.page_size), p.first)) : 0) - j0 * kPackedTile;
+      float m = -INFINITY, l = 0.f;  // the maximum the row refers to (scaled, log2; -inf: nothing counted yet), its sum
+      // After an abort the loop runs on with whatever tensor memory holds: no
+      // wait blocks any more, and the status word tells that O is not valid.
+      for (int j = 0; j < n; ++j) {
+        mbar_wait(&bars[bMask + j % kMasks], (j / kMasks) & 1, g);
+        uint32_t valid[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) valid[c] = masks[(j % kMasks) * 4 + c];
+        const int cols = limit - j * kPackedTile;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int k = cols - 32 * c;
+          valid[c] &= k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+        }
+        mbar_wait(&bars[bSFull + s], j & 1, g);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, x[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_order32(x[c]);
+        if (__any_sync(0xffffffffu, (valid[0] & valid[1] & valid[2] & valid[3]) != 0xffffffffu)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((valid[c] >> e) & 1u)) x[c][e] = 0xff800000u;  // -inf
+        }
+        float mx[4];  // four chains side by side
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+#pragma unroll
+        for (int e = 2; e < 32; e += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(x[c][e])), __uint_as_float(x[c][e + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool moves = top > m + kLazy;
+        if (__any_sync(0xffffffffu, moves)) {
+          // the product before has completed (it did before S(j) did), so O may be rewritten here
+          const float m_new = moves ? top : m;
+          const float f = moves ? ex2(m - m_new) : 1.f;
+          m = m_new;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t r[16];
+              tmem_ld16(tO + c0, r);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tmem_st16(tO + c0, r);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[4] = {l, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float a0 = ex2(fmaf(__uint_as_float(x[c][e]), p.scale_log2, -ref));
+            const float a1 = ex2(fmaf(__uint_as_float(x[c][e + 1]), p.scale_log2, -ref));
+            sum[e / 2 & 3] += a0 + a1;
+            pk[e >> 1] = pack_bf16(a0, a1);
+          }
+          tmem_st16(tS + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[bPFull + s]);
+        l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      const bool ok = mbar_wait(&bars[bOFull + s], 0, g);
+      __syncwarp();
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t at = ((size_t)b * p.Hq + h) * (p.parts_before + p.max_splits) + split;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(tO + c0, r);
+        if (real && ok) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) st_32b(p.part_o + at * D + c0 + e, r + e, p.wide);
+        }
+      }
+      if (real && ok) p.part_ml[at] = make_float2(m, l);
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int smem_bytes() {
+  return Cfg<D>::kSmemBytes > (uint32_t)kMinSmemOneCtaPerSm ? (int)Cfg<D>::kSmemBytes : kMinSmemOneCtaPerSm;
+}
+
+template <int D>
+cudaError_t prepare_t() {
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, dash_prefix_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+  return cudaFuncSetAttribute(dash_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+}
+
+}  // namespace
+
+cudaError_t prepare_shared() {
+  const cudaError_t e = prepare_t<64>();
+  return e != cudaSuccess ? e : prepare_t<128>();
+}
+
+cudaError_t launch_decode_shared(int D, const SharedParams &p, int num_sms, cudaStream_t stream) {
+  const dim3 grid(p.parts_before, (unsigned)(((long long)p.B * p.group + 2 * kPackedTile - 1) / (2 * kPackedTile)),
+                  p.Hkv);
+  const cudaError_t e =
+      D == 64 ? launch(dash_prefix_kernel<64>, grid, kThreads, smem_bytes<64>(), stream, nullptr, p)
+              : launch(dash_prefix_kernel<128>, grid, kThreads, smem_bytes<128>(), stream, nullptr, p);
+  return e != cudaSuccess ? e : launch_decode(D, p, num_sms, stream);
+}
+
+}  // namespace dash

@@ -571,6 +571,24 @@ dash_status_t dash_cache_write(const void *k, const void *v, void *k_pages, void
 dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, const int32_t *dst, int n, int Hkv,
                               int D, int n_pages, int page_size, const int64_t *strides, dash_stream_t stream);
 
+/* As dash_attn_decode, for a batch whose sequences begin with the same `prefix`
+ * tokens (a host value, 0 <= prefix <= max_pages * page_size): those lie in the
+ * pages that the table's first row names, and the other rows' entries for them
+ * are not read, but for a page that the prefix fills in part, which every
+ * sequence continues in the page of its own row.  Their K and V are read once
+ * for the batch instead of once per sequence.  `lengths` count the prefix; a
+ * sequence may also end inside it.  The parts are cut by the sizes alone, so a
+ * call's bits are the same in every run; they depend on B and prefix, unlike
+ * those of dash_attn_decode, which a prefix of 0 is.  Workspace:
+ * dash_decode_shared_workspace() bytes.  A device wait that lasts 2 s ends the
+ * call, and dash_sync_status reports DASH_ERR_TIMEOUT. */
+dash_status_t dash_attn_decode_shared(const void *q, const void *k_pages, const void *v_pages,
+                                      const int32_t *page_table, const int32_t *lengths, int prefix, void *o,
+                                      float *lse, int B, int Hq, int Hkv, int D, int n_pages, int page_size,
+                                      int max_pages, const int64_t *strides, float scale, void *workspace,
+                                      long long workspace_bytes, dash_stream_t stream);
+long long dash_decode_shared_workspace(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int prefix);
+
 /* -------------------------------------------- 8-bit paged key-value cache
  * The paged cache in half the bytes.  k_pages and v_pages are e4m3
  * [n_pages][page_size][Hkv][D] (strides {page, token, head}, multiples of 16 of
