@@ -13,11 +13,11 @@
 //   x_t = scale log2(e) a_t (q . k_t),  o = (1/l) sum 2^(x_t - m) c_t v_t.
 // The codes are widened to f16, which holds them exactly, and multiplied there:
 //   S^T [16 tokens x 8 heads] = K Q^T,   O^T [16 dims x 8 heads] += V^T P^T
-// so that the codes are the large operand, read straight from global memory into
-// the lanes that need them (16 tokens' K and V are 8 loads of 16 bytes a lane),
-// and the 8 columns are the heads of a group: no shared memory stands between.
-// Contraction order is free, so a lane takes what lies side by side: of K the
-// 16 bytes at 16 (lane % 4) of two tokens, of V the same D / 8 dims of four.
+// so that the codes are the large operand and the 8 columns are the heads of a
+// group.  Contraction order is free, so a lane takes what lies side by side: of K
+// the 16 bytes at 16 (lane % 4) of two tokens, of V the same D / 8 dims of four;
+// what it multiplies, it has fetched itself, and its asynchronous copies need
+// shared memory only as a queue of its own: no swizzle, no ldmatrix, no exchange.
 // Q is multiplied by a power of two first (its largest value lands at 2^14), so
 // that f16 holds its 8 bits down to 2^-29 of that.
 // P goes to f16 as 2^(x_t - M) c_t with M the maximum of x_t + log2 c_t of its
@@ -277,43 +277,70 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 ld16(const uint8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ int quotient(const Divisor &d, int n) {
+  return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
 }
-__device__ __forceinline__ uint2 ld8(const uint8_t *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+template <class T>
+__device__ __forceinline__ const T *wide_add(const T *p, int a, int b) {
+  return p + (long long)a * b;
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+  if (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async_if(uint32_t dst, const void *src, bool valid) {
+  const int n = valid ? kBytes : 0;  // 0: fills with zeros, reads nothing
+  if (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Sixteen tokens as a lane holds them: of tokens g and g + 8 its 16-byte pieces
-// of K and both scales, of tokens 2t, 2t + 1, 2t + 8, 2t + 9 its dims of V
-// (g = lane / 4, t = lane % 4).
+// A step of a warp in its queue: 16 tokens.  Pieces stand lane by lane: of tokens
+// g and g + 8 the lane's 16-byte pieces of K, of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+// its D / 8 bytes of V (g = lane / 4, t = lane % 4); then 16 scales of K, 16 of V.
 template <int D>
-struct Tokens {
+struct Queue {
+  static constexpr int kStages = 3;
   static constexpr int kK = D / 64, kV = D / 32;  // 16-byte pieces of a K row, words of V
-  uint4 k[2][kK];
-  uint32_t v[4][kV];
-  float ks[2], vs[2];
-  uint32_t valid;
+  static constexpr int kVBytes = D / 8;
+  static constexpr int oV = 2 * kK * 512, oScale = oV + 4 * 32 * kVBytes;
+  static constexpr int kStage = oScale + 128;
+  static constexpr int kWarpBytes = kStages * kStage;
+};
+
+// Dynamic shared memory: the queues; their place is reused to join the warps, and
+// in a cluster for the split's own result.
+template <int D, int NT>
+struct Dec8 {
+  static constexpr int oMl = kWarps * 8 * NT * D * 4, oPart = oMl + kWarps * 8 * NT * 8;
+  static constexpr int kJoin = oPart + 16 * (D * 4 + 8);
+  static constexpr int kCtas = NT == 1 ? 4 : 2;  // on an SM
+  static constexpr int kSmem = kWarps * Queue<D>::kWarpBytes > kJoin ? kWarps * Queue<D>::kWarpBytes : kJoin;
 };
 
 // NT tiles of 8 Q heads.
 template <int D, int NT, Deal kDeal>
-__global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kDecodeThreads, Dec8<D, NT>::kCtas)
     dash_decode8_kernel(const __grid_constant__ Decode8Params p) {
-  using T = Tokens<D>;
-  constexpr int kRowF = 8 * NT * D;                         // floats of a warp's result
-  __shared__ __align__(16) float s_o[kWarps * kRowF];       // [warp][head][D]
-  __shared__ float2 s_ml[kWarps * 8 * NT];
-  __shared__ __align__(16) uint8_t s_part[kDeal == kCluster ? 16 * (D * 4 + 8) : 16];
+  using Q = Queue<D>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float *s_o = reinterpret_cast<float *>(smem);                                       // [warp][head][D]
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + Dec8<D, NT>::oMl);                 // [warp][head]
+  uint8_t *s_part = smem + Dec8<D, NT>::oPart;
   // the join may be set up now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  uint8_t *queue = smem + warp * Q::kWarpBytes;
   Items<kDeal> it;
   for (long long item = blockIdx.x;; item += gridDim.x) {
     const int found = it.find(p, item);
@@ -331,51 +358,74 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
     const uint8_t *kbase = p.c.k + hk * p.c.ks.head, *vbase = p.c.v + hk * p.c.vs.head;
     const float *ksbase = p.c.k_scale + hk * p.c.kss.head, *vsbase = p.c.v_scale + hk * p.c.vss.head;
 
-    // Lanes 0-15 know where a token of the step lies, lanes 16-31 likewise.
+    // Where the lane's pieces lie, but for the page and the step's place in it.
+    const uint8_t *klane = kbase + g * p.c.ks.token + 16 * t4, *vlane = vbase + 2 * t4 * p.c.vs.token + Q::kVBytes * g;
+    const CacheStrides &ss = lane < 16 ? p.c.kss : p.c.vss;
+    const float *sbase = lane < 16 ? ksbase : vsbase, *slane = sbase + (lane & 15) * ss.token;
+    const int sp = (int)ss.page, st = (int)ss.token;  // only used where they fit
+
+    // Lanes 0-15 know the page of a token of the step, lanes 16-31 likewise.
     auto page_of = [&](int step) -> int {
       const int t = begin + step * kStep + warp * kTok + (lane & 15);
-      return t < end ? table[t / p.page_size] : -1;
+      return t < end ? table[quotient(p.page, t)] : -1;
     };
-    auto load = [&](T &x, int step, int page) {
+    // Asks for a step's tokens; returns a bit for each that counts.
+    auto load = [&](int step, int slot, int page) -> uint32_t {
       const int t = begin + step * kStep + warp * kTok + (lane & 15);
       const bool inside = step < steps && t < end;
       const bool ok = inside && page >= 0 && page < p.n_pages;
-      if (inside && !ok) atomicCAS(p.status, 0, kStatusBadPage);
-      const int off = t % p.page_size;
-      x.valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const uint32_t dst = smem_u32(queue) + slot * Q::kStage;
+      if (valid == 0xffffu && p.whole) {
+        const int off = t - (lane & 15) - quotient(p.page, t) * p.page_size;
+        const uint8_t *kr = wide_add(wide_add(klane, off, (int)p.c.ks.token), page, (int)p.c.ks.page);
+        const uint8_t *vr = wide_add(wide_add(vlane, off, (int)p.c.vs.token), page, (int)p.c.vs.page);
+        const uint32_t kd = dst + lane * 16, vd = dst + Q::oV + lane * Q::kVBytes;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int tok = g + 8 * r;
-        const long long pg = __shfl_sync(0xffffffffu, page, tok);
-        const int of = __shfl_sync(0xffffffffu, off, tok);
-        const bool v = (x.valid >> tok) & 1u;
-        const uint8_t *row = kbase + pg * p.c.ks.page + of * p.c.ks.token + 16 * t4;
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int i = 0; i < T::kK; ++i) x.k[r][i] = v ? ld16(row + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
-        x.ks[r] = v ? __ldg(ksbase + pg * p.c.kss.page + of * p.c.kss.token) : 0.f;
-        x.vs[r] = v ? __ldg(vsbase + pg * p.c.vss.page + of * p.c.vss.token) : 0.f;
-      }
+          for (int i = 0; i < Q::kK; ++i)
+            cp_async<16>(kd + (r * Q::kK + i) * 512, kr + 8 * r * p.c.ks.token + 64 * i);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = 2 * t4 + (r & 1) + 8 * (r >> 1);
-        const long long pg = __shfl_sync(0xffffffffu, page, tok);
-        const int of = __shfl_sync(0xffffffffu, off, tok);
-        const bool v = (x.valid >> tok) & 1u;
-        const uint8_t *row = vbase + pg * p.c.vs.page + of * p.c.vs.token + (D / 8) * g;
-        if (D == 128) {
-          const uint4 w = v ? ld16(row) : make_uint4(0u, 0u, 0u, 0u);
-          x.v[r][0] = w.x, x.v[r][1] = w.y, x.v[r][T::kV - 2] = w.z, x.v[r][T::kV - 1] = w.w;
-        } else {
-          const uint2 w = v ? ld8(row) : make_uint2(0u, 0u);
-          x.v[r][0] = w.x, x.v[r][1] = w.y;
+        for (int r = 0; r < 4; ++r)
+          cp_async<Q::kVBytes>(vd + r * 32 * Q::kVBytes, vr + ((r & 1) + 8 * (r >> 1)) * p.c.vs.token);
+        cp_async<4>(dst + Q::oScale + lane * 4, wide_add(wide_add(slane, off, st), page, sp));
+      } else if (step < steps) {
+        if (inside && !ok) atomicCAS(p.status, 0, kStatusBadPage);
+        const int off = t - quotient(p.page, t) * p.page_size;
+        // a token that does not count is read nowhere: its pieces are zero
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int tok = g + 8 * r, pg = __shfl_sync(0xffffffffu, page, tok), of = __shfl_sync(0xffffffffu, off, tok);
+          const bool v = (valid >> tok) & 1u;
+          const uint8_t *row = v ? kbase + pg * p.c.ks.page + of * p.c.ks.token + 16 * t4 : p.c.k;
+#pragma unroll
+          for (int i = 0; i < Q::kK; ++i)
+            cp_async_if<16>(dst + (r * Q::kK + i) * 512 + lane * 16, row + (v ? 64 * i : 0), v);
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int tok = 2 * t4 + (r & 1) + 8 * (r >> 1);
+          const int pg = __shfl_sync(0xffffffffu, page, tok), of = __shfl_sync(0xffffffffu, off, tok);
+          const bool v = (valid >> tok) & 1u;
+          cp_async_if<Q::kVBytes>(dst + Q::oV + (r * 32 + lane) * Q::kVBytes,
+                                  v ? vbase + pg * p.c.vs.page + of * p.c.vs.token + Q::kVBytes * g : p.c.v, v);
+        }
+        cp_async_if<4>(dst + Q::oScale + lane * 4, ok ? sbase + page * ss.page + off * ss.token : sbase, ok);
       }
+      cp_commit();
+      return valid;
     };
 
-    T x[2];
+    constexpr int kAhead = Q::kStages - 1;
+    uint64_t fifo = 0;  // 16 bits for each step ahead
     int page = page_of(0);
-    load(x[0], 0, page);
-    page = page_of(1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int next = page_of(i + 1);
+      fifo |= (uint64_t)load(i, i, page) << (16 * i);
+      page = next;
+    }
 
     // Q: head g of each tile, the 16 values of each K piece; its power of two goes into the score's factor
     uint32_t qf[NT][D / 16][2];
@@ -425,42 +475,68 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
         l[nt][c] = 0.f;
       }
 
-    auto compute = [&](const T &x) {
-      float s[NT][4] = {};
+    int slot = 0;
+    for (int step = 0; step < steps; ++step) {
+      const int next = page_of(step + kAhead + 1);
+      const uint32_t valid = (uint32_t)fifo & 0xffffu;
+      fifo = fifo >> 16 | (uint64_t)load(step + kAhead, slot == 0 ? kAhead : slot - 1, page) << (16 * (kAhead - 1));
+      page = next;
+      cp_wait<kAhead>();
+      __syncwarp();  // the scales of other lanes
+      const uint8_t *here = queue + slot * Q::kStage;
+      slot = slot == kAhead ? 0 : slot + 1;
+      const float *scales = reinterpret_cast<const float *>(here + Q::oScale);
+      const float ks[2] = {scales[g], scales[g + 8]}, vs[2] = {scales[16 + g], scales[24 + g]};
+      float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products
 #pragma unroll
-      for (int i = 0; i < T::kK; ++i) {
-        const uint32_t w0[4] = {x.k[0][i].x, x.k[0][i].y, x.k[0][i].z, x.k[0][i].w};
-        const uint32_t w1[4] = {x.k[1][i].x, x.k[1][i].y, x.k[1][i].z, x.k[1][i].w};
+      for (int i = 0; i < Q::kK; ++i) {
+        const uint4 k0 = *reinterpret_cast<const uint4 *>(here + i * 512 + lane * 16);
+        const uint4 k1 = *reinterpret_cast<const uint4 *>(here + (Q::kK + i) * 512 + lane * 16);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t a0 = widen8(w0[w]), a1 = widen8(w1[w]), a2 = widen8(w0[w] >> 16), a3 = widen8(w1[w] >> 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(w & 1 ? s2[nt] : s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
         }
       }
       // s[nt][2 r + c]: token g + 8 r, head 2 t4 + c
-      float pv[NT][4];
-      bool fast = true;
+      float pr[NT][4], pv[NT][4], lsum[NT][2], most = 0.f;
+      if (valid != 0xffffu) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = e >> 1, c = e & 1;
-          const float y = s[nt][e] * sc[nt][c] * x.ks[r];
-          s[nt][e] = (x.valid >> (g + 8 * r)) & 1u ? y : -INFINITY;
-        }
-      float pr[NT][4];
+          for (int e = 0; e < 4; ++e)
+            if (!((valid >> (g + 8 * (e >> 1))) & 1u)) s[nt][e] = s2[nt][e] = -INFINITY;
+      }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = e >> 1, c = e & 1;
-          pr[nt][e] = ex2(s[nt][e] - m[nt][c]);
-          pv[nt][e] = pr[nt][e] * (x.vs[r] * up[nt][c]);
-          fast = fast && pr[nt][e] <= kLazy && pv[nt][e] <= kLazy;  // false for NaN
+          s[nt][e] += s2[nt][e];
+          pr[nt][e] = ex2(fmaf(s[nt][e], sc[nt][c] * ks[r], -m[nt][c]));
+          pv[nt][e] = pr[nt][e] * (vs[r] * up[nt][c]);
         }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          lsum[nt][c] = pr[nt][c] + pr[nt][2 + c];
+          most += lsum[nt][c] + (pv[nt][c] + pv[nt][2 + c]);
+        }
+      }
+      // All terms are >= 0: where their sum is within the limit, each is.  A NaN is not within it, and a token that
+      // does not count is one here (-inf times its zero scale).
+      const bool fast = most <= kLazy;
       if (!__all_sync(0xffffffffu, fast)) {
-        const float lv[2] = {lg2(x.vs[0]), lg2(x.vs[1])};
+        const float lv[2] = {lg2(vs[0]), lg2(vs[1])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = s[nt][e] * (sc[nt][e & 1] * ks[e >> 1]);
+            s[nt][e] = (valid >> (g + 8 * (e >> 1))) & 1u ? y : -INFINITY;
+          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float fo[2];
@@ -485,6 +561,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
               pr[nt][2 * r + c] = ex2(s[nt][2 * r + c] - mr);
               pv[nt][2 * r + c] = ex2(s[nt][2 * r + c] + lv[r] - Mr);
             }
+            lsum[nt][c] = pr[nt][c] + pr[nt][2 + c];
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
@@ -496,32 +573,37 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) l[nt][c] += pr[nt][c] + pr[nt][2 + c];
+        for (int c = 0; c < 2; ++c) l[nt][c] += lsum[nt][c];
         pb[nt][0] = transpose8x8(pack_f16(pv[nt][0], pv[nt][1]));
         pb[nt][1] = transpose8x8(pack_f16(pv[nt][2], pv[nt][3]));
       }
+      uint32_t v[4][Q::kV];
 #pragma unroll
-      for (int w = 0; w < T::kV; ++w)
+      for (int r = 0; r < 4; ++r) {
+        const uint8_t *at = here + Q::oV + (r * 32 + lane) * Q::kVBytes;
+        if (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(at);
+          v[r][0] = w.x, v[r][1] = w.y, v[r][Q::kV - 2] = w.z, v[r][Q::kV - 1] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2 *>(at);
+          v[r][0] = w.x, v[r][1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < Q::kV; ++w)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           // dims 2 half, 2 half + 1 of the word: {first, second token} pairs of codes
-          const uint32_t y0 = __byte_perm(x.v[0][w], x.v[1][w], half ? 0x7362 : 0x5140);
-          const uint32_t y1 = __byte_perm(x.v[2][w], x.v[3][w], half ? 0x7362 : 0x5140);
+          const uint32_t y0 = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
+          const uint32_t y1 = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
           const uint32_t a0 = widen8(y0), a1 = widen8(y0 >> 16), a2 = widen8(y1), a3 = widen8(y1 >> 16);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][2 * w + half], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
         }
-    };
-
-    for (int step = 0; step < steps; step += 2) {
-      load(x[1], step + 1, page);
-      page = page_of(step + 2);
-      compute(x[0]);
-      if (step + 1 >= steps) break;
-      load(x[0], step + 2, page);
-      page = page_of(step + 3);
-      compute(x[1]);
+      __syncwarp();  // every lane has read the slot that the next step fills
     }
+    cp_wait<0>();
+    __syncthreads();  // every warp has left its queue
 
     // ---- each warp's average with its maximum and sum, then their join
 #pragma unroll
@@ -534,7 +616,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
         const float f = l[nt][c] == 0.f ? 0.f : ex2(M[nt][c] - m[nt][c]), inv = inverse_sum(l[nt][c]);
         float *o = s_o + (warp * 8 * NT + row) * D + (D / 8) * g;
 #pragma unroll
-        for (int w = 0; w < T::kV; ++w)
+        for (int w = 0; w < Q::kV; ++w)
           *reinterpret_cast<float4 *>(o + 4 * w) =
               make_float4(acc[nt][2 * w][c] * inv * f, acc[nt][2 * w][2 + c] * inv * f,
                           acc[nt][2 * w + 1][c] * inv * f, acc[nt][2 * w + 1][2 + c] * inv * f);
@@ -584,27 +666,29 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 3 : 2)
 
 template <int D, int NT>
 cudaError_t launch_decode_t(const Decode8Params &p, int num_sms, cudaStream_t stream) {
+  constexpr int kSmem = Dec8<D, NT>::kSmem;
   const long long items = (long long)p.B * p.max_splits * p.Hkv * p.hblocks;
   if (decode_clustered(p.B, p.Hq, p.max_splits)) {
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = p.max_splits;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    return launch(dash_decode8_kernel<D, NT, kCluster>, (int)items, kDecodeThreads, 0, stream, &attr, p);
+    return launch(dash_decode8_kernel<D, NT, kCluster>, (int)items, kDecodeThreads, kSmem, stream, &attr, p);
   }
-  const int resident = (NT == 1 ? 3 : 2) * num_sms;
+  const int resident = Dec8<D, NT>::kCtas * num_sms;
   const bool all = items <= resident;
   const cudaError_t e = launch(all ? dash_decode8_kernel<D, NT, kPlain> : dash_decode8_kernel<D, NT, kScan>,
-                               all ? (int)items : resident, kDecodeThreads, 0, stream, nullptr, p);
+                               all ? (int)items : resident, kDecodeThreads, kSmem, stream, nullptr, p);
   return e != cudaSuccess || p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
 }
 
 template <int D, int NT>
 cudaError_t prepare_t() {
-  cudaFuncAttributes fa;
   for (auto kernel : {dash_decode8_kernel<D, NT, kPlain>, dash_decode8_kernel<D, NT, kScan>,
                       dash_decode8_kernel<D, NT, kCluster>})
-    if (const cudaError_t e = cudaFuncGetAttributes(&fa, kernel)) return e;
+    if (const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D, NT>::kSmem))
+      return e;
   return cudaSuccess;
 }
 

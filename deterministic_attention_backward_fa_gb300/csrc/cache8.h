@@ -33,8 +33,24 @@ struct Cache8CopyParams {
 // pairs: n x {source page, destination page}, on the host.
 cudaError_t launch_cache8_copy(const Cache8CopyParams &p, const int2 *pairs, int n, cudaStream_t stream);
 
+// Division of 0 <= n < 2^31 by a divisor d >= 1, as a product:
+// n / d = (n + floor(n mul / 2^32)) >> shift, with 2^shift >= d the next power of
+// two and mul = floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery).
+struct Divisor {
+  unsigned mul;
+  int shift;
+};
+inline Divisor divisor(unsigned d) {
+  int shift = 0;
+  while ((1ull << shift) < d) ++shift;
+  return {(unsigned)((((1ull << shift) - d) << 32) / d + 1), shift};
+}
+
 struct Decode8Params : DecodeParams {
   Cache8 c;
+  Divisor page;  // page_size
+  // Steps of 16 tokens lie in one page, and strides fit 32 bits.
+  bool whole;
 };
 cudaError_t prepare_cache8();
 cudaError_t launch_decode8(int D, const Decode8Params &p, int num_sms, cudaStream_t stream);

@@ -132,6 +132,10 @@ dash_status_t dash_attn_decode_fp8(const void *q, const void *k_pages, const voi
   if ((st = cache8_of(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, Hkv, D,
                       strides ? strides + 4 : nullptr, &p.c)))
     return st;
+  p.page = dash::divisor(page_size);
+  p.whole = page_size % 16 == 0;
+  for (const dash::CacheStrides &s : {p.c.ks, p.c.vs, p.c.kss, p.c.vss})
+    for (long long x : {s.page, s.token}) p.whole = p.whole && x <= INT32_MAX;
   int dev = 0;
   Device device;
   if ((st = current_device(&dev, &device)) != DASH_OK) return st;
