@@ -16,6 +16,8 @@ import array
 import contextlib
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import math
 import os
 
@@ -132,6 +134,25 @@ def lib():
             f.restype = res
         _LIB = L
     return _LIB
+
+
+_FAST = None
+
+
+def _fast():
+    """The compiled part of the binding (csrc/binding.cpp): small calls spend most of their time in ctypes."""
+    global _FAST
+    if _FAST is None:
+        lib()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader, origin=path))
+        loader.exec_module(module)
+        module.setup(_check)
+        _FAST = module
+    return _FAST
 
 
 def _check(code: int):
@@ -1032,6 +1053,10 @@ def cache_copy(k_pages, v_pages, src, dst, stream=None):
 def attn_decode_shared(q, k_pages, v_pages, page_table, lengths, prefix: int, scale: float | None = None, stream=None):
     """``attn_decode`` for a batch whose sequences begin with the same ``prefix`` tokens, in the pages that the table's
     first row names: their K and V are read once for the batch (see dash_attn_decode_shared)."""
+    if stream is None:
+        out = (_FAST or _fast()).attn_decode_shared(q, k_pages, v_pages, page_table, lengths, prefix, scale)
+        if out is not None:
+            return out
     _decode_inputs(q, k_pages, v_pages, page_table, lengths)
     B, heads, dim = q.shape
     prefix = _prefix(prefix)
@@ -1048,6 +1073,9 @@ def attn_decode_shared(q, k_pages, v_pages, page_table, lengths, prefix: int, sc
 def cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new, stream=None):
     """``cache_write`` into an 8-bit cache: pages in float8_e4m3fn, and a power-of-two scale (fp32) for each token and
     head, ``k_scales`` and ``v_scales`` [pages, tokens, heads] (see dash_cache_write_fp8)."""
+    if stream is None and (_FAST or _fast()).cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table,
+                                                             starts, cu_new):
+        return
     with _using(stream, k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new):
         dash_cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, starts, cu_new, stream)
 
@@ -1055,6 +1083,10 @@ def cache_write_fp8(k, v, k_pages, v_pages, k_scales, v_scales, page_table, star
 def cache_read_fp8(k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, rows: int, stream=None):
     """K and V [rows, heads, D] (bf16) of tokens starts[b] .. of each sequence, packed: sequence b has rows cu[b] ..
     cu[b + 1] - 1.  Rows behind the last sequence are zero."""
+    if stream is None:
+        out = (_FAST or _fast()).cache_read_fp8(k_pages, v_pages, k_scales, v_scales, page_table, starts, cu, rows)
+        if out is not None:
+            return out
     shape = (int(rows), *k_pages.shape[2:])
     k = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
     v = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
@@ -1072,6 +1104,10 @@ def cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None):
 def attn_decode_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, scale: float | None = None,
                     stream=None):
     """``attn_decode`` over an 8-bit cache: O [B, heads, D] (bf16) and LSE [B, heads] (fp32)."""
+    if stream is None:
+        out = (_FAST or _fast()).attn_decode_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, scale)
+        if out is not None:
+            return out
     _decode8_inputs(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths)
     B, heads, dim = q.shape
     scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
@@ -1098,6 +1134,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps: float = 1e-6, p
     """Norms of queries [rows, heads, D] and keys [rows, kv_heads, D], head by head, times their weights, and turned by
     ``positions`` (int32 [rows]) with the angles of ``rope`` (see rope_table): what attn_packed_fwd, attn_decode and
     cache_write take.  Value i turns with value i + rot / 2, or with its neighbour (``pairs``).  New bf16 tensors."""
+    if stream is None:
+        out = (_FAST or _fast()).qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps, pairs)
+        if out is not None:
+            return out
     sizes = _norm_inputs(q, k, q_weight, k_weight, rope, positions)
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
@@ -1109,6 +1149,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps: float = 1e-6, p
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps: float = 1e-6,
                      pairs: bool = False, stream=None):
     """dq, dk (bf16) and the weights' gradients (fp32 [D]) from ``qk_norm_rope``'s inputs and its outputs' gradients."""
+    if stream is None:
+        out = (_FAST or _fast()).qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps, pairs)
+        if out is not None:
+            return out
     sizes = _norm_inputs(q, k, q_weight, k_weight, rope, positions)
     _norm_grads(q, k, dq_out, dk_out)
     dev, dim = q.device, sizes[3]

@@ -2,7 +2,8 @@
 
 Each translation unit compiles in its own nvcc process (in parallel); the
 objects go to ``_build/`` beside this file and the shared library next to the
-package's ``__init__``.  The library links the CUDA runtime statically and
+package's ``__init__``, with the compiled part of the Python binding (named by
+the torch version that it is compiled against).  The library links the CUDA runtime statically and
 reaches the driver (for tensor-map encoding) through the runtime's
 entry-point query, so it loads on machines without a GPU driver.
 """
@@ -11,6 +12,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,7 @@ LIB = os.path.join(PKG, "libdash.so")
 SOURCES = ["api.cpp", "schedule.cpp", "place.cpp", "packed_api.cpp", "packed_plan.cpp", "bwd.cu", "fwd.cu",
            "noalloc.cu", "place.cu", "packed_fwd.cu", "packed_bwd.cu", "paged.cu", "ops_api.cpp", "norm_rope.cu",
            "cache8_api.cpp", "cache8.cu", "shared.cu"]
+BINDING = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE]
 
@@ -34,6 +37,22 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libdash.so")
 
 
+def binding_path() -> str:
+    """The compiled part of the binding for the torch of this process."""
+    import torch
+    return os.path.join(PKG, f"_binding_{torch.__version__.replace('+', '_')}.so")
+
+
+def _torch_flags():
+    import torch
+    top = os.path.dirname(torch.__file__)
+    inc = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
+    abi = int(torch.compiled_with_cxx11_abi())
+    return ([x for i in inc for x in ("-I", i)] + [f"-D_GLIBCXX_USE_CXX11_ABI={abi}"],
+            ["-L", os.path.join(top, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+
+
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "dash.h"))
@@ -42,9 +61,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(binding_path()):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(binding_path()))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -54,8 +73,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
 
+    flags, libs = _torch_flags()
+
     def compile_one(src):
         obj = os.path.join(BUILD, src + ".o")
+        if src == BINDING:
+            cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", os.path.join(CSRC, src), "-o", obj]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"g++ failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            return obj, ""
         cmd = [cc, *ARCH, *COMMON, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cu"):
             cmd.insert(1, "-Xptxas=-v" if verbose else "-Xptxas=-warn-spills")
@@ -64,8 +91,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return obj, (r.stdout + r.stderr)
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        results = list(ex.map(compile_one, [*SOURCES, BINDING]))
+    binding = results.pop()[0]
     if verbose:
         for (_, log) in results:
             if log.strip():
@@ -76,6 +104,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = binding_path() + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, binding, "-L", PKG, "-l:" + os.path.basename(LIB), *libs, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, binding_path())
     return LIB
 
 
