@@ -63,136 +63,206 @@ __device__ __forceinline__ int scale_field(uint32_t top) {
 }
 
 // ---------------------------------------------------------- write and read
-// Where token t of the call lies: its page and place, or -1.
+// Where token t of the call lies: its page and place, or -1.  All lanes ask
+// together; the sequence (the last b with cu[b] <= t) is found 32 ways at a time,
+// since each look-up waits for the one before.
 struct Place {
   int page, off;
+  bool behind;  // the token is behind the last sequence
 };
-__device__ __forceinline__ Place place_of(const Cache8RowsParams &p, int t, bool &behind) {
-  int lo = 0, hi = p.B;  // the sequence of the token: the last b with cu[b] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu[mid + 1] <= t) lo = mid + 1;
-    else hi = mid;
+__device__ __forceinline__ Place place_of(const Cache8RowsParams &p, int t, int lane) {
+  int lo = 0, n = p.B;
+  while (n > 32) {
+    const int step = (n + 31) >> 5, at = (lane + 1) * step;
+    const int whole = __popc(__ballot_sync(0xffffffffu, at <= n && p.cu[lo + at] <= t));
+    lo += whole * step;
+    n = min(step, n - whole * step);
   }
-  behind = lo >= p.B;  // rows behind the last sequence
-  Place at{-1, 0};
-  if (behind) return at;
+  lo += __popc(__ballot_sync(0xffffffffu, lane < n && p.cu[lo + lane + 1] <= t));
+  Place at{-1, 0, lo >= p.B};
+  if (at.behind) return at;
   const int first = p.cu[lo];
   const long long pos = (long long)p.starts[lo] + (t - first);
-  const long long slot = pos / p.page_size;
-  if (t >= first && pos >= 0 && slot < p.max_pages) at.page = p.table[lo * p.table_row + slot];
-  at.off = (int)(pos - slot * p.page_size);
+  if (t >= first && pos >= 0 && pos < (long long)p.max_pages * p.page_size) {
+    const unsigned slot = (unsigned)pos / (unsigned)p.page_size;  // pos is below 2^32
+    at.page = p.table[lo * p.table_row + slot];
+    at.off = (int)((unsigned)pos - slot * (unsigned)p.page_size);
+  }
   if (at.page < 0 || at.page >= p.n_pages) at.page = -1;
   return at;
 }
 
-// A warp takes a token: D / 8 lanes a row of a head, 8 values a lane.
+// A warp takes a token and `passes` steps of its heads, K's rows and V's: D / 8
+// lanes a row, 8 values a lane.
+struct Item8 {
+  int t, first, end;
+};
+template <int D>
+__device__ __forceinline__ Item8 item_of(const Cache8RowsParams &p) {
+  const unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5), t = item / (unsigned)p.blocks;
+  const int first = (int)(item - t * p.blocks) * p.passes;
+  return {(int)t, first, min(first + p.passes, (p.heads * D / 8 + 31) / 32)};
+}
+constexpr int kRowsAhead = 4;  // rows of K and of V that a lane has in flight
+
+// The lane's place in the rows of K or of V: the packed one, the codes, the scale;
+// `step` of each to the rows of the next step.
+struct Rows8 {
+  __nv_bfloat16 *x;
+  uint8_t *codes;
+  float *scale;
+  long long x_step, codes_step, scale_step;
+};
+template <int D>
+__device__ __forceinline__ Rows8 rows_of8(const Cache8RowsParams &p, bool is_v, int t, int row, int e) {
+  Rows8 r;
+  constexpr int kRows = 256 / D;
+  const long long head = is_v ? p.v_head : p.k_head;
+  const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
+  r.x = (is_v ? p.v + t * p.v_row : p.k + t * p.k_row) + row * head + e;
+  r.codes = (is_v ? p.c.v : p.c.k) + row * st.head + e;
+  r.scale = (is_v ? p.c.v_scale : p.c.k_scale) + row * ss.head;
+  r.x_step = kRows * head;
+  r.codes_step = kRows * st.head;
+  r.scale_step = kRows * ss.head;
+  return r;
+}
+__device__ __forceinline__ void place_rows(Rows8 &r, const CacheStrides &st, const CacheStrides &ss, Place at) {
+  r.codes += at.page * st.page + at.off * st.token;
+  r.scale += at.page * ss.page + at.off * ss.token;
+}
+
+template <int D>
+__device__ __forceinline__ void quantise_row(uint4 x, uint8_t *codes, float *scale, bool first, bool real) {
+  constexpr int kLanes = D / 8;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // magnitudes in order are bits in order, infinities and NaN above all others
+  const uint32_t both = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                 __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  uint32_t top = max(both & 0xffffu, both >> 16);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool finite = top < 0x7f80u;
+  const int f = finite ? scale_field(top) : 1;
+  const float inv = finite ? pow2_field(254 - f) : 0.f;
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+  uint2 two = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  if (!finite) two = make_uint2(0u, 0u);
+  if (!real) return;
+  *reinterpret_cast<uint2 *>(codes) = two;
+  if (first) *scale = finite ? pow2_field(f) : NAN;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) dash_cache8_write_kernel(const __grid_constant__ Cache8RowsParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, e = (lane % kLanes) * 8;
-  const int nwarps = gridDim.x * 8;
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.n_tokens; t += nwarps) {
-    bool behind;
-    const Place at = place_of(p, t, behind);
-    if (behind) break;  // and so are the rows after it
-    if (at.page < 0) {
-      if (lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
-      continue;
+  const int lane = threadIdx.x & 31, e = (lane % kLanes) * 8;
+  const Item8 it = item_of<D>(p);
+  if (it.t >= p.n_tokens) return;
+  int row = it.first * kRows + lane / kLanes;
+  Rows8 k = rows_of8<D>(p, false, it.t, row, e), v = rows_of8<D>(p, true, it.t, row, e);
+  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, row += kRowsAhead * kRows) {
+    uint4 kx[kRowsAhead], vx[kRowsAhead];
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      kx[u] = vx[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (s0 + u < it.end && row + u * kRows < p.heads) {
+        kx[u] = *reinterpret_cast<const uint4 *>(k.x);
+        vx[u] = *reinterpret_cast<const uint4 *>(v.x);
+      }
+      k.x += k.x_step;
+      v.x += v.x_step;
     }
-    const int rows = 2 * p.heads;  // K's, then V's
-    constexpr int kU = 4;
-    for (int r0 = 0; r0 < rows; r0 += kRows * kU) {
-      uint4 x[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int r = r0 + u * kRows + sub;
-        x[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const __nv_bfloat16 *src = r < p.heads ? p.k + t * p.k_row + r * p.k_head
-                                                 : p.v + t * p.v_row + (r - p.heads) * p.v_head;
-          x[u] = *reinterpret_cast<const uint4 *>(src + e);
-        }
+    if (s0 == it.first) {  // the rows are on their way meanwhile
+      const Place at = place_of(p, it.t, lane);
+      if (at.behind) return;
+      if (at.page < 0) {
+        if (lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
+        return;
       }
+      place_rows(k, p.c.ks, p.c.kss, at);
+      place_rows(v, p.c.vs, p.c.vss, at);
+    }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t top = 0;  // magnitudes in order are bits in order, infinities and NaN above all others
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool finite = top < 0x7f80u;
-        const int f = finite ? scale_field(top) : 1;
-        const float inv = pow2_field(254 - f);
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
-        const int r = r0 + u * kRows + sub;
-        if (r >= rows) continue;
-        const bool is_v = r >= p.heads;
-        const int h = is_v ? r - p.heads : r;
-        const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
-        uint2 codes = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-        if (!finite) codes = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2 *>((is_v ? p.c.v : p.c.k) + at.page * st.page + at.off * st.token + h * st.head + e) =
-            codes;
-        if (e == 0)
-          (is_v ? p.c.v_scale : p.c.k_scale)[at.page * ss.page + at.off * ss.token + h * ss.head] =
-              finite ? pow2_field(f) : NAN;
-      }
+    for (int u = 0; u < kRowsAhead; ++u) {
+      if (s0 + u >= it.end) break;
+      const bool real = row + u * kRows < p.heads;
+      quantise_row<D>(kx[u], k.codes, k.scale, e == 0, real);
+      quantise_row<D>(vx[u], v.codes, v.scale, e == 0, real);
+      k.codes += k.codes_step;
+      v.codes += v.codes_step;
+      k.scale += k.scale_step;
+      v.scale += v.scale_step;
     }
   }
+}
+
+__device__ __forceinline__ uint4 row_values(uint2 codes, float scale) {
+  uint4 w;
+  uint32_t *out = &w.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = widen8((i < 2 ? codes.x : codes.y) >> (16 * (i & 1)));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+    out[i] = pack_bf16(v.x * scale, v.y * scale);
+  }
+  return w;
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) dash_cache8_read_kernel(const __grid_constant__ Cache8RowsParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, e = (lane % kLanes) * 8;
-  const int nwarps = gridDim.x * 8;
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.n_tokens; t += nwarps) {
-    bool behind;
-    const Place at = place_of(p, t, behind);
-    const bool none = at.page < 0;  // such rows are zero
-    if (none && !behind && lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
-    const int rows = 2 * p.heads;
-    constexpr int kU = 4;
-    for (int r0 = 0; r0 < rows; r0 += kRows * kU) {
-      uint2 x[kU];
-      float s[kU];
+  const int lane = threadIdx.x & 31, e = (lane % kLanes) * 8;
+  const Item8 it = item_of<D>(p);
+  if (it.t >= p.n_tokens) return;
+  int row = it.first * kRows + lane / kLanes;
+  Rows8 k = rows_of8<D>(p, false, it.t, row, e), v = rows_of8<D>(p, true, it.t, row, e);
+  const Place at = place_of(p, it.t, lane);
+  const bool none = at.page < 0;  // such rows are zero
+  if (none && !at.behind && lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
+  place_rows(k, p.c.ks, p.c.kss, at);
+  place_rows(v, p.c.vs, p.c.vss, at);
+  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, row += kRowsAhead * kRows) {
+    uint2 kx[kRowsAhead], vx[kRowsAhead];
+    float ks[kRowsAhead], vs[kRowsAhead];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int r = r0 + u * kRows + sub;
-        x[u] = make_uint2(0u, 0u);
-        s[u] = 0.f;
-        if (r < rows && !none) {
-          const bool is_v = r >= p.heads;
-          const int h = is_v ? r - p.heads : r;
-          const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
-          x[u] = *reinterpret_cast<const uint2 *>((is_v ? p.c.v : p.c.k) + at.page * st.page + at.off * st.token +
-                                                  h * st.head + e);
-          s[u] = (is_v ? p.c.v_scale : p.c.k_scale)[at.page * ss.page + at.off * ss.token + h * ss.head];
-        }
+    for (int u = 0; u < kRowsAhead; ++u) {
+      kx[u] = vx[u] = make_uint2(0u, 0u);
+      ks[u] = vs[u] = 0.f;
+      if (s0 + u < it.end && row + u * kRows < p.heads && !none) {
+        kx[u] = *reinterpret_cast<const uint2 *>(k.codes);
+        vx[u] = *reinterpret_cast<const uint2 *>(v.codes);
+        ks[u] = *k.scale;
+        vs[u] = *v.scale;
       }
+      k.codes += k.codes_step;
+      v.codes += v.codes_step;
+      k.scale += k.scale_step;
+      v.scale += v.scale_step;
+    }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int r = r0 + u * kRows + sub;
-        if (r >= rows) continue;
-        uint4 w;
-        uint32_t *out = &w.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two = widen8((i < 2 ? x[u].x : x[u].y) >> (16 * (i & 1)));
-          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&two));
-          out[i] = pack_bf16(v.x * s[u], v.y * s[u]);
-        }
-        __nv_bfloat16 *dst =
-            r < p.heads ? p.k + t * p.k_row + r * p.k_head : p.v + t * p.v_row + (r - p.heads) * p.v_head;
-        *reinterpret_cast<uint4 *>(dst + e) = w;
-      }
+    for (int u = 0; u < kRowsAhead; ++u) {
+      if (s0 + u >= it.end || row + u * kRows >= p.heads) break;
+      *reinterpret_cast<uint4 *>(k.x) = row_values(kx[u], ks[u]);
+      *reinterpret_cast<uint4 *>(v.x) = row_values(vx[u], vs[u]);
+      k.x += k.x_step;
+      v.x += v.x_step;
     }
   }
+}
+
+// A token's rows are one warp's, or, of few tokens, several warps'.
+cudaError_t launch_rows(void (*kernel)(const Cache8RowsParams), Cache8RowsParams p, cudaStream_t stream) {
+  const int steps = (p.heads * p.D / 8 + 31) / 32, want = 4096;
+  p.blocks = p.n_tokens >= want ? 1 : (want + p.n_tokens - 1) / p.n_tokens;
+  if (p.blocks > steps) p.blocks = steps;
+  p.passes = (steps + p.blocks - 1) / p.blocks;
+  p.blocks = (steps + p.passes - 1) / p.passes;
+  const long long warps = (long long)p.n_tokens * p.blocks;
+  return launch(kernel, (unsigned)((warps + 7) / 8), 256, 0, stream, nullptr, p);
 }
 
 // ------------------------------------------------------------------- copy
@@ -692,11 +762,6 @@ cudaError_t prepare_t() {
   return cudaSuccess;
 }
 
-int rows_grid(int n_tokens, int num_sms) {
-  const int want = (n_tokens + 7) / 8;
-  return want < 8 * num_sms ? want : 8 * num_sms;
-}
-
 }  // namespace
 
 cudaError_t prepare_cache8() {
@@ -718,14 +783,12 @@ cudaError_t launch_decode8(int D, const Decode8Params &p, int num_sms, cudaStrea
   return small ? launch_decode_t<128, 1>(p, num_sms, stream) : launch_decode_t<128, 2>(p, num_sms, stream);
 }
 
-cudaError_t launch_cache8_write(const Cache8RowsParams &p, int num_sms, cudaStream_t stream) {
-  return launch(p.D == 64 ? dash_cache8_write_kernel<64> : dash_cache8_write_kernel<128>,
-                rows_grid(p.n_tokens, num_sms), 256, 0, stream, nullptr, p);
+cudaError_t launch_cache8_write(const Cache8RowsParams &p, cudaStream_t stream) {
+  return launch_rows(p.D == 64 ? dash_cache8_write_kernel<64> : dash_cache8_write_kernel<128>, p, stream);
 }
 
-cudaError_t launch_cache8_read(const Cache8RowsParams &p, int num_sms, cudaStream_t stream) {
-  return launch(p.D == 64 ? dash_cache8_read_kernel<64> : dash_cache8_read_kernel<128>,
-                rows_grid(p.n_tokens, num_sms), 256, 0, stream, nullptr, p);
+cudaError_t launch_cache8_read(const Cache8RowsParams &p, cudaStream_t stream) {
+  return launch_rows(p.D == 64 ? dash_cache8_read_kernel<64> : dash_cache8_read_kernel<128>, p, stream);
 }
 
 cudaError_t launch_cache8_copy(const Cache8CopyParams &p, const int2 *pairs, int n, cudaStream_t stream) {

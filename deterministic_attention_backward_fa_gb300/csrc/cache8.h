@@ -21,10 +21,11 @@ struct Cache8RowsParams {       // write and read
   const int *table, *starts, *cu;
   long long table_row;
   int n_tokens, B, heads, D, n_pages, page_size, max_pages;
+  int blocks, passes;           // a token's rows are dealt to `blocks` warps, `passes` steps each
   int *status;
 };
-cudaError_t launch_cache8_write(const Cache8RowsParams &p, int num_sms, cudaStream_t stream);
-cudaError_t launch_cache8_read(const Cache8RowsParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache8_write(const Cache8RowsParams &p, cudaStream_t stream);
+cudaError_t launch_cache8_read(const Cache8RowsParams &p, cudaStream_t stream);
 
 struct Cache8CopyParams {
   Cache8 c;

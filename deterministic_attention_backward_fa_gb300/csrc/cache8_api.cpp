@@ -74,7 +74,7 @@ dash_status_t cache8_rows(bool write, const void *k, const void *v, const void *
   if ((st = current_device(&dev, &device)) != DASH_OK) return st;
   p.status = device.status;
   const cudaError_t e = (write ? dash::launch_cache8_write : dash::launch_cache8_read)(
-      p, device.sms, reinterpret_cast<cudaStream_t>(stream));
+      p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DASH_OK : cuda_error(e, write ? "cache write launch" : "cache read launch");
 }
 

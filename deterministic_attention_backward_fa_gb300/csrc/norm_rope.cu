@@ -25,16 +25,41 @@ using namespace dev;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // head rows that a lane has in flight
+constexpr int kAhead = 4;     // head rows that a lane has in flight, forward
+constexpr int kAheadBwd = 4;  // and backward (x and dz)
 
-__device__ __forceinline__ void widen(uint2 w, float *v) {
-  v[0] = __uint_as_float(w.x << 16);
-  v[1] = __uint_as_float(w.x & 0xffff0000u);
-  v[2] = __uint_as_float(w.y << 16);
-  v[3] = __uint_as_float(w.y & 0xffff0000u);
+// Two 32-bit values; the arithmetic is one instruction for both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ float2 parts(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator-(F2 a) { return a * f2(-1.f, -1.f); }
 
-// What a lane holds of a head row: its eight values as pairs (a[i], b[i]).
+// A lane's eight values of a row as pairs (a[i], b[i]), i < 4.
+struct Eight {
+  F2 a[2], b[2];
+};
+
+// What a lane holds of a head row.
 template <int D, bool kPairs>
 struct Lane {
   static constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a head row, head rows of a warp's step
@@ -59,187 +84,216 @@ struct Lane {
     w[0] = *reinterpret_cast<const uint2 *>(row + lo);
     w[1] = *reinterpret_cast<const uint2 *>(row + hi);
   }
-  static __device__ __forceinline__ void split(const uint2 (&w)[2], float (&a)[4], float (&b)[4]) {
-    float v[8];
-    widen(w[0], v);
-    widen(w[1], v + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = kPairs ? v[2 * i] : v[i];
-      b[i] = kPairs ? v[2 * i + 1] : v[4 + i];
-    }
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16 *row, const float (&a)[4], const float (&b)[4]) const {
-    uint2 w[2];
+  static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  static __device__ __forceinline__ Eight widen(const uint2 (&w)[2]) {
+    Eight x;
     if (kPairs) {
-      w[0] = make_uint2(pack_bf16(a[0], b[0]), pack_bf16(a[1], b[1]));
-      w[1] = make_uint2(pack_bf16(a[2], b[2]), pack_bf16(a[3], b[3]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x.a[i] = f2(low(w[i].x), low(w[i].y));
+        x.b[i] = f2(high(w[i].x), high(w[i].y));
+      }
     } else {
-      w[0] = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
-      w[1] = make_uint2(pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3]));
+      x.a[0] = f2(low(w[0].x), high(w[0].x));
+      x.a[1] = f2(low(w[0].y), high(w[0].y));
+      x.b[0] = f2(low(w[1].x), high(w[1].x));
+      x.b[1] = f2(low(w[1].y), high(w[1].y));
+    }
+    return x;
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16 *row, const Eight &x) const {
+    uint2 w[2];
+    const float2 a0 = parts(x.a[0]), a1 = parts(x.a[1]), b0 = parts(x.b[0]), b1 = parts(x.b[1]);
+    if (kPairs) {
+      w[0] = make_uint2(pack_bf16(a0.x, b0.x), pack_bf16(a0.y, b0.y));
+      w[1] = make_uint2(pack_bf16(a1.x, b1.x), pack_bf16(a1.y, b1.y));
+    } else {
+      w[0] = make_uint2(pack_bf16(a0.x, a0.y), pack_bf16(a1.x, a1.y));
+      w[1] = make_uint2(pack_bf16(b0.x, b0.y), pack_bf16(b1.x, b1.y));
     }
     *reinterpret_cast<uint2 *>(row + lo) = w[0];
     *reinterpret_cast<uint2 *>(row + hi) = w[1];
   }
-  __device__ __forceinline__ void weight(const NormRopeParams &p, int which, float (&a)[4], float (&b)[4]) const {
-    float v[8];
-    if (p.weight32) {
-      const float *w = static_cast<const float *>(p.t[which].weight);
-      *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(w + lo);
-      *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(w + hi);
-    } else {
+  __device__ __forceinline__ Eight weight(const NormRopeParams &p, int which) const {
+    if (!p.weight32) {
       uint2 w[2];
       load(static_cast<const __nv_bfloat16 *>(p.t[which].weight), w);
-      widen(w[0], v);
-      widen(w[1], v + 4);
+      return widen(w);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = kPairs ? v[2 * i] : v[i];
-      b[i] = kPairs ? v[2 * i + 1] : v[4 + i];
+    const float *w = static_cast<const float *>(p.t[which].weight);
+    const float4 u = *reinterpret_cast<const float4 *>(w + lo), v = *reinterpret_cast<const float4 *>(w + hi);
+    Eight x;
+    if (kPairs) {
+      x.a[0] = f2(u.x, u.z), x.a[1] = f2(v.x, v.z);
+      x.b[0] = f2(u.y, u.w), x.b[1] = f2(v.y, v.w);
+    } else {
+      x.a[0] = f2(u.x, u.y), x.a[1] = f2(u.z, u.w);
+      x.b[0] = f2(v.x, v.y), x.b[1] = f2(v.z, v.w);
     }
+    return x;
   }
-  // Cosines and sines of a row's position.  False: the position is outside the table.
-  __device__ __forceinline__ bool angles(const NormRopeParams &p, long long row, float (&c)[4], float (&s)[4]) const {
+  // Cosines (a) and sines (b) of a row's position; NaN, and a report, where it is outside the table.
+  __device__ __forceinline__ Eight angles(const NormRopeParams &p, long long row, int lane) const {
     const int pos = p.positions[row];
     const bool ok = pos >= 0 && pos < p.max_positions;
+    Eight x;
     if (ok && angle >= 0) {
       const float *t = p.rope + (long long)pos * p.rot + angle;
-      *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(t));
-      *reinterpret_cast<float4 *>(s) = __ldg(reinterpret_cast<const float4 *>(t + p.rot / 2));
+      const float4 c = __ldg(reinterpret_cast<const float4 *>(t));
+      const float4 s = __ldg(reinterpret_cast<const float4 *>(t + p.rot / 2));
+      x.a[0] = f2(c.x, c.y), x.a[1] = f2(c.z, c.w);
+      x.b[0] = f2(s.x, s.y), x.b[1] = f2(s.z, s.w);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-      }
+      if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
+      x.a[0] = x.a[1] = ok ? f2(1.f, 1.f) : f2(NAN, NAN);
+      x.b[0] = x.b[1] = ok ? f2(0.f, 0.f) : f2(NAN, NAN);
     }
-    return ok;
+    return x;
+  }
+  static __device__ __forceinline__ float sum(F2 x) {
+    const float2 v = parts(x);
+    float s = v.x + v.y;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
   }
 };
 
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float x) {
+// Steps first .. end - 1 of a tensor's heads for one row of the batch, with
+// w cos, w sin made once: z_a = r (x_a (w_a cos) - x_b (w_b sin)) and so on.
+template <int D, bool kPairs>
+__device__ __forceinline__ void norm_heads(const NormRopeParams &p, const Lane<D, kPairs> &l, int which, long long row,
+                                           const Eight &angle, int lane, int first, int end) {
+  using L = Lane<D, kPairs>;
+  const NormRopeTensor &t = p.t[which];
+  const int sub = lane / L::kLanes;
+  const __nv_bfloat16 *in = t.x + row * t.x_row + (first * L::kRows + sub) * t.x_head;
+  __nv_bfloat16 *out = t.out + row * t.out_row + (first * L::kRows + sub) * t.out_head;
+  const long long in_step = L::kRows * t.x_head, out_step = L::kRows * t.out_head;
+  F2 ac[2], bs[2], bc[2], as[2];
+  const Eight w = l.weight(p, which);
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  for (int i = 0; i < 2; ++i) {
+    ac[i] = w.a[i] * angle.a[i];
+    bs[i] = -(w.b[i] * angle.b[i]);
+    bc[i] = w.b[i] * angle.a[i];
+    as[i] = w.a[i] * angle.b[i];
+  }
+  for (int s0 = first; s0 < end; s0 += kAhead) {
+    uint2 x[kAhead][2];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      x[u][0] = x[u][1] = make_uint2(0u, 0u);
+      if (s0 + u < end && (s0 + u) * L::kRows + sub < t.heads) l.load(in + u * in_step, x[u]);
+    }
+    in += kAhead * in_step;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (s0 + u >= end) break;
+      const Eight v = L::widen(x[u]);
+      F2 sq = v.a[0] * v.a[0];
+      sq = fma(v.a[1], v.a[1], sq);
+      sq = fma(v.b[0], v.b[0], sq);
+      sq = fma(v.b[1], v.b[1], sq);
+      const float r = rsqrtf(L::sum(sq) * (1.f / D) + p.eps);
+      const F2 rr = f2(r, r);
+      Eight z;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        z.a[i] = rr * fma(v.a[i], ac[i], v.b[i] * bs[i]);
+        z.b[i] = rr * fma(v.b[i], bc[i], v.a[i] * as[i]);
+      }
+      if ((s0 + u) * L::kRows + sub < t.heads) l.store(out, z);
+      out += out_step;
+    }
+  }
 }
 
-// A warp takes one row of the batch and `passes` steps of its heads.
+// A warp takes one row of the batch and `passes` steps of its heads, the queries' first.
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) dash_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) dash_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   using L = Lane<D, kPairs>;
   const int lane = threadIdx.x & 31;
   const unsigned item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // below 2^31: many rows are a warp each
   const unsigned at_row = item / (unsigned)p.blocks;
   if (at_row >= p.rows) return;
   const int first = (int)(item - at_row * p.blocks) * p.passes;
-  const long long row = at_row;
   const L l(lane, p.rot);
-  const int heads = p.t[0].heads + p.t[1].heads;
-  const int sub = lane / L::kLanes;
-  float wa[2][4], wb[2][4], c[4], s[4];
-  uint2 x[kAhead][2];
-  auto at = [&](int pass, int &which, int &h) {
-    h = (first + pass) * L::kRows + sub;
-    which = h >= p.t[0].heads;
-    const bool valid = pass < p.passes && h < heads;
-    if (which) h -= p.t[0].heads;
-    return valid;
-  };
-  auto load = [&](int pass0) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      int which, h;
-      x[u][0] = x[u][1] = make_uint2(0u, 0u);
-      if (at(pass0 + u, which, h)) l.load(p.t[which].x + row * p.t[which].x_row + h * p.t[which].x_head, x[u]);
-    }
-  };
-  load(0);
-  const bool ok = l.angles(p, row, c, s);
-  if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
-  l.weight(p, 0, wa[0], wb[0]);
-  l.weight(p, 1, wa[1], wb[1]);
-  for (int pass0 = 0; pass0 < p.passes; pass0 += kAhead) {
-    if (pass0) load(pass0);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float a[4], b[4], sum = 0.f;
-      l.split(x[u], a, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
-      const float r = ok ? rsqrtf(row_sum<L::kLanes>(sum) * (1.f / D) + p.eps) : NAN;
-      int which, h;
-      if (!at(pass0 + u, which, h)) continue;
-      float za[4], zb[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ya = a[i] * r * (which ? wa[1][i] : wa[0][i]), yb = b[i] * r * (which ? wb[1][i] : wb[0][i]);
-        za[i] = ya * c[i] - yb * s[i];
-        zb[i] = yb * c[i] + ya * s[i];
-      }
-      l.store(p.t[which].out + row * p.t[which].out_row + h * p.t[which].out_head, za, zb);
-    }
-  }
+  const int q_steps = (p.t[0].heads + L::kRows - 1) / L::kRows, k_steps = (p.t[1].heads + L::kRows - 1) / L::kRows;
+  const int end = min(first + p.passes, q_steps + k_steps);
+  const Eight angle = l.angles(p, at_row, lane);
+  if (first < q_steps) norm_heads(p, l, 0, at_row, angle, lane, first, min(end, q_steps));
+  if (end > q_steps) norm_heads(p, l, 1, at_row, angle, lane, max(first - q_steps, 0), end - q_steps);
 }
 
 // A warp takes rows of the batch in turn and keeps its sums of dw in registers.
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) dash_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) dash_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   using L = Lane<D, kPairs>;
   constexpr int kWarps = kThreads / 32;
   // the sum of the parts may be set up now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L::kLanes;
   const L l(lane, p.rot);
-  float dwa[2][4] = {}, dwb[2][4] = {};
+  Eight w[2], dw[2];
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    const NormRopeTensor &t = p.t[which];
-    float wa[4], wb[4];
-    l.weight(p, which, wa, wb);
-    for (long long row = (long long)blockIdx.x * kWarps + warp; row < p.rows; row += (long long)gridDim.x * kWarps) {
-      float c[4], s[4];
-      const bool ok = l.angles(p, row, c, s);
-      if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
-      for (int h0 = 0; h0 < t.heads; h0 += 2 * L::kRows) {
-        uint2 xw[2][2], gw[2][2];
+    w[which] = l.weight(p, which);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int h = h0 + u * L::kRows + sub;
-          xw[u][0] = xw[u][1] = gw[u][0] = gw[u][1] = make_uint2(0u, 0u);
-          if (h < t.heads) {
-            l.load(t.x + row * t.x_row + h * t.x_head, xw[u]);
-            l.load(t.dz + row * t.dz_row + h * t.dz_head, gw[u]);
+    for (int i = 0; i < 2; ++i) dw[which].a[i] = dw[which].b[i] = f2(0.f, 0.f);
+  }
+  for (long long row = (long long)blockIdx.x * kWarps + warp; row < p.rows; row += (long long)gridDim.x * kWarps) {
+    const Eight angle = l.angles(p, row, lane);
+    F2 minus[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) minus[i] = -angle.b[i];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const NormRopeTensor &t = p.t[which];
+      const __nv_bfloat16 *xs = t.x + row * t.x_row + sub * t.x_head, *zs = t.dz + row * t.dz_row + sub * t.dz_head;
+      __nv_bfloat16 *out = t.out + row * t.out_row + sub * t.out_head;
+      for (int h0 = 0; h0 < t.heads; h0 += kAheadBwd * L::kRows) {
+        uint2 xw[kAheadBwd][2], zw[kAheadBwd][2];
+#pragma unroll
+        for (int u = 0; u < kAheadBwd; ++u) {
+          xw[u][0] = xw[u][1] = zw[u][0] = zw[u][1] = make_uint2(0u, 0u);
+          if (h0 + u * L::kRows + sub < t.heads) {
+            l.load(xs + (h0 + u * L::kRows) * t.x_head, xw[u]);
+            l.load(zs + (h0 + u * L::kRows) * t.dz_head, zw[u]);
           }
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int h = h0 + u * L::kRows + sub;
-          float a[4], b[4], za[4], zb[4], ga[4], gb[4], sum = 0.f, dot = 0.f;
-          l.split(xw[u], a, b);
-          l.split(gw[u], za, zb);
+        for (int u = 0; u < kAheadBwd; ++u) {
+          if (h0 + u * L::kRows >= t.heads) break;
+          const Eight x = L::widen(xw[u]), z = L::widen(zw[u]);
+          Eight g, gw;
+          F2 sq = f2(0.f, 0.f), dot = f2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ga[i] = za[i] * c[i] + zb[i] * s[i];
-            gb[i] = zb[i] * c[i] - za[i] * s[i];
-            sum += a[i] * a[i] + b[i] * b[i];
-            dot += ga[i] * wa[i] * a[i] + gb[i] * wb[i] * b[i];
+          for (int i = 0; i < 2; ++i) {
+            g.a[i] = fma(z.a[i], angle.a[i], z.b[i] * angle.b[i]);
+            g.b[i] = fma(z.b[i], angle.a[i], z.a[i] * minus[i]);
+            gw.a[i] = g.a[i] * w[which].a[i];
+            gw.b[i] = g.b[i] * w[which].b[i];
+            sq = fma(x.a[i], x.a[i], sq);
+            sq = fma(x.b[i], x.b[i], sq);
+            dot = fma(gw.a[i], x.a[i], dot);
+            dot = fma(gw.b[i], x.b[i], dot);
           }
-          sum = row_sum<L::kLanes>(sum);
-          dot = row_sum<L::kLanes>(dot);
-          if (h >= t.heads) continue;
-          const float r = ok ? rsqrtf(sum * (1.f / D) + p.eps) : NAN;
-          const float m = dot * (1.f / D) * r * r;
-          float xa[4], xb[4];
+          // lanes past the last head hold zeros: their r is 0, so that they add nothing to dw whatever eps is
+          const bool real = h0 + u * L::kRows + sub < t.heads;
+          const float var = L::sum(sq) * (1.f / D) + p.eps, r = real ? rsqrtf(var) : 0.f;
+          const float m = -(L::sum(dot) * (1.f / D) * r * r * r);
+          const F2 rr = f2(r, r), mm = f2(m, m);
+          Eight d;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xa[i] = r * (ga[i] * wa[i] - a[i] * m);
-            xb[i] = r * (gb[i] * wb[i] - b[i] * m);
-            dwa[which][i] += ga[i] * (a[i] * r);
-            dwb[which][i] += gb[i] * (b[i] * r);
+          for (int i = 0; i < 2; ++i) {
+            d.a[i] = fma(gw.a[i], rr, x.a[i] * mm);
+            d.b[i] = fma(gw.b[i], rr, x.b[i] * mm);
+            dw[which].a[i] = fma(g.a[i], x.a[i] * rr, dw[which].a[i]);
+            dw[which].b[i] = fma(g.b[i], x.b[i] * rr, dw[which].b[i]);
           }
-          l.store(t.out + row * t.out_row + h * t.out_head, xa, xb);
+          if (real) l.store(out + (h0 + u * L::kRows) * t.out_head, d);
         }
       }
     }
@@ -250,7 +304,8 @@ __global__ void __launch_bounds__(kThreads) dash_norm_rope_bwd_kernel(const __gr
   for (int which = 0; which < 2; ++which)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float a = dwa[which][i], b = dwb[which][i];
+      const float2 va = parts(dw[which].a[i / 2]), vb = parts(dw[which].b[i / 2]);
+      float a = i & 1 ? va.y : va.x, b = i & 1 ? vb.y : vb.x;
 #pragma unroll
       for (int o = L::kLanes; o < 32; o <<= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -292,7 +347,7 @@ __global__ void __launch_bounds__(256) dash_norm_rope_sum_kernel(const __grid_co
 template <int D>
 cudaError_t launch_fwd(NormRopeParams &p, cudaStream_t stream) {
   constexpr int kRows = 256 / D;
-  const int steps = (p.t[0].heads + p.t[1].heads + kRows - 1) / kRows;
+  const int steps = (p.t[0].heads + kRows - 1) / kRows + (p.t[1].heads + kRows - 1) / kRows;
   // Rows enough to fill the GPU are a warp each, which reads a row's angles once;
   // of few rows, a warp takes a part of the heads.
   const long long want = 4096;

@@ -32,7 +32,7 @@ struct NormRopeParams {
 
 // CTAs of a backward: a number of its own for each size, whatever the GPU, so
 // that the weights' gradients are the same sums everywhere.
-constexpr int kNormBwdCtas = 608;
+constexpr int kNormBwdCtas = 304;
 inline int norm_bwd_ctas(long long rows) { return rows < 8LL * kNormBwdCtas ? (int)((rows + 7) / 8) : kNormBwdCtas; }
 
 cudaError_t prepare_norm_rope();
