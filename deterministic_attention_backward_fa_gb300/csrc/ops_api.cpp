@@ -163,7 +163,6 @@ dash_status_t dash_attn_decode_shared(const void *q, const void *k_pages, const 
   if ((st = decode_cache(k_pages, v_pages, Hkv, D, n_pages, page_size, strides, &p)) != DASH_OK) return st;
   p.prefix_tiles = (prefix + dash::kPackedTile - 1) / dash::kPackedTile;
   p.tiles_per_split = cut.tiles;
-  p.wide = (reinterpret_cast<uintptr_t>(workspace) & 31u) == 0;
   p.spin_limit_ns = kSpinNs;
   int dev = 0;
   Device device;

@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
     }
     __syncthreads();  // the ring is free for the next item
   }
+  // where this grid was let in before the end of the prefix's, its own end says that both have ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins the splits of a (sequence, Q head) in their order.
@@ -373,8 +375,10 @@ cudaError_t launch_decode_t(const DecodeParams &p, int num_sms, cudaStream_t str
   // for, the scan is left out (one sequence of 701 tokens on 4 K/V heads, before
   // it was a cluster's: 6.3 us against 7.0).
   const bool all = items <= 2LL * num_sms;
+  cudaLaunchAttribute attr = overlap_attr();
   const cudaError_t e = launch(all ? dash_decode_kernel<D, kPlain> : dash_decode_kernel<D, kScan>,
-                               all ? (int)items : 2 * num_sms, kThreads, C::kSmem, stream, nullptr, p);
+                               all ? (int)items : 2 * num_sms, kThreads, C::kSmem, stream,
+                               p.parts_before > 0 ? &attr : nullptr, p);
   return e != cudaSuccess || p.parts_before + p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
 }
 

@@ -16,8 +16,11 @@
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a thread owns a row), 8 and 9 MMA
 // issue for tile 0 and 1, 12-15 fetch K and V: a token's row lies wherever its
 // page does, so rows are fetched with 16-byte asynchronous copies (16 lanes a
-// row at D = 128) into the swizzled layout that the MMAs read, three tiles ahead
-// of the one that is handed over.
+// row at D = 128) into the swizzled layout that the MMAs read.  A copy's end
+// arrives on its stage's barrier by itself; the MMA warps put the proxy fence
+// between that and their reads.  (Handed over by the fetching warps, which wait
+// for one load after they have issued another, a stage comes late: 36 us for
+// 32000 tokens, 64 sequences of 4 heads on each of 8 K/V heads.)
 #include <cuda_runtime.h>
 
 #include "packed.h"
@@ -37,8 +40,8 @@ constexpr int kRegsOther = 80;
 static_assert(2 * 128 * kRegsSoftmax + 2 * 128 * kRegsOther <= kRegsLaunch * kThreads,
               "register split exceeds the CTA's allocation");
 constexpr float kLazy = 8.f;
-constexpr int kLag = 3;    // loads in flight; see the producer
 constexpr int kMasks = 4;  // tiles whose masks are held
+constexpr int kPages = 4;  // tiles whose pages are looked up ahead
 
 template <int D>
 struct Cfg {
@@ -56,21 +59,16 @@ struct Cfg {
   static constexpr uint32_t cO = 256;
 };
 static_assert(Cfg<128>::kSmemBytes <= 232448, "shared memory of one CTA");
-// A stage is filled again when the load kStages before has been read.  V of tile
-// j is read once K of j + 1 has been handed over, one load on, which happens
-// kLag loads later: kLag + 1 < kStages, or the producer would wait for itself.
-static_assert(kLag + 1 < Cfg<128>::kStages, "loads ahead");
-
 enum { bSFull = 0, bPFull = 2, bOFull = 4, bFinal = 6, bMask = 8, bKvFull0 = 8 + kMasks };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
   const int n = valid ? 16 : 0;  // 0: fills with zeros, reads nothing
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrives on `bar` when this thread's copies so far have landed; the barrier counts it like any arrival.
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 template <int N>
@@ -96,6 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oMISC + 4);
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + C::oMASK);  // [kMasks][4]: tokens that count
 
+  // the tails' kernel may start where there is room: it needs nothing of this one's
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int split = blockIdx.x, hk = blockIdx.z;
   const int rows = p.B * p.group, row0 = blockIdx.y * 2 * kPackedTile;
   const int tiles = rows - row0 > kPackedTile ? 2 : 1;  // Q tiles
@@ -108,13 +108,13 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars[bSFull + s], 1);
-      mbar_init(&bars[bPFull + s], 4);
+      mbar_init(&bars[bPFull + s], 5);  // four softmax warps and the turn
       mbar_init(&bars[bOFull + s], 1);
       mbar_init(&bars[bFinal + s], 1);
     }
     for (int i = 0; i < kMasks; ++i) mbar_init(&bars[bMask + i], 4);
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&kvFull[s], 4);       // the producer's warps
+      mbar_init(&kvFull[s], 128);     // the fetching threads
       mbar_init(&kvEmpty[s], tiles);  // the MMA warps
     }
     *abort_flag = 0;
@@ -137,38 +137,40 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
     constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;  // 16-byte pieces of a row, rows of a warp's copy
     const int c = lane % kChunks, rsub = lane / kChunks;
     const uint32_t col = (uint32_t)(c >> 3) * C::kPanel;
-    // Q, with the first K tile's group; rows past the last are zero
-    for (int s = 0; s < tiles; ++s)
-#pragma unroll 4
-      for (int i = 0; i < 32 / kRowsPer; ++i) {
-        const int r = w * 32 + i * kRowsPer + rsub, row = row0 + s * kPackedTile + r;
-        const bool ok = row < rows;
-        const int b = ok ? row / p.group : 0, h = hk * p.group + (ok ? row - b * p.group : 0);
-        cp16(smem_u32(smem + C::oQ + s * C::kTile) + col + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-             p.q + b * p.q_batch + h * p.q_head + 8 * c, ok);
-      }
     const int *table = p.table;  // the prefix's pages are those of the first sequence
     auto page_of = [&](int j) -> int {
       const int t = (j0 + j) * kPackedTile + w * 32 + lane;
       return j < n && t < p.first ? table[t / p.page_size] : -1;
     };
-    Ring<C::kStages> r, done;
-    int loads = 0, page = page_of(0);
-    auto hand_over = [&]() {
-      fence_proxy_async_smem();  // the copies' writes, before the MMAs read them
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kvFull[done.st]);
-      done.next();
-    };
+    // the pages of the next tiles, asked for side by side: each look-up takes as long as a tile's products
+    int pages[kPages];
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) pages[i] = page_of(i);
+    // Q, with the first K tile; rows past the last are zero.  Every lane knows where one row lies.
+    for (int s = 0; s < tiles; ++s) {
+      const int mine = row0 + s * kPackedTile + w * 32 + lane, b = mine / p.group;
+      const bool real = mine < rows;
+      const long long a = real ? b * p.q_batch + (hk * p.group + mine - b * p.group) * p.q_head : 0;
+      const uint32_t ok = __ballot_sync(0xffffffffu, real);
+#pragma unroll 4
+      for (int i = 0; i < 32 / kRowsPer; ++i) {
+        const int from = i * kRowsPer + rsub, r = w * 32 + from;
+        cp16(smem_u32(smem + C::oQ + s * C::kTile) + col + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+             p.q + __shfl_sync(0xffffffffu, a, from) + 8 * c, (ok >> from) & 1u);
+      }
+    }
+    Ring<C::kStages> r;
     for (int j = 0; j < n; ++j) {
-      const int t = (j0 + j) * kPackedTile + w * 32 + lane;
+      const int t = (j0 + j) * kPackedTile + w * 32 + lane, page = pages[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kPages; ++i) pages[i] = pages[i + 1];
+      pages[kPages - 1] = page_of(j + kPages);
       const bool ok = page >= 0 && page < p.n_pages;
       if (t < p.first && !ok) atomicCAS(p.status, 0, kStatusBadPage);
       const uint32_t valid = __ballot_sync(0xffffffffu, ok);
       const int off = t % p.page_size;
       const long long ka = ok ? page * p.ks.page + off * p.ks.token + hk * p.ks.head : 0;
       const long long va = ok ? page * p.vs.page + off * p.vs.token + hk * p.vs.head : 0;
-      page = page_of(j + 1);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         mbar_wait(&kvEmpty[r.st], r.ph ^ 1, g);
@@ -190,21 +192,18 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
             cp16(dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), base + a + 8 * c, (valid >> from) & 1u);
           }
         }
-        cp_commit();
+        cp_arrive(&kvFull[r.st]);
         r.next();
-        if (++loads > kLag) {
-          cp_wait<kLag>();
-          hand_over();
-        }
       }
     }
-    cp_wait<0>();
-    for (int i = min(loads, kLag); i > 0; --i) hand_over();
+    cp_wait_all();
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     const int s = warp - 8;
     if (s < tiles) {
       // --------------------------------------- MMA: a warp for each Q tile
+      // They take turns, as in the packed forward: tile 0's PV and next S, then tile
+      // 1's, so that one tile's softmax runs under the other's MMAs.
       constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
       constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
       Ring<C::kStages> rk;          // next K or V tile to be read
@@ -217,26 +216,38 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
       auto wait = [&](uint64_t *bar, uint32_t ph) {
         if (!mbar_wait(bar, ph, g)) lead = 0;
       };
-      auto issue_s = [&](int stage) {
+      auto wait_copies = [&](const Ring<C::kStages> &r) {
+        wait(&kvFull[r.st], r.ph);
+        fence_proxy_async_smem();
+      };
+      auto give_turn = [&](int to) {
+        if (lead) mbar_arrive(&bars[bPFull + to]);
+      };
+      auto issue_s = [&](int stage, bool pass) {
         tc_fence_after();
         const uint64_t dk = dk0 + ((stage * C::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
+          if (pass && kk == D / 16 - 2) give_turn(s ^ 1);  // the other warp wakes up under the last MMAs
           mma_ss_if(lead, tS, dq + off, dk + off, idS, kk > 0);
         }
         tc_commit_if(lead, &bars[bSFull + s]);
       };
-      wait(&kvFull[rk.st], rk.ph);  // Q and the first K tile
-      issue_s(rk.st);
+      wait_copies(rk);  // Q and the first K tile
+      issue_s(rk.st, false);
       tc_commit_if(lead, &kvEmpty[rk.st]);
       rk.next();
+      const bool pass = tiles == 2;
       for (int j = 0; j < n; ++j) {
         const Ring<C::kStages> rv = rk;  // V tile j; the next K tile follows it in the ring
         rk.next();
-        wait(&kvFull[rv.st], rv.ph);
-        if (j + 1 < n) wait(&kvFull[rk.st], rk.ph);
+        wait_copies(rv);
+        if (j + 1 < n) wait_copies(rk);
         const uint64_t dv = dv0 + ((rv.st * C::kTile) >> 4);
+        // tile 1's turn comes from tile 0's warp at the same KV tile, tile 0's from tile 1's at the one before, or,
+        // where there was none, from itself
+        if (s == 0 && (j == 0 || !pass)) give_turn(0);
         wait(&bars[bPFull + s], p_ph);
         p_ph ^= 1;
         tc_fence_after();
@@ -245,10 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
           mma_ts_if(lead, tO, tS + kk * 8, dv + ((kk * 2048) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
         tc_commit_if(lead, &kvEmpty[rv.st]);
         if (j + 1 < n) {
-          issue_s(rk.st);  // MMAs run in issue order: PV has read P before S overwrites it
+          issue_s(rk.st, pass);  // MMAs run in issue order: PV has read P before S overwrites it
           tc_commit_if(lead, &kvEmpty[rk.st]);
           rk.next();
         } else {
+          if (pass && s == 0) give_turn(1);
           tc_commit_if(lead, &bars[bOFull + s]);
         }
       }
@@ -269,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
       // tokens of the split that this row attends: a sequence may end inside the prefix
       const int limit =
           (real ? max(0, min(min(p.lengths[b], p.max_pages * p.page_size), p.first)) : 0) - j0 * kPackedTile;
-      float m = -INFINITY, l = 0.f;  // the maximum the row refers to (scaled, log2; -inf: nothing counted yet), its sum
+      float m = -INFINITY;   // the maximum the row refers to (scaled, log2; -inf: nothing counted yet)
+      uint64_t l2 = 0;       // its sum, in two halves
       // After an abort the loop runs on with whatever tensor memory holds: no
       // wait blocks any more, and the status word tells that O is not valid.
       for (int j = 0; j < n; ++j) {
@@ -311,10 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
         const bool moves = top > m + kLazy;
         if (__any_sync(0xffffffffu, moves)) {
           // the product before has completed (it did before S(j) did), so O may be rewritten here
-          const float m_new = moves ? top : m;
-          const float f = moves ? ex2(m - m_new) : 1.f;
-          m = m_new;
-          l *= f;
+          const float f = moves ? ex2(m - top) : 1.f;
+          m = moves ? top : m;
+          l2 = mul2(l2, pack2(f, f));
           if (j > 0) {
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 16) {
@@ -327,15 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {l, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nm2 = pack2(-ref, -ref);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float a0 = ex2(fmaf(__uint_as_float(x[c][e]), p.scale_log2, -ref));
-            const float a1 = ex2(fmaf(__uint_as_float(x[c][e + 1]), p.scale_log2, -ref));
-            sum[e / 2 & 3] += a0 + a1;
+            float a0, a1;
+            unpack2(fma2(pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2), a0, a1);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+            x[c][e] = __float_as_uint(a0);
+            x[c][e + 1] = __float_as_uint(a1);
             pk[e >> 1] = pack_bf16(a0, a1);
           }
           tmem_st16(tS + 16 * c, pk);
@@ -344,23 +359,53 @@ __global__ void __launch_bounds__(kThreads, 1) dash_prefix_kernel(const __grid_c
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[bPFull + s]);
-        l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // the sum is not on the product's path
+        uint64_t acc2[4] = {l2, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc2[c] = add2(acc2[c], pack2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+        l2 = add2(add2(acc2[0], acc2[1]), add2(acc2[2], acc2[3]));
       }
+      float la, lb;
+      unpack2(l2, la, lb);
+      const float l = la + lb;
       const bool ok = mbar_wait(&bars[bOFull + s], 0, g);
       __syncwarp();
       tc_fence_after();
+      // A row's result goes through this tile's place of Q, which every S has read, so that a warp's store is two
+      // rows (or four) side by side and not a piece of 32; half the columns at a time, each warp its own rows.
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const size_t at = ((size_t)b * p.Hq + h) * (p.parts_before + p.max_splits) + split;
+      const int parts = p.parts_before + p.max_splits;
+      const size_t at = ((size_t)b * p.Hq + h) * parts + split;
+      constexpr int kWide = D / 2, kVecs = kWide / 4, kPer = 32 / kVecs;  // columns at a time; rows of a warp's store
+      static_assert(kPackedTile * kWide * 4 == C::kTile, "a tile's rows fill its Q");
+      float4 *stage = reinterpret_cast<float4 *>(smem + C::oQ + s * C::kTile) + sub * 32 * kVecs;
+      const uint32_t out = __ballot_sync(0xffffffffu, real && ok);
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(tO + c0, r);
-        if (real && ok) {
+      for (int c0 = 0; c0 < D; c0 += kWide) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * inv);
+        for (int part = 0; part < kWide / 32; ++part) {
+          uint32_t r[32];
+          tmem_ld32(tO + c0 + 32 * part, r);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) st_32b(p.part_o + at * D + c0 + e, r + e, p.wide);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t *v = r + 4 * e;
+            stage[lane * kVecs + ((8 * part + e) ^ (lane & (kVecs - 1)))] =
+                make_float4(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv, __uint_as_float(v[2]) * inv,
+                            __uint_as_float(v[3]) * inv);
+          }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int from = kPer * i + lane / kVecs, c = lane % kVecs;
+          const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)at, from);
+          if ((out >> from) & 1u)
+            *reinterpret_cast<float4 *>(p.part_o + to * D + c0 + 4 * c) = stage[from * kVecs + (c ^ (from & (kVecs - 1)))];
+        }
+        __syncwarp();
       }
       if (real && ok) p.part_ml[at] = make_float2(m, l);
       tc_fence_before();

@@ -9,7 +9,6 @@ namespace dash {
 struct SharedParams : DecodeParams {  // first: the prefix; parts_before: its splits
   int prefix_tiles;      // KV tiles of 128 tokens
   int tiles_per_split;
-  bool wide;             // part_o starts at a multiple of 32 bytes
   long long spin_limit_ns;
 };
 
