@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libdash.so")
 
 SOURCES = ["api.cpp", "schedule.cpp", "place.cpp", "packed_api.cpp", "packed_plan.cpp", "bwd.cu", "fwd.cu",
            "noalloc.cu", "place.cu", "packed_fwd.cu", "packed_bwd.cu", "paged.cu", "ops_api.cpp", "norm_rope.cu",
-           "cache8_api.cpp", "cache8.cu", "shared.cu"]
+           "cache8_api.cpp", "cache8.cu", "decode8.cu", "shared.cu"]
 BINDING = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE]

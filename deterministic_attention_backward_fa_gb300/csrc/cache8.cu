@@ -30,6 +30,7 @@
 
 #include "cache8.h"
 #include "decode.cuh"
+#include "fp8.cuh"
 #include "packed.h"
 #include "sm103.cuh"
 
@@ -40,21 +41,6 @@ using namespace dev;
 namespace {
 
 // ------------------------------------------------------------------ codes
-// 2^(e - 127) of an exponent field 1 <= e <= 254
-__device__ __forceinline__ float pow2_field(int e) { return __uint_as_float((uint32_t)e << 23); }
-
-// Two e4m3 codes as two f16 of the same values.
-__device__ __forceinline__ uint32_t widen8(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-  return r;
-}
-__device__ __forceinline__ uint32_t narrow8(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The scale's exponent field for a row whose largest magnitude has the bf16 bits
 // `top` (below 0x7f80): 448 = 1.75 x 2^8, so a mantissa of up to 0x60 fits with
 // 8 less, and one above it needs 7 less.
@@ -326,11 +312,6 @@ constexpr int kTok = 16;              // tokens of a warp's step
 constexpr int kStep = kWarps * kTok;  // tokens of the CTA's step
 constexpr float kLazy = 256.f;        // growth of a term past its maximum that is left standing
 
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -346,28 +327,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ int quotient(const Divisor &d, int n) {
-  return (int)((__umulhi((unsigned)n, d.mul) + (unsigned)n) >> d.shift);
-}
-template <class T>
-__device__ __forceinline__ const T *wide_add(const T *p, int a, int b) {
-  return p + (long long)a * b;
-}
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
-  if (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
-}
-template <int kBytes>
-__device__ __forceinline__ void cp_async_if(uint32_t dst, const void *src, bool valid) {
-  const int n = valid ? kBytes : 0;  // 0: fills with zeros, reads nothing
-  if (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(kBytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -516,7 +475,7 @@ __global__ void __launch_bounds__(kDecodeThreads, Dec8<D, NT>::kCtas)
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int f = min(253, 268 - (int)(top >> 7));  // the largest magnitude becomes 2^14 to 2^15
-      const float up = pow2_field(f);
+      const float up = top < 0x7f80u ? pow2_field(f) : NAN;  // a head with a NaN or an infinity is all NaN
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -599,25 +558,30 @@ __global__ void __launch_bounds__(kDecodeThreads, Dec8<D, NT>::kCtas)
       // does not count is one here (-inf times its zero scale).
       const bool fast = most <= kLazy;
       if (!__all_sync(0xffffffffu, fast)) {
+        // only the heads that need it move, so that a head's bits do not depend on the others
         const float lv[2] = {lg2(vs[0]), lg2(vs[1])};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = s[nt][e] * (sc[nt][e & 1] * ks[e >> 1]);
-            s[nt][e] = (valid >> (g + 8 * (e >> 1))) & 1u ? y : -INFINITY;
-          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float fo[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float tm = fmaxf(s[nt][c], s[nt][2 + c]), tM = fmaxf(s[nt][c] + lv[0], s[nt][2 + c] + lv[1]);
+            bool within = true;
+            float x[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int e = 2 * r + c;
+              within = within && pr[nt][e] <= kLazy && pv[nt][e] <= kLazy;
+              x[r] = (valid >> (g + 8 * r)) & 1u ? s[nt][e] * (sc[nt][c] * ks[r]) : -INFINITY;
+            }
+            const bool moves = (__ballot_sync(0xffffffffu, !within) & (0x11111111u << t4)) != 0;
+            float tm = fmaxf(x[0], x[1]), tM = fmaxf(x[0] + lv[0], x[1] + lv[1]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
               tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
               tM = fmaxf(tM, __shfl_xor_sync(0xffffffffu, tM, o));
             }
+            fo[c] = 1.f;
+            if (!moves) continue;
             const float m1 = fmaxf(m[nt][c], tm), M1 = fmaxf(M[nt][c], tM);
             const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
             l[nt][c] *= ex2(m[nt][c] - mr);
@@ -628,8 +592,8 @@ __global__ void __launch_bounds__(kDecodeThreads, Dec8<D, NT>::kCtas)
             up[nt][c] = fabsf(m1 - M1) < 100.f ? ex2(m1 - M1) : NAN;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              pr[nt][2 * r + c] = ex2(s[nt][2 * r + c] - mr);
-              pv[nt][2 * r + c] = ex2(s[nt][2 * r + c] + lv[r] - Mr);
+              pr[nt][2 * r + c] = ex2(x[r] - mr);
+              pv[nt][2 * r + c] = ex2(x[r] + lv[r] - Mr);
             }
             lsum[nt][c] = pr[nt][c] + pr[nt][2 + c];
           }
@@ -747,6 +711,12 @@ cudaError_t launch_decode_t(const Decode8Params &p, int num_sms, cudaStream_t st
   }
   const int resident = Dec8<D, NT>::kCtas * num_sms;
   const bool all = items <= resident;
+  if (!all && NT == 1) {
+    Decode8Params q = p;
+    q.least_chunk = 1024;  // an item's start and end cost as much as two tiles of 128 tokens
+    const cudaError_t e = launch_decode8_wide(D, q, num_sms, stream);
+    return e != cudaSuccess || q.max_splits <= 1 ? e : launch_decode_join(D, q, stream);
+  }
   const cudaError_t e = launch(all ? dash_decode8_kernel<D, NT, kPlain> : dash_decode8_kernel<D, NT, kScan>,
                                all ? (int)items : resident, kDecodeThreads, kSmem, stream, nullptr, p);
   return e != cudaSuccess || p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
@@ -769,7 +739,8 @@ cudaError_t prepare_cache8() {
   for (auto kernel : {dash_cache8_write_kernel<64>, dash_cache8_write_kernel<128>, dash_cache8_read_kernel<64>,
                       dash_cache8_read_kernel<128>})
     if (const cudaError_t e = cudaFuncGetAttributes(&fa, kernel)) return e;
-  cudaError_t e = cudaFuncGetAttributes(&fa, dash_cache8_copy_kernel<64>);
+  cudaError_t e = prepare_decode8_wide();
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, dash_cache8_copy_kernel<64>);
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, dash_cache8_copy_kernel<kCopyPairs8>);
   if (e == cudaSuccess) e = prepare_t<64, 1>();
   if (e == cudaSuccess) e = prepare_t<64, 2>();

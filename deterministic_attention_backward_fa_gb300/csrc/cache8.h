@@ -52,8 +52,12 @@ struct Decode8Params : DecodeParams {
   Divisor page;  // page_size
   // Steps of 16 tokens lie in one page, and strides fit 32 bits.
   bool whole;
+  long long spin_limit_ns;
 };
 cudaError_t prepare_cache8();
+// The form for calls that fill the GPU with groups of up to 8 heads (decode8.cu), but for the join.
+cudaError_t prepare_decode8_wide();
+cudaError_t launch_decode8_wide(int D, const Decode8Params &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode8(int D, const Decode8Params &p, int num_sms, cudaStream_t stream);
 
 }  // namespace dash

@@ -133,6 +133,7 @@ dash_status_t dash_attn_decode_fp8(const void *q, const void *k_pages, const voi
                       strides ? strides + 4 : nullptr, &p.c)))
     return st;
   p.page = dash::divisor(page_size);
+  p.spin_limit_ns = kSpinNs;
   p.whole = page_size % 16 == 0;
   for (const dash::CacheStrides &s : {p.c.ks, p.c.vs, p.c.kss, p.c.vss})
     for (long long x : {s.page, s.token}) p.whole = p.whole && x <= INT32_MAX;

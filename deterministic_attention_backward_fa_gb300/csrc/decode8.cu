@@ -1,0 +1,641 @@
+// Decode attention over the 8-bit paged cache for calls that fill the GPU: the
+// products on the 5th-generation tensor cores, with the codes as they lie.
+//
+// Per sequence, K/V head and split, over tiles of 128 tokens (scales a_t of K,
+// c_t of V, up to 8 Q heads of the group):
+//   x_t = scale log2(e) a_t (q . k_t),  l += 2^(x_t - m),  O += 2^(x_t - M) c_t v_t,
+// m and M the running maxima of x_t and x_t + log2 c_t.  The codes are the large
+// operand and need no widening; what meets them, Q and the weights, is split
+// into three e4m3 terms of 4 bits each, every next one 16 times larger:
+//   y = y1 + y2 / 16 + y3 / 256,  y1 = e4m3(y), y2 = e4m3(16 (y - y1)), ...
+// which are columns of their own, so that their scales stay apart until the sums
+// are 32-bit:
+//   S^T [128 tokens x 32] = K [128 x D] Q^T,  O^T [D x 32] += V^T [D x 128] P^T,
+// columns (term, head).  Q's 8 bits are exact down to 2^-17 of its row's largest
+// value and off by 2^-26 of that below; a weight is off by at most 2^-12 of
+// itself, or by 2^-22 of the largest that its head has met (whose own M goes by
+// x_t + log2 c_t, so that it is what counts in O, whatever the scales of V are).
+//
+// The bound is HBM: 2 (D + 4) bytes a token and K/V head.  On the plain pipes the
+// widening alone takes half the issue slots (cache8.cu's kernel stays at 60 % of
+// the copy rate); here a token costs a softmax thread's instructions for its 8
+// heads, once.
+//
+// A persistent CTA, two on an SM, walks its items (longest splits first) without
+// a break in its loads.  Warps: 0-3 softmax (a thread owns a token, and in the
+// end a dim), 4-7 fetch (a token's row lies wherever its page does: 16-byte
+// asynchronous copies into the swizzled layout, whose ends arrive on barriers by
+// themselves) and split Q, 8 issues the MMAs, the next tile's scores before this
+// tile's O.  Tensor memory: S twice at 0 and 16, O at 32.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "cache8.h"
+#include "decode.cuh"
+#include "fp8.cuh"
+#include "sm103.cuh"
+
+namespace dash {
+
+using namespace dev;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kFetch = 4;  // warps that fetch, 32 rows each
+constexpr int kMma = 8;    // the warp that issues; 9-11 make the warpgroup whole
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsFetch = 64, kRegsMma = 48;
+static_assert(kRegsSoftmax + kRegsFetch + kRegsMma <= 3 * kRegsLaunch, "register split exceeds the CTA's allocation");
+constexpr int kHeads = 8, kTerms = 2, kCols = kTerms * kHeads;
+constexpr int kTile8 = 128;        // tokens
+constexpr int kStages = 5;         // K and V tiles
+constexpr int kSlots = 4;          // tiles whose scales and masks are held
+constexpr float kTop = 16.f;       // where a weight's maximum is put, ...
+constexpr float kMost = 256.f;     // ... and where it is moved
+
+constexpr uint32_t kStageBytes = kTile8 * 128;  // rows of 128 bytes, D of them used
+constexpr uint32_t kColBytes = kCols * 128;     // Q or P: a row of 128 bytes for each column
+constexpr uint32_t oKV = 0;
+constexpr uint32_t oQ = oKV + kStages * kStageBytes;   // twice
+constexpr uint32_t oP = oQ + 2 * kColBytes;            // twice
+constexpr uint32_t oScale = oP + 2 * kColBytes;        // [kSlots][2][128]
+constexpr uint32_t oMask = oScale + kSlots * 2 * kTile8 * 4;  // [kSlots][4]
+constexpr uint32_t oSc = oMask + kSlots * 16;          // [2][8] a score's factor
+constexpr uint32_t oRed = oSc + 2 * kHeads * 4;        // [4][16], then a mask of heads [4]
+constexpr uint32_t oSum = oRed + 4 * 16 * 4 + 16;           // [4][8]
+constexpr uint32_t oBar = oSum + 4 * kHeads * 4;
+enum {
+  bSFull = 0, bPFull = 2, bPvDone = 4, bQFull = 6, bQEmpty = 8, bTile = 10, bKvFull = bTile + kSlots,
+  bKvEmpty = bKvFull + kStages, bFinal = bKvEmpty + kStages, kBars
+};
+constexpr uint32_t oMisc = oBar + kBars * 8;
+constexpr uint32_t kSmem = oMisc + 16;
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
+constexpr uint32_t cS = 0, cO = 2 * kCols, kTmem = 64;
+
+// D[tmem] (+)= A[smem] * B[smem], 8-bit operands
+__device__ __forceinline__ void mma8_if(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// Instruction descriptor: e4m3 operands, 32-bit sums; a_mn: A is MN-major.
+__host__ __device__ constexpr uint32_t idesc8(int M, int N, int a_mn) {
+  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Whether any of the 128 softmax threads says so.
+__device__ __forceinline__ bool any_of_128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float x) {  // NaN counts as -inf
+  int i = x == x ? __float_as_int(x) : (int)0xff800000;
+  i ^= (i >> 31) & 0x7fffffff;
+  i = __reduce_max_sync(0xffffffffu, i);
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// The terms of two values, as codes: term k in bytes {a, b} of t[k].
+__device__ __forceinline__ void terms_of(float a, float b, uint32_t (&t)[kTerms]) {
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k) {
+    t[k] = narrow8(a, b);
+    if (k + 1 < kTerms) {
+      const uint32_t w = widen8(t[k]);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+      a = (a - v.x) * 16.f;
+      b = (b - v.y) * 16.f;
+    }
+  }
+}
+
+// Items of a CTA: (split, K/V head) numbers item, item + grid, ...; splits are
+// numbered by sequence, those of the longest kind first (of up to kSorted
+// sequences).  A warp scans 32 sequences at a time and remembers how far it got.
+constexpr int kSorted = 1024;
+struct Walk {
+  long long base = 0;  // splits before the block of sequences b0
+  int b0 = 0, chunk, at = -1;
+  int n = 0, upto = 0, total = 0;  // of the lane's sequence, up to it, of the block
+  int b, split;
+
+  __device__ __forceinline__ explicit Walk(const DecodeParams &p)
+      : chunk(p.B <= kSorted ? decode_chunk(p.max_pages * p.page_size, p.least_chunk) : 0) {}
+  // All lanes of a warp ask together.
+  __device__ __forceinline__ bool find(const DecodeParams &p, long long want, int lane) {
+    while (true) {
+      if (at != b0) {
+        const int mine = b0 + lane, len = mine < p.B ? decode_len(p, mine) : 0;
+        n = mine < p.B && (chunk == 0 || decode_chunk(len, p.least_chunk) == chunk)
+                ? max(1, decode_splits(len, p.least_chunk))
+                : 0;
+        upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        at = b0;
+      }
+      if (want < base + total) {
+        const int off = (int)(want - base);
+        const int src = __popc(__ballot_sync(0xffffffffu, upto <= off));
+        b = b0 + src;
+        split = off - __shfl_sync(0xffffffffu, upto - n, src);
+        return true;
+      }
+      base += total;
+      b0 += 32;
+      at = -1;
+      if (b0 >= p.B) {
+        b0 = 0;
+        if (chunk <= p.least_chunk) return false;  // nothing shorter, or all in one walk
+        chunk >>= 1;
+      }
+    }
+  }
+};
+
+// Tiles and place of an item.
+struct Part {
+  int b, hk, split, n_splits, begin, end, tiles;
+  __device__ __forceinline__ Part(const DecodeParams &p, const Walk &w, int head) : b(w.b), hk(head), split(w.split) {
+    const int len = decode_len(p, b), chunk = decode_chunk(len, p.least_chunk);
+    n_splits = max(1, decode_splits(len, p.least_chunk));
+    begin = split * chunk;
+    end = min(len, begin + chunk);
+    tiles = (end - begin + kTile8 - 1) / kTile8;  // 0: an empty sequence
+  }
+};
+
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __grid_constant__ Decode8Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // the join may be set up now; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = warp_id(), lane = threadIdx.x & 31;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + oBar);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + oMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + oMisc + 4);
+  float *scales = reinterpret_cast<float *>(smem + oScale);
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + oMask);
+  float *factors = reinterpret_cast<float *>(smem + oSc);
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[bSFull + s], 1);
+      mbar_init(&bars[bPFull + s], 1);
+      mbar_init(&bars[bPvDone + s], 1);
+      mbar_init(&bars[bQFull + s], kFetch);
+      mbar_init(&bars[bQEmpty + s], 5);  // the MMA warp and the softmax warps
+    }
+    for (int s = 0; s < kSlots; ++s) mbar_init(&bars[bTile + s], 33 * kFetch);  // the copies' ends and the masks
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars[bKvFull + s], 32 * kFetch);
+      mbar_init(&bars[bKvEmpty + s], 1);
+    }
+    mbar_init(&bars[bFinal], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
+  Walk walk(p);
+  int ib = 0;            // the item's place of Q
+  uint32_t iph = 0;      // and its phase
+  uint32_t T = 0;        // tiles before this item
+
+  if (warp >= 4 && warp < kMma) {
+    // ------------------------------------------------------ loads, and Q
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFetch));
+    const int w = warp - 4, row = w * 32 + lane;
+    constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;  // 16-byte pieces of a row, rows of a warp's copy
+    const int c = lane % kChunks, rsub = lane / kChunks;
+    Ring<kStages> r;
+    for (long long item = blockIdx.x;; item += gridDim.x) {
+      const long long want = item / p.Hkv;
+      if (!walk.find(p, want, lane)) break;
+      const Part it(p, walk, (int)(item - want * p.Hkv));
+      if (it.tiles == 0) continue;
+      // Q: a head is D / 8 lanes
+      constexpr int kLanes = D / 8;
+      const int head = row / kLanes, dim = lane % kLanes * 8;
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (head < p.group)
+        raw = *reinterpret_cast<const uint4 *>(p.q + it.b * p.q_batch + (long long)(it.hk * p.group + head) * p.q_head +
+                                               dim);
+      const int *table = p.table + it.b * p.table_row;
+      const uint8_t *kbase = p.c.k + it.hk * p.c.ks.head + 16 * c, *vbase = p.c.v + it.hk * p.c.vs.head + 16 * c;
+      const float *ksbase = p.c.k_scale + it.hk * p.c.kss.head, *vsbase = p.c.v_scale + it.hk * p.c.vss.head;
+      auto page_of = [&](int j) -> int {
+        const int t = it.begin + j * kTile8 + row;
+        return t < it.end ? table[quotient(p.page, t)] : -1;
+      };
+      // The rows of a tile of K (with the scales of both) or V, where the page and place of the lane's token are known.
+      struct Where {
+        int page, off;
+        uint32_t valid;
+      };
+      auto fetch = [&](bool is_v, uint32_t tile, const Where &at) {
+        mbar_wait(&bars[bKvEmpty + r.st], r.ph ^ 1, g);
+        __syncwarp();
+        const CacheStrides &st = is_v ? p.c.vs : p.c.ks;
+        const uint32_t slot = tile % kSlots;
+        const uint32_t dst = smem_u32(smem + oKV + r.st * kStageBytes) + (w * 32 + rsub) * 128;
+        const uint8_t *base = is_v ? vbase : kbase;
+        if (!warp_aborted(g)) {
+          if (at.valid == 0xffffffffu && p.whole) {
+            const long long step = kRowsPer * st.token;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // 16 tokens lie in one page
+              const int pg = __shfl_sync(0xffffffffu, at.page, 16 * half), of = __shfl_sync(0xffffffffu, at.off, 16 * half);
+              const uint8_t *from = wide_add(wide_add(base, pg, (int)st.page), of + rsub, (int)st.token);
+#pragma unroll
+              for (int i = 0; i < 16 / kRowsPer; ++i, from += step) {
+                const int rr = 16 * half + i * kRowsPer;
+                cp_async<16>(dst + rr * 128 + ((c ^ ((rr + rsub) & 7)) << 4), from);
+              }
+            }
+          } else {
+            const long long a = (at.valid >> lane) & 1u ? at.page * st.page + at.off * st.token : 0;
+#pragma unroll
+            for (int i = 0; i < 32 / kRowsPer; ++i) {
+              const int rr = i * kRowsPer + rsub;
+              const long long x = __shfl_sync(0xffffffffu, a, rr);
+              cp_async_if<16>(dst + i * kRowsPer * 128 + ((c ^ (rr & 7)) << 4), base + x, (at.valid >> rr) & 1u);
+            }
+          }
+          if (!is_v) {
+            const bool ok = (at.valid >> lane) & 1u;
+            const uint32_t sd = smem_u32(scales + slot * 2 * kTile8 + row);
+            cp_async_if<4>(sd, ok ? ksbase + at.page * p.c.kss.page + at.off * p.c.kss.token : ksbase, ok);
+            cp_async_if<4>(sd + kTile8 * 4, ok ? vsbase + at.page * p.c.vss.page + at.off * p.c.vss.token : vsbase, ok);
+          }
+        }
+        if (!is_v) {
+          // the slot's last tile has been read: its weights were, by the product that freed this stage
+          if (lane == 0) {
+            masks[slot * 4 + w] = at.valid;
+            mbar_arrive(&bars[bTile + slot]);
+          }
+          cp_arrive(&bars[bTile + slot]);
+        }
+        cp_arrive(&bars[bKvFull + r.st]);
+        r.next();
+      };
+      // V of a tile follows K of the next one; pages are looked up two tiles ahead of K
+      Where k, v = {};
+      int page = page_of(0), next = page_of(1);
+      for (int j = 0; j <= it.tiles; ++j) {
+        if (j < it.tiles) {
+          const int t = it.begin + j * kTile8 + row;
+          k.page = page;
+          const bool ok = page >= 0 && page < p.n_pages;
+          if (t < it.end && !ok) atomicCAS(p.status, 0, kStatusBadPage);
+          k.off = t - quotient(p.page, t) * p.page_size;
+          k.valid = __ballot_sync(0xffffffffu, ok);
+          page = next;
+          next = page_of(j + 2);
+          fetch(false, T + j, k);
+          if (j == 0) {
+            // Q's largest value is put at 2^7 to 2^8; a head with a NaN or an infinity is all NaN
+            mbar_wait(&bars[bQEmpty + ib], iph ^ 1, g);
+            __syncwarp();
+            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int f = min(253, 261 - (int)(top >> 7));
+            const float up = top < 0x7f80u ? pow2_field(f) : NAN;
+            uint32_t codes[kTerms][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t t2[kTerms];
+              terms_of(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up, t2);
+#pragma unroll
+              for (int n = 0; n < kTerms; ++n) codes[n][i >> 1] = i & 1 ? codes[n][i >> 1] | t2[n] << 16 : t2[n];
+            }
+            if (head < kHeads) {
+#pragma unroll
+              for (int i = 0; i < kTerms; ++i) {
+                const int n = i * kHeads + head;
+                *reinterpret_cast<uint2 *>(smem + oQ + ib * kColBytes + n * 128 + (((dim >> 4) ^ (n & 7)) << 4) +
+                                           (dim & 15)) = make_uint2(codes[i][0], codes[i][1]);
+              }
+              if (dim == 0) factors[ib * kHeads + head] = p.scale_log2 * pow2_field(254 - f);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[bQFull + ib]);
+          }
+        }
+        if (j > 0) fetch(true, 0, v);
+        v = k;
+      }
+      T += it.tiles;
+      ib ^= 1;
+      if (ib == 0) iph ^= 1;
+    }
+    cp_wait_all();
+  } else if (warp >= kMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == kMma) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t idS = idesc8(128, kCols, 0), idO = idesc8(128, kCols, 1);
+    Ring<kStages> r;
+    uint32_t lead = elect_one();  // 0 in every lane once a wait has failed: nothing more is issued
+    const uint64_t k0 = sw128_desc(smem_u32(smem + oKV), 16, 1024), v0 = sw128_desc(smem_u32(smem + oKV), kStageBytes, 1024);
+    const uint64_t q0 = sw128_desc(smem_u32(smem + oQ), 16, 1024), p0 = sw128_desc(smem_u32(smem + oP), 16, 1024);
+    auto wait = [&](uint64_t *bar, uint32_t ph) {
+      if (!mbar_wait(bar, ph, g)) lead = 0;
+    };
+    for (long long item = blockIdx.x;; item += gridDim.x) {
+      const long long want = item / p.Hkv;
+      if (!walk.find(p, want, lane)) break;
+      const Part it(p, walk, (int)(item - want * p.Hkv));
+      if (it.tiles == 0) continue;
+      auto issue_s = [&](uint32_t tile) {
+        wait(&bars[bKvFull + r.st], r.ph);
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t a = k0 + ((r.st * kStageBytes) >> 4), b = q0 + ((ib * kColBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) mma8_if(lead, tmem + cS + (tile & 1) * kCols, a + 2 * kk, b + 2 * kk, idS, kk > 0);
+        tc_commit_if(lead, &bars[bSFull + (tile & 1)]);
+        tc_commit_if(lead, &bars[bKvEmpty + r.st]);
+        r.next();
+      };
+      wait(&bars[bQFull + ib], iph);
+      issue_s(T);
+      if (it.tiles == 1) tc_commit_if(lead, &bars[bQEmpty + ib]);
+      for (int j = 0; j < it.tiles; ++j) {
+        const uint32_t tile = T + j;
+        // its place of S was read before the weights of the tile before this one came
+        if (j + 1 < it.tiles) {
+          issue_s(tile + 1);
+          if (j + 2 == it.tiles) tc_commit_if(lead, &bars[bQEmpty + ib]);
+        }
+        wait(&bars[bKvFull + r.st], r.ph);
+        fence_proxy_async_smem();
+        wait(&bars[bPFull + (tile & 1)], (tile >> 1) & 1);
+        tc_fence_after();
+        const uint64_t a = v0 + ((r.st * kStageBytes) >> 4), b = p0 + (((tile & 1) * kColBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTile8 / 32; ++kk)
+          mma8_if(lead, tmem + cO, a + kk * (4096 >> 4), b + 2 * kk, idO, (j > 0 || kk > 0) ? 1u : 0u);
+        tc_commit_if(lead, &bars[bPvDone + (tile & 1)]);
+        tc_commit_if(lead, &bars[bKvEmpty + r.st]);
+        r.next();
+      }
+      T += it.tiles;
+      ib ^= 1;
+      if (ib == 0) iph ^= 1;
+    }
+    // every MMA has completed before tensor memory is released (at once if none was issued)
+    tc_commit_if(elect_one(), &bars[bFinal]);
+    mbar_drain(&bars[bFinal], 0, g.limit_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int tok = threadIdx.x;
+    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+    float *red = reinterpret_cast<float *>(smem + oRed), *sums = reinterpret_cast<float *>(smem + oSum);
+    for (long long item = blockIdx.x;; item += gridDim.x) {
+      const long long want = item / p.Hkv;
+      if (!walk.find(p, want, lane)) break;
+      const Part it(p, walk, (int)(item - want * p.Hkv));
+      const int h0 = it.hk * p.group;
+      float sc[kHeads], m[kHeads], M[kHeads], up[kHeads], l[kHeads];
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        sc[h] = 0.f;
+        m[h] = M[h] = -INFINITY;
+        up[h] = NAN;
+        l[h] = 0.f;
+      }
+      if (it.tiles > 0) {
+        mbar_wait(&bars[bQFull + ib], iph, g);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) sc[h] = factors[ib * kHeads + h];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[bQEmpty + ib]);
+      }
+      // After an abort the loop runs on with whatever tensor memory holds: no
+      // wait blocks any more, and the status word tells that O is not valid.
+      for (int j = 0; j < it.tiles; ++j) {
+        const uint32_t tile = T + j, slot = tile % kSlots;
+        mbar_wait(&bars[bTile + slot], (tile / kSlots) & 1, g);
+        const float ks = scales[slot * 2 * kTile8 + tok], vs = scales[slot * 2 * kTile8 + kTile8 + tok];
+        const bool valid = (masks[slot * 4 + warp] >> lane) & 1u;
+        mbar_wait(&bars[bSFull + (tile & 1)], (tile >> 1) & 1, g);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t s[16];
+        tmem_ld16(tl + cS + (tile & 1) * kCols, s);
+        float pr[kHeads], pv[kHeads], most = 0.f;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+          const float y = fmaf(__uint_as_float(s[kHeads + h]), 1.f / 16, __uint_as_float(s[h])) * ks;
+          s[h] = __float_as_uint(y);
+          pr[h] = valid ? ex2(fmaf(y, sc[h], -m[h])) : 0.f;
+          pv[h] = valid ? pr[h] * (vs * up[h]) : 0.f;
+          most = max_nan(most, max_nan(pr[h], pv[h]));
+        }
+        mbar_wait(&bars[bPvDone + (tile & 1)], ((tile >> 1) & 1) ^ 1, g);  // its place of P is free
+        // the weights' terms, a byte in each column's row
+        uint8_t *pt = smem + oP + (tile & 1) * kColBytes + (tok & 15);
+        auto send = [&]() {
+#pragma unroll
+          for (int h = 0; h < kHeads; h += 2) {
+            uint32_t t2[kTerms];
+            terms_of(pv[h], pv[h + 1], t2);
+#pragma unroll
+            for (int k = 0; k < kTerms; ++k) {
+              const int n = k * kHeads + h;
+              pt[n * 128 + (((tok >> 4) ^ (n & 7)) << 4)] = (uint8_t)t2[k];
+              pt[(n + 1) * 128 + (((tok >> 4) ^ ((n + 1) & 7)) << 4)] = (uint8_t)(t2[k] >> 8);
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+        };
+        send();
+        // A NaN is not within the limit, and where nothing counts yet no number is: the step is done anew, with new maxima.
+        if (any_of_128(!(most <= kMost))) {
+          // only the heads that need it move, so that a head's bits do not depend on the others
+          const float lv = lg2(vs);
+          uint32_t over = 0;
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h) {
+            const float x = valid ? __uint_as_float(s[h]) * sc[h] : -INFINITY;
+            const float a = warp_max(x), b = warp_max(x + lv);
+            s[h] = __float_as_uint(x);
+            over |= (pr[h] <= kMost && pv[h] <= kMost ? 0u : 1u) << h;
+            if (lane == 0) {
+              red[warp * 16 + h] = a;
+              red[warp * 16 + 8 + h] = b;
+            }
+          }
+          over = __reduce_or_sync(0xffffffffu, over);
+          uint32_t *all_over = reinterpret_cast<uint32_t *>(red + 64);
+          if (lane == 0) all_over[warp] = over;
+          named_bar(2, 128);
+          over = (all_over[0] | all_over[1]) | (all_over[2] | all_over[3]);
+          if (j > 0) {  // the product before has completed: O may be rewritten
+            mbar_wait(&bars[bPvDone + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, g);
+            __syncwarp();
+            tc_fence_after();
+          }
+          float fo[kHeads];
+#pragma unroll
+          for (int h = 0; h < kHeads; ++h) {
+            fo[h] = 1.f;
+            if (!((over >> h) & 1u)) continue;
+            float m1 = m[h], M1 = M[h];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              m1 = fmaxf(m1, red[w * 16 + h]);
+              M1 = fmaxf(M1, red[w * 16 + 8 + h]);
+            }
+            const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
+            l[h] *= ex2(m[h] - mr);
+            fo[h] = ex2(M[h] - Mr);
+            m[h] = m1;
+            M[h] = M1;
+            // a factor that 32 bits cannot hold stays NaN, and every step comes here
+            up[h] = fabsf(m1 - M1) < 100.f ? kTop * ex2(m1 - M1) : NAN;
+            const float x = __uint_as_float(s[h]);
+            pr[h] = ex2(x - mr);
+            pv[h] = valid ? kTop * ex2(x + lv - Mr) : 0.f;
+          }
+          if (j > 0) {
+            uint32_t o[16];
+            tmem_ld16(tl + cO, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo[e & 7]);
+            tmem_st16(tl + cO, o);
+            tmem_st_wait();
+          }
+          send();
+          named_bar(2, 128);
+        }
+        if (tok == 0) mbar_arrive(&bars[bPFull + (tile & 1)]);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) l[h] += pr[h];
+      }
+      // ---- the split's average, a thread a dim
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        if (lane == 0) sums[warp * kHeads + h] = l[h];
+      }
+      named_bar(2, 128);
+      uint32_t o[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = 0u;
+      if (it.tiles > 0) {
+        const uint32_t last = T + it.tiles - 1;
+        mbar_wait(&bars[bPvDone + (last & 1)], (last >> 1) & 1, g);
+        __syncwarp();
+        tc_fence_after();
+        tmem_ld16(tl + cO, o);
+        tc_fence_before();
+      }
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        const float ll = (sums[h] + sums[kHeads + h]) + (sums[2 * kHeads + h] + sums[3 * kHeads + h]);
+        const float f = ll == 0.f ? 0.f : ex2(M[h] - m[h]) * (1.f / kTop);
+        const float y = fmaf(__uint_as_float(o[kHeads + h]), 1.f / 16, __uint_as_float(o[h])) * inverse_sum(ll) * f;
+        if (h < p.group && tok < D) {
+          if (it.n_splits == 1) {
+            p.o[it.b * p.o_batch + (long long)(h0 + h) * p.o_head + tok] = __float2bfloat16_rn(y);
+            if (tok == 0 && p.lse) p.lse[(size_t)it.b * p.Hq + h0 + h] = log_sum(m[h], ll);
+          } else {
+            const size_t at = ((size_t)it.b * p.Hq + h0 + h) * p.max_splits + it.split;
+            p.part_o[at * D + tok] = y;
+            if (tok == 0) p.part_ml[at] = make_float2(m[h], ll);
+          }
+        }
+      }
+      named_bar(2, 128);  // `sums` is free for the next item
+      if (it.tiles > 0) {
+        T += it.tiles;
+        ib ^= 1;
+        if (ib == 0) iph ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+}  // namespace
+
+cudaError_t prepare_decode8_wide() {
+  for (auto kernel : {dash_decode8_wide_kernel<64>, dash_decode8_wide_kernel<128>}) {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e == cudaSuccess && fa.numRegs != kRegsLaunch) e = cudaErrorInvalidConfiguration;  // the register split counts on it
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_decode8_wide(int D, const Decode8Params &p, int num_sms, cudaStream_t stream) {
+  return launch(D == 64 ? dash_decode8_wide_kernel<64> : dash_decode8_wide_kernel<128>, 2 * num_sms, kThreads, kSmem,
+                stream, nullptr, p);
+}
+
+}  // namespace dash

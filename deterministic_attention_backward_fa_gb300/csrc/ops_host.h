@@ -200,6 +200,7 @@ inline dash_status_t decode_params(const void *q, const int32_t *page_table, con
   p.hblocks = (p.group + 15) / 16;
   p.first = first;
   p.parts_before = parts_before;
+  p.least_chunk = kMinChunk;
   p.scale_log2 = scale * kLog2e;
   return DASH_OK;
 }

@@ -168,6 +168,7 @@ struct DecodeParams {
   int hblocks;                // blocks of 16 Q heads in a group
   int first;                  // the tokens before this one are attended elsewhere ...
   int parts_before;           // ... and have left that many parts
+  int least_chunk;            // tokens of the shortest kind of split
   float scale_log2;
   int *status;
 };
@@ -175,13 +176,14 @@ struct DecodeParams {
 // Long ones get longer splits (a split's partial result costs as much as eight
 // cached tokens to write and read) but up to 64 of them, so that one sequence
 // on few heads still spreads.
-__host__ __device__ inline int decode_chunk(int len) {
-  int c = 256;
+constexpr int kMinChunk = 256;
+__host__ __device__ inline int decode_chunk(int len, int least = kMinChunk) {
+  int c = least;
   while ((long long)c * 64 < len || (c < 1024 && c * 16 < len)) c *= 2;
   return c;
 }
-__host__ __device__ inline int decode_splits(int len) {
-  const int c = decode_chunk(len);
+__host__ __device__ inline int decode_splits(int len, int least = kMinChunk) {
+  const int c = decode_chunk(len, least);
   return (int)(((long long)len + c - 1) / c);
 }
 // The most splits that a sequence of up to `cap` tokens can have: a length from

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
   // every block waits, so that this grid never ends before the first one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int h = blockIdx.x, b = blockIdx.y;
-  const int n = p.parts_before + decode_splits(decode_len(p, b));
+  const int n = p.parts_before + decode_splits(decode_len(p, b), p.least_chunk);
   if (n <= 1 && p.parts_before == 0) return;  // written by the first kernel
   const size_t at = ((size_t)b * p.Hq + h) * (p.parts_before + p.max_splits);
   __shared__ float s_w[128];

@@ -1,12 +1,17 @@
 """Plain 64-bit forms of the 8-bit paged cache, with bounds on the decode's errors.
 
-A decode's result is rounded to bf16 (U = 2^-8 of the value).  Inside, Q and the
-codes are exact in f16 (Q's values below 2^-29 of its row's largest are rounded
-to 2^-39 of it, which EPS covers for the standard normal rows of these tests),
-sums and softmax are 32-bit, and the weights 2^(x - m) c are rounded to f16: by
-2^-11 of themselves, and by 2^-25 at least, counted against the largest of them,
-which stands at 2^-8 to 2^8 of 1: 2^-17 of the largest term at most, for each of the n
-terms.  EPS = 2^-13 bounds the 32-bit arithmetic as for the bf16 cache.
+A decode's result is rounded to bf16 (U = 2^-8 of the value).  Inside, the codes
+are exact, sums and softmax are 32-bit, and Q and the weights 2^(x - m) c are
+rounded.  Q: exact in f16 down to 2^-29 of its row's largest value, in two e4m3
+terms down to 2^-14 and off by 2^-22 of the largest below, which EPS covers for
+the standard normal rows of these tests.  Weights: in f16 by 2^-11 of themselves,
+and by 2^-25 at least, counted against the largest of them, which stands at 2^-8
+to 2^8 of 1: 2^-17 of the largest term at most; in two e4m3 terms by 2^-8 = U of
+themselves (each term keeps 4 bits, so half a step is 2^-4 of what is left, twice),
+and by 2^-14 at least (half of 2^-9, under a factor of 16) where the largest
+stands at 16 at least: 2^-18 of it.  So U of each weight and 2^-17 of the largest
+term for each of the n terms.  EPS = 2^-13 bounds the 32-bit arithmetic as for the
+bf16 cache.
 """
 import torch
 
@@ -61,5 +66,5 @@ def decode(q, pages, scales, table, lengths, scale):
 
 def within(name, o, ref, mag, top):
     err = (o.to(F64) - ref).abs()
-    bad = ~(err <= P.U * ref.abs() + (1 + P.U) * ((2.0 ** -11 + P.EPS) * mag + top) + 1e-30)
+    bad = ~(err <= P.U * ref.abs() + (1 + P.U) * ((P.U + P.EPS) * mag + top) + 1e-30)
     assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} outside their bound, worst {err[bad].max()}"

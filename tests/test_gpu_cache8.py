@@ -196,9 +196,17 @@ CASES = [([1], 1, 1, 64, 16), ([0, 5, 0], 4, 2, 128, 16), ([64, 63, 65, 256, 257
          (list(range(0, 900, 7)), 9, 1, 128, 16)]
 
 
+# Room in the table alone decides between the forms for small calls and for those that fill the GPU: a table row of
+# 16384 tokens has room for 64 splits.
+ROOM = 16384
+
+
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("lens,hq,hkv,D,page", CASES, ids=lambda x: str(x)[:40])
-def test_decode(lens, hq, hkv, D, page):
-    c = cache(lens, hkv, D, page, heads_first=hq != 3)
+def test_decode(lens, hq, hkv, D, page, room):
+    if room:  # more sequences, so that there is room for more splits than CTAs
+        lens = (lens * 10)[:max(len(lens), 10)] + [0, 1, 129]
+    c = cache(lens, hkv, D, page, heads_first=hq != 3, width=max(room, max(lens)) // page + 1 if room else None)
     kp, vp, ks, vs, table = c
     # whatever stands behind a sequence's last token is not read into its result
     for b, n in enumerate(lens):
@@ -214,17 +222,18 @@ def test_decode(lens, hq, hkv, D, page):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("spread", [3.0, 20.0])
 @pytest.mark.parametrize("hq,hkv", [(4, 2), (12, 1)])
-def test_decode_of_rows_of_very_different_scales(hq, hkv, spread):
+def test_decode_of_rows_of_very_different_scales(hq, hkv, spread, room):
     # K's scale far down as well, so that scores stay small whatever the rows' scales are; V's as they come
-    lens, D, page = [700, 65, 3000], 128, 16
-    kp, vp, ks, vs, table = cache(lens, hkv, D, page, spread=spread)
+    lens, D, page = [700, 65, 3000, 5, 128, 129], 128, 16
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page, spread=spread, width=room // page or None)
     ks = torch.ones_like(ks) * 2.0 ** -8
     # the largest V rows first, in the middle, and on tokens that hardly count
     c = (kp, vp, ks, vs, table)
     for seed in (1, 2):
-        q = P.normal(seed, 3, hq, D)
+        q = P.normal(seed, 6, hq, D)
         o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
         check(q, c, lens, 1 / math.sqrt(D), o, lse)
     # scales of zero weigh nothing in O and count in the sum; arbitrary (not power of two) scales
@@ -238,11 +247,12 @@ def test_decode_of_rows_of_very_different_scales(hq, hkv, spread):
     assert not o.any() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("gain", [2.0 ** -100, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100])
-def test_decode_of_queries_of_any_magnitude(gain):
-    lens, hq, hkv, D, page = [300, 40], 4, 2, 64, 16
-    kp, vp, ks, vs, table = cache(lens, hkv, D, page)
-    q = (P.normal(3, 2, hq, D).double() * gain).bfloat16()
+def test_decode_of_queries_of_any_magnitude(gain, room):
+    lens, hq, hkv, D, page = [300, 40, 129, 0, 7], 4, 2, 64, 16
+    kp, vp, ks, vs, table = cache(lens, hkv, D, page, width=room // page or None)
+    q = (P.normal(3, 5, hq, D).double() * gain).bfloat16()
     ks = (ks.double() / gain).float()
     o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
     check(q, (kp, vp, ks, vs, table), lens, 1 / math.sqrt(D), o, lse)
@@ -250,15 +260,29 @@ def test_decode_of_queries_of_any_magnitude(gain):
     check(torch.zeros_like(q), (kp, vp, ks, vs, table), lens, 1 / math.sqrt(D), o, lse)
 
 
-def test_decode_does_not_depend_on_the_batch():
+def test_decode_does_not_depend_on_the_other_sequences():
     lens, hq, hkv, D, page = [5000, 130, 20000, 1, 700], 8, 2, 128, 16
     kp, vp, ks, vs, table = cache(lens, hkv, D, page, width=4000)
     q = P.normal(5, 5, hq, D)
-    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
-    for b, n in enumerate(lens):
+    # three of them in a small call, and each alone
+    o, lse = dash.attn_decode_fp8(q[:3], kp, vp, ks, vs, table[:3], i32(lens[:3]))
+    for b, n in enumerate(lens[:3]):
         w = -(-n // page)
         ob, lb = dash.attn_decode_fp8(q[b:b + 1], kp, vp, ks, vs, table[b:b + 1, :w].contiguous(), i32([n]))
         assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0])
+    # all in calls that fill the GPU, in another order, with other neighbours
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    order = torch.tensor([3, 0, 4, 2, 1, 0, 3, 3], device="cuda")
+    oo, ll = dash.attn_decode_fp8(q[order], kp, vp, ks, vs, table[order], i32(lens)[order])
+    assert torch.equal(oo, o[order]) and torch.equal(ll, lse[order])
+    check(q, (kp, vp, ks, vs, table), lens, 1 / math.sqrt(D), o, lse)
+    # more sequences than are sorted by their length
+    many = torch.arange(1500, device="cuda") % 5
+    small = torch.minimum(i32(lens), i32([300, 130, 299, 1, 257]))
+    oo, ll = dash.attn_decode_fp8(q[many], kp, vp, ks, vs, table[many], small[many])
+    o, lse = oo[:5], ll[:5]
+    assert torch.equal(oo, o[many]) and torch.equal(ll, lse[many])
+    check(q, (kp, vp, ks, vs, table), small.tolist(), 1 / math.sqrt(D), o, lse)
 
 
 @pytest.mark.parametrize("hq,hkv,D,page,width", [(16, 4, 128, 16, 44), (8, 1, 64, 16, 64), (20, 1, 128, 7, 90),
@@ -272,16 +296,17 @@ def test_decode_small_calls_and_captures(hq, hkv, D, page, width):
     o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
     dash.dash_sync_status()
     check(q, c, lens, 1 / math.sqrt(D), o, lse)
-    for b, n in enumerate(lens):
-        ob, lb = dash.attn_decode_fp8(q[b:b + 1], kp, vp, ks, vs, table[b:b + 1], i32([n]))
-        assert torch.equal(o[b], ob[0]) and torch.equal(lse[b], lb[0]), n
-    length, graph = i32([1]), torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        og, lg = dash.attn_decode_fp8(q[-1:], kp, vp, ks, vs, table[-1:], length)
-    length.copy_(i32(lens[-1:]))
-    graph.replay()
-    torch.cuda.synchronize()
-    assert torch.equal(og[0], o[-1]) and torch.equal(lg[0], lse[-1])
+    ones = [dash.attn_decode_fp8(q[b:b + 1], kp, vp, ks, vs, table[b:b + 1], i32([n])) for b, n in enumerate(lens)]
+    o1, l1 = (torch.cat(t) for t in zip(*ones))
+    check(q, c, lens, 1 / math.sqrt(D), o1, l1)
+    for rows, want in ((slice(-1, None), (o1, l1)), (slice(None), (o, lse))):
+        length, graph = i32([1] * len(lens))[rows], torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            og, lg = dash.attn_decode_fp8(q[rows], kp, vp, ks, vs, table[rows], length)
+        length.copy_(i32(lens)[rows])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(og, want[0][rows]) and torch.equal(lg, want[1][rows])
     dash.dash_sync_status()
 
 
@@ -316,11 +341,12 @@ def test_decode_strides_streams_and_lengths_out_of_range():
     assert torch.equal(o, want[0])
 
 
-def test_decode_of_bad_pages_nan_and_infinite_scores():
-    lens, hq, hkv, D, page = [70, 40], 4, 2, 128, 16
-    c = cache(lens, hkv, D, page)
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_decode_of_bad_pages_nan_and_infinite_scores(room):
+    lens, hq, hkv, D, page = [70, 40, 300, 128, 700], 4, 2, 128, 16
+    c = cache(lens, hkv, D, page, width=room // page or None)
     kp, vp, ks, vs, table = c
-    q = P.normal(7, 2, hq, D)
+    q = P.normal(7, 5, hq, D)
     for bad in (-1, kp.shape[0], 2**31 - 1):
         t = table.clone()
         t[0, 1] = bad
@@ -339,22 +365,26 @@ def test_decode_of_bad_pages_nan_and_infinite_scores():
         else:
             where[at] = NAN
         o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
-        assert torch.equal(o[1], good[0][1]) and torch.equal(o[0, :2], good[0][0, :2])
+        assert torch.equal(o[1:], good[0][1:]) and torch.equal(o[0, :2], good[0][0, :2])
         if what == "code":
             assert o[0, 2:, 17].isnan().all() and o[0, 2:, 16].isfinite().all()
         else:
             assert o[0, 2:].isnan().all() and (lse[0, 2:].isnan().all() if what == "k" else lse[0, 2:].isfinite().all())
         bits(where).copy_(bits(kept))
-    # queries: NaN and +inf make the row NaN; scores of -inf weigh nothing
-    one = q.clone()
-    one[0, 0, 3] = NAN
-    o, lse = dash.attn_decode_fp8(one, kp, vp, ks, vs, table, i32(lens))
-    assert o[0, 0].isnan().all() and lse[0, 0].isnan() and torch.equal(o[0, 1:], good[0][0, 1:])
-    bits(kp)[:, :, :, 0] = 0x38  # 1.0
-    one = q.clone()
-    one[0, 0, 0], one[0, 1, 0] = INF, -INF
-    o, lse = dash.attn_decode_fp8(one, kp, vp, ks, vs, table, i32(lens))
-    assert o[0, 0].isnan().all() and not o[0, 1].any() and lse[0, 1] == -INF
+    # a query with a NaN or an infinity makes its row NaN
+    for bad in (NAN, INF, -INF):
+        one = q.clone()
+        one[0, 1, 3], one[4, 2, 100] = bad, bad
+        o, lse = dash.attn_decode_fp8(one, kp, vp, ks, vs, table, i32(lens))
+        for b, h in ((0, 1), (4, 2)):
+            assert o[b, h].isnan().all() and lse[b, h].isnan()
+            o[b, h], lse[b, h] = good[0][b, h], good[1][b, h]
+        assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+    # rows far below the others, and a first tile that weighs next to nothing
+    ks[table[4, :16].long()] *= 2.0 ** -20
+    ks[table[4, 16:44].long()] *= 4.0
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
     dash.dash_sync_status()
 
 
