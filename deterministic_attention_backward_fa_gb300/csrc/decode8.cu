@@ -44,7 +44,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kFetch = 4;  // warps that fetch, 32 rows each
 constexpr int kMma = 8;    // the warp that issues; 9-11 make the warpgroup whole
-constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsFetch = 64, kRegsMma = 48;
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsFetch = 72, kRegsMma = 40;
 static_assert(kRegsSoftmax + kRegsFetch + kRegsMma <= 3 * kRegsLaunch, "register split exceeds the CTA's allocation");
 constexpr int kHeads = 8, kTerms = 2, kCols = kTerms * kHeads;
 constexpr int kTile8 = 128;        // tokens
@@ -61,9 +61,10 @@ constexpr uint32_t oP = oQ + 2 * kColBytes;            // twice
 constexpr uint32_t oScale = oP + 2 * kColBytes;        // [kSlots][2][128]
 constexpr uint32_t oMask = oScale + kSlots * 2 * kTile8 * 4;  // [kSlots][4]
 constexpr uint32_t oSc = oMask + kSlots * 16;          // [2][8] a score's factor
-constexpr uint32_t oRed = oSc + 2 * kHeads * 4;        // [4][16], then a mask of heads [4]
-constexpr uint32_t oSum = oRed + 4 * 16 * 4 + 16;           // [4][8]
-constexpr uint32_t oBar = oSum + 4 * kHeads * 4;
+constexpr uint32_t oItem = oSc + 2 * kHeads * 4;       // [2] what the item is
+constexpr uint32_t oRed = oItem + 2 * 32;              // [16][4] maxima of the warps, then masks of heads [4]
+constexpr uint32_t oSum = oRed + 4 * 16 * 4 + 16;      // [8][4] sums of the warps, then [8] factors
+constexpr uint32_t oBar = oSum + 5 * kHeads * 4;
 enum {
   bSFull = 0, bPFull = 2, bPvDone = 4, bQFull = 6, bQEmpty = 8, bTile = 10, bKvFull = bTile + kSlots,
   bKvEmpty = bKvFull + kStages, bFinal = bKvEmpty + kStages, kBars
@@ -107,11 +108,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float warp_max(float x) {  // NaN counts as -inf
-  int i = x == x ? __float_as_int(x) : (int)0xff800000;
-  i ^= (i >> 31) & 0x7fffffff;
-  i = __reduce_max_sync(0xffffffffu, i);
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+// Reduces N values (a power of two up to 32) over the lanes of a warp, all at
+// once: each exchange halves the values that a lane keeps.  The lane ends with
+// value number lane / (32 / N); lanes of the same number hold the same.
+template <int N, class Op>
+__device__ __forceinline__ float reduce_all(float (&v)[N], int lane, Op op) {
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
+    const bool high = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = high ? v[i] : v[n + i], keep = high ? v[n + i] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  for (; o > 0; o /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
 }
 
 // The terms of two values, as codes: term k in bytes {a, b} of t[k].
@@ -176,17 +189,24 @@ struct Walk {
   }
 };
 
-// Tiles and place of an item.
-struct Part {
-  int b, hk, split, n_splits, begin, end, tiles;
-  __device__ __forceinline__ Part(const DecodeParams &p, const Walk &w, int head) : b(w.b), hk(head), split(w.split) {
-    const int len = decode_len(p, b), chunk = decode_chunk(len, p.least_chunk);
-    n_splits = max(1, decode_splits(len, p.least_chunk));
-    begin = split * chunk;
-    end = min(len, begin + chunk);
-    tiles = (end - begin + kTile8 - 1) / kTile8;  // 0: an empty sequence
-  }
+// An item, as the fetching warps tell it to the others with its Q.
+struct Item {
+  int b, hk, split, n_splits, begin, end;
+  int tiles;  // -1: there is none behind the last
+  int pad;
 };
+static_assert(sizeof(Item) == 32, "a place in shared memory");
+__device__ __forceinline__ Item item_of(const DecodeParams &p, const Walk &w, int head) {
+  Item it;
+  it.b = w.b, it.hk = head, it.split = w.split;
+  const int len = decode_len(p, it.b), chunk = decode_chunk(len, p.least_chunk);
+  it.n_splits = max(1, decode_splits(len, p.least_chunk));
+  it.begin = it.split * chunk;
+  it.end = min(len, it.begin + chunk);
+  it.tiles = (it.end - it.begin + kTile8 - 1) / kTile8;  // 0: an empty sequence
+  it.pad = 0;
+  return it;
+}
 
 template <int N>
 struct Ring {
@@ -212,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
   float *scales = reinterpret_cast<float *>(smem + oScale);
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + oMask);
   float *factors = reinterpret_cast<float *>(smem + oSc);
+  Item *items = reinterpret_cast<Item *>(smem + oItem);
   if ((smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
     return;
@@ -242,8 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, p.status, (uint64_t)p.spin_limit_ns};
-  Walk walk(p);
-  int ib = 0;            // the item's place of Q
+  int ib = 0;            // the item's place, and its Q's
   uint32_t iph = 0;      // and its phase
   uint32_t T = 0;        // tiles before this item
 
@@ -253,26 +273,83 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
     const int w = warp - 4, row = w * 32 + lane;
     constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;  // 16-byte pieces of a row, rows of a warp's copy
     const int c = lane % kChunks, rsub = lane / kChunks;
+    constexpr int kLanes = D / 8;  // of a head of Q
+    const int head = row / kLanes, dim = lane % kLanes * 8;
     Ring<kStages> r;
-    for (long long item = blockIdx.x;; item += gridDim.x) {
-      const long long want = item / p.Hkv;
-      if (!walk.find(p, want, lane)) break;
-      const Part it(p, walk, (int)(item - want * p.Hkv));
-      if (it.tiles == 0) continue;
-      // Q: a head is D / 8 lanes
-      constexpr int kLanes = D / 8;
-      const int head = row / kLanes, dim = lane % kLanes * 8;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    Walk walk(p);
+    long long number = blockIdx.x;
+    // The next item that has tokens, with what its start waits for: its Q and the pages of its first two tiles.
+    // Empty sequences are answered on the way.
+    struct Next {
+      Item it;
+      uint4 q;
+      int page[2];
+    } next;
+    auto page_of = [&](const Item &it, int j) -> int {
+      const int t = it.begin + j * kTile8 + row;
+      return t < it.end ? p.table[it.b * p.table_row + quotient(p.page, t)] : -1;
+    };
+    auto look_up = [&]() {
+      for (;; number += gridDim.x) {
+        const long long want = number / p.Hkv;
+        next.it.tiles = -1;
+        if (!walk.find(p, want, lane)) return;
+        next.it = item_of(p, walk, (int)(number - want * p.Hkv));
+        if (next.it.tiles > 0) break;
+        for (int h = 0; h < p.group; ++h) {
+          const int hh = next.it.hk * p.group + h;
+          if (row < D) p.o[next.it.b * p.o_batch + hh * p.o_head + row] = __float2bfloat16_rn(0.f);
+          if (row == 0 && p.lse) p.lse[(size_t)next.it.b * p.Hq + hh] = -INFINITY;
+        }
+      }
+      number += gridDim.x;
+      next.q = make_uint4(0u, 0u, 0u, 0u);
       if (head < p.group)
-        raw = *reinterpret_cast<const uint4 *>(p.q + it.b * p.q_batch + (long long)(it.hk * p.group + head) * p.q_head +
-                                               dim);
-      const int *table = p.table + it.b * p.table_row;
+        next.q = *reinterpret_cast<const uint4 *>(p.q + next.it.b * p.q_batch +
+                                                  (long long)(next.it.hk * p.group + head) * p.q_head + dim);
+      next.page[0] = page_of(next.it, 0);
+      next.page[1] = page_of(next.it, 1);
+    };
+    look_up();
+    while (true) {
+      const Item it = next.it;
+      // Q's largest value is put at 2^7 to 2^8; a head with a NaN or an infinity is all NaN
+      mbar_wait(&bars[bQEmpty + ib], iph ^ 1, g);
+      __syncwarp();
+      if (it.tiles > 0) {
+        const uint32_t x[4] = {next.q.x, next.q.y, next.q.z, next.q.w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int f = min(253, 261 - (int)(top >> 7));
+        const float up = top < 0x7f80u ? pow2_field(f) : NAN;
+        uint32_t codes[kTerms][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t t2[kTerms];
+          terms_of(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up, t2);
+#pragma unroll
+          for (int n = 0; n < kTerms; ++n) codes[n][i >> 1] = i & 1 ? codes[n][i >> 1] | t2[n] << 16 : t2[n];
+        }
+        if (head < kHeads) {
+#pragma unroll
+          for (int i = 0; i < kTerms; ++i) {
+            const int n = i * kHeads + head;
+            *reinterpret_cast<uint2 *>(smem + oQ + ib * kColBytes + n * 128 + (((dim >> 4) ^ (n & 7)) << 4) +
+                                       (dim & 15)) = make_uint2(codes[i][0], codes[i][1]);
+          }
+          if (dim == 0) factors[ib * kHeads + head] = p.scale_log2 * pow2_field(254 - f);
+        }
+        fence_proxy_async_smem();
+      }
+      if (row == 0) items[ib] = it;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bQFull + ib]);
+      if (it.tiles < 0) break;
       const uint8_t *kbase = p.c.k + it.hk * p.c.ks.head + 16 * c, *vbase = p.c.v + it.hk * p.c.vs.head + 16 * c;
       const float *ksbase = p.c.k_scale + it.hk * p.c.kss.head, *vsbase = p.c.v_scale + it.hk * p.c.vss.head;
-      auto page_of = [&](int j) -> int {
-        const int t = it.begin + j * kTile8 + row;
-        return t < it.end ? table[quotient(p.page, t)] : -1;
-      };
       // The rows of a tile of K (with the scales of both) or V, where the page and place of the lane's token are known.
       struct Where {
         int page, off;
@@ -327,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
       };
       // V of a tile follows K of the next one; pages are looked up two tiles ahead of K
       Where k, v = {};
-      int page = page_of(0), next = page_of(1);
+      int page = next.page[0], after = next.page[1];
       for (int j = 0; j <= it.tiles; ++j) {
         if (j < it.tiles) {
           const int t = it.begin + j * kTile8 + row;
@@ -336,42 +413,10 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
           if (t < it.end && !ok) atomicCAS(p.status, 0, kStatusBadPage);
           k.off = t - quotient(p.page, t) * p.page_size;
           k.valid = __ballot_sync(0xffffffffu, ok);
-          page = next;
-          next = page_of(j + 2);
+          page = after;
+          after = page_of(it, j + 2);
           fetch(false, T + j, k);
-          if (j == 0) {
-            // Q's largest value is put at 2^7 to 2^8; a head with a NaN or an infinity is all NaN
-            mbar_wait(&bars[bQEmpty + ib], iph ^ 1, g);
-            __syncwarp();
-            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int f = min(253, 261 - (int)(top >> 7));
-            const float up = top < 0x7f80u ? pow2_field(f) : NAN;
-            uint32_t codes[kTerms][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t t2[kTerms];
-              terms_of(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up, t2);
-#pragma unroll
-              for (int n = 0; n < kTerms; ++n) codes[n][i >> 1] = i & 1 ? codes[n][i >> 1] | t2[n] << 16 : t2[n];
-            }
-            if (head < kHeads) {
-#pragma unroll
-              for (int i = 0; i < kTerms; ++i) {
-                const int n = i * kHeads + head;
-                *reinterpret_cast<uint2 *>(smem + oQ + ib * kColBytes + n * 128 + (((dim >> 4) ^ (n & 7)) << 4) +
-                                           (dim & 15)) = make_uint2(codes[i][0], codes[i][1]);
-              }
-              if (dim == 0) factors[ib * kHeads + head] = p.scale_log2 * pow2_field(254 - f);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[bQFull + ib]);
-          }
+          if (j == 0) look_up();
         }
         if (j > 0) fetch(true, 0, v);
         v = k;
@@ -393,11 +438,11 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
     auto wait = [&](uint64_t *bar, uint32_t ph) {
       if (!mbar_wait(bar, ph, g)) lead = 0;
     };
-    for (long long item = blockIdx.x;; item += gridDim.x) {
-      const long long want = item / p.Hkv;
-      if (!walk.find(p, want, lane)) break;
-      const Part it(p, walk, (int)(item - want * p.Hkv));
-      if (it.tiles == 0) continue;
+    while (true) {
+      wait(&bars[bQFull + ib], iph);
+      const int tiles = items[ib].tiles;
+      if (tiles < 0 || warp_aborted(g)) break;
+      __syncwarp();
       auto issue_s = [&](uint32_t tile) {
         wait(&bars[bKvFull + r.st], r.ph);
         fence_proxy_async_smem();
@@ -409,15 +454,14 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
         tc_commit_if(lead, &bars[bKvEmpty + r.st]);
         r.next();
       };
-      wait(&bars[bQFull + ib], iph);
       issue_s(T);
-      if (it.tiles == 1) tc_commit_if(lead, &bars[bQEmpty + ib]);
-      for (int j = 0; j < it.tiles; ++j) {
+      if (tiles == 1) tc_commit_if(lead, &bars[bQEmpty + ib]);
+      for (int j = 0; j < tiles; ++j) {
         const uint32_t tile = T + j;
         // its place of S was read before the weights of the tile before this one came
-        if (j + 1 < it.tiles) {
+        if (j + 1 < tiles) {
           issue_s(tile + 1);
-          if (j + 2 == it.tiles) tc_commit_if(lead, &bars[bQEmpty + ib]);
+          if (j + 2 == tiles) tc_commit_if(lead, &bars[bQEmpty + ib]);
         }
         wait(&bars[bKvFull + r.st], r.ph);
         fence_proxy_async_smem();
@@ -431,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
         tc_commit_if(lead, &bars[bKvEmpty + r.st]);
         r.next();
       }
-      T += it.tiles;
+      T += tiles;
       ib ^= 1;
       if (ib == 0) iph ^= 1;
     }
@@ -445,26 +489,20 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
     const int tok = threadIdx.x;
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
     float *red = reinterpret_cast<float *>(smem + oRed), *sums = reinterpret_cast<float *>(smem + oSum);
-    for (long long item = blockIdx.x;; item += gridDim.x) {
-      const long long want = item / p.Hkv;
-      if (!walk.find(p, want, lane)) break;
-      const Part it(p, walk, (int)(item - want * p.Hkv));
-      const int h0 = it.hk * p.group;
+    while (true) {
+      mbar_wait(&bars[bQFull + ib], iph, g);
+      const Item it = items[ib];
+      if (any_of_128(it.tiles < 0 || *g.abort)) break;  // one answer, as barriers follow
       float sc[kHeads], m[kHeads], M[kHeads], up[kHeads], l[kHeads];
 #pragma unroll
       for (int h = 0; h < kHeads; ++h) {
-        sc[h] = 0.f;
+        sc[h] = factors[ib * kHeads + h];
         m[h] = M[h] = -INFINITY;
         up[h] = NAN;
         l[h] = 0.f;
       }
-      if (it.tiles > 0) {
-        mbar_wait(&bars[bQFull + ib], iph, g);
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) sc[h] = factors[ib * kHeads + h];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[bQEmpty + ib]);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bQEmpty + ib]);
       // After an abort the loop runs on with whatever tensor memory holds: no
       // wait blocks any more, and the status word tells that O is not valid.
       for (int j = 0; j < it.tiles; ++j) {
@@ -510,19 +548,19 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
           // only the heads that need it move, so that a head's bits do not depend on the others
           const float lv = lg2(vs);
           uint32_t over = 0;
+          float both[2 * kHeads];  // x and x + log2 c
 #pragma unroll
           for (int h = 0; h < kHeads; ++h) {
             const float x = valid ? __uint_as_float(s[h]) * sc[h] : -INFINITY;
-            const float a = warp_max(x), b = warp_max(x + lv);
             s[h] = __float_as_uint(x);
+            both[h] = x;
+            both[kHeads + h] = x + lv;
             over |= (pr[h] <= kMost && pv[h] <= kMost ? 0u : 1u) << h;
-            if (lane == 0) {
-              red[warp * 16 + h] = a;
-              red[warp * 16 + 8 + h] = b;
-            }
           }
+          const float top = reduce_all(both, lane, [](float a, float b) { return fmaxf(a, b); });
           over = __reduce_or_sync(0xffffffffu, over);
           uint32_t *all_over = reinterpret_cast<uint32_t *>(red + 64);
+          red[(lane >> 1) * 4 + warp] = top;
           if (lane == 0) all_over[warp] = over;
           named_bar(2, 128);
           over = (all_over[0] | all_over[1]) | (all_over[2] | all_over[3]);
@@ -536,12 +574,9 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
           for (int h = 0; h < kHeads; ++h) {
             fo[h] = 1.f;
             if (!((over >> h) & 1u)) continue;
-            float m1 = m[h], M1 = M[h];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              m1 = fmaxf(m1, red[w * 16 + h]);
-              M1 = fmaxf(M1, red[w * 16 + 8 + h]);
-            }
+            const float4 a = reinterpret_cast<const float4 *>(red)[h], b = reinterpret_cast<const float4 *>(red)[kHeads + h];
+            const float m1 = fmaxf(m[h], fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+            const float M1 = fmaxf(M[h], fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
             const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
             l[h] *= ex2(m[h] - mr);
             fo[h] = ex2(M[h] - Mr);
@@ -569,46 +604,47 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
         for (int h = 0; h < kHeads; ++h) l[h] += pr[h];
       }
       // ---- the split's average, a thread a dim
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-        if (lane == 0) sums[warp * kHeads + h] = l[h];
-      }
+      const float mine = reduce_all(l, lane, [](float a, float b) { return a + b; });
+      sums[(lane >> 2) * 4 + warp] = mine;
       named_bar(2, 128);
+      float *averages = sums + 4 * kHeads;
+      const int h0 = it.hk * p.group, parts = p.max_splits;
+      const size_t first = ((size_t)it.b * p.Hq + h0) * parts + it.split;
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (tok == h) {
+          const float4 w = reinterpret_cast<const float4 *>(sums)[h];
+          const float ll = (w.x + w.y) + (w.z + w.w);
+          averages[h] = ll == 0.f ? 0.f : ex2(M[h] - m[h]) * (1.f / kTop) * inverse_sum(ll);
+          if (h < p.group) {
+            if (it.n_splits > 1) p.part_ml[first + (size_t)h * parts] = make_float2(m[h], ll);
+            else if (p.lse) p.lse[(size_t)it.b * p.Hq + h0 + h] = log_sum(m[h], ll);
+          }
+        }
+      const uint32_t last = T + it.tiles - 1;
+      mbar_wait(&bars[bPvDone + (last & 1)], (last >> 1) & 1, g);
+      __syncwarp();
+      tc_fence_after();
       uint32_t o[16];
+      tmem_ld16(tl + cO, o);
+      tc_fence_before();
+      named_bar(2, 128);
+      if (tok < D) {
+        float *part = p.part_o + first * D + tok;
+        __nv_bfloat16 *out = p.o + it.b * p.o_batch + h0 * p.o_head + tok;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = 0u;
-      if (it.tiles > 0) {
-        const uint32_t last = T + it.tiles - 1;
-        mbar_wait(&bars[bPvDone + (last & 1)], (last >> 1) & 1, g);
-        __syncwarp();
-        tc_fence_after();
-        tmem_ld16(tl + cO, o);
-        tc_fence_before();
-      }
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-        const float ll = (sums[h] + sums[kHeads + h]) + (sums[2 * kHeads + h] + sums[3 * kHeads + h]);
-        const float f = ll == 0.f ? 0.f : ex2(M[h] - m[h]) * (1.f / kTop);
-        const float y = fmaf(__uint_as_float(o[kHeads + h]), 1.f / 16, __uint_as_float(o[h])) * inverse_sum(ll) * f;
-        if (h < p.group && tok < D) {
-          if (it.n_splits == 1) {
-            p.o[it.b * p.o_batch + (long long)(h0 + h) * p.o_head + tok] = __float2bfloat16_rn(y);
-            if (tok == 0 && p.lse) p.lse[(size_t)it.b * p.Hq + h0 + h] = log_sum(m[h], ll);
-          } else {
-            const size_t at = ((size_t)it.b * p.Hq + h0 + h) * p.max_splits + it.split;
-            p.part_o[at * D + tok] = y;
-            if (tok == 0) p.part_ml[at] = make_float2(m[h], ll);
+        for (int h = 0; h < kHeads; ++h) {
+          const float y = fmaf(__uint_as_float(o[kHeads + h]), 1.f / 16, __uint_as_float(o[h])) * averages[h];
+          if (h < p.group) {
+            if (it.n_splits > 1) part[(size_t)h * parts * D] = y;
+            else out[h * p.o_head] = __float2bfloat16_rn(y);
           }
         }
       }
       named_bar(2, 128);  // `sums` is free for the next item
-      if (it.tiles > 0) {
-        T += it.tiles;
-        ib ^= 1;
-        if (ib == 0) iph ^= 1;
-      }
+      T += it.tiles;
+      ib ^= 1;
+      if (ib == 0) iph ^= 1;
     }
   }
   __syncwarp();
