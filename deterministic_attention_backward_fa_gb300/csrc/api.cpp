@@ -659,6 +659,22 @@ dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long 
                               long long head_stride, int box_rows) {
   return make_rows_map(m, base, heads, rows, D, row_stride, head_stride, box_rows);
 }
+// The map of 8-bit pages [n_pages][page_size][heads][D] with strides in bytes;
+// boxes of `box` tokens of a page and head.  False where the driver takes no such map.
+bool encode_pages8_map(CUtensorMap *m, const void *base, int n_pages, int page_size, int heads, int D, long long page,
+                       long long token, long long head, int box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || page >= (1LL << 40) || token >= (1LL << 40) || head >= (1LL << 40)) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)page_size, (cuuint64_t)n_pages};
+  // a stride along an extent of one is never used
+  cuuint64_t strides[3] = {(cuuint64_t)(heads > 1 ? head : D), (cuuint64_t)(page_size > 1 ? token : D),
+                           (cuuint64_t)(n_pages > 1 ? page : D)};
+  cuuint32_t boxes[4] = {(cuuint32_t)D, 1, (cuuint32_t)box, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace dash
 
 extern "C" {

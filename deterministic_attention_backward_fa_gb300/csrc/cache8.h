@@ -58,6 +58,8 @@ cudaError_t prepare_cache8();
 // The form for calls that fill the GPU with groups of up to 8 heads (decode8.cu), but for the join.
 cudaError_t prepare_decode8_wide();
 cudaError_t launch_decode8_wide(int D, const Decode8Params &p, int num_sms, cudaStream_t stream);
+bool encode_pages8_map(CUtensorMap *m, const void *base, int n_pages, int page_size, int heads, int D, long long page,
+                       long long token, long long head, int box);  // api.cpp
 cudaError_t launch_decode8(int D, const Decode8Params &p, int num_sms, cudaStream_t stream);
 
 }  // namespace dash

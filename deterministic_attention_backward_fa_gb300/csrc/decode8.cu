@@ -23,10 +23,11 @@
 //
 // A persistent CTA, two on an SM, walks its items (longest splits first) without
 // a break in its loads.  Warps: 0-3 softmax (a thread owns a token, and in the
-// end a dim), 4-7 fetch (a token's row lies wherever its page does: 16-byte
-// asynchronous copies into the swizzled layout, whose ends arrive on barriers by
-// themselves) and split Q, 8 issues the MMAs, the next tile's scores before this
-// tile's O.  Tensor memory: S twice at 0 and 16, O at 32.
+// end a dim), 4-7 fetch and split Q, 8 issues the MMAs, the next tile's scores
+// before this tile's O.  A token's row lies wherever its page does.  Where a tile's
+// tokens all count, TMA takes the tokens of a page at once (D = 128, pages of a
+// multiple of 8 tokens); other rows come by 16-byte asynchronous copies, which can
+// leave zeros for a token that does not count.  Tensor memory: S twice at 0 and 16, O at 32.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -70,7 +71,9 @@ enum {
   bKvEmpty = bKvFull + kStages, bFinal = bKvEmpty + kStages, kBars
 };
 constexpr uint32_t oMisc = oBar + kBars * 8;
-constexpr uint32_t kSmem = oMisc + 16;
+constexpr int kSorted = 1024;  // sequences whose lengths are held
+constexpr uint32_t oLens = oMisc + 16;
+constexpr uint32_t kSmem = oLens + 4 * kSorted;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
 constexpr uint32_t cS = 0, cO = 2 * kCols, kTmem = 64;
 
@@ -141,26 +144,37 @@ __device__ __forceinline__ void terms_of(float a, float b, uint32_t (&t)[kTerms]
   }
 }
 
-// Items of a CTA: (split, K/V head) numbers item, item + grid, ...; splits are
-// numbered by sequence, those of the longest kind first (of up to kSorted
-// sequences).  A warp scans 32 sequences at a time and remembers how far it got.
-constexpr int kSorted = 1024;
+// Items of a CTA: (split, K/V head) numbers item, item + grid, ..., numbered by
+// their size, so that what a CTA is dealt last is small: splits of more than
+// kind / 2 and up to `kind` tokens, sequence by sequence, for each power of two
+// down to a tile (of up to kSorted sequences; of more, all in one walk).  A warp
+// scans 32 sequences at a time and remembers how far it got.
 struct Walk {
   long long base = 0;  // splits before the block of sequences b0
-  int b0 = 0, chunk, at = -1;
-  int n = 0, upto = 0, total = 0;  // of the lane's sequence, up to it, of the block
-  int b, split;
+  int b0 = 0, kind, at = -1;
+  int n = 0, upto = 0, total = 0, whole = 0, full = 0;  // of the lane's sequence: splits of the kind, those up to it, of
+                                                        // the block; whole splits of the kind, and of any
+  int len_of = 0;      // the lane's sequence's tokens
+  const int *lens;     // up to kSorted sequences' tokens in shared memory
+  int b, split, len;   // found: the sequence, its split, its tokens
 
-  __device__ __forceinline__ explicit Walk(const DecodeParams &p)
-      : chunk(p.B <= kSorted ? decode_chunk(p.max_pages * p.page_size, p.least_chunk) : 0) {}
+  __device__ __forceinline__ Walk(const DecodeParams &p, const int *lens)
+      : kind(p.B <= kSorted ? decode_chunk(p.max_pages * p.page_size, p.least_chunk) : 0), lens(lens) {}
   // All lanes of a warp ask together.
   __device__ __forceinline__ bool find(const DecodeParams &p, long long want, int lane) {
     while (true) {
       if (at != b0) {
-        const int mine = b0 + lane, len = mine < p.B ? decode_len(p, mine) : 0;
-        n = mine < p.B && (chunk == 0 || decode_chunk(len, p.least_chunk) == chunk)
-                ? max(1, decode_splits(len, p.least_chunk))
-                : 0;
+        const int mine = b0 + lane;
+        n = whole = full = 0;
+        if (mine < p.B) {
+          len_of = kind == 0 ? decode_len(p, mine) : lens[mine];
+          const int chunk = decode_chunk(len_of, p.least_chunk);
+          full = len_of >> (31 - __clz(chunk));
+          const int rest = len_of & (chunk - 1);
+          whole = kind == 0 || kind == chunk ? full : 0;
+          // the rest, or the one item of an empty sequence
+          n = whole + ((rest > 0 || len_of == 0) && (kind == 0 || (rest <= kind && (rest > kind / 2 || kind <= kTile8))));
+        }
         upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -174,7 +188,9 @@ struct Walk {
         const int off = (int)(want - base);
         const int src = __popc(__ballot_sync(0xffffffffu, upto <= off));
         b = b0 + src;
-        split = off - __shfl_sync(0xffffffffu, upto - n, src);
+        const int i = off - __shfl_sync(0xffffffffu, upto - n, src);
+        split = i < __shfl_sync(0xffffffffu, whole, src) ? i : __shfl_sync(0xffffffffu, full, src);
+        len = __shfl_sync(0xffffffffu, len_of, src);
         return true;
       }
       base += total;
@@ -182,8 +198,8 @@ struct Walk {
       at = -1;
       if (b0 >= p.B) {
         b0 = 0;
-        if (chunk <= p.least_chunk) return false;  // nothing shorter, or all in one walk
-        chunk >>= 1;
+        if (kind <= kTile8) return false;  // nothing shorter, or all in one walk
+        kind >>= 1;
       }
     }
   }
@@ -199,10 +215,10 @@ static_assert(sizeof(Item) == 32, "a place in shared memory");
 __device__ __forceinline__ Item item_of(const DecodeParams &p, const Walk &w, int head) {
   Item it;
   it.b = w.b, it.hk = head, it.split = w.split;
-  const int len = decode_len(p, it.b), chunk = decode_chunk(len, p.least_chunk);
-  it.n_splits = max(1, decode_splits(len, p.least_chunk));
+  const int chunk = decode_chunk(w.len, p.least_chunk);
+  it.n_splits = max(1, decode_splits(w.len, p.least_chunk));
   it.begin = it.split * chunk;
-  it.end = min(len, it.begin + chunk);
+  it.end = min(w.len, it.begin + chunk);
   it.tiles = (it.end - it.begin + kTile8 - 1) / kTile8;  // 0: an empty sequence
   it.pad = 0;
   return it;
@@ -221,7 +237,9 @@ struct Ring {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __grid_constant__ Decode8Params p) {
+__global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
+    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Decode8Params p,
+    int box) {  // tokens that TMA takes at once; 0: none
   extern __shared__ __align__(1024) uint8_t smem[];
   // the join may be set up now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -254,6 +272,9 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
     *abort_flag = 0;
     fence_mbar_init();
   }
+  int *lens = reinterpret_cast<int *>(smem + oLens);
+  if (p.B <= kSorted)
+    for (int b = threadIdx.x; b < p.B; b += kThreads) lens[b] = decode_len(p, b);
   if (warp == kMma) {
     tmem_alloc(tmem_slot, kTmem);
     tmem_relinquish();
@@ -276,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
     constexpr int kLanes = D / 8;  // of a head of Q
     const int head = row / kLanes, dim = lane % kLanes * 8;
     Ring<kStages> r;
-    Walk walk(p);
+    uint32_t loads = 0;
+    Walk walk(p, lens);
     long long number = blockIdx.x;
     // The next item that has tokens, with what its start waits for: its Q and the pages of its first two tiles.
     // Empty sequences are answered on the way.
@@ -354,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
       struct Where {
         int page, off;
         uint32_t valid;
+        bool whole;  // the tile has 128 tokens
       };
       auto fetch = [&](bool is_v, uint32_t tile, const Where &at) {
         mbar_wait(&bars[bKvEmpty + r.st], r.ph ^ 1, g);
@@ -362,8 +385,18 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
         const uint32_t slot = tile % kSlots;
         const uint32_t dst = smem_u32(smem + oKV + r.st * kStageBytes) + (w * 32 + rsub) * 128;
         const uint8_t *base = is_v ? vbase : kbase;
+        bool by_copies = true;
         if (!warp_aborted(g)) {
-          if (at.valid == 0xffffffffu && p.whole) {
+          if (D == 128 && box > 0 && at.whole && at.valid == 0xffffffffu) {
+            by_copies = false;
+            uint64_t *bar = &bars[bKvFull + r.st];
+            if ((row & (box - 1)) == 0) {
+              mbar_arrive_expect_tx(bar, box * 128);
+              tma_load_4d(smem + oKV + r.st * kStageBytes + row * 128, is_v ? &tmV : &tmK, bar, 0, it.hk, at.off, at.page);
+            } else {
+              mbar_arrive(bar);
+            }
+          } else if (at.valid == 0xffffffffu && p.whole) {
             const long long step = kRowsPer * st.token;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {  // 16 tokens lie in one page
@@ -399,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
           }
           cp_arrive(&bars[bTile + slot]);
         }
-        cp_arrive(&bars[bKvFull + r.st]);
+        if (by_copies) cp_arrive(&bars[bKvFull + r.st]);
+        ++loads;
         r.next();
       };
       // V of a tile follows K of the next one; pages are looked up two tiles ahead of K
@@ -409,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
         if (j < it.tiles) {
           const int t = it.begin + j * kTile8 + row;
           k.page = page;
+          k.whole = it.begin + (j + 1) * kTile8 <= it.end;
           const bool ok = page >= 0 && page < p.n_pages;
           if (t < it.end && !ok) atomicCAS(p.status, 0, kStatusBadPage);
           k.off = t - quotient(p.page, t) * p.page_size;
@@ -426,6 +461,11 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(const __
       if (ib == 0) iph ^= 1;
     }
     cp_wait_all();
+    // what TMA still has in flight lands before the CTA exits
+    for (int s = 0; s < kStages; ++s) {
+      const uint32_t f = loads / kStages + ((uint32_t)s < loads % kStages ? 1u : 0u);
+      if (f) mbar_drain(&bars[bKvFull + s], (f - 1) & 1, g.limit_ns);
+    }
   } else if (warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kMma) {
@@ -670,8 +710,16 @@ cudaError_t prepare_decode8_wide() {
 }
 
 cudaError_t launch_decode8_wide(int D, const Decode8Params &p, int num_sms, cudaStream_t stream) {
+  CUtensorMap k = {}, v = {};
+  // tokens of a page that are a part of a tile
+  int box = 128;
+  while (p.page_size % box) box /= 2;
+  if (D != 128 || box < 8 ||
+      !encode_pages8_map(&k, p.c.k, p.n_pages, p.page_size, p.Hkv, D, p.c.ks.page, p.c.ks.token, p.c.ks.head, box) ||
+      !encode_pages8_map(&v, p.c.v, p.n_pages, p.page_size, p.Hkv, D, p.c.vs.page, p.c.vs.token, p.c.vs.head, box))
+    box = 0;
   return launch(D == 64 ? dash_decode8_wide_kernel<64> : dash_decode8_wide_kernel<128>, 2 * num_sms, kThreads, kSmem,
-                stream, nullptr, p);
+                stream, nullptr, k, v, p, box);
 }
 
 }  // namespace dash

@@ -178,13 +178,26 @@ struct DecodeParams {
 // on few heads still spreads.
 constexpr int kMinChunk = 256;
 __host__ __device__ inline int decode_chunk(int len, int least = kMinChunk) {
-  int c = least;
-  while ((long long)c * 64 < len || (c < 1024 && c * 16 < len)) c *= 2;
-  return c;
+  // the smallest power of two with at most 64 splits, and with at most 16 if they are shorter than 1024
+  const int of64 = (int)(((unsigned)len + 63) / 64), of16 = (int)(((unsigned)len + 15) / 16);
+  int c = of16 < 1024 ? of16 : 1024;
+  c = c > of64 ? c : of64;
+  c = c > least ? c : least;
+#ifdef __CUDA_ARCH__
+  return 1 << (32 - __clz(c - 1));
+#else
+  int p = least;
+  while (p < c) p *= 2;
+  return p;
+#endif
 }
 __host__ __device__ inline int decode_splits(int len, int least = kMinChunk) {
   const int c = decode_chunk(len, least);
+#ifdef __CUDA_ARCH__
+  return (int)(((unsigned)len + c - 1) >> (31 - __clz(c)));
+#else
   return (int)(((long long)len + c - 1) / c);
+#endif
 }
 // The most splits that a sequence of up to `cap` tokens can have: a length from
 // which splits get longer has more of them than the ones just above it, and

@@ -222,6 +222,28 @@ def test_decode(lens, hq, hkv, D, page, room):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("page", [1, 8, 12, 24, 32, 48, 64, 128, 200, 256])
+def test_decode_of_whole_tiles_in_pages_of_every_kind(page):
+    # rows are fetched a page's part of a tile at a time where it has one, row by row elsewhere; one bad page
+    lens, hq, hkv, D = [128, 1024, 1023, 640, 2500, 0, 127, 256, 1, 3000], 16, 2, 128
+    kp, vp, ks, vs, table = c = cache(lens, hkv, D, page, width=max(ROOM, 3000) // page + 1)
+    q = P.normal(9, len(lens), hq, D)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    dash.dash_sync_status()
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
+    # heads first, K and V side by side
+    both = torch.zeros((kp.shape[0], 2, hkv, page, D), dtype=torch.uint8, device="cuda")
+    both[:, 0], both[:, 1] = bits(kp).transpose(1, 2), bits(vp).transpose(1, 2)
+    k2, v2 = both[:, 0].transpose(1, 2).view(FP8), both[:, 1].transpose(1, 2).view(FP8)
+    o2, lse2 = dash.attn_decode_fp8(q, k2, v2, ks, vs, table, i32(lens))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    table[4, 700 // page] = -1
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    with pytest.raises(dash.DashError, match="outside the cache"):
+        dash.dash_sync_status()
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
+
+
 @pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("spread", [3.0, 20.0])
 @pytest.mark.parametrize("hq,hkv", [(4, 2), (12, 1)])
