@@ -51,8 +51,9 @@ constexpr int kHeads = 8, kTerms = 2, kCols = kTerms * kHeads;
 constexpr int kTile8 = 128;        // tokens
 constexpr int kStages = 5;         // K and V tiles
 constexpr int kSlots = 4;          // tiles whose scales and masks are held
-constexpr float kTop = 16.f;       // where a weight's maximum is put, ...
-constexpr float kMost = 256.f;     // ... and where it is moved
+// log2 of where a head's largest weight is put, of how far a weight may grow past
+// that (e4m3 holds 448), and of how far 2^(x - m) may.
+constexpr float kTopLog = 4.f, kGrow = 4.f, kLazy = 8.f;
 
 constexpr uint32_t kStageBytes = kTile8 * 128;  // rows of 128 bytes, D of them used
 constexpr uint32_t kColBytes = kCols * 128;     // Q or P: a row of 128 bytes for each column
@@ -64,8 +65,10 @@ constexpr uint32_t oMask = oScale + kSlots * 2 * kTile8 * 4;  // [kSlots][4]
 constexpr uint32_t oSc = oMask + kSlots * 16;          // [2][8] a score's factor
 constexpr uint32_t oItem = oSc + 2 * kHeads * 4;       // [2] what the item is
 constexpr uint32_t oRed = oItem + 2 * 32;              // [16][4] maxima of the warps, then masks of heads [4]
-constexpr uint32_t oSum = oRed + 4 * 16 * 4 + 16;      // [8][4] sums of the warps, then [8] factors
-constexpr uint32_t oBar = oSum + 5 * kHeads * 4;
+constexpr uint32_t oSum = oRed + 4 * 16 * 4 + 16;      // [8][4] sums of the warps
+constexpr uint32_t oHead = oSum + 4 * kHeads * 4;      // [8] the state of each head
+constexpr uint32_t oMove = oHead + 32 * kHeads;        // [8] {l's, O's} factors of a step that moves maxima; in the end O's
+constexpr uint32_t oBar = oMove + 8 * kHeads;
 enum {
   bSFull = 0, bPFull = 2, bPvDone = 4, bQFull = 6, bQEmpty = 8, bTile = 10, bKvFull = bTile + kSlots,
   bKvEmpty = bKvFull + kStages, bFinal = bKvEmpty + kStages, kBars
@@ -106,11 +109,26 @@ __device__ __forceinline__ bool any_of_128(bool x) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Two columns of the warp's 32 lanes, waited on.
+__device__ __forceinline__ float2 tmem_ld1x2(uint32_t a, uint32_t b) {
+  float2 r;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b)
+      : "memory");
   return r;
 }
+// A head of the item in hand, the same for all 128 tokens of a tile.
+struct Head {
+  float factor;          // of its scores
+  float ref, limit;      // what 2^(x - m) refers to (m, or 0), and from where m moves
+  float wref, wlimit;    // the same of the weights: M less kTopLog, or 0
+  float m, M, pad;
+};
+static_assert(sizeof(Head) == 32, "two 16-byte words");
 // Reduces N values (a power of two up to 32) over the lanes of a warp, all at
 // once: each exchange halves the values that a lane keeps.  The lane ends with
 // value number lane / (32 / N); lanes of the same number hold the same.
@@ -299,7 +317,10 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
     Ring<kStages> r;
     uint32_t loads = 0;
     Walk walk(p, lens);
-    long long number = blockIdx.x;
+    // split and head of the next item, and the steps to the one after it
+    long long want = blockIdx.x / p.Hkv;
+    int hk = blockIdx.x % p.Hkv;
+    const int want_step = gridDim.x / p.Hkv, hk_step = gridDim.x % p.Hkv;
     // The next item that has tokens, with what its start waits for: its Q and the pages of its first two tiles.
     // Empty sequences are answered on the way.
     struct Next {
@@ -312,11 +333,16 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       return t < it.end ? p.table[it.b * p.table_row + quotient(p.page, t)] : -1;
     };
     auto look_up = [&]() {
-      for (;; number += gridDim.x) {
-        const long long want = number / p.Hkv;
+      while (true) {
         next.it.tiles = -1;
         if (!walk.find(p, want, lane)) return;
-        next.it = item_of(p, walk, (int)(number - want * p.Hkv));
+        next.it = item_of(p, walk, hk);
+        want += want_step;
+        hk += hk_step;
+        if (hk >= p.Hkv) {
+          hk -= p.Hkv;
+          ++want;
+        }
         if (next.it.tiles > 0) break;
         for (int h = 0; h < p.group; ++h) {
           const int hh = next.it.hk * p.group + h;
@@ -324,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
           if (row == 0 && p.lse) p.lse[(size_t)next.it.b * p.Hq + hh] = -INFINITY;
         }
       }
-      number += gridDim.x;
       next.q = make_uint4(0u, 0u, 0u, 0u);
       if (head < p.group)
         next.q = *reinterpret_cast<const uint4 *>(p.q + next.it.b * p.q_batch +
@@ -529,49 +554,55 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
     const int tok = threadIdx.x;
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
     float *red = reinterpret_cast<float *>(smem + oRed), *sums = reinterpret_cast<float *>(smem + oSum);
+    Head *heads = reinterpret_cast<Head *>(smem + oHead);
+    float2 *moves = reinterpret_cast<float2 *>(smem + oMove);
     while (true) {
       mbar_wait(&bars[bQFull + ib], iph, g);
       const Item it = items[ib];
+      if (tok < kHeads)
+        heads[tok] = {factors[ib * kHeads + tok], 0.f, -INFINITY, 0.f, -INFINITY, -INFINITY, -INFINITY, 0.f};
       if (any_of_128(it.tiles < 0 || *g.abort)) break;  // one answer, as barriers follow
-      float sc[kHeads], m[kHeads], M[kHeads], up[kHeads], l[kHeads];
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-        sc[h] = factors[ib * kHeads + h];
-        m[h] = M[h] = -INFINITY;
-        up[h] = NAN;
-        l[h] = 0.f;
-      }
-      __syncwarp();
       if (lane == 0) mbar_arrive(&bars[bQEmpty + ib]);
+      float l[kHeads];
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) l[h] = 0.f;
       // After an abort the loop runs on with whatever tensor memory holds: no
       // wait blocks any more, and the status word tells that O is not valid.
       for (int j = 0; j < it.tiles; ++j) {
         const uint32_t tile = T + j, slot = tile % kSlots;
         mbar_wait(&bars[bTile + slot], (tile / kSlots) & 1, g);
-        const float ks = scales[slot * 2 * kTile8 + tok], vs = scales[slot * 2 * kTile8 + kTile8 + tok];
+        const float ks = scales[slot * 2 * kTile8 + tok], lv = lg2(scales[slot * 2 * kTile8 + kTile8 + tok]);
         const bool valid = (masks[slot * 4 + warp] >> lane) & 1u;
         mbar_wait(&bars[bSFull + (tile & 1)], (tile >> 1) & 1, g);
         __syncwarp();
         tc_fence_after();
         uint32_t s[16];
         tmem_ld16(tl + cS + (tile & 1) * kCols, s);
-        float pr[kHeads], pv[kHeads], most = 0.f;
+        float x[kHeads];
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) {
           const float y = fmaf(__uint_as_float(s[kHeads + h]), 1.f / 16, __uint_as_float(s[h])) * ks;
-          s[h] = __float_as_uint(y);
-          pr[h] = valid ? ex2(fmaf(y, sc[h], -m[h])) : 0.f;
-          pv[h] = valid ? pr[h] * (vs * up[h]) : 0.f;
-          most = max_nan(most, max_nan(pr[h], pv[h]));
+          x[h] = valid ? y * heads[h].factor : -INFINITY;
         }
         mbar_wait(&bars[bPvDone + (tile & 1)], ((tile >> 1) & 1) ^ 1, g);  // its place of P is free
-        // the weights' terms, a byte in each column's row
         uint8_t *pt = smem + oP + (tile & 1) * kColBytes + (tok & 15);
-        auto send = [&]() {
+        float pr[kHeads];
+        for (int turn = 0;; ++turn) {
+          // the weights' terms, a byte in each column's row
+          uint32_t over = 0;
 #pragma unroll
           for (int h = 0; h < kHeads; h += 2) {
+            float pv[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 st = *reinterpret_cast<const float4 *>(&heads[h + i]);
+              const float wlimit = heads[h + i].wlimit, a = x[h + i] + lv;
+              over |= (x[h + i] > st.z || a > wlimit ? 1u : 0u) << (h + i);
+              pr[h + i] = ex2(x[h + i] - st.y);
+              pv[i] = ex2(a - st.w);
+            }
             uint32_t t2[kTerms];
-            terms_of(pv[h], pv[h + 1], t2);
+            terms_of(pv[0], pv[1], t2);
 #pragma unroll
             for (int k = 0; k < kTerms; ++k) {
               const int n = k * kHeads + h;
@@ -581,21 +612,18 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
           }
           fence_proxy_async_smem();
           tc_fence_before();
-        };
-        send();
-        // A NaN is not within the limit, and where nothing counts yet no number is: the step is done anew, with new maxima.
-        if (any_of_128(!(most <= kMost))) {
-          // only the heads that need it move, so that a head's bits do not depend on the others
-          const float lv = lg2(vs);
-          uint32_t over = 0;
-          float both[2 * kHeads];  // x and x + log2 c
+          if (turn > 0) {
+            named_bar(2, 128);
+            break;
+          }
+          if (!any_of_128(over != 0)) break;
+          // Maxima move, of the heads that need it only, so that a head's bits do not depend on the others; then the
+          // weights are made anew.
+          float both[2 * kHeads];
 #pragma unroll
           for (int h = 0; h < kHeads; ++h) {
-            const float x = valid ? __uint_as_float(s[h]) * sc[h] : -INFINITY;
-            s[h] = __float_as_uint(x);
-            both[h] = x;
-            both[kHeads + h] = x + lv;
-            over |= (pr[h] <= kMost && pv[h] <= kMost ? 0u : 1u) << h;
+            both[h] = x[h];
+            both[kHeads + h] = x[h] + lv;
           }
           const float top = reduce_all(both, lane, [](float a, float b) { return fmaxf(a, b); });
           over = __reduce_or_sync(0xffffffffu, over);
@@ -603,41 +631,43 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
           red[(lane >> 1) * 4 + warp] = top;
           if (lane == 0) all_over[warp] = over;
           named_bar(2, 128);
-          over = (all_over[0] | all_over[1]) | (all_over[2] | all_over[3]);
+          if (tok < kHeads) {
+            Head &hd = heads[tok];
+            float2 f = make_float2(1.f, 1.f);
+            if (((all_over[0] | all_over[1] | all_over[2] | all_over[3]) >> tok) & 1u) {
+              const float4 a = reinterpret_cast<const float4 *>(red)[tok], b = reinterpret_cast<const float4 *>(red)[kHeads + tok];
+              const float m1 = fmaxf(hd.m, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+              const float M1 = fmaxf(hd.M, fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+              const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
+              f = make_float2(ex2(hd.m - mr), ex2(hd.M - Mr));
+              hd.m = m1;
+              hd.M = M1;
+              hd.ref = mr;
+              hd.limit = m1 + kLazy;
+              hd.wref = M1 == -INFINITY ? 0.f : M1 - kTopLog;
+              hd.wlimit = M1 + kGrow;
+            }
+            moves[tok] = f;
+          }
           if (j > 0) {  // the product before has completed: O may be rewritten
             mbar_wait(&bars[bPvDone + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, g);
             __syncwarp();
             tc_fence_after();
           }
-          float fo[kHeads];
+          named_bar(2, 128);
+          uint32_t o[16];
+          if (j > 0) tmem_ld16(tl + cO, o);
 #pragma unroll
           for (int h = 0; h < kHeads; ++h) {
-            fo[h] = 1.f;
-            if (!((over >> h) & 1u)) continue;
-            const float4 a = reinterpret_cast<const float4 *>(red)[h], b = reinterpret_cast<const float4 *>(red)[kHeads + h];
-            const float m1 = fmaxf(m[h], fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
-            const float M1 = fmaxf(M[h], fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
-            const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
-            l[h] *= ex2(m[h] - mr);
-            fo[h] = ex2(M[h] - Mr);
-            m[h] = m1;
-            M[h] = M1;
-            // a factor that 32 bits cannot hold stays NaN, and every step comes here
-            up[h] = fabsf(m1 - M1) < 100.f ? kTop * ex2(m1 - M1) : NAN;
-            const float x = __uint_as_float(s[h]);
-            pr[h] = ex2(x - mr);
-            pv[h] = valid ? kTop * ex2(x + lv - Mr) : 0.f;
+            const float2 f = moves[h];
+            l[h] *= f.x;
+            o[h] = __float_as_uint(__uint_as_float(o[h]) * f.y);
+            o[kHeads + h] = __float_as_uint(__uint_as_float(o[kHeads + h]) * f.y);
           }
           if (j > 0) {
-            uint32_t o[16];
-            tmem_ld16(tl + cO, o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo[e & 7]);
             tmem_st16(tl + cO, o);
             tmem_st_wait();
           }
-          send();
-          named_bar(2, 128);
         }
         if (tok == 0) mbar_arrive(&bars[bPFull + (tile & 1)]);
 #pragma unroll
@@ -647,41 +677,35 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       const float mine = reduce_all(l, lane, [](float a, float b) { return a + b; });
       sums[(lane >> 2) * 4 + warp] = mine;
       named_bar(2, 128);
-      float *averages = sums + 4 * kHeads;
       const int h0 = it.hk * p.group, parts = p.max_splits;
       const size_t first = ((size_t)it.b * p.Hq + h0) * parts + it.split;
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h)
-        if (tok == h) {
-          const float4 w = reinterpret_cast<const float4 *>(sums)[h];
-          const float ll = (w.x + w.y) + (w.z + w.w);
-          averages[h] = ll == 0.f ? 0.f : ex2(M[h] - m[h]) * (1.f / kTop) * inverse_sum(ll);
-          if (h < p.group) {
-            if (it.n_splits > 1) p.part_ml[first + (size_t)h * parts] = make_float2(m[h], ll);
-            else if (p.lse) p.lse[(size_t)it.b * p.Hq + h0 + h] = log_sum(m[h], ll);
-          }
-        }
+      if (tok < p.group) {
+        const float4 w = reinterpret_cast<const float4 *>(sums)[tok];
+        const float ll = (w.x + w.y) + (w.z + w.w), m = heads[tok].m;
+        moves[tok].x = ll == 0.f ? 0.f : ex2(heads[tok].M - kTopLog - m) * inverse_sum(ll);
+        if (it.n_splits > 1) p.part_ml[first + (size_t)tok * parts] = make_float2(m, ll);
+        else if (p.lse) p.lse[(size_t)it.b * p.Hq + h0 + tok] = log_sum(m, ll);
+      }
       const uint32_t last = T + it.tiles - 1;
       mbar_wait(&bars[bPvDone + (last & 1)], (last >> 1) & 1, g);
       __syncwarp();
       tc_fence_after();
-      uint32_t o[16];
-      tmem_ld16(tl + cO, o);
-      tc_fence_before();
       named_bar(2, 128);
-      if (tok < D) {
-        float *part = p.part_o + first * D + tok;
-        __nv_bfloat16 *out = p.o + it.b * p.o_batch + h0 * p.o_head + tok;
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          const float y = fmaf(__uint_as_float(o[kHeads + h]), 1.f / 16, __uint_as_float(o[h])) * averages[h];
-          if (h < p.group) {
-            if (it.n_splits > 1) part[(size_t)h * parts * D] = y;
-            else out[h * p.o_head] = __float2bfloat16_rn(y);
-          }
+      float *part = p.part_o + first * D + tok;
+      __nv_bfloat16 *out = p.o + it.b * p.o_batch + h0 * p.o_head + tok;
+#pragma unroll 1
+      for (int h = 0; h < p.group; ++h) {
+        const float2 o = tmem_ld1x2(tl + cO + h, tl + cO + kHeads + h);
+        const float y = fmaf(o.y, 1.f / 16, o.x) * moves[h].x;
+        if (tok < D) {
+          if (it.n_splits > 1) *part = y;
+          else *out = __float2bfloat16_rn(y);
         }
+        part += (size_t)parts * D;
+        out += p.o_head;
       }
-      named_bar(2, 128);  // `sums` is free for the next item
+      tc_fence_before();
+      named_bar(2, 128);  // shared memory is free for the next item
       T += it.tiles;
       ib ^= 1;
       if (ib == 0) iph ^= 1;
