@@ -327,34 +327,52 @@ __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
   const int n = p.parts_before + decode_splits(decode_len(p, b), p.least_chunk);
   if (n <= 1 && p.parts_before == 0) return;  // written by the first kernel
   const size_t at = ((size_t)b * p.Hq + h) * (p.parts_before + p.max_splits);
-  __shared__ float s_w[128];
+  __shared__ __align__(16) float s_w[128];
+  __shared__ float s_m[4];
   __shared__ float4 s_o[128];
-  const int tid = threadIdx.x;
+  using J = Join<D>;
+  const int tid = threadIdx.x, c = tid % J::kVec, part = tid / J::kVec;
+  // the first rows are on their way while the weights are made
+  constexpr int kAhead = 8;
+  const float *row = p.part_o + at * D + 4 * c;
+  float4 v[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = part + k * J::kPart;
+    v[k] = i < n ? *reinterpret_cast<const float4 *>(row + (size_t)i * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   // at most 128 splits: one per thread
   const float2 ml = tid < n ? p.part_ml[at + tid] : make_float2(-INFINITY, 0.f);
-  s_w[tid] = ml.x;
+  float m = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) s_m[tid >> 5] = m;
   __syncthreads();
-  float m = -INFINITY;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, s_w[i]);
-  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
   const float ref = m == -INFINITY ? 0.f : m;
-  using J = Join<D>;
   s_w[tid] = J::weight(ml, ref);
   __syncthreads();
-  float l = 0.f;
-  for (int i = 0; i < n; ++i) l += s_w[i];
-  const int c = tid % J::kVec, part = tid / J::kVec;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = part; i < n; i += J::kPart)
-    J::add(o, s_w[i], *reinterpret_cast<const float4 *>(p.part_o + (at + i) * D + 4 * c));
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (part + k * J::kPart < n) J::add(o, s_w[part + k * J::kPart], v[k]);
+#pragma unroll 8
+  for (int i = part + kAhead * J::kPart; i < n; i += J::kPart)
+    J::add(o, s_w[i], *reinterpret_cast<const float4 *>(row + (size_t)i * D));
   s_o[tid] = o;
+  // the weights' sum, in their order (those behind the last split are 0)
+  float l = 0.f;
+  for (int i = 0; i < n; i += 4) {
+    const float4 w = *reinterpret_cast<const float4 *>(s_w + i);
+    l = ((l + w.x) + w.y) + w.z;
+    l += w.w;
+  }
   __syncthreads();
   if (part == 0) {
 #pragma unroll
     for (int k = 1; k < J::kPart; ++k) {
-      const float4 v = s_o[k * J::kVec + c];
-      o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+      const float4 u = s_o[k * J::kVec + c];
+      o = make_float4(o.x + u.x, o.y + u.y, o.z + u.z, o.w + u.w);
     }
     J::write(p, b, h, 4 * c, o, m, l);
   }
