@@ -660,7 +660,7 @@ dash_status_t encode_rows_map(CUtensorMap *m, const void *base, int heads, long 
   return make_rows_map(m, base, heads, rows, D, row_stride, head_stride, box_rows);
 }
 // The map of 8-bit pages [n_pages][page_size][heads][D] with strides in bytes;
-// boxes of `box` tokens of a page and head.  False where the driver takes no such map.
+// boxes of `box` tokens of a page and head, swizzled within a row.  False where the driver takes no such map.
 bool encode_pages8_map(CUtensorMap *m, const void *base, int n_pages, int page_size, int heads, int D, long long page,
                        long long token, long long head, int box) {
   EncodeTiledFn fn = encode_fn();
@@ -672,8 +672,8 @@ bool encode_pages8_map(CUtensorMap *m, const void *base, int n_pages, int page_s
   cuuint32_t boxes[4] = {(cuuint32_t)D, 1, (cuuint32_t)box, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, boxes, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace dash
 

@@ -25,8 +25,8 @@
 // a break in its loads.  Warps: 0-3 softmax (a thread owns a token, and in the
 // end a dim), 4-7 fetch and split Q, 8 issues the MMAs, the next tile's scores
 // before this tile's O.  A token's row lies wherever its page does.  Where a tile's
-// tokens all count, TMA takes the tokens of a page at once (D = 128, pages of a
-// multiple of 8 tokens); other rows come by 16-byte asynchronous copies, which can
+// tokens all count, TMA takes the tokens of a page at once (pages of a multiple of 8
+// tokens); other rows come by 16-byte asynchronous copies, which can
 // leave zeros for a token that does not count.  Tensor memory: S twice at 0 and 16, O at 32.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,16 +49,15 @@ constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsFetch = 72, kRegsMma = 
 static_assert(kRegsSoftmax + kRegsFetch + kRegsMma <= 3 * kRegsLaunch, "register split exceeds the CTA's allocation");
 constexpr int kHeads = 8, kTerms = 2, kCols = kTerms * kHeads;
 constexpr int kTile8 = 128;        // tokens
-constexpr int kStages = 5;         // K and V tiles
-constexpr int kSlots = 4;          // tiles whose scales and masks are held
+constexpr int kSlots = 8;          // tiles whose scales and masks are held
 // log2 of where a head's largest weight is put, of how far a weight may grow past
 // that (e4m3 holds 448), and of how far 2^(x - m) may.
 constexpr float kTopLog = 4.f, kGrow = 4.f, kLazy = 8.f;
 
-constexpr uint32_t kStageBytes = kTile8 * 128;  // rows of 128 bytes, D of them used
+constexpr uint32_t kRing = 5 * 128 * kTile8;    // bytes of K and V tiles
 constexpr uint32_t kColBytes = kCols * 128;     // Q or P: a row of 128 bytes for each column
 constexpr uint32_t oKV = 0;
-constexpr uint32_t oQ = oKV + kStages * kStageBytes;   // twice
+constexpr uint32_t oQ = oKV + kRing;                   // twice
 constexpr uint32_t oP = oQ + 2 * kColBytes;            // twice
 constexpr uint32_t oScale = oP + 2 * kColBytes;        // [kSlots][2][128]
 constexpr uint32_t oMask = oScale + kSlots * 2 * kTile8 * 4;  // [kSlots][4]
@@ -71,7 +70,26 @@ constexpr uint32_t oMove = oHead + 32 * kHeads;        // [8] {l's, O's} factors
 constexpr uint32_t oBar = oMove + 8 * kHeads;
 enum {
   bSFull = 0, bPFull = 2, bPvDone = 4, bQFull = 6, bQEmpty = 8, bTile = 10, bKvFull = bTile + kSlots,
-  bKvEmpty = bKvFull + kStages, bFinal = bKvEmpty + kStages, kBars
+  bKvEmpty = bKvFull + 10, bFinal = bKvEmpty + 10, kBars  // up to 10 stages
+};
+// K and V tiles: rows of D bytes, swizzled within 128 bytes or within 64.
+template <int D>
+struct Tile {
+  static constexpr uint32_t kBytes = kTile8 * D, kGroup = 8 * D;  // a stage; eight rows, the unit of the layout
+  static constexpr int kStages = kRing / kBytes;
+  static_assert(kStages <= 10, "barriers");
+  // K of tile j + n is asked for once the load kStages before it has been read.  V of tile j is read after the tile's
+  // scales are, and 2 n - 3 loads lie between the two, so n reaches (kStages + 2) / 2.
+  static_assert(kSlots > (kStages + 2) / 2, "a slot would be filled before it is read");
+  // where 16-byte piece c of a row stands in it
+  static __device__ __forceinline__ int place(int row, int c) { return (c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4; }
+  // Descriptors.  K's rows are the operand's rows.  V's are its columns: of D = 64
+  // the upper half of the 128 rows that an MMA has is the lower half again (an
+  // offset of 0 between the panels of 64), and nobody reads what comes of it.
+  static __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t panel) {
+    const uint64_t d = sw128_desc(addr, panel, kGroup);
+    return D == 128 ? d : (d & ~(7ull << 61)) | 4ull << 61;  // 64-byte swizzle
+  }
 };
 constexpr uint32_t oMisc = oBar + kBars * 8;
 constexpr int kSorted = 1024;  // sequences whose lengths are held
@@ -258,6 +276,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Decode8Params p,
     int box) {  // tokens that TMA takes at once; 0: none
+  using Ti = Tile<D>;
+  constexpr int kStages = Ti::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   // the join may be set up now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -405,52 +425,51 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       };
       auto fetch = [&](bool is_v, uint32_t tile, const Where &at) {
         mbar_wait(&bars[bKvEmpty + r.st], r.ph ^ 1, g);
-        __syncwarp();
+        // After an abort nothing more arrives at a stage: one that waits for bytes of TMA has no arrivals left to take.
+        if (warp_aborted(g)) return;
         const CacheStrides &st = is_v ? p.c.vs : p.c.ks;
         const uint32_t slot = tile % kSlots;
-        const uint32_t dst = smem_u32(smem + oKV + r.st * kStageBytes) + (w * 32 + rsub) * 128;
+        const uint32_t dst = smem_u32(smem + oKV + r.st * Ti::kBytes) + (w * 32 + rsub) * D;
         const uint8_t *base = is_v ? vbase : kbase;
         bool by_copies = true;
-        if (!warp_aborted(g)) {
-          if (D == 128 && box > 0 && at.whole && at.valid == 0xffffffffu) {
-            by_copies = false;
-            uint64_t *bar = &bars[bKvFull + r.st];
-            if ((row & (box - 1)) == 0) {
-              mbar_arrive_expect_tx(bar, box * 128);
-              tma_load_4d(smem + oKV + r.st * kStageBytes + row * 128, is_v ? &tmV : &tmK, bar, 0, it.hk, at.off, at.page);
-            } else {
-              mbar_arrive(bar);
-            }
-          } else if (at.valid == 0xffffffffu && p.whole) {
-            const long long step = kRowsPer * st.token;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // 16 tokens lie in one page
-              const int pg = __shfl_sync(0xffffffffu, at.page, 16 * half), of = __shfl_sync(0xffffffffu, at.off, 16 * half);
-              const uint8_t *from = wide_add(wide_add(base, pg, (int)st.page), of + rsub, (int)st.token);
-#pragma unroll
-              for (int i = 0; i < 16 / kRowsPer; ++i, from += step) {
-                const int rr = 16 * half + i * kRowsPer;
-                cp_async<16>(dst + rr * 128 + ((c ^ ((rr + rsub) & 7)) << 4), from);
-              }
-            }
+        if (box > 0 && at.whole && at.valid == 0xffffffffu) {
+          by_copies = false;
+          uint64_t *bar = &bars[bKvFull + r.st];
+          if ((row & (box - 1)) == 0) {
+            mbar_arrive_expect_tx(bar, box * D);
+            tma_load_4d(smem + oKV + r.st * Ti::kBytes + row * D, is_v ? &tmV : &tmK, bar, 0, it.hk, at.off, at.page);
           } else {
-            const long long a = (at.valid >> lane) & 1u ? at.page * st.page + at.off * st.token : 0;
+            mbar_arrive(bar);
+          }
+        } else if (at.valid == 0xffffffffu && p.whole) {
+          const long long step = kRowsPer * st.token;
 #pragma unroll
-            for (int i = 0; i < 32 / kRowsPer; ++i) {
-              const int rr = i * kRowsPer + rsub;
-              const long long x = __shfl_sync(0xffffffffu, a, rr);
-              cp_async_if<16>(dst + i * kRowsPer * 128 + ((c ^ (rr & 7)) << 4), base + x, (at.valid >> rr) & 1u);
+          for (int half = 0; half < 2; ++half) {  // 16 tokens lie in one page
+            const int pg = __shfl_sync(0xffffffffu, at.page, 16 * half), of = __shfl_sync(0xffffffffu, at.off, 16 * half);
+            const uint8_t *from = wide_add(wide_add(base, pg, (int)st.page), of + rsub, (int)st.token);
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsPer; ++i, from += step) {
+              const int rr = 16 * half + i * kRowsPer;
+              cp_async<16>(dst + rr * D + Ti::place(rr + rsub, c), from);
             }
           }
-          if (!is_v) {
-            const bool ok = (at.valid >> lane) & 1u;
-            const uint32_t sd = smem_u32(scales + slot * 2 * kTile8 + row);
-            cp_async_if<4>(sd, ok ? ksbase + at.page * p.c.kss.page + at.off * p.c.kss.token : ksbase, ok);
-            cp_async_if<4>(sd + kTile8 * 4, ok ? vsbase + at.page * p.c.vss.page + at.off * p.c.vss.token : vsbase, ok);
+        } else {
+          const long long a = (at.valid >> lane) & 1u ? at.page * st.page + at.off * st.token : 0;
+#pragma unroll
+          for (int i = 0; i < 32 / kRowsPer; ++i) {
+            const int rr = i * kRowsPer + rsub;
+            const long long x = __shfl_sync(0xffffffffu, a, rr);
+            cp_async_if<16>(dst + i * kRowsPer * D + Ti::place(rr, c), base + x, (at.valid >> rr) & 1u);
           }
         }
         if (!is_v) {
-          // the slot's last tile has been read: its weights were, by the product that freed this stage
+          const bool ok = (at.valid >> lane) & 1u;
+          const uint32_t sd = smem_u32(scales + slot * 2 * kTile8 + row);
+          cp_async_if<4>(sd, ok ? ksbase + at.page * p.c.kss.page + at.off * p.c.kss.token : ksbase, ok);
+          cp_async_if<4>(sd + kTile8 * 4, ok ? vsbase + at.page * p.c.vss.page + at.off * p.c.vss.token : vsbase, ok);
+        }
+        if (!is_v) {
+          // the slot's last tile has been read (see kSlots)
           if (lane == 0) {
             masks[slot * 4 + w] = at.valid;
             mbar_arrive(&bars[bTile + slot]);
@@ -498,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
     constexpr uint32_t idS = idesc8(128, kCols, 0), idO = idesc8(128, kCols, 1);
     Ring<kStages> r;
     uint32_t lead = elect_one();  // 0 in every lane once a wait has failed: nothing more is issued
-    const uint64_t k0 = sw128_desc(smem_u32(smem + oKV), 16, 1024), v0 = sw128_desc(smem_u32(smem + oKV), kStageBytes, 1024);
+    const uint64_t k0 = Ti::desc(smem_u32(smem + oKV), 16), v0 = Ti::desc(smem_u32(smem + oKV), 0);
     const uint64_t q0 = sw128_desc(smem_u32(smem + oQ), 16, 1024), p0 = sw128_desc(smem_u32(smem + oP), 16, 1024);
     auto wait = [&](uint64_t *bar, uint32_t ph) {
       if (!mbar_wait(bar, ph, g)) lead = 0;
@@ -512,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
         wait(&bars[bKvFull + r.st], r.ph);
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t a = k0 + ((r.st * kStageBytes) >> 4), b = q0 + ((ib * kColBytes) >> 4);
+        const uint64_t a = k0 + ((r.st * Ti::kBytes) >> 4), b = q0 + ((ib * kColBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) mma8_if(lead, tmem + cS + (tile & 1) * kCols, a + 2 * kk, b + 2 * kk, idS, kk > 0);
         tc_commit_if(lead, &bars[bSFull + (tile & 1)]);
@@ -532,10 +551,10 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
         fence_proxy_async_smem();
         wait(&bars[bPFull + (tile & 1)], (tile >> 1) & 1);
         tc_fence_after();
-        const uint64_t a = v0 + ((r.st * kStageBytes) >> 4), b = p0 + (((tile & 1) * kColBytes) >> 4);
+        const uint64_t a = v0 + ((r.st * Ti::kBytes) >> 4), b = p0 + (((tile & 1) * kColBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTile8 / 32; ++kk)
-          mma8_if(lead, tmem + cO, a + kk * (4096 >> 4), b + 2 * kk, idO, (j > 0 || kk > 0) ? 1u : 0u);
+          mma8_if(lead, tmem + cO, a + kk * (4 * Ti::kGroup >> 4), b + 2 * kk, idO, (j > 0 || kk > 0) ? 1u : 0u);
         tc_commit_if(lead, &bars[bPvDone + (tile & 1)]);
         tc_commit_if(lead, &bars[bKvEmpty + r.st]);
         r.next();
@@ -738,7 +757,7 @@ cudaError_t launch_decode8_wide(int D, const Decode8Params &p, int num_sms, cuda
   // tokens of a page that are a part of a tile
   int box = 128;
   while (p.page_size % box) box /= 2;
-  if (D != 128 || box < 8 ||
+  if (box < 8 ||
       !encode_pages8_map(&k, p.c.k, p.n_pages, p.page_size, p.Hkv, D, p.c.ks.page, p.c.ks.token, p.c.ks.head, box) ||
       !encode_pages8_map(&v, p.c.v, p.n_pages, p.page_size, p.Hkv, D, p.c.vs.page, p.c.vs.token, p.c.vs.head, box))
     box = 0;

@@ -222,10 +222,11 @@ def test_decode(lens, hq, hkv, D, page, room):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("D", [128, 64])
 @pytest.mark.parametrize("page", [1, 8, 12, 24, 32, 48, 64, 128, 200, 256])
-def test_decode_of_whole_tiles_in_pages_of_every_kind(page):
+def test_decode_of_whole_tiles_in_pages_of_every_kind(page, D):
     # rows are fetched a page's part of a tile at a time where it has one, row by row elsewhere; one bad page
-    lens, hq, hkv, D = [128, 1024, 1023, 640, 2500, 0, 127, 256, 1, 3000], 16, 2, 128
+    lens, hq, hkv = [128, 1024, 1023, 640, 2500, 0, 127, 256, 1, 3000], 16, 2
     kp, vp, ks, vs, table = c = cache(lens, hkv, D, page, width=max(ROOM, 3000) // page + 1)
     q = P.normal(9, len(lens), hq, D)
     o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
@@ -242,6 +243,22 @@ def test_decode_of_whole_tiles_in_pages_of_every_kind(page):
     with pytest.raises(dash.DashError, match="outside the cache"):
         dash.dash_sync_status()
     check(q, c, lens, 1 / math.sqrt(D), o, lse)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(16, 8, 64), (16, 8, 128), (3, 1, 64)])
+def test_decode_of_many_long_sequences(hq, hkv, D):
+    # loads run ahead of the products and the softmax as far as there is room, item after item
+    lens, page = [4096, 5000, 3000, 4096, 100, 8192, 4097, 1] * 4, 16
+    kp, vp, ks, vs, table = c = cache(lens, hkv, D, page, width=ROOM * (8 // hkv) // page)
+    q = P.normal(2, len(lens), hq, D)
+    o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+    dash.dash_sync_status()
+    few = slice(0, 8)
+    check(q[few], (kp, vp, ks, vs, table[few]), lens[few], 1 / math.sqrt(D), o[few], lse[few])
+    for _ in range(5):
+        o2, lse2 = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, i32(lens))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    dash.dash_sync_status()
 
 
 @pytest.mark.parametrize("room", [0, ROOM])
