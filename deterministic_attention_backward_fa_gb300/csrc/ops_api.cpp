@@ -132,6 +132,8 @@ long long dash_decode_shared_workspace(int B, int Hq, int Hkv, int D, int page_s
   if (B < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 || prefix < 0 ||
       (long long)page_size * max_pages > kMaxCached || prefix > (long long)page_size * max_pages)
     return -1;
+  if (dash::prefix_with_tails(B, Hq, Hkv, page_size * max_pages))
+    return dash_decode_workspace(B, Hq, D, page_size, max_pages);
   const int parts = dash::prefix_cut(std::max(B, 1), Hq, Hkv, prefix).splits +
                     std::max(1, dash::decode_max_splits(page_size * max_pages - prefix));
   return (long long)B * Hq * parts * (D * 4 + 8) + 256;
@@ -154,10 +156,12 @@ dash_status_t dash_attn_decode_shared(const void *q, const void *k_pages, const 
     return report(DASH_ERR_UNSUPPORTED, "more than %lld rows on one K/V head", 65535LL * 2 * dash::kPackedTile);
   dash::SharedParams p = {};
   const dash::PrefixCut cut = dash::prefix_cut(std::max(B, 1), Hq, Hkv, prefix);
+  const bool together = max_pages >= 0 && page_size > 0 && (long long)page_size * max_pages <= kMaxCached && B >= 0 &&
+                        dash::prefix_with_tails(B, Hq, Hkv, page_size * max_pages);
   if ((st = decode_params(q, page_table, lengths, o, lse, B, Hq, Hkv, D, n_pages, page_size, max_pages, strides,
                           strides ? strides + 10 : nullptr, scale, workspace, workspace_bytes,
-                          dash_decode_shared_workspace(B, Hq, Hkv, D, page_size, max_pages, prefix), prefix,
-                          cut.splits, &p)) != DASH_OK ||
+                          dash_decode_shared_workspace(B, Hq, Hkv, D, page_size, max_pages, prefix),
+                          together ? 0 : prefix, together ? 0 : cut.splits, &p)) != DASH_OK ||
       B == 0)
     return st;
   if ((st = decode_cache(k_pages, v_pages, Hkv, D, n_pages, page_size, strides, &p)) != DASH_OK) return st;
@@ -168,7 +172,10 @@ dash_status_t dash_attn_decode_shared(const void *q, const void *k_pages, const 
   Device device;
   if ((st = current_device(&dev, &device)) != DASH_OK) return st;
   p.status = device.status;
-  const cudaError_t e = dash::launch_decode_shared(D, p, device.sms, reinterpret_cast<cudaStream_t>(stream));
+  p.shared = together ? prefix : 0;
+  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = together ? dash::launch_decode(D, p, device.sms, on)
+                                 : dash::launch_decode_shared(D, p, device.sms, on);
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "decode launch");
 }
 

@@ -199,6 +199,7 @@ inline dash_status_t decode_params(const void *q, const int32_t *page_table, con
   p.max_pages = max_pages;
   p.hblocks = (p.group + 15) / 16;
   p.first = first;
+  p.shared = 0;
   p.parts_before = parts_before;
   p.least_chunk = kMinChunk;
   p.scale_log2 = scale * kLog2e;

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
     // A lane below 16 keeps the row of one of the warp's tokens.
     auto page_of = [&](int step) -> int {
       const int t = begin + step * kStep + warp * kTok + (lane & 15);
-      return t < end ? table[(p.first + t) / p.page_size] : -1;
+      return t < end ? (t < p.shared ? p.table : table)[(p.first + t) / p.page_size] : -1;
     };
     uint32_t valid_ring[kStages];  // the tokens of each stage that count
     auto load = [&](int step, int page, int slot) -> uint32_t {

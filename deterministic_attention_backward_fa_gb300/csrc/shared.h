@@ -29,6 +29,16 @@ inline PrefixCut prefix_cut(int B, int Hq, int Hkv, int prefix) {
   return {(int)((n + tiles - 1) / tiles), (int)tiles};
 }
 
+// Whether the prefix is left to dash_decode_kernel, for every sequence by itself:
+// where all its splits run at once and are short, what re-reads of the prefix cost
+// (they hit L2) is less than two more launches.  4 sequences of 1501 tokens and
+// some, 16 heads on 4: 7.8 us against 9.9; 12 of 512 on 8 K/V heads 9.9 and 10.1;
+// beyond, 16 of 512 14.3 and 10.0, and one of 4096 in longer splits 11.3 and 9.9.
+inline bool prefix_with_tails(int B, int Hq, int Hkv, int cap) {
+  return decode_chunk(cap) == kMinChunk &&
+         (long long)B * Hkv * ((Hq / Hkv + 15) / 16) * decode_max_splits(cap) <= 2 * kPrefixCtas;
+}
+
 cudaError_t prepare_shared();
 // The prefix, the tails behind it, and their join.
 cudaError_t launch_decode_shared(int D, const SharedParams &p, int num_sms, cudaStream_t stream);

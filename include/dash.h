@@ -576,7 +576,8 @@ dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, 
  * pages that the table's first row names, and the other rows' entries for them
  * are not read, but for a page that the prefix fills in part, which every
  * sequence continues in the page of its own row.  Their K and V are read once
- * for the batch instead of once per sequence.  `lengths` count the prefix; a
+ * for the batch instead of once per sequence (small calls, in which that saves
+ * nothing, attend it with each sequence's tail).  `lengths` count the prefix; a
  * sequence may also end inside it.  The parts are cut by the sizes alone, so a
  * call's bits are the same in every run; they depend on B and prefix, unlike
  * those of dash_attn_decode, which a prefix of 0 is.  Workspace:

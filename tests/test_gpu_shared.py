@@ -24,10 +24,12 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def cache(lens, prefix, hkv, D, page, seed=1, extra=0):
+def cache(lens, prefix, hkv, D, page, seed=1, wide=False):
     """Pages in random order.  Whole pages of the prefix belong to all; the page that it fills in part is each
     sequence's own copy.  ``seen``: the table as the call sees it, whose entries for the prefix's whole pages are
-    named by the first row alone."""
+    named by the first row alone.  ``wide``: a table of more than 4096 tokens, for which the prefix is attended apart
+    from the tails however few the sequences are."""
+    extra = 4096 // page + 1 if wide else 0
     full = prefix // page
     width = max([-(-n // page) for n in lens] + [-(-prefix // page)]) + extra
     need = [max(0, -(-max(n, prefix if b == 0 else 0) // page) - full) for b, n in enumerate(lens)]
@@ -66,10 +68,14 @@ CASES = [(1, [0], 1, 1, 64, 16), (128, [0, 1], 4, 2, 128, 16), (127, [3, 0, 17],
          (20000, [1, 2], 2, 1, 128, 16), (300, [4] * 70, 8, 1, 128, 32), (9000, [33, 0], 32, 32, 64, 128)]
 
 
+both = pytest.mark.parametrize("wide", [False, True], ids=["", "wide"])
+
+
+@both
 @pytest.mark.parametrize("prefix,tails,hq,hkv,D,page", CASES, ids=lambda x: str(x)[:30])
-def test_shared(prefix, tails, hq, hkv, D, page):
+def test_shared(prefix, tails, hq, hkv, D, page, wide):
     lens = [prefix + n for n in tails]
-    kp, vp, table, seen = cache(lens, prefix, hkv, D, page)
+    kp, vp, table, seen = cache(lens, prefix, hkv, D, page, wide=wide)
     for b, n in enumerate(lens):  # whatever stands behind a sequence's last token is not read into its result
         if n % page:
             last = table[b, n // page].long()
@@ -83,9 +89,10 @@ def test_shared(prefix, tails, hq, hkv, D, page):
     dash.dash_sync_status()
 
 
-def test_sequences_that_end_inside_the_prefix():
+@pytest.mark.parametrize("longest", [2000, 5000])
+def test_sequences_that_end_inside_the_prefix(longest):
     prefix, hq, hkv, D, page = 900, 4, 2, 128, 16
-    lens = [900, 0, 1, 127, 128, 129, 500, 899, 950, 2000, 640]
+    lens = [900, 0, 1, 127, 128, 129, 500, 899, 950, longest, 640]
     kp, vp, table, seen = cache(lens, prefix, hkv, D, page)
     q = R.normal(3, len(lens), hq, D)
     o, lse = dash.attn_decode_shared(q, kp, vp, seen, i32(lens), prefix)
@@ -95,7 +102,7 @@ def test_sequences_that_end_inside_the_prefix():
     with torch.cuda.graph(graph):
         og, lg = dash.attn_decode_shared(q, kp, vp, seen, lengths, prefix)
     cap = table.shape[1] * page
-    for now in (lens, [cap if n == 2000 else min(n, 900) for n in lens]):
+    for now in (lens, [cap if n == longest else min(n, 900) for n in lens]):
         lengths.copy_(i32(now))
         graph.replay()
         check(q, kp, vp, table, now, og, lg)
@@ -117,11 +124,12 @@ def test_no_prefix_is_the_plain_decode_and_a_prefix_alone():
     dash.dash_sync_status()
 
 
-def test_rows_whose_first_tiles_count_nothing():
+@both
+def test_rows_whose_first_tiles_count_nothing(wide):
     # bad pages (reported), scores of -inf, then tokens that count, with scores far below zero
     prefix, hq, hkv, D, page = 128 * 7, 4, 1, 64, 64
     lens = [prefix + 10, prefix]
-    kp, vp, table, seen = cache(lens, prefix, hkv, D, page)
+    kp, vp, table, seen = cache(lens, prefix, hkv, D, page, wide=wide)
     q = R.normal(5, 2, hq, D)
     bad = table.clone()
     bad[:, :3], bad[:, 9] = 10**6, -1
@@ -132,7 +140,7 @@ def test_rows_whose_first_tiles_count_nothing():
     check(q, kp, vp, bad, lens, o, lse)
     q = q.abs() + 2.0
     kp[table[0, :4].long()] = -INF
-    kp[table[0, 4:].long()] = -kp[table[0, 4:].long()].abs() - 20.0  # scores of some -500
+    kp[table[0, 4:prefix // page].long()] = -kp[table[0, 4:prefix // page].long()].abs() - 20.0  # scores of some -500
     o, lse = dash.attn_decode_shared(q, kp, vp, seen, i32([prefix, prefix]), prefix)
     ro, rl, mag = R.decode(q, kp, vp, table, [prefix, prefix], 1 / math.sqrt(D))
     # 32-bit scores of this size are off by 2^-24 x 64 roundings of their terms' magnitudes: 2e-3 in a weight's
@@ -140,16 +148,17 @@ def test_rows_whose_first_tiles_count_nothing():
     assert (lse.double() - rl).abs().max() <= 2e-3 * 1.5
     err = (o.double() - ro).abs()
     assert (err <= R.bound(ro, mag) + 4e-3 * mag).all()
-    kp[table[0, 4:].long()] = -INF
+    kp[table[0, 4:prefix // page].long()] = -INF
     o, lse = dash.attn_decode_shared(q, kp, vp, seen, i32([prefix, prefix]), prefix)
     assert not o.any() and (lse == -INF).all()
     dash.dash_sync_status()
 
 
-def test_nan_and_infinite_scores_reach_their_rows_alone():
+@both
+def test_nan_and_infinite_scores_reach_their_rows_alone(wide):
     prefix, hq, hkv, D, page = 700, 4, 2, 128, 16
     lens = [prefix, prefix + 5, 200]
-    kp, vp, table, seen = cache(lens, prefix, hkv, D, page)
+    kp, vp, table, seen = cache(lens, prefix, hkv, D, page, wide=wide)
     q = R.normal(6, 3, hq, D)
     good = dash.attn_decode_shared(q, kp, vp, seen, i32(lens), prefix)
     k1 = kp.clone()
@@ -169,14 +178,15 @@ def test_nan_and_infinite_scores_reach_their_rows_alone():
     dash.dash_sync_status()
 
 
-def test_strides_streams_and_two_calls_at_once():
+@both
+def test_strides_streams_and_two_calls_at_once(wide):
     prefix, hq, hkv, D, page = 1000, 8, 2, 64, 16
     lens = [prefix + n for n in (0, 5, 300)]
-    kp, vp, table, seen = cache(lens, prefix, hkv, D, page)
+    kp, vp, table, seen = cache(lens, prefix, hkv, D, page, wide=wide)
     q = R.normal(6, 3, hq, D)
     want = dash.attn_decode_shared(q, kp, vp, seen, i32(lens), prefix)
-    both = torch.full((kp.shape[0], 2, hkv, page, D), NAN, dtype=kp.dtype, device="cuda")
-    k2, v2 = both[:, 0].transpose(1, 2), both[:, 1].transpose(1, 2)
+    kv = torch.full((kp.shape[0], 2, hkv, page, D), NAN, dtype=kp.dtype, device="cuda")
+    k2, v2 = kv[:, 0].transpose(1, 2), kv[:, 1].transpose(1, 2)
     k2.copy_(kp)
     v2.copy_(vp)
     fused = torch.full((3, hq + 4, D), NAN, dtype=kp.dtype, device="cuda")
@@ -199,7 +209,8 @@ def test_strides_streams_and_two_calls_at_once():
     dash.dash_sync_status()
 
 
-def test_a_captured_first_call_and_large_offsets():
+@pytest.mark.parametrize("width", [4, 70])
+def test_a_captured_first_call_and_large_offsets(width):
     # a cache of more than 2^31 elements
     hq, hkv, D, page = 4, 4, 128, 64
     n_pages = (2**31 // (page * hkv * D)) + 40
@@ -208,14 +219,14 @@ def test_a_captured_first_call_and_large_offsets():
     pages = [n_pages - 1, 3, n_pages - 20, n_pages - 2]
     for i, p in enumerate(pages):
         kp[p], vp[p] = R.normal(100 + i, page, hkv, D), R.normal(200 + i, page, hkv, D)
-    q, table = R.normal(8, 2, hq, D), i32([pages, pages])
+    q, table = R.normal(8, 2, hq, D), i32([pages + [0] * (width - 4)] * 2)
     o, lse = dash.attn_decode_shared(q, kp, vp, table, i32([250, 210]), 200)
     dash.dash_sync_status()
     check(q, kp, vp, table, [250, 210], o, lse)
 
 
 def test_refusals():
-    kp, vp, table, seen = cache([40, 40], 32, 2, 64, 16)
+    kp, vp, table, seen = cache([40, 40], 32, 2, 64, 16, wide=True)
     q, n = R.normal(1, 2, 4, 64), i32([40, 40])
     f = dash.attn_decode_shared
     for bad in (lambda: f(q.float(), kp, vp, table, n, 32), lambda: f(q, kp, vp, table, n, -1),

@@ -36,7 +36,7 @@ def test_refusals_before_any_device_call():
     for prefix in (-1, 65, 2**31 - 1):
         assert call(prefix=prefix) == 1 and "does not fit" in dash.dash_last_error()
     for kw in ({"ws": nul}, {"ws": odd}, {"size": 64}):
-        assert call(**kw) == 1 and "workspace" in dash.dash_last_error()
+        assert call(width=300, **kw) == 1 and "workspace" in dash.dash_last_error()
     assert call(B=65000, hq=65000, hkv=1) == 2 and "rows on one" in dash.dash_last_error()
     for bad in ((2, 5, 2, 64, 16, 4, 20), (2, 4, 0, 64, 16, 4, 20), (2, 4, 2, 80, 16, 4, 20), (2, 4, 2, 64, 16, 4, 65),
                 (2, 4, 2, 64, 16, 4, -1), (-1, 4, 2, 64, 16, 4, 20), (2, 4, 2, 64, 16, 1 << 28, 20)):
