@@ -108,7 +108,7 @@ _SIGS = {
     "dash_cache_copy_fp8": ([_P] * 6 + [_I] * 5 + [_P, _P], _I),
     "dash_qk_norm_rope": ([_P] * 6 + [_I] + [_P] * 2 + [_L] + [_I] * 6 + [_F, _P, _P], _I),
     "dash_qk_norm_rope_bwd": ([_P] * 8 + [_I] + [_P] * 4 + [_L] + [_I] * 6 + [_F, _P, _P, _L, _P], _I),
-    "dash_norm_rope_workspace": ([_L, _I], _L),
+    "dash_norm_rope_workspace": ([_L, _I, _I, _I], _L),
     "dash_sync_status": ([_P], _I),
     "dash_release_workspace": ([], None),
     "dash_last_error": ([], ctypes.c_char_p),
@@ -891,8 +891,8 @@ def dash_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, rope, positions, e
 
 
 @functools.lru_cache(maxsize=64)
-def dash_norm_rope_workspace(rows: int, head_dim: int) -> int:
-    return int(lib().dash_norm_rope_workspace(rows, head_dim))
+def dash_norm_rope_workspace(rows: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().dash_norm_rope_workspace(rows, heads, kv_heads, head_dim))
 
 
 def _norm_bwd(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, sizes, eps,
@@ -1160,7 +1160,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, 
     dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
     dq_weight = torch.empty(dim, dtype=torch.float32, device=dev)
     dk_weight = torch.empty(dim, dtype=torch.float32, device=dev)
-    ws = torch.empty(max(0, dash_norm_rope_workspace(sizes[0], dim)), dtype=torch.uint8, device=dev)
+    ws = torch.empty(max(0, dash_norm_rope_workspace(*sizes[:4])), dtype=torch.uint8, device=dev)
     with _using(stream, q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, ws):
         _norm_bwd(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, rope, positions, sizes, eps,
                   pairs, ws, stream)

@@ -158,17 +158,19 @@ PyObject *qk_norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int64_t dim = x.q->size(2);
   const at::Tensor *gq = c.rows(a[2], x.q->size(0), x.q->size(1), dim),
                    *gk = c.rows(a[3], x.q->size(0), x.k->size(1), dim);
-  const int64_t need = dash_norm_rope_workspace(x.q->size(0), (int)dim);
+  const int64_t need = dash_norm_rope_workspace(x.q->size(0), (int)x.q->size(1), (int)x.k->size(1), (int)dim);
   if (!c.ok || need < 0) Py_RETURN_NONE;
   const at::Tensor dq = c.empty(x.q->sizes(), at::kBFloat16), dk = c.empty(x.k->sizes(), at::kBFloat16);
-  const at::Tensor wq = c.empty({dim}, at::kFloat), wk = c.empty({dim}, at::kFloat), ws = c.empty({need}, at::kByte);
+  const at::Tensor wq = c.empty({dim}, at::kFloat), wk = c.empty({dim}, at::kFloat);
+  at::Tensor ws;
+  if (need > 0) ws = c.empty({need}, at::kByte);
   Strides s;
   for (const at::Tensor *t : {x.q, x.k, gq, gk, &dq, &dk}) s.add(*t, 2);
   const int st = dash_qk_norm_rope_bwd(
       ptr(*x.q), ptr(*x.k), ptr(*gq), ptr(*gk), ptr(dq), ptr(dk), ptr(*x.wq), ptr(*x.wk),
       x.wq->scalar_type() == at::kFloat, ptr<float>(wq), ptr<float>(wk), ptr<float>(*x.rope),
       ptr<int32_t>(*x.positions), x.q->size(0), (int)x.q->size(1), (int)x.k->size(1), (int)dim, (int)x.rope->size(1),
-      (int)x.rope->size(0), x.pairs, (float)x.eps, s.v, ptr(ws), need, c.stream());
+      (int)x.rope->size(0), x.pairs, (float)x.eps, s.v, need > 0 ? ptr(ws) : nullptr, need, c.stream());
   return st ? failed(st) : tensors(dq, dk, wq, wk);
 }
 

@@ -10,9 +10,17 @@
 //
 // Bound by bytes: 2 + 2 a value forward, 4 + 2 backward.  A row is D / 8 lanes:
 // a lane holds both sides of four pairs (4 values at `a`, 4 at `b`, 8 bytes
-// each), so that the rotation needs no exchange and every lane reads the four
+// each), so that the rotation needs no exchange and every lane holds the four
 // cosines and sines that it needs, once for all heads of a row of the batch.
+// 16384 tokens of 16 + 4 heads of 128: 32.1 us forward and 48.1 us backward, 5.2
+// and 5.3 TB/s.  Next to the bytes stand the instructions (some 100 and 160 for
+// 32 lanes x 8 values): forward, loads of four steps straight into registers and
+// their arithmetic side by side beat a ring in shared memory (35.1 us); backward,
+// where registers hold the sums of dw too, the ring wins (53.3 us without it).
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "norm_rope.h"
 #include "packed.h"
@@ -25,8 +33,8 @@ using namespace dev;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;     // head rows that a lane has in flight, forward
-constexpr int kAheadBwd = 4;  // and backward (x and dz)
+constexpr int kAhead = 4;   // head rows that a lane has in flight, forward
+constexpr int kStages = 6;  // steps of a warp that are in flight, backward (4: the same, 8: 2 % slower)
 
 // Two 32-bit values; the arithmetic is one instruction for both.
 struct F2 {
@@ -81,8 +89,14 @@ struct Lane {
     }
   }
   __device__ __forceinline__ void load(const __nv_bfloat16 *row, uint2 (&w)[2]) const {
-    w[0] = *reinterpret_cast<const uint2 *>(row + lo);
-    w[1] = *reinterpret_cast<const uint2 *>(row + hi);
+    if (kPairs) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(row + lo);
+      w[0] = make_uint2(u.x, u.y);
+      w[1] = make_uint2(u.z, u.w);
+    } else {
+      w[0] = *reinterpret_cast<const uint2 *>(row + lo);
+      w[1] = *reinterpret_cast<const uint2 *>(row + hi);
+    }
   }
   static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -133,19 +147,15 @@ struct Lane {
     }
     return x;
   }
-  // Cosines (a) and sines (b) of a row's position; NaN, and a report, where it is outside the table.
-  __device__ __forceinline__ Eight angles(const NormRopeParams &p, long long row, int lane) const {
-    const int pos = p.positions[row];
-    const bool ok = pos >= 0 && pos < p.max_positions;
+  // Cosines (a) and sines (b) of a row, from its part of the table; NaN where its position is outside.
+  __device__ __forceinline__ Eight angles(const float *t, int rot, bool ok) const {
     Eight x;
     if (ok && angle >= 0) {
-      const float *t = p.rope + (long long)pos * p.rot + angle;
-      const float4 c = __ldg(reinterpret_cast<const float4 *>(t));
-      const float4 s = __ldg(reinterpret_cast<const float4 *>(t + p.rot / 2));
+      const float4 c = *reinterpret_cast<const float4 *>(t + angle);
+      const float4 s = *reinterpret_cast<const float4 *>(t + rot / 2 + angle);
       x.a[0] = f2(c.x, c.y), x.a[1] = f2(c.z, c.w);
       x.b[0] = f2(s.x, s.y), x.b[1] = f2(s.z, s.w);
     } else {
-      if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
       x.a[0] = x.a[1] = ok ? f2(1.f, 1.f) : f2(NAN, NAN);
       x.b[0] = x.b[1] = ok ? f2(0.f, 0.f) : f2(NAN, NAN);
     }
@@ -222,81 +232,211 @@ __global__ void __launch_bounds__(kThreads, 4) dash_norm_rope_kernel(const __gri
   const L l(lane, p.rot);
   const int q_steps = (p.t[0].heads + L::kRows - 1) / L::kRows, k_steps = (p.t[1].heads + L::kRows - 1) / L::kRows;
   const int end = min(first + p.passes, q_steps + k_steps);
-  const Eight angle = l.angles(p, at_row, lane);
+  const int pos = p.positions[at_row];
+  const bool ok = pos >= 0 && pos < p.max_positions;
+  if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
+  const Eight angle = l.angles(p.rope + (ok ? (long long)pos * p.rot : 0), p.rot, ok);
   if (first < q_steps) norm_heads(p, l, 0, at_row, angle, lane, first, min(end, q_steps));
   if (end > q_steps) norm_heads(p, l, 1, at_row, angle, lane, max(first - q_steps, 0), end - q_steps);
 }
 
-// A warp takes rows of the batch in turn and keeps its sums of dw in registers.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: fills with zeros, reads nothing
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// A warp's steps: a step is 512 bytes of head rows of one row of the batch (the
+// queries' steps, then the keys'), and a warp takes a run of them.  They come
+// through a ring in shared memory, up to kStages ahead; a row's angles come with
+// its first step.
+template <int D, bool kPairs>
+struct Steps {
+  using L = Lane<D, kPairs>;
+  static constexpr uint32_t kDz = 512, kAngles = 1024, kStage = 1536;
+  static constexpr uint32_t kWarpBytes = kStages * kStage + 16 * ((kStages + 3) / 4);  // and whether they are in the table
+
+  const NormRopeParams &p;
+  uint8_t *ring;
+  int *ok;
+  int lane, sub, q_steps, steps;
+  // the place of the next step to be asked for, and of the one at hand
+  long long to_ask;
+  int ask_row, ask_s, ask_slot = 0, row, s, slot = 0, next_pos;
+  bool ask_angles = true, fresh = true;
+  const __nv_bfloat16 *x = nullptr, *dz = nullptr;
+
+  __device__ __forceinline__ Steps(const NormRopeParams &p_, uint8_t *smem, int warp, int lane_, long long first,
+                                   long long n)
+      : p(p_), ring(smem + warp * kWarpBytes), ok(reinterpret_cast<int *>(ring + kStages * kStage)), lane(lane_),
+        sub(lane_ / L::kLanes), to_ask(n) {
+    q_steps = (p.t[0].heads + L::kRows - 1) / L::kRows;
+    steps = q_steps + (p.t[1].heads + L::kRows - 1) / L::kRows;
+    ask_row = row = (int)(first / steps);
+    ask_s = s = (int)(first - (long long)row * steps);
+    if (n > 0) next_pos = p.positions[row];
+  }
+  __device__ __forceinline__ void ask() {
+    if (to_ask > 0) {
+      --to_ask;
+      const bool k = ask_s >= q_steps;
+      const NormRopeTensor &t = p.t[k];
+      const int h = (k ? ask_s - q_steps : ask_s) * L::kRows + sub;
+      if (ask_angles || ask_s == q_steps) {
+        const int c = (lane % L::kLanes) * 8;
+        x = t.x + ask_row * t.x_row + h * t.x_head + c;
+        dz = t.dz + ask_row * t.dz_row + h * t.dz_head + c;
+      }
+      const uint32_t at = smem_u32(ring) + ask_slot * kStage;
+      const bool real = h < t.heads;  // else the address is not looked at
+      cp16(at + lane * 16, x, real);
+      cp16(at + kDz + lane * 16, dz, real);
+      x += L::kRows * t.x_head;
+      dz += L::kRows * t.dz_head;
+      if (ask_angles) {
+        const int pos = next_pos;
+        const bool in = pos >= 0 && pos < p.max_positions;
+        if (lane * 4 < p.rot) cp16(at + kAngles + lane * 16, p.rope + (in ? (long long)pos * p.rot + lane * 4 : 0), in);
+        if (lane == 0) {
+          ok[ask_slot] = in;
+          if (!in) atomicCAS(p.status, 0, kStatusBadPosition);
+        }
+        if (ask_row + 1 < p.rows) next_pos = p.positions[ask_row + 1];
+      }
+      ask_angles = ++ask_s == steps;
+      if (ask_angles) {
+        ask_s = 0;
+        ++ask_row;
+      }
+      if (++ask_slot == kStages) ask_slot = 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void begin() {
+#pragma unroll
+    for (int i = 0; i < kStages - 2; ++i) ask();
+  }
+  // The next kN steps have come.
+  template <int kN>
+  __device__ __forceinline__ void take() {
+    static_assert(kN <= 2, "two steps more than the ring was filled to");
+#pragma unroll
+    for (int i = 0; i < kN; ++i) ask();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();
+  }
+  __device__ __forceinline__ const uint8_t *stage(int i) const {
+    const int at = slot + i;
+    return ring + (at < kStages ? at : at - kStages) * kStage;
+  }
+  __device__ __forceinline__ void done(int n) {
+    __syncwarp();  // every lane has read the stages
+    slot += n;
+    if (slot >= kStages) slot -= kStages;
+    s += n;
+    fresh = s == steps;
+    if (fresh) {
+      s = 0;
+      ++row;
+    }
+  }
+  __device__ __forceinline__ const __nv_bfloat16 *head_row(const uint8_t *stage) const {
+    return reinterpret_cast<const __nv_bfloat16 *>(stage) + sub * D;
+  }
+};
+
+// The steps of warp `w`: p.per_warp each.
+__device__ __forceinline__ long long first_step(const NormRopeParams &p, long long w, long long *n) {
+  const long long first = w * p.per_warp, left = p.steps - first;
+  *n = left < 0 ? 0 : left < p.per_warp ? left : p.per_warp;
+  return first;
+}
+
+// A warp keeps its sums of dw in registers, the CTA's go to its part.
 template <int D, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 2) dash_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   using L = Lane<D, kPairs>;
   constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint8_t smem[];
   // the sum of the parts may be set up now; it waits for this grid's end before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L::kLanes;
+  long long n;
+  const long long first = first_step(p, (long long)blockIdx.x * kWarps + warp, &n);
   const L l(lane, p.rot);
-  Eight w[2], dw[2];
+  Steps<D, kPairs> steps(p, smem, warp, lane, first, n);
+  steps.begin();
+  Eight w[2], dw[2], angle;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     w[which] = l.weight(p, which);
 #pragma unroll
     for (int i = 0; i < 2; ++i) dw[which].a[i] = dw[which].b[i] = f2(0.f, 0.f);
   }
-  for (long long row = (long long)blockIdx.x * kWarps + warp; row < p.rows; row += (long long)gridDim.x * kWarps) {
-    const Eight angle = l.angles(p, row, lane);
-    F2 minus[2];
+  F2 minus[2];
+  __nv_bfloat16 *out = nullptr;
+  // kN steps of the queries or of the keys
+  auto step = [&](auto key, auto count) {
+    constexpr int which = decltype(key)::value, kN = decltype(count)::value;
+    const NormRopeTensor &t = p.t[which];
+    steps.template take<kN>();
+    const int s = which ? steps.s - steps.q_steps : steps.s, h = s * L::kRows + sub;
+    if (steps.fresh) {
+      angle = l.angles(reinterpret_cast<const float *>(steps.stage(0) + steps.kAngles), p.rot, steps.ok[steps.slot]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) minus[i] = -angle.b[i];
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const NormRopeTensor &t = p.t[which];
-      const __nv_bfloat16 *xs = t.x + row * t.x_row + sub * t.x_head, *zs = t.dz + row * t.dz_row + sub * t.dz_head;
-      __nv_bfloat16 *out = t.out + row * t.out_row + sub * t.out_head;
-      for (int h0 = 0; h0 < t.heads; h0 += kAheadBwd * L::kRows) {
-        uint2 xw[kAheadBwd][2], zw[kAheadBwd][2];
-#pragma unroll
-        for (int u = 0; u < kAheadBwd; ++u) {
-          xw[u][0] = xw[u][1] = zw[u][0] = zw[u][1] = make_uint2(0u, 0u);
-          if (h0 + u * L::kRows + sub < t.heads) {
-            l.load(xs + (h0 + u * L::kRows) * t.x_head, xw[u]);
-            l.load(zs + (h0 + u * L::kRows) * t.dz_head, zw[u]);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kAheadBwd; ++u) {
-          if (h0 + u * L::kRows >= t.heads) break;
-          const Eight x = L::widen(xw[u]), z = L::widen(zw[u]);
-          Eight g, gw;
-          F2 sq = f2(0.f, 0.f), dot = f2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            g.a[i] = fma(z.a[i], angle.a[i], z.b[i] * angle.b[i]);
-            g.b[i] = fma(z.b[i], angle.a[i], z.a[i] * minus[i]);
-            gw.a[i] = g.a[i] * w[which].a[i];
-            gw.b[i] = g.b[i] * w[which].b[i];
-            sq = fma(x.a[i], x.a[i], sq);
-            sq = fma(x.b[i], x.b[i], sq);
-            dot = fma(gw.a[i], x.a[i], dot);
-            dot = fma(gw.b[i], x.b[i], dot);
-          }
-          // lanes past the last head hold zeros: their r is 0, so that they add nothing to dw whatever eps is
-          const bool real = h0 + u * L::kRows + sub < t.heads;
-          const float var = L::sum(sq) * (1.f / D) + p.eps, r = real ? rsqrtf(var) : 0.f;
-          const float m = -(L::sum(dot) * (1.f / D) * r * r * r);
-          const F2 rr = f2(r, r), mm = f2(m, m);
-          Eight d;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            d.a[i] = fma(gw.a[i], rr, x.a[i] * mm);
-            d.b[i] = fma(gw.b[i], rr, x.b[i] * mm);
-            dw[which].a[i] = fma(g.a[i], x.a[i] * rr, dw[which].a[i]);
-            dw[which].b[i] = fma(g.b[i], x.b[i] * rr, dw[which].b[i]);
-          }
-          if (real) l.store(out + (h0 + u * L::kRows) * t.out_head, d);
-        }
-      }
+      for (int i = 0; i < 2; ++i) minus[i] = -angle.b[i];
     }
+    if (steps.fresh || s == 0) out = t.out + steps.row * t.out_row + h * t.out_head;
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+      uint2 xw[2], zw[2];
+      l.load(steps.head_row(steps.stage(u)), xw);
+      l.load(steps.head_row(steps.stage(u) + steps.kDz), zw);
+      const Eight x = L::widen(xw), z = L::widen(zw);
+      Eight g, gw;
+      F2 sq = f2(0.f, 0.f), dot = f2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        g.a[i] = fma(z.a[i], angle.a[i], z.b[i] * angle.b[i]);
+        g.b[i] = fma(z.b[i], angle.a[i], z.a[i] * minus[i]);
+        gw.a[i] = g.a[i] * w[which].a[i];
+        gw.b[i] = g.b[i] * w[which].b[i];
+        sq = fma(x.a[i], x.a[i], sq);
+        sq = fma(x.b[i], x.b[i], sq);
+        dot = fma(gw.a[i], x.a[i], dot);
+        dot = fma(gw.b[i], x.b[i], dot);
+      }
+      // lanes past the last head hold zeros: their r is 0, so that they add nothing to dw whatever eps is
+      const bool real = h + u * L::kRows < t.heads;
+      const float var = L::sum(sq) * (1.f / D) + p.eps, r = real ? rsqrtf(var) : 0.f;
+      const float m = -(L::sum(dot) * (1.f / D) * r * r * r);
+      const F2 rr = f2(r, r), mm = f2(m, m);
+      Eight d;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        d.a[i] = fma(gw.a[i], rr, x.a[i] * mm);
+        d.b[i] = fma(gw.b[i], rr, x.b[i] * mm);
+        dw[which].a[i] = fma(g.a[i], x.a[i] * rr, dw[which].a[i]);
+        dw[which].b[i] = fma(g.b[i], x.b[i] * rr, dw[which].b[i]);
+      }
+      if (real) l.store(out, d);
+      out += L::kRows * t.out_head;
+    }
+    steps.done(kN);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  using Q = std::integral_constant<int, 0>;
+  using K = One;
+  while (n > 0) {
+    const bool q = steps.s < steps.q_steps, two = n > 1 && steps.s + 2 <= (q ? steps.q_steps : steps.steps);
+    if (q) {
+      if (two) step(Q(), Two());
+      else step(Q(), One());
+    } else {
+      if (two) step(K(), Two());
+      else step(K(), One());
+    }
+    n -= two ? 2 : 1;
   }
   // the CTA's sums: lanes that hold the same values, then warps, in their order
   __shared__ float s_dw[kWarps][2][D];
@@ -317,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_norm_rope_bwd_kernel(const _
       }
     }
   __syncthreads();
-  for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+  for (int x = threadIdx.x; x < 2 * D; x += kWarps * 32) {
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += (&s_dw[w][0][0])[x];
@@ -361,20 +501,30 @@ cudaError_t launch_fwd(NormRopeParams &p, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t launch_bwd(const NormRopeParams &p, cudaStream_t stream) {
-  const int ctas = norm_bwd_ctas(p.rows);  // 0 without rows: dw is then a sum of nothing
-  cudaError_t e = ctas == 0 ? cudaSuccess : launch(p.pairs ? dash_norm_rope_bwd_kernel<D, true> : dash_norm_rope_bwd_kernel<D, false>, ctas,
-                         kThreads, 0, stream, nullptr, p);
-  if (e != cudaSuccess) return e;
+constexpr int kSmemBwd = kThreads / 32 * (int)Steps<D, false>::kWarpBytes;
+
+template <int D>
+cudaError_t launch_bwd(NormRopeParams &p, cudaStream_t stream) {
+  p.steps = norm_steps(p.rows, p.t[0].heads, p.t[1].heads, D);
+  const int ctas = norm_bwd_ctas(p.steps);  // 0 without rows: dw is then a sum of nothing
+  if (ctas > 0) {
+    const long long warps = (long long)ctas * (kThreads / 32);
+    p.per_warp = (p.steps + warps - 1) / warps;
+    const cudaError_t e = launch(p.pairs ? dash_norm_rope_bwd_kernel<D, true> : dash_norm_rope_bwd_kernel<D, false>,
+                                 ctas, kThreads, kSmemBwd<D>, stream, nullptr, p);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr = overlap_attr();
   return launch(dash_norm_rope_sum_kernel, 2 * D / 8, 256, 0, stream, &attr, p, ctas);
 }
 
 template <int D>
 cudaError_t prepare_t() {
-  cudaFuncAttributes fa;
-  for (auto kernel : {dash_norm_rope_kernel<D, true>, dash_norm_rope_kernel<D, false>,
-                      dash_norm_rope_bwd_kernel<D, true>, dash_norm_rope_bwd_kernel<D, false>})
+  for (auto kernel : {dash_norm_rope_bwd_kernel<D, true>, dash_norm_rope_bwd_kernel<D, false>})
+    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBwd<D>))
+      return e;
+  cudaFuncAttributes fa;  // loads the others
+  for (auto kernel : {dash_norm_rope_kernel<D, true>, dash_norm_rope_kernel<D, false>})
     if (const cudaError_t e = cudaFuncGetAttributes(&fa, kernel)) return e;
   return cudaFuncGetAttributes(&fa, dash_norm_rope_sum_kernel);
 }

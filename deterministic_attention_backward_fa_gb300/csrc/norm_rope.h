@@ -24,16 +24,24 @@ struct NormRopeParams {
   float *parts;                // backward: [CTA][2][D], the weights' gradients of the CTA's rows
   long long rows;
   int D, rot, max_positions;
-  int blocks, passes;          // a row's heads are dealt to `blocks` warps, `passes` steps each
+  int blocks, passes;          // forward: a row's heads are dealt to `blocks` warps, `passes` steps each
+  long long steps, per_warp;   // backward: of the call, of a warp
   bool weight32, pairs;
   float eps;
   int *status;
 };
 
+// Steps of a call: 512 bytes of a row's queries or of its keys each.
+inline long long norm_steps(long long rows, int Hq, int Hkv, int D) {
+  const int n = 256 / D;
+  return rows * ((Hq + n - 1) / n + (Hkv + n - 1) / n);
+}
 // CTAs of a backward: a number of its own for each size, whatever the GPU, so
 // that the weights' gradients are the same sums everywhere.
 constexpr int kNormBwdCtas = 304;
-inline int norm_bwd_ctas(long long rows) { return rows < 8LL * kNormBwdCtas ? (int)((rows + 7) / 8) : kNormBwdCtas; }
+inline int norm_bwd_ctas(long long steps) {
+  return steps < 8LL * kNormBwdCtas ? (int)((steps + 7) / 8) : kNormBwdCtas;
+}
 
 cudaError_t prepare_norm_rope();
 cudaError_t launch_norm_rope(NormRopeParams p, cudaStream_t stream);

@@ -84,9 +84,9 @@ dash_status_t dash_qk_norm_rope(const void *q, const void *k, void *q_out, void 
   return e == cudaSuccess ? DASH_OK : cuda_error(e, "norm launch");
 }
 
-long long dash_norm_rope_workspace(long long rows, int D) {
-  if (rows < 0 || (D != 64 && D != 128)) return -1;
-  return (long long)dash::norm_bwd_ctas(rows) * 2 * D * 4;
+long long dash_norm_rope_workspace(long long rows, int Hq, int Hkv, int D) {
+  if (rows < 0 || rows > INT32_MAX || Hq < 1 || Hkv < 1 || Hq > 65535 || Hkv > 65535 || (D != 64 && D != 128)) return -1;
+  return (long long)dash::norm_bwd_ctas(dash::norm_steps(rows, Hq, Hkv, D)) * 2 * D * 4;
 }
 
 dash_status_t dash_qk_norm_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq,
@@ -115,7 +115,7 @@ dash_status_t dash_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
     t.dz = static_cast<const __nv_bfloat16 *>(dz[i]);
     t.out = static_cast<__nv_bfloat16 *>(out[i]);
   }
-  const long long need = dash_norm_rope_workspace(rows, D);
+  const long long need = dash_norm_rope_workspace(rows, Hq, Hkv, D);
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || workspace_bytes < need))
     return report(DASH_ERR_INVALID_ARG, "the workspace must hold %lld bytes, 16-byte aligned", need);
   p.parts = static_cast<float *>(workspace);

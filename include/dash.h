@@ -674,7 +674,7 @@ dash_status_t dash_qk_norm_rope_bwd(const void *q, const void *k, const void *dq
                                     long long rows, int Hq, int Hkv, int D, int rot, int max_positions, int pairs,
                                     float eps, const int64_t *strides, void *workspace, long long workspace_bytes,
                                     dash_stream_t stream);
-long long dash_norm_rope_workspace(long long rows, int D);
+long long dash_norm_rope_workspace(long long rows, int Hq, int Hkv, int D);
 
 /* Synchronises `stream` and returns the device status of the calling
  * thread's current device workspace for that stream: DASH_OK, or

@@ -49,7 +49,8 @@ def check(parts, grads, w, rope, positions, eps, pairs, z, back):
 
 
 CASES = [(1, 1, 1, 64, 64), (3, 4, 2, 128, 128), (37, 5, 1, 128, 32), (1, 32, 8, 128, 128), (64, 16, 4, 64, 48),
-         (300, 3, 3, 64, 8), (19, 40, 40, 128, 120), (2, 1, 7, 64, 16)]
+         (300, 3, 3, 64, 8), (19, 40, 40, 128, 120), (2, 1, 7, 64, 16),
+         (700, 5, 2, 128, 64), (4000, 3, 1, 64, 32), (3, 1000, 30, 128, 128)]
 
 
 @pytest.mark.parametrize("pairs", [False, True])
@@ -96,7 +97,7 @@ def test_in_place_and_heads_first():
     want = dash.qk_norm_rope(*parts, *w, rope, positions)
     wback = dash.qk_norm_rope_bwd(*parts, *grads, *w, rope, positions)
     # gradients first, over their inputs, then the rows themselves
-    ws = torch.empty(dash.dash_norm_rope_workspace(50, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(dash.dash_norm_rope_workspace(50, 6, 2, 128), dtype=torch.uint8, device="cuda")
     dws = [torch.empty(128, device="cuda") for _ in range(2)]
     dash.dash_qk_norm_rope_bwd(*parts, *grads, *grads, *w, *dws, rope, positions, 1e-6, ws)
     dash.dash_qk_norm_rope(*parts, *parts, *w, rope, positions, 1e-6)

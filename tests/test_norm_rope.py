@@ -69,12 +69,13 @@ def test_refusals_before_any_device_call():
         if not bwd:
             assert norm(bwd, rows=0, ptr=nul, positions=nul) == 0
     for kw in ({"ws": nul}, {"ws": odd}, {"size": 100}):
-        assert norm(True, **kw) == 1 and "workspace" in dash.dash_last_error()
+        assert norm(True, rows=100, **kw) == 1 and "workspace" in dash.dash_last_error()
     assert norm(True, dw=nul) == 1 and "dq_weight" in dash.dash_last_error()
-    assert dash.dash_norm_rope_workspace(-1, 64) == -1 == dash.dash_norm_rope_workspace(5, 80)
+    need = dash.dash_norm_rope_workspace
+    assert {need(-1, 4, 2, 64), need(2**31, 4, 2, 64), need(5, 4, 2, 80), need(5, 0, 2, 64), need(5, 4, 70000, 64)} == {-1}
     # a few rows need few parts, many rows a bounded number
-    assert 0 == dash.dash_norm_rope_workspace(0, 64) < dash.dash_norm_rope_workspace(1, 64)
-    assert dash.dash_norm_rope_workspace(10**6, 128) == dash.dash_norm_rope_workspace(10**9, 128) < 1 << 20
+    assert 0 == need(0, 4, 2, 64) < need(1, 4, 2, 64) < need(100, 4, 2, 64) < need(100, 400, 2, 64)
+    assert need(10**6, 8, 2, 128) == need(10**9, 8, 2, 128) < 1 << 20
 
 
 def test_binding_refuses_wrong_tensors():
