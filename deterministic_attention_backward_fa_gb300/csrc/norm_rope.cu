@@ -12,10 +12,10 @@
 // a lane holds both sides of four pairs (4 values at `a`, 4 at `b`, 8 bytes
 // each), so that the rotation needs no exchange and every lane holds the four
 // cosines and sines that it needs, once for all heads of a row of the batch.
-// 16384 tokens of 16 + 4 heads of 128: 32.1 us forward and 48.1 us backward, 5.2
+// 16384 tokens of 16 + 4 heads of 128: 31.4 us forward and 48.1 us backward, 5.4
 // and 5.3 TB/s.  Next to the bytes stand the instructions (some 100 and 160 for
-// 32 lanes x 8 values): forward, loads of four steps straight into registers and
-// their arithmetic side by side beat a ring in shared memory (35.1 us); backward,
+// 32 lanes x 8 values): forward, loads straight into registers and two steps'
+// arithmetic side by side beat a ring in shared memory (35.1 us); backward,
 // where registers hold the sums of dw too, the ring wins (53.3 us without it).
 #include <cuda_runtime.h>
 
@@ -33,7 +33,7 @@ using namespace dev;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;   // head rows that a lane has in flight, forward
+constexpr int kAhead = 2;   // steps that a lane has in flight beside those at hand, forward (4 on 3 CTAs of an SM: the same)
 constexpr int kStages = 6;  // steps of a warp that are in flight, backward (4: the same, 8: 2 % slower)
 
 // Two 32-bit values; the arithmetic is one instruction for both.
@@ -170,37 +170,63 @@ struct Lane {
   }
 };
 
-// Steps first .. end - 1 of a tensor's heads for one row of the batch, with
-// w cos, w sin made once: z_a = r (x_a (w_a cos) - x_b (w_b sin)) and so on.
+// A warp takes one row of the batch and `passes` steps of its heads, the queries'
+// first, kAhead at a time; the next ones' loads are under way by then.  w cos
+// and w sin are made once for the queries and once for the keys:
+// z_a = r (x_a (w_a cos) - x_b (w_b sin)) and so on.
 template <int D, bool kPairs>
-__device__ __forceinline__ void norm_heads(const NormRopeParams &p, const Lane<D, kPairs> &l, int which, long long row,
-                                           const Eight &angle, int lane, int first, int end) {
+__global__ void __launch_bounds__(kThreads, 4) dash_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   using L = Lane<D, kPairs>;
-  const NormRopeTensor &t = p.t[which];
-  const int sub = lane / L::kLanes;
-  const __nv_bfloat16 *in = t.x + row * t.x_row + (first * L::kRows + sub) * t.x_head;
-  __nv_bfloat16 *out = t.out + row * t.out_row + (first * L::kRows + sub) * t.out_head;
-  const long long in_step = L::kRows * t.x_head, out_step = L::kRows * t.out_head;
-  F2 ac[2], bs[2], bc[2], as[2];
-  const Eight w = l.weight(p, which);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    ac[i] = w.a[i] * angle.a[i];
-    bs[i] = -(w.b[i] * angle.b[i]);
-    bc[i] = w.b[i] * angle.a[i];
-    as[i] = w.a[i] * angle.b[i];
-  }
-  for (int s0 = first; s0 < end; s0 += kAhead) {
-    uint2 x[kAhead][2];
+  const int lane = threadIdx.x & 31, sub = lane / L::kLanes;
+  const unsigned item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // below 2^31: many rows are a warp each
+  const unsigned row = item / (unsigned)p.blocks;
+  if (row >= p.rows) return;
+  const int pos = p.positions[row];
+  const int q_steps = (p.t[0].heads + L::kRows - 1) / L::kRows, k_steps = (p.t[1].heads + L::kRows - 1) / L::kRows;
+  const int first = (int)(item - row * p.blocks) * p.passes, end = min(first + p.passes, q_steps + k_steps);
+  const L l(lane, p.rot);
+  // steps s .. of one tensor
+  auto load = [&](int s, uint2 (&x)[kAhead][2]) {
+    const bool k = s >= q_steps;
+    const NormRopeTensor &t = p.t[k];
+    int h = (k ? s - q_steps : s) * L::kRows + sub;
+    const __nv_bfloat16 *in = t.x + row * t.x_row + h * t.x_head;
+    const long long by = L::kRows * t.x_head;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       x[u][0] = x[u][1] = make_uint2(0u, 0u);
-      if (s0 + u < end && (s0 + u) * L::kRows + sub < t.heads) l.load(in + u * in_step, x[u]);
+      if (s + u < end && h < t.heads) l.load(in, x[u]);
+      in += by;
+      h += L::kRows;
     }
-    in += kAhead * in_step;
+  };
+  uint2 x[kAhead][2], ahead[kAhead][2];
+  load(first, x);
+  const bool ok = pos >= 0 && pos < p.max_positions;
+  if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
+  const Eight angle = l.angles(p.rope + (ok ? (long long)pos * p.rot : 0), p.rot, ok);
+  F2 ac[2], bs[2], bc[2], as[2];
+  for (int s = first, next; s < end; s = next) {
+    const bool k = s >= q_steps;
+    const NormRopeTensor &t = p.t[k];
+    next = min(s + kAhead, k ? end : min(end, q_steps));
+    if (next < end) load(next, ahead);
+    if (s == first || s == q_steps) {
+      const Eight w = l.weight(p, k);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ac[i] = w.a[i] * angle.a[i];
+        bs[i] = -(w.b[i] * angle.b[i]);
+        bc[i] = w.b[i] * angle.a[i];
+        as[i] = w.a[i] * angle.b[i];
+      }
+    }
+    int h = (k ? s - q_steps : s) * L::kRows + sub;
+    __nv_bfloat16 *out = t.out + row * t.out_row + h * t.out_head;
+    const long long by = L::kRows * t.out_head;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (s0 + u >= end) break;
+      if (s + u >= next) break;
       const Eight v = L::widen(x[u]);
       F2 sq = v.a[0] * v.a[0];
       sq = fma(v.a[1], v.a[1], sq);
@@ -214,30 +240,16 @@ __device__ __forceinline__ void norm_heads(const NormRopeParams &p, const Lane<D
         z.a[i] = rr * fma(v.a[i], ac[i], v.b[i] * bs[i]);
         z.b[i] = rr * fma(v.b[i], bc[i], v.a[i] * as[i]);
       }
-      if ((s0 + u) * L::kRows + sub < t.heads) l.store(out, z);
-      out += out_step;
+      if (h < t.heads) l.store(out, z);
+      out += by;
+      h += L::kRows;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      x[u][0] = ahead[u][0];
+      x[u][1] = ahead[u][1];
     }
   }
-}
-
-// A warp takes one row of the batch and `passes` steps of its heads, the queries' first.
-template <int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 4) dash_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  using L = Lane<D, kPairs>;
-  const int lane = threadIdx.x & 31;
-  const unsigned item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // below 2^31: many rows are a warp each
-  const unsigned at_row = item / (unsigned)p.blocks;
-  if (at_row >= p.rows) return;
-  const int first = (int)(item - at_row * p.blocks) * p.passes;
-  const L l(lane, p.rot);
-  const int q_steps = (p.t[0].heads + L::kRows - 1) / L::kRows, k_steps = (p.t[1].heads + L::kRows - 1) / L::kRows;
-  const int end = min(first + p.passes, q_steps + k_steps);
-  const int pos = p.positions[at_row];
-  const bool ok = pos >= 0 && pos < p.max_positions;
-  if (!ok && lane == 0) atomicCAS(p.status, 0, kStatusBadPosition);
-  const Eight angle = l.angles(p.rope + (ok ? (long long)pos * p.rot : 0), p.rot, ok);
-  if (first < q_steps) norm_heads(p, l, 0, at_row, angle, lane, first, min(end, q_steps));
-  if (end > q_steps) norm_heads(p, l, 1, at_row, angle, lane, max(first - q_steps, 0), end - q_steps);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
