@@ -78,89 +78,72 @@ __device__ __forceinline__ Place place_of(const Cache8RowsParams &p, int t, int 
   return at;
 }
 
-// A warp takes a token and `passes` steps of its heads, K's rows and V's: D / 8
-// lanes a row, 8 values a lane.
+// A warp takes a token and `passes` steps of its rows, K's heads and then V's:
+// D / 16 lanes a row, 8 values of each half a lane, as what is done once for a
+// row weighs (with 8 values a lane the write of 16384 tokens of 8 heads of 128
+// takes 22.0 us instead of 20.0).  A write is 3 (+ 4 / D) bytes a value, and so is a
+// read: 4.9 TB/s both, where adding 1 to as many bytes gets 6.2.  What is missing
+// is the look-up before a token's rows can be placed (sequence, start, page: each
+// waits for the one before).  Runs of 2 to 4 tokens, looked up at once, are no
+// faster (22.6 and 21.0 us): fewer warps then wait for more rows each.
 struct Item8 {
   int t, first, end;
 };
 template <int D>
 __device__ __forceinline__ Item8 item_of(const Cache8RowsParams &p) {
+  constexpr int kRows = 32 / (D / 16);
   const unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5), t = item / (unsigned)p.blocks;
   const int first = (int)(item - t * p.blocks) * p.passes;
-  return {(int)t, first, min(first + p.passes, (p.heads * D / 8 + 31) / 32)};
+  return {(int)t, first, min(first + p.passes, (2 * p.heads + kRows - 1) / kRows)};
 }
-constexpr int kRowsAhead = 4;  // rows of K and of V that a lane has in flight
+constexpr int kRowsAhead = 2;  // rows that a lane has in flight (4 on 4 CTAs of an SM 21.9, 1 on 6 of them 21.6)
 
-// The lane's place in the rows of K or of V: the packed one, the codes, the scale;
-// `step` of each to the rows of the next step.
-struct Rows8 {
-  __nv_bfloat16 *x;
-  uint8_t *codes;
-  float *scale;
-  long long x_step, codes_step, scale_step;
+// A row of K or of V: the packed one, its codes, its scale.
+struct Row8 {
+  bool is_v;
+  int head;  // -1: there is none
 };
-template <int D>
-__device__ __forceinline__ Rows8 rows_of8(const Cache8RowsParams &p, bool is_v, int t, int row, int e) {
-  Rows8 r;
-  constexpr int kRows = 256 / D;
-  const long long head = is_v ? p.v_head : p.k_head;
-  const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
-  r.x = (is_v ? p.v + t * p.v_row : p.k + t * p.k_row) + row * head + e;
-  r.codes = (is_v ? p.c.v : p.c.k) + row * st.head + e;
-  r.scale = (is_v ? p.c.v_scale : p.c.k_scale) + row * ss.head;
-  r.x_step = kRows * head;
-  r.codes_step = kRows * st.head;
-  r.scale_step = kRows * ss.head;
-  return r;
+__device__ __forceinline__ Row8 row_of8(const Cache8RowsParams &p, int r) {
+  return {r >= p.heads, r < p.heads ? r : r < 2 * p.heads ? r - p.heads : -1};
 }
-__device__ __forceinline__ void place_rows(Rows8 &r, const CacheStrides &st, const CacheStrides &ss, Place at) {
-  r.codes += at.page * st.page + at.off * st.token;
-  r.scale += at.page * ss.page + at.off * ss.token;
+__device__ __forceinline__ __nv_bfloat16 *packed_row(const Cache8RowsParams &p, int t, Row8 r) {
+  return r.is_v ? p.v + t * p.v_row + r.head * p.v_head : p.k + t * p.k_row + r.head * p.k_head;
 }
-
-template <int D>
-__device__ __forceinline__ void quantise_row(uint4 x, uint8_t *codes, float *scale, bool first, bool real) {
-  constexpr int kLanes = D / 8;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  // magnitudes in order are bits in order, infinities and NaN above all others
-  const uint32_t both = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                 __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-  uint32_t top = max(both & 0xffffu, both >> 16);
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const bool finite = top < 0x7f80u;
-  const int f = finite ? scale_field(top) : 1;
-  const float inv = finite ? pow2_field(254 - f) : 0.f;
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
-  uint2 two = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-  if (!finite) two = make_uint2(0u, 0u);
-  if (!real) return;
-  *reinterpret_cast<uint2 *>(codes) = two;
-  if (first) *scale = finite ? pow2_field(f) : NAN;
+// Where a token's rows begin.
+struct Base8 {
+  uint8_t *codes[2];
+  float *scale[2];
+};
+__device__ __forceinline__ Base8 base_of(const Cache8 &c, Place at) {
+  return {{c.k + at.page * c.ks.page + at.off * c.ks.token, c.v + at.page * c.vs.page + at.off * c.vs.token},
+          {c.k_scale + at.page * c.kss.page + at.off * c.kss.token, c.v_scale + at.page * c.vss.page + at.off * c.vss.token}};
+}
+__device__ __forceinline__ uint8_t *codes_of(const Cache8 &c, const Base8 &b, Row8 r) {
+  return (r.is_v ? b.codes[1] : b.codes[0]) + r.head * (r.is_v ? c.vs.head : c.ks.head);
+}
+__device__ __forceinline__ float *scale_of(const Cache8 &c, const Base8 &b, Row8 r) {
+  return (r.is_v ? b.scale[1] : b.scale[0]) + r.head * (r.is_v ? c.vss.head : c.kss.head);
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) dash_cache8_write_kernel(const __grid_constant__ Cache8RowsParams p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+__global__ void __launch_bounds__(256, 5) dash_cache8_write_kernel(const __grid_constant__ Cache8RowsParams p) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31, e = (lane % kLanes) * 8;
   const Item8 it = item_of<D>(p);
   if (it.t >= p.n_tokens) return;
-  int row = it.first * kRows + lane / kLanes;
-  Rows8 k = rows_of8<D>(p, false, it.t, row, e), v = rows_of8<D>(p, true, it.t, row, e);
-  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, row += kRowsAhead * kRows) {
-    uint4 kx[kRowsAhead], vx[kRowsAhead];
+  int r = it.first * kRows + lane / kLanes;
+  Base8 base;
+  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, r += kRowsAhead * kRows) {
+    uint4 x[kRowsAhead][2];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      kx[u] = vx[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (s0 + u < it.end && row + u * kRows < p.heads) {
-        kx[u] = *reinterpret_cast<const uint4 *>(k.x);
-        vx[u] = *reinterpret_cast<const uint4 *>(v.x);
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      const Row8 row = row_of8(p, r + u * kRows);
+      if (s0 + u < it.end && row.head >= 0) {
+        const __nv_bfloat16 *from = packed_row(p, it.t, row) + e;
+        x[u][0] = *reinterpret_cast<const uint4 *>(from);
+        x[u][1] = *reinterpret_cast<const uint4 *>(from + D / 2);
       }
-      k.x += k.x_step;
-      v.x += v.x_step;
     }
     if (s0 == it.first) {  // the rows are on their way meanwhile
       const Place at = place_of(p, it.t, lane);
@@ -169,19 +152,34 @@ __global__ void __launch_bounds__(256) dash_cache8_write_kernel(const __grid_con
         if (lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
         return;
       }
-      place_rows(k, p.c.ks, p.c.kss, at);
-      place_rows(v, p.c.vs, p.c.vss, at);
+      base = base_of(p.c, at);
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       if (s0 + u >= it.end) break;
-      const bool real = row + u * kRows < p.heads;
-      quantise_row<D>(kx[u], k.codes, k.scale, e == 0, real);
-      quantise_row<D>(vx[u], v.codes, v.scale, e == 0, real);
-      k.codes += k.codes_step;
-      v.codes += v.codes_step;
-      k.scale += k.scale_step;
-      v.scale += v.scale_step;
+      const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+      // magnitudes in order are bits in order, infinities and NaN above all others
+      uint32_t both = w[0] & 0x7fff7fffu;
+#pragma unroll
+      for (int i = 1; i < 8; ++i) both = __vmaxu2(both, w[i] & 0x7fff7fffu);
+      uint32_t top = max(both & 0xffffu, both >> 16);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top < 0x7f80u;
+      const int f = finite ? scale_field(top) : 1;
+      const float inv = pow2_field(254 - f);
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+      uint2 lo = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16), hi = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
+      if (!finite) lo = hi = make_uint2(0u, 0u);
+      const Row8 row = row_of8(p, r + u * kRows);
+      if (row.head < 0) continue;
+      uint8_t *codes = codes_of(p.c, base, row) + e;
+      *reinterpret_cast<uint2 *>(codes) = lo;
+      *reinterpret_cast<uint2 *>(codes + D / 2) = hi;
+      if (e == 0) *scale_of(p.c, base, row) = finite ? pow2_field(f) : NAN;
     }
   }
 }
@@ -199,50 +197,45 @@ __device__ __forceinline__ uint4 row_values(uint2 codes, float scale) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) dash_cache8_read_kernel(const __grid_constant__ Cache8RowsParams p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+__global__ void __launch_bounds__(256, 6) dash_cache8_read_kernel(const __grid_constant__ Cache8RowsParams p) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31, e = (lane % kLanes) * 8;
   const Item8 it = item_of<D>(p);
   if (it.t >= p.n_tokens) return;
-  int row = it.first * kRows + lane / kLanes;
-  Rows8 k = rows_of8<D>(p, false, it.t, row, e), v = rows_of8<D>(p, true, it.t, row, e);
+  int r = it.first * kRows + lane / kLanes;
   const Place at = place_of(p, it.t, lane);
   const bool none = at.page < 0;  // such rows are zero
   if (none && !at.behind && lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
-  place_rows(k, p.c.ks, p.c.kss, at);
-  place_rows(v, p.c.vs, p.c.vss, at);
-  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, row += kRowsAhead * kRows) {
-    uint2 kx[kRowsAhead], vx[kRowsAhead];
-    float ks[kRowsAhead], vs[kRowsAhead];
+  const Base8 base = base_of(p.c, at);
+  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, r += kRowsAhead * kRows) {
+    uint2 x[kRowsAhead][2];
+    float scale[kRowsAhead];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      kx[u] = vx[u] = make_uint2(0u, 0u);
-      ks[u] = vs[u] = 0.f;
-      if (s0 + u < it.end && row + u * kRows < p.heads && !none) {
-        kx[u] = *reinterpret_cast<const uint2 *>(k.codes);
-        vx[u] = *reinterpret_cast<const uint2 *>(v.codes);
-        ks[u] = *k.scale;
-        vs[u] = *v.scale;
+      x[u][0] = x[u][1] = make_uint2(0u, 0u);
+      scale[u] = 0.f;
+      const Row8 row = row_of8(p, r + u * kRows);
+      if (s0 + u < it.end && row.head >= 0 && !none) {
+        const uint8_t *from = codes_of(p.c, base, row) + e;
+        x[u][0] = *reinterpret_cast<const uint2 *>(from);
+        x[u][1] = *reinterpret_cast<const uint2 *>(from + D / 2);
+        scale[u] = *scale_of(p.c, base, row);
       }
-      k.codes += k.codes_step;
-      v.codes += v.codes_step;
-      k.scale += k.scale_step;
-      v.scale += v.scale_step;
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      if (s0 + u >= it.end || row + u * kRows >= p.heads) break;
-      *reinterpret_cast<uint4 *>(k.x) = row_values(kx[u], ks[u]);
-      *reinterpret_cast<uint4 *>(v.x) = row_values(vx[u], vs[u]);
-      k.x += k.x_step;
-      v.x += v.x_step;
+      const Row8 row = row_of8(p, r + u * kRows);
+      if (s0 + u >= it.end || row.head < 0) break;
+      __nv_bfloat16 *to = packed_row(p, it.t, row) + e;
+      *reinterpret_cast<uint4 *>(to) = row_values(x[u][0], scale[u]);
+      *reinterpret_cast<uint4 *>(to + D / 2) = row_values(x[u][1], scale[u]);
     }
   }
 }
 
 // A token's rows are one warp's, or, of few tokens, several warps'.
 cudaError_t launch_rows(void (*kernel)(const Cache8RowsParams), Cache8RowsParams p, cudaStream_t stream) {
-  const int steps = (p.heads * p.D / 8 + 31) / 32, want = 4096;
+  const int rows = 512 / p.D, steps = (2 * p.heads + rows - 1) / rows, want = 4096;
   p.blocks = p.n_tokens >= want ? 1 : (want + p.n_tokens - 1) / p.n_tokens;
   if (p.blocks > steps) p.blocks = steps;
   p.passes = (steps + p.blocks - 1) / p.blocks;
@@ -711,25 +704,31 @@ cudaError_t launch_decode_t(const Decode8Params &p, int num_sms, cudaStream_t st
   }
   const int resident = Dec8<D, NT>::kCtas * num_sms;
   const bool all = items <= resident;
-  if (!all && NT == 1) {
-    Decode8Params q = p;
-    q.least_chunk = 1024;  // an item's start and end cost as much as two tiles of 128 tokens
-    const cudaError_t e = launch_decode8_wide(D, q, num_sms, stream);
-    return e != cudaSuccess || q.max_splits <= 1 ? e : launch_decode_join(D, q, stream);
+  if constexpr (NT == 1) {
+    if (!all) {
+      Decode8Params q = p;
+      q.least_chunk = 1024;  // an item's start and end cost as much as two tiles of 128 tokens
+      const cudaError_t e = launch_decode8_wide(D, q, num_sms, stream);
+      return e != cudaSuccess || q.max_splits <= 1 ? e : launch_decode_join(D, q, stream);
+    }
   }
-  const cudaError_t e = launch(all ? dash_decode8_kernel<D, NT, kPlain> : dash_decode8_kernel<D, NT, kScan>,
-                               all ? (int)items : resident, kDecodeThreads, kSmem, stream, nullptr, p);
+  void (*kernel)(const Decode8Params) = dash_decode8_kernel<D, NT, kPlain>;
+  if constexpr (NT == 2)
+    if (!all) kernel = dash_decode8_kernel<D, NT, kScan>;
+  const cudaError_t e = launch(kernel, all ? (int)items : resident, kDecodeThreads, kSmem, stream, nullptr, p);
   return e != cudaSuccess || p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
 }
 
 template <int D, int NT>
 cudaError_t prepare_t() {
-  for (auto kernel : {dash_decode8_kernel<D, NT, kPlain>, dash_decode8_kernel<D, NT, kScan>,
-                      dash_decode8_kernel<D, NT, kCluster>})
-    if (const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D, NT>::kSmem))
-      return e;
-  return cudaSuccess;
+  auto set = [](void (*kernel)(const Decode8Params)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D, NT>::kSmem);
+  };
+  cudaError_t e = set(dash_decode8_kernel<D, NT, kPlain>);
+  if (e == cudaSuccess) e = set(dash_decode8_kernel<D, NT, kCluster>);
+  if constexpr (NT == 2)
+    if (e == cudaSuccess) e = set(dash_decode8_kernel<D, NT, kScan>);
+  return e;
 }
 
 }  // namespace
