@@ -131,6 +131,7 @@ struct Norm {
     rope = c.plain(w[2], at::kFloat, -1, 2);
     positions = c.plain(w[3], at::kInt, q->size(0));
     pairs = PyObject_IsTrue(w[5]);
+    if (pairs < 0) PyErr_Clear();  // the Python form says it again
     return c.ok && number(w[4], &eps) && pairs >= 0 && fits(q->size(1)) && fits(k->size(1)) && fits(rope->size(0));
   }
 };

@@ -25,6 +25,11 @@
 // of V are.  l and O are 32-bit sums, l of the unrounded 2^(x_t - m).
 // m and M move only when a term has grown past 2^8 of them (most steps need no
 // reduction across lanes and no rescaling).
+// This form takes calls whose items all run at once (701 tokens, 16 heads on 4:
+// 7.2 us, a chain of length, page, rows, products and the cluster's join) and
+// groups of 9 to 16 heads (64 sequences of 8192 tokens, 16 heads on 1 of 128: 61
+// us, 2.3 TB/s, bound by instructions: the widening, and a reduction's share of
+// each head); decode8.cu has the one for calls that fill the GPU.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

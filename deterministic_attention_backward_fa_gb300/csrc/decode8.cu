@@ -6,20 +6,27 @@
 //   x_t = scale log2(e) a_t (q . k_t),  l += 2^(x_t - m),  O += 2^(x_t - M) c_t v_t,
 // m and M the running maxima of x_t and x_t + log2 c_t.  The codes are the large
 // operand and need no widening; what meets them, Q and the weights, is split
-// into three e4m3 terms of 4 bits each, every next one 16 times larger:
-//   y = y1 + y2 / 16 + y3 / 256,  y1 = e4m3(y), y2 = e4m3(16 (y - y1)), ...
+// into two e4m3 terms of 4 bits each, the second 16 times larger:
+//   y = y1 + y2 / 16,  y1 = e4m3(y), y2 = e4m3(16 (y - y1)),
 // which are columns of their own, so that their scales stay apart until the sums
 // are 32-bit:
-//   S^T [128 tokens x 32] = K [128 x D] Q^T,  O^T [D x 32] += V^T [D x 128] P^T,
-// columns (term, head).  Q's 8 bits are exact down to 2^-17 of its row's largest
-// value and off by 2^-26 of that below; a weight is off by at most 2^-12 of
-// itself, or by 2^-22 of the largest that its head has met (whose own M goes by
-// x_t + log2 c_t, so that it is what counts in O, whatever the scales of V are).
+//   S^T [128 tokens x 16] = K [128 x D] Q^T,  O^T [D x 16] += V^T [D x 128] P^T,
+// columns (term, head).  Two terms hold Q's 8 bits: exactly down to 2^-13 of its
+// row's largest value, and to 2^-21 of that below (the largest lands at 2^7 to
+// 2^8, and a term's last place is 2^-9).  A weight is off by at most 2^-8 of
+// itself, as one rounded to bf16 would be, or by 2^-18 of the largest that its
+// head has met (whose own M goes by x_t + log2 c_t, so that it is what counts in
+// O, whatever the scales of V are).  l sums the unrounded 2^(x_t - m).
 //
 // The bound is HBM: 2 (D + 4) bytes a token and K/V head.  On the plain pipes the
 // widening alone takes half the issue slots (cache8.cu's kernel stays at 60 % of
 // the copy rate); here a token costs a softmax thread's instructions for its 8
-// heads, once.
+// heads, once.  66 sequences of 460000 tokens, 8 K/V heads of 128: 163 us, 5.8
+// TB/s or 86 % of the copy rate (rows fetched by 16-byte copies alone: 182); 32
+// of 8192: 94 us (87 %); 64 of 4096 with D = 64: 81 us (52 %).  What is left is
+// a tile's chain from its scores to its weights (3000 clocks of the one group of
+// softmax warps, which half the bytes a token do not shorten), and an item's
+// start and end.
 //
 // A persistent CTA, two on an SM, walks its items (longest splits first) without
 // a break in its loads.  Warps: 0-3 softmax (a thread owns a token, and in the
@@ -45,8 +52,10 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kFetch = 4;  // warps that fetch, 32 rows each
 constexpr int kMma = 8;    // the warp that issues; 9-11 make the warpgroup whole
-constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsFetch = 72, kRegsMma = 40;
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 128, kRegsFetch = 80, kRegsMma = 32;
 static_assert(kRegsSoftmax + kRegsFetch + kRegsMma <= 3 * kRegsLaunch, "register split exceeds the CTA's allocation");
+// the fetching warps keep what they were launched with: they execute no setmaxnreg
+static_assert(kRegsFetch == kRegsLaunch && kRegsMma < kRegsLaunch && kRegsSoftmax > kRegsLaunch, "inc and dec as they are used");
 constexpr int kHeads = 8, kTerms = 2, kCols = kTerms * kHeads;
 constexpr int kTile8 = 128;        // tokens
 constexpr int kSlots = 8;          // tiles whose scales and masks are held
@@ -81,6 +90,12 @@ struct Tile {
   // K of tile j + n is asked for once the load kStages before it has been read.  V of tile j is read after the tile's
   // scales are, and 2 n - 3 loads lie between the two, so n reaches (kStages + 2) / 2.
   static_assert(kSlots > (kStages + 2) / 2, "a slot would be filled before it is read");
+  // The fetching warps take tiles in turn, kPer of them together (all four: 3 % slower, 9 % at D = 64; each by itself,
+  // with the ten stages of D = 64: 20 % slower).  A warp that waits for a stage goes by the parity of
+  // its phase, so it has to know already that the phase before that has ended: its last load was at most
+  // 2 kUnits - 1 loads ago, and waited for the one kStages before it.
+  static constexpr int kPer = 2, kUnits = kFetch / kPer, kGroups = 4 / kPer;
+  static_assert(2 * kUnits - 1 <= kStages, "a phase could be taken for the one two before it");
   // where 16-byte piece c of a row stands in it
   static __device__ __forceinline__ int place(int row, int c) { return (c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4; }
   // Descriptors.  K's rows are the operand's rows.  V's are its columns: of D = 64
@@ -93,7 +108,8 @@ struct Tile {
 };
 constexpr uint32_t oMisc = oBar + kBars * 8;
 constexpr int kSorted = 1024;  // sequences whose lengths are held
-constexpr uint32_t oLens = oMisc + 16;
+constexpr uint32_t oLast = oMisc + 16;  // [10] the last load of each stage
+constexpr uint32_t oLens = oLast + 48;
 constexpr uint32_t kSmem = oLens + 4 * kSorted;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
 constexpr uint32_t cS = 0, cO = 2 * kCols, kTmem = 64;
@@ -289,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + oMask);
   float *factors = reinterpret_cast<float *>(smem + oSc);
   Item *items = reinterpret_cast<Item *>(smem + oItem);
+  volatile int *last = reinterpret_cast<volatile int *>(smem + oLast);
   if ((smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusSmemMisaligned);
     return;
@@ -301,12 +318,13 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       mbar_init(&bars[bQFull + s], kFetch);
       mbar_init(&bars[bQEmpty + s], 5);  // the MMA warp and the softmax warps
     }
-    for (int s = 0; s < kSlots; ++s) mbar_init(&bars[bTile + s], 33 * kFetch);  // the copies' ends and the masks
+    for (int s = 0; s < kSlots; ++s) mbar_init(&bars[bTile + s], 33 * Ti::kPer);  // the copies' ends and the masks
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars[bKvFull + s], 32 * kFetch);
+      mbar_init(&bars[bKvFull + s], 32 * Ti::kPer);
       mbar_init(&bars[bKvEmpty + s], 1);
     }
     mbar_init(&bars[bFinal], 1);
+    for (int s = 0; s < kStages; ++s) last[s] = -1;
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -328,31 +346,36 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
 
   if (warp >= 4 && warp < kMma) {
     // ------------------------------------------------------ loads, and Q
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFetch));
     const int w = warp - 4, row = w * 32 + lane;
+    constexpr int kPer = Ti::kPer, kUnits = Ti::kUnits, kGroups = Ti::kGroups;
+    const int mine = (w % kPer) * 32 * kGroups + lane;  // the lane's first token of a tile that its warp takes part in
     constexpr int kChunks = D / 16, kRowsPer = 32 / kChunks;  // 16-byte pieces of a row, rows of a warp's copy
     const int c = lane % kChunks, rsub = lane / kChunks;
     constexpr int kLanes = D / 8;  // of a head of Q
     const int head = row / kLanes, dim = lane % kLanes * 8;
-    Ring<kStages> r;
-    uint32_t loads = 0;
     Walk walk(p, lens);
     // split and head of the next item, and the steps to the one after it
     long long want = blockIdx.x / p.Hkv;
     int hk = blockIdx.x % p.Hkv;
     const int want_step = gridDim.x / p.Hkv, hk_step = gridDim.x % p.Hkv;
-    // The next item that has tokens, with what its start waits for: its Q and the pages of its first two tiles.
+    // The next item that has tokens, with what its start waits for: its Q and the pages of the warp's first tile.
     // Empty sequences are answered on the way.
     struct Next {
       Item it;
       uint4 q;
-      int page[2];
+      int page[kGroups];
     } next;
-    auto page_of = [&](const Item &it, int j) -> int {
-      const int t = it.begin + j * kTile8 + row;
-      return t < it.end ? p.table[it.b * p.table_row + quotient(p.page, t)] : -1;
+    // A lane holds the pages of the warp's tokens lane, lane + 32, ... of a tile.
+    auto pages_of = [&](const Item &it, int j, int (&page)[kGroups]) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const int t = it.begin + j * kTile8 + mine + 32 * i;
+        page[i] = t < it.end ? p.table[it.b * p.table_row + quotient(p.page, t)] : -1;
+      }
     };
-    auto look_up = [&]() {
+    // the warp's first tile of an item with `before` tiles before it
+    auto first_of = [&](uint32_t before) { return (int)((w / kPer - before) & (kUnits - 1)); };
+    auto look_up = [&](uint32_t before) {
       while (true) {
         next.it.tiles = -1;
         if (!walk.find(p, want, lane)) return;
@@ -374,10 +397,9 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       if (head < p.group)
         next.q = *reinterpret_cast<const uint4 *>(p.q + next.it.b * p.q_batch +
                                                   (long long)(next.it.hk * p.group + head) * p.q_head + dim);
-      next.page[0] = page_of(next.it, 0);
-      next.page[1] = page_of(next.it, 1);
+      pages_of(next.it, first_of(before), next.page);
     };
-    look_up();
+    look_up(0);
     while (true) {
       const Item it = next.it;
       // Q's largest value is put at 2^7 to 2^8; a head with a NaN or an infinity is all NaN
@@ -417,99 +439,118 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       if (it.tiles < 0) break;
       const uint8_t *kbase = p.c.k + it.hk * p.c.ks.head + 16 * c, *vbase = p.c.v + it.hk * p.c.vs.head + 16 * c;
       const float *ksbase = p.c.k_scale + it.hk * p.c.kss.head, *vsbase = p.c.v_scale + it.hk * p.c.vss.head;
-      // The rows of a tile of K (with the scales of both) or V, where the page and place of the lane's token are known.
-      struct Where {
-        int page, off;
-        uint32_t valid;
-        bool whole;  // the tile has 128 tokens
-      };
-      auto fetch = [&](bool is_v, uint32_t tile, const Where &at) {
-        mbar_wait(&bars[bKvEmpty + r.st], r.ph ^ 1, g);
+      // The rows of the item's tile j of K (with the scales of both) or V: load number `pos` of the CTA.
+      auto fetch = [&](bool is_v, uint32_t pos, int j, const int (&page)[kGroups]) {
+        const int st_at = pos % kStages;
+        mbar_wait(&bars[bKvEmpty + st_at], (pos / kStages & 1) ^ 1, g);
         // After an abort nothing more arrives at a stage: one that waits for bytes of TMA has no arrivals left to take.
         if (warp_aborted(g)) return;
+        if (lane == 0) last[st_at] = (int)pos;
         const CacheStrides &st = is_v ? p.c.vs : p.c.ks;
-        const uint32_t slot = tile % kSlots;
-        const uint32_t dst = smem_u32(smem + oKV + r.st * Ti::kBytes) + (w * 32 + rsub) * D;
-        const uint8_t *base = is_v ? vbase : kbase;
-        bool by_copies = true;
-        if (box > 0 && at.whole && at.valid == 0xffffffffu) {
-          by_copies = false;
-          uint64_t *bar = &bars[bKvFull + r.st];
-          if ((row & (box - 1)) == 0) {
-            mbar_arrive_expect_tx(bar, box * D);
-            tma_load_4d(smem + oKV + r.st * Ti::kBytes + row * D, is_v ? &tmV : &tmK, bar, 0, it.hk, at.off, at.page);
-          } else {
-            mbar_arrive(bar);
-          }
-        } else if (at.valid == 0xffffffffu && p.whole) {
-          const long long step = kRowsPer * st.token;
+        uint8_t *const stage = smem + oKV + st_at * Ti::kBytes;
+        uint64_t *bar = &bars[bKvFull + st_at];
+        const int t0 = it.begin + j * kTile8;
+        uint32_t valid[kGroups];
+        int off[kGroups];
+        bool all = true;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 16 tokens lie in one page
-            const int pg = __shfl_sync(0xffffffffu, at.page, 16 * half), of = __shfl_sync(0xffffffffu, at.off, 16 * half);
-            const uint8_t *from = wide_add(wide_add(base, pg, (int)st.page), of + rsub, (int)st.token);
+        for (int i = 0; i < kGroups; ++i) {
+          const int t = t0 + mine + 32 * i;
+          const bool ok = page[i] >= 0 && page[i] < p.n_pages;
+          if (!is_v && t < it.end && !ok) atomicCAS(p.status, 0, kStatusBadPage);
+          off[i] = t - quotient(p.page, t) * p.page_size;
+          valid[i] = __ballot_sync(0xffffffffu, ok);
+          all = all && valid[i] == 0xffffffffu;
+        }
+        // TMA: where all of the warp's tokens count, and with it, as a box may reach into another warp's, all of the tile's
+        const bool by_copies = !(box > 0 && all && (box <= 32 * kGroups || t0 + kTile8 <= it.end));
+        if (!by_copies) {
+          int n = 0;
 #pragma unroll
-            for (int i = 0; i < 16 / kRowsPer; ++i, from += step) {
-              const int rr = 16 * half + i * kRowsPer;
-              cp_async<16>(dst + rr * D + Ti::place(rr + rsub, c), from);
+          for (int i = 0; i < kGroups; ++i) n += ((mine + 32 * i) & (box - 1)) == 0;
+          if (n > 0) mbar_arrive_expect_tx(bar, n * box * D);
+          else mbar_arrive(bar);
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i)
+            if (((mine + 32 * i) & (box - 1)) == 0)
+              tma_load_4d(stage + (mine + 32 * i) * D, is_v ? &tmV : &tmK, bar, 0, it.hk, off[i], page[i]);
+        } else {
+          const uint8_t *base = is_v ? vbase : kbase;
+#pragma unroll 1
+          for (int i = 0; i < kGroups; ++i) {
+            int pg_i = page[0], off_i = off[0];
+            uint32_t valid_i = valid[0];
+#pragma unroll
+            for (int k = 1; k < kGroups; ++k)
+              if (i == k) pg_i = page[k], off_i = off[k], valid_i = valid[k];
+            const uint32_t dst = smem_u32(stage) + (mine - lane + 32 * i + rsub) * D;
+            if (valid_i == 0xffffffffu && p.whole) {
+              const long long step = kRowsPer * st.token;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {  // 16 tokens lie in one page
+                const int pg = __shfl_sync(0xffffffffu, pg_i, 16 * half), of = __shfl_sync(0xffffffffu, off_i, 16 * half);
+                const uint8_t *from = wide_add(wide_add(base, pg, (int)st.page), of + rsub, (int)st.token);
+#pragma unroll
+                for (int k = 0; k < 16 / kRowsPer; ++k, from += step) {
+                  const int rr = 16 * half + k * kRowsPer;
+                  cp_async<16>(dst + rr * D + Ti::place(rr + rsub, c), from);
+                }
+              }
+            } else {
+              const long long a = (valid_i >> lane) & 1u ? pg_i * st.page + off_i * st.token : 0;
+#pragma unroll
+              for (int k = 0; k < 32 / kRowsPer; ++k) {
+                const int rr = k * kRowsPer + rsub;
+                const long long x = __shfl_sync(0xffffffffu, a, rr);
+                cp_async_if<16>(dst + k * kRowsPer * D + Ti::place(rr, c), base + x, (valid_i >> rr) & 1u);
+              }
             }
           }
-        } else {
-          const long long a = (at.valid >> lane) & 1u ? at.page * st.page + at.off * st.token : 0;
+        }
+        if (!is_v) {
+          const uint32_t slot = (T + j) % kSlots;
 #pragma unroll
-          for (int i = 0; i < 32 / kRowsPer; ++i) {
-            const int rr = i * kRowsPer + rsub;
-            const long long x = __shfl_sync(0xffffffffu, a, rr);
-            cp_async_if<16>(dst + i * kRowsPer * D + Ti::place(rr, c), base + x, (at.valid >> rr) & 1u);
+          for (int i = 0; i < kGroups; ++i) {
+            const bool ok = (valid[i] >> lane) & 1u;
+            const uint32_t sd = smem_u32(scales + slot * 2 * kTile8 + mine + 32 * i);
+            cp_async_if<4>(sd, ok ? ksbase + page[i] * p.c.kss.page + off[i] * p.c.kss.token : ksbase, ok);
+            cp_async_if<4>(sd + kTile8 * 4, ok ? vsbase + page[i] * p.c.vss.page + off[i] * p.c.vss.token : vsbase, ok);
           }
-        }
-        if (!is_v) {
-          const bool ok = (at.valid >> lane) & 1u;
-          const uint32_t sd = smem_u32(scales + slot * 2 * kTile8 + row);
-          cp_async_if<4>(sd, ok ? ksbase + at.page * p.c.kss.page + at.off * p.c.kss.token : ksbase, ok);
-          cp_async_if<4>(sd + kTile8 * 4, ok ? vsbase + at.page * p.c.vss.page + at.off * p.c.vss.token : vsbase, ok);
-        }
-        if (!is_v) {
           // the slot's last tile has been read (see kSlots)
           if (lane == 0) {
-            masks[slot * 4 + w] = at.valid;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) masks[slot * 4 + (w % kPer) * kGroups + i] = valid[i];
             mbar_arrive(&bars[bTile + slot]);
           }
           cp_arrive(&bars[bTile + slot]);
         }
-        if (by_copies) cp_arrive(&bars[bKvFull + r.st]);
-        ++loads;
-        r.next();
+        if (by_copies) cp_arrive(bar);
       };
-      // V of a tile follows K of the next one; pages are looked up two tiles ahead of K
-      Where k, v = {};
-      int page = next.page[0], after = next.page[1];
-      for (int j = 0; j <= it.tiles; ++j) {
-        if (j < it.tiles) {
-          const int t = it.begin + j * kTile8 + row;
-          k.page = page;
-          k.whole = it.begin + (j + 1) * kTile8 <= it.end;
-          const bool ok = page >= 0 && page < p.n_pages;
-          if (t < it.end && !ok) atomicCAS(p.status, 0, kStatusBadPage);
-          k.off = t - quotient(p.page, t) * p.page_size;
-          k.valid = __ballot_sync(0xffffffffu, ok);
-          page = after;
-          after = page_of(it, j + 2);
-          fetch(false, T + j, k);
-          if (j == 0) look_up();
-        }
-        if (j > 0) fetch(true, 0, v);
-        v = k;
-      }
+      // In the order of loads V of a tile follows K of the next one.
+      int page[kGroups], after[kGroups];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) page[i] = next.page[i];
+      int j = first_of(T);
+      bool ahead = false;
+      do {
+        if (j < it.tiles) fetch(false, 2 * T + (j > 0 ? 2 * j - 1 : 0), j, page);
+        pages_of(it, j + kUnits, after);
+        if (!ahead) look_up(T + it.tiles);
+        ahead = true;
+        if (j < it.tiles) fetch(true, 2 * T + (j + 1 < it.tiles ? 2 * j + 2 : 2 * j + 1), j, page);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) page[i] = after[i];
+        j += kUnits;
+      } while (j < it.tiles);
       T += it.tiles;
       ib ^= 1;
       if (ib == 0) iph ^= 1;
     }
     cp_wait_all();
     // what TMA still has in flight lands before the CTA exits
-    for (int s = 0; s < kStages; ++s) {
-      const uint32_t f = loads / kStages + ((uint32_t)s < loads % kStages ? 1u : 0u);
-      if (f) mbar_drain(&bars[bKvFull + s], (f - 1) & 1, g.limit_ns);
-    }
+    named_bar(3, 32 * kFetch);  // nothing more is issued
+    for (int s = 0; s < kStages; ++s)
+      if (last[s] >= 0) mbar_drain(&bars[bKvFull + s], last[s] / kStages & 1, g.limit_ns);
   } else if (warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kMma) {

@@ -19,8 +19,13 @@
 // row at D = 128) into the swizzled layout that the MMAs read.  A copy's end
 // arrives on its stage's barrier by itself; the MMA warps put the proxy fence
 // between that and their reads.  (Handed over by the fetching warps, which wait
-// for one load after they have issued another, a stage comes late: 36 us for
-// 32000 tokens, 64 sequences of 4 heads on each of 8 K/V heads.)
+// for one load after they have issued another, a stage comes late.)
+//
+// Bound by the products (4 D a token and row) and the bytes (4 D a token and K/V
+// head), which are about even at 256 rows: 32000 tokens, 64 sequences of 4 heads
+// on each of 8 K/V heads of 128 in 32 us, 18 and 19 of them those two.  What is
+// left is each tile's chain of scores, softmax and product, of which two run in
+// turn.  With tails of 512 tokens the call takes 69.5 us.
 #include <cuda_runtime.h>
 
 #include "packed.h"

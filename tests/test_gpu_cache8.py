@@ -261,6 +261,17 @@ def test_decode_of_many_long_sequences(hq, hkv, D):
     dash.dash_sync_status()
 
 
+@pytest.mark.parametrize("n", [1024, 1025, 1500])
+def test_decode_of_very_many_sequences(n):
+    # of up to 1024 the lengths are held and the items sorted by them
+    lens, hq, hkv, D, page = [i * 37 % 300 for i in range(n)], 2, 1, 64, 16
+    c = cache(lens, hkv, D, page)
+    q = P.normal(4, n, hq, D)
+    o, lse = dash.attn_decode_fp8(q, *c, i32(lens))
+    dash.dash_sync_status()
+    check(q, c, lens, 1 / math.sqrt(D), o, lse)
+
+
 @pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("spread", [3.0, 20.0])
 @pytest.mark.parametrize("hq,hkv", [(4, 2), (12, 1)])
