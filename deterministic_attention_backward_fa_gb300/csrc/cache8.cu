@@ -83,51 +83,78 @@ __device__ __forceinline__ Place place_of(const Cache8RowsParams &p, int t, int 
   return at;
 }
 
-// A warp takes a token and `passes` steps of its rows, K's heads and then V's:
-// D / 16 lanes a row, 8 values of each half a lane, as what is done once for a
-// row weighs (with 8 values a lane the write of 16384 tokens of 8 heads of 128
-// takes 22.0 us instead of 20.0).  A write is 3 (+ 4 / D) bytes a value, and so is a
-// read: 4.9 TB/s both, where adding 1 to as many bytes gets 6.2.  What is missing
-// is the look-up before a token's rows can be placed (sequence, start, page: each
-// waits for the one before).  Runs of 2 to 4 tokens, looked up at once, are no
-// faster (22.6 and 21.0 us): fewer warps then wait for more rows each.
+// A warp takes a token and `passes` steps of its heads, K's rows and V's: D / 16
+// lanes a row, 8 values of each half a lane, since what is done once for a row
+// weighs: the issue slots are half full.  16384 tokens of 8 heads of 128, 3 (+ 4 / D) bytes
+// a value: written in 19.0 us, read in 20.0, 5.4 and 5.1 TB/s, where adding 1 to
+// as many bytes gets 6.2.  (8 values a lane: 22.0 and 20.1; K's and V's rows in
+// one list, 20.6 and 20.0: addresses by lane.)  What is missing is the look-up
+// before a token's rows can be placed (sequence, start, page: each waits for the
+// one before).  Runs of 2 to 4 tokens, looked up at once, are no faster (22.6 and
+// 21.0 us): fewer warps then wait for more rows each.
 struct Item8 {
   int t, first, end;
 };
 template <int D>
 __device__ __forceinline__ Item8 item_of(const Cache8RowsParams &p) {
-  constexpr int kRows = 32 / (D / 16);
+  constexpr int kRows = 512 / D;
   const unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5), t = item / (unsigned)p.blocks;
   const int first = (int)(item - t * p.blocks) * p.passes;
-  return {(int)t, first, min(first + p.passes, (2 * p.heads + kRows - 1) / kRows)};
+  return {(int)t, first, min(first + p.passes, (p.heads + kRows - 1) / kRows)};
 }
-constexpr int kRowsAhead = 2;  // rows that a lane has in flight (4 on 4 CTAs of an SM 21.9, 1 on 6 of them 21.6)
+constexpr int kRowsAhead = 1;  // rows of K and of V that a lane has in flight (2 on 4 CTAs of an SM: write 20.3, read 21.3)
 
-// A row of K or of V: the packed one, its codes, its scale.
-struct Row8 {
-  bool is_v;
-  int head;  // -1: there is none
+// The lane's place in the rows of K or of V: the packed one, the codes, the scale;
+// `step` of each to the rows of the next step.
+struct Rows8 {
+  __nv_bfloat16 *x;
+  uint8_t *codes;
+  float *scale;
+  long long x_step, codes_step, scale_step;
 };
-__device__ __forceinline__ Row8 row_of8(const Cache8RowsParams &p, int r) {
-  return {r >= p.heads, r < p.heads ? r : r < 2 * p.heads ? r - p.heads : -1};
+template <int D>
+__device__ __forceinline__ Rows8 rows_of8(const Cache8RowsParams &p, bool is_v, int t, int row, int e) {
+  Rows8 r;
+  constexpr int kRows = 512 / D;
+  const long long head = is_v ? p.v_head : p.k_head;
+  const CacheStrides &st = is_v ? p.c.vs : p.c.ks, &ss = is_v ? p.c.vss : p.c.kss;
+  r.x = (is_v ? p.v + t * p.v_row : p.k + t * p.k_row) + row * head + e;
+  r.codes = (is_v ? p.c.v : p.c.k) + row * st.head + e;
+  r.scale = (is_v ? p.c.v_scale : p.c.k_scale) + row * ss.head;
+  r.x_step = kRows * head;
+  r.codes_step = kRows * st.head;
+  r.scale_step = kRows * ss.head;
+  return r;
 }
-__device__ __forceinline__ __nv_bfloat16 *packed_row(const Cache8RowsParams &p, int t, Row8 r) {
-  return r.is_v ? p.v + t * p.v_row + r.head * p.v_head : p.k + t * p.k_row + r.head * p.k_head;
+__device__ __forceinline__ void place_rows(Rows8 &r, const CacheStrides &st, const CacheStrides &ss, Place at) {
+  r.codes += at.page * st.page + at.off * st.token;
+  r.scale += at.page * ss.page + at.off * ss.token;
 }
-// Where a token's rows begin.
-struct Base8 {
-  uint8_t *codes[2];
-  float *scale[2];
-};
-__device__ __forceinline__ Base8 base_of(const Cache8 &c, Place at) {
-  return {{c.k + at.page * c.ks.page + at.off * c.ks.token, c.v + at.page * c.vs.page + at.off * c.vs.token},
-          {c.k_scale + at.page * c.kss.page + at.off * c.kss.token, c.v_scale + at.page * c.vss.page + at.off * c.vss.token}};
-}
-__device__ __forceinline__ uint8_t *codes_of(const Cache8 &c, const Base8 &b, Row8 r) {
-  return (r.is_v ? b.codes[1] : b.codes[0]) + r.head * (r.is_v ? c.vs.head : c.ks.head);
-}
-__device__ __forceinline__ float *scale_of(const Cache8 &c, const Base8 &b, Row8 r) {
-  return (r.is_v ? b.scale[1] : b.scale[0]) + r.head * (r.is_v ? c.vss.head : c.kss.head);
+
+template <int D>
+__device__ __forceinline__ void quantise_row(const uint4 (&x)[2], uint8_t *codes, float *scale, bool first, bool real) {
+  constexpr int kLanes = D / 16;
+  const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  // magnitudes in order are bits in order, infinities and NaN above all others
+  uint32_t both = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) both = __vmaxu2(both, w[i] & 0x7fff7fffu);
+  uint32_t top = max(both & 0xffffu, both >> 16);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool finite = top < 0x7f80u;
+  const int f = finite ? scale_field(top) : 1;
+  const float inv = pow2_field(254 - f);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+  uint2 lo = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16), hi = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
+  if (!finite) lo = hi = make_uint2(0u, 0u);
+  if (!real) return;
+  *reinterpret_cast<uint2 *>(codes) = lo;
+  *reinterpret_cast<uint2 *>(codes + D / 2) = hi;
+  if (first) *scale = finite ? pow2_field(f) : NAN;
 }
 
 template <int D>
@@ -136,19 +163,21 @@ __global__ void __launch_bounds__(256, 5) dash_cache8_write_kernel(const __grid_
   const int lane = threadIdx.x & 31, e = (lane % kLanes) * 8;
   const Item8 it = item_of<D>(p);
   if (it.t >= p.n_tokens) return;
-  int r = it.first * kRows + lane / kLanes;
-  Base8 base;
-  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, r += kRowsAhead * kRows) {
-    uint4 x[kRowsAhead][2];
+  int row = it.first * kRows + lane / kLanes;
+  Rows8 k = rows_of8<D>(p, false, it.t, row, e), v = rows_of8<D>(p, true, it.t, row, e);
+  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, row += kRowsAhead * kRows) {
+    uint4 kx[kRowsAhead][2], vx[kRowsAhead][2];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
-      const Row8 row = row_of8(p, r + u * kRows);
-      if (s0 + u < it.end && row.head >= 0) {
-        const __nv_bfloat16 *from = packed_row(p, it.t, row) + e;
-        x[u][0] = *reinterpret_cast<const uint4 *>(from);
-        x[u][1] = *reinterpret_cast<const uint4 *>(from + D / 2);
+      kx[u][0] = kx[u][1] = vx[u][0] = vx[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (s0 + u < it.end && row + u * kRows < p.heads) {
+        kx[u][0] = *reinterpret_cast<const uint4 *>(k.x);
+        kx[u][1] = *reinterpret_cast<const uint4 *>(k.x + D / 2);
+        vx[u][0] = *reinterpret_cast<const uint4 *>(v.x);
+        vx[u][1] = *reinterpret_cast<const uint4 *>(v.x + D / 2);
       }
+      k.x += k.x_step;
+      v.x += v.x_step;
     }
     if (s0 == it.first) {  // the rows are on their way meanwhile
       const Place at = place_of(p, it.t, lane);
@@ -157,34 +186,19 @@ __global__ void __launch_bounds__(256, 5) dash_cache8_write_kernel(const __grid_
         if (lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
         return;
       }
-      base = base_of(p.c, at);
+      place_rows(k, p.c.ks, p.c.kss, at);
+      place_rows(v, p.c.vs, p.c.vss, at);
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       if (s0 + u >= it.end) break;
-      const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-      // magnitudes in order are bits in order, infinities and NaN above all others
-      uint32_t both = w[0] & 0x7fff7fffu;
-#pragma unroll
-      for (int i = 1; i < 8; ++i) both = __vmaxu2(both, w[i] & 0x7fff7fffu);
-      uint32_t top = max(both & 0xffffu, both >> 16);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool finite = top < 0x7f80u;
-      const int f = finite ? scale_field(top) : 1;
-      const float inv = pow2_field(254 - f);
-      uint32_t c[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        c[i] = narrow8(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
-      uint2 lo = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16), hi = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
-      if (!finite) lo = hi = make_uint2(0u, 0u);
-      const Row8 row = row_of8(p, r + u * kRows);
-      if (row.head < 0) continue;
-      uint8_t *codes = codes_of(p.c, base, row) + e;
-      *reinterpret_cast<uint2 *>(codes) = lo;
-      *reinterpret_cast<uint2 *>(codes + D / 2) = hi;
-      if (e == 0) *scale_of(p.c, base, row) = finite ? pow2_field(f) : NAN;
+      const bool real = row + u * kRows < p.heads;
+      quantise_row<D>(kx[u], k.codes, k.scale, e == 0, real);
+      quantise_row<D>(vx[u], v.codes, v.scale, e == 0, real);
+      k.codes += k.codes_step;
+      v.codes += v.codes_step;
+      k.scale += k.scale_step;
+      v.scale += v.scale_step;
     }
   }
 }
@@ -207,40 +221,50 @@ __global__ void __launch_bounds__(256, 6) dash_cache8_read_kernel(const __grid_c
   const int lane = threadIdx.x & 31, e = (lane % kLanes) * 8;
   const Item8 it = item_of<D>(p);
   if (it.t >= p.n_tokens) return;
-  int r = it.first * kRows + lane / kLanes;
+  int row = it.first * kRows + lane / kLanes;
+  Rows8 k = rows_of8<D>(p, false, it.t, row, e), v = rows_of8<D>(p, true, it.t, row, e);
   const Place at = place_of(p, it.t, lane);
   const bool none = at.page < 0;  // such rows are zero
   if (none && !at.behind && lane == 0) atomicCAS(p.status, 0, kStatusBadPage);
-  const Base8 base = base_of(p.c, at);
-  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, r += kRowsAhead * kRows) {
-    uint2 x[kRowsAhead][2];
-    float scale[kRowsAhead];
+  place_rows(k, p.c.ks, p.c.kss, at);
+  place_rows(v, p.c.vs, p.c.vss, at);
+  for (int s0 = it.first; s0 < it.end; s0 += kRowsAhead, row += kRowsAhead * kRows) {
+    uint2 kx[kRowsAhead][2], vx[kRowsAhead][2];
+    float ks[kRowsAhead], vs[kRowsAhead];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      x[u][0] = x[u][1] = make_uint2(0u, 0u);
-      scale[u] = 0.f;
-      const Row8 row = row_of8(p, r + u * kRows);
-      if (s0 + u < it.end && row.head >= 0 && !none) {
-        const uint8_t *from = codes_of(p.c, base, row) + e;
-        x[u][0] = *reinterpret_cast<const uint2 *>(from);
-        x[u][1] = *reinterpret_cast<const uint2 *>(from + D / 2);
-        scale[u] = *scale_of(p.c, base, row);
+      kx[u][0] = kx[u][1] = vx[u][0] = vx[u][1] = make_uint2(0u, 0u);
+      ks[u] = vs[u] = 0.f;
+      if (s0 + u < it.end && row + u * kRows < p.heads && !none) {
+        kx[u][0] = *reinterpret_cast<const uint2 *>(k.codes);
+        kx[u][1] = *reinterpret_cast<const uint2 *>(k.codes + D / 2);
+        vx[u][0] = *reinterpret_cast<const uint2 *>(v.codes);
+        vx[u][1] = *reinterpret_cast<const uint2 *>(v.codes + D / 2);
+        ks[u] = *k.scale;
+        vs[u] = *v.scale;
       }
+      k.codes += k.codes_step;
+      v.codes += v.codes_step;
+      k.scale += k.scale_step;
+      v.scale += v.scale_step;
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      const Row8 row = row_of8(p, r + u * kRows);
-      if (s0 + u >= it.end || row.head < 0) break;
-      __nv_bfloat16 *to = packed_row(p, it.t, row) + e;
-      *reinterpret_cast<uint4 *>(to) = row_values(x[u][0], scale[u]);
-      *reinterpret_cast<uint4 *>(to + D / 2) = row_values(x[u][1], scale[u]);
+      if (s0 + u >= it.end || row + u * kRows >= p.heads) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<uint4 *>(k.x + i * (D / 2)) = row_values(kx[u][i], ks[u]);
+        *reinterpret_cast<uint4 *>(v.x + i * (D / 2)) = row_values(vx[u][i], vs[u]);
+      }
+      k.x += k.x_step;
+      v.x += v.x_step;
     }
   }
 }
 
 // A token's rows are one warp's, or, of few tokens, several warps'.
 cudaError_t launch_rows(void (*kernel)(const Cache8RowsParams), Cache8RowsParams p, cudaStream_t stream) {
-  const int rows = 512 / p.D, steps = (2 * p.heads + rows - 1) / rows, want = 4096;
+  const int rows = 512 / p.D, steps = (p.heads + rows - 1) / rows, want = 4096;
   p.blocks = p.n_tokens >= want ? 1 : (want + p.n_tokens - 1) / p.n_tokens;
   if (p.blocks > steps) p.blocks = steps;
   p.passes = (steps + p.blocks - 1) / p.blocks;
