@@ -23,10 +23,10 @@
 // the copy rate); here a token costs a softmax thread's instructions for its 8
 // heads, once.  66 sequences of 460000 tokens, 8 K/V heads of 128: 163 us, 5.8
 // TB/s or 86 % of the copy rate (rows fetched by 16-byte copies alone: 182); 32
-// of 8192: 94 us (87 %); 64 of 4096 with D = 64: 81 us (52 %).  What is left is
-// a tile's chain from its scores to its weights in the one group of softmax warps
-// (at D = 64 a tile takes a CTA 2900 clocks, twice what its bytes would), and an
-// item's start and end.
+// of 8192: 94 us (87 %); 64 of 4096 with D = 64: 81 us (52 %).  With three
+// quarters of the softmax's work left out these take 160, 92 and 69: what is left
+// is, at D = 128, an item's start and end, at D = 64 also a tile's chain from
+// scores to weights, which half as many bytes do not shorten.
 //
 // A persistent CTA, two on an SM, walks its items (longest splits first) without
 // a break in its loads.  Warps: 0-3 softmax (a thread owns a token, and in the
