@@ -25,7 +25,7 @@
 // of V are.  l and O are 32-bit sums, l of the unrounded 2^(x_t - m).
 // m and M move only when a term has grown past 2^8 of them (most steps need no
 // reduction across lanes and no rescaling).
-// This form takes calls whose items all run at once (701 tokens, 16 heads on 4:
+// This form takes calls whose items all run at once or are short (701 tokens, 16 heads on 4:
 // 7.2 us, a chain of length, page, rows, products and the cluster's join) and
 // groups of 9 to 16 heads (64 sequences of 8192 tokens, 16 heads on 1 of 128: 61
 // us, 2.3 TB/s, bound by instructions: the widening, and a reduction's share of
@@ -734,17 +734,17 @@ cudaError_t launch_decode_t(const Decode8Params &p, int num_sms, cudaStream_t st
   const int resident = Dec8<D, NT>::kCtas * num_sms;
   const bool all = items <= resident;
   if constexpr (NT == 1) {
-    if (!all) {
+    // An item of the other form costs as much as two or three of its tiles, however short, so sequences that cannot be
+    // long stay here: at D = 64 up to 512 tokens (256 of 256, 32 heads on 8: 27.9 us against 35.0; 64 of 768 on 16 K/V
+    // heads 38.6 and 36.1), at D = 128 up to 64 (500 of 64: 43.0 and 49.3; 256 of 128: 30.8 and 27.6).
+    if (!all && p.max_pages * p.page_size > (D == 64 ? 512 : 64)) {
       Decode8Params q = p;
       q.least_chunk = 1024;  // an item's start and end cost as much as two tiles of 128 tokens
       const cudaError_t e = launch_decode8_wide(D, q, num_sms, stream);
       return e != cudaSuccess || q.max_splits <= 1 ? e : launch_decode_join(D, q, stream);
     }
   }
-  void (*kernel)(const Decode8Params) = dash_decode8_kernel<D, NT, kPlain>;
-  if constexpr (NT == 2)
-    if (!all) kernel = dash_decode8_kernel<D, NT, kScan>;
-  const cudaError_t e = launch(kernel, all ? (int)items : resident, kDecodeThreads, kSmem, stream, nullptr, p);
+  const cudaError_t e = launch(all ? dash_decode8_kernel<D, NT, kPlain> : dash_decode8_kernel<D, NT, kScan>, all ? (int)items : resident, kDecodeThreads, kSmem, stream, nullptr, p);
   return e != cudaSuccess || p.max_splits <= 1 ? e : launch_decode_join(D, p, stream);
 }
 
@@ -754,9 +754,8 @@ cudaError_t prepare_t() {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Dec8<D, NT>::kSmem);
   };
   cudaError_t e = set(dash_decode8_kernel<D, NT, kPlain>);
+  if (e == cudaSuccess) e = set(dash_decode8_kernel<D, NT, kScan>);
   if (e == cudaSuccess) e = set(dash_decode8_kernel<D, NT, kCluster>);
-  if constexpr (NT == 2)
-    if (e == cudaSuccess) e = set(dash_decode8_kernel<D, NT, kScan>);
   return e;
 }
 

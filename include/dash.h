@@ -628,7 +628,7 @@ dash_status_t dash_cache_copy_fp8(void *k_pages, void *v_pages, float *k_scales,
 /* As dash_attn_decode, over the 8-bit cache, whose scales may be any finite
  * values >= 0, or NaN: o is then NaN for the heads that attend the row (lse too,
  * if it is a K row).  A Q row with a NaN or an infinity gives NaN.  There are two
- * forms, for small calls and for those that fill the GPU (by B, the table's room
+ * forms, for small calls and for those that fill the GPU (by B, D, the table's room
  * and Hkv): a sequence's bits do not depend on the other sequences', but on the
  * form.  In the second one a device wait that lasts 2 s ends the call, and
  * dash_sync_status reports DASH_ERR_TIMEOUT.

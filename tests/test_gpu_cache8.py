@@ -261,10 +261,10 @@ def test_decode_of_many_long_sequences(hq, hkv, D):
     dash.dash_sync_status()
 
 
-@pytest.mark.parametrize("n", [1024, 1025, 1500])
-def test_decode_of_very_many_sequences(n):
-    # of up to 1024 the lengths are held and the items sorted by them
-    lens, hq, hkv, D, page = [i * 37 % 300 for i in range(n)], 2, 1, 64, 16
+@pytest.mark.parametrize("n,D,top", [(256, 128, 900), (257, 128, 900), (1500, 128, 300), (1500, 64, 300), (3000, 128, 60)])
+def test_decode_of_very_many_sequences(n, D, top):
+    # up to 256 the lengths are held and the items sorted by them; sequences that are all short have a form of their own
+    lens, hq, hkv, page = [i * 37 % (top + 1) for i in range(n)], 3, 1, 4
     c = cache(lens, hkv, D, page)
     q = P.normal(4, n, hq, D)
     o, lse = dash.attn_decode_fp8(q, *c, i32(lens))
