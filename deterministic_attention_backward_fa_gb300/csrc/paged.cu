@@ -318,8 +318,66 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Joins the splits of a (sequence, Q head) in their order.
+// One Q head's attention of the first `len` tokens, which lie in the pages of the
+// table's first row: a block of 128 threads takes 128 tokens at a time, a thread
+// a score and then a value of the row.  What does not count is not multiplied.
 template <int D>
+__device__ __noinline__ void attend_row(const DecodeParams &p, int b, int h, int len, float *s_w, int *s_page,
+                                        float *s_m) {
+  const int tid = threadIdx.x, hk = h / p.group;
+  const __nv_bfloat16 *q = p.q + b * p.q_batch + h * p.q_head;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int t0 = 0; t0 < len; t0 += 128) {
+    const int t = t0 + tid, page = t < len ? p.table[t / p.page_size] : -1;
+    const bool ok = page >= 0 && page < p.n_pages;
+    float x = -INFINITY;
+    if (ok) {
+      const __nv_bfloat16 *k = p.k + page * p.ks.page + t % p.page_size * p.ks.token + hk * p.ks.head;
+      float dot = 0.f;
+      for (int c = 0; c < D; c += 8) {
+        const uint4 kw = *reinterpret_cast<const uint4 *>(k + c), qw = *reinterpret_cast<const uint4 *>(q + c);
+        const uint32_t a[4] = {kw.x, kw.y, kw.z, kw.w}, e[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dot = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(e[i] << 16), dot);
+          dot = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(e[i] & 0xffff0000u), dot);
+        }
+      }
+      x = dot * p.scale_log2;
+    }
+    float top = x;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    if ((tid & 31) == 0) s_m[tid >> 5] = top;
+    __syncthreads();
+    const float m1 = fmaxf(m, fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])));
+    const float ref = m1 == -INFINITY ? 0.f : m1, f = ex2(m - ref);
+    m = m1;
+    l *= f;
+    o *= f;
+    s_w[tid] = ex2(x - ref);
+    s_page[tid] = ok ? page : -1;
+    __syncthreads();
+    for (int i = 0; i < 128; ++i) {
+      if (s_page[i] < 0) continue;
+      l += s_w[i];
+      if (tid < D)
+        o = fmaf(s_w[i], __bfloat162float(p.v[s_page[i] * p.vs.page + (t0 + i) % p.page_size * p.vs.token +
+                                              hk * p.vs.head + tid]), o);
+    }
+    __syncthreads();
+  }
+  if (tid < D) p.o[b * p.o_batch + h * p.o_head + tid] = __float2bfloat16_rn(o * inverse_sum(l));
+  if (tid == 0 && p.lse) p.lse[(size_t)b * p.Hq + h] = log_sum(m, l);
+}
+
+// Joins the splits of a (sequence, Q head) in their order.  kPrefix: parts of a
+// shared prefix are among them.  Its products take a token that one sequence
+// attends and a shorter one does not with a weight of 0 for the latter, and 0 times
+// a NaN or an infinity in that token's V is a NaN.  So where a sequence ends inside
+// the prefix and its row is not finite, the row is made anew from the tokens that it
+// has: the masked ones are then the cause, or the row is not finite by its own.
+template <int D, bool kPrefix>
 __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
   // every block waits, so that this grid never ends before the first one
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -359,6 +417,14 @@ __global__ void __launch_bounds__(128) dash_decode_join(const DecodeParams p) {
 #pragma unroll 8
   for (int i = part + kAhead * J::kPart; i < n; i += J::kPart)
     J::add(o, s_w[i], *reinterpret_cast<const float4 *>(row + (size_t)i * D));
+  if (kPrefix) {
+    const int len = max(0, min(p.lengths[b], p.max_pages * p.page_size));
+    // a part that weighs 0 counts too: 0 times what is not finite is a NaN
+    if (len < p.first && __syncthreads_or(!isfinite(o.x) || !isfinite(o.y) || !isfinite(o.z) || !isfinite(o.w))) {
+      attend_row<D>(p, b, h, len, s_w, reinterpret_cast<int *>(s_o), s_m);
+      return;
+    }
+  }
   s_o[tid] = o;
   // the weights' sum, in their order (those behind the last split are 0)
   float l = 0.f;
@@ -526,7 +592,9 @@ cudaError_t prepare_decode() {
 
 cudaError_t launch_decode_join(int D, const DecodeParams &p, cudaStream_t stream) {
   cudaLaunchAttribute attr = overlap_attr();
-  return launch(D == 64 ? dash_decode_join<64> : dash_decode_join<128>, dim3(p.Hq, p.B), 128, 0, stream, &attr, p);
+  auto *kernel = p.parts_before > 0 ? (D == 64 ? dash_decode_join<64, true> : dash_decode_join<128, true>)
+                                    : (D == 64 ? dash_decode_join<64, false> : dash_decode_join<128, false>);
+  return launch(kernel, dim3(p.Hq, p.B), 128, 0, stream, &attr, p);
 }
 
 cudaError_t launch_decode(int D, const DecodeParams &p, int num_sms, cudaStream_t stream) {

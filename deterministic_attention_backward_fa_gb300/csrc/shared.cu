@@ -12,6 +12,9 @@
 //   O' = O 2^(m-m') + P V,   x = scale log2(e) q.k,  P = 2^(x - m'),
 // with S, P (bf16, in S's place) and O in tensor memory.  The maximum moves when
 // it has grown by 2^8 (kLazy), or from nothing.
+// A sequence may end inside the prefix.  What it does not attend has P = 0, and
+// V as the other rows attend it: 0 times a NaN or an infinity is then a NaN, and
+// the join makes such a row anew, from the tokens that the sequence has (paged.cu).
 //
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1 (a thread owns a row), 8 and 9 MMA
 // issue for tile 0 and 1, 12-15 fetch K and V: a token's row lies wherever its

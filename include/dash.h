@@ -578,7 +578,9 @@ dash_status_t dash_cache_copy(void *k_pages, void *v_pages, const int32_t *src, 
  * sequence continues in the page of its own row.  Their K and V are read once
  * for the batch instead of once per sequence (small calls, in which that saves
  * nothing, attend it with each sequence's tail).  `lengths` count the prefix; a
- * sequence may also end inside it.  The parts are cut by the sizes alone, so a
+ * sequence may also end inside it: what lies behind its end, in whatever values,
+ * does not reach its row (a row beside a NaN or an infinity there is attended by
+ * itself, slowly).  The parts are cut by the sizes alone, so a
  * call's bits are the same in every run; they depend on B and prefix, unlike
  * those of dash_attn_decode, which a prefix of 0 is.  Workspace:
  * dash_decode_shared_workspace() bytes.  A device wait that lasts 2 s ends the

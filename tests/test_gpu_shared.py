@@ -238,3 +238,54 @@ def test_refusals():
         f(q, kp, vp, table, n, table.shape[1] * 16 + 1)
     with pytest.raises(dash.DashError, match="workspace"):
         dash.dash_attn_decode_shared(q, kp, vp, table, n, 32, torch.empty_like(q), None, 0.1)
+
+
+@both
+@pytest.mark.parametrize("bad", [NAN, INF, -INF], ids=["nan", "inf", "-inf"])
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 24)])
+def test_values_that_a_sequence_does_not_attend_stay_out_of_its_rows(D, page, bad, wide):
+    # tokens 250 and 699 of head 1 of V: behind the end of the shorter sequences, attended by the longer ones
+    prefix, hq, hkv = 700, 4, 2
+    lens = [prefix, 200, prefix + 5, 0, 250, 251, 249, 699, 1]
+    kp, vp, table, seen = cache(lens, prefix, hkv, D, page, wide=wide)
+    q = R.normal(6, len(lens), hq, D)
+    v1 = vp.clone()
+    for tok in (250, 699):
+        for rows in (table[0, tok // page], *(table[b, tok // page] for b, n in enumerate(lens) if n > tok)):
+            v1[rows.long(), tok % page, 1, 5:40:7] = bad
+    o, lse = dash.attn_decode_shared(q, kp, v1, seen, i32(lens), prefix)
+    ro, rl, mag = R.decode(q, kp, v1, table, lens, 1 / math.sqrt(D))
+    assert torch.equal(o.double().isnan(), ro.isnan()) and torch.equal(o.double().isinf(), ro.isinf())
+    some = rl.isfinite()
+    assert (lse.double() - rl)[some].abs().max() <= 1e-4
+    fine = ro.isfinite()
+    assert fine[:, :2].all() and fine[1].all() and fine[[3, 4, 6, 8]].all() and not fine[[0, 2, 5, 7], 2:].all()
+    R.within("O", torch.where(fine, o.double(), 0.0), torch.where(fine, ro, 0.0), torch.where(fine, mag, 0.0))
+    assert not o[3].any() and lse[3].eq(-INF).all()
+    dash.dash_sync_status()
+
+
+@both
+@pytest.mark.parametrize("D", [128, 64])
+def test_pages_of_the_prefix_that_nobody_attends_may_hold_anything(D, wide):
+    # every sequence ends inside the prefix; behind the longest, nothing was ever written
+    prefix, hq, hkv, page = 1000, 8, 2, 16
+    lens = [3, 0, 257, 128, 1, 300]
+    kp, vp, table, seen = cache(lens, prefix, hkv, D, page, wide=wide)
+    for pages in (kp, vp):
+        flat = pages[table[0, :-(-prefix // page)].long()].flatten(0, 1)
+        flat[max(lens):] = NAN
+        pages[table[0, :-(-prefix // page)].long()] = flat.unflatten(0, (-1, page))
+    q = R.normal(7, len(lens), hq, D)
+    o, lse = dash.attn_decode_shared(q, kp, vp, seen, i32(lens), prefix)
+    check(q, kp, vp, table[:1].expand(len(lens), -1), lens, o, lse)
+    graph = torch.cuda.CUDAGraph()
+    lengths = i32([0] * len(lens))
+    with torch.cuda.graph(graph):
+        og, lg = dash.attn_decode_shared(q, kp, vp, seen, lengths, prefix)
+    for now in ([0] * len(lens), lens):
+        lengths.copy_(i32(now))
+        graph.replay()
+        check(q, kp, vp, table[:1].expand(len(lens), -1), now, og, lg)
+    assert torch.equal(og, o) and torch.equal(lg, lse)
+    dash.dash_sync_status()
