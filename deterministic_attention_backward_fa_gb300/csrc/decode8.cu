@@ -14,9 +14,15 @@
 // columns (term, head).  Two terms hold Q's 8 bits: exactly down to 2^-13 of its
 // row's largest value, and to 2^-21 of that below (the largest lands at 2^7 to
 // 2^8, and a term's last place is 2^-9).  A weight is off by at most 2^-8 of
-// itself, as one rounded to bf16 would be, or by 2^-18 of the largest that its
-// head has met (whose own M goes by x_t + log2 c_t, so that it is what counts in
-// O, whatever the scales of V are).  l sums the unrounded 2^(x_t - m).
+// itself, as one rounded to bf16 would be, or, where that is more, by 2^-18 of the
+// one that M was set by (M goes by x_t + log2 c_t, so that it is what counts in O,
+// whatever the scales of V are).  So that this does not add up over a long split,
+// behind a token that outweighs all that follow it, M is set anew, down as well as
+// up, at every 8th tile: 1024 tokens together lose 2^-8 of that one weight at most,
+// however long the sequence is.  (With an M that only rises, splits of 4096 tokens
+// lost up to 1.6 % and splits of 16384 up to 6 %.)  O, in 32 bits, takes an M of up
+// to 2^64 below the largest one; what is lost under that is nothing.  l sums the
+// unrounded 2^(x_t - m), and m only rises.
 //
 // The bound is HBM: 2 (D + 4) bytes a token and K/V head.  On the plain pipes the
 // widening alone takes half the issue slots (cache8.cu's kernel stays at 60 % of
@@ -62,6 +68,10 @@ constexpr int kSlots = 8;          // tiles whose scales and masks are held
 // log2 of where a head's largest weight is put, of how far a weight may grow past
 // that (e4m3 holds 448), and of how far 2^(x - m) may.
 constexpr float kTopLog = 4.f, kGrow = 4.f, kLazy = 8.f;
+// Tiles after which M is set anew (as many as splits of sequences of up to 65536 tokens have: no step more for those;
+// looking for low tiles at each one: 66 sequences 3 % slower, 64 of 4096 at D = 64 11 %), and how far M may fall.
+constexpr int kAgain = 8;
+constexpr float kMostDrop = 64.f;
 
 constexpr uint32_t kRing = 5 * 128 * kTile8;    // bytes of K and V tiles
 constexpr uint32_t kColBytes = kCols * 128;     // Q or P: a row of 128 bytes for each column
@@ -160,7 +170,7 @@ struct Head {
   float factor;          // of its scores
   float ref, limit;      // what 2^(x - m) refers to (m, or 0), and from where m moves
   float wref, wlimit;    // the same of the weights: M less kTopLog, or 0
-  float m, M, pad;
+  float m, M, top;       // top: the largest M so far
 };
 static_assert(sizeof(Head) == 32, "two 16-byte words");
 // Reduces N values (a power of two up to 32) over the lanes of a warp, all at
@@ -622,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       mbar_wait(&bars[bQFull + ib], iph, g);
       const Item it = items[ib];
       if (tok < kHeads)
-        heads[tok] = {factors[ib * kHeads + tok], 0.f, -INFINITY, 0.f, -INFINITY, -INFINITY, -INFINITY, 0.f};
+        heads[tok] = {factors[ib * kHeads + tok], 0.f, -INFINITY, 0.f, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (any_of_128(it.tiles < 0 || *g.abort)) break;  // one answer, as barriers follow
       if (lane == 0) mbar_arrive(&bars[bQEmpty + ib]);
       float l[kHeads];
@@ -649,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
         mbar_wait(&bars[bPvDone + (tile & 1)], ((tile >> 1) & 1) ^ 1, g);  // its place of P is free
         uint8_t *pt = smem + oP + (tile & 1) * kColBytes + (tok & 15);
         float pr[kHeads];
+        const bool again = j > 0 && j % kAgain == 0;
         for (int turn = 0;; ++turn) {
           // the weights' terms, a byte in each column's row
           uint32_t over = 0;
@@ -678,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
             named_bar(2, 128);
             break;
           }
-          if (!any_of_128(over != 0)) break;
+          if (!any_of_128(over != 0 || again)) break;
           // Maxima move, of the heads that need it only, so that a head's bits do not depend on the others; then the
           // weights are made anew.
           float both[2 * kHeads];
@@ -696,14 +707,15 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
           if (tok < kHeads) {
             Head &hd = heads[tok];
             float2 f = make_float2(1.f, 1.f);
-            if (((all_over[0] | all_over[1] | all_over[2] | all_over[3]) >> tok) & 1u) {
+            if (again || ((all_over[0] | all_over[1] | all_over[2] | all_over[3]) >> tok) & 1u) {
               const float4 a = reinterpret_cast<const float4 *>(red)[tok], b = reinterpret_cast<const float4 *>(red)[kHeads + tok];
               const float m1 = fmaxf(hd.m, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
-              const float M1 = fmaxf(hd.M, fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+              const float M1 = fmaxf(again ? hd.top - kMostDrop : hd.M, fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
               const float mr = m1 == -INFINITY ? 0.f : m1, Mr = M1 == -INFINITY ? 0.f : M1;
               f = make_float2(ex2(hd.m - mr), ex2(hd.M - Mr));
               hd.m = m1;
               hd.M = M1;
+              hd.top = fmaxf(hd.top, M1);
               hd.ref = mr;
               hd.limit = m1 + kLazy;
               hd.wref = M1 == -INFINITY ? 0.f : M1 - kTopLog;
@@ -744,7 +756,9 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
       if (tok < p.group) {
         const float4 w = reinterpret_cast<const float4 *>(sums)[tok];
         const float ll = (w.x + w.y) + (w.z + w.w), m = heads[tok].m;
-        moves[tok].x = ll == 0.f ? 0.f : ex2(heads[tok].M - kTopLog - m) * inverse_sum(ll);
+        // 2^(M - kTopLog - m) as a square: M may be far below m
+        moves[tok] = ll == 0.f ? make_float2(0.f, 0.f)
+                               : make_float2(inverse_sum(ll), ex2(0.5f * (heads[tok].M - kTopLog - m)));
         if (it.n_splits > 1) p.part_ml[first + (size_t)tok * parts] = make_float2(m, ll);
         else if (p.lse) p.lse[(size_t)it.b * p.Hq + h0 + tok] = log_sum(m, ll);
       }
@@ -758,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
 #pragma unroll 1
       for (int h = 0; h < p.group; ++h) {
         const float2 o = tmem_ld1x2(tl + cO + h, tl + cO + kHeads + h);
-        const float y = fmaf(o.y, 1.f / 16, o.x) * moves[h].x;
+        const float2 f = moves[h];
+        const float y = fmaf(o.y, 1.f / 16, o.x) * f.x * f.y * f.y;
         if (tok < D) {
           if (it.n_splits > 1) *part = y;
           else *out = __float2bfloat16_rn(y);

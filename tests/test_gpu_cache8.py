@@ -513,3 +513,110 @@ def test_prompt_fork_and_decode_together():
     ro, _, mag = P.decode(q[rows:], R.values(kp, ks), R.values(vp, vs), table, now, D ** -0.5)
     P.within("packed", po[last], ro, mag)
     assert (pl[:, last].T - lse).abs().max() <= 2e-4
+
+
+# Very long sequences whose weights differ widely.  What a weight loses beyond U of itself does not add up over a long
+# split: in two e4m3 terms it is 2^-14 where the weight that the maximum was last set by stands at 2^4, which is in the
+# same 1024 tokens: 2^-18 of their largest (2^-82 of the largest of all, where that is more); in f16 it is 2^-25 of the
+# largest of its split.
+def check_long(q, c, n, scale, o, lse, form):
+    kp, vp, ks, vs, row = c
+    page, D, U = kp.shape[1], kp.shape[3], P.U
+    x = (R.values(kp, ks)[row.long()].reshape(-1, D)[:n] @ q.double().T * scale).T          # [heads, n]
+    codes = bits(vp)[row.long()].view(FP8).reshape(-1, D)[:n].double().abs()
+    cs = vs[row.long()].reshape(-1)[:n].double()
+    v = R.values(vp, vs)[row.long()].reshape(-1, D)[:n]
+    rl = torch.logsumexp(x, 1)
+    p = torch.exp(x - rl[:, None])
+    ro, mag = p @ v, p @ v.abs()
+    chunk = 1024 if form == "wide" else max(256, 1 << (-(-n // 64) - 1).bit_length())
+    pad = -n % chunk
+    tops = torch.nn.functional.pad(p * cs, (0, pad)).unflatten(1, (-1, chunk)).amax(2)        # [heads, pieces]
+    sums = torch.nn.functional.pad(codes, (0, 0, 0, pad)).unflatten(0, (-1, chunk)).sum(1)    # [pieces, D]
+    floor = (2.0 ** -18 if form == "wide" else 2.0 ** -25) * (tops @ sums)
+    if form == "wide":
+        floor += 2.0 ** -82 * tops.amax(1, keepdim=True) * codes.sum(0)
+    assert (lse.double() - rl).abs().max() <= 1e-4
+    err = (o.double() - ro).abs()
+    bad = ~(err <= U * ro.abs() + (1 + U) * ((U + P.EPS) * mag + floor) + 1e-30)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside their bound, worst {(err / mag)[bad].max()} of it"
+
+
+def long_cache(n, D, page=128):
+    """One sequence's pages, K of zeros and V of ones, scales of 1, and a table row that names them in random order."""
+    n_pages = -(-n // page)
+    row = torch.randperm(n_pages, generator=torch.Generator().manual_seed(3)).int().cuda()
+    kp = torch.zeros(n_pages, page, 1, D, dtype=torch.uint8, device="cuda").view(FP8)
+    vp = torch.full((n_pages, page, 1, D), 0x38, dtype=torch.uint8, device="cuda").view(FP8)
+    ks, vs = (torch.ones(n_pages, 1, page, device="cuda").transpose(1, 2) for _ in range(2))
+    return kp, vp, ks, vs, row
+
+
+# 12 sequences of 64 splits are more items than a GPU takes at once, 2 are not
+FORMS = pytest.mark.parametrize("form,B", [("wide", 12), ("small", 2)], ids=["wide", "small"])
+
+
+def put(pages, row, t, dim, codes):
+    """Codes of tokens t in one dim."""
+    page = pages.shape[1]
+    bits(pages)[row[t // page].long(), t % page, 0, dim] = bits(codes.to(FP8))
+
+
+@FORMS
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("n,D", [(262144, 128), (262144, 64), (1000003, 64)])
+def test_decode_of_a_token_that_outweighs_a_long_sequence(n, D, where, form, B):
+    hq = 8
+    kp, vp, ks, vs, row = c = long_cache(n, D)
+    t = torch.arange(n, device="cuda")
+    at = {"first": 0, "middle": n // 2 + 77, "last": n - 1}[where]
+    put(kp, row, t[at:at + 1], 0, torch.ones(1, device="cuda"))
+    put(kp, row, t, 1, torch.randn(n, generator=torch.Generator("cuda").manual_seed(5), device="cuda") / 4)
+    split = 1 << (-(-n // 64) - 1).bit_length()
+    put(kp, row, t, 2, torch.where(t // split == at // split, 0.0, -60.0))
+    # powers of two between that token's weight and the others', which are equal or (the last two) random; heads 2 and 3
+    # have next to nothing in the other splits
+    q = torch.zeros(B, hq, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = torch.tensor([16.0, 17.0, 18.0, 19.0, 20.0, 18.125, 18.125, 22.0])
+    q[:, 6:, 1] = 1.0
+    q[:, 2:4, 2] = 1.0
+    lens, table = i32([n] * B), row[None].expand(B, -1).contiguous()
+    g = torch.Generator("cuda").manual_seed(6)
+    for values in ("ones", "positive"):
+        if values == "positive":
+            bits(vp).copy_(bits((torch.randn(vp.shape, generator=g, device="cuda").abs() * 100).clamp(max=448).to(FP8)))
+            vs.copy_(torch.exp2(torch.randint(-3, 4, vs.shape, generator=g, device="cuda").float()))
+        o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, lens, scale=math.log(2))
+        dash.dash_sync_status()
+        check_long(q[0], c, n, math.log(2), o[0], lse[0], form)
+        assert torch.equal(o, o[:1].expand_as(o)) and torch.equal(lse, lse[:1].expand_as(lse))
+        if values == "ones":
+            # whole powers of two are held exactly, but for those within 1024 tokens of that one, which lose 2^-18 of it
+            # each at most: what is left is the result's own rounding and the 32-bit arithmetic
+            assert ((o[0, :5].double() - 1).abs() <= P.U + 2.0 * P.EPS + 1023 * 2.0 ** -18).all()
+
+
+@FORMS
+@pytest.mark.parametrize("D", [128, 64])
+def test_decode_of_tiles_whose_weights_rise_and_fall(D, form, B):
+    # each 128 tokens stand at a level of their own, up to 2^120 apart, and the levels of V's rows as well
+    n, hq = 300001, 8
+    kp, vp, ks, vs, row = c = long_cache(n, D)
+    t, g = torch.arange(n, device="cuda"), torch.Generator("cuda").manual_seed(7)
+    levels = torch.randn(n // 128 + 1, generator=g, device="cuda") * 18
+    put(kp, row, t, 0, levels.clamp(-60, 60)[t // 128])
+    put(kp, row, t, 1, torch.linspace(60, -60, n, device="cuda"))      # ever down, split by split and over all
+    put(kp, row, t, 2, ((t % 4096) < 128).float() * 40)                # the first tile of a split above the others
+    put(kp, row, t, 3, torch.randn(n, generator=g, device="cuda") * 2)
+    bits(vp).copy_(bits((torch.randn(vp.shape, generator=g, device="cuda") * 100).clamp(-448, 448).to(FP8)))
+    q = torch.zeros(B, hq, D, dtype=torch.bfloat16, device="cuda")
+    for h, w in enumerate([(1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (0, 0, -1, 0), (1, 0, 0, 1), (0, 0, 1, 1),
+                           (0, 8, 0, 1), (0.25, 0, 0, 1)]):
+        q[:, h, :4] = torch.tensor(w)
+    lens, table = i32([n] * B), row[None].expand(B, -1).contiguous()
+    for _ in range(2):
+        o, lse = dash.attn_decode_fp8(q, kp, vp, ks, vs, table, lens, scale=math.log(2))
+        dash.dash_sync_status()
+        check_long(q[0], c, n, math.log(2), o[0], lse[0], form)
+        assert torch.equal(o, o[:1].expand_as(o)) and torch.equal(lse, lse[:1].expand_as(lse))
+        vs.copy_(torch.exp2(torch.randint(-30, 31, vs.shape, generator=g, device="cuda").float()))
