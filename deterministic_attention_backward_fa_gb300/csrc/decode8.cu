@@ -46,6 +46,7 @@
 
 #include "cache8.h"
 #include "decode.cuh"
+#include "drain.h"
 #include "fp8.cuh"
 #include "sm103.cuh"
 
@@ -561,8 +562,10 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode8_wide_kernel(
     cp_wait_all();
     // what TMA still has in flight lands before the CTA exits
     named_bar(3, 32 * kFetch);  // nothing more is issued
-    for (int s = 0; s < kStages; ++s)
-      if (last[s] >= 0) mbar_drain(&bars[bKvFull + s], last[s] / kStages & 1, g.limit_ns);
+    // (after an abort a stage at which a warp has not arrived never completes)
+    drain_all(
+        kStages, [&](int s) { return last[s] < 0 || mbar_test(&bars[bKvFull + s], last[s] / kStages & 1); },
+        [] { return globaltimer_ns(); }, g.limit_ns);
   } else if (warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kMma) {

@@ -632,8 +632,9 @@ dash_status_t dash_cache_copy_fp8(void *k_pages, void *v_pages, float *k_scales,
  * if it is a K row).  A Q row with a NaN or an infinity gives NaN.  There are two
  * forms, for small calls and for those that fill the GPU (by B, D, the table's room
  * and Hkv): a sequence's bits do not depend on the other sequences', but on the
- * form.  In the second one a device wait that lasts 2 s ends the call, and
- * dash_sync_status reports DASH_ERR_TIMEOUT.
+ * form.  In the second one a device wait that lasts 2 s ends the call (after at
+ * most 2 s more for what it has in flight), and dash_sync_status reports
+ * DASH_ERR_TIMEOUT.
  * Workspace: dash_decode_workspace() bytes.  strides, 17 values: q {batch,
  * head}, o {batch, head}, k_pages, v_pages, k_scales, v_scales, page_table
  * row. */

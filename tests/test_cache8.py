@@ -1,5 +1,7 @@
 """The 8-bit paged cache, what needs no GPU: refusals and the plain form's own quantisation."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -87,3 +89,28 @@ def test_binding_refuses_wrong_tensors():
     pages, scales = torch.zeros(2, 3, 4, 64, dtype=torch.float8_e4m3fn), torch.zeros(2, 3, 4)
     with pytest.raises(ValueError, match="CUDA float8"):
         dash.cache_copy_fp8(pages, pages, scales, scales, [0], [1])
+
+
+def test_the_waits_on_the_way_out_have_one_limit(tmp_path):
+    # ten barriers, of which some never complete, with a clock that the host drives
+    (tmp_path / "d.cpp").write_text("""
+#include "drain.h"
+#include <cstdio>
+int main() {
+  for (int never = 0; never < 1024; ++never) {  // a bit for each that never completes
+    unsigned long long clock = 5000, asked = 0;
+    dash::drain_all(
+        10, [&](int i) { ++asked; clock += 7; return !(never >> i & 1) && clock > 5000u + 40 * i; }, [&] { return clock; },
+        1000);
+    if (clock > 5000 + 1000 + 2 * 7) return std::printf("%d: took %llu\\n", never, clock - 5000), 1;
+    if (!never && clock <= 5000 + 360) return std::printf("left too early\\n"), 1;
+    if (!asked) return 1;
+  }
+  return 0;
+}
+""")
+    exe = str(tmp_path / "d")
+    src = os.path.join(os.path.dirname(dash.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", src, "-o", exe, str(tmp_path / "d.cpp")], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
