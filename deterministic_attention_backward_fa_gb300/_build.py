@@ -3,7 +3,7 @@
 Each translation unit compiles in its own nvcc process (in parallel); the
 objects go to ``_build/`` beside this file and the shared library next to the
 package's ``__init__``, with the compiled part of the Python binding (named by
-the torch version that it is compiled against).  The library links the CUDA runtime statically and
+the torch version and the interpreter that it is compiled against).  The library links the CUDA runtime statically and
 reaches the driver (for tensor-map encoding) through the runtime's
 entry-point query, so it loads on machines without a GPU driver.
 """
@@ -38,9 +38,9 @@ def nvcc() -> str:
 
 
 def binding_path() -> str:
-    """The compiled part of the binding for the torch of this process."""
+    """The compiled part of the binding for the torch and the interpreter of this process."""
     import torch
-    return os.path.join(PKG, f"_binding_{torch.__version__.replace('+', '_')}.so")
+    return os.path.join(PKG, f"_binding_{torch.__version__.replace('+', '_')}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _torch_flags():
