@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +44,20 @@ def binding_path() -> str:
     return os.path.join(PKG, f"_binding_{torch.__version__.replace('+', '_')}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
+def binding_lacks() -> str | None:
+    """What this machine lacks for the compiled part of the binding, or None.  The C ABI needs none of it, and the
+    Python form of the calls stands in for the compiled one."""
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    for path in (os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd", "python_variable.h"),
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(path):
+            return path
+    return None if shutil.which("g++") else "g++"
+
+
 def _torch_flags():
     import torch
     top = os.path.dirname(torch.__file__)
@@ -61,9 +76,10 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(binding_path()):
+    made = [LIB] if binding_lacks() else [LIB, binding_path()]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(binding_path()))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -73,16 +89,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
 
-    flags, libs = _torch_flags()
-
     def compile_one(src):
         obj = os.path.join(BUILD, src + ".o")
-        if src == BINDING:
-            cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", os.path.join(CSRC, src), "-o", obj]
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            if r.returncode != 0:
-                raise RuntimeError(f"g++ failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-            return obj, ""
         cmd = [cc, *ARCH, *COMMON, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cu"):
             cmd.insert(1, "-Xptxas=-v" if verbose else "-Xptxas=-warn-spills")
@@ -91,9 +99,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return obj, (r.stdout + r.stderr)
 
+    lacks = binding_lacks()
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        results = list(ex.map(compile_one, [*SOURCES, BINDING]))
-    binding = results.pop()[0]
+        binding = None if lacks else ex.submit(_compile_binding)
+        results = list(ex.map(compile_one, SOURCES))
     if verbose:
         for (_, log) in results:
             if log.strip():
@@ -104,13 +113,32 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # the library stands by now, whatever becomes of the binding
+    if lacks:
+        warnings.warn(f"the compiled part of the Python binding is left out: this machine lacks {lacks}")
+    else:
+        _link_binding(*binding.result())
+    return LIB
+
+
+def _compile_binding():
+    """Compiles the binding; its object and the libraries that it links against."""
+    flags, libs = _torch_flags()
+    obj = os.path.join(BUILD, BINDING + ".o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", os.path.join(CSRC, BINDING), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj, libs
+
+
+def _link_binding(obj, libs):
     tmp = binding_path() + ".tmp"
-    cmd = ["g++", "-shared", "-o", tmp, binding, "-L", PKG, "-l:" + os.path.basename(LIB), *libs, "-Wl,-rpath,$ORIGIN"]
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), *libs, "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, binding_path())
-    return LIB
 
 
 if __name__ == "__main__":

@@ -30,3 +30,28 @@ def test_the_compiled_form_is_the_one_that_is_asked():
         f = getattr(fast, name)
         assert type(f).__name__ == "builtin_function_or_method"
         assert f() is None  # a wrong number of arguments: the Python form's to answer
+
+
+def test_the_library_is_built_without_what_the_binding_needs(tmp_path, monkeypatch):
+    # a stand-in for nvcc that makes empty files: only the order and the needs are looked at
+    cc = tmp_path / "nvcc"
+    cc.write_text("#!/bin/sh\nwhile [ $# -gt 1 ]; do if [ $1 = -o ]; then : > $2; fi; shift; done\n")
+    cc.chmod(0o755)
+    lib, so = tmp_path / "lib.so", tmp_path / "binding.so"
+    for name, value in (("nvcc", lambda: str(cc)), ("BUILD", str(tmp_path / "objects")), ("LIB", str(lib)),
+                        ("binding_path", lambda: str(so))):
+        monkeypatch.setattr(_build, name, value)
+    # without Python's headers
+    monkeypatch.setattr(_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path / "none")})
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert _build.build(force=True) == str(lib)
+    assert lib.exists() and not so.exists() and _build.up_to_date()
+    monkeypatch.undo()
+    # with all of them, where it does not compile: the library stands, and the error is told
+    for name, value in (("nvcc", lambda: str(cc)), ("BUILD", str(tmp_path / "objects")), ("LIB", str(lib)),
+                        ("binding_path", lambda: str(so)), ("_torch_flags", lambda: (["-DDASH_H", "-include", "/none"], []))):
+        monkeypatch.setattr(_build, name, value)
+    lib.unlink()
+    with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
+        _build.build(force=True)
+    assert lib.exists() and not so.exists()
