@@ -20,6 +20,7 @@ import importlib.machinery
 import importlib.util
 import math
 import os
+import warnings
 
 import numpy as np
 import torch
@@ -139,14 +140,25 @@ def lib():
 _FAST = None
 
 
+class _NoFast:
+    """Answers every call as the compiled part answers what it does not take."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _fast():
-    """The compiled part of the binding (csrc/binding.cpp): small calls spend most of their time in ctypes."""
+    """The compiled part of the binding (csrc/binding.cpp): small calls spend most of their time in ctypes.  Where it
+    was not built for this torch and interpreter, the Python form makes every call, with the same kernels."""
     global _FAST
     if _FAST is None:
         lib()
         path = _build.binding_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+            warnings.warn(f"{path} is missing: calls go through ctypes, which costs small ones 10 to 30 us; "
+                          "__graft_entry__.build() builds it")
+            _FAST = _NoFast()
+            return _FAST
         loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader, origin=path))
         loader.exec_module(module)

@@ -55,3 +55,47 @@ def test_the_library_is_built_without_what_the_binding_needs(tmp_path, monkeypat
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         _build.build(force=True)
     assert lib.exists() and not so.exists()
+
+
+def test_without_the_file_the_python_form_makes_the_calls(tmp_path, monkeypatch):
+    monkeypatch.setattr(dash, "_FAST", None)
+    monkeypatch.setattr(_build, "binding_path", lambda: str(tmp_path / "none.so"))
+    pages, scales = torch.zeros(2, 3, 4, 64, dtype=torch.float8_e4m3fn), torch.zeros(2, 3, 4)
+    q, i = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    with pytest.warns(UserWarning, match="is missing"):
+        with pytest.raises(ValueError, match="q must be a CUDA"):
+            dash.attn_decode_fp8(q, pages, pages, scales, scales, i[None], i[:1])
+    for call in (lambda: dash.qk_norm_rope(q, q, q[0, 0], q[0, 0], scales[0], i[:1]),
+                 lambda: dash.cache_write_fp8(q, q, pages, pages, scales, scales, i[None], i[:1], i),
+                 lambda: dash.attn_decode_shared(q, q[None], q[None], i[None], i[:1], 3)):
+        with pytest.raises(ValueError, match="must be a CUDA"):
+            call()
+
+
+@pytest.mark.gpu
+def test_both_forms_give_the_same(monkeypatch):
+    g = torch.Generator("cuda").manual_seed(1)
+    normal = lambda *shape: torch.randn(*shape, generator=g, device="cuda").bfloat16()
+    hq, hkv, D, page, n = 4, 2, 128, 16, 50
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    q, k, dq, dk = normal(n, hq, D), normal(n, hkv, D), normal(n, hq, D), normal(n, hkv, D)
+    w = [torch.ones(D, device="cuda")] * 2
+    rope, pos = dash.rope_table(n, D), torch.arange(n, dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+
+    def all_calls():
+        kp, vp = (torch.zeros(4, page, hkv, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in "kv")
+        ks, vs = (torch.zeros(4, page, hkv, device="cuda") for _ in "kv")
+        out = [*dash.qk_norm_rope(q, k, *w, rope, pos), *dash.qk_norm_rope_bwd(q, k, dq, dk, *w, rope, pos)]
+        dash.cache_write_fp8(k, dk, kp, vp, ks, vs, table, i32(0), i32(0, n))
+        out += [kp.view(torch.uint8), vp.view(torch.uint8), ks, vs]
+        out += dash.cache_read_fp8(kp, vp, ks, vs, table, i32(0), i32(0, n), n)
+        out += dash.attn_decode_fp8(q[:1], kp, vp, ks, vs, table, i32(n))
+        out += dash.attn_decode_shared(q[:1], *(torch.nn.functional.pad(t, (0, 0, 0, 0, 0, 14)).reshape(
+            4, page, hkv, D) for t in (k, dk)), table, i32(n), 20)
+        dash.dash_sync_status()
+        return out
+
+    compiled = all_calls()
+    monkeypatch.setattr(dash, "_FAST", dash._NoFast())
+    assert all(torch.equal(a, b) for a, b in zip(compiled, all_calls(), strict=True))
