@@ -143,14 +143,14 @@ struct Items {
       if (want >= (long long)p.B * p.max_splits) return 0;
       b = (int)(want / p.max_splits);
       split = (int)(want - (long long)b * p.max_splits);
-      if (split > 0 && split >= decode_splits(decode_len(p, b))) return -1;
+      if (split > 0 && split >= decode_splits(decode_len(p, b), p.least_chunk)) return -1;
     }
     while (kDeal == kScan) {
       if (in_block != base_b) {  // the block's prefix sums
         __syncthreads();
         const int mine = base_b + (int)threadIdx.x;
         int n = 0;
-        if (mine < p.B) n = decode_splits(decode_len(p, mine));
+        if (mine < p.B) n = decode_splits(decode_len(p, mine), p.least_chunk);
         // an empty sequence still has an item, which writes its zero row
         if (mine < p.B && n == 0) n = 1;
         int x = n;

@@ -168,7 +168,7 @@ struct DecodeParams {
   int hblocks;                // blocks of 16 Q heads in a group
   int first;                  // the tokens before this one are attended elsewhere ...
   int parts_before;           // ... and have left that many parts
-  int least_chunk;            // tokens of the shortest kind of split
+  int least_chunk;            // tokens of the shortest kind of split, for all kernels of a call; kMinChunk at least
   int shared;                 // the tokens before this one lie in the pages of the table's first row
   float scale_log2;
   int *status;

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) dash_decode_kernel(const DecodePa
     const int hk = rest / p.hblocks, hb = rest - hk * p.hblocks;
     const int h0 = hk * p.group + hb * 16, nh = min(16, p.group - hb * 16);
     const int len = decode_len(p, b);
-    const int chunk = decode_chunk(len), n_splits = max(1, decode_splits(len));
+    const int chunk = decode_chunk(len, p.least_chunk), n_splits = max(1, decode_splits(len, p.least_chunk));
     const bool mine = kDeal != kCluster || split < n_splits;  // or the sequence does not have this split of the cluster
     const int begin = split * chunk, end = min(len, begin + chunk);
     const int steps = mine ? (end - begin + kStep - 1) / kStep : 0;
