@@ -289,3 +289,52 @@ def test_pages_of_the_prefix_that_nobody_attends_may_hold_anything(D, wide):
         check(q, kp, vp, table[:1].expand(len(lens), -1), now, og, lg)
     assert torch.equal(og, o) and torch.equal(lg, lse)
     dash.dash_sync_status()
+
+
+@pytest.mark.parametrize("what", ["samples", "batch", "batch of the 8-bit cache", "rows of the 8-bit cache", "norms"])
+def test_the_first_call_of_a_process_may_be_captured(what):
+    # one launch; the prefix, the tails and their join; items and their join; write, read and copy; two launches
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys
+import torch, deterministic_attention_backward_fa_gb300 as dash
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+rand = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+what, D, page = sys.argv[1], 128, 16
+q, kp, vp = rand(12, 8, D), rand(40, page, 2, D), rand(40, page, 2, D)
+table = (torch.arange(12 * 1100, device="cuda").int() % 40).reshape(12, 1100)
+table[:, :20] = torch.arange(20, device="cuda").int()
+lens = i([300 + 29 * b for b in range(12)])
+c8 = [rand(40, page, 2, D).to(torch.float8_e4m3fn) for _ in "kv"] + [torch.rand(40, page, 2, device="cuda") for _ in "kv"]
+k, v = rand(25, 2, D), rand(25, 2, D)
+x, w, rope, pos = rand(25, 8, D), rand(D), torch.rand(30, D, device="cuda"), torch.arange(25, device="cuda").int()
+
+def call():
+    if what == "samples":
+        return dash.attn_decode_shared(q[:2], kp, vp, table[:2, :40], lens[:2], 310)
+    if what == "batch":
+        return dash.attn_decode_shared(q, kp, vp, table, lens, 310)
+    if what == "batch of the 8-bit cache":
+        return dash.attn_decode_fp8(q, *c8, table, lens)
+    if what == "norms":
+        return *dash.qk_norm_rope(x, k, w, w, rope, pos), *dash.qk_norm_rope_bwd(x, k, x, v, w, w, rope, pos)
+    dash.cache_write_fp8(k, v, *c8, table[:2], lens[:2], i_cu)
+    dash.cache_copy_fp8(*c8, [1, 2], [30, 31])
+    return *dash.cache_read_fp8(*c8, table[:2], starts, i_cu, 25), *(t.view(torch.uint8).clone() for t in c8[:2])
+
+i_cu, starts = i([0, 20, 25]), i([295, 300])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = call()
+g.replay()
+torch.cuda.synchronize()
+again = call()
+dash.dash_sync_status()
+assert all(torch.equal(a, b) for a, b in zip(out, again))
+assert all(t.float().abs().sum() > 0 for t in out)
+"""
+    r = subprocess.run([sys.executable, "-c", code, what], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
