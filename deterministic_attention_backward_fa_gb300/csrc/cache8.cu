@@ -22,14 +22,17 @@
 // that f16 holds its 8 bits down to 2^-29 of that.
 // P goes to f16 as 2^(x_t - M) c_t with M the maximum of x_t + log2 c_t of its
 // head, not of x_t: what counts in O keeps f16's 11 bits whatever the scales
-// of V are.  l and O are 32-bit sums, l of the unrounded 2^(x_t - m).
+// of V are, and a weight of less than 2^-25 of the largest, which f16 gives up, is
+// 2^-11 of it even 16384 times, the longest split of a warp's four.  l and O are 32-bit sums, l of the unrounded 2^(x_t - m).
 // m and M move only when a term has grown past 2^8 of them (most steps need no
 // reduction across lanes and no rescaling).
 // This form takes calls whose items all run at once or are short (701 tokens, 16 heads on 4:
 // 7.2 us, a chain of length, page, rows, products and the cluster's join) and
 // groups of 9 to 16 heads (64 sequences of 8192 tokens, 16 heads on 1 of 128: 61
-// us, 2.3 TB/s, bound by instructions: the widening, and a reduction's share of
-// each head); decode8.cu has the one for calls that fill the GPU.
+// us, 2.3 TB/s, bound by latency: two tiles of heads take 241 registers, so that 8
+// warps of an SM stand in each step's chain of copies, widening, scores and weights
+// and issue in 30 % of their cycles); decode8.cu has the one for calls that fill the
+// GPU.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -13,8 +13,8 @@
 // each), so that the rotation needs no exchange and every lane holds the four
 // cosines and sines that it needs, once for all heads of a row of the batch.
 // 16384 tokens of 16 + 4 heads of 128: 31.4 us forward and 48.1 us backward, 5.4
-// and 5.3 TB/s.  Next to the bytes stand the instructions (some 100 and 160 for
-// 32 lanes x 8 values): forward, loads straight into registers and two steps'
+// and 5.3 TB/s.  Next to the bytes stand the instructions (130 and 213 a step
+// of 32 lanes x 8 values): forward, loads straight into registers and two steps'
 // arithmetic side by side beat a ring in shared memory (35.1 us); backward,
 // where registers hold the sums of dw too, the ring wins (53.3 us without it).
 #include <cuda_runtime.h>

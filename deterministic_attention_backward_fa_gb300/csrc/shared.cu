@@ -28,7 +28,7 @@
 // head), which are about even at 256 rows: 32000 tokens, 64 sequences of 4 heads
 // on each of 8 K/V heads of 128 in 32 us, 18 and 19 of them those two.  What is
 // left is each tile's chain of scores, softmax and product, of which two run in
-// turn.  With tails of 512 tokens the call takes 69.5 us.
+// turn.  With tails of 512 tokens the call takes 69.5 us (55 with D = 64).
 #include <cuda_runtime.h>
 
 #include "packed.h"

@@ -32,8 +32,10 @@ inline PrefixCut prefix_cut(int B, int Hq, int Hkv, int prefix) {
 // Whether the prefix is left to dash_decode_kernel, for every sequence by itself:
 // where all its splits run at once and are short, what re-reads of the prefix cost
 // (they hit L2) is less than two more launches.  4 sequences of 1501 tokens and
-// some, 16 heads on 4: 7.8 us against 9.9; 12 of 512 on 8 K/V heads 9.9 and 10.1;
-// beyond, 16 of 512 14.3 and 10.0, and one of 4096 in longer splits 11.3 and 9.9.
+// some, 16 heads on 4: 8.1 us against 9.9; 12 of 512 on 8 K/V heads 10.2 and 10.6;
+// beyond, 16 of 512 14.7 and 10.7, and one of 4096 in longer splits 11.7 and 11.7.
+// It goes by the table's room, as a captured call has to: the 4 sequences with a
+// table of more than 4096 tokens take 10.6.
 inline bool prefix_with_tails(int B, int Hq, int Hkv, int cap) {
   return decode_chunk(cap) == kMinChunk &&
          (long long)B * Hkv * ((Hq / Hkv + 15) / 16) * decode_max_splits(cap) <= 2 * kPrefixCtas;

@@ -629,10 +629,15 @@ dash_status_t dash_cache_copy_fp8(void *k_pages, void *v_pages, float *k_scales,
 
 /* As dash_attn_decode, over the 8-bit cache, whose scales may be any finite
  * values >= 0, or NaN: o is then NaN for the heads that attend the row (lse too,
- * if it is a K row).  A Q row with a NaN or an infinity gives NaN.  There are two
- * forms, for small calls and for those that fill the GPU (by B, D, the table's room
- * and Hkv): a sequence's bits do not depend on the other sequences', but on the
- * form.  In the second one a device wait that lasts 2 s ends the call (after at
+ * if it is a K row).  A scale of V below 2^-126 counts as 0.  A Q row with a NaN or
+ * an infinity gives NaN.  There are two forms, for small calls and for those that
+ * fill the GPU (by B, Hkv, Hq / Hkv, D, the table's room and the number of SMs): a
+ * sequence's bits do not depend on the other sequences', but on the form.  Weights
+ * are rounded as products' operands, to 2^-11 of themselves in the first (and by
+ * 2^-25 of the split's largest) and to 2^-8 in the second (and by 2^-18 of the
+ * largest of the same 1024 tokens); lse is not touched by that.  A table with more
+ * room than the batch needs may select a slower form: pass a view of the columns
+ * in use where the host knows them.  In the second one a device wait that lasts 2 s ends the call (after at
  * most 2 s more for what it has in flight), and dash_sync_status reports
  * DASH_ERR_TIMEOUT.
  * Workspace: dash_decode_workspace() bytes.  strides, 17 values: q {batch,
