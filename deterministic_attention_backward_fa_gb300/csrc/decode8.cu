@@ -18,11 +18,12 @@
 // one that M was set by (M goes by x_t + log2 c_t, so that it is what counts in O,
 // whatever the scales of V are).  So that this does not add up over a long split,
 // behind a token that outweighs all that follow it, M is set anew, down as well as
-// up, at every 8th tile: 1024 tokens together lose 2^-8 of that one weight at most,
-// however long the sequence is.  (With an M that only rises, splits of 4096 tokens
-// lost up to 1.6 % and splits of 16384 up to 6 %.)  O, in 32 bits, takes an M of up
-// to 2^64 below the largest one; what is lost under that is nothing.  l sums the
-// unrounded 2^(x_t - m), and m only rises.
+// up, at every 8th tile: 1024 tokens together lose 2^-8 of that one weight at most.
+// (With an M that only rises, splits of 4096 tokens lost up to 1.6 % and splits of
+// 16384 up to 6 %.)  O is a 32-bit sum: it takes an M of up to 2^64 below the largest
+// one, but what stands 2^-24 and more under O itself the tensor cores cut off, as in
+// any such sum; of a million tokens, in splits of 16384, that is 2^-10 at most.  l
+// sums the unrounded 2^(x_t - m), and m only rises.
 //
 // The bound is HBM: 2 (D + 4) bytes a token and K/V head.  On the plain pipes the
 // widening alone takes half the issue slots (cache8.cu's kernel stays at 60 % of

@@ -635,7 +635,9 @@ dash_status_t dash_cache_copy_fp8(void *k_pages, void *v_pages, float *k_scales,
  * sequence's bits do not depend on the other sequences', but on the form.  Weights
  * are rounded as products' operands, to 2^-11 of themselves in the first (and by
  * 2^-25 of the split's largest) and to 2^-8 in the second (and by 2^-18 of the
- * largest of the same 1024 tokens); lse is not touched by that.  A table with more
+ * largest of the same 1024 tokens); lse is not touched by that.  O's sums are
+ * 32-bit: behind a token that outweighs its split, tokens of less than 2^-24 of it
+ * do not count, which shows (beyond 2^-10) past a million tokens.  A table with more
  * room than the batch needs may select a slower form: pass a view of the columns
  * in use where the host knows them.  In the second one a device wait that lasts 2 s ends the call (after at
  * most 2 s more for what it has in flight), and dash_sync_status reports
